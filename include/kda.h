@@ -374,6 +374,152 @@ typedef struct {
 
 kda_status_t kda_recurrent_step(const kda_step_args *args, struct CUstream_st *stream);
 
+/* ------------------------------------------ linear attention, a decay per head
+ * The recurrence without the delta rule's erase term, for the linear-attention layers that models
+ * place beside KDA layers (fixed or learned decay, no write strength):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t
+ * with one log-decay g per head and token (g_per_token = 1, [T, H]), one per head ([H]), or none
+ * (g NULL: exp(g) = 1).  g is fp32 and at most 0; a log-decay below -104 (-inf included) counts as
+ * -104, whose factor is 0 in fp32: it erases the state.  Values above 0 are computed as given and may
+ * overflow; a NaN spreads over its sequence and head from its token on (in a gradient, over the sequence).
+ *
+ * Heads: H states per sequence.  Hq, Hk and Hv say how many heads q, k and v have; each divides H, the
+ * largest of them is H, and state head h reads head h / (H / Hx) of each (q and k shared by groups of
+ * value heads, or k and v by groups of query heads).  o has H heads.
+ *
+ * Shapes: q [T, Hq, dk], k [T, Hk, dk], v [T, Hv, dv], o [T, H, dv]; dk and dv each 64 or 128; states
+ * [N, H, dk, dv] fp32.  Memory, packing, streams and errors are as for kda_chunk_fwd; cu_seqlens
+ * contents are checked on the device (KDA_ERR_BAD_SEQLENS; sequences with a bad range are skipped and
+ * rows that belong to no sequence are left as they were).  An empty sequence's final state is its
+ * initial state, exactly.  Outputs may not overlap inputs, except that final_state may be
+ * initial_state.  Every call is free of atomics on its results: the same inputs give the same bits. */
+typedef struct {
+    int64_t T, N;                  /* tokens (all sequences packed), sequences (>= 1) */
+    int32_t H, Hq, Hk, Hv, dk, dv;
+    kda_dtype_t dtype;             /* dtype of q, k, v and o */
+    const void *q, *k, *v;
+    const float *g;                /* log-decay [T, H] or [H], or NULL */
+    int32_t g_per_token;           /* 1: g is [T, H]; 0: [H] */
+    float scale;
+    const int32_t *cu_seqlens;     /* [N + 1] device, or NULL for N sequences of T / N tokens */
+    const float *initial_state;    /* [N, H, dk, dv] or NULL (zero) */
+    float *final_state;            /* [N, H, dk, dv] or NULL */
+    void *o;
+} kda_linear_args;
+
+/* Bytes of device scratch the two calls need for these sizes (0 on invalid sizes). */
+size_t kda_linear_chunk_fwd_workspace_size(int64_t T, int64_t N, int32_t H, int32_t dk, int32_t dv,
+                                           kda_dtype_t dtype);
+size_t kda_linear_chunk_bwd_workspace_size(int64_t T, int64_t N, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv,
+                                           int32_t dk, int32_t dv, kda_dtype_t dtype);
+
+/* Prefill, evaluated in chunks: with G the cumulative log-decay inside a chunk,
+ *     O = scale (Tril[Q K^T * e^{G_r - G_j}] V + e^G Q S),   S <- e^{G_last} S + (K e^{G_last - G})^T V.
+ * workspace: at least kda_linear_chunk_fwd_workspace_size() bytes, 256-byte aligned; its contents need no
+ * initialisation; calls that share one (captured graphs among them) must not overlap in time.  The call may be
+ * captured into a graph and replayed with other contents of the same buffers. */
+kda_status_t kda_linear_chunk_fwd(const kda_linear_args *args, void *workspace, size_t workspace_bytes,
+                                  struct CUstream_st *stream);
+
+/* Gradients of kda_linear_chunk_fwd given dL/do and optionally dL/dS_T; nothing is kept from the forward
+ * call.  The state's adjoint runs backwards, Lambda <- e^{G_last} Lambda + scale (Q e^G)^T dO; with
+ * dA = scale Tril[dO V^T * e^{G_r - G_j}]:
+ *     dQ = dA K + scale e^G dO S^T,  dK = dA^T Q + f V Lambda^T,  dV = A^T dO + f K Lambda,  f = e^{G_last - G},
+ * and the gradient of g_t is the sum of all that passes from before t to t or later.  grad_q, grad_k and grad_v
+ * have the heads of q, k and v (sums over the states that share one, in fp32, in a fixed order) and are rounded once
+ * to dtype; grad_g has the shape of g and, like the state gradient, is fp32. */
+typedef struct {
+    int64_t T, N;
+    int32_t H, Hq, Hk, Hv, dk, dv;
+    kda_dtype_t dtype;              /* dtype of q, k, v, grad_o, grad_q, grad_k, grad_v */
+    const void *q, *k, *v;
+    const float *g;
+    int32_t g_per_token;
+    float scale;
+    const int32_t *cu_seqlens;
+    const float *initial_state;     /* [N, H, dk, dv] or NULL (zero) */
+    const void *grad_o;             /* [T, H, dv] */
+    const float *grad_final_state;  /* [N, H, dk, dv] or NULL (zero) */
+    void *grad_q, *grad_k, *grad_v;
+    float *grad_g;                  /* shape of g, or NULL to skip (NULL when g is) */
+    float *grad_initial_state;      /* [N, H, dk, dv], or NULL to skip */
+} kda_linear_bwd_args;
+
+kda_status_t kda_linear_chunk_bwd(const kda_linear_bwd_args *args, void *workspace, size_t workspace_bytes,
+                                  struct CUstream_st *stream);
+
+/* One decode token per sequence: the recurrence once per (sequence, head), the state updated in place.
+ * Shapes as above with N in the place of T.  state_indices: as kda_recurrent_step, with two more promises:
+ * a slot of -1 marks an unused row of a padded batch (nothing is read or written for it), and a slot that
+ * an earlier row already has is not raced on: the later row is skipped and sets KDA_ERR_BAD_STATE_INDEX. */
+typedef struct {
+    int64_t N;
+    int32_t H, Hq, Hk, Hv, dk, dv;
+    kda_dtype_t dtype;
+    const void *q, *k, *v;
+    const float *g;                /* [N, H] (g_per_token = 1), [H], or NULL */
+    int32_t g_per_token;
+    float scale;
+    float *state;                  /* [num_slots, H, dk, dv] fp32 */
+    const int32_t *state_indices;  /* [N], or NULL (slot n) */
+    int64_t num_slots;             /* 0 = N */
+    void *o;                       /* [N, H, dv] */
+} kda_linear_step_args;
+
+kda_status_t kda_linear_recurrent_step(const kda_linear_step_args *args, struct CUstream_st *stream);
+
+/* ------------------------------------------------------------- kda_state_copy
+ * Upkeep of a pool of recurrent states (the slots that kda_recurrent_step and its kin read through
+ * state_indices): for p = 0 .. P - 1, in this order, slot dst[p] of dst_pool becomes a copy of slot
+ * src[p] of src_pool.  The pools may be one and the same (forking a prompt's state, compacting a pool:
+ * a later pair sees what an earlier one wrote) or must not overlap (saving and restoring states).
+ * src[p] = -1 clears the slot to zeros; dst[p] = -1 skips the pair.  Any other index outside its pool
+ * sets KDA_ERR_BAD_STATE_INDEX and the pair is skipped.  Slots are slot_bytes apart, a multiple of 16
+ * (any element type), copied bit for bit. */
+typedef struct {
+    const void *src_pool;          /* [src_slots] slots, 16-byte aligned; NULL if every src is -1 and src_slots is 0 */
+    void *dst_pool;                /* [dst_slots] slots, 16-byte aligned */
+    int64_t slot_bytes;
+    int64_t src_slots, dst_slots;  /* at most 2^31 - 1 each */
+    int64_t P;                     /* pairs */
+    const int32_t *src, *dst;      /* [P] device */
+} kda_state_copy_args;
+
+kda_status_t kda_state_copy(const kda_state_copy_args *args, struct CUstream_st *stream);
+
+/* ------------------------------------------------------------------- kda_rope
+ * Rotary positions on q and k (either may be absent): pair i of the first `rot` channels of every head,
+ * (x_a, x_b), becomes scale * (x_a cos - x_b sin, x_b cos + x_a sin) with the angle positions[t] * freqs[i];
+ * further channels are copied.  Pairs are (i, i + rot / 2) (KDA_ROPE_HALF) or (2 i, 2 i + 1)
+ * (KDA_ROPE_INTERLEAVED).  inverse = 1 turns by the opposite angle, which is also the gradient:
+ * dL/dx = kda_rope(dL/dy, inverse = 1).  Long contexts are a matter of freqs and scale.
+ *
+ * freqs is a HOST array of rot / 2 doubles, radians per position (at most 1e6 in size), copied during the call (a captured
+ * call keeps the values).  Angles are reduced in 64-bit fixed point turns, so that no position of an
+ * int32 loses accuracy; sine and cosine are fp32, each output is rounded once to dtype.
+ * A token's heads are contiguous, [H, d]; tokens are *_stride elements apart (0: H * d, dense), so a view of a
+ * fused projection can be rotated where it lies.  An output may be its input (same pointer and stride) and must not
+ * overlap it, or another tensor of the call, otherwise.  Rows whose addresses are multiples of 16 bytes move as
+ * 16-byte vectors; others by single elements. */
+#define KDA_ROPE_HALF 0
+#define KDA_ROPE_INTERLEAVED 1
+typedef struct {
+    int64_t T;
+    int32_t Hq, Hk;                /* heads of q and k; 0: absent */
+    int32_t d;                     /* channels of a head, 2 .. 1024 */
+    int32_t rot;                   /* rotated channels, even, 2 .. min(d, 256) */
+    kda_dtype_t dtype;
+    int32_t layout, inverse;
+    float scale;
+    const int32_t *positions;      /* [T] device, any int32 */
+    const double *freqs;           /* [rot / 2] HOST */
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} kda_rope_args;
+
+kda_status_t kda_rope(const kda_rope_args *args, struct CUstream_st *stream);
+
 /* ------------------------------------------------------------------ errors */
 const char *kda_status_string(kda_status_t status);
 
@@ -391,7 +537,8 @@ int kda_abi_version(void);
 /* ------------------------------------------------------------- debug checks
  * Not an operation of the paper: optional checks for debugging a model.  With KDA_CHECK_FINITE set,
  * every entry point that writes results (kda_gate, kda_chunk_fwd and kda_chunk_fwd_static_ws,
- * kda_recurrent_step, kda_recurrent_replay, kda_output_gate, kda_chunk_bwd) launches one more pass
+ * kda_recurrent_step, kda_recurrent_replay, kda_output_gate, kda_chunk_bwd, the three kda_linear_* calls
+ * and kda_rope where its outputs are dense) launches one more pass
  * over what it wrote (outputs, final or updated states, gradients) that sets KDA_ERR_NUMERIC in the
  * device error word (kda_get_device_error) when any value is NaN or infinite.  The pass reads those
  * results once more from HBM.  Index checks need no switch: cu_seqlens contents, state indices and

@@ -41,6 +41,8 @@ size_t dtype_size(kda_dtype_t t) { return t == KDA_BF16 ? 2 : 4; }
 
 }  // namespace
 
+kda_status_t kda_check_device() { return check_device(); }
+
 namespace {
 constexpr int kMaxProfileEvents = 16;
 cudaEvent_t g_prof_events[kMaxProfileEvents];

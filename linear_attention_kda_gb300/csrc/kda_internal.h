@@ -105,3 +105,15 @@ size_t kda_chunk_bwd_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv);
 // segments when the whole pass does not fit (segments of 16 chunks at this size).
 size_t kda_chunk_bwd_min_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv);
 kda_status_t kda_launch_chunk_bwd(const kda_chunk_bwd_args *a, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+// Linear attention with a decay per head, state-slot copies and rotary positions (kda_linear_api.cu checks the
+// arguments; these launch).
+kda_status_t kda_check_device();  // KDA_OK on a current device of compute capability 10.3
+size_t kda_linear_fwd_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv, kda_dtype_t dtype);
+size_t kda_linear_bwd_layout_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv,
+                                   kda_dtype_t dtype);
+kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStream_t stream);
+kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream);
+kda_status_t kda_launch_linear_step(const kda_linear_step_args *a, cudaStream_t stream);
+kda_status_t kda_launch_state_copy(const kda_state_copy_args *a, cudaStream_t stream);
+kda_status_t kda_launch_rope(const kda_rope_args *a, cudaStream_t stream);

@@ -1,0 +1,92 @@
+// Shared by the linear-attention kernels (a decay per head): where the chunks of a packed batch lie, and the
+// cumulative log-decays of one chunk.
+#pragma once
+#include "kda_common.cuh"
+
+namespace kda {
+namespace lin {
+
+// Sequence n's tokens, [a, b).  False (and the device error set by one caller) where cu_seqlens is not
+// 0 = c_0 <= ... <= c_N = T around it: nothing out of range is ever formed from it.
+struct span {
+    int64_t a, b;
+};
+__device__ __forceinline__ int64_t seq_start(const int32_t *cu, int64_t T, int64_t N, int64_t n) {
+    return cu ? (int64_t)cu[n] : n * (T / N);
+}
+__device__ __forceinline__ bool seq_span(const int32_t *cu, int64_t T, int64_t N, int64_t n, span *s) {
+    s->a = seq_start(cu, T, N, n);
+    s->b = seq_start(cu, T, N, n + 1);
+    return s->a >= 0 && s->a <= s->b && s->b <= T && (n > 0 || s->a == 0) && (n < N - 1 || s->b == T);
+}
+
+// Chunks need no plan kernel: sequence n's first chunk has slot a / C + n, and since
+// ceil((b - a) / C) <= b / C - a / C + 1, its chunks end before the next sequence's begin.  A batch has
+// T / C + N slots, a few of which stay empty.
+__host__ __device__ __forceinline__ int64_t chunk_slots(int64_t T, int64_t N, int C) { return T / C + N; }
+
+struct chunk {
+    int64_t tok0;  // first token
+    int len;       // tokens, 1 .. C
+};
+// The chunk in a slot (false: an empty slot, or a sequence with a bad range).  Every lane of a warp calls it: the
+// 32 lanes search the sequences 32 ways at once.
+template <int C>
+__device__ __forceinline__ bool find_chunk(const int32_t *cu, int64_t T, int64_t N, int64_t slot, chunk *c) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, hi = N;
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const bool at_or_before = i < hi && seq_start(cu, T, N, i) / C + i <= slot;
+        const unsigned m = __ballot_sync(0xffffffffu, at_or_before);
+        lo += (m ? 31 - __clz(m) : 0) * step;
+        hi = hi < lo + step ? hi : lo + step;
+    }
+    span s;
+    if (!seq_span(cu, T, N, lo, &s)) return false;
+    const int64_t i = slot - (s.a / C + lo), t = s.a + i * C;
+    if (i < 0 || t >= s.b) return false;
+    c->tok0 = t;
+    c->len = (int)(s.b - t < C ? s.b - t : C);
+    return true;
+}
+
+// A log-decay below -104 counts as -104 (exp of it is 0 in fp32); a NaN stays one.
+__device__ __forceinline__ double clamp_decay(float g) { return g < -104.f ? -104.0 : (double)g; }
+
+// Cumulative log-decays G of one chunk, by one warp.  Sums run in fp64 and are kept as fp32 pairs hi + lo: the
+// difference of two of them, (hi_r - hi_j) + (lo_r - lo_j), is then good to an fp32 rounding of itself even where
+// many erasing decays have made both large.
+template <int C>
+__device__ __forceinline__ void chunk_decays(const float *g, int g_stride, int len, float *hi, float *lo) {
+    static_assert(C % 32 == 0, "lanes");
+    constexpr int P = C / 32;
+    const int lane = threadIdx.x & 31;
+    double x[P], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int r = lane * P + i;
+        x[i] = g && r < len ? clamp_decay(g[(int64_t)r * g_stride]) : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        sum += x[i];
+        x[i] = sum;
+    }
+    double pre = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, pre, off);
+        if (lane >= off) pre += y;
+    }
+    pre -= sum;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const double G = pre + x[i];
+        hi[lane * P + i] = (float)G;
+        lo[lane * P + i] = (float)(G - (double)(float)G);
+    }
+}
+
+}  // namespace lin
+}  // namespace kda

@@ -8,6 +8,7 @@ built or cannot be loaded, every call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional
@@ -33,7 +34,9 @@ EXPORTED = ["kda_gate", "kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_re
             "kda_last_cuda_error", "kda_chunk_fwd_schedule", "kda_output_gate", "kda_recurrent_replay",
             "kda_chunk_fwd_workspace_size_gate", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size",
             "kda_selftest_bounded_wait", "kda_set_debug_checks", "kda_set_chunk_schedule",
-            "kda_chunk_bwd_workspace_size_min"]
+            "kda_chunk_bwd_workspace_size_min", "kda_linear_chunk_fwd", "kda_linear_chunk_fwd_workspace_size",
+            "kda_linear_chunk_bwd", "kda_linear_chunk_bwd_workspace_size", "kda_linear_recurrent_step",
+            "kda_state_copy", "kda_rope"]
 STATIC_WORKSPACE_BYTES = 64 << 20
 
 _vp = ctypes.c_void_p
@@ -82,6 +85,39 @@ class StepArgs(ctypes.Structure):
                 ("q", _vp), ("k", _vp), ("z", _vp), ("v", _vp), ("beta", _vp),
                 ("dt_bias", _vp), ("A_log", _vp), ("g_min", _f32), ("scale", _f32),
                 ("state", _vp), ("state_indices", _vp), ("num_slots", _i64), ("o", _vp), ("gate_kind", _i32)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64), ("H", _i32), ("Hq", _i32), ("Hk", _i32), ("Hv", _i32), ("dk", _i32),
+                ("dv", _i32), ("dtype", ctypes.c_int), ("q", _vp), ("k", _vp), ("v", _vp), ("g", _vp),
+                ("g_per_token", _i32), ("scale", _f32), ("cu_seqlens", _vp), ("initial_state", _vp),
+                ("final_state", _vp), ("o", _vp)]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64), ("H", _i32), ("Hq", _i32), ("Hk", _i32), ("Hv", _i32), ("dk", _i32),
+                ("dv", _i32), ("dtype", ctypes.c_int), ("q", _vp), ("k", _vp), ("v", _vp), ("g", _vp),
+                ("g_per_token", _i32), ("scale", _f32), ("cu_seqlens", _vp), ("initial_state", _vp), ("grad_o", _vp),
+                ("grad_final_state", _vp), ("grad_q", _vp), ("grad_k", _vp), ("grad_v", _vp), ("grad_g", _vp),
+                ("grad_initial_state", _vp)]
+
+
+class LinearStepArgs(ctypes.Structure):
+    _fields_ = [("N", _i64), ("H", _i32), ("Hq", _i32), ("Hk", _i32), ("Hv", _i32), ("dk", _i32), ("dv", _i32),
+                ("dtype", ctypes.c_int), ("q", _vp), ("k", _vp), ("v", _vp), ("g", _vp), ("g_per_token", _i32),
+                ("scale", _f32), ("state", _vp), ("state_indices", _vp), ("num_slots", _i64), ("o", _vp)]
+
+
+class StateCopyArgs(ctypes.Structure):
+    _fields_ = [("src_pool", _vp), ("dst_pool", _vp), ("slot_bytes", _i64), ("src_slots", _i64), ("dst_slots", _i64),
+                ("P", _i64), ("src", _vp), ("dst", _vp)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("Hq", _i32), ("Hk", _i32), ("d", _i32), ("rot", _i32), ("dtype", ctypes.c_int),
+                ("layout", _i32), ("inverse", _i32), ("scale", _f32), ("positions", _vp), ("freqs", _vp), ("q", _vp),
+                ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("q_stride", _i64), ("k_stride", _i64),
+                ("q_out_stride", _i64), ("k_out_stride", _i64)]
 
 
 class KDAError(RuntimeError):
@@ -144,6 +180,17 @@ def load_library(path: Optional[str] = None):
         L.kda_recurrent_replay.restype = ctypes.c_int
         L.kda_output_gate.argtypes = [ctypes.POINTER(OutputGateArgs), _vp]
         L.kda_output_gate.restype = ctypes.c_int
+        for name, struct in (("kda_linear_chunk_fwd", LinearArgs), ("kda_linear_chunk_bwd", LinearBwdArgs)):
+            getattr(L, name).argtypes = [ctypes.POINTER(struct), _vp, ctypes.c_size_t, _vp]
+            getattr(L, name).restype = ctypes.c_int
+        for name, struct in (("kda_linear_recurrent_step", LinearStepArgs), ("kda_state_copy", StateCopyArgs),
+                             ("kda_rope", RopeArgs)):
+            getattr(L, name).argtypes = [ctypes.POINTER(struct), _vp]
+            getattr(L, name).restype = ctypes.c_int
+        L.kda_linear_chunk_fwd_workspace_size.argtypes = [_i64, _i64, _i32, _i32, _i32, ctypes.c_int]
+        L.kda_linear_chunk_fwd_workspace_size.restype = ctypes.c_size_t
+        L.kda_linear_chunk_bwd_workspace_size.argtypes = [_i64, _i64] + [_i32] * 6 + [ctypes.c_int]
+        L.kda_linear_chunk_bwd_workspace_size.restype = ctypes.c_size_t
         L.kda_last_cuda_error.argtypes = []
         L.kda_last_cuda_error.restype = _i32
         _lib = L
@@ -361,6 +408,266 @@ def recurrent_replay(cached, n_replay, new, n_commit, dt_bias, A_log, state, *, 
                    gate_kind=_gate_kind(gate))
     _check(L.kda_recurrent_replay(ctypes.byref(a), _stream(q)), "kda_recurrent_replay")
     return o
+
+
+# ---------------------------------------------------------------- linear attention with a decay per head
+def _tensors(where: str, device, **ts):
+    """Checks name=(tensor, shape, dtype) of one call: shape, dtype, dense layout, one CUDA device (None passes)."""
+    for name, (t, shape, dtype) in ts.items():
+        if t is None:
+            continue
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{where}: {name} is {t.dtype}, not {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, not {device}")
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+
+
+def _linear_shapes(where, q, k, v, g):
+    """Heads, head sizes and the log-decay's layout of a linear-attention call."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"{where}: q, k and v have three dimensions (rows, heads, channels)")
+    T, Hq, dk = q.shape
+    Hk, Hv, dv = k.shape[1], v.shape[1], v.shape[2]
+    H = max(Hq, Hk, Hv)
+    _dtype_code(q)
+    if g is not None and g.dim() not in (1, 2):
+        raise ValueError(f"{where}: g has shape [rows, heads] or [heads]")
+    gshape = None if g is None else (T, H) if g.dim() == 2 else (H,)
+    spec = dict(q=(q, (T, Hq, dk), q.dtype), k=(k, (T, Hk, dk), q.dtype), v=(v, (T, Hv, dv), q.dtype),
+                g=(g, gshape, torch.float32))
+    return T, H, Hq, Hk, Hv, dk, dv, int(g is not None and g.dim() == 2), spec
+
+
+def _n_sequences(where, T, cu_seqlens, n_seq):
+    if cu_seqlens is None:
+        return n_seq
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError(f"{where}: cu_seqlens has shape [sequences + 1]")
+    return cu_seqlens.numel() - 1
+
+
+def _workspace(where, workspace, need, device):
+    if workspace is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{where}: the workspace must be contiguous and on {device}")
+    return workspace
+
+
+def linear_chunk_fwd_workspace_size(T, N, H, dk, dv, dtype: torch.dtype) -> int:
+    """kda_linear_chunk_fwd_workspace_size (bytes; 0 on invalid sizes)."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(load_library().kda_linear_chunk_fwd_workspace_size(T, N, H, dk, dv, code))
+
+
+def linear_chunk_bwd_workspace_size(T, N, H, dk, dv, dtype: torch.dtype, Hq=None, Hk=None, Hv=None) -> int:
+    """kda_linear_chunk_bwd_workspace_size (bytes; 0 on invalid sizes)."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(load_library().kda_linear_chunk_bwd_workspace_size(T, N, H, Hq or H, Hk or H, Hv or H, dk, dv, code))
+
+
+def linear_chunk_fwd(q, k, v, g=None, *, scale: float = 1.0, cu_seqlens: Optional[torch.Tensor] = None,
+                     n_seq: int = 1, initial_state: Optional[torch.Tensor] = None, output_final_state: bool = False,
+                     final_state: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None):
+    """kda_linear_chunk_fwd: linear attention with a decay per head over whole sequences,
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  Returns (o, final_state).
+
+    q [T, Hq, dk], k [T, Hk, dk], v [T, Hv, dv] (fp32 or bf16; H = the largest head count, a multiple of the
+    others); g: log-decay, at most 0, fp32 [T, H] or [H], or None (no decay); states fp32 [N, H, dk, dv]."""
+    where, L = "linear_chunk_fwd", load_library()
+    T, H, Hq, Hk, Hv, dk, dv, per_token, spec = _linear_shapes(where, q, k, v, g)
+    N = _n_sequences(where, T, cu_seqlens, n_seq)
+    state, f32 = (N, H, dk, dv), torch.float32
+    _tensors(where, q.device, **spec, cu_seqlens=(cu_seqlens, (N + 1,), torch.int32),
+             initial_state=(initial_state, state, f32), final_state=(final_state, state, f32),
+             out=(out, (T, H, dv), q.dtype))
+    with torch.cuda.device(q.device):
+        o = out if out is not None else torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        fs = final_state
+        if fs is None and output_final_state:
+            fs = torch.empty(state, dtype=f32, device=q.device)
+        workspace = _workspace(where, workspace, linear_chunk_fwd_workspace_size(T, N, H, dk, dv, q.dtype), q.device)
+        a = LinearArgs(T=T, N=N, H=H, Hq=Hq, Hk=Hk, Hv=Hv, dk=dk, dv=dv, dtype=_dtype_code(q), q=_ptr(q), k=_ptr(k),
+                       v=_ptr(v), g=_ptr(g), g_per_token=per_token, scale=scale, cu_seqlens=_ptr(cu_seqlens),
+                       initial_state=_ptr(initial_state), final_state=_ptr(fs), o=_ptr(o))
+        _check(L.kda_linear_chunk_fwd(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream(q)), "kda_linear_chunk_fwd")
+    return o, fs
+
+
+def linear_chunk_bwd(q, k, v, g, grad_o, *, scale: float = 1.0, cu_seqlens: Optional[torch.Tensor] = None,
+                     n_seq: int = 1, initial_state: Optional[torch.Tensor] = None,
+                     grad_final_state: Optional[torch.Tensor] = None, decay_grad: bool = True,
+                     state_grad: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """kda_linear_chunk_bwd: gradients of linear_chunk_fwd given grad_o (and grad_final_state).
+
+    Returns a dict with q, k, v (shapes and dtype of the inputs) and, when asked, g (fp32, the shape of g; not
+    without g) and initial_state (fp32 [N, H, dk, dv])."""
+    where, L = "linear_chunk_bwd", load_library()
+    T, H, Hq, Hk, Hv, dk, dv, per_token, spec = _linear_shapes(where, q, k, v, g)
+    N = _n_sequences(where, T, cu_seqlens, n_seq)
+    state, f32 = (N, H, dk, dv), torch.float32
+    _tensors(where, q.device, **spec, cu_seqlens=(cu_seqlens, (N + 1,), torch.int32), grad_o=(grad_o, (T, H, dv), q.dtype),
+             initial_state=(initial_state, state, f32), grad_final_state=(grad_final_state, state, f32))
+    with torch.cuda.device(q.device):
+        grads = {n: torch.empty_like(x) for n, x in (("q", q), ("k", k), ("v", v))}
+        if decay_grad and g is not None:
+            grads["g"] = torch.empty_like(g)
+        if state_grad:
+            grads["initial_state"] = torch.empty(state, dtype=f32, device=q.device)
+        need = linear_chunk_bwd_workspace_size(T, N, H, dk, dv, q.dtype, Hq, Hk, Hv)
+        workspace = _workspace(where, workspace, need, q.device)
+        a = LinearBwdArgs(T=T, N=N, H=H, Hq=Hq, Hk=Hk, Hv=Hv, dk=dk, dv=dv, dtype=_dtype_code(q), q=_ptr(q), k=_ptr(k),
+                          v=_ptr(v), g=_ptr(g), g_per_token=per_token, scale=scale, cu_seqlens=_ptr(cu_seqlens),
+                          initial_state=_ptr(initial_state), grad_o=_ptr(grad_o),
+                          grad_final_state=_ptr(grad_final_state), grad_q=_ptr(grads["q"]), grad_k=_ptr(grads["k"]),
+                          grad_v=_ptr(grads["v"]), grad_g=_ptr(grads.get("g")),
+                          grad_initial_state=_ptr(grads.get("initial_state")))
+        _check(L.kda_linear_chunk_bwd(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream(q)), "kda_linear_chunk_bwd")
+    return grads
+
+
+def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, state_indices: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None):
+    """kda_linear_recurrent_step: one decode token per sequence of linear attention with a decay per head; `state`
+    [slots, H, dk, dv] is updated in place.  Shapes as linear_chunk_fwd with N rows; state_indices int32 [N] (-1: an
+    unused row of a padded batch, left alone with its row of the output).  Returns o [N, H, dv]."""
+    where, L = "linear_recurrent_step", load_library()
+    N, H, Hq, Hk, Hv, dk, dv, per_token, spec = _linear_shapes(where, q, k, v, g)
+    if state.dim() != 4:
+        raise ValueError(f"{where}: state has shape [slots, heads, dk, dv]")
+    _tensors(where, q.device, **spec, state=(state, (state.shape[0], H, dk, dv), torch.float32),
+             state_indices=(state_indices, (N,), torch.int32), out=(out, (N, H, dv), q.dtype))
+    if N > 0 and state.shape[0] < (1 if state_indices is not None else N):
+        raise ValueError(f"{where}: {state.shape[0]} state slots for {N} sequences")
+    with torch.cuda.device(q.device):
+        o = out if out is not None else torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        a = LinearStepArgs(N=N, H=H, Hq=Hq, Hk=Hk, Hv=Hv, dk=dk, dv=dv, dtype=_dtype_code(q), q=_ptr(q), k=_ptr(k),
+                           v=_ptr(v), g=_ptr(g), g_per_token=per_token, scale=scale, state=_ptr(state),
+                           state_indices=_ptr(state_indices), num_slots=state.shape[0], o=_ptr(o))
+        _check(L.kda_linear_recurrent_step(ctypes.byref(a), _stream(q)), "kda_linear_recurrent_step")
+    return o
+
+
+# ---------------------------------------------------------------- upkeep of state pools
+def state_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, *, out_pool: Optional[torch.Tensor] = None):
+    """kda_state_copy: slot dst[p] becomes a copy of slot src[p], for p = 0, 1, ... in this order; src[p] = -1 clears
+    the slot, dst[p] = -1 skips the pair.  pool, out_pool: [slots, ...] of any dtype (a slot's bytes a multiple of
+    16); out_pool, by default the pool itself, is changed in place and returned.  src, dst: int32 [P]."""
+    where, L = "state_copy", load_library()
+    to = pool if out_pool is None else out_pool
+    if pool.dim() < 2 or src.dim() != 1:
+        raise ValueError(f"{where}: pool has shape [slots, ...] and src one dimension")
+    _tensors(where, pool.device, pool=(pool, pool.shape, pool.dtype),
+             out_pool=(to, (to.shape[0],) + tuple(pool.shape[1:]), pool.dtype), src=(src, src.shape, torch.int32),
+             dst=(dst, src.shape, torch.int32))
+    slot = pool[0].numel() * pool.element_size() if pool.shape[0] else to[0].numel() * to.element_size() if to.shape[0] else 0
+    with torch.cuda.device(pool.device):
+        a = StateCopyArgs(src_pool=_ptr(pool), dst_pool=_ptr(to), slot_bytes=slot, src_slots=pool.shape[0],
+                          dst_slots=to.shape[0], P=src.numel(), src=_ptr(src), dst=_ptr(dst))
+        _check(L.kda_state_copy(ctypes.byref(a), _stream(pool)), "kda_state_copy")
+    return to
+
+
+# ---------------------------------------------------------------- rotary positions
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0, *,
+                     original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0) -> torch.Tensor:
+    """Frequencies of kda.rope, radians per position: float64 [rot / 2] on the host, base^(-2 i / rot).
+
+    scaling for contexts `factor` times as long: None; "linear" (positions interpolated: every frequency divided by
+    factor); "ntk" (the base raised so that the slowest frequency alone is divided by factor); "yarn" (pairs that turn
+    less than beta_slow times over original_length positions as "linear", those that turn more than beta_fast times as
+    they are, a ramp over the pairs' index between them; rope_attention_scale(factor) is the matching scale)."""
+    if rot < 2 or rot % 2 or not base > 1 or not factor > 0:
+        raise ValueError("rope_frequencies: rot is even and at least 2, base above 1, factor above 0")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot == 2:
+            raise ValueError("rope_frequencies: ntk scaling needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * i / rot)
+    if scaling is None or scaling == "ntk":
+        return f
+    if scaling == "linear":
+        return f / factor
+    if scaling != "yarn":
+        raise ValueError('rope_frequencies: scaling is None, "linear", "ntk" or "yarn"')
+    if original_length < 1 or not beta_fast > beta_slow > 0:
+        raise ValueError("rope_frequencies: yarn needs original_length and beta_fast > beta_slow > 0")
+
+    def pair(turns):  # index of the pair that turns this often over the original length
+        return rot * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rot - 1)
+    ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+    return f * (1.0 - ramp) + f / factor * ramp
+
+
+def rope_attention_scale(factor: float) -> float:
+    """The scale that goes with "yarn" frequencies, 0.1 ln(factor) + 1 (1 up to factor 1)."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+
+
+def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor, *,
+         layout: str = "half", scale: float = 1.0, inverse: bool = False, out_q: Optional[torch.Tensor] = None,
+         out_k: Optional[torch.Tensor] = None):
+    """kda_rope: rotary positions on q [T, Hq, d] and k [T, Hk, d] (either may be None).  Returns (q, k) rotated.
+
+    positions: int32 [T] on the device; freqs: float64 [rot / 2] on the host (rope_frequencies), rotating the first
+    rot channels of every head.  layout "half" pairs channel i with i + rot / 2, "interleaved" 2 i with 2 i + 1.
+    inverse=True turns back, which is also the gradient: rope(grad_q, grad_k, ..., inverse=True).  out_q = q rotates in
+    place; q and k may be views with a token stride (heads and channels dense), as slices of a fused projection are."""
+    where, L = "rope", load_library()
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError(f"{where}: q or k is needed")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"{where}: layout must be one of {sorted(ROPE_LAYOUTS)}")
+    if first.dim() != 3:
+        raise ValueError(f"{where}: q and k have three dimensions (tokens, heads, channels)")
+    T, _, d = first.shape
+    if freqs.device.type != "cpu" or freqs.dtype != torch.float64 or freqs.dim() != 1:
+        raise ValueError(f"{where}: freqs is a float64 vector on the host")
+    freqs = freqs.contiguous()
+    _tensors(where, first.device, positions=(positions, (T,), torch.int32))
+
+    def rows(name, x, shape=None):  # a tensor's token stride (0 heads: absent)
+        if x is None:
+            return 0
+        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != d or (shape is not None and x.shape != shape):
+            raise ValueError(f"{where}: {name} has shape {tuple(x.shape)}")
+        if x.dtype != first.dtype:
+            raise TypeError(f"{where}: {name} is {x.dtype}, not {first.dtype}")
+        if x.device != first.device:
+            raise ValueError(f"{where}: {name} is on {x.device}, not {first.device}")
+        H = x.shape[1]
+        if T > 0 and H > 0 and ((d > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != d) or (T > 1 and x.stride(0) < H * d)):
+            raise ValueError(f"{where}: {name}'s heads and channels must be dense, its tokens at most strided")
+        return x.stride(0) if T > 1 else 0
+
+    _dtype_code(first)
+    sq, sk = rows("q", q), rows("k", k)
+    with torch.cuda.device(first.device):
+        yq = None if q is None else out_q if out_q is not None else torch.empty((T,) + tuple(q.shape[1:]), dtype=q.dtype, device=q.device)
+        yk = None if k is None else out_k if out_k is not None else torch.empty((T,) + tuple(k.shape[1:]), dtype=k.dtype, device=k.device)
+        oq, ok = rows("out_q", yq, None if q is None else q.shape), rows("out_k", yk, None if k is None else k.shape)
+        a = RopeArgs(T=T, Hq=0 if q is None else q.shape[1], Hk=0 if k is None else k.shape[1], d=d,
+                     rot=2 * freqs.numel(), dtype=_dtype_code(first), layout=ROPE_LAYOUTS[layout], inverse=int(inverse),
+                     scale=scale, positions=_ptr(positions), freqs=freqs.data_ptr(), q=_ptr(q), k=_ptr(k),
+                     q_out=_ptr(yq), k_out=_ptr(yk), q_stride=sq, k_stride=sk, q_out_stride=oq, k_out_stride=ok)
+        _check(L.kda_rope(ctypes.byref(a), _stream(first)), "kda_rope")
+    return yq, yk
 
 
 def selftest_bounded_wait(device=None) -> tuple:
