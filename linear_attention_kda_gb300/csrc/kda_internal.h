@@ -112,6 +112,9 @@ kda_status_t kda_check_device();  // KDA_OK on a current device of compute capab
 size_t kda_linear_fwd_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv, kda_dtype_t dtype);
 size_t kda_linear_bwd_layout_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv,
                                    kda_dtype_t dtype);
+// bf16 on the tensor cores (T > 0)
+size_t kda_linear_fwd_tc_bytes(int64_t T, int64_t N, int H, int dk, int dv);
+kda_status_t kda_launch_linear_fwd_tc(const kda_linear_args *a, void *ws, cudaStream_t stream, int *err);
 kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_linear_step(const kda_linear_step_args *a, cudaStream_t stream);

@@ -25,29 +25,37 @@ __device__ __forceinline__ bool seq_span(const int32_t *cu, int64_t T, int64_t N
 // T / C + N slots, a few of which stay empty.
 __host__ __device__ __forceinline__ int64_t chunk_slots(int64_t T, int64_t N, int C) { return T / C + N; }
 
-struct chunk {
-    int64_t tok0;  // first token
-    int len;       // tokens, 1 .. C
-};
-// The chunk in a slot (false: an empty slot, or a sequence with a bad range).  Every lane of a warp calls it: the
-// 32 lanes search the sequences 32 ways at once.
-template <int C>
-__device__ __forceinline__ bool find_chunk(const int32_t *cu, int64_t T, int64_t N, int64_t slot, chunk *c) {
+// The sequence and index of the run of W tokens in a slot (false: a slot that lies in no sequence with a good
+// range; the caller compares the index with the sequence's length).  Every lane of a warp calls it: the 32 lanes
+// search the sequences 32 ways at once.
+__device__ __forceinline__ bool find_slot(const int32_t *cu, int64_t T, int64_t N, int64_t W, int64_t slot, int64_t *n,
+                                          int64_t *index, span *s) {
     const int lane = threadIdx.x & 31;
     int64_t lo = 0, hi = N;
     while (hi - lo > 1) {
         const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const bool at_or_before = i < hi && seq_start(cu, T, N, i) / C + i <= slot;
+        const bool at_or_before = i < hi && seq_start(cu, T, N, i) / W + i <= slot;
         const unsigned m = __ballot_sync(0xffffffffu, at_or_before);
         lo += (m ? 31 - __clz(m) : 0) * step;
         hi = hi < lo + step ? hi : lo + step;
     }
+    *n = lo;
+    if (!seq_span(cu, T, N, lo, s)) return false;
+    *index = slot - (s->a / W + lo);
+    return *index >= 0;
+}
+
+struct chunk {
+    int64_t tok0;  // first token
+    int len;       // tokens, 1 .. C
+};
+template <int C>
+__device__ __forceinline__ bool find_chunk(const int32_t *cu, int64_t T, int64_t N, int64_t slot, chunk *c) {
+    int64_t n, i;
     span s;
-    if (!seq_span(cu, T, N, lo, &s)) return false;
-    const int64_t i = slot - (s.a / C + lo), t = s.a + i * C;
-    if (i < 0 || t >= s.b) return false;
-    c->tok0 = t;
-    c->len = (int)(s.b - t < C ? s.b - t : C);
+    if (!find_slot(cu, T, N, C, slot, &n, &i, &s) || s.a + i * C >= s.b) return false;
+    c->tok0 = s.a + i * C;
+    c->len = (int)(s.b - c->tok0 < C ? s.b - c->tok0 : C);
     return true;
 }
 

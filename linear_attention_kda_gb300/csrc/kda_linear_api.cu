@@ -75,7 +75,7 @@ kda_status_t kda_linear_chunk_fwd(const kda_linear_args *a, void *workspace, siz
         !aligned(a->cu_seqlens, 4) || !aligned(a->initial_state, 16) || !aligned(a->final_state, 16))
         return KDA_ERR_MISALIGNED;
     const size_t need = kda_linear_fwd_layout_bytes(a->T, a->N, a->H, a->dk, a->dv, a->dtype);
-    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
     st = kda_check_device();
     if (st != KDA_OK) return st;

@@ -609,7 +609,8 @@ static cudaError_t bwd_t(const kda_linear_bwd_args *a, char *ws, cudaStream_t s,
 }  // namespace lin
 }  // namespace kda
 
-size_t kda_linear_fwd_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv, kda_dtype_t) {
+size_t kda_linear_fwd_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv, kda_dtype_t dtype) {
+    if (dtype == KDA_BF16) return kda_linear_fwd_tc_bytes(T, N, H, dk, dv);
     return kda::lin::up256((size_t)kda::lin::chunk_slots(T, N, kda::lin::C) * H * dk * dv * 4);
 }
 
@@ -620,6 +621,7 @@ size_t kda_linear_bwd_layout_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, 
 kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
+    if (a->dtype == KDA_BF16 && a->T > 0) return kda_launch_linear_fwd_tc(a, ws, stream, err);
     return kda_cuda_status(a->dtype == KDA_BF16 ? kda::lin::fwd_t<kda::bf16>(a, (char *)ws, stream, err)
                                                 : kda::lin::fwd_t<float>(a, (char *)ws, stream, err));
 }

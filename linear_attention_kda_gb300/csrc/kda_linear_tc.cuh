@@ -1,0 +1,166 @@
+// Shared by the tensor-core kernels of linear attention with a decay per head (bf16 tensors, chunks of 128 tokens):
+// tile maps, the decays of a chunk as its kernels use them, and the roles that every chain of chunks has.
+#pragma once
+#include <cuda.h>
+
+#include "kda_internal.h"
+#include "kda_linear.cuh"
+#include "tc_util.cuh"
+
+namespace kda {
+namespace lin {
+namespace tcl {
+
+using namespace kda::tc;
+
+constexpr int C = 128;       // tokens of a chunk: M of every product over tokens
+constexpr int BLK = 32;      // tokens of a decay block (one warp's rows)
+
+// The decays of one chunk.  With G the cumulative log-decay and E_b its value at the end of 32-token block b,
+//     rel_j = G_j - E_{b-1} (from the start of j's block),   w_j = e^{E_b - G_j},
+//     e^{G_r - G_j} = e^{G_r - E_b} w_j for j's block b before r's,   e^{rel_r - rel_j} inside one block,
+// so that 128 x 128 masked decays take 32 + 3 exponentials a row, and a factor never exceeds 1 (for decays).  Only
+// inside a block is a difference of two rounded values formed, off by 2^-24 of the block's whole log-decay, and that
+// goes into bf16 products alone.  A NaN reaches the tokens from its own on, through rel, and what follows its block.
+struct decays {
+    float rel[C];
+    float w[C];
+    float hi[4], lo[4];  // E_b as fp32 pairs
+};
+__device__ __forceinline__ float ends(const decays &d, int a, int b) {  // E_a - E_b; E_{-1} = 0
+    if (a < 0) return b < 0 ? 0.f : -d.hi[b];
+    return b < 0 ? d.hi[a] : (d.hi[a] - d.hi[b]) + (d.lo[a] - d.lo[b]);
+}
+// Sums of two floats each (48 bits): the fp64 pipe of this GPU would take three times as long for a chunk's sums.
+struct ff {
+    float h, l;
+};
+__device__ __forceinline__ ff ff_add(const ff &a, const ff &b) {
+    const float s = a.h + b.h, t = s - a.h, e = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l), h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ float ff_diff(const ff &a, const ff &b) { return (a.h - b.h) + (a.l - b.l); }
+__device__ __forceinline__ ff ff_shfl(const ff &a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
+}
+
+// One warp computes a chunk's decays, four tokens a lane, from log-decays that it has loaded before.
+__device__ __forceinline__ float4 load_log_decays(const float *g, int g_stride, int len) {
+    const int r = (threadIdx.x & 31) * 4;
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = g && r + i < len ? __ldg(g + (int64_t)(r + i) * g_stride) : 0.f;
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void make_decays(const float4 &g, decays &d) {
+    const int lane = threadIdx.x & 31;
+    const float in[4] = {g.x, g.y, g.z, g.w};
+    ff x[4], pre;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const ff y{in[i] < -104.f ? -104.f : in[i], 0.f};
+        x[i] = i ? ff_add(x[i - 1], y) : y;
+    }
+    pre = x[3];  // up to and with this lane
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const ff y = ff_shfl(pre, lane - off);
+        if (lane >= off) pre = ff_add(y, pre);
+    }
+    const ff end = ff_shfl(pre, lane | 7);  // at the block's last lane
+    ff before = ff_shfl(pre, lane - 1);
+    if (lane == 0) before = {0.f, 0.f};
+    const ff start = ff_shfl(before, lane & 24);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const ff G = ff_add(before, x[i]);
+        d.rel[lane * 4 + i] = ff_diff(G, start);
+        d.w[lane * 4 + i] = expf(ff_diff(end, G));
+    }
+    if ((lane & 7) == 7) {
+        d.hi[lane >> 3] = end.h;
+        d.lo[lane >> 3] = end.l;
+    }
+    __syncwarp();
+}
+
+// A bounded wait in a few instructions (a chain's roles together have to fit the instruction cache, and every wait is
+// a copy): attempts of about a microsecond each, given up after a million of them.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+#pragma unroll 1
+    for (int n = 0; n < (1 << 20); ++n) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(1000u) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
+// [T, heads, D] bf16 as (channel, head, token), boxes of 64 channels x 1 head x 128 tokens, 128-byte swizzle: a box
+// lands as the [128 tokens][64 channels] half of an operand tile.  Tokens past T read as zeros.
+bool make_token_map(CUtensorMap *m, const void *base, int64_t T, int heads, int D);
+
+// Chunks j0 .. j0 + N - 1 (16 bytes each) of row `row` of a [128][*] K-major tile times f, in place as its bf16 part,
+// the rest of it to `rest`, by packed bf16 arithmetic: with f = fh + fl in two bf16 parts, hi = bf16(k fh),
+// k fh - hi is a bf16 number exactly (16 bits in all), and lo = bf16(k fl + (k fh - hi)).  Lost: 2^-16 of the row in
+// fl, 2^-16 in lo, at most.
+template <int N>
+__device__ __forceinline__ void scale_chunks(unsigned char *tile, unsigned char *rest, int row, int j0, float f) {
+    const bf16 fh = __float2bfloat16_rn(f), fl = __float2bfloat16_rn(f - __bfloat162float(fh));
+    const __nv_bfloat162 h2 = __halves2bfloat162(fh, fh), l2 = __halves2bfloat162(fl, fl);
+    union chunk16 {
+        uint4 u;
+        __nv_bfloat162 p[4];
+    } x[N], lo;
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j].u = *reinterpret_cast<const uint4 *>(tile + img_chunk_off(C, row, j0 + j));
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (f == 0.f) x[j].u = make_uint4(0, 0, 0, 0);  // erased, whatever the row holds
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 hi = __hmul2(x[j].p[i], h2);
+            lo.p[i] = __hfma2(x[j].p[i], l2, __hfma2(x[j].p[i], h2, __hneg2(hi)));
+            x[j].p[i] = hi;
+        }
+        *reinterpret_cast<uint4 *>(tile + img_chunk_off(C, row, j0 + j)) = x[j].u;
+        *reinterpret_cast<uint4 *>(rest + img_chunk_off(C, row, j0 + j)) = lo.u;
+    }
+}
+template <int N>
+__device__ __forceinline__ void clear_chunks(unsigned char *tile, int row, int j0) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        *reinterpret_cast<uint4 *>(tile + img_chunk_off(C, row, j0 + j)) = make_uint4(0, 0, 0, 0);
+}
+
+template <int N> __device__ __forceinline__ void tmem_load(uint32_t taddr, float *v) {
+    if constexpr (N == 32) tmem_ld32(taddr, v);
+    else tmem_ld16(taddr, v);
+}
+template <int N> __device__ __forceinline__ void tmem_store(uint32_t taddr, const float *v) {
+    if constexpr (N == 32) tmem_st32(taddr, v);
+    else tmem_st16(taddr, v);
+}
+// Meeting of the `threads` threads that share named barrier `id` (1 .. 15).
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+// 32 bytes of a row: one whole sector at a time where the tensor's address allows it (wide), else two halves of one.
+__device__ __forceinline__ void st_row_32B(void *p, const uint32_t *v, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+}  // namespace tcl
+}  // namespace lin
+}  // namespace kda

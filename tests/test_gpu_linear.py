@@ -191,6 +191,21 @@ def test_final_state_over_initial_state(dtype):
     assert torch.equal(o, o2) and torch.equal(S, S2) and S2.data_ptr() == x["initial_state"].data_ptr()
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("lens", [[3000], [2500, 0, 130, 1], [1, 128, 4100]])
+def test_few_long_sequences(dk, dv, lens):
+    """Few chains of many chunks (cut into segments), the final states written over the initial ones."""
+    d = LU.batch(lens, 2, dk, dv, "bf16", sum(lens))
+    o, S = _run_fwd(d)
+    _check_fwd(d, o, S)
+    x = LU.to(d, "cuda")
+    o2, S2 = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["g"], scale=d["scale"], cu_seqlens=x["cu_seqlens"],
+                                  initial_state=x["initial_state"], final_state=x["initial_state"])
+    _no_error()
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    _check_bwd(d, _run_bwd(d))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_split_prompt_equals_whole(dtype):
     """Two calls, the second from the first one's state, against the oracle of the whole."""
