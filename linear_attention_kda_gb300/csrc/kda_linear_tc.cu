@@ -67,12 +67,26 @@ struct work {
     bool last;                             // the sequence's last segment
     int h;
 };
-__device__ __forceinline__ bool find_work(const chain_args &a, work *w) {
+constexpr int SORTED = 128;  // batches of up to this many sequences run longest first
+__device__ __forceinline__ bool find_work(const chain_args &a, work *w, int *n_smem) {
     w->h = (int)(blockIdx.x % a.H);
     w->slot = blockIdx.x / a.H;
     span s;
     if (a.seg == 0) {
         w->n = w->slot;
+        if (a.cu && a.N > 1 && a.N <= SORTED) {
+            if (threadIdx.x < a.N) {  // sequence t is the slot'th longest
+                const int t = threadIdx.x, len = a.cu[t + 1] - a.cu[t];
+                int rank = 0;
+                for (int m = 0; m < (int)a.N; ++m) {
+                    const int l = a.cu[m + 1] - a.cu[m];
+                    rank += l > len || (l == len && m < t);
+                }
+                if (rank == (int)w->slot) *n_smem = t;
+            }
+            __syncthreads();
+            w->n = *n_smem;
+        }
         w->index = 0;
         if (!seq_span(a.cu, a.T, a.N, w->n, &s)) return false;
         w->tok0 = s.a;
@@ -101,10 +115,11 @@ __device__ __forceinline__ void check_seqlens(const int32_t *cu, int64_t T, int6
 // ---------------------------------------------------------------------------------------------------- forward
 template <int DK, int DV> struct fwd_smem {
     static constexpr int TILE = C * (DK > DV ? DK : DV) * 2;
-    static constexpr int SLOTS = 5;
+    static constexpr int SLOTS = 4;
     static constexpr int SIMG = SLOTS * TILE;           // bf16 S, rows dk, 64-column halves of dv
-    static constexpr int LO = SIMG + DK * DV * 2;       // second parts of the scaled keys, and outputs being stored
-    static constexpr int DEC = LO + TILE;
+    static constexpr int LO = SIMG + DK * DV * 2;       // second parts of the scaled keys
+    static constexpr int OUT = LO + C * DK * 2;         // outputs on their way to memory
+    static constexpr int DEC = OUT + C * DV * 2;
     static constexpr int BAR = DEC + 2 * (int)sizeof(decays);
     static constexpr int BYTES = BAR + 256;
 };
@@ -112,16 +127,17 @@ static_assert(sizeof(decays) % 16 == 0, "alignment");
 static_assert(fwd_smem<128, 128>::BYTES <= 227 * 1024, "shared memory");
 
 constexpr int FWD_THREADS = 640;
-enum { T_X = 0, T_D1 = 128, T_D2 = 256, T_S = 384 };  // tensor memory columns; P (bf16) lies over X
+enum { T_X = 0, T_D = 256, T_S = 384 };  // tensor memory columns: X of two chunks in turn (P, bf16, lies over it), outputs, state
 
 // Warps: 0 loads tiles, 1 issues the products, 2 makes the decays; 4-19 work on what the products leave, all of them on
 // one thing after the other: warp w has lane quarter w % 4 and column quarter (w - 4) / 4 of every 128 x 128 piece.
 // (With four warps on each of keys, P, state and outputs instead, every piece took four times as long, most of it
 // one warp's own latency, and a step of the chain 8400 cycles.)
 //
-// Tiles of 128 tokens go through a ring of five slots in the order Q K V Q K V ..., each freed by the product that
-// reads it last: a chunk and two thirds in flight in 160 KB.  Products are issued in the order Q S, (K f)^T V twice,
-// P V, next X, which lets the state's loop run: keys and P are made under Q S, the state under P V and X.
+// Tiles of 128 tokens go through a ring of four slots in the order Q K V Q K V ..., each freed by the product that
+// reads it last.  Products are issued in the order Q S, the next chunk's X, (K f)^T V twice, P V: X is there before
+// its keys are scaled (in place), the state's loop (products, read, scale, image) has the outputs and P made beside
+// it.  Q S lands where P V adds to it, its rows multiplied by e^G in between.
 template <int DK, int DV>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
 linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ chain_args a) {
@@ -130,14 +146,16 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
     decays *dec = reinterpret_cast<decays *>(sm + L::DEC);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *free_ = full + L::SLOTS, *dec_ready = free_ + L::SLOTS,
              *dec_free = dec_ready + 2, *x_done = dec_free + 2, *p_ready = x_done + 1, *s_ready = p_ready + 1,
-             *k_ready = s_ready + 1, *u_done = k_ready + 1, *o_done = u_done + 1, *o_read = o_done + 1, *o_staged = o_read + 1, *o_stored = o_staged + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_stored + 1);
+             *k_ready = s_ready + 1, *u_done = k_ready + 1, *o_done = u_done + 1, *o_read = o_done + 1, *o_staged = o_read + 1, *o_stored = o_staged + 1,
+             *d_done = o_stored + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_done + 1);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (blockIdx.x == 0) check_seqlens(a.cu, a.T, a.N, a.err);
     work w;
-    if (!find_work(a, &w)) return;
+    if (!find_work(a, &w, fail)) return;
+    __syncthreads();  // the place that held the sequence's number is used again
     if (tid == 0) {
         for (int i = 0; i < L::SLOTS; ++i) {
             mbar_init(full + i, 1);
@@ -156,6 +174,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
         mbar_init(o_read, 16);
         mbar_init(o_staged, 16);
         mbar_init(o_stored, 1);
+        mbar_init(d_done, 1);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -174,35 +193,55 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
 
     if (warp == 0) {
         if (lane == 0) {
-            const int hq = w.h / a.rq, hk = w.h / a.rk, hv = w.h / a.rv;
+            const int hs[3] = {w.h / a.rq, w.h / a.rk, w.h / a.rv};
             int sent = 0;
-            for (int t = 0; t < 3 * nc; ++t) {
+            // Tile t goes to shared memory when its slot is free, to L2 AHEAD tiles before
+            constexpr int AHEAD = 0;
+            for (int t = -AHEAD; t < 3 * nc; ++t) {
+                const int ta = t + AHEAD;
+                if (AHEAD > 0 && ta < 3 * nc) {
+                    const int kind = ta % 3;
+                    const CUtensorMap *m = kind == 0 ? &tm.q : kind == 1 ? &tm.k : &tm.v;
+                    for (int b = 0; b < (kind == 2 ? DV : DK) / 64; ++b)
+                        tma_prefetch_3d(m, 64 * b, hs[kind], (int)(w.tok0 + (int64_t)(ta / 3) * C));
+                }
+                if (t < 0) continue;
                 if (t >= L::SLOTS) ok = bar_wait(free_ + t % L::SLOTS, tile_phase(t) ^ 1);
                 if (!ok) break;
-                const int i = t / 3, kind = t % 3, D = kind == 2 ? DV : DK, h = kind == 0 ? hq : kind == 1 ? hk : hv;
+                const int kind = t % 3, D = kind == 2 ? DV : DK;
                 const CUtensorMap *m = kind == 0 ? &tm.q : kind == 1 ? &tm.k : &tm.v;
                 uint64_t *bar = full + t % L::SLOTS;
                 mbar_arrive_expect_tx(bar, C * D * 2);
                 for (int b = 0; b < D / 64; ++b)
-                    tma_load_3d(tile(t) + b * C * 128, m, 64 * b, h, (int)(w.tok0 + (int64_t)i * C), bar);
+                    tma_load_3d(tile(t) + b * C * 128, m, 64 * b, hs[kind], (int)(w.tok0 + (int64_t)(t / 3) * C), bar);
                 sent = t + 1;
             }
             if (!ok)  // copies still in flight land before the block ends
                 for (int t = sent > L::SLOTS ? sent - L::SLOTS : 0; t < sent; ++t) bar_wait(full + t % L::SLOTS, tile_phase(t));
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t id_x = idesc_bf16(128, 128), id_d1 = idesc_bf16(128, DV, false, true),
                            id_u = idesc_bf16(128, DV, true, true);
             constexpr uint32_t KLBO = DK == 128 ? 16384 : 0;  // dk = 64: rows 64 .. 127 repeat rows 0 .. 63, unread
             const uint32_t simg = smem_u32(sm + L::SIMG), klo = smem_u32(sm + L::LO);
+            auto x_of = [&](int i) {
+                const int t = 3 * i;
+                ok = ok && bar_wait(full + t % L::SLOTS, tile_phase(t)) && bar_wait(full + (t + 1) % L::SLOTS, tile_phase(t + 1));
+                if (!ok) return;
+                fence_after_sync();
+                mma_bf16_k(tb + T_X + 128 * (i & 1), smem_u32(tile(t)), C, smem_u32(tile(t + 1)), C, DK / 16, id_x, false);
+                mma_commit(x_done);
+            };
+#pragma unroll 1
             for (int i = -1; i < nc && nc > 0; ++i) {
                 if (i >= 0) {
-                    const uint32_t q = smem_u32(tile(3 * i)), k = smem_u32(tile(3 * i + 1)), v = smem_u32(tile(3 * i + 2));
+                    const uint32_t k = smem_u32(tile(3 * i + 1)), v = smem_u32(tile(3 * i + 2));
                     ok = bar_wait(s_ready, i & 1) && (i == 0 || bar_wait(o_read, (i - 1) & 1));
                     if (!ok) break;
                     fence_after_sync();
-                    mma_bf16_kmn(tb + T_D1, q, C, simg, DK * 128, DK / 16, id_d1, false);
+                    mma_bf16_kmn(tb + T_D, smem_u32(tile(3 * i)), C, simg, DK * 128, DK / 16, id_d1, false);
+                    mma_commit(d_done);
                     mma_commit(free_ + (3 * i) % L::SLOTS);
                     ok = bar_wait(k_ready, i & 1) && bar_wait(full + (3 * i + 2) % L::SLOTS, tile_phase(3 * i + 2));
                     if (!ok) break;
@@ -214,18 +253,12 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                     ok = bar_wait(p_ready, i & 1);
                     if (!ok) break;
                     fence_after_sync();
-                    mma_ts_mn(tb + T_D2, tb + T_X, v, 16384, C / 16, id_d1, false);
+                    mma_ts_mn(tb + T_D, tb + T_X + 128 * (i & 1), v, 16384, C / 16, id_d1, true);
                     mma_commit(o_done);
                     mma_commit(free_ + (3 * i + 2) % L::SLOTS);
                 }
-                const int t = 3 * (i + 1);
-                if (i + 1 < nc) {
-                    ok = bar_wait(full + t % L::SLOTS, tile_phase(t)) && bar_wait(full + (t + 1) % L::SLOTS, tile_phase(t + 1));
-                    if (!ok) break;
-                    fence_after_sync();
-                    mma_bf16_k(tb + T_X, smem_u32(tile(t)), C, smem_u32(tile(t + 1)), C, DK / 16, id_x, false);
-                    mma_commit(x_done);
-                }
+                if (i + 1 < nc) x_of(i + 1);
+                if (!ok) break;
             }
         }
     } else if (warp == 2) {
@@ -243,12 +276,12 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
             if (lane == 0) mbar_arrive(dec_ready + (i & 1));
         }
     } else if (warp == 3) {
-        if (lane == 0) {  // whole chunks of outputs leave through the buffer of the keys' second parts
+        if (lane == 0) {  // whole chunks of outputs leave by TMA
             for (int i = 0; i < nc && len_of(i) == C; ++i) {
                 ok = bar_wait(o_staged, i & 1);
                 if (!ok) break;
                 for (int b = 0; b < DV / 64; ++b)
-                    tma_store_3d(&tm.o, sm + L::LO + b * C * 128, 64 * b, w.h, (int)(w.tok0 + (int64_t)i * C));
+                    tma_store_3d(&tm.o, sm + L::OUT + b * C * 128, 64 * b, w.h, (int)(w.tok0 + (int64_t)i * C));
                 bulk_commit();
                 bulk_wait_read0();
                 mbar_arrive(o_stored);
@@ -321,31 +354,25 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
             }
             // ---- outputs of chunk i - 1
             if (i > 0) {
-                const decays &p = dec[(i - 1) & 1];
-                const float e = a.scale * expf(ends(p, quarter - 1, -1) + p.rel[row]);
+                const int len = len_of(i - 1);
+                if (i > 1) wait(o_stored, i & 1);  // chunk i - 2's have left
                 wait(o_done, (i - 1) & 1);
                 if (!ok) break;
                 fence_after_sync();
-                const int len = len_of(i - 1);
+                float x[CW];
+                tmem_load<CW>(tl + T_D + CW * part, x);
+                fence_before_sync();
+                arrive(o_read);
 #pragma unroll
                 for (int b = 0; b < CW; b += 16) {
-                    float x[16], y[16];
-                    tmem_ld16(tl + T_D1 + CW * part + b, x);
-                    tmem_ld16(tl + T_D2 + CW * part + b, y);
-                    if (b + 16 == CW) {  // all read
-                        fence_before_sync();
-                        arrive(o_read);
-                        if (lane == 0) mbar_arrive(dec_free + ((i - 1) & 1));
-                    }
                     uint32_t u[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        u[c] = pack_bf16(fmaf(e, x[2 * c], a.scale * y[2 * c]), fmaf(e, x[2 * c + 1], a.scale * y[2 * c + 1]));
+                    for (int c = 0; c < 8; ++c) u[c] = pack_bf16(a.scale * x[b + 2 * c], a.scale * x[b + 2 * c + 1]);
                     const int c0 = CW * part + b;
                     if (len == C) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            *reinterpret_cast<uint4 *>(sm + L::LO + img_chunk_off(C, row, c0 / 8 + j)) =
+                            *reinterpret_cast<uint4 *>(sm + L::OUT + img_chunk_off(C, row, c0 / 8 + j)) =
                                 make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
                     } else if (row < len) {  // a sequence's ragged end: the rows behind it are another's
                         st_row_32B(a.o + ((w.tok0 + (int64_t)(i - 1) * C + row) * a.H + w.h) * DV + c0, u, wide);
@@ -359,8 +386,6 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
             if (i == nc) break;
             // ---- keys of chunk i, scaled
             const int len = len_of(i), tk = 3 * i + 1, tv = tk + 1;
-            wait(full + tk % L::SLOTS, tile_phase(tk));
-            if (i > 0) wait(o_stored, (i - 1) & 1);  // what lay in the second parts' buffer is out
             wait(x_done, i & 1);  // X has read the keys
             if (!ok) break;
             fence_after_sync();
@@ -372,12 +397,13 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
             }
             fence_proxy_async();
             arrive(k_ready);
-            // ---- P of chunk i: columns 32 part ..
+            // ---- P of chunk i, columns 32 part .., and the rows of Q S times e^G
             {
+                const uint32_t tx = tl + T_X + 128 * (i & 1);
+                const float rel = d.rel[row];
                 float x[32];
                 uint32_t p[16];
-                if (part <= quarter) tmem_ld32(tl + T_X + 32 * part, x);
-                const float rel = d.rel[row];
+                if (part <= quarter) tmem_ld32(tx + 32 * part, x);
                 if (part < quarter) {
                     const float u = __expf(ends(d, quarter - 1, part) + rel);
 #pragma unroll
@@ -403,10 +429,23 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                 fence_before_sync();
                 bar_sync(1 + quarter, 128);  // the quarter's X is read: P may lie over it
                 fence_after_sync();
-                tmem_st16u(tl + T_X + 16 * part, p);
+                tmem_st16u(tx + 16 * part, p);
+                wait(d_done, i & 1);
+                if (!ok) break;
+                fence_after_sync();
+                const float e = expf(ends(d, quarter - 1, -1) + rel);
+                float y[CW];
+                tmem_load<CW>(tl + T_D + CW * part, y);
+#pragma unroll
+                for (int c = 0; c < CW; ++c) y[c] *= e;
+                tmem_store<CW>(tl + T_D + CW * part, y);
                 tmem_st_wait();
                 fence_before_sync();
-                arrive(p_ready);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(p_ready);
+                    mbar_arrive(dec_free + (i & 1));
+                }
             }
         }
         if (ok && w.last && a.final) {  // the loop's last round has waited for the last state products
@@ -451,7 +490,7 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     work w;
-    if (!find_work(a, &w) || w.last) return;
+    if (!find_work(a, &w, fail) || w.last) return;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(full + i, 1);
