@@ -195,17 +195,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
         if (lane == 0) {
             const int hs[3] = {w.h / a.rq, w.h / a.rk, w.h / a.rv};
             int sent = 0;
-            // Tile t goes to shared memory when its slot is free, to L2 AHEAD tiles before
-            constexpr int AHEAD = 0;
-            for (int t = -AHEAD; t < 3 * nc; ++t) {
-                const int ta = t + AHEAD;
-                if (AHEAD > 0 && ta < 3 * nc) {
-                    const int kind = ta % 3;
-                    const CUtensorMap *m = kind == 0 ? &tm.q : kind == 1 ? &tm.k : &tm.v;
-                    for (int b = 0; b < (kind == 2 ? DV : DK) / 64; ++b)
-                        tma_prefetch_3d(m, 64 * b, hs[kind], (int)(w.tok0 + (int64_t)(ta / 3) * C));
-                }
-                if (t < 0) continue;
+            for (int t = 0; t < 3 * nc; ++t) {
                 if (t >= L::SLOTS) ok = bar_wait(free_ + t % L::SLOTS, tile_phase(t) ^ 1);
                 if (!ok) break;
                 const int kind = t % 3, D = kind == 2 ? DV : DK;
