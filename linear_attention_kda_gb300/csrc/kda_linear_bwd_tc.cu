@@ -1,0 +1,739 @@
+// Gradients of linear attention with a decay per head on the tensor cores: bf16 tensors, chunks of 128 tokens.
+//
+//   linear_bwd_states_tc_kernel  the chains over chunks, forwards S <- e^{G_C} S + (K e^{G_C - G})^T V and backwards
+//                                Lambda <- e^{G_C} Lambda + scale (Q e^G)^T dO; before every chunk the state as it is
+//                                goes to the workspace as operand images in two bf16 parts (hi + lo).
+//   linear_grads_tc_kernel       per (chunk, head): with A = scale Tril[Q K^T * D], dA = scale Tril[dO V^T * D],
+//                                D = e^{G_r - G_t},
+//                                    dQ = scale e^G (dO S^T) + dA K,   dK = f (V Lambda^T) + dA^T Q,
+//                                    dV = f (K Lambda) + A^T dO,       f = e^{G_C - G},
+//                                and the decay's gradient.
+//
+// Numerics: A, dA and the first parts of S and Lambda are rounded to bf16 once; they make bf16 gradients.  The decay's
+// gradient is an fp32 result: the products that it is summed from, Q K^T, dO V^T, dO S^T and V Lambda^T, have exact
+// bf16 operands or both parts of a state (2^-16), and are taken in fp32 before any rounding.
+#include <type_traits>
+
+#include "kda_linear_tc.cuh"
+
+namespace kda {
+namespace lin {
+namespace tcl {
+namespace bw {
+
+constexpr int THREADS = 640;  // warps 0-3: loads, products, decays, stores; 16 warps that work on the results
+
+struct states_dir {
+    CUtensorMap a, b;      // forwards k and v, backwards q and grad_o
+    int ra, rb;            // states per head of each
+    const float *init;     // [N, H, dk, dv] or NULL
+    float *fin;            // likewise
+    unsigned char *images; // [slots, H] x (hi, lo) images, or NULL
+    float scale;
+};
+struct states_maps {
+    states_dir d[2];
+};
+struct states_args {
+    const float *g;
+    int g_stride;
+    const int32_t *cu;
+    int64_t T, N;
+    int H, lo;             // lo: the images' second parts are wanted
+    int *err;
+};
+
+constexpr int W = 64;      // value columns of a CTA
+
+template <int DK> struct states_smem {
+    static constexpr int AT = C * DK * 2, BT = C * W * 2;
+    static constexpr int A = 0, LO = 2 * AT, B = 4 * AT, STG = B + 2 * BT;  // STG: hi and lo images on their way out
+    static constexpr int IMG = DK * W * 2;
+    static constexpr int DEC = STG + 2 * IMG;
+    static constexpr int BAR = DEC + 2 * (int)sizeof(decays);
+    static constexpr int BYTES = BAR + 256;
+};
+
+// The chain of 64 value columns of one (sequence, head), S [dk lanes][64 columns] in tensor memory.  The loop is:
+// product (both parts of the scaled rows), state out and scaled, product; the next chunk's rows are scaled under it.
+template <int DK, int DV>
+__global__ void __launch_bounds__(THREADS, 1)
+linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __grid_constant__ states_args a) {
+    using L = states_smem<DK>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    decays *dec = reinterpret_cast<decays *>(sm + L::DEC);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint64_t *full = bars, *free_ = bars + 2, *dec_ready = bars + 4, *dec_free = bars + 6, *k_ready = bars + 8,
+             *s_ready = bars + 9, *u_done = bars + 10, *stg_full = bars + 11, *stg_free = bars + 12;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 13);
+    int *fail = reinterpret_cast<int *>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool back = blockIdx.y == 1;
+    const states_dir &D = dirs.d[back];
+    const int col = blockIdx.x % (DV / W);
+    const int64_t u = blockIdx.x / (DV / W), n = u / a.H;
+    const int h = (int)(u % a.H);
+    span sp;
+    if (!seq_span(a.cu, a.T, a.N, n, &sp)) {
+        if (tid == 0) set_error(a.err, KDA_ERR_BAD_SEQLENS);
+        return;
+    }
+    const int nc = (int)((sp.b - sp.a + C - 1) / C);
+    const int64_t slot0 = sp.a / C + n;
+    auto chunk_of = [&](int i) { return back ? nc - 1 - i : i; };
+    auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
+    auto len_of = [&](int i) { const int64_t r = sp.b - tok_of(i); return (int)(r < C ? r : C); };
+    if (tid == 0) {
+        for (int i = 0; i < 13; ++i) mbar_init(bars + i, i >= 6 && i <= 9 || i == 11 ? 16 : 1);
+        *fail = 0;
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, W);
+    fence_proxy_async();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tb = *tmem_slot;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, parity)); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int ha = h / D.ra, hb = h / D.rb;
+            int i = 0;
+            for (; i < nc; ++i) {
+                const int s = i & 1, t = (int)tok_of(i);
+                if (i >= 2) ok = bar_wait(free_ + s, ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(full + s, L::AT + L::BT);
+                for (int b = 0; b < DK / 64; ++b) tma_load_3d(sm + L::A + s * L::AT + b * C * 128, &D.a, 64 * b, ha, t, full + s);
+                tma_load_3d(sm + L::B + s * L::BT, &D.b, W * col, hb, t, full + s);
+            }
+            if (!ok)  // copies still in flight land before the block ends
+                for (int j = i > 2 ? i - 2 : 0; j < i; ++j) bar_wait(full + (j & 1), (j >> 1) & 1);
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            const uint32_t id = idesc_bf16(128, W, true, true);
+            constexpr uint32_t ALBO = DK == 128 ? 16384 : 0;  // dk = 64: lanes 64 .. 127 repeat lanes 0 .. 63, unread
+            for (int i = 0; i < nc; ++i) {
+                const int s = i & 1;
+                ok = bar_wait(k_ready, i & 1) && bar_wait(s_ready, i & 1) && bar_wait(full + s, (i >> 1) & 1);
+                if (!ok) break;
+                fence_after_sync();
+                const uint32_t b = smem_u32(sm + L::B + s * L::BT);
+                mma_bf16_mnmn(tb, smem_u32(sm + L::A + s * L::AT), ALBO, b, 16384, C / 16, id, true);
+                mma_bf16_mnmn(tb, smem_u32(sm + L::LO + s * L::AT), ALBO, b, 16384, C / 16, id, true);
+                mma_commit(u_done);
+                mma_commit(free_ + s);
+            }
+        }
+    } else if (warp == 2) {
+        auto load = [&](int i) {
+            const bool in = i < nc;
+            return load_log_decays(a.g && in ? a.g + tok_of(i) * a.g_stride + h : nullptr, a.g_stride, in ? len_of(i) : 0);
+        };
+        float4 g = load(0);
+        for (int i = 0; i < nc; ++i) {
+            const float4 next = load(i + 1);
+            if (i >= 2) wait(dec_free + (i & 1), ((i >> 1) - 1) & 1);
+            if (!ok) break;
+            make_decays(g, dec[i & 1]);
+            g = next;
+            if (lane == 0) mbar_arrive(dec_ready + (i & 1));
+        }
+    } else if (warp == 3) {
+        if (lane == 0 && D.images) {
+            for (int i = 0; i < nc; ++i) {
+                unsigned char *dst = D.images + ((slot0 + chunk_of(i)) * a.H + h) * (int64_t)(2 * DK * DV * 2) + col * L::IMG;
+                ok = bar_wait(stg_full, i & 1);
+                if (!ok) break;
+                bulk_s2g(dst, sm + L::STG, L::IMG);
+                if (a.lo) bulk_s2g(dst + DK * DV * 2, sm + L::STG + L::IMG, L::IMG);
+                bulk_commit();
+                bulk_wait_read0();
+                mbar_arrive(stg_free);
+            }
+        }
+    } else {
+        constexpr int KC = DK / 32, CW = W / 4;
+        const int quarter = warp & 3, part = (warp - 4) >> 2, row = 32 * quarter + lane;
+        const bool mine = row < DK;
+        const uint32_t ts = tmem_addr(tb, 32 * quarter, CW * part);
+        const int64_t at = u * (int64_t)(DK * DV) + (int64_t)row * DV + W * col + CW * part;
+        auto arrive = [&](uint64_t *bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto scale_rows = [&](int i) {
+            const int s = i & 1, len = len_of(i);
+            wait(dec_ready + s, (i >> 1) & 1);
+            wait(full + s, (i >> 1) & 1);
+            if (!ok) return;
+            const decays &d = dec[s];
+            const float f = back ? D.scale * expf(ends(d, quarter - 1, -1) + d.rel[row]) : expf(ends(d, 3, quarter)) * d.w[row];
+            scale_chunks<KC>(sm + L::A + s * L::AT, sm + L::LO + s * L::AT, row, KC * part, row < len ? f : 0.f);
+            if (row >= len) clear_chunks<W / 32>(sm + L::B + s * L::BT, row, W / 32 * part);
+            fence_proxy_async();
+            arrive(k_ready);
+        };
+        float x[CW];
+#pragma unroll
+        for (int c = 0; c < CW; c += 4) {
+            const float4 v = mine && D.init ? *reinterpret_cast<const float4 *>(D.init + at + c) : make_float4(0, 0, 0, 0);
+            x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
+        }
+        if (nc > 0) scale_rows(0);
+        for (int i = 0; i < nc; ++i) {
+            if (i > 0) {
+                wait(u_done, (i - 1) & 1);
+                if (!ok) break;
+                fence_after_sync();
+                tmem_load<CW>(ts, x);
+            }
+            const float all = expf(dec[i & 1].hi[3]);
+            float y[CW];
+#pragma unroll
+            for (int c = 0; c < CW; ++c) y[c] = x[c] * all;
+            tmem_store<CW>(ts, y);
+            tmem_st_wait();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(s_ready);
+                mbar_arrive(dec_free + (i & 1));
+            }
+            if (D.images) {  // under the product
+                if (i > 0) wait(stg_free, (i - 1) & 1);
+                if (!ok) break;
+                if (mine) {
+#pragma unroll
+                    for (int c = 0; c < CW; c += 8) {
+                        uint4 hi, lo;
+                        split2(x[c], x[c + 1], hi.x, lo.x);
+                        split2(x[c + 2], x[c + 3], hi.y, lo.y);
+                        split2(x[c + 4], x[c + 5], hi.z, lo.z);
+                        split2(x[c + 6], x[c + 7], hi.w, lo.w);
+                        unsigned char *p = sm + L::STG + img_chunk_off(DK, row, (CW * part + c) / 8);
+                        *reinterpret_cast<uint4 *>(p) = hi;
+                        *reinterpret_cast<uint4 *>(p + L::IMG) = lo;
+                    }
+                }
+                fence_proxy_async();
+                arrive(stg_full);
+            }
+            if (i + 1 < nc) scale_rows(i + 1);
+            if (!ok) break;
+        }
+        if (ok && D.fin) {
+            if (nc > 0) {
+                wait(u_done, (nc - 1) & 1);
+                fence_after_sync();
+                tmem_load<CW>(ts, x);
+            }
+            if (mine && ok) {
+#pragma unroll
+                for (int c = 0; c < CW; c += 4)
+                    *reinterpret_cast<float4 *>(D.fin + at + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            }
+        } else if (ok && nc > 0) {
+            wait(u_done, (nc - 1) & 1);
+        }
+    }
+    if (!ok) atomicExch(fail, 1);
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tb, W);
+    if (tid == 0 && *fail) set_error(a.err, KDA_ERR_DEVICE_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------------------------------- gradients
+struct grads_maps {
+    CUtensorMap q, k, v, o, dq, dk, dv;
+};
+struct grads_args {
+    const float *g;
+    int g_stride;
+    float scale;
+    const int32_t *cu;
+    int64_t T, N;
+    int H, rq, rk, rv;
+    const unsigned char *states, *adj;  // images of S before and Lambda behind every chunk
+    bf16 *dq, *dk, *dv;
+    float *pq, *pk, *pv;                // fp32 [T, H, d] instead, where heads share a row
+    float *dg, *dg_slot;                // [T, H], or sums over a chunk [slots, H]; neither: no decay gradient
+    int *err;
+};
+
+struct grads_sums {                     // per column quarter (or row quarter) of the chunk's 128 x 128 pieces
+    float row[4][C], col[4][C], qdq[4][C], kdk[4][C], dot[16];
+};
+
+template <int DK, int DV> struct grads_smem {
+    static constexpr int QT = C * DK * 2, VT = C * DV * 2, SI = DK * DV * 2, SQ = C * C * 2;
+    static constexpr int Q = 0, K = Q + QT, O = K + QT;
+    static constexpr int V = O + VT;         // values, then A
+    static constexpr int B0 = V + SQ;        // S hi, then Lambda lo
+    static constexpr int B1 = B0 + SI;       // S lo, then dA
+    static constexpr int B2 = B1 + SQ;       // Lambda hi
+    static constexpr int DEC = B2 + (SI > 9216 ? SI : 9216);
+    static constexpr int RLO = DEC + (int)sizeof(decays);
+    static constexpr int BAR = RLO + C * 4;
+    static constexpr int BYTES = BAR + 128;
+    static_assert(sizeof(grads_sums) <= DEC - B2, "sums lie over Lambda hi once its products are done");
+};
+static_assert(grads_smem<128, 128>::BYTES <= 227 * 1024, "shared memory");
+
+// Sum over the 32 lanes of x[c], for every c: lane c's result.
+__device__ __forceinline__ float transpose_sum(float *x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 16; n > 0; n >>= 1) {
+        const bool up = lane & n;
+#pragma unroll
+        for (int c = 0; c < n; ++c) {
+            const float give = up ? x[c] : x[c + n], keep = up ? x[c + n] : x[c];
+            x[c] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+        }
+    }
+    return x[0];
+}
+// Sum over channels of a row's fp32 values with the bf16 tile's.
+template <int CW>
+__device__ __forceinline__ float row_dot(const float *x, const unsigned char *tile, int row, int c0) {
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < CW; c += 8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(tile + img_chunk_off(C, row, (c0 + c) / 8));
+        s = fmaf(x[c], bf_lo(u.x), s), s = fmaf(x[c + 1], bf_hi(u.x), s);
+        s = fmaf(x[c + 2], bf_lo(u.y), s), s = fmaf(x[c + 3], bf_hi(u.y), s);
+        s = fmaf(x[c + 4], bf_lo(u.z), s), s = fmaf(x[c + 5], bf_hi(u.z), s);
+        s = fmaf(x[c + 6], bf_lo(u.w), s), s = fmaf(x[c + 7], bf_hi(u.w), s);
+    }
+    return s;
+}
+
+enum { T_X = 0, T_Y = 128, T_Q = 256, T_K = 384 };  // tensor memory: X, then dV; Y; dQ; dK
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(THREADS, 1)
+linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_constant__ grads_args a) {
+    using L = grads_smem<DK, DV>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    decays &d = *reinterpret_cast<decays *>(sm + L::DEC);
+    float *rel_lo = reinterpret_cast<float *>(sm + L::RLO);
+    grads_sums &sums = *reinterpret_cast<grads_sums *>(sm + L::B2);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint64_t *f_qk = bars, *f_ov = bars + 1, *f_s = bars + 2, *f_l = bars + 3, *f_ll = bars + 4, *xy_done = bars + 5,
+             *q_done = bars + 6, *k_done = bars + 7, *dot_done = bars + 8, *a_ready = bars + 9, *v_done = bars + 10,
+             *d_ready = bars + 11, *out_done = bars + 12, *dec_ready = bars + 13;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 14);
+    int *fail = reinterpret_cast<int *>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = (int)(blockIdx.x % a.H);
+    const int64_t slot = blockIdx.x / a.H;
+    const bool decay = a.dg || a.dg_slot;
+    chunk c;
+    if (!find_chunk<C>(a.cu, a.T, a.N, slot, &c)) {
+        if (a.dg_slot && tid == 0) a.dg_slot[slot * a.H + h] = 0.f;
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 14; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 ? 16 : 1);
+        *fail = 0;
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    fence_proxy_async();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tb = *tmem_slot;
+    const int len = c.len;
+    const unsigned char *S = a.states + (slot * a.H + h) * (int64_t)(2 * L::SI), *G = a.adj + (slot * a.H + h) * (int64_t)(2 * L::SI);
+    bool ok = true;
+    auto wait = [&](uint64_t *bar) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, 0)); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int t = (int)c.tok0, hq = h / a.rq, hk = h / a.rk, hv = h / a.rv;
+            mbar_arrive_expect_tx(f_qk, 2 * L::QT);
+            for (int b = 0; b < DK / 64; ++b) {
+                tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, hq, t, f_qk);
+                tma_load_3d(sm + L::K + b * C * 128, &tm.k, 64 * b, hk, t, f_qk);
+            }
+            mbar_arrive_expect_tx(f_ov, 2 * L::VT);
+            for (int b = 0; b < DV / 64; ++b) {
+                tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
+                tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, hv, t, f_ov);
+            }
+            mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
+            bulk_g2s(sm + L::B0, S, L::SI, f_s);
+            if (decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
+            mbar_arrive_expect_tx(f_l, L::SI);
+            bulk_g2s(sm + L::B2, G, L::SI, f_l);
+            bool more = decay && bar_wait(q_done, 0) && bar_wait(dot_done, 0);
+            if (decay && !more) ok = false;
+            if (more) {
+                mbar_arrive_expect_tx(f_ll, L::SI);
+                bulk_g2s(sm + L::B0, G + L::SI, L::SI, f_ll);
+            }
+            // copies land before the block ends, whatever the others have given up on
+            ok = bar_wait(f_qk, 0) && ok;
+            ok = bar_wait(f_ov, 0) && ok;
+            ok = bar_wait(f_s, 0) && ok;
+            ok = bar_wait(f_l, 0) && ok;
+            if (more) ok = bar_wait(f_ll, 0) && ok;
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            const uint32_t q = smem_u32(sm + L::Q), k = smem_u32(sm + L::K), o = smem_u32(sm + L::O), v = smem_u32(sm + L::V),
+                           b0 = smem_u32(sm + L::B0), b1 = smem_u32(sm + L::B1), b2 = smem_u32(sm + L::B2);
+            const uint32_t id_c = idesc_bf16(128, 128), id_k = idesc_bf16(128, DK), id_v = idesc_bf16(128, DV, false, true),
+                           id_dq = idesc_bf16(128, DK, false, true), id_dk = idesc_bf16(128, DK, true, true),
+                           id_dv = idesc_bf16(128, DV, true, true);
+            do {
+                if (!(ok = bar_wait(f_qk, 0))) break;
+                fence_after_sync();
+                mma_bf16_k(tb + T_X, q, C, k, C, DK / 16, id_c, false);
+                if (!(ok = bar_wait(f_ov, 0))) break;
+                mma_bf16_k(tb + T_Y, o, C, v, C, DV / 16, id_c, false);
+                mma_commit(xy_done);
+                if (!(ok = bar_wait(f_s, 0))) break;
+                mma_bf16_k(tb + T_Q, o, C, b0, DK, DV / 16, id_k, false);
+                if (decay) mma_bf16_k(tb + T_Q, o, C, b1, DK, DV / 16, id_k, true);
+                mma_commit(q_done);
+                if (!(ok = bar_wait(f_l, 0))) break;
+                mma_bf16_k(tb + T_K, v, C, b2, DK, DV / 16, id_k, false);
+                if (decay) {
+                    if (!(ok = bar_wait(f_ll, 0))) break;
+                    mma_bf16_k(tb + T_K, v, C, b0, DK, DV / 16, id_k, true);
+                }
+                mma_commit(k_done);
+                if (!(ok = bar_wait(a_ready, 0))) break;
+                fence_after_sync();
+                mma_bf16_kmn(tb + T_X, k, C, b2, DK * 128, DK / 16, id_v, false);
+                mma_commit(v_done);
+                if (!(ok = bar_wait(d_ready, 0))) break;
+                fence_after_sync();
+                mma_bf16_kmn(tb + T_Q, b1, C, k, 16384, C / 16, id_dq, true);
+                mma_bf16_mnmn(tb + T_K, b1, 16384, q, 16384, C / 16, id_dk, true);
+                mma_bf16_mnmn(tb + T_X, v, 16384, o, 16384, C / 16, id_dv, true);
+                mma_commit(out_done);
+            } while (false);
+        }
+    } else if (warp == 2) {
+        const float4 g = load_log_decays(a.g ? a.g + c.tok0 * a.g_stride + h : nullptr, a.g_stride, len);
+        make_decays(g, d, rel_lo);
+        if (lane == 0) mbar_arrive(dec_ready);
+    } else if (warp >= 4) {
+        constexpr int KW = DK / 4, VW = DV / 4;
+        const int quarter = warp & 3, part = (warp - 4) >> 2, row = 32 * quarter + lane;
+        const uint32_t tl = tmem_addr(tb, 32 * quarter, 0);
+        auto arrive = [&](uint64_t *bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        float dot = 0.f, qdq = 0.f, kdk = 0.f, w_row = 0.f, w_col = 0.f;
+        if (decay) {  // <S, Lambda>, both parts of each; Lambda's second one straight from memory
+            constexpr int PER = L::SI / 16 / 512;  // 16-byte pieces of a thread
+            uint4 l[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) l[i] = __ldg(reinterpret_cast<const uint4 *>(G + L::SI) + (tid - 128) + 512 * i);
+            wait(f_s);
+            wait(f_l);
+            if (ok) {
+                float acc = 0.f;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int at = ((tid - 128) + 512 * i) * 16;
+                    const uint4 s0 = *reinterpret_cast<const uint4 *>(sm + L::B0 + at), s1 = *reinterpret_cast<const uint4 *>(sm + L::B1 + at),
+                                l0 = *reinterpret_cast<const uint4 *>(sm + L::B2 + at);
+                    const uint4 l1 = l[i];
+                    auto two = [&](uint32_t sh, uint32_t sl, uint32_t lh, uint32_t ll) {
+                        acc = fmaf(bf_lo(sh) + bf_lo(sl), bf_lo(lh) + bf_lo(ll), acc);
+                        acc = fmaf(bf_hi(sh) + bf_hi(sl), bf_hi(lh) + bf_hi(ll), acc);
+                    };
+                    two(s0.x, s1.x, l0.x, l1.x);
+                    two(s0.y, s1.y, l0.y, l1.y);
+                    two(s0.z, s1.z, l0.z, l1.z);
+                    two(s0.w, s1.w, l0.w, l1.w);
+                }
+                dot = acc;
+            }
+            arrive(dot_done);
+        }
+        // ---- A and dA, columns 32 part .. of the chunk, and what the decay's gradient takes from their products
+        wait(dec_ready);
+        wait(xy_done);
+        uint32_t pa[16], pd[16];
+        const float rel = d.rel[row], rlo = rel_lo[row];
+        if (ok) fence_after_sync();
+        if (ok && part <= quarter) {
+            float x[32], y[32];
+            tmem_ld32(tl + T_X + 32 * part, x);
+            tmem_ld32(tl + T_Y + 32 * part, y);
+            const float u = part < quarter ? a.scale * __expf(ends(d, quarter - 1, part) + rel) : 0.f;
+            const bool in = row < len;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float f[2], p[2], q[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int t = 32 * part + e + j;
+                    if (part < quarter) f[j] = u * d.w[t];
+                    else f[j] = a.scale * __expf((rel - d.rel[t]) + (rlo - rel_lo[t]));
+                    const bool keep = in && t <= row;
+                    p[j] = keep ? x[e + j] * f[j] : 0.f;
+                    q[j] = keep ? y[e + j] * f[j] : 0.f;
+                    // what passes from t to r; t = r adds the same to both of its sums and is left out of them
+                    const float wgt = keep && t < row ? x[e + j] * q[j] : 0.f;
+                    w_row += wgt;
+                    x[e + j] = wgt;
+                }
+                pa[e / 2] = pack_bf16(p[0], p[1]);
+                pd[e / 2] = pack_bf16(q[0], q[1]);
+            }
+            if (decay) w_col = transpose_sum(x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pa[e] = pd[e] = 0;
+        }
+        wait(q_done);  // S has been read: dA may lie where its second part was
+        if (decay) wait(dot_done);
+        if (ok) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(sm + L::B1 + img_chunk_off(C, row, 4 * part + j)) =
+                    make_uint4(pd[4 * j], pd[4 * j + 1], pd[4 * j + 2], pd[4 * j + 3]);
+            if (row >= len) {  // rows behind the sequence are another's: they meet zeros, which an infinity would spoil
+                clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
+                clear_chunks<DV / 32>(sm + L::O, row, DV / 32 * part);
+            }
+            // ---- dQ's first part
+            fence_after_sync();
+            float x[KW];
+            tmem_load<KW>(tl + T_Q + KW * part, x);
+            const float e = a.scale * expf(ends(d, quarter - 1, -1) + rel);
+#pragma unroll
+            for (int i = 0; i < KW; ++i) x[i] *= e;
+            if (decay && row < len) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
+            tmem_store<KW>(tl + T_Q + KW * part, x);
+        }
+        wait(k_done);  // the values have been read: A may lie over them
+        const float f = expf(ends(d, 3, quarter)) * d.w[row];
+        if (ok) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(sm + L::V + img_chunk_off(C, row, 4 * part + j)) =
+                    make_uint4(pa[4 * j], pa[4 * j + 1], pa[4 * j + 2], pa[4 * j + 3]);
+            if (row >= len) clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
+            fence_proxy_async();
+            fence_before_sync();
+        }
+        arrive(a_ready);
+        if (ok) {  // ---- dK's first part
+            fence_after_sync();
+            float x[KW];
+            tmem_load<KW>(tl + T_K + KW * part, x);
+#pragma unroll
+            for (int i = 0; i < KW; ++i) x[i] *= f;
+            if (decay && row < len) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
+            tmem_store<KW>(tl + T_K + KW * part, x);
+        }
+        wait(v_done);  // ---- dV's first part; Lambda has been read
+        if (ok) {
+            fence_after_sync();
+            float x[VW];
+            tmem_load<VW>(tl + T_X + VW * part, x);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) x[i] *= f;
+            tmem_store<VW>(tl + T_X + VW * part, x);
+            tmem_st_wait();
+            fence_before_sync();
+        }
+        arrive(d_ready);
+        if (decay) {
+            sums.row[part][row] = w_row;
+            sums.col[quarter][32 * part + lane] = w_col;
+            sums.qdq[part][row] = qdq;
+            sums.kdk[part][row] = kdk;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            if (lane == 0) sums.dot[warp - 4] = dot;
+            bar_sync(1, 512);
+            if (warp == 4 && ok) {
+                // dg_t = sum_{r >= t} (pairs inside the chunk + outputs of S) + sum_{j < t} keys into Lambda
+                //        + e^{G_C} <S, Lambda>; four tokens a lane
+                float p[4], kk[4], after = 0.f, before = 0.f, whole = lane < 16 ? sums.dot[lane] : 0.f;
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
+                whole = __shfl_sync(0xffffffffu, whole, 0) * expf(d.hi[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 4 * lane + i;
+                    p[i] = kk[i] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        p[i] += (sums.row[j][r] - sums.col[j][r]) + sums.qdq[j][r];
+                        kk[i] += sums.kdk[j][r];
+                    }
+                    after += p[i];
+                    before += kk[i];
+                }
+                const float own_after = after, own_before = before;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float x = __shfl_down_sync(0xffffffffu, after, off), y = __shfl_up_sync(0xffffffffu, before, off);
+                    if (lane + off < 32) after += x;
+                    if (lane >= off) before += y;
+                }
+                after -= own_after;    // of later lanes
+                before -= own_before;  // of earlier lanes
+                float out[4], total = 0.f;
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    after += p[i];
+                    out[i] = after;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    out[i] += before + whole;
+                    before += kk[i];
+                    const int r = 4 * lane + i;
+                    if (r < len) {
+                        if (a.dg) a.dg[(c.tok0 + r) * a.H + h] = out[i];
+                        total += out[i];
+                    }
+                }
+                if (a.dg_slot) {
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+                    if (lane == 0) a.dg_slot[slot * a.H + h] = total;
+                }
+            }
+        }
+        wait(out_done);
+        if (ok) {
+            fence_after_sync();
+            // whole chunks leave by TMA from where the tiles were; ragged ends, and fp32 parts of shared heads, row by row
+            auto put = [&](auto width, uint32_t t, unsigned char *stage, bf16 *out, float *shared, int D) {
+                constexpr int N = decltype(width)::value;
+                float x[N];
+                tmem_load<N>(tl + t + N * part, x);
+                const int64_t at = ((c.tok0 + row) * a.H + h) * D + N * part;
+                if (shared) {
+                    if (row < len) {
+#pragma unroll
+                        for (int i = 0; i < N; i += 4)
+                            *reinterpret_cast<float4 *>(shared + at + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int i = 0; i < N; i += 8) {
+                    const uint4 u = make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
+                                               pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
+                    if (len == C) *reinterpret_cast<uint4 *>(stage + img_chunk_off(C, row, (N * part + i) / 8)) = u;
+                    else if (row < len) *reinterpret_cast<uint4 *>(out + at + i) = u;
+                }
+            };
+            put(std::integral_constant<int, KW>{}, T_Q, sm + L::Q, a.dq, a.pq, DK);
+            put(std::integral_constant<int, KW>{}, T_K, sm + L::K, a.dk, a.pk, DK);
+            put(std::integral_constant<int, VW>{}, T_X, sm + L::O, a.dv, a.pv, DV);
+            fence_proxy_async();
+        }
+        bar_sync(1, 512);
+        if (warp == 4 && lane == 0 && ok && len == C) {
+            const int t = (int)c.tok0;
+            if (!a.pq)
+                for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dq, sm + L::Q + b * C * 128, 64 * b, h, t);
+            if (!a.pk)
+                for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dk, sm + L::K + b * C * 128, 64 * b, h, t);
+            if (!a.pv)
+                for (int b = 0; b < DV / 64; ++b) tma_store_3d(&tm.dv, sm + L::O + b * C * 128, 64 * b, h, t);
+            bulk_commit();
+            bulk_wait_read0();
+        }
+    }
+    if (!ok) atomicExch(fail, 1);
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tb, 512);
+    if (tid == 0 && *fail) set_error(a.err, KDA_ERR_DEVICE_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------------------------------- launches
+struct layout {
+    int64_t slots;
+    size_t states, adj, pq, pk, pv, dg, total;
+    layout(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv) {
+        auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+        slots = chunk_slots(T, N, C);
+        const size_t each = up((size_t)slots * H * dk * dv * 4), rk = up((size_t)T * H * dk * 4), rv = up((size_t)T * H * dv * 4);
+        size_t at = 0;
+        states = at, at += each;
+        adj = at, at += each;
+        pq = at, at += Hq != H ? rk : 0;
+        pk = at, at += Hk != H ? rk : 0;
+        pv = at, at += Hv != H ? rv : 0;
+        dg = at, at += up((size_t)slots * H * 4);
+        total = at;
+    }
+};
+
+template <int DK, int DV>
+static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t stream, int *err) {
+    const layout L(a->T, a->N, a->H, a->Hq, a->Hk, a->Hv, DK, DV);
+    const int gs = a->g_per_token ? a->H : 0;
+    states_maps sm;
+    grads_maps gm;
+    if (!make_token_map(&gm.q, a->q, a->T, a->Hq, DK) || !make_token_map(&gm.k, a->k, a->T, a->Hk, DK) ||
+        !make_token_map(&gm.v, a->v, a->T, a->Hv, DV) || !make_token_map(&gm.o, a->grad_o, a->T, a->H, DV) ||
+        !make_token_map(&gm.dq, a->grad_q, a->T, a->Hq, DK) || !make_token_map(&gm.dk, a->grad_k, a->T, a->Hk, DK) ||
+        !make_token_map(&gm.dv, a->grad_v, a->T, a->Hv, DV))
+        return KDA_ERR_CUDA;
+    const int rq = a->H / a->Hq, rk = a->H / a->Hk, rv = a->H / a->Hv;
+    sm.d[0] = {gm.k, gm.v, rk, rv, a->initial_state, nullptr, (unsigned char *)ws + L.states, 1.f};
+    sm.d[1] = {gm.q, gm.o, rq, 1, a->grad_final_state, a->grad_initial_state, (unsigned char *)ws + L.adj, a->scale};
+    const states_args s{a->g, gs, a->cu_seqlens, a->T, a->N, a->H, a->grad_g != nullptr, err};
+    constexpr int smem1 = states_smem<DK>::BYTES, smem2 = grads_smem<DK, DV>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(linear_bwd_states_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_grads_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
+    if (e != cudaSuccess) return kda_cuda_status(e);
+    linear_bwd_states_tc_kernel<DK, DV><<<dim3((unsigned)(a->N * a->H * (DV / W)), 2), THREADS, smem1, stream>>>(sm, s);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return kda_cuda_status(e);
+    grads_args g{};
+    g.g = a->g, g.g_stride = gs, g.scale = a->scale, g.cu = a->cu_seqlens, g.T = a->T, g.N = a->N, g.H = a->H;
+    g.rq = rq, g.rk = rk, g.rv = rv;
+    g.states = (const unsigned char *)ws + L.states, g.adj = (const unsigned char *)ws + L.adj;
+    g.dq = (bf16 *)a->grad_q, g.dk = (bf16 *)a->grad_k, g.dv = (bf16 *)a->grad_v;
+    g.pq = rq > 1 ? (float *)(ws + L.pq) : nullptr;
+    g.pk = rk > 1 ? (float *)(ws + L.pk) : nullptr;
+    g.pv = rv > 1 ? (float *)(ws + L.pv) : nullptr;
+    if (a->grad_g) {
+        if (a->g_per_token) g.dg = a->grad_g;
+        else g.dg_slot = (float *)(ws + L.dg);
+    }
+    g.err = err;
+    linear_grads_tc_kernel<DK, DV><<<(unsigned)(L.slots * a->H), THREADS, smem2, stream>>>(gm, g);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return kda_cuda_status(e);
+    return kda_linear_sum_parts(a, g.pq, g.pk, g.pv, g.dg_slot, L.slots, stream);
+}
+
+}  // namespace bw
+}  // namespace tcl
+}  // namespace lin
+}  // namespace kda
+
+size_t kda_linear_bwd_tc_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv) {
+    return kda::lin::tcl::bw::layout(T, N, H, Hq, Hk, Hv, dk, dv).total;
+}
+
+kda_status_t kda_launch_linear_bwd_tc(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream, int *err) {
+    using namespace kda::lin::tcl::bw;
+    if (a->dk == 128)
+        return a->dv == 128 ? run<128, 128>(a, (char *)ws, stream, err) : run<128, 64>(a, (char *)ws, stream, err);
+    return a->dv == 128 ? run<64, 128>(a, (char *)ws, stream, err) : run<64, 64>(a, (char *)ws, stream, err);
+}

@@ -542,11 +542,23 @@ struct bwd_layout {
 template <typename T>
 static cudaError_t sum_heads(const float *part, void *out, const kda_linear_bwd_args *a, int Hx, int D,
                              cudaStream_t stream) {
-    if (Hx == a->H) return cudaSuccess;
+    if (!part) return cudaSuccess;
     const int64_t want = (a->T * Hx * D + NT - 1) / NT;
     linear_sum_heads_kernel<T><<<(unsigned)(want < 4096 ? want : 4096), NT, 0, stream>>>(
         part, (T *)out, a->T, a->N, a->cu_seqlens, Hx, a->H / Hx, D);
     return cudaGetLastError();
+}
+template <typename T>
+static cudaError_t sum_parts(const kda_linear_bwd_args *a, const float *pq, const float *pk, const float *pv,
+                             const float *dg_slot, int64_t slots, cudaStream_t stream) {
+    cudaError_t e = sum_heads<T>(pq, a->grad_q, a, a->Hq, a->dk, stream);
+    if (e == cudaSuccess) e = sum_heads<T>(pk, a->grad_k, a, a->Hk, a->dk, stream);
+    if (e == cudaSuccess) e = sum_heads<T>(pv, a->grad_v, a, a->Hv, a->dv, stream);
+    if (e == cudaSuccess && dg_slot) {
+        linear_sum_decay_kernel<<<(unsigned)a->H, NT, 0, stream>>>(dg_slot, a->grad_g, slots, a->H);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 template <int DK, int DV, typename T>
@@ -585,14 +597,8 @@ static cudaError_t bwd(const kda_linear_bwd_args *a, char *ws, cudaStream_t stre
     if (e != cudaSuccess) return e;
     linear_grads_kernel<DK, DV, T><<<(unsigned)(slots * a->H), NT, smem, stream>>>(G);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = sum_heads<T>(G.pq, a->grad_q, a, a->Hq, DK, stream);
-    if (e == cudaSuccess) e = sum_heads<T>(G.pk, a->grad_k, a, a->Hk, DK, stream);
-    if (e == cudaSuccess) e = sum_heads<T>(G.pv, a->grad_v, a, a->Hv, DV, stream);
-    if (e == cudaSuccess && G.dg_slot) {
-        linear_sum_decay_kernel<<<(unsigned)a->H, NT, 0, stream>>>(G.dg_slot, a->grad_g, slots, a->H);
-        e = cudaGetLastError();
-    }
-    return e;
+    if (e != cudaSuccess) return e;
+    return sum_parts<T>(a, G.pq, G.pk, G.pv, G.dg_slot, slots, stream);
 }
 
 template <typename T>
@@ -614,7 +620,9 @@ size_t kda_linear_fwd_layout_bytes(int64_t T, int64_t N, int H, int dk, int dv, 
     return kda::lin::up256((size_t)kda::lin::chunk_slots(T, N, kda::lin::C) * H * dk * dv * 4);
 }
 
-size_t kda_linear_bwd_layout_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv, kda_dtype_t) {
+size_t kda_linear_bwd_layout_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv,
+                                   kda_dtype_t dtype) {
+    if (dtype == KDA_BF16) return kda_linear_bwd_tc_bytes(T, N, H, Hq, Hk, Hv, dk, dv);
     return kda::lin::bwd_layout(T, N, H, Hq, Hk, Hv, dk, dv).total;
 }
 
@@ -629,6 +637,13 @@ kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStrea
 kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
+    if (a->dtype == KDA_BF16 && a->T > 0) return kda_launch_linear_bwd_tc(a, ws, stream, err);
     return kda_cuda_status(a->dtype == KDA_BF16 ? kda::lin::bwd_t<kda::bf16>(a, (char *)ws, stream, err)
                                                 : kda::lin::bwd_t<float>(a, (char *)ws, stream, err));
+}
+
+kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const float *pq, const float *pk, const float *pv,
+                                  const float *dg_slot, int64_t slots, cudaStream_t stream) {
+    return kda_cuda_status(a->dtype == KDA_BF16 ? kda::lin::sum_parts<kda::bf16>(a, pq, pk, pv, dg_slot, slots, stream)
+                                                : kda::lin::sum_parts<float>(a, pq, pk, pv, dg_slot, slots, stream));
 }

@@ -52,7 +52,8 @@ __device__ __forceinline__ float4 load_log_decays(const float *g, int g_stride, 
     for (int i = 0; i < 4; ++i) x[i] = g && r + i < len ? __ldg(g + (int64_t)(r + i) * g_stride) : 0.f;
     return make_float4(x[0], x[1], x[2], x[3]);
 }
-__device__ __forceinline__ void make_decays(const float4 &g, decays &d) {
+// (rel_lo: what rel leaves out of G_j - E_{b-1}, where fp32 results are made from differences inside a block.)
+__device__ __forceinline__ void make_decays(const float4 &g, decays &d, float *rel_lo = nullptr) {
     const int lane = threadIdx.x & 31;
     const float in[4] = {g.x, g.y, g.z, g.w};
     ff x[4], pre;
@@ -74,7 +75,9 @@ __device__ __forceinline__ void make_decays(const float4 &g, decays &d) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const ff G = ff_add(before, x[i]);
-        d.rel[lane * 4 + i] = ff_diff(G, start);
+        const ff R = ff_add(G, {-start.h, -start.l});
+        d.rel[lane * 4 + i] = R.h;
+        if (rel_lo) rel_lo[lane * 4 + i] = R.l;
         d.w[lane * 4 + i] = expf(ff_diff(end, G));
     }
     if ((lane & 7) == 7) {
@@ -129,6 +132,13 @@ __device__ __forceinline__ void scale_chunks(unsigned char *tile, unsigned char 
         *reinterpret_cast<uint4 *>(rest + img_chunk_off(C, row, j0 + j)) = lo.u;
     }
 }
+// x = hi + lo of two bf16 each, packed: 2^-16 of x is lost at most
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16(a, b);
+    lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 template <int N>
 __device__ __forceinline__ void clear_chunks(unsigned char *tile, int row, int j0) {
 #pragma unroll
