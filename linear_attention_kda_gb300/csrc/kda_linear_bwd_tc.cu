@@ -28,7 +28,7 @@ struct states_dir {
     int ra, rb;            // states per head of each
     const float *init;     // [N, H, dk, dv] or NULL
     float *fin;            // likewise
-    unsigned char *images; // [slots, H] x (hi, lo) images, or NULL
+    unsigned char *images; // [slots, H] x (hi, lo) images
     float scale;
 };
 struct states_maps {
@@ -46,16 +46,18 @@ struct states_args {
 constexpr int W = 64;      // value columns of a CTA
 
 template <int DK> struct states_smem {
-    static constexpr int AT = C * DK * 2, BT = C * W * 2;
-    static constexpr int A = 0, LO = 2 * AT, B = 4 * AT, STG = B + 2 * BT;  // STG: hi and lo images on their way out
-    static constexpr int IMG = DK * W * 2;
-    static constexpr int DEC = STG + 2 * IMG;
-    static constexpr int BAR = DEC + 2 * (int)sizeof(decays);
+    static constexpr int AT = C * DK * 2, BT = C * W * 2, STAGE = AT + BT, IMG = DK * W * 2;
+    static constexpr int LO = 3 * STAGE;                // second parts of the scaled rows, of two chunks
+    static constexpr int DEC = LO + 2 * AT;
+    static constexpr int BAR = DEC + 3 * (int)sizeof(decays);
     static constexpr int BYTES = BAR + 256;
+    static_assert(2 * IMG <= AT, "a chunk's images leave through the rows' tile of the chunk before");
 };
 
 // The chain of 64 value columns of one (sequence, head), S [dk lanes][64 columns] in tensor memory.  The loop is:
-// product (both parts of the scaled rows), state out and scaled, product; the next chunk's rows are scaled under it.
+// product (both parts of the scaled rows), state out and scaled, product; the images of the state go to memory and
+// the next chunk's rows are scaled under it.  Three stages of tiles: with two, a chunk's tiles were asked for when the
+// last product but one had ended, and their way (2000 cycles) and the scaling (1200) made the step.
 template <int DK, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __grid_constant__ states_args a) {
@@ -63,9 +65,10 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     extern __shared__ __align__(1024) unsigned char sm[];
     decays *dec = reinterpret_cast<decays *>(sm + L::DEC);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
-    uint64_t *full = bars, *free_ = bars + 2, *dec_ready = bars + 4, *dec_free = bars + 6, *k_ready = bars + 8,
-             *s_ready = bars + 9, *u_done = bars + 10, *stg_full = bars + 11, *stg_free = bars + 12;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 13);
+    // in: a chunk's tiles and its decays
+    uint64_t *in = bars, *dec_free = bars + 3, *k_ready = bars + 6, *s_ready = bars + 7, *u_done = bars + 8,
+             *stg_full = bars + 9, *stg_done = bars + 10;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 11);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool back = blockIdx.y == 1;
@@ -84,7 +87,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
     auto len_of = [&](int i) { const int64_t r = sp.b - tok_of(i); return (int)(r < C ? r : C); };
     if (tid == 0) {
-        for (int i = 0; i < 13; ++i) mbar_init(bars + i, i >= 6 && i <= 9 || i == 11 ? 16 : 1);
+        for (int i = 0; i < 11; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 8 || i == 10 ? 1 : 16);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, W);
@@ -101,57 +104,57 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             const int ha = h / D.ra, hb = h / D.rb;
             int i = 0;
             for (; i < nc; ++i) {
-                const int s = i & 1, t = (int)tok_of(i);
-                if (i >= 2) ok = bar_wait(free_ + s, ((i >> 1) - 1) & 1);
+                unsigned char *st = sm + i % 3 * L::STAGE;
+                const int t = (int)tok_of(i);
+                if (i >= 2) ok = bar_wait(stg_done, i & 1);  // chunk i - 2's images have left by this stage
                 if (!ok) break;
-                mbar_arrive_expect_tx(full + s, L::AT + L::BT);
-                for (int b = 0; b < DK / 64; ++b) tma_load_3d(sm + L::A + s * L::AT + b * C * 128, &D.a, 64 * b, ha, t, full + s);
-                tma_load_3d(sm + L::B + s * L::BT, &D.b, W * col, hb, t, full + s);
+                mbar_arrive_expect_tx(in + i % 3, L::STAGE);
+                for (int b = 0; b < DK / 64; ++b) tma_load_3d(st + b * C * 128, &D.a, 64 * b, ha, t, in + i % 3);
+                tma_load_3d(st + L::AT, &D.b, W * col, hb, t, in + i % 3);
             }
             if (!ok)  // copies still in flight land before the block ends
-                for (int j = i > 2 ? i - 2 : 0; j < i; ++j) bar_wait(full + (j & 1), (j >> 1) & 1);
+                for (int j = i > 2 ? i - 2 : 0; j < i; ++j) bar_wait(in + j % 3, (j / 3) & 1);
         }
     } else if (warp == 1) {
         if (elect_one()) {
             const uint32_t id = idesc_bf16(128, W, true, true);
             constexpr uint32_t ALBO = DK == 128 ? 16384 : 0;  // dk = 64: lanes 64 .. 127 repeat lanes 0 .. 63, unread
             for (int i = 0; i < nc; ++i) {
-                const int s = i & 1;
-                ok = bar_wait(k_ready, i & 1) && bar_wait(s_ready, i & 1) && bar_wait(full + s, (i >> 1) & 1);
+                const uint32_t st = smem_u32(sm + i % 3 * L::STAGE);
+                ok = bar_wait(k_ready, i & 1) && bar_wait(s_ready, i & 1) && bar_wait(in + i % 3, (i / 3) & 1);
                 if (!ok) break;
                 fence_after_sync();
-                const uint32_t b = smem_u32(sm + L::B + s * L::BT);
-                mma_bf16_mnmn(tb, smem_u32(sm + L::A + s * L::AT), ALBO, b, 16384, C / 16, id, true);
-                mma_bf16_mnmn(tb, smem_u32(sm + L::LO + s * L::AT), ALBO, b, 16384, C / 16, id, true);
+                mma_bf16_mnmn(tb, st, ALBO, st + L::AT, 16384, C / 16, id, true);
+                mma_bf16_mnmn(tb, smem_u32(sm + L::LO + (i & 1) * L::AT), ALBO, st + L::AT, 16384, C / 16, id, true);
                 mma_commit(u_done);
-                mma_commit(free_ + s);
             }
         }
     } else if (warp == 2) {
         auto load = [&](int i) {
-            const bool in = i < nc;
-            return load_log_decays(a.g && in ? a.g + tok_of(i) * a.g_stride + h : nullptr, a.g_stride, in ? len_of(i) : 0);
+            const bool is = i < nc;
+            return load_log_decays(a.g && is ? a.g + tok_of(i) * a.g_stride + h : nullptr, a.g_stride, is ? len_of(i) : 0);
         };
         float4 g = load(0);
         for (int i = 0; i < nc; ++i) {
             const float4 next = load(i + 1);
-            if (i >= 2) wait(dec_free + (i & 1), ((i >> 1) - 1) & 1);
+            if (i >= 3) wait(dec_free + i % 3, (i / 3 - 1) & 1);
             if (!ok) break;
-            make_decays(g, dec[i & 1]);
+            make_decays(g, dec[i % 3]);
             g = next;
-            if (lane == 0) mbar_arrive(dec_ready + (i & 1));
+            if (lane == 0) mbar_arrive(in + i % 3);
         }
     } else if (warp == 3) {
-        if (lane == 0 && D.images) {
+        if (lane == 0) {
             for (int i = 0; i < nc; ++i) {
                 unsigned char *dst = D.images + ((slot0 + chunk_of(i)) * a.H + h) * (int64_t)(2 * DK * DV * 2) + col * L::IMG;
+                const unsigned char *src = sm + (i + 2) % 3 * L::STAGE;
                 ok = bar_wait(stg_full, i & 1);
                 if (!ok) break;
-                bulk_s2g(dst, sm + L::STG, L::IMG);
-                if (a.lo) bulk_s2g(dst + DK * DV * 2, sm + L::STG + L::IMG, L::IMG);
+                bulk_s2g(dst, src, L::IMG);
+                if (a.lo) bulk_s2g(dst + DK * DV * 2, src + L::IMG, L::IMG);
                 bulk_commit();
                 bulk_wait_read0();
-                mbar_arrive(stg_free);
+                mbar_arrive(stg_done);
             }
         }
     } else {
@@ -165,14 +168,14 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             if (lane == 0) mbar_arrive(bar);
         };
         auto scale_rows = [&](int i) {
-            const int s = i & 1, len = len_of(i);
-            wait(dec_ready + s, (i >> 1) & 1);
-            wait(full + s, (i >> 1) & 1);
+            const int len = len_of(i);
+            unsigned char *st = sm + i % 3 * L::STAGE;
+            wait(in + i % 3, (i / 3) & 1);
             if (!ok) return;
-            const decays &d = dec[s];
+            const decays &d = dec[i % 3];
             const float f = back ? D.scale * expf(ends(d, quarter - 1, -1) + d.rel[row]) : expf(ends(d, 3, quarter)) * d.w[row];
-            scale_chunks<KC>(sm + L::A + s * L::AT, sm + L::LO + s * L::AT, row, KC * part, row < len ? f : 0.f);
-            if (row >= len) clear_chunks<W / 32>(sm + L::B + s * L::BT, row, W / 32 * part);
+            scale_chunks<KC>(st, sm + L::LO + (i & 1) * L::AT, row, KC * part, row < len ? f : 0.f);
+            if (row >= len) clear_chunks<W / 32>(st + L::AT, row, W / 32 * part);
             fence_proxy_async();
             arrive(k_ready);
         };
@@ -190,7 +193,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 fence_after_sync();
                 tmem_load<CW>(ts, x);
             }
-            const float all = expf(dec[i & 1].hi[3]);
+            const float all = expf(dec[i % 3].hi[3]);
             float y[CW];
 #pragma unroll
             for (int c = 0; c < CW; ++c) y[c] = x[c] * all;
@@ -200,11 +203,9 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(s_ready);
-                mbar_arrive(dec_free + (i & 1));
+                mbar_arrive(dec_free + i % 3);
             }
-            if (D.images) {  // under the product
-                if (i > 0) wait(stg_free, (i - 1) & 1);
-                if (!ok) break;
+            {  // the images, under the product, by way of the rows' tile of the chunk before
                 if (mine) {
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
@@ -213,7 +214,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                         split2(x[c + 2], x[c + 3], hi.y, lo.y);
                         split2(x[c + 4], x[c + 5], hi.z, lo.z);
                         split2(x[c + 6], x[c + 7], hi.w, lo.w);
-                        unsigned char *p = sm + L::STG + img_chunk_off(DK, row, (CW * part + c) / 8);
+                        unsigned char *p = sm + (i + 2) % 3 * L::STAGE + img_chunk_off(DK, row, (CW * part + c) / 8);
                         *reinterpret_cast<uint4 *>(p) = hi;
                         *reinterpret_cast<uint4 *>(p + L::IMG) = lo;
                     }

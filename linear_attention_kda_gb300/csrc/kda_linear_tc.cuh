@@ -90,6 +90,7 @@ __device__ __forceinline__ void make_decays(const float4 &g, decays &d, float *r
 // A bounded wait in a few instructions (a chain's roles together have to fit the instruction cache, and every wait is
 // a copy): attempts of about a microsecond each, given up after a million of them.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    if (mbar_test_wait(bar, parity)) return true;
     uint32_t done;
 #pragma unroll 1
     for (int n = 0; n < (1 << 20); ++n) {
