@@ -262,6 +262,7 @@ struct grads_args {
     bf16 *dq, *dk, *dv;
     float *pq, *pk, *pv;                // fp32 [T, H, d] instead, where heads share a row
     float *dg, *dg_slot;                // [T, H], or sums over a chunk [slots, H]; neither: no decay gradient
+    int sms;
     int *err;
 };
 
@@ -326,8 +327,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint64_t *f_qk = bars, *f_ov = bars + 1, *f_s = bars + 2, *f_l = bars + 3, *f_ll = bars + 4, *xy_done = bars + 5,
              *q_done = bars + 6, *k_done = bars + 7, *dot_done = bars + 8, *a_ready = bars + 9, *v_done = bars + 10,
-             *d_ready = bars + 11, *out_done = bars + 12, *dec_ready = bars + 13;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 14);
+             *d_ready = bars + 11, *out_done = bars + 12, *dec_ready = bars + 13, *clean = bars + 14;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 15);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = (int)(blockIdx.x % a.H);
@@ -339,7 +340,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 14; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 ? 16 : 1);
+        for (int i = 0; i < 15; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 ? 16 : 1);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -356,6 +357,12 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     if (warp == 0) {
         if (lane == 0) {
             const int t = (int)c.tok0, hq = h / a.rq, hk = h / a.rk, hv = h / a.rv;
+            // (the states first: their product with one another is taken while the tiles are on their way)
+            mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
+            bulk_g2s(sm + L::B0, S, L::SI, f_s);
+            if (decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
+            mbar_arrive_expect_tx(f_l, L::SI);
+            bulk_g2s(sm + L::B2, G, L::SI, f_l);
             mbar_arrive_expect_tx(f_qk, 2 * L::QT);
             for (int b = 0; b < DK / 64; ++b) {
                 tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, hq, t, f_qk);
@@ -366,11 +373,6 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
                 tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, hv, t, f_ov);
             }
-            mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
-            bulk_g2s(sm + L::B0, S, L::SI, f_s);
-            if (decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
-            mbar_arrive_expect_tx(f_l, L::SI);
-            bulk_g2s(sm + L::B2, G, L::SI, f_l);
             bool more = decay && bar_wait(q_done, 0) && bar_wait(dot_done, 0);
             if (decay && !more) ok = false;
             if (more) {
@@ -392,7 +394,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                            id_dq = idesc_bf16(128, DK, false, true), id_dk = idesc_bf16(128, DK, true, true),
                            id_dv = idesc_bf16(128, DV, true, true);
             do {
-                if (!(ok = bar_wait(f_qk, 0))) break;
+                if (!(ok = bar_wait(f_qk, 0) && (len == C || bar_wait(clean, 0)))) break;
                 fence_after_sync();
                 mma_bf16_k(tb + T_X, q, C, k, C, DK / 16, id_c, false);
                 if (!(ok = bar_wait(f_ov, 0))) break;
@@ -425,6 +427,25 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         const float4 g = load_log_decays(a.g ? a.g + c.tok0 * a.g_stride + h : nullptr, a.g_stride, len);
         make_decays(g, d, rel_lo);
         if (lane == 0) mbar_arrive(dec_ready);
+    } else if (warp == 3) {
+        // What the block that runs here next will load (blocks start in order, one on each SM): its way from memory
+        // is half of a block's time otherwise, since all blocks load at once and then compute at once.
+        const int64_t next = (int64_t)blockIdx.x + a.sms;
+        chunk x;
+        if (next < gridDim.x && find_chunk<C>(a.cu, a.T, a.N, next / a.H, &x) && lane == 0 && bar_wait(f_ov, 0)) {
+            const int t = (int)x.tok0, g = (int)(next % a.H);
+            const unsigned char *s = a.states + next * (int64_t)(2 * L::SI), *l = a.adj + next * (int64_t)(2 * L::SI);
+            for (int b = 0; b < DK / 64; ++b) {
+                tma_prefetch_3d(&tm.q, 64 * b, g / a.rq, t);
+                tma_prefetch_3d(&tm.k, 64 * b, g / a.rk, t);
+            }
+            for (int b = 0; b < DV / 64; ++b) {
+                tma_prefetch_3d(&tm.o, 64 * b, g, t);
+                tma_prefetch_3d(&tm.v, 64 * b, g / a.rv, t);
+            }
+            bulk_prefetch_l2(s, decay ? 2 * L::SI : L::SI);
+            bulk_prefetch_l2(l, decay ? 2 * L::SI : L::SI);
+        }
     } else if (warp >= 4) {
         constexpr int KW = DK / 4, VW = DV / 4;
         const int quarter = warp & 3, part = (warp - 4) >> 2, row = 32 * quarter + lane;
@@ -462,6 +483,18 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             }
             arrive(dot_done);
         }
+        if (len < C) {  // rows behind the sequence are another's: zeros from here on
+            wait(f_qk);
+            wait(f_ov);
+            if (ok && row >= len) {
+                clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
+                clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
+                clear_chunks<DV / 32>(sm + L::O, row, DV / 32 * part);
+                clear_chunks<DV / 32>(sm + L::V, row, DV / 32 * part);
+            }
+            fence_proxy_async();
+            arrive(clean);
+        }
         // ---- A and dA, columns 32 part .. of the chunk, and what the decay's gradient takes from their products
         wait(dec_ready);
         wait(xy_done);
@@ -472,26 +505,42 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             float x[32], y[32];
             tmem_ld32(tl + T_X + 32 * part, x);
             tmem_ld32(tl + T_Y + 32 * part, y);
-            const float u = part < quarter ? a.scale * __expf(ends(d, quarter - 1, part) + rel) : 0.f;
-            const bool in = row < len;
+            if (part < quarter) {  // all of it before the row's own block
+                const float u = a.scale * __expf(ends(d, quarter - 1, part) + rel);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float f[2], p[2], q[2];
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 w4 = *reinterpret_cast<const float4 *>(&d.w[32 * part + e]);
+                    const float f[4] = {u * w4.x, u * w4.y, u * w4.z, u * w4.w};
+                    float q[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int t = 32 * part + e + j;
-                    if (part < quarter) f[j] = u * d.w[t];
-                    else f[j] = a.scale * __expf((rel - d.rel[t]) + (rlo - rel_lo[t]));
-                    const bool keep = in && t <= row;
-                    p[j] = keep ? x[e + j] * f[j] : 0.f;
-                    q[j] = keep ? y[e + j] * f[j] : 0.f;
-                    // what passes from t to r; t = r adds the same to both of its sums and is left out of them
-                    const float wgt = keep && t < row ? x[e + j] * q[j] : 0.f;
-                    w_row += wgt;
-                    x[e + j] = wgt;
+                    for (int j = 0; j < 4; ++j) q[j] = y[e + j] * f[j];
+                    pa[e / 2] = pack_bf16(x[e] * f[0], x[e + 1] * f[1]);
+                    pa[e / 2 + 1] = pack_bf16(x[e + 2] * f[2], x[e + 3] * f[3]);
+                    pd[e / 2] = pack_bf16(q[0], q[1]);
+                    pd[e / 2 + 1] = pack_bf16(q[2], q[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[e + j] *= q[j];  // what passes from t to r
+                        w_row += x[e + j];
+                    }
                 }
-                pa[e / 2] = pack_bf16(p[0], p[1]);
-                pd[e / 2] = pack_bf16(q[0], q[1]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float p[2], q[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int t = 32 * part + e + j;
+                        const float f = a.scale * __expf((rel - d.rel[t]) + (rlo - rel_lo[t]));
+                        p[j] = t <= row ? x[e + j] * f : 0.f;
+                        q[j] = t <= row ? y[e + j] * f : 0.f;
+                        // (t = r adds the same to both of its sums and is left out of them)
+                        x[e + j] = t < row ? x[e + j] * q[j] : 0.f;
+                        w_row += x[e + j];
+                    }
+                    pa[e / 2] = pack_bf16(p[0], p[1]);
+                    pd[e / 2] = pack_bf16(q[0], q[1]);
+                }
             }
             if (decay) w_col = transpose_sum(x);
         } else {
@@ -505,10 +554,6 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint4 *>(sm + L::B1 + img_chunk_off(C, row, 4 * part + j)) =
                     make_uint4(pd[4 * j], pd[4 * j + 1], pd[4 * j + 2], pd[4 * j + 3]);
-            if (row >= len) {  // rows behind the sequence are another's: they meet zeros, which an infinity would spoil
-                clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
-                clear_chunks<DV / 32>(sm + L::O, row, DV / 32 * part);
-            }
             // ---- dQ's first part
             fence_after_sync();
             float x[KW];
@@ -516,7 +561,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             const float e = a.scale * expf(ends(d, quarter - 1, -1) + rel);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= e;
-            if (decay && row < len) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
+            if (decay) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
             tmem_store<KW>(tl + T_Q + KW * part, x);
         }
         wait(k_done);  // the values have been read: A may lie over them
@@ -526,7 +571,6 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint4 *>(sm + L::V + img_chunk_off(C, row, 4 * part + j)) =
                     make_uint4(pa[4 * j], pa[4 * j + 1], pa[4 * j + 2], pa[4 * j + 3]);
-            if (row >= len) clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
             fence_proxy_async();
             fence_before_sync();
         }
@@ -537,7 +581,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             tmem_load<KW>(tl + T_K + KW * part, x);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= f;
-            if (decay && row < len) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
+            if (decay) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
             tmem_store<KW>(tl + T_K + KW * part, x);
         }
         wait(v_done);  // ---- dV's first part; Lambda has been read
@@ -717,6 +761,9 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
         else g.dg_slot = (float *)(ws + L.dg);
     }
     g.err = err;
+    int dev = 0;
+    g.sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&g.sms, cudaDevAttrMultiProcessorCount, dev);
     linear_grads_tc_kernel<DK, DV><<<(unsigned)(L.slots * a->H), THREADS, smem2, stream>>>(gm, g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return kda_cuda_status(e);
