@@ -1,10 +1,25 @@
 // Shared by the linear-attention kernels (a decay per head): where the chunks of a packed batch lie, and the
 // cumulative log-decays of one chunk.
 #pragma once
+#include <atomic>
+
 #include "kda_common.cuh"
 
 namespace kda {
 namespace lin {
+
+// Allows a kernel its dynamic shared memory, once for each device.  `done`: a bit per device, one such word per kernel.
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Sequence n's tokens, [a, b).  False (and the device error set by one caller) where cu_seqlens is not
 // 0 = c_0 <= ... <= c_N = T around it: nothing out of range is ever formed from it.

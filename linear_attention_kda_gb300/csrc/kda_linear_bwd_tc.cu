@@ -741,9 +741,10 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     sm.d[1] = {gm.q, gm.o, rq, 1, a->grad_final_state, a->grad_initial_state, (unsigned char *)ws + L.adj, a->scale};
     const states_args s{a->g, gs, a->cu_seqlens, a->T, a->N, a->H, a->grad_g != nullptr, err};
     constexpr int smem1 = states_smem<DK>::BYTES, smem2 = grads_smem<DK, DV>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(linear_bwd_states_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+    static std::atomic<uint64_t> states_allowed{0}, grads_allowed{0};
+    cudaError_t e = allow_smem(linear_bwd_states_tc_kernel<DK, DV>, smem1, states_allowed);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(linear_grads_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
+        e = allow_smem(linear_grads_tc_kernel<DK, DV>, smem2, grads_allowed);
     if (e != cudaSuccess) return kda_cuda_status(e);
     linear_bwd_states_tc_kernel<DK, DV><<<dim3((unsigned)(a->N * a->H * (DV / W)), 2), THREADS, smem1, stream>>>(sm, s);
     e = cudaGetLastError();

@@ -515,7 +515,8 @@ static cudaError_t fwd(const kda_linear_args *a, char *ws, cudaStream_t stream, 
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a->T == 0) return e;
     constexpr int smem = out_smem_floats<DK, DV>() * 4;
-    e = cudaFuncSetAttribute(linear_out_kernel<DK, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_smem(linear_out_kernel<DK, DV, T>, smem, allowed);
     if (e != cudaSuccess) return e;
     linear_out_kernel<DK, DV, T><<<(unsigned)(slots * a->H), NT, smem, stream>>>(
         (const T *)a->q, (const T *)a->k, (const T *)a->v, a->Hq, a->Hk, a->Hv, a->g, gs, gt, states, a->scale,
@@ -593,7 +594,8 @@ static cudaError_t bwd(const kda_linear_bwd_args *a, char *ws, cudaStream_t stre
     }
     constexpr int smem = grads_smem_floats<DK, DV>() * 4;
     static_assert(smem <= 227 * 1024, "shared memory");
-    e = cudaFuncSetAttribute(linear_grads_kernel<DK, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_smem(linear_grads_kernel<DK, DV, T>, smem, allowed);
     if (e != cudaSuccess) return e;
     linear_grads_kernel<DK, DV, T><<<(unsigned)(slots * a->H), NT, smem, stream>>>(G);
     e = cudaGetLastError();

@@ -654,14 +654,16 @@ static kda_status_t fwd(const kda_linear_args *a, char *ws, cudaStream_t stream,
             c.initial = (const float *)(ws + L.init);
         }
         constexpr int smem = seg_smem<DK, DV>::BYTES;
-        cudaError_t e = cudaFuncSetAttribute(linear_segments_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> allowed{0};
+        cudaError_t e = allow_smem(linear_segments_tc_kernel<DK, DV>, smem, allowed);
         if (e != cudaSuccess) return kda_cuda_status(e);
         linear_segments_tc_kernel<DK, DV><<<grid, SEG_THREADS, smem, stream>>>(tm, c);
         e = cudaGetLastError();
         if (e != cudaSuccess) return kda_cuda_status(e);
     }
     constexpr int smem = fwd_smem<DK, DV>::BYTES;
-    const cudaError_t e = cudaFuncSetAttribute(linear_fwd_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(linear_fwd_tc_kernel<DK, DV>, smem, allowed);
     if (e != cudaSuccess) return kda_cuda_status(e);
     linear_fwd_tc_kernel<DK, DV><<<grid, FWD_THREADS, smem, stream>>>(tm, c);
     return kda_cuda_status(cudaGetLastError());

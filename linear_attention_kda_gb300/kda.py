@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -180,12 +181,12 @@ def load_library(path: Optional[str] = None):
         L.kda_recurrent_replay.restype = ctypes.c_int
         L.kda_output_gate.argtypes = [ctypes.POINTER(OutputGateArgs), _vp]
         L.kda_output_gate.restype = ctypes.c_int
-        for name, struct in (("kda_linear_chunk_fwd", LinearArgs), ("kda_linear_chunk_bwd", LinearBwdArgs)):
-            getattr(L, name).argtypes = [ctypes.POINTER(struct), _vp, ctypes.c_size_t, _vp]
+        # (arguments as packed bytes or by reference to their ctypes structures)
+        for name in ("kda_linear_chunk_fwd", "kda_linear_chunk_bwd"):
+            getattr(L, name).argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
             getattr(L, name).restype = ctypes.c_int
-        for name, struct in (("kda_linear_recurrent_step", LinearStepArgs), ("kda_state_copy", StateCopyArgs),
-                             ("kda_rope", RopeArgs)):
-            getattr(L, name).argtypes = [ctypes.POINTER(struct), _vp]
+        for name in ("kda_linear_recurrent_step", "kda_state_copy", "kda_rope"):
+            getattr(L, name).argtypes = [_vp, _vp]
             getattr(L, name).restype = ctypes.c_int
         L.kda_linear_chunk_fwd_workspace_size.argtypes = [_i64, _i64, _i32, _i32, _i32, ctypes.c_int]
         L.kda_linear_chunk_fwd_workspace_size.restype = ctypes.c_size_t
@@ -411,40 +412,72 @@ def recurrent_replay(cached, n_replay, new, n_commit, dt_bias, A_log, state, *, 
 
 
 # ---------------------------------------------------------------- linear attention with a decay per head
-def _tensors(where: str, device, **ts):
-    """Checks name=(tensor, shape, dtype) of one call: shape, dtype, dense layout, one CUDA device (None passes)."""
-    for name, (t, shape, dtype) in ts.items():
+# A decode step's kernel takes 4 us, so what a call does on the host counts: checks in one pass over the tensors (a
+# second, descriptive one only where something is wrong), arguments packed by struct (a third of a ctypes.Structure's
+# time, same layout), the current device and stream asked for once.
+_LINEAR = struct.Struct("@qq7iPPPPifPPPP")
+_LINEAR_BWD = struct.Struct("@qq7iPPPPif" + "P" * 9)
+_LINEAR_STEP = struct.Struct("@q7iPPPPifPPqP")
+_STATE_COPY = struct.Struct("@PPqqqqPP")
+_ROPE = struct.Struct("@qiiiiiiifPPPPPPqqqq")
+assert [x.size for x in (_LINEAR, _LINEAR_BWD, _LINEAR_STEP, _STATE_COPY, _ROPE)] == [
+    ctypes.sizeof(x) for x in (LinearArgs, LinearBwdArgs, LinearStepArgs, StateCopyArgs, RopeArgs)]
+
+
+def _require(where: str, device: int, spec):
+    """Checks (name, tensor, shape, dtype) of one call: shape, dtype, dense layout, one CUDA device (None passes)."""
+    for _, t, shape, dtype in spec:
+        if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
+            break
+    else:
+        if device >= 0:
+            return
+    for name, t, shape, dtype in spec:
         if t is None:
             continue
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{where}: {name} is {t.dtype}, not {dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{where}: {name} is on {t.device}, not {device}")
-    if device.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on a CUDA device")
+        if t.get_device() != device:
+            raise ValueError(f"{where}: {name} is not on the device of the others")
+    raise ValueError(f"{where}: tensors must be on a CUDA device")
 
 
-def _linear_shapes(where, q, k, v, g):
-    """Heads, head sizes and the log-decay's layout of a linear-attention call."""
+def _run(where: str, device: int, fn, packed: bytes, *more):
+    """Calls fn(args, *more, stream) with `device` current, on its current stream."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            code = fn(packed, *more, _raw_stream(device))
+    else:
+        code = fn(packed, *more, _raw_stream(device))
+    if code:
+        _check(code, where)
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)  # torch.cuda.current_stream without its Python object
+
+
+def _p(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _linear_heads(where, q, k, v, g):
+    """(rows, H, Hq, Hk, Hv, dk, dv, g per token, dtype code) of a linear-attention call."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError(f"{where}: q, k and v have three dimensions (rows, heads, channels)")
     T, Hq, dk = q.shape
-    Hk, Hv, dv = k.shape[1], v.shape[1], v.shape[2]
-    H = max(Hq, Hk, Hv)
-    _dtype_code(q)
+    Hk = k.shape[1]
+    _, Hv, dv = v.shape
     if g is not None and g.dim() not in (1, 2):
         raise ValueError(f"{where}: g has shape [rows, heads] or [heads]")
-    gshape = None if g is None else (T, H) if g.dim() == 2 else (H,)
-    spec = dict(q=(q, (T, Hq, dk), q.dtype), k=(k, (T, Hk, dk), q.dtype), v=(v, (T, Hv, dv), q.dtype),
-                g=(g, gshape, torch.float32))
-    return T, H, Hq, Hk, Hv, dk, dv, int(g is not None and g.dim() == 2), spec
+    return T, max(Hq, Hk, Hv), Hq, Hk, Hv, dk, dv, int(g is not None and g.dim() == 2), _dtype_code(q)
 
 
-def _n_sequences(where, T, cu_seqlens, n_seq):
+def _n_sequences(where, cu_seqlens, n_seq):
     if cu_seqlens is None:
         return n_seq
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
@@ -453,15 +486,18 @@ def _n_sequences(where, T, cu_seqlens, n_seq):
 
 
 def _workspace(where, workspace, need, device):
+    """(address, bytes, tensor that holds it)"""
     if workspace is None:
-        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
+        if need == 0:
+            return 0, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"{where}: the workspace must be contiguous and on {device}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def linear_chunk_fwd_workspace_size(T, N, H, dk, dv, dtype: torch.dtype) -> int:
-    """kda_linear_chunk_fwd_workspace_size (bytes; 0 on invalid sizes)."""
+    """kda_linear_chunk_fwd_workspace_size (bytes; 0 on invalid sizes, and where none is needed)."""
     code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
     return int(load_library().kda_linear_chunk_fwd_workspace_size(T, N, H, dk, dv, code))
 
@@ -481,25 +517,23 @@ def linear_chunk_fwd(q, k, v, g=None, *, scale: float = 1.0, cu_seqlens: Optiona
 
     q [T, Hq, dk], k [T, Hk, dk], v [T, Hv, dv] (fp32 or bf16; H = the largest head count, a multiple of the
     others); g: log-decay, at most 0, fp32 [T, H] or [H], or None (no decay); states fp32 [N, H, dk, dv]."""
-    where, L = "linear_chunk_fwd", load_library()
-    T, H, Hq, Hk, Hv, dk, dv, per_token, spec = _linear_shapes(where, q, k, v, g)
-    N = _n_sequences(where, T, cu_seqlens, n_seq)
-    state, f32 = (N, H, dk, dv), torch.float32
-    _tensors(where, q.device, **spec, cu_seqlens=(cu_seqlens, (N + 1,), torch.int32),
-             initial_state=(initial_state, state, f32), final_state=(final_state, state, f32),
-             out=(out, (T, H, dv), q.dtype))
-    with torch.cuda.device(q.device):
-        o = out if out is not None else torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-        fs = final_state
-        if fs is None and output_final_state:
-            fs = torch.empty(state, dtype=f32, device=q.device)
-        workspace = _workspace(where, workspace, linear_chunk_fwd_workspace_size(T, N, H, dk, dv, q.dtype), q.device)
-        a = LinearArgs(T=T, N=N, H=H, Hq=Hq, Hk=Hk, Hv=Hv, dk=dk, dv=dv, dtype=_dtype_code(q), q=_ptr(q), k=_ptr(k),
-                       v=_ptr(v), g=_ptr(g), g_per_token=per_token, scale=scale, cu_seqlens=_ptr(cu_seqlens),
-                       initial_state=_ptr(initial_state), final_state=_ptr(fs), o=_ptr(o))
-        _check(L.kda_linear_chunk_fwd(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                      _stream(q)), "kda_linear_chunk_fwd")
-    return o, fs
+    where, L, f32 = "linear_chunk_fwd", _lib or load_library(), torch.float32
+    T, H, Hq, Hk, Hv, dk, dv, per_token, code = _linear_heads(where, q, k, v, g)
+    N, dt, dev = _n_sequences(where, cu_seqlens, n_seq), q.dtype, q.get_device()
+    state = (N, H, dk, dv)
+    _require(where, dev, (("q", q, (T, Hq, dk), dt), ("k", k, (T, Hk, dk), dt), ("v", v, (T, Hv, dv), dt),
+                          ("g", g, (T, H) if per_token else (H,), f32), ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32),
+                          ("initial_state", initial_state, state, f32), ("final_state", final_state, state, f32),
+                          ("out", out, (T, H, dv), dt)))
+    if out is None:
+        out = torch.empty_like(v) if Hv == H else torch.empty((T, H, dv), dtype=dt, device=q.device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(state, dtype=f32, device=q.device)
+    ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_linear_chunk_fwd_workspace_size(T, N, H, dk, dv, code), q.device)
+    _run("kda_linear_chunk_fwd", dev, L.kda_linear_chunk_fwd,
+         _LINEAR.pack(T, N, H, Hq, Hk, Hv, dk, dv, code, _p(q), _p(k), _p(v), _p(g), per_token, scale, _p(cu_seqlens),
+                      _p(initial_state), _p(final_state), _p(out)), ws, ws_bytes)
+    return out, final_state
 
 
 def linear_chunk_bwd(q, k, v, g, grad_o, *, scale: float = 1.0, cu_seqlens: Optional[torch.Tensor] = None,
@@ -510,28 +544,25 @@ def linear_chunk_bwd(q, k, v, g, grad_o, *, scale: float = 1.0, cu_seqlens: Opti
 
     Returns a dict with q, k, v (shapes and dtype of the inputs) and, when asked, g (fp32, the shape of g; not
     without g) and initial_state (fp32 [N, H, dk, dv])."""
-    where, L = "linear_chunk_bwd", load_library()
-    T, H, Hq, Hk, Hv, dk, dv, per_token, spec = _linear_shapes(where, q, k, v, g)
-    N = _n_sequences(where, T, cu_seqlens, n_seq)
-    state, f32 = (N, H, dk, dv), torch.float32
-    _tensors(where, q.device, **spec, cu_seqlens=(cu_seqlens, (N + 1,), torch.int32), grad_o=(grad_o, (T, H, dv), q.dtype),
-             initial_state=(initial_state, state, f32), grad_final_state=(grad_final_state, state, f32))
-    with torch.cuda.device(q.device):
-        grads = {n: torch.empty_like(x) for n, x in (("q", q), ("k", k), ("v", v))}
-        if decay_grad and g is not None:
-            grads["g"] = torch.empty_like(g)
-        if state_grad:
-            grads["initial_state"] = torch.empty(state, dtype=f32, device=q.device)
-        need = linear_chunk_bwd_workspace_size(T, N, H, dk, dv, q.dtype, Hq, Hk, Hv)
-        workspace = _workspace(where, workspace, need, q.device)
-        a = LinearBwdArgs(T=T, N=N, H=H, Hq=Hq, Hk=Hk, Hv=Hv, dk=dk, dv=dv, dtype=_dtype_code(q), q=_ptr(q), k=_ptr(k),
-                          v=_ptr(v), g=_ptr(g), g_per_token=per_token, scale=scale, cu_seqlens=_ptr(cu_seqlens),
-                          initial_state=_ptr(initial_state), grad_o=_ptr(grad_o),
-                          grad_final_state=_ptr(grad_final_state), grad_q=_ptr(grads["q"]), grad_k=_ptr(grads["k"]),
-                          grad_v=_ptr(grads["v"]), grad_g=_ptr(grads.get("g")),
-                          grad_initial_state=_ptr(grads.get("initial_state")))
-        _check(L.kda_linear_chunk_bwd(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                      _stream(q)), "kda_linear_chunk_bwd")
+    where, L, f32 = "linear_chunk_bwd", _lib or load_library(), torch.float32
+    T, H, Hq, Hk, Hv, dk, dv, per_token, code = _linear_heads(where, q, k, v, g)
+    N, dt, dev = _n_sequences(where, cu_seqlens, n_seq), q.dtype, q.get_device()
+    state = (N, H, dk, dv)
+    _require(where, dev, (("q", q, (T, Hq, dk), dt), ("k", k, (T, Hk, dk), dt), ("v", v, (T, Hv, dv), dt),
+                          ("g", g, (T, H) if per_token else (H,), f32), ("grad_o", grad_o, (T, H, dv), dt),
+                          ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, state, f32),
+                          ("grad_final_state", grad_final_state, state, f32)))
+    grads = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v)}
+    if decay_grad and g is not None:
+        grads["g"] = torch.empty_like(g)
+    if state_grad:
+        grads["initial_state"] = torch.empty(state, dtype=f32, device=q.device)
+    need = L.kda_linear_chunk_bwd_workspace_size(T, N, H, Hq, Hk, Hv, dk, dv, code)
+    ws, ws_bytes, _keep = _workspace(where, workspace, need, q.device)
+    _run("kda_linear_chunk_bwd", dev, L.kda_linear_chunk_bwd,
+         _LINEAR_BWD.pack(T, N, H, Hq, Hk, Hv, dk, dv, code, _p(q), _p(k), _p(v), _p(g), per_token, scale, _p(cu_seqlens),
+                          _p(initial_state), _p(grad_o), _p(grad_final_state), _p(grads["q"]), _p(grads["k"]), _p(grads["v"]),
+                          _p(grads.get("g")), _p(grads.get("initial_state"))), ws, ws_bytes)
     return grads
 
 
@@ -540,21 +571,23 @@ def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, state_indice
     """kda_linear_recurrent_step: one decode token per sequence of linear attention with a decay per head; `state`
     [slots, H, dk, dv] is updated in place.  Shapes as linear_chunk_fwd with N rows; state_indices int32 [N] (-1: an
     unused row of a padded batch, left alone with its row of the output).  Returns o [N, H, dv]."""
-    where, L = "linear_recurrent_step", load_library()
-    N, H, Hq, Hk, Hv, dk, dv, per_token, spec = _linear_shapes(where, q, k, v, g)
+    where, L = "linear_recurrent_step", _lib or load_library()
+    N, H, Hq, Hk, Hv, dk, dv, per_token, code = _linear_heads(where, q, k, v, g)
     if state.dim() != 4:
         raise ValueError(f"{where}: state has shape [slots, heads, dk, dv]")
-    _tensors(where, q.device, **spec, state=(state, (state.shape[0], H, dk, dv), torch.float32),
-             state_indices=(state_indices, (N,), torch.int32), out=(out, (N, H, dv), q.dtype))
-    if N > 0 and state.shape[0] < (1 if state_indices is not None else N):
-        raise ValueError(f"{where}: {state.shape[0]} state slots for {N} sequences")
-    with torch.cuda.device(q.device):
-        o = out if out is not None else torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-        a = LinearStepArgs(N=N, H=H, Hq=Hq, Hk=Hk, Hv=Hv, dk=dk, dv=dv, dtype=_dtype_code(q), q=_ptr(q), k=_ptr(k),
-                           v=_ptr(v), g=_ptr(g), g_per_token=per_token, scale=scale, state=_ptr(state),
-                           state_indices=_ptr(state_indices), num_slots=state.shape[0], o=_ptr(o))
-        _check(L.kda_linear_recurrent_step(ctypes.byref(a), _stream(q)), "kda_linear_recurrent_step")
-    return o
+    slots, dt, dev = state.shape[0], q.dtype, q.get_device()
+    _require(where, dev, (("q", q, (N, Hq, dk), dt), ("k", k, (N, Hk, dk), dt), ("v", v, (N, Hv, dv), dt),
+                          ("g", g, (N, H) if per_token else (H,), torch.float32),
+                          ("state", state, (slots, H, dk, dv), torch.float32),
+                          ("state_indices", state_indices, (N,), torch.int32), ("out", out, (N, H, dv), dt)))
+    if N > 0 and slots < (1 if state_indices is not None else N):
+        raise ValueError(f"{where}: {slots} state slots for {N} sequences")
+    if out is None:
+        out = torch.empty_like(v) if Hv == H else torch.empty((N, H, dv), dtype=dt, device=q.device)
+    _run("kda_linear_recurrent_step", dev, L.kda_linear_recurrent_step,
+         _LINEAR_STEP.pack(N, H, Hq, Hk, Hv, dk, dv, code, _p(q), _p(k), _p(v), _p(g), per_token, scale, _p(state),
+                           _p(state_indices), slots, _p(out)))
+    return out
 
 
 # ---------------------------------------------------------------- upkeep of state pools
@@ -562,18 +595,16 @@ def state_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, *, out_
     """kda_state_copy: slot dst[p] becomes a copy of slot src[p], for p = 0, 1, ... in this order; src[p] = -1 clears
     the slot, dst[p] = -1 skips the pair.  pool, out_pool: [slots, ...] of any dtype (a slot's bytes a multiple of
     16); out_pool, by default the pool itself, is changed in place and returned.  src, dst: int32 [P]."""
-    where, L = "state_copy", load_library()
+    where, L = "state_copy", _lib or load_library()
     to = pool if out_pool is None else out_pool
-    if pool.dim() < 2 or src.dim() != 1:
-        raise ValueError(f"{where}: pool has shape [slots, ...] and src one dimension")
-    _tensors(where, pool.device, pool=(pool, pool.shape, pool.dtype),
-             out_pool=(to, (to.shape[0],) + tuple(pool.shape[1:]), pool.dtype), src=(src, src.shape, torch.int32),
-             dst=(dst, src.shape, torch.int32))
-    slot = pool[0].numel() * pool.element_size() if pool.shape[0] else to[0].numel() * to.element_size() if to.shape[0] else 0
-    with torch.cuda.device(pool.device):
-        a = StateCopyArgs(src_pool=_ptr(pool), dst_pool=_ptr(to), slot_bytes=slot, src_slots=pool.shape[0],
-                          dst_slots=to.shape[0], P=src.numel(), src=_ptr(src), dst=_ptr(dst))
-        _check(L.kda_state_copy(ctypes.byref(a), _stream(pool)), "kda_state_copy")
+    if pool.dim() < 2 or src.dim() != 1 or to.dim() != pool.dim():
+        raise ValueError(f"{where}: the pools have shape [slots, ...] and src one dimension")
+    dt, dev, P = pool.dtype, pool.get_device(), src.shape
+    _require(where, dev, (("pool", pool, pool.shape, dt), ("out_pool", to, to.shape[:1] + pool.shape[1:], dt),
+                          ("src", src, P, torch.int32), ("dst", dst, P, torch.int32)))
+    n, m = pool.shape[0], to.shape[0]
+    slot = (pool.numel() // n if n else to.numel() // m if m else 0) * pool.element_size()
+    _run("kda_state_copy", dev, L.kda_state_copy, _STATE_COPY.pack(_p(pool), _p(to), slot, n, m, P[0], _p(src), _p(dst)))
     return to
 
 
@@ -628,7 +659,7 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
     rot channels of every head.  layout "half" pairs channel i with i + rot / 2, "interleaved" 2 i with 2 i + 1.
     inverse=True turns back, which is also the gradient: rope(grad_q, grad_k, ..., inverse=True).  out_q = q rotates in
     place; q and k may be views with a token stride (heads and channels dense), as slices of a fused projection are."""
-    where, L = "rope", load_library()
+    where, L = "rope", _lib or load_library()
     first = q if q is not None else k
     if first is None:
         raise ValueError(f"{where}: q or k is needed")
@@ -637,36 +668,45 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
     if first.dim() != 3:
         raise ValueError(f"{where}: q and k have three dimensions (tokens, heads, channels)")
     T, _, d = first.shape
-    if freqs.device.type != "cpu" or freqs.dtype != torch.float64 or freqs.dim() != 1:
+    dt, dev = first.dtype, first.get_device()
+    code = _dtype_code(first)
+    if freqs.is_cuda or freqs.dtype is not torch.float64 or freqs.dim() != 1:
         raise ValueError(f"{where}: freqs is a float64 vector on the host")
-    freqs = freqs.contiguous()
-    _tensors(where, first.device, positions=(positions, (T,), torch.int32))
+    if not freqs.is_contiguous():
+        freqs = freqs.contiguous()
+    _require(where, dev, (("positions", positions, (T,), torch.int32),))
 
-    def rows(name, x, shape=None):  # a tensor's token stride (0 heads: absent)
+    def rows(name, x, y):  # (heads, input, its token stride, output, its token stride); 0 heads: absent
         if x is None:
-            return 0
-        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != d or (shape is not None and x.shape != shape):
+            return 0, None, 0, None, 0
+        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != d:
             raise ValueError(f"{where}: {name} has shape {tuple(x.shape)}")
-        if x.dtype != first.dtype:
-            raise TypeError(f"{where}: {name} is {x.dtype}, not {first.dtype}")
-        if x.device != first.device:
-            raise ValueError(f"{where}: {name} is on {x.device}, not {first.device}")
         H = x.shape[1]
-        if T > 0 and H > 0 and ((d > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != d) or (T > 1 and x.stride(0) < H * d)):
-            raise ValueError(f"{where}: {name}'s heads and channels must be dense, its tokens at most strided")
-        return x.stride(0) if T > 1 else 0
+        dense = x.is_contiguous()
+        if y is None:
+            y = torch.empty_like(x) if dense else torch.empty((T, H, d), dtype=dt, device=x.device)
+        strides = []
+        for t in (x, y):
+            if t.shape != x.shape:
+                raise ValueError(f"{where}: out_{name} has shape {tuple(t.shape)}, not {tuple(x.shape)}")
+            if t.dtype is not dt:
+                raise TypeError(f"{where}: {name} or its output is {t.dtype}, not {dt}")
+            if t.get_device() != dev:
+                raise ValueError(f"{where}: {name} or its output is not on the device of the others")
+            if t.is_contiguous():
+                strides.append(0)
+                continue
+            st, sh, sd = t.stride()
+            if T > 0 and H > 0 and (sd != 1 or (H > 1 and sh != d) or (T > 1 and st < H * d)):
+                raise ValueError(f"{where}: {name}'s heads and channels must be dense, its tokens at most strided")
+            strides.append(st if T > 1 else 0)
+        return H, x, strides[0], y, strides[1]
 
-    _dtype_code(first)
-    sq, sk = rows("q", q), rows("k", k)
-    with torch.cuda.device(first.device):
-        yq = None if q is None else out_q if out_q is not None else torch.empty((T,) + tuple(q.shape[1:]), dtype=q.dtype, device=q.device)
-        yk = None if k is None else out_k if out_k is not None else torch.empty((T,) + tuple(k.shape[1:]), dtype=k.dtype, device=k.device)
-        oq, ok = rows("out_q", yq, None if q is None else q.shape), rows("out_k", yk, None if k is None else k.shape)
-        a = RopeArgs(T=T, Hq=0 if q is None else q.shape[1], Hk=0 if k is None else k.shape[1], d=d,
-                     rot=2 * freqs.numel(), dtype=_dtype_code(first), layout=ROPE_LAYOUTS[layout], inverse=int(inverse),
-                     scale=scale, positions=_ptr(positions), freqs=freqs.data_ptr(), q=_ptr(q), k=_ptr(k),
-                     q_out=_ptr(yq), k_out=_ptr(yk), q_stride=sq, k_stride=sk, q_out_stride=oq, k_out_stride=ok)
-        _check(L.kda_rope(ctypes.byref(a), _stream(first)), "kda_rope")
+    Hq, q, sq, yq, oq = rows("q", q, out_q)
+    Hk, k, sk, yk, ok = rows("k", k, out_k)
+    _run("kda_rope", dev, L.kda_rope,
+         _ROPE.pack(T, Hq, Hk, d, 2 * freqs.numel(), code, ROPE_LAYOUTS[layout], int(inverse), scale, positions.data_ptr(),
+                    freqs.data_ptr(), _p(q), _p(k), _p(yq), _p(yk), sq, sk, oq, ok))
     return yq, yk
 
 
