@@ -505,7 +505,7 @@ kda_status_t kda_state_copy(const kda_state_copy_args *args, struct CUstream_st 
 #define KDA_ROPE_INTERLEAVED 1
 typedef struct {
     int64_t T;
-    int32_t Hq, Hk;                /* heads of q and k; 0: absent */
+    int32_t Hq, Hk;                /* heads of q and k, up to 1024; 0: absent */
     int32_t d;                     /* channels of a head, 2 .. 1024 */
     int32_t rot;                   /* rotated channels, even, 2 .. min(d, 256) */
     kda_dtype_t dtype;

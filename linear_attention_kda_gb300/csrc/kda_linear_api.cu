@@ -187,7 +187,7 @@ kda_status_t kda_rope(const kda_rope_args *a, struct CUstream_st *stream) {
     if (a->T < 0 || a->Hq < 0 || a->Hk < 0 || (a->Hq == 0 && a->Hk == 0)) return KDA_ERR_INVALID_ARG;
     if (!dtype_ok(a->dtype)) return KDA_ERR_UNSUPPORTED_DTYPE;
     if (a->d < 2 || a->d > 1024 || a->rot < 2 || a->rot > 256 || a->rot > a->d || a->rot % 2 != 0 ||
-        a->T > INT32_MAX || a->Hq > 65535 || a->Hk > 65535)
+        a->T > INT32_MAX || a->Hq > 1024 || a->Hk > 1024)
         return KDA_ERR_UNSUPPORTED_SHAPE;
     if ((a->layout != KDA_ROPE_HALF && a->layout != KDA_ROPE_INTERLEAVED) || (a->inverse != 0 && a->inverse != 1) ||
         !isfinite(a->scale) || !a->freqs)

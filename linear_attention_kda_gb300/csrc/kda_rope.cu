@@ -7,9 +7,11 @@
 // fraction of a turn, go to sincospif.
 //
 // A CTA takes TB tokens: it first writes their sines and cosines (shared by all heads) to shared memory, then
-// streams the heads' rows through 16-byte vectors.  Bound by HBM: q and k read once and written once; channels behind
-// `rot` are copied, or left alone when the output is the input.
+// streams the heads' rows, q's and k's as one list of 16-byte pieces, a few in flight per thread.  Bound by HBM: q and
+// k read once and written once; channels behind `rot` are copied, or left alone when the output is the input.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kda_common.cuh"
 #include "kda_internal.h"
@@ -31,85 +33,148 @@ template <typename T, int V> struct alignas(sizeof(T) * V) vec {
     T x[V];
 };
 
-// One item: V elements of each half of a pair group (half layout), or V elements holding V / 2 pairs (interleaved;
-// one pair by its elements where V is 1), or V elements behind `rot`.
+// x / d for x * d < 2^32, by a product with ceil(2^32 / d)
+struct divisor {
+    uint32_t d, m;
+};
+static divisor make_divisor(uint32_t d) { return {d, d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0}; }
+__device__ __forceinline__ uint32_t quotient(uint32_t x, const divisor &v) { return v.d > 1 ? __umulhi(x, v.m) : x; }
+
+struct job {
+    tensor t;
+    divisor heads, per;   // per: pieces of a head's row, those that turn, then those that are copied
+};
+
+// V values as fp32 and back, packed conversions where they are 16 bytes or pairs
 template <typename T, int V>
-__device__ __forceinline__ void rows(const tensor &t, int64_t tok0, int ntok, int d, int rot, int layout,
-                                     const float2 *cs) {
-    const int half = rot >> 1;
-    const int turn = layout == KDA_ROPE_HALF ? half / V : (V > 1 ? rot / V : half);  // items that turn
-    const int rest = t.in == t.out && t.si == t.so ? 0 : (d - rot) / V;     // items that are copied
-    const int per = turn + rest;
-    const int total = ntok * t.H * per;
+__device__ __forceinline__ void unpack(const vec<T, V> &v, float *f) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = ld(&v.x[i]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void pack(vec<T, V> &v, const float *f) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        __nv_bfloat162 *w = reinterpret_cast<__nv_bfloat162 *>(&v);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) st(&v.x[i], f[i]);
+    }
+}
+
+constexpr int FLIGHT = 4;  // pieces a thread has in flight
+
+// A piece: V elements of each half of a pair group (half layout), or V elements holding V / 2 pairs (interleaved; one
+// pair by its elements where V is 1), or V elements behind `rot`.
+template <typename T, int V, bool HALVES>
+__device__ __forceinline__ void rows(const job &J, int64_t tok0, int ntok, int d, int half, int turn, const float2 *cs) {
     using VT = vec<T, V>;
-    for (int e = threadIdx.x; e < total; e += blockDim.x) {
-        const int r = e / per, i = e - r * per;
-        const int tk = r / t.H, h = r - tk * t.H;
-        const T *in = (const T *)t.in + (tok0 + tk) * t.si + (int64_t)h * d;
-        T *out = (T *)t.out + (tok0 + tk) * t.so + (int64_t)h * d;
-        if (i >= turn) {
-            const int c = rot + (i - turn) * V;
-            *reinterpret_cast<VT *>(out + c) = *reinterpret_cast<const VT *>(in + c);
-        } else if (layout == KDA_ROPE_HALF) {
-            const int c = i * V;
-            VT a = *reinterpret_cast<const VT *>(in + c), b = *reinterpret_cast<const VT *>(in + half + c);
+    constexpr bool TWO = HALVES || V == 1;  // a turning piece is two vectors
+    const uint32_t per = J.per.d, total = (uint32_t)ntok * J.heads.d * per;
+    const T *base = (const T *)J.t.in + tok0 * J.t.si;
+    T *dest = (T *)J.t.out + tok0 * J.t.so;
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 256 * FLIGHT) {
+        VT a[FLIGHT], b[FLIGHT];
+        uint32_t tk[FLIGHT], h[FLIGHT], i[FLIGHT];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float2 w = cs[tk * half + c + j];
-                const float x = ld(&a.x[j]), y = ld(&b.x[j]);
-                st(&a.x[j], x * w.x - y * w.y);
-                st(&b.x[j], y * w.x + x * w.y);
-            }
-            *reinterpret_cast<VT *>(out + c) = a;
-            *reinterpret_cast<VT *>(out + half + c) = b;
-        } else if (V == 1) {
-            const float2 w = cs[tk * half + i];
-            const float x = ld(in + 2 * i), y = ld(in + 2 * i + 1);
-            st(out + 2 * i, x * w.x - y * w.y);
-            st(out + 2 * i + 1, y * w.x + x * w.y);
-        } else {
-            const int c = i * V;
-            VT a = *reinterpret_cast<const VT *>(in + c);
+        for (int j = 0; j < FLIGHT; ++j) {
+            const uint32_t e = e0 + 256 * j, r = quotient(e, J.per);
+            i[j] = e - r * per;
+            tk[j] = quotient(r, J.heads);
+            h[j] = r - tk[j] * J.heads.d;
+            if (e >= total) continue;
+            const bool turned = (int)i[j] < turn;
+            const uint32_t at = h[j] * d + (turned ? (TWO && !HALVES ? 2 : V) * i[j] : 2 * half + (i[j] - turn) * V);
+            const T *p = base + tk[j] * J.t.si + at;
+            a[j] = *reinterpret_cast<const VT *>(p);
+            if (TWO && turned) b[j] = *reinterpret_cast<const VT *>(p + (HALVES ? half : 1));
+        }
 #pragma unroll
-            for (int j = 0; j + 1 < V; j += 2) {
-                const float2 w = cs[tk * half + ((c + j) >> 1)];
-                const float x = ld(&a.x[j]), y = ld(&a.x[j + 1]);
-                st(&a.x[j], x * w.x - y * w.y);
-                st(&a.x[j + 1], y * w.x + x * w.y);
+        for (int j = 0; j < FLIGHT; ++j) {
+            if (e0 + 256 * j >= total) continue;
+            const bool turned = (int)i[j] < turn;
+            const uint32_t at = h[j] * d + (turned ? (TWO && !HALVES ? 2 : V) * i[j] : 2 * half + (i[j] - turn) * V);
+            T *p = dest + tk[j] * J.t.so + at;
+            if (turned) {
+                float x[V], y[V];
+                unpack<T, V>(a[j], x);
+                if constexpr (TWO) {
+                    const float2 *w = cs + tk[j] * half + V * i[j];
+                    unpack<T, V>(b[j], y);
+#pragma unroll
+                    for (int n = 0; n < V; ++n) {
+                        const float2 c = w[n];
+                        const float u = x[n] * c.x - y[n] * c.y;
+                        y[n] = y[n] * c.x + x[n] * c.y;
+                        x[n] = u;
+                    }
+                    pack<T, V>(b[j], y);
+                    *reinterpret_cast<VT *>(p + (HALVES ? half : 1)) = b[j];
+                } else {
+                    const float2 *w = cs + tk[j] * half + V / 2 * i[j];
+#pragma unroll
+                    for (int n = 0; n + 1 < V; n += 2) {
+                        const float2 c = w[n / 2];
+                        const float u = x[n] * c.x - x[n + 1] * c.y;
+                        x[n + 1] = x[n + 1] * c.x + x[n] * c.y;
+                        x[n] = u;
+                    }
+                }
+                pack<T, V>(a[j], x);
             }
-            *reinterpret_cast<VT *>(out + c) = a;
+            *reinterpret_cast<VT *>(p) = a[j];
         }
     }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ turns F, tensor q, tensor k, int64_t tokens,
-                                                   int TB, const int32_t *__restrict__ pos, int d, int rot, int layout,
-                                                   int inverse, float scale) {
-    extern __shared__ float2 cs[];  // [TB][rot / 2] cosine and sine, times scale
-    const int half = rot >> 1;
+template <typename T, int V, bool HALVES>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ turns F, const __grid_constant__ job q,
+                                                   const __grid_constant__ job k, int64_t tokens, int TB,
+                                                   const int32_t *__restrict__ pos, int d, int half, int turn, int inverse,
+                                                   float scale) {
+    extern __shared__ __align__(16) float2 cs[];  // [TB][rot / 2] cosine and sine, times scale
     const int64_t tok0 = (int64_t)blockIdx.x * TB;
     const int ntok = (int)(tokens - tok0 < TB ? tokens - tok0 : TB);
     for (int e = threadIdx.x; e < ntok * half; e += 256) {
         const int tk = e / half, i = e - tk * half;
-        const uint64_t turn = (uint64_t)(int64_t)pos[tok0 + tk] * F.f[i];
+        const uint64_t turn64 = (uint64_t)(int64_t)pos[tok0 + tk] * F.f[i];
         float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns: 2^-31 each
+        sincospif((float)(int32_t)(turn64 >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns: 2^-31 each
         cs[e] = make_float2(scale * c, scale * (inverse ? -s : s));
     }
     __syncthreads();
-    if (q.H) rows<T, V>(q, tok0, ntok, d, rot, layout, cs);
-    if (k.H) rows<T, V>(k, tok0, ntok, d, rot, layout, cs);
+    if (q.t.H) rows<T, V, HALVES>(q, tok0, ntok, d, half, turn, cs);
+    if (k.t.H) rows<T, V, HALVES>(k, tok0, ntok, d, half, turn, cs);
 }
 
-template <typename T, int V>
+template <typename T, int V, bool HALVES>
 static void launch(const kda_rope_args *a, const turns &F, cudaStream_t stream) {
-    const tensor q{a->q, a->q_out, a->q_stride, a->q_out_stride, a->Hq};
-    const tensor k{a->k, a->k_out, a->k_stride, a->k_out_stride, a->Hk};
-    const int TB = 1;
-    const unsigned grid = (unsigned)((a->T + TB - 1) / TB);
-    rope_kernel<T, V><<<grid, 256, (size_t)TB * (a->rot / 2) * sizeof(float2), stream>>>(
-        F, q, k, a->T, TB, a->positions, a->d, a->rot, a->layout, a->inverse, a->scale);
+    const int half = a->rot / 2, turn = HALVES ? half / V : (V > 1 ? a->rot / V : half);
+    auto job_of = [&](const void *in, void *out, int64_t si, int64_t so, int H) {
+        const bool copied = !(in == out && si == so);
+        return job{{in, out, si, so, H}, make_divisor((uint32_t)H),
+                   make_divisor((uint32_t)(turn + (copied ? (a->d - a->rot) / V : 0)))};
+    };
+    // Enough tokens to a CTA for a few rounds of its pieces, as long as every SM still has a few CTAs.  (At most 2048
+    // rows, or one token: quotient()'s range.)
+    int64_t TB = 2048 / (a->Hq + a->Hk);
+    if (TB > a->T / (4 * 152)) TB = a->T / (4 * 152);
+    if (TB > 4) TB = 4;
+    if (TB < 1) TB = 1;
+    rope_kernel<T, V, HALVES><<<(unsigned)((a->T + TB - 1) / TB), 256, (size_t)TB * half * sizeof(float2), stream>>>(
+        F, job_of(a->q, a->q_out, a->q_stride, a->q_out_stride, a->Hq),
+        job_of(a->k, a->k_out, a->k_stride, a->k_out_stride, a->Hk), a->T, (int)TB, a->positions, a->d, half, turn,
+        a->inverse, a->scale);
 }
 
 template <typename T>
@@ -127,9 +192,14 @@ static void launch_t(const kda_rope_args *a, const turns &F, cudaStream_t stream
         return q && k;
     };
     constexpr int V16 = 16 / (int)sizeof(T);
-    if (fits(V16)) launch<T, V16>(a, F, stream);
-    else if (fits(4)) launch<T, 4>(a, F, stream);
-    else launch<T, 1>(a, F, stream);
+    auto go = [&](auto halves) {
+        constexpr bool H = decltype(halves)::value;
+        if (fits(V16)) launch<T, V16, H>(a, F, stream);
+        else if (fits(4)) launch<T, 4, H>(a, F, stream);
+        else launch<T, 1, H>(a, F, stream);
+    };
+    if (a->layout == KDA_ROPE_HALF) go(std::true_type{});
+    else go(std::false_type{});
 }
 
 }  // namespace rope

@@ -110,7 +110,7 @@ def test_linear_rejects(lib, make, kw, code):
     (_copy(src_slots=4), 1), (_copy(dst_pool=FAKE + 4096), 1), (_copy(dst_pool=FAKE * 5 + 8), 4), (_copy(src=FAKE + 64), 1), (_copy(dst=2 * FAKE + 2), 4),
     (_copy(src_slots=1 << 31), 2),
     (_rope(T=-1), 1), (_rope(Hq=0, Hk=0), 1), (_rope(rot=0), 2), (_rope(rot=63), 2), (_rope(rot=130), 2), (_rope(d=2048), 2), (_rope(d=1), 2),
-    (_rope(d=512, rot=258), 2), (_rope(dtype=5), 3), (_rope(layout=2), 1), (_rope(inverse=3), 1), (_rope(scale=float("inf")), 1), (_rope(freqs=None), 1),
+    (_rope(d=512, rot=258), 2), (_rope(Hq=1025), 2), (_rope(dtype=5), 3), (_rope(layout=2), 1), (_rope(inverse=3), 1), (_rope(scale=float("inf")), 1), (_rope(freqs=None), 1),
     (_rope(positions=None), 1), (_rope(q=None), 1), (_rope(k_out=None), 1), (_rope(q_stride=500), 1), (_rope(q=FAKE * 2 + 1), 4), (_rope(positions=FAKE + 2), 4),
     (_rope(q_out=FAKE * 2 + 256), 1), (_rope(q_out=FAKE * 2, q_out_stride=1024), 1), (_rope(k_out=FAKE * 2), 1), (_rope(k_out=FAKE * 4), 1), (_rope(q_out=FAKE), 1),
 ])
