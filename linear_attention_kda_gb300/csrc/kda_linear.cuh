@@ -74,40 +74,59 @@ __device__ __forceinline__ bool find_chunk(const int32_t *cu, int64_t T, int64_t
     return true;
 }
 
-// A log-decay below -104 counts as -104 (exp of it is 0 in fp32); a NaN stays one.
-__device__ __forceinline__ double clamp_decay(float g) { return g < -104.f ? -104.0 : (double)g; }
+// Sums of two floats each (48 bits): the fp64 pipe of this GPU would take three times as long for a chunk's sums.
+struct ff {
+    float h, l;
+};
+__device__ __forceinline__ ff ff_add(const ff &a, const ff &b) {
+    const float s = a.h + b.h, t = s - a.h, e = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l), h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ float ff_diff(const ff &a, const ff &b) { return (a.h - b.h) + (a.l - b.l); }
+__device__ __forceinline__ ff ff_shfl(const ff &a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
+}
 
-// Cumulative log-decays G of one chunk, by one warp.  Sums run in fp64 and are kept as fp32 pairs hi + lo: the
-// difference of two of them, (hi_r - hi_j) + (lo_r - lo_j), is then good to an fp32 rounding of itself even where
-// many erasing decays have made both large.
+// A log-decay below -104 counts as -104 (exp of it is 0 in fp32); a NaN stays one.
+__device__ __forceinline__ float clamp_decay(float g) { return g < -104.f ? -104.f : g; }
+
+// Cumulative log-decays G of one chunk, by one warp, kept as fp32 pairs hi + lo: the difference of two of them, (hi_r -
+// hi_j) + (lo_r - lo_j), is then good to an fp32 rounding of itself even where many erasing decays have made both
+// large.  x: this lane's log-decays, tokens lane * C / 32 on.
 template <int C>
-__device__ __forceinline__ void chunk_decays(const float *g, int g_stride, int len, float *hi, float *lo) {
-    static_assert(C % 32 == 0, "lanes");
+__device__ __forceinline__ void load_decays(const float *g, int g_stride, int len, float *x) {
     constexpr int P = C / 32;
     const int lane = threadIdx.x & 31;
-    double x[P], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int r = lane * P + i;
-        x[i] = g && r < len ? clamp_decay(g[(int64_t)r * g_stride]) : 0.0;
+        x[i] = g && r < len ? g[(int64_t)r * g_stride] : 0.f;
     }
+}
+template <int C>
+__device__ __forceinline__ void chunk_decays(const float *x, float *hi, float *lo) {
+    static_assert(C % 32 == 0, "lanes");
+    constexpr int P = C / 32;
+    const int lane = threadIdx.x & 31;
+    ff G[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        sum += x[i];
-        x[i] = sum;
+        const ff y{clamp_decay(x[i]), 0.f};
+        G[i] = i ? ff_add(G[i - 1], y) : y;
     }
-    double pre = sum;
+    ff pre = G[P - 1];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, pre, off);
-        if (lane >= off) pre += y;
+        const ff y = ff_shfl(pre, lane - off);
+        if (lane >= off) pre = ff_add(y, pre);
     }
-    pre -= sum;
+    ff before = ff_shfl(pre, lane - 1);
+    if (lane == 0) before = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const double G = pre + x[i];
-        hi[lane * P + i] = (float)G;
-        lo[lane * P + i] = (float)(G - (double)(float)G);
+        const ff y = ff_add(before, G[i]);
+        hi[lane * P + i] = y.h;
+        lo[lane * P + i] = y.l;
     }
 }
 

@@ -83,8 +83,10 @@ __global__ void __launch_bounds__(NT) linear_states_kernel(states_args fwd, stat
     constexpr int TN = DK / 32;          // columns of a thread (4 rows x TN columns)
     constexpr int CG = CW / TN;          // column groups
     constexpr int SPLIT = DV / CW;
-    __shared__ float s_k[C][DK], s_v[C][CW];
-    __shared__ float s_hi[C], s_lo[C], s_f[C];
+    constexpr int V = vec16<T>::N;
+    constexpr int KE = C * DK / V / NT, VE = (C * CW / V + NT - 1) / NT;  // 16-byte pieces of a thread
+    __shared__ __align__(16) float s_k[C][DK], s_v[C][CW];
+    __shared__ float s_hi[2][C], s_lo[2][C], s_f[2][C];
     const bool back = blockIdx.y == 1;
     const states_args &A = back ? bwd : fwd;
     const int part = blockIdx.x % SPLIT;
@@ -97,36 +99,78 @@ __global__ void __launch_bounds__(NT) linear_states_kernel(states_args fwd, stat
         return;
     }
     const int64_t at = unit * (int64_t)(DK * DV) + part * CW + c0;
+    const int rk = H / A.Hk, rv = H / A.Hv;
+    const T *k = (const T *)A.k + (int64_t)(h / rk) * DK, *v = (const T *)A.v + (int64_t)(h / rv) * DV + part * CW;
+    const int64_t chunks = (sp.b - sp.a + C - 1) / C, slot0 = sp.a / C + n;
+    auto chunk_of = [&](int64_t i) { return back ? chunks - 1 - i : i; };
+    // the next chunk's tiles wait in registers while this one's are used
+    uint4 kx[KE], vx[VE];
+    float gx[C / 32];
+    auto fetch = [&](int64_t i) {
+        if (i >= chunks) return;
+        const int64_t t0 = sp.a + chunk_of(i) * C;
+        const int len = (int)(sp.b - t0 < C ? sp.b - t0 : C);
+#pragma unroll
+        for (int j = 0; j < KE; ++j) {
+            const int e = tid + NT * j, r = e / (DK / V), c = (e % (DK / V)) * V;
+            kx[j] = r < len ? *reinterpret_cast<const uint4 *>(k + (t0 + r) * A.Hk * DK + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            const int e = tid + NT * j, r = e / (CW / V), c = (e % (CW / V)) * V;
+            vx[j] = r < len ? *reinterpret_cast<const uint4 *>(v + (t0 + r) * A.Hv * DV + c) : make_uint4(0, 0, 0, 0);
+        }
+        if (tid < 32) load_decays<C>(g ? g + t0 * g_tok + h : nullptr, g_stride, len, gx);
+    };
+    auto decays_of = [&](int64_t i) {  // of the chunk in the registers
+        if (tid >= 32 || i >= chunks) return;
+        const int b = i & 1;
+        chunk_decays<C>(gx, s_hi[b], s_lo[b]);
+        __syncwarp();
+        const float eh = s_hi[b][C - 1], el = s_lo[b][C - 1];
+        for (int r = tid; r < C; r += 32)
+            s_f[b][r] = A.scale * (back ? expf(s_hi[b][r]) : expf((eh - s_hi[b][r]) + (el - s_lo[b][r])));
+    };
+    fetch(0);
     float S[4][TN];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) S[i][j] = A.init ? A.init[at + (int64_t)(r0 + i) * DV + j] : 0.f;
-    const int rk = H / A.Hk, rv = H / A.Hv;
-    const T *k = (const T *)A.k + (int64_t)(h / rk) * DK, *v = (const T *)A.v + (int64_t)(h / rv) * DV + part * CW;
-    const int64_t chunks = (sp.b - sp.a + C - 1) / C, slot0 = sp.a / C + n;
+    decays_of(0);
     for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t ci = back ? chunks - 1 - i : i, t0 = sp.a + ci * C;
-        const int len = (int)(sp.b - t0 < C ? sp.b - t0 : C);
         if (A.each) {
-            float *e = A.each + ((slot0 + ci) * H + h) * (int64_t)(DK * DV) + part * CW + c0;
+            float *e = A.each + ((slot0 + chunk_of(i)) * H + h) * (int64_t)(DK * DV) + part * CW + c0;
 #pragma unroll
             for (int a = 0; a < 4; ++a)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) e[(int64_t)(r0 + a) * DV + j] = S[a][j];
         }
-        if (tid < 32) {
-            chunk_decays<C>(g ? g + t0 * g_tok + h : nullptr, g_stride, len, s_hi, s_lo);
-            __syncwarp();
-            const float eh = s_hi[C - 1], el = s_lo[C - 1];
-            for (int r = tid; r < C; r += 32)
-                s_f[r] = A.scale * (back ? expf(s_hi[r]) : expf((eh - s_hi[r]) + (el - s_lo[r])));
+        __syncthreads();  // the chunk's decays are there; the last one's tiles are used
+#pragma unroll
+        for (int j = 0; j < KE; ++j) {
+            const int e = tid + NT * j, r = e / (DK / V), c = (e % (DK / V)) * V;
+            float x[V];
+            vec16<T>::get(reinterpret_cast<const T *>(&kx[j]), x);
+            const float f = s_f[i & 1][r];
+#pragma unroll
+            for (int a = 0; a < V; a += 4)
+                *reinterpret_cast<float4 *>(&s_k[r][c + a]) = make_float4(x[a] * f, x[a + 1] * f, x[a + 2] * f, x[a + 3] * f);
         }
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            const int e = tid + NT * j, r = e / (CW / V), c = (e % (CW / V)) * V;
+            float x[V];
+            vec16<T>::get(reinterpret_cast<const T *>(&vx[j]), x);
+            if (r < C) {
+#pragma unroll
+                for (int a = 0; a < V; a += 4)
+                    *reinterpret_cast<float4 *>(&s_v[r][c + a]) = make_float4(x[a], x[a + 1], x[a + 2], x[a + 3]);
+            }
+        }
+        const float all = expf(s_hi[i & 1][C - 1]);
         __syncthreads();
-        load_tile<DK>(&s_k[0][0], DK, k + t0 * A.Hk * DK, (int64_t)A.Hk * DK, len, s_f);
-        load_tile<CW>(&s_v[0][0], CW, v + t0 * A.Hv * DV, (int64_t)A.Hv * DV, len, nullptr);
-        const float all = expf(s_hi[C - 1]);
-        __syncthreads();
+        fetch(i + 1);
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -143,7 +187,7 @@ __global__ void __launch_bounds__(NT) linear_states_kernel(states_args fwd, stat
 #pragma unroll
                 for (int j = 0; j < TN; ++j) S[a][j] = fmaf(xs[a], y[j], S[a][j]);
         }
-        __syncthreads();
+        decays_of(i + 1);
     }
     if (A.fin) {
 #pragma unroll
@@ -244,7 +288,11 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(const T *q, const T *k, 
     chunk c;
     if (!find_chunk<C>(cu, tokens, N, slot, &c)) return;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    if (tid < 32) chunk_decays<C>(g ? g + c.tok0 * g_tok + h : nullptr, g_stride, c.len, s_hi, s_lo);
+    if (tid < 32) {
+        float x[C / 32];
+        load_decays<C>(g ? g + c.tok0 * g_tok + h : nullptr, g_stride, c.len, x);
+        chunk_decays<C>(x, s_hi, s_lo);
+    }
     load_tile<DK>(s_q, PK, q + (c.tok0 * Hq + h / (H / Hq)) * DK, (int64_t)Hq * DK, c.len, nullptr);
     load_tile<DK>(s_b, PK, k + (c.tok0 * Hk + h / (H / Hk)) * DK, (int64_t)Hk * DK, c.len, nullptr);
     load_tile<DV>(s_v, PV, v + (c.tok0 * Hv + h / (H / Hv)) * DV, (int64_t)Hv * DV, c.len, nullptr);
@@ -346,7 +394,11 @@ __global__ void __launch_bounds__(NT) linear_grads_kernel(grads_args A) {
         if (A.dg_slot && tid == 0) A.dg_slot[slot * H + h] = 0.f;
         return;
     }
-    if (tid < 32) chunk_decays<C>(A.g ? A.g + c.tok0 * A.g_tok + h : nullptr, A.g_stride, c.len, s_hi, s_lo);
+    if (tid < 32) {
+        float x[C / 32];
+        load_decays<C>(A.g ? A.g + c.tok0 * A.g_tok + h : nullptr, A.g_stride, c.len, x);
+        chunk_decays<C>(x, s_hi, s_lo);
+    }
     load_tile<DK>(s_q, PK, (const T *)A.q + (c.tok0 * A.Hq + h / (H / A.Hq)) * DK, (int64_t)A.Hq * DK, c.len, nullptr);
     load_tile<DK>(s_k, PK, (const T *)A.k + (c.tok0 * A.Hk + h / (H / A.Hk)) * DK, (int64_t)A.Hk * DK, c.len, nullptr);
     load_tile<DV>(s_v, PV, (const T *)A.v + (c.tok0 * A.Hv + h / (H / A.Hv)) * DV, (int64_t)A.Hv * DV, c.len, nullptr);
@@ -450,25 +502,31 @@ __global__ void __launch_bounds__(NT) linear_grads_kernel(grads_args A) {
     // dg_t = sum_{r >= t} (own pairs + outputs of the entering state) + sum_{j < t} keys into the leaving state
     //        + e^{G_C} <S, Lambda>
     if (tid < 32) {
-        double whole = 0.0;
-        for (int w = 0; w < NT / 32; ++w) whole += (double)s_dot[w];
-        whole *= (double)expf(Gh);
-        double x0 = (double)s_row[2 * tid] + s_qdq[2 * tid], x1 = (double)s_row[2 * tid + 1] + s_qdq[2 * tid + 1];
-        double after = x0 + x1, k0 = s_kdk[2 * tid], k1 = s_kdk[2 * tid + 1], before = k0 + k1;
+        ff whole{0.f, 0.f};
+        for (int w = 0; w < NT / 32; ++w) whole = ff_add(whole, {s_dot[w], 0.f});
+        const float all = (whole.h + whole.l) * expf(Gh);
+        const ff x0 = ff_add({s_row[2 * tid], 0.f}, {s_qdq[2 * tid], 0.f});
+        const ff own = ff_add(x0, ff_add({s_row[2 * tid + 1], 0.f}, {s_qdq[2 * tid + 1], 0.f}));
+        const float k0 = s_kdk[2 * tid];
+        const ff keys = ff_add({k0, 0.f}, {s_kdk[2 * tid + 1], 0.f});
+        ff after = own, before = keys;
         for (int off = 1; off < 32; off <<= 1) {
-            const double a = __shfl_down_sync(0xffffffffu, after, off), b = __shfl_up_sync(0xffffffffu, before, off);
-            if (tid + off < 32) after += a;
-            if (tid >= off) before += b;
+            const ff a = ff_shfl(after, (tid + off) & 31), b = ff_shfl(before, (tid - off) & 31);
+            if (tid + off < 32) after = ff_add(after, a);
+            if (tid >= off) before = ff_add(b, before);
         }
-        before -= k0 + k1;
-        const double g0 = after + before + whole, g1 = after - x0 + before + k0 + whole;
+        before = ff_add(before, {-keys.h, -keys.l});
+        const ff base = ff_add(before, {all, 0.f});
+        const ff g0 = ff_add(after, base), g1 = ff_add(ff_add(after, {-x0.h, -x0.l}), ff_add(base, {k0, 0.f}));
         if (A.dg) {
-            if (2 * tid < c.len) A.dg[(c.tok0 + 2 * tid) * H + h] = (float)g0;
-            if (2 * tid + 1 < c.len) A.dg[(c.tok0 + 2 * tid + 1) * H + h] = (float)g1;
+            if (2 * tid < c.len) A.dg[(c.tok0 + 2 * tid) * H + h] = g0.h + g0.l;
+            if (2 * tid + 1 < c.len) A.dg[(c.tok0 + 2 * tid + 1) * H + h] = g1.h + g1.l;
         } else {
-            double sum = (2 * tid < c.len ? g0 : 0.0) + (2 * tid + 1 < c.len ? g1 : 0.0);
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (tid == 0) A.dg_slot[slot * H + h] = (float)sum;
+            ff sum{0.f, 0.f};
+            if (2 * tid < c.len) sum = g0;
+            if (2 * tid + 1 < c.len) sum = ff_add(sum, g1);
+            for (int off = 16; off > 0; off >>= 1) sum = ff_add(sum, ff_shfl(sum, (tid + off) & 31));
+            if (tid == 0) A.dg_slot[slot * H + h] = sum.h + sum.l;
         }
     }
 }

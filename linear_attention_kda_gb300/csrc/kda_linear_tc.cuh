@@ -31,19 +31,6 @@ __device__ __forceinline__ float ends(const decays &d, int a, int b) {  // E_a -
     if (a < 0) return b < 0 ? 0.f : -d.hi[b];
     return b < 0 ? d.hi[a] : (d.hi[a] - d.hi[b]) + (d.lo[a] - d.lo[b]);
 }
-// Sums of two floats each (48 bits): the fp64 pipe of this GPU would take three times as long for a chunk's sums.
-struct ff {
-    float h, l;
-};
-__device__ __forceinline__ ff ff_add(const ff &a, const ff &b) {
-    const float s = a.h + b.h, t = s - a.h, e = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l), h = s + e;
-    return {h, e - (h - s)};
-}
-__device__ __forceinline__ float ff_diff(const ff &a, const ff &b) { return (a.h - b.h) + (a.l - b.l); }
-__device__ __forceinline__ ff ff_shfl(const ff &a, int lane) {
-    return {__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
-}
-
 // One warp computes a chunk's decays, four tokens a lane, from log-decays that it has loaded before.
 __device__ __forceinline__ float4 load_log_decays(const float *g, int g_stride, int len) {
     const int r = (threadIdx.x & 31) * 4;
@@ -59,7 +46,7 @@ __device__ __forceinline__ void make_decays(const float4 &g, decays &d, float *r
     ff x[4], pre;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const ff y{in[i] < -104.f ? -104.f : in[i], 0.f};
+        const ff y{clamp_decay(in[i]), 0.f};
         x[i] = i ? ff_add(x[i - 1], y) : y;
     }
     pre = x[3];  // up to and with this lane

@@ -674,7 +674,16 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
         raise ValueError(f"{where}: freqs is a float64 vector on the host")
     if not freqs.is_contiguous():
         freqs = freqs.contiguous()
-    _require(where, dev, (("positions", positions, (T,), torch.int32),))
+    plain = out_q is None and out_k is None and (q is None or q.is_contiguous()) and (k is None or k.is_contiguous())
+    Hq, Hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    _require(where, dev, (("positions", positions, (T,), torch.int32), ("q", q if plain else None, (T, Hq, d), dt),
+                          ("k", k if plain else None, (T, Hk, d), dt)))
+    if plain:
+        yq, yk = None if q is None else torch.empty_like(q), None if k is None else torch.empty_like(k)
+        _run("kda_rope", dev, L.kda_rope,
+             _ROPE.pack(T, Hq, Hk, d, 2 * freqs.numel(), code, ROPE_LAYOUTS[layout], int(inverse), scale, positions.data_ptr(),
+                        freqs.data_ptr(), _p(q), _p(k), _p(yq), _p(yk), 0, 0, 0, 0))
+        return yq, yk
 
     def rows(name, x, y):  # (heads, input, its token stride, output, its token stride); 0 heads: absent
         if x is None:
