@@ -412,8 +412,8 @@ def recurrent_replay(cached, n_replay, new, n_commit, dt_bias, A_log, state, *, 
 
 
 # ---------------------------------------------------------------- linear attention with a decay per head
-# A decode step's kernel takes 4 us, so what a call does on the host counts: checks in one pass over the tensors (a
-# second, descriptive one only where something is wrong), arguments packed by struct (a third of a ctypes.Structure's
+# A decode step's kernel takes 4 us, so what a call does on the host counts: quick checks (a second,
+# descriptive look only where something is wrong), arguments packed by struct (a third of a ctypes.Structure's
 # time, same layout), the current device and stream asked for once.
 _LINEAR = struct.Struct("@qq7iPPPPifPPPP")
 _LINEAR_BWD = struct.Struct("@qq7iPPPPif" + "P" * 9)
@@ -425,13 +425,8 @@ assert [x.size for x in (_LINEAR, _LINEAR_BWD, _LINEAR_STEP, _STATE_COPY, _ROPE)
 
 
 def _require(where: str, device: int, spec):
-    """Checks (name, tensor, shape, dtype) of one call: shape, dtype, dense layout, one CUDA device (None passes)."""
-    for _, t, shape, dtype in spec:
-        if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
-            break
-    else:
-        if device >= 0:
-            return
+    """Says what is wrong with a call's (name, tensor, shape, dtype): shape, dtype, dense layout, one CUDA device (None
+    passes)."""
     for name, t, shape, dtype in spec:
         if t is None:
             continue
@@ -443,7 +438,12 @@ def _require(where: str, device: int, spec):
             raise ValueError(f"{where}: {name} must be contiguous")
         if t.get_device() != device:
             raise ValueError(f"{where}: {name} is not on the device of the others")
-    raise ValueError(f"{where}: tensors must be on a CUDA device")
+    if device < 0:
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+
+
+def _off(t, shape, dtype, device) -> bool:
+    return t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()
 
 
 def _run(where: str, device: int, fn, packed: bytes, *more):
@@ -520,11 +520,15 @@ def linear_chunk_fwd(q, k, v, g=None, *, scale: float = 1.0, cu_seqlens: Optiona
     where, L, f32 = "linear_chunk_fwd", _lib or load_library(), torch.float32
     T, H, Hq, Hk, Hv, dk, dv, per_token, code = _linear_heads(where, q, k, v, g)
     N, dt, dev = _n_sequences(where, cu_seqlens, n_seq), q.dtype, q.get_device()
-    state = (N, H, dk, dv)
-    _require(where, dev, (("q", q, (T, Hq, dk), dt), ("k", k, (T, Hk, dk), dt), ("v", v, (T, Hv, dv), dt),
-                          ("g", g, (T, H) if per_token else (H,), f32), ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32),
-                          ("initial_state", initial_state, state, f32), ("final_state", final_state, state, f32),
-                          ("out", out, (T, H, dv), dt)))
+    state, gshape = (N, H, dk, dv), (T, H) if per_token else (H,)
+    if (dev < 0 or not q.is_contiguous() or _off(k, (T, Hk, dk), dt, dev) or _off(v, (T, Hv, dv), dt, dev)
+            or (g is not None and _off(g, gshape, f32, dev)) or (cu_seqlens is not None and _off(cu_seqlens, (N + 1,), torch.int32, dev))
+            or (initial_state is not None and _off(initial_state, state, f32, dev))
+            or (final_state is not None and _off(final_state, state, f32, dev)) or (out is not None and _off(out, (T, H, dv), dt, dev))):
+        _require(where, dev, (("q", q, (T, Hq, dk), dt), ("k", k, (T, Hk, dk), dt), ("v", v, (T, Hv, dv), dt),
+                              ("g", g, gshape, f32), ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32),
+                              ("initial_state", initial_state, state, f32), ("final_state", final_state, state, f32),
+                              ("out", out, (T, H, dv), dt)))
     if out is None:
         out = torch.empty_like(v) if Hv == H else torch.empty((T, H, dv), dtype=dt, device=q.device)
     if final_state is None and output_final_state:
@@ -547,11 +551,16 @@ def linear_chunk_bwd(q, k, v, g, grad_o, *, scale: float = 1.0, cu_seqlens: Opti
     where, L, f32 = "linear_chunk_bwd", _lib or load_library(), torch.float32
     T, H, Hq, Hk, Hv, dk, dv, per_token, code = _linear_heads(where, q, k, v, g)
     N, dt, dev = _n_sequences(where, cu_seqlens, n_seq), q.dtype, q.get_device()
-    state = (N, H, dk, dv)
-    _require(where, dev, (("q", q, (T, Hq, dk), dt), ("k", k, (T, Hk, dk), dt), ("v", v, (T, Hv, dv), dt),
-                          ("g", g, (T, H) if per_token else (H,), f32), ("grad_o", grad_o, (T, H, dv), dt),
-                          ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, state, f32),
-                          ("grad_final_state", grad_final_state, state, f32)))
+    state, gshape = (N, H, dk, dv), (T, H) if per_token else (H,)
+    if (dev < 0 or not q.is_contiguous() or _off(k, (T, Hk, dk), dt, dev) or _off(v, (T, Hv, dv), dt, dev)
+            or _off(grad_o, (T, H, dv), dt, dev) or (g is not None and _off(g, gshape, f32, dev))
+            or (cu_seqlens is not None and _off(cu_seqlens, (N + 1,), torch.int32, dev))
+            or (initial_state is not None and _off(initial_state, state, f32, dev))
+            or (grad_final_state is not None and _off(grad_final_state, state, f32, dev))):
+        _require(where, dev, (("q", q, (T, Hq, dk), dt), ("k", k, (T, Hk, dk), dt), ("v", v, (T, Hv, dv), dt),
+                              ("g", g, gshape, f32), ("grad_o", grad_o, (T, H, dv), dt),
+                              ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, state, f32),
+                              ("grad_final_state", grad_final_state, state, f32)))
     grads = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v)}
     if decay_grad and g is not None:
         grads["g"] = torch.empty_like(g)
@@ -576,10 +585,14 @@ def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, state_indice
     if state.dim() != 4:
         raise ValueError(f"{where}: state has shape [slots, heads, dk, dv]")
     slots, dt, dev = state.shape[0], q.dtype, q.get_device()
-    _require(where, dev, (("q", q, (N, Hq, dk), dt), ("k", k, (N, Hk, dk), dt), ("v", v, (N, Hv, dv), dt),
-                          ("g", g, (N, H) if per_token else (H,), torch.float32),
-                          ("state", state, (slots, H, dk, dv), torch.float32),
-                          ("state_indices", state_indices, (N,), torch.int32), ("out", out, (N, H, dv), dt)))
+    f32, gshape = torch.float32, (N, H) if per_token else (H,)
+    if (dev < 0 or not q.is_contiguous() or _off(k, (N, Hk, dk), dt, dev) or _off(v, (N, Hv, dv), dt, dev)
+            or _off(state, (slots, H, dk, dv), f32, dev) or (g is not None and _off(g, gshape, f32, dev))
+            or (state_indices is not None and _off(state_indices, (N,), torch.int32, dev))
+            or (out is not None and _off(out, (N, H, dv), dt, dev))):
+        _require(where, dev, (("q", q, (N, Hq, dk), dt), ("k", k, (N, Hk, dk), dt), ("v", v, (N, Hv, dv), dt), ("g", g, gshape, f32),
+                              ("state", state, (slots, H, dk, dv), f32), ("state_indices", state_indices, (N,), torch.int32),
+                              ("out", out, (N, H, dv), dt)))
     if N > 0 and slots < (1 if state_indices is not None else N):
         raise ValueError(f"{where}: {slots} state slots for {N} sequences")
     if out is None:
@@ -600,8 +613,10 @@ def state_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, *, out_
     if pool.dim() < 2 or src.dim() != 1 or to.dim() != pool.dim():
         raise ValueError(f"{where}: the pools have shape [slots, ...] and src one dimension")
     dt, dev, P = pool.dtype, pool.get_device(), src.shape
-    _require(where, dev, (("pool", pool, pool.shape, dt), ("out_pool", to, to.shape[:1] + pool.shape[1:], dt),
-                          ("src", src, P, torch.int32), ("dst", dst, P, torch.int32)))
+    if (dev < 0 or not pool.is_contiguous() or _off(src, P, torch.int32, dev) or _off(dst, P, torch.int32, dev)
+            or (to is not pool and _off(to, to.shape[:1] + pool.shape[1:], dt, dev))):
+        _require(where, dev, (("pool", pool, pool.shape, dt), ("out_pool", to, to.shape[:1] + pool.shape[1:], dt),
+                              ("src", src, P, torch.int32), ("dst", dst, P, torch.int32)))
     n, m = pool.shape[0], to.shape[0]
     slot = (pool.numel() // n if n else to.numel() // m if m else 0) * pool.element_size()
     _run("kda_state_copy", dev, L.kda_state_copy, _STATE_COPY.pack(_p(pool), _p(to), slot, n, m, P[0], _p(src), _p(dst)))
@@ -676,8 +691,9 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
         freqs = freqs.contiguous()
     plain = out_q is None and out_k is None and (q is None or q.is_contiguous()) and (k is None or k.is_contiguous())
     Hq, Hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
-    _require(where, dev, (("positions", positions, (T,), torch.int32), ("q", q if plain else None, (T, Hq, d), dt),
-                          ("k", k if plain else None, (T, Hk, d), dt)))
+    if (dev < 0 or _off(positions, (T,), torch.int32, dev) or (plain and k is not None and _off(k, (T, Hk, d), dt, dev))):
+        _require(where, dev, (("positions", positions, (T,), torch.int32), ("q", q if plain else None, (T, Hq, d), dt),
+                              ("k", k if plain else None, (T, Hk, d), dt)))
     if plain:
         yq, yk = None if q is None else torch.empty_like(q), None if k is None else torch.empty_like(k)
         _run("kda_rope", dev, L.kda_rope,
