@@ -9,7 +9,8 @@
 //                                    dV = f (K Lambda) + A^T dO,       f = e^{G_C - G},
 //                                and the decay's gradient.
 //
-// Numerics: A, dA and the first parts of S and Lambda are rounded to bf16 once; they make bf16 gradients.  The decay's
+// Numerics: the chains' terms are fp32 products in three bf16 parts.  A, dA and the first parts of S and Lambda are
+// rounded to bf16 once; they make bf16 gradients.  The decay's
 // gradient is an fp32 result: the products that it is summed from, Q K^T, dO V^T, dO S^T and V Lambda^T, have exact
 // bf16 operands or both parts of a state (2^-16), and are taken in fp32 before any rounding.
 #include <type_traits>
@@ -47,16 +48,17 @@ constexpr int W = 64;      // value columns of a CTA
 
 template <int DK> struct states_smem {
     static constexpr int AT = C * DK * 2, BT = C * W * 2, STAGE = AT + BT, IMG = DK * W * 2;
-    static constexpr int LO = 3 * STAGE;                // second parts of the scaled rows, of two chunks
-    static constexpr int DEC = LO + 2 * AT;
+    static constexpr int MID = 3 * STAGE, LO = MID + AT;  // second and third parts of the scaled rows
+    static constexpr int DEC = LO + AT;
     static constexpr int BAR = DEC + 3 * (int)sizeof(decays);
     static constexpr int BYTES = BAR + 256;
     static_assert(2 * IMG <= AT, "a chunk's images leave through the rows' tile of the chunk before");
 };
 
 // The chain of 64 value columns of one (sequence, head), S [dk lanes][64 columns] in tensor memory.  The loop is:
-// product (both parts of the scaled rows), state out and scaled, product; the images of the state go to memory and
-// the next chunk's rows are scaled under it.  Three stages of tiles: with two, a chunk's tiles were asked for when the
+// product (three parts of the scaled rows: with two, 2^-16 of a term, the decay's gradient was off by 1e-5), state out
+// and scaled, second and third parts to their places, product; the images of the state go to memory and the next
+// chunk's rows are scaled and split under it.  Three stages of tiles: with two, a chunk's tiles were asked for when the
 // last product but one had ended, and their way (2000 cycles) and the scaling (1200) made the step.
 template <int DK, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -66,9 +68,9 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     decays *dec = reinterpret_cast<decays *>(sm + L::DEC);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     // in: a chunk's tiles and its decays
-    uint64_t *in = bars, *dec_free = bars + 3, *k_ready = bars + 6, *s_ready = bars + 7, *u_done = bars + 8,
-             *stg_full = bars + 9, *stg_done = bars + 10;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 11);
+    uint64_t *in = bars, *dec_free = bars + 3, *s_ready = bars + 6, *u_done = bars + 7, *stg_full = bars + 8,
+             *stg_done = bars + 9;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 10);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool back = blockIdx.y == 1;
@@ -87,7 +89,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
     auto len_of = [&](int i) { const int64_t r = sp.b - tok_of(i); return (int)(r < C ? r : C); };
     if (tid == 0) {
-        for (int i = 0; i < 11; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 8 || i == 10 ? 1 : 16);
+        for (int i = 0; i < 10; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 7 || i == 9 ? 1 : 16);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, W);
@@ -121,11 +123,12 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             constexpr uint32_t ALBO = DK == 128 ? 16384 : 0;  // dk = 64: lanes 64 .. 127 repeat lanes 0 .. 63, unread
             for (int i = 0; i < nc; ++i) {
                 const uint32_t st = smem_u32(sm + i % 3 * L::STAGE);
-                ok = bar_wait(k_ready, i & 1) && bar_wait(s_ready, i & 1) && bar_wait(in + i % 3, (i / 3) & 1);
+                ok = bar_wait(s_ready, i & 1) && bar_wait(in + i % 3, (i / 3) & 1);
                 if (!ok) break;
                 fence_after_sync();
                 mma_bf16_mnmn(tb, st, ALBO, st + L::AT, 16384, C / 16, id, true);
-                mma_bf16_mnmn(tb, smem_u32(sm + L::LO + (i & 1) * L::AT), ALBO, st + L::AT, 16384, C / 16, id, true);
+                mma_bf16_mnmn(tb, smem_u32(sm + L::MID), ALBO, st + L::AT, 16384, C / 16, id, true);
+                mma_bf16_mnmn(tb, smem_u32(sm + L::LO), ALBO, st + L::AT, 16384, C / 16, id, true);
                 mma_commit(u_done);
             }
         }
@@ -167,17 +170,16 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        auto scale_rows = [&](int i) {
+        uint4 mid[KC], low[KC];  // of the next chunk's rows
+        auto split_rows = [&](int i) {
             const int len = len_of(i);
             unsigned char *st = sm + i % 3 * L::STAGE;
             wait(in + i % 3, (i / 3) & 1);
             if (!ok) return;
             const decays &d = dec[i % 3];
             const float f = back ? D.scale * expf(ends(d, quarter - 1, -1) + d.rel[row]) : expf(ends(d, 3, quarter)) * d.w[row];
-            scale_chunks<KC>(st, sm + L::LO + (i & 1) * L::AT, row, KC * part, row < len ? f : 0.f);
+            split_chunks<KC>(st, row, KC * part, row < len ? f : 0.f, mid, low);
             if (row >= len) clear_chunks<W / 32>(st + L::AT, row, W / 32 * part);
-            fence_proxy_async();
-            arrive(k_ready);
         };
         float x[CW];
 #pragma unroll
@@ -185,7 +187,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             const float4 v = mine && D.init ? *reinterpret_cast<const float4 *>(D.init + at + c) : make_float4(0, 0, 0, 0);
             x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
         }
-        if (nc > 0) scale_rows(0);
+        if (nc > 0) split_rows(0);
         for (int i = 0; i < nc; ++i) {
             if (i > 0) {
                 wait(u_done, (i - 1) & 1);
@@ -198,7 +200,13 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
 #pragma unroll
             for (int c = 0; c < CW; ++c) y[c] = x[c] * all;
             tmem_store<CW>(ts, y);
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                *reinterpret_cast<uint4 *>(sm + L::MID + img_chunk_off(C, row, KC * part + j)) = mid[j];
+                *reinterpret_cast<uint4 *>(sm + L::LO + img_chunk_off(C, row, KC * part + j)) = low[j];
+            }
             tmem_st_wait();
+            fence_proxy_async();
             fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -222,7 +230,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 fence_proxy_async();
                 arrive(stg_full);
             }
-            if (i + 1 < nc) scale_rows(i + 1);
+            if (i + 1 < nc) split_rows(i + 1);
             if (!ok) break;
         }
         if (ok && D.fin) {

@@ -94,9 +94,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
 bool make_token_map(CUtensorMap *m, const void *base, int64_t T, int heads, int D);
 
 // Chunks j0 .. j0 + N - 1 (16 bytes each) of row `row` of a [128][*] K-major tile times f, in place as its bf16 part,
-// the rest of it to `rest`, by packed bf16 arithmetic: with f = fh + fl in two bf16 parts, hi = bf16(k fh),
-// k fh - hi is a bf16 number exactly (16 bits in all), and lo = bf16(k fl + (k fh - hi)).  Lost: 2^-16 of the row in
-// fl, 2^-16 in lo, at most.
+// the rest of it to `rest`, by packed bf16 arithmetic: with f = fh + fl in two bf16 parts, hi = bf16(k fh + k fl),
+// lo = bf16(k fl + (k fh - hi)).  Lost: 2^-16 of the row at most, 3e-6 of it on average.
 template <int N>
 __device__ __forceinline__ void scale_chunks(unsigned char *tile, unsigned char *rest, int row, int j0, float f) {
     const bf16 fh = __float2bfloat16_rn(f), fl = __float2bfloat16_rn(f - __bfloat162float(fh));
@@ -112,7 +111,7 @@ __device__ __forceinline__ void scale_chunks(unsigned char *tile, unsigned char 
         if (f == 0.f) x[j].u = make_uint4(0, 0, 0, 0);  // erased, whatever the row holds
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 hi = __hmul2(x[j].p[i], h2);
+            const __nv_bfloat162 hi = __hfma2(x[j].p[i], h2, __hmul2(x[j].p[i], l2));
             lo.p[i] = __hfma2(x[j].p[i], l2, __hfma2(x[j].p[i], h2, __hneg2(hi)));
             x[j].p[i] = hi;
         }
@@ -127,6 +126,27 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// The same in three parts, which together are the fp32 product: hi in place, mid and lo left in registers.
+template <int N>
+__device__ __forceinline__ void split_chunks(unsigned char *tile, int row, int j0, float f, uint4 *mid, uint4 *lo) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        unsigned char *at = tile + img_chunk_off(C, row, j0 + j);
+        uint4 u = *reinterpret_cast<const uint4 *>(at);
+        if (f == 0.f) u = make_uint4(0, 0, 0, 0);  // erased, whatever the row holds
+        uint32_t *x = reinterpret_cast<uint32_t *>(&u), *m = reinterpret_cast<uint32_t *>(mid + j),
+                 *l = reinterpret_cast<uint32_t *>(lo + j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a = bf_lo(x[i]) * f, b = bf_hi(x[i]) * f;
+            x[i] = pack_bf16(a, b);
+            a -= bf_lo(x[i]), b -= bf_hi(x[i]);
+            m[i] = pack_bf16(a, b);
+            l[i] = pack_bf16(a - bf_lo(m[i]), b - bf_hi(m[i]));
+        }
+        *reinterpret_cast<uint4 *>(at) = u;
+    }
+}
 template <int N>
 __device__ __forceinline__ void clear_chunks(unsigned char *tile, int row, int j0) {
 #pragma unroll
