@@ -55,10 +55,11 @@ template <int DK> struct states_smem {
     static_assert(2 * IMG <= AT, "a chunk's images leave through the rows' tile of the chunk before");
 };
 
-// The chain of 64 value columns of one (sequence, head), S [dk lanes][64 columns] in tensor memory.  The loop is:
-// product (three parts of the scaled rows: with two, 2^-16 of a term, the decay's gradient was off by 1e-5), state out
-// and scaled, second and third parts to their places, product; the images of the state go to memory and the next
-// chunk's rows are scaled and split under it.  Three stages of tiles: with two, a chunk's tiles were asked for when the
+// The chain of 64 value columns of one (sequence, head), S [dk rows][64 columns] in the threads' registers; a chunk's
+// products, three parts of the scaled rows (with two, 2^-16 of a term, the decay's gradient was off by 1e-5), are made
+// anew in tensor memory and added there in fp32: an accumulator that the chain itself ran through would lose a little at
+// every K-step, always in one direction (2.6e-6 of a slowly decaying state).  Under a chunk's products the state before
+// it goes to memory as images and the next chunk's rows are scaled and split.  Three stages of tiles: with two, a chunk's tiles were asked for when the
 // last product but one had ended, and their way (2000 cycles) and the scaling (1200) made the step.
 template <int DK, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -92,7 +93,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         for (int i = 0; i < 10; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 7 || i == 9 ? 1 : 16);
         *fail = 0;
     }
-    if (warp == 1) tmem_alloc(tmem_slot, W);
+    if (warp == 1) tmem_alloc(tmem_slot, 2 * W);
     fence_proxy_async();
     fence_before_sync();
     __syncthreads();
@@ -126,9 +127,10 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 ok = bar_wait(s_ready, i & 1) && bar_wait(in + i % 3, (i / 3) & 1);
                 if (!ok) break;
                 fence_after_sync();
-                mma_bf16_mnmn(tb, st, ALBO, st + L::AT, 16384, C / 16, id, true);
-                mma_bf16_mnmn(tb, smem_u32(sm + L::MID), ALBO, st + L::AT, 16384, C / 16, id, true);
-                mma_bf16_mnmn(tb, smem_u32(sm + L::LO), ALBO, st + L::AT, 16384, C / 16, id, true);
+                const uint32_t t = tb + (i & 1) * W;  // smallest terms first
+                mma_bf16_mnmn(t, smem_u32(sm + L::LO), ALBO, st + L::AT, 16384, C / 16, id, false);
+                mma_bf16_mnmn(t, smem_u32(sm + L::MID), ALBO, st + L::AT, 16384, C / 16, id, true);
+                mma_bf16_mnmn(t, st, ALBO, st + L::AT, 16384, C / 16, id, true);
                 mma_commit(u_done);
             }
         }
@@ -188,31 +190,30 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
         }
         if (nc > 0) split_rows(0);
+        float all = 1.f;
+        auto add_products = [&](int i) {  // of chunk i, behind the whole decay of it
+            float y[CW];
+            tmem_load<CW>(ts + (i & 1) * W, y);
+#pragma unroll
+            for (int c = 0; c < CW; ++c) x[c] = fmaf(x[c], all, y[c]);
+        };
         for (int i = 0; i < nc; ++i) {
             if (i > 0) {
                 wait(u_done, (i - 1) & 1);
                 if (!ok) break;
                 fence_after_sync();
-                tmem_load<CW>(ts, x);
             }
-            const float all = expf(dec[i % 3].hi[3]);
-            float y[CW];
-#pragma unroll
-            for (int c = 0; c < CW; ++c) y[c] = x[c] * all;
-            tmem_store<CW>(ts, y);
 #pragma unroll
             for (int j = 0; j < KC; ++j) {
                 *reinterpret_cast<uint4 *>(sm + L::MID + img_chunk_off(C, row, KC * part + j)) = mid[j];
                 *reinterpret_cast<uint4 *>(sm + L::LO + img_chunk_off(C, row, KC * part + j)) = low[j];
             }
-            tmem_st_wait();
             fence_proxy_async();
+            arrive(s_ready);
+            if (i > 0) add_products(i - 1);
             fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(s_ready);
-                mbar_arrive(dec_free + i % 3);
-            }
+            all = expf(dec[i % 3].hi[3]);
+            arrive(dec_free + i % 3);
             {  // the images, under the product, by way of the rows' tile of the chunk before
                 if (mine) {
 #pragma unroll
@@ -233,25 +234,25 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             if (i + 1 < nc) split_rows(i + 1);
             if (!ok) break;
         }
-        if (ok && D.fin) {
-            if (nc > 0) {
-                wait(u_done, (nc - 1) & 1);
+        if (ok && nc > 0) {
+            wait(u_done, (nc - 1) & 1);
+            if (ok) {
                 fence_after_sync();
-                tmem_load<CW>(ts, x);
+                add_products(nc - 1);
             }
+        }
+        if (ok && D.fin) {
             if (mine && ok) {
 #pragma unroll
                 for (int c = 0; c < CW; c += 4)
                     *reinterpret_cast<float4 *>(D.fin + at + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
             }
-        } else if (ok && nc > 0) {
-            wait(u_done, (nc - 1) & 1);
         }
     }
     if (!ok) atomicExch(fail, 1);
     fence_before_sync();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tb, W);
+    if (warp == 1) tmem_dealloc(tb, 2 * W);
     if (tid == 0 && *fail) set_error(a.err, KDA_ERR_DEVICE_TIMEOUT);
 }
 
