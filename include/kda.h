@@ -382,6 +382,8 @@ kda_status_t kda_recurrent_step(const kda_step_args *args, struct CUstream_st *s
  * (g NULL: exp(g) = 1).  g is fp32 and at most 0; a log-decay below -104 (-inf included) counts as
  * -104, whose factor is 0 in fp32: it erases the state.  Values above 0 are computed as given and may
  * overflow; a NaN spreads over its sequence and head from its token on (in a gradient, over the sequence).
+ * A NaN or an infinity in q, k, v or grad_o stays in its sequence and head too, but may reach the tokens before it in
+ * its chunk (64 tokens in fp32, 128 in bf16): products with masked zeros are formed there.
  *
  * Heads: H states per sequence.  Hq, Hk and Hv say how many heads q, k and v have; each divides H, the
  * largest of them is H, and state head h reads head h / (H / Hx) of each (q and k shared by groups of
@@ -389,8 +391,8 @@ kda_status_t kda_recurrent_step(const kda_step_args *args, struct CUstream_st *s
  *
  * Shapes: q [T, Hq, dk], k [T, Hk, dk], v [T, Hv, dv], o [T, H, dv]; dk and dv each 64 or 128; states
  * [N, H, dk, dv] fp32.  Memory, packing, streams and errors are as for kda_chunk_fwd; cu_seqlens
- * contents are checked on the device (KDA_ERR_BAD_SEQLENS; sequences with a bad range are skipped and
- * rows that belong to no sequence are left as they were).  An empty sequence's final state is its
+ * contents are checked on the device (KDA_ERR_BAD_SEQLENS; sequences with a bad range are skipped, their
+ * gradients' rows unspecified, and rows that belong to no sequence are left as they were).  An empty sequence's final state is its
  * initial state, exactly.  Outputs may not overlap inputs, except that final_state may be
  * initial_state.  Every call is free of atomics on its results: the same inputs give the same bits. */
 typedef struct {

@@ -519,7 +519,7 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
                 for (int j = i > 2 ? i - 2 : 0; j < i; ++j) bar_wait(full + (j & 1), (j >> 1) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t id_u = idesc_bf16(128, DV, true, true);
             constexpr uint32_t KLBO = DK == 128 ? 16384 : 0;
             for (int i = 0; i < nc; ++i) {

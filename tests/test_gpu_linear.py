@@ -151,6 +151,24 @@ def test_nan_decay_stays_in_its_sequence_and_head(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_no_number_stays_in_its_sequence(dtype, value):
+    """The neighbours of a sequence full of NaN or infinities, ragged ends in its chunks, keep every bit."""
+    d = LU.batch([100, 77, 130, 3], 2, 64, 128, dtype, 19)
+    bad = dict(d)
+    for n in ("q", "k", "v", "grad_o"):
+        bad[n] = d[n].clone()
+        bad[n][100:177] = value
+    keep = torch.ones(310, dtype=torch.bool, device="cuda")
+    keep[100:177] = False
+    (o, S), (bo, bS), r, br = _run_fwd(d), _run_fwd(bad), _run_bwd(d), _run_bwd(bad)
+    assert torch.equal(o[keep], bo[keep]) and torch.equal(S[[0, 2, 3]], bS[[0, 2, 3]])
+    for n in ("q", "k", "v", "g"):
+        assert torch.equal(r[n][keep], br[n][keep]), n
+    assert torch.equal(r["initial_state"][[0, 2, 3]], br["initial_state"][[0, 2, 3]])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_empty_batch_and_empty_sequences(dtype):
     d = LU.batch([0, 0, 0], 2, 128, 64, dtype, 3)
     x = LU.to(d, "cuda")
@@ -231,6 +249,19 @@ def test_bad_cu_seqlens_is_reported(dtype, cu):
     kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["grad_o"], cu_seqlens=bad)
     assert kda.get_device_error() == 7
     assert kda.get_device_error() == 0
+
+
+@pytest.mark.parametrize("H,N", [(1, 1), (5, 2), (64, 3), (7, 130)])
+def test_batches_of_other_shapes(H, N):
+    """One head, many heads, more sequences than are sorted by length; bf16 against the fp32 kernels on the same values
+    (each is checked against the oracle elsewhere): the difference is both bounds'."""
+    lens = [(37 * i + 5 * H) % 190 for i in range(N)]
+    d = LU.batch(lens, H, 64, 64, "bf16", H + N)
+    f = {n: x.float() if isinstance(x, torch.Tensor) and x.dtype == torch.bfloat16 else x for n, x in d.items()}
+    (o, S), (fo, fS) = _run_fwd(d), _run_fwd(f)
+    mo, mS = (torch.from_numpy(x).cuda() for x in LU.forward_ref(d, True))
+    assert ((o.double() - fo.double()).abs() <= 2 * _per_term(d, False) * mo + LU.EPS_BF16 * fo.double().abs() + 1e-37).all()
+    assert ((S.double() - fS.double()).abs() <= 2 * _per_term(d, True) * mS + 1e-37).all()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -84,6 +84,23 @@ def test_between_pools(P):
     assert torch.equal(_bits(x), _bits(a)) and torch.equal(_bits(y), _bits(_in_order(a, src, dst, b)))
 
 
+@pytest.mark.parametrize("pairs", [
+    [(i, i + 40) for i in range(40)],                                   # independent: pairs are split over blocks
+    [(i, i + 40) for i in range(39)] + [(41, 0)],                       # the last one reads a target
+    [(i, i + 40) for i in range(39)] + [(5, 40)],                       # a target twice
+    [(i, i) for i in range(80)],                                        # onto themselves
+    [(i, i + 40) for i in range(39)] + [(0, 90)],                       # one outside the pool
+])
+def test_pairs_of_small_slots(pairs):
+    pool = _pool(80, (4, 8), torch.float32, 11)
+    got = pool.cuda()
+    kda.state_copy(got, _idx([p[0] for p in pairs]), _idx([p[1] for p in pairs]))
+    bad = [p for p in pairs if max(p) >= 80]
+    assert kda.get_device_error() == (8 if bad else 0)
+    good = [p for p in pairs if max(p) < 80]
+    assert torch.equal(_bits(got), _bits(_in_order(pool, [p[0] for p in good], [p[1] for p in good])))
+
+
 def test_many_pairs_and_slots():
     """A permutation-like move of many small slots, more than one block's worth of pairs."""
     g = torch.Generator().manual_seed(0)
