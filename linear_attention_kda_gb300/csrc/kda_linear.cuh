@@ -63,6 +63,7 @@ __device__ __forceinline__ bool find_slot(const int32_t *cu, int64_t T, int64_t 
 struct chunk {
     int64_t tok0;  // first token
     int len;       // tokens, 1 .. C
+    bool first, last;  // of its sequence
 };
 template <int C>
 __device__ __forceinline__ bool find_chunk(const int32_t *cu, int64_t T, int64_t N, int64_t slot, chunk *c) {
@@ -71,6 +72,8 @@ __device__ __forceinline__ bool find_chunk(const int32_t *cu, int64_t T, int64_t
     if (!find_slot(cu, T, N, C, slot, &n, &i, &s) || s.a + i * C >= s.b) return false;
     c->tok0 = s.a + i * C;
     c->len = (int)(s.b - c->tok0 < C ? s.b - c->tok0 : C);
+    c->first = i == 0;
+    c->last = s.b - c->tok0 <= C;
     return true;
 }
 

@@ -2,7 +2,8 @@
 //
 //   linear_bwd_states_tc_kernel  the chains over chunks, forwards S <- e^{G_C} S + (K e^{G_C - G})^T V and backwards
 //                                Lambda <- e^{G_C} Lambda + scale (Q e^G)^T dO; before every chunk the state as it is
-//                                goes to the workspace as operand images in two bf16 parts (hi + lo).
+//                                goes to the workspace as operand images in two bf16 parts (hi + lo).  The zeros that
+//                                a chain begins with where it is given no state are neither written nor multiplied.
 //   linear_grads_tc_kernel       per (chunk, head): with A = scale Tril[Q K^T * D], dA = scale Tril[dO V^T * D],
 //                                D = e^{G_r - G_t},
 //                                    dQ = scale e^G (dO S^T) + dA K,   dK = f (V Lambda^T) + dA^T Q,
@@ -59,8 +60,9 @@ template <int DK> struct states_smem {
 // products, three parts of the scaled rows (with two, 2^-16 of a term, the decay's gradient was off by 1e-5), are made
 // anew in tensor memory and added there in fp32: an accumulator that the chain itself ran through would lose a little at
 // every K-step, always in one direction (2.6e-6 of a slowly decaying state).  Under a chunk's products the state before
-// it goes to memory as images and the next chunk's rows are scaled and split.  Three stages of tiles: with two, a chunk's tiles were asked for when the
-// last product but one had ended, and their way (2000 cycles) and the scaling (1200) made the step.
+// it goes to memory as images and the next chunk's rows are scaled and split.  Three stages of tiles: with two, a
+// chunk's tiles were asked for when the last product but one had ended, and their way (2000 cycles) and the scaling
+// (1200) made the step.
 template <int DK, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __grid_constant__ states_args a) {
@@ -86,6 +88,9 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     }
     const int nc = (int)((sp.b - sp.a + C - 1) / C);
     const int64_t slot0 = sp.a / C + n;
+    const int np = D.fin ? nc : nc - 1;  // chunks whose products are wanted
+    const int i0 = D.init ? 0 : 1;       // first chunk that has a state before it
+    if (np <= 0 && i0 >= nc && !D.fin) return;
     auto chunk_of = [&](int i) { return back ? nc - 1 - i : i; };
     auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
     auto len_of = [&](int i) { const int64_t r = sp.b - tok_of(i); return (int)(r < C ? r : C); };
@@ -106,10 +111,10 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         if (lane == 0) {
             const int ha = h / D.ra, hb = h / D.rb;
             int i = 0;
-            for (; i < nc; ++i) {
+            for (; i < np; ++i) {
                 unsigned char *st = sm + i % 3 * L::STAGE;
                 const int t = (int)tok_of(i);
-                if (i >= 2) ok = bar_wait(stg_done, i & 1);  // chunk i - 2's images have left by this stage
+                if (i >= 2 + i0) ok = bar_wait(stg_done, (i - i0) & 1);  // chunk i - 2's images have left by this stage
                 if (!ok) break;
                 mbar_arrive_expect_tx(in + i % 3, L::STAGE);
                 for (int b = 0; b < DK / 64; ++b) tma_load_3d(st + b * C * 128, &D.a, 64 * b, ha, t, in + i % 3);
@@ -122,7 +127,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         if (elect_one()) {
             const uint32_t id = idesc_bf16(128, W, true, true);
             constexpr uint32_t ALBO = DK == 128 ? 16384 : 0;  // dk = 64: lanes 64 .. 127 repeat lanes 0 .. 63, unread
-            for (int i = 0; i < nc; ++i) {
+            for (int i = 0; i < np; ++i) {
                 const uint32_t st = smem_u32(sm + i % 3 * L::STAGE);
                 ok = bar_wait(s_ready, i & 1) && bar_wait(in + i % 3, (i / 3) & 1);
                 if (!ok) break;
@@ -136,11 +141,11 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         }
     } else if (warp == 2) {
         auto load = [&](int i) {
-            const bool is = i < nc;
+            const bool is = i < np;
             return load_log_decays(a.g && is ? a.g + tok_of(i) * a.g_stride + h : nullptr, a.g_stride, is ? len_of(i) : 0);
         };
         float4 g = load(0);
-        for (int i = 0; i < nc; ++i) {
+        for (int i = 0; i < np; ++i) {
             const float4 next = load(i + 1);
             if (i >= 3) wait(dec_free + i % 3, (i / 3 - 1) & 1);
             if (!ok) break;
@@ -150,10 +155,10 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         }
     } else if (warp == 3) {
         if (lane == 0) {
-            for (int i = 0; i < nc; ++i) {
+            for (int i = i0; i < nc; ++i) {
                 unsigned char *dst = D.images + ((slot0 + chunk_of(i)) * a.H + h) * (int64_t)(2 * DK * DV * 2) + col * L::IMG;
                 const unsigned char *src = sm + (i + 2) % 3 * L::STAGE;
-                ok = bar_wait(stg_full, i & 1);
+                ok = bar_wait(stg_full, (i - i0) & 1);
                 if (!ok) break;
                 bulk_s2g(dst, src, L::IMG);
                 if (a.lo) bulk_s2g(dst + DK * DV * 2, src + L::IMG, L::IMG);
@@ -189,7 +194,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             const float4 v = mine && D.init ? *reinterpret_cast<const float4 *>(D.init + at + c) : make_float4(0, 0, 0, 0);
             x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
         }
-        if (nc > 0) split_rows(0);
+        if (np > 0) split_rows(0);
         float all = 1.f;
         auto add_products = [&](int i) {  // of chunk i, behind the whole decay of it
             float y[CW];
@@ -203,18 +208,22 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 if (!ok) break;
                 fence_after_sync();
             }
+            if (i < np) {
 #pragma unroll
-            for (int j = 0; j < KC; ++j) {
-                *reinterpret_cast<uint4 *>(sm + L::MID + img_chunk_off(C, row, KC * part + j)) = mid[j];
-                *reinterpret_cast<uint4 *>(sm + L::LO + img_chunk_off(C, row, KC * part + j)) = low[j];
+                for (int j = 0; j < KC; ++j) {
+                    *reinterpret_cast<uint4 *>(sm + L::MID + img_chunk_off(C, row, KC * part + j)) = mid[j];
+                    *reinterpret_cast<uint4 *>(sm + L::LO + img_chunk_off(C, row, KC * part + j)) = low[j];
+                }
+                fence_proxy_async();
+                arrive(s_ready);
             }
-            fence_proxy_async();
-            arrive(s_ready);
             if (i > 0) add_products(i - 1);
             fence_before_sync();
-            all = expf(dec[i % 3].hi[3]);
-            arrive(dec_free + i % 3);
-            {  // the images, under the product, by way of the rows' tile of the chunk before
+            if (i < np) {
+                all = expf(dec[i % 3].hi[3]);
+                arrive(dec_free + i % 3);
+            }
+            if (i >= i0) {  // the images, under the product, by way of the rows' tile of the chunk before
                 if (mine) {
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
@@ -231,22 +240,20 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 fence_proxy_async();
                 arrive(stg_full);
             }
-            if (i + 1 < nc) split_rows(i + 1);
+            if (i + 1 < np) split_rows(i + 1);
             if (!ok) break;
         }
-        if (ok && nc > 0) {
+        if (ok && np == nc && nc > 0) {
             wait(u_done, (nc - 1) & 1);
             if (ok) {
                 fence_after_sync();
                 add_products(nc - 1);
             }
         }
-        if (ok && D.fin) {
-            if (mine && ok) {
+        if (ok && D.fin && mine) {
 #pragma unroll
-                for (int c = 0; c < CW; c += 4)
-                    *reinterpret_cast<float4 *>(D.fin + at + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-            }
+            for (int c = 0; c < CW; c += 4)
+                *reinterpret_cast<float4 *>(D.fin + at + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
         }
     }
     if (!ok) atomicExch(fail, 1);
@@ -268,6 +275,7 @@ struct grads_args {
     int64_t T, N;
     int H, rq, rk, rv;
     const unsigned char *states, *adj;  // images of S before and Lambda behind every chunk
+    bool init, fin;                     // the first chunks have an S, the last ones a Lambda
     bf16 *dq, *dk, *dv;
     float *pq, *pk, *pv;                // fp32 [T, H, d] instead, where heads share a row
     float *dg, *dg_slot;                // [T, H], or sums over a chunk [slots, H]; neither: no decay gradient
@@ -360,6 +368,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     const uint32_t tb = *tmem_slot;
     const int len = c.len;
     const unsigned char *S = a.states + (slot * a.H + h) * (int64_t)(2 * L::SI), *G = a.adj + (slot * a.H + h) * (int64_t)(2 * L::SI);
+    const bool has_s = !c.first || a.init, has_l = !c.last || a.fin;  // zeros otherwise
     bool ok = true;
     auto wait = [&](uint64_t *bar) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, 0)); };
 
@@ -367,11 +376,15 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         if (lane == 0) {
             const int t = (int)c.tok0, hq = h / a.rq, hk = h / a.rk, hv = h / a.rv;
             // (the states first: their product with one another is taken while the tiles are on their way)
-            mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
-            bulk_g2s(sm + L::B0, S, L::SI, f_s);
-            if (decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
-            mbar_arrive_expect_tx(f_l, L::SI);
-            bulk_g2s(sm + L::B2, G, L::SI, f_l);
+            if (has_s) {
+                mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
+                bulk_g2s(sm + L::B0, S, L::SI, f_s);
+                if (decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
+            }
+            if (has_l) {
+                mbar_arrive_expect_tx(f_l, L::SI);
+                bulk_g2s(sm + L::B2, G, L::SI, f_l);
+            }
             mbar_arrive_expect_tx(f_qk, 2 * L::QT);
             for (int b = 0; b < DK / 64; ++b) {
                 tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, hq, t, f_qk);
@@ -382,8 +395,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
                 tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, hv, t, f_ov);
             }
-            bool more = decay && bar_wait(q_done, 0) && bar_wait(dot_done, 0);
-            if (decay && !more) ok = false;
+            bool more = decay && has_l;
+            if (more) ok = more = bar_wait(q_done, 0) && bar_wait(dot_done, 0);
             if (more) {
                 mbar_arrive_expect_tx(f_ll, L::SI);
                 bulk_g2s(sm + L::B0, G + L::SI, L::SI, f_ll);
@@ -391,8 +404,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             // copies land before the block ends, whatever the others have given up on
             ok = bar_wait(f_qk, 0) && ok;
             ok = bar_wait(f_ov, 0) && ok;
-            ok = bar_wait(f_s, 0) && ok;
-            ok = bar_wait(f_l, 0) && ok;
+            if (has_s) ok = bar_wait(f_s, 0) && ok;
+            if (has_l) ok = bar_wait(f_l, 0) && ok;
             if (more) ok = bar_wait(f_ll, 0) && ok;
         }
     } else if (warp == 1) {
@@ -409,20 +422,24 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 if (!(ok = bar_wait(f_ov, 0))) break;
                 mma_bf16_k(tb + T_Y, o, C, v, C, DV / 16, id_c, false);
                 mma_commit(xy_done);
-                if (!(ok = bar_wait(f_s, 0))) break;
-                mma_bf16_k(tb + T_Q, o, C, b0, DK, DV / 16, id_k, false);
-                if (decay) mma_bf16_k(tb + T_Q, o, C, b1, DK, DV / 16, id_k, true);
+                if (has_s) {
+                    if (!(ok = bar_wait(f_s, 0))) break;
+                    mma_bf16_k(tb + T_Q, o, C, b0, DK, DV / 16, id_k, false);
+                    if (decay) mma_bf16_k(tb + T_Q, o, C, b1, DK, DV / 16, id_k, true);
+                }
                 mma_commit(q_done);
-                if (!(ok = bar_wait(f_l, 0))) break;
-                mma_bf16_k(tb + T_K, v, C, b2, DK, DV / 16, id_k, false);
-                if (decay) {
-                    if (!(ok = bar_wait(f_ll, 0))) break;
-                    mma_bf16_k(tb + T_K, v, C, b0, DK, DV / 16, id_k, true);
+                if (has_l) {
+                    if (!(ok = bar_wait(f_l, 0))) break;
+                    mma_bf16_k(tb + T_K, v, C, b2, DK, DV / 16, id_k, false);
+                    if (decay) {
+                        if (!(ok = bar_wait(f_ll, 0))) break;
+                        mma_bf16_k(tb + T_K, v, C, b0, DK, DV / 16, id_k, true);
+                    }
                 }
                 mma_commit(k_done);
                 if (!(ok = bar_wait(a_ready, 0))) break;
                 fence_after_sync();
-                mma_bf16_kmn(tb + T_X, k, C, b2, DK * 128, DK / 16, id_v, false);
+                if (has_l) mma_bf16_kmn(tb + T_X, k, C, b2, DK * 128, DK / 16, id_v, false);
                 mma_commit(v_done);
                 if (!(ok = bar_wait(d_ready, 0))) break;
                 fence_after_sync();
@@ -452,8 +469,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 tma_prefetch_3d(&tm.o, 64 * b, g, t);
                 tma_prefetch_3d(&tm.v, 64 * b, g / a.rv, t);
             }
-            bulk_prefetch_l2(s, decay ? 2 * L::SI : L::SI);
-            bulk_prefetch_l2(l, decay ? 2 * L::SI : L::SI);
+            if (!x.first || a.init) bulk_prefetch_l2(s, decay ? 2 * L::SI : L::SI);
+            if (!x.last || a.fin) bulk_prefetch_l2(l, decay ? 2 * L::SI : L::SI);
         }
     } else if (warp >= 4) {
         constexpr int KW = DK / 4, VW = DV / 4;
@@ -464,7 +481,9 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             if (lane == 0) mbar_arrive(bar);
         };
         float dot = 0.f, qdq = 0.f, kdk = 0.f, w_row = 0.f, w_col = 0.f;
-        if (decay) {  // <S, Lambda>, both parts of each; Lambda's second one straight from memory
+        if (decay && !(has_s && has_l)) {
+            arrive(dot_done);
+        } else if (decay) {  // <S, Lambda>, both parts of each; Lambda's second one straight from memory
             constexpr int PER = L::SI / 16 / 512;  // 16-byte pieces of a thread
             uint4 l[PER];
 #pragma unroll
@@ -565,8 +584,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                     make_uint4(pd[4 * j], pd[4 * j + 1], pd[4 * j + 2], pd[4 * j + 3]);
             // ---- dQ's first part
             fence_after_sync();
-            float x[KW];
-            tmem_load<KW>(tl + T_Q + KW * part, x);
+            float x[KW] = {};
+            if (has_s) tmem_load<KW>(tl + T_Q + KW * part, x);
             const float e = a.scale * expf(ends(d, quarter - 1, -1) + rel);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= e;
@@ -586,8 +605,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         arrive(a_ready);
         if (ok) {  // ---- dK's first part
             fence_after_sync();
-            float x[KW];
-            tmem_load<KW>(tl + T_K + KW * part, x);
+            float x[KW] = {};
+            if (has_l) tmem_load<KW>(tl + T_K + KW * part, x);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= f;
             if (decay) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
@@ -596,8 +615,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         wait(v_done);  // ---- dV's first part; Lambda has been read
         if (ok) {
             fence_after_sync();
-            float x[VW];
-            tmem_load<VW>(tl + T_X + VW * part, x);
+            float x[VW] = {};
+            if (has_l) tmem_load<VW>(tl + T_X + VW * part, x);
 #pragma unroll
             for (int i = 0; i < VW; ++i) x[i] *= f;
             tmem_store<VW>(tl + T_X + VW * part, x);
@@ -762,6 +781,7 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     g.g = a->g, g.g_stride = gs, g.scale = a->scale, g.cu = a->cu_seqlens, g.T = a->T, g.N = a->N, g.H = a->H;
     g.rq = rq, g.rk = rk, g.rv = rv;
     g.states = (const unsigned char *)ws + L.states, g.adj = (const unsigned char *)ws + L.adj;
+    g.init = a->initial_state != nullptr, g.fin = a->grad_final_state != nullptr;
     g.dq = (bf16 *)a->grad_q, g.dk = (bf16 *)a->grad_k, g.dv = (bf16 *)a->grad_v;
     g.pq = rq > 1 ? (float *)(ws + L.pq) : nullptr;
     g.pk = rk > 1 ? (float *)(ws + L.pk) : nullptr;
