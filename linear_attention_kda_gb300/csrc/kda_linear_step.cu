@@ -7,7 +7,7 @@
 // (CW = 128: one 512-byte row per warp; CW = 32: whole 128-byte lines, four rows per warp).  A thread keeps its
 // rows in registers between the read and the write and forms its part of S^T q on the way; the parts of the rows
 // meet by shuffles and through shared memory.  Columns are independent, so a small batch splits every state over
-// dv / 32 CTAs (see launch).
+// dv / 32 CTAs (see launch_w).  256 sequences x 32 heads, bf16, dk = dv = 128: 160 us, 6.78 TB/s.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -106,8 +106,9 @@ static void launch(const kda_linear_step_args *a, cudaStream_t stream, int *err)
 
 template <int DK, int DV, typename T>
 static void launch_w(const kda_linear_step_args *a, cudaStream_t stream, int *err) {
-    // Few states: a state on one CTA leaves most SMs idle, so each is split into columns.
-    if (a->N * a->H <= 512) launch<DK, DV, 32, T>(a, stream, err);
+    // Fewer states than half of the SMs: each is split into columns.  Measured, dk = dv = 128, 32 heads, split and
+    // whole: 1 sequence 2.26 / 3.07 us, 4 sequences 3.69 / 3.08, 16 sequences 8.6 / 8.0, 32 sequences 15.0 / 13.7.
+    if (a->N * a->H <= 76) launch<DK, DV, 32, T>(a, stream, err);
     else launch<DK, DV, DV, T>(a, stream, err);
 }
 

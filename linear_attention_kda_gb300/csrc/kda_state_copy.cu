@@ -97,7 +97,8 @@ kda_status_t kda_launch_state_copy(const kda_state_copy_args *a, cudaStream_t st
     using namespace kda::slots;
     const int64_t blocks = (a->slot_bytes / 16 + NT - 1) / NT;
     if (blocks > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
-    // Pairs are split where the places of a slot make fewer than four blocks for an SM, W pairs to a block at least.
+    // Pairs are split where the places of a slot make fewer than four blocks for an SM, W pairs to a block at least:
+    // 150 slots of 32 KB moved take 4.1 us, one block for all pairs 25; of 256 KB 18 and 28, of 512 KB 50 either way.
     int64_t split = 608 / blocks, groups = (a->P + W - 1) / W;
     if (split > groups) split = groups;
     if (split < 1 || a->dst_slots > MAP) split = 1;
