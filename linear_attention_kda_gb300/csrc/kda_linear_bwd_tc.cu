@@ -60,7 +60,8 @@ template <int DK> struct states_smem {
 // products, three parts of the scaled rows (with two, 2^-16 of a term, the decay's gradient was off by 1e-5), are made
 // anew in tensor memory and added there in fp32: an accumulator that the chain itself ran through would lose a little at
 // every K-step, always in one direction (2.6e-6 of a slowly decaying state).  Under a chunk's products the state before
-// it goes to memory as images and the next chunk's rows are scaled and split.  Three stages of tiles: with two, a
+// it goes to memory as images and the next chunk's rows are scaled and split; a step takes 2.2 us at d = 128, 5 TB/s of
+// tiles and images between L2 and the SMs (the three products in accumulators of their own: the same).  Three stages of tiles: with two, a
 // chunk's tiles were asked for when the last product but one had ended, and their way (2000 cycles) and the scaling
 // (1200) made the step.
 template <int DK, int DV>
@@ -274,10 +275,12 @@ struct grads_args {
     const int32_t *cu;
     int64_t T, N;
     int H, rq, rk, rv;
+    int r;                              // heads of a block, all of one head of q and of one of k
     const unsigned char *states, *adj;  // images of S before and Lambda behind every chunk
     bool init, fin;                     // the first chunks have an S, the last ones a Lambda
     bf16 *dq, *dk, *dv;
-    float *pq, *pk, *pv;                // fp32 [T, H, d] instead, where heads share a row
+    float *pq, *pk, *pv;                // fp32 parts [T, H / r, dk] and [T, H, dv] instead, where others share the row
+    float4 *sums;                       // a block's sums over the heads so far of dQ and dK
     float *dg, *dg_slot;                // [T, H], or sums over a chunk [slots, H]; neither: no decay gradient
     int sms;
     int *err;
@@ -297,7 +300,7 @@ template <int DK, int DV> struct grads_smem {
     static constexpr int DEC = B2 + (SI > 9216 ? SI : 9216);
     static constexpr int RLO = DEC + (int)sizeof(decays);
     static constexpr int BAR = RLO + C * 4;
-    static constexpr int BYTES = BAR + 128;
+    static constexpr int BYTES = BAR + 160;
     static_assert(sizeof(grads_sums) <= DEC - B2, "sums lie over Lambda hi once its products are done");
 };
 static_assert(grads_smem<128, 128>::BYTES <= 227 * 1024, "shared memory");
@@ -333,6 +336,9 @@ __device__ __forceinline__ float row_dot(const float *x, const unsigned char *ti
 
 enum { T_X = 0, T_Y = 128, T_Q = 256, T_K = 384 };  // tensor memory: X, then dV; Y; dQ; dK
 
+// A block takes a chunk and r heads, one after the other.  Bound by latency: of a head's 12 to 14 us the ten products hold
+// the tensor pipe a fifth, tiles and images come (256 KB) and results leave (96 KB) while little is computed, since no
+// second block fits an SM; 4096 tokens of 32 heads, d = 128: 99 us, 0.44 of HBM.
 template <int DK, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_constant__ grads_args a) {
@@ -344,20 +350,22 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint64_t *f_qk = bars, *f_ov = bars + 1, *f_s = bars + 2, *f_l = bars + 3, *f_ll = bars + 4, *xy_done = bars + 5,
              *q_done = bars + 6, *k_done = bars + 7, *dot_done = bars + 8, *a_ready = bars + 9, *v_done = bars + 10,
-             *d_ready = bars + 11, *out_done = bars + 12, *dec_ready = bars + 13, *clean = bars + 14;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 15);
+             *d_ready = bars + 11, *out_done = bars + 12, *dec_ready = bars + 13, *clean = bars + 14, *t_free = bars + 15,
+             *end = bars + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = (int)(blockIdx.x % a.H);
-    const int64_t slot = blockIdx.x / a.H;
+    const int groups = a.H / a.r, h0 = (int)(blockIdx.x % groups) * a.r;
+    const int64_t slot = blockIdx.x / groups;
     const bool decay = a.dg || a.dg_slot;
     chunk c;
     if (!find_chunk<C>(a.cu, a.T, a.N, slot, &c)) {
-        if (a.dg_slot && tid == 0) a.dg_slot[slot * a.H + h] = 0.f;
+        if (a.dg_slot)
+            for (int i = tid; i < a.r; i += THREADS) a.dg_slot[slot * a.H + h0 + i] = 0.f;
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 15; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 ? 16 : 1);
+        for (int i = 0; i < 17; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 || i == 15 ? 16 : 1);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -367,46 +375,62 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     fence_after_sync();
     const uint32_t tb = *tmem_slot;
     const int len = c.len;
-    const unsigned char *S = a.states + (slot * a.H + h) * (int64_t)(2 * L::SI), *G = a.adj + (slot * a.H + h) * (int64_t)(2 * L::SI);
+    const unsigned char *S0 = a.states + (slot * a.H + h0) * (int64_t)(2 * L::SI), *G0 = a.adj + (slot * a.H + h0) * (int64_t)(2 * L::SI);
     const bool has_s = !c.first || a.init, has_l = !c.last || a.fin;  // zeros otherwise
     bool ok = true;
-    auto wait = [&](uint64_t *bar) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, 0)); };
+    // Head i of the block is the i-th phase of every barrier (f_qk has one, the others' tiles come with each head).
+    auto wait = [&](uint64_t *bar, uint32_t ph) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, ph)); };
 
     if (warp == 0) {
         if (lane == 0) {
-            const int t = (int)c.tok0, hq = h / a.rq, hk = h / a.rk, hv = h / a.rv;
-            // (the states first: their product with one another is taken while the tiles are on their way)
-            if (has_s) {
-                mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
-                bulk_g2s(sm + L::B0, S, L::SI, f_s);
-                if (decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
-            }
-            if (has_l) {
-                mbar_arrive_expect_tx(f_l, L::SI);
-                bulk_g2s(sm + L::B2, G, L::SI, f_l);
-            }
-            mbar_arrive_expect_tx(f_qk, 2 * L::QT);
-            for (int b = 0; b < DK / 64; ++b) {
-                tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, hq, t, f_qk);
-                tma_load_3d(sm + L::K + b * C * 128, &tm.k, 64 * b, hk, t, f_qk);
-            }
-            mbar_arrive_expect_tx(f_ov, 2 * L::VT);
-            for (int b = 0; b < DV / 64; ++b) {
-                tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
-                tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, hv, t, f_ov);
-            }
-            bool more = decay && has_l;
-            if (more) ok = more = bar_wait(q_done, 0) && bar_wait(dot_done, 0);
-            if (more) {
-                mbar_arrive_expect_tx(f_ll, L::SI);
-                bulk_g2s(sm + L::B0, G + L::SI, L::SI, f_ll);
+            const int t = (int)c.tok0, hq = h0 / a.rq, hk = h0 / a.rk;
+            int n_qk = 0, n_ov = 0, n_s = 0, n_l = 0, n_ll = 0;  // copies asked for
+            for (int i = 0; i < a.r; ++i) {
+                const int h = h0 + i, ph = i & 1;
+                const unsigned char *S = S0 + (int64_t)i * (2 * L::SI), *G = G0 + (int64_t)i * (2 * L::SI);
+                // (the states first: their product with one another is taken while the tiles are on their way)
+                if (has_s) {
+                    if (i && !(ok = bar_wait(k_done, ph ^ 1))) break;
+                    mbar_arrive_expect_tx(f_s, decay ? 2 * L::SI : L::SI);
+                    ++n_s;
+                    bulk_g2s(sm + L::B0, S, L::SI, f_s);
+                }
+                if (i && !(ok = bar_wait(out_done, ph ^ 1))) break;
+                if (has_s && decay) bulk_g2s(sm + L::B1, S + L::SI, L::SI, f_s);
+                auto lambda = [&] {
+                    mbar_arrive_expect_tx(f_l, L::SI);
+                    ++n_l;
+                    bulk_g2s(sm + L::B2, G, L::SI, f_l);
+                };
+                if (!i) {
+                    if (has_l) lambda();
+                    mbar_arrive_expect_tx(f_qk, 2 * L::QT);
+                    ++n_qk;
+                    for (int b = 0; b < DK / 64; ++b) {
+                        tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, hq, t, f_qk);
+                        tma_load_3d(sm + L::K + b * C * 128, &tm.k, 64 * b, hk, t, f_qk);
+                    }
+                }
+                mbar_arrive_expect_tx(f_ov, 2 * L::VT);
+                ++n_ov;
+                for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, h / a.rv, t, f_ov);
+                if (i && !(ok = bar_wait(end, ph ^ 1))) break;
+                for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
+                if (i && has_l) lambda();
+                if (decay && has_l) {
+                    if (!(ok = bar_wait(q_done, ph) && bar_wait(dot_done, ph))) break;
+                    mbar_arrive_expect_tx(f_ll, L::SI);
+                    ++n_ll;
+                    bulk_g2s(sm + L::B0, G + L::SI, L::SI, f_ll);
+                }
             }
             // copies land before the block ends, whatever the others have given up on
-            ok = bar_wait(f_qk, 0) && ok;
-            ok = bar_wait(f_ov, 0) && ok;
-            if (has_s) ok = bar_wait(f_s, 0) && ok;
-            if (has_l) ok = bar_wait(f_l, 0) && ok;
-            if (more) ok = bar_wait(f_ll, 0) && ok;
+            auto landed = [&](uint64_t *bar, int n) { ok = (n == 0 || bar_wait(bar, (n - 1) & 1)) && ok; };
+            landed(f_qk, n_qk);
+            landed(f_ov, n_ov);
+            landed(f_s, n_s);
+            landed(f_l, n_l);
+            landed(f_ll, n_ll);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -415,62 +439,73 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             const uint32_t id_c = idesc_bf16(128, 128), id_k = idesc_bf16(128, DK), id_v = idesc_bf16(128, DV, false, true),
                            id_dq = idesc_bf16(128, DK, false, true), id_dk = idesc_bf16(128, DK, true, true),
                            id_dv = idesc_bf16(128, DV, true, true);
-            do {
-                if (!(ok = bar_wait(f_qk, 0) && (len == C || bar_wait(clean, 0)))) break;
+            for (int i = 0; i < a.r; ++i) {
+                const int ph = i & 1;
+                // the first head's q and k are to be cleared, all heads' rows of dO and V
+                if (!(ok = i ? bar_wait(t_free, ph ^ 1) : bar_wait(f_qk, 0) && (len == C || bar_wait(clean, 0)))) break;
                 fence_after_sync();
                 mma_bf16_k(tb + T_X, q, C, k, C, DK / 16, id_c, false);
-                if (!(ok = bar_wait(f_ov, 0))) break;
+                if (!(ok = bar_wait(f_ov, ph) && (len == C || bar_wait(clean, ph)))) break;
                 mma_bf16_k(tb + T_Y, o, C, v, C, DV / 16, id_c, false);
                 mma_commit(xy_done);
                 if (has_s) {
-                    if (!(ok = bar_wait(f_s, 0))) break;
+                    if (!(ok = bar_wait(f_s, ph))) break;
                     mma_bf16_k(tb + T_Q, o, C, b0, DK, DV / 16, id_k, false);
                     if (decay) mma_bf16_k(tb + T_Q, o, C, b1, DK, DV / 16, id_k, true);
                 }
                 mma_commit(q_done);
                 if (has_l) {
-                    if (!(ok = bar_wait(f_l, 0))) break;
+                    if (!(ok = bar_wait(f_l, ph))) break;
                     mma_bf16_k(tb + T_K, v, C, b2, DK, DV / 16, id_k, false);
                     if (decay) {
-                        if (!(ok = bar_wait(f_ll, 0))) break;
+                        if (!(ok = bar_wait(f_ll, ph))) break;
                         mma_bf16_k(tb + T_K, v, C, b0, DK, DV / 16, id_k, true);
                     }
                 }
                 mma_commit(k_done);
-                if (!(ok = bar_wait(a_ready, 0))) break;
+                if (!(ok = bar_wait(a_ready, ph))) break;
                 fence_after_sync();
                 if (has_l) mma_bf16_kmn(tb + T_X, k, C, b2, DK * 128, DK / 16, id_v, false);
                 mma_commit(v_done);
-                if (!(ok = bar_wait(d_ready, 0))) break;
+                if (!(ok = bar_wait(d_ready, ph))) break;
                 fence_after_sync();
                 mma_bf16_kmn(tb + T_Q, b1, C, k, 16384, C / 16, id_dq, true);
                 mma_bf16_mnmn(tb + T_K, b1, 16384, q, 16384, C / 16, id_dk, true);
                 mma_bf16_mnmn(tb + T_X, v, 16384, o, 16384, C / 16, id_dv, true);
                 mma_commit(out_done);
-            } while (false);
+            }
         }
     } else if (warp == 2) {
-        const float4 g = load_log_decays(a.g ? a.g + c.tok0 * a.g_stride + h : nullptr, a.g_stride, len);
-        make_decays(g, d, rel_lo);
-        if (lane == 0) mbar_arrive(dec_ready);
+        for (int i = 0; i < a.r; ++i) {
+            const float4 g = load_log_decays(a.g ? a.g + c.tok0 * a.g_stride + h0 + i : nullptr, a.g_stride, len);
+            if (i) wait(end, (i - 1) & 1);
+            if (!ok) break;
+            make_decays(g, d, rel_lo);
+            if (lane == 0) mbar_arrive(dec_ready);
+        }
     } else if (warp == 3) {
-        // What the block that runs here next will load (blocks start in order, one on each SM): its way from memory
-        // is half of a block's time otherwise, since all blocks load at once and then compute at once.
-        const int64_t next = (int64_t)blockIdx.x + a.sms;
-        chunk x;
-        if (next < gridDim.x && find_chunk<C>(a.cu, a.T, a.N, next / a.H, &x) && lane == 0 && bar_wait(f_ov, 0)) {
-            const int t = (int)x.tok0, g = (int)(next % a.H);
-            const unsigned char *s = a.states + next * (int64_t)(2 * L::SI), *l = a.adj + next * (int64_t)(2 * L::SI);
-            for (int b = 0; b < DK / 64; ++b) {
-                tma_prefetch_3d(&tm.q, 64 * b, g / a.rq, t);
-                tma_prefetch_3d(&tm.k, 64 * b, g / a.rk, t);
-            }
+        // What the next head, or the block that runs here next, will load (blocks start in order, one on each SM): its
+        // way from memory is half of a block's time otherwise, since all blocks load at once and then compute at once.
+        for (int i = 0; i < a.r; ++i) {
+            const bool more = i + 1 < a.r;
+            const int64_t next = more ? blockIdx.x : (int64_t)blockIdx.x + a.sms, at = next / groups;
+            const int g = more ? h0 + i + 1 : (int)(next % groups) * a.r;
+            chunk x;
+            if (next >= gridDim.x || !find_chunk<C>(a.cu, a.T, a.N, at, &x)) break;
+            if (lane || !bar_wait(f_ov, i & 1)) continue;
+            const int t = (int)x.tok0;
+            const int64_t image = (at * a.H + g) * (int64_t)(2 * L::SI);
+            if (!more)
+                for (int b = 0; b < DK / 64; ++b) {
+                    tma_prefetch_3d(&tm.q, 64 * b, g / a.rq, t);
+                    tma_prefetch_3d(&tm.k, 64 * b, g / a.rk, t);
+                }
             for (int b = 0; b < DV / 64; ++b) {
                 tma_prefetch_3d(&tm.o, 64 * b, g, t);
                 tma_prefetch_3d(&tm.v, 64 * b, g / a.rv, t);
             }
-            if (!x.first || a.init) bulk_prefetch_l2(s, decay ? 2 * L::SI : L::SI);
-            if (!x.last || a.fin) bulk_prefetch_l2(l, decay ? 2 * L::SI : L::SI);
+            if (!x.first || a.init) bulk_prefetch_l2(a.states + image, decay ? 2 * L::SI : L::SI);
+            if (!x.last || a.fin) bulk_prefetch_l2(a.adj + image, decay ? 2 * L::SI : L::SI);
         }
     } else if (warp >= 4) {
         constexpr int KW = DK / 4, VW = DV / 4;
@@ -480,6 +515,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        for (int it = 0; it < a.r; ++it) {
+        const int h = h0 + it, ph = it & 1;
         float dot = 0.f, qdq = 0.f, kdk = 0.f, w_row = 0.f, w_col = 0.f;
         if (decay && !(has_s && has_l)) {
             arrive(dot_done);
@@ -487,9 +524,9 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             constexpr int PER = L::SI / 16 / 512;  // 16-byte pieces of a thread
             uint4 l[PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) l[i] = __ldg(reinterpret_cast<const uint4 *>(G + L::SI) + (tid - 128) + 512 * i);
-            wait(f_s);
-            wait(f_l);
+            for (int i = 0; i < PER; ++i) l[i] = __ldg(reinterpret_cast<const uint4 *>(G0 + it * (int64_t)(2 * L::SI) + L::SI) + (tid - 128) + 512 * i);
+            wait(f_s, ph);
+            wait(f_l, ph);
             if (ok) {
                 float acc = 0.f;
 #pragma unroll
@@ -512,11 +549,13 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             arrive(dot_done);
         }
         if (len < C) {  // rows behind the sequence are another's: zeros from here on
-            wait(f_qk);
-            wait(f_ov);
+            wait(f_qk, 0);
+            wait(f_ov, ph);
             if (ok && row >= len) {
-                clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
-                clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
+                if (!it) {
+                    clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
+                    clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
+                }
                 clear_chunks<DV / 32>(sm + L::O, row, DV / 32 * part);
                 clear_chunks<DV / 32>(sm + L::V, row, DV / 32 * part);
             }
@@ -524,8 +563,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             arrive(clean);
         }
         // ---- A and dA, columns 32 part .. of the chunk, and what the decay's gradient takes from their products
-        wait(dec_ready);
-        wait(xy_done);
+        wait(dec_ready, ph);
+        wait(xy_done, ph);
         uint32_t pa[16], pd[16];
         const float rel = d.rel[row], rlo = rel_lo[row];
         if (ok) fence_after_sync();
@@ -575,8 +614,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 #pragma unroll
             for (int e = 0; e < 16; ++e) pa[e] = pd[e] = 0;
         }
-        wait(q_done);  // S has been read: dA may lie where its second part was
-        if (decay) wait(dot_done);
+        wait(q_done, ph);  // S has been read: dA may lie where its second part was
+        if (decay) wait(dot_done, ph);
         if (ok) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -592,7 +631,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             if (decay) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
             tmem_store<KW>(tl + T_Q + KW * part, x);
         }
-        wait(k_done);  // the values have been read: A may lie over them
+        wait(k_done, ph);  // the values have been read: A may lie over them
         const float f = expf(ends(d, 3, quarter)) * d.w[row];
         if (ok) {
 #pragma unroll
@@ -612,7 +651,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             if (decay) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
             tmem_store<KW>(tl + T_K + KW * part, x);
         }
-        wait(v_done);  // ---- dV's first part; Lambda has been read
+        wait(v_done, ph);  // ---- dV's first part; Lambda has been read
         if (ok) {
             fence_after_sync();
             float x[VW] = {};
@@ -684,15 +723,32 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 }
             }
         }
-        wait(out_done);
+        wait(out_done, ph);
         if (ok) {
             fence_after_sync();
-            // whole chunks leave by TMA from where the tiles were; ragged ends, and fp32 parts of shared heads, row by row
-            auto put = [&](auto width, uint32_t t, unsigned char *stage, bf16 *out, float *shared, int D) {
+            // Whole chunks leave by TMA from where the tiles were; ragged ends, and fp32 parts of shared heads, row by
+            // row.  dQ and dK run over the block's heads by way of memory, a thread's own values.
+            auto put = [&](auto width, uint32_t t, unsigned char *stage, bf16 *out, float *shared, int D, int heads, int head,
+                           float4 *sum) {
                 constexpr int N = decltype(width)::value;
                 float x[N];
                 tmem_load<N>(tl + t + N * part, x);
-                const int64_t at = ((c.tok0 + row) * a.H + h) * D + N * part;
+                if (sum) {
+                    float4 *own = sum + (tid - 128);
+                    if (it) {
+#pragma unroll
+                        for (int i = 0; i < N; i += 4) {
+                            const float4 y = own[512 * (i / 4)];
+                            x[i] += y.x, x[i + 1] += y.y, x[i + 2] += y.z, x[i + 3] += y.w;
+                        }
+                    }
+                    if (it + 1 < a.r) {
+#pragma unroll
+                        for (int i = 0; i < N; i += 4) own[512 * (i / 4)] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        return;
+                    }
+                }
+                const int64_t at = ((c.tok0 + row) * heads + head) * D + N * part;
                 if (shared) {
                     if (row < len) {
 #pragma unroll
@@ -709,22 +765,31 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                     else if (row < len) *reinterpret_cast<uint4 *>(out + at + i) = u;
                 }
             };
-            put(std::integral_constant<int, KW>{}, T_Q, sm + L::Q, a.dq, a.pq, DK);
-            put(std::integral_constant<int, KW>{}, T_K, sm + L::K, a.dk, a.pk, DK);
-            put(std::integral_constant<int, VW>{}, T_X, sm + L::O, a.dv, a.pv, DV);
+            using kw = std::integral_constant<int, KW>;
+            float4 *sum = a.sums ? a.sums + blockIdx.x * (int64_t)(C * DK / 2) : nullptr;
+            put(kw{}, T_Q, sm + L::Q, a.dq, a.pq, DK, groups, h0 / a.r, sum);
+            put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / a.r, sum ? sum + C * DK / 4 : nullptr);
+            put(std::integral_constant<int, VW>{}, T_X, sm + L::O, a.dv, a.pv, DV, a.H, h, nullptr);
+            fence_before_sync();
             fence_proxy_async();
         }
+        arrive(t_free);
         bar_sync(1, 512);
-        if (warp == 4 && lane == 0 && ok && len == C) {
-            const int t = (int)c.tok0;
-            if (!a.pq)
-                for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dq, sm + L::Q + b * C * 128, 64 * b, h, t);
-            if (!a.pk)
-                for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dk, sm + L::K + b * C * 128, 64 * b, h, t);
-            if (!a.pv)
-                for (int b = 0; b < DV / 64; ++b) tma_store_3d(&tm.dv, sm + L::O + b * C * 128, 64 * b, h, t);
-            bulk_commit();
-            bulk_wait_read0();
+        if (warp == 4 && lane == 0) {
+            if (ok && len == C) {
+                const int t = (int)c.tok0;
+                const bool last = it + 1 == a.r;
+                if (!a.pq && last)
+                    for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dq, sm + L::Q + b * C * 128, 64 * b, h0 / a.rq, t);
+                if (!a.pk && last)
+                    for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dk, sm + L::K + b * C * 128, 64 * b, h0 / a.rk, t);
+                if (!a.pv)
+                    for (int b = 0; b < DV / 64; ++b) tma_store_3d(&tm.dv, sm + L::O + b * C * 128, 64 * b, h, t);
+                bulk_commit();
+                bulk_wait_read0();
+            }
+            mbar_arrive(end);
+        }
         }
     }
     if (!ok) atomicExch(fail, 1);
@@ -735,19 +800,33 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 }
 
 // ---------------------------------------------------------------------------------------------------- launches
+// Heads that a block takes in turn, a divisor of those that share a head of q and one of k: the sum over them then stays
+// with the block, which also loads q and k once.  As many as leave a block for every second SM: d = 128, 32 heads that
+// share 8, 16384 tokens: 4 heads to a block 600 us, one 860; 4096 tokens 173 and 237; 2048 tokens: 4 heads 90, two 125;
+// 1024 tokens of 32 heads that share one: 4 heads 65, two 78, 32 heads 365.
+static int heads_of_block(int64_t slots, int H, int rq, int rk) {
+    int r = 1;
+    for (int d = 2; d <= rq && d <= rk; ++d)
+        if (rq % d == 0 && rk % d == 0 && slots * (H / d) >= 76) r = d;
+    return r;
+}
+
 struct layout {
     int64_t slots;
-    size_t states, adj, pq, pk, pv, dg, total;
+    int r;
+    size_t states, adj, pq, pk, pv, sums, dg, total;
     layout(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv) {
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
         slots = chunk_slots(T, N, C);
-        const size_t each = up((size_t)slots * H * dk * dv * 4), rk = up((size_t)T * H * dk * 4), rv = up((size_t)T * H * dv * 4);
+        r = heads_of_block(slots, H, H / Hq, H / Hk);
+        const size_t each = up((size_t)slots * H * dk * dv * 4), rk = up((size_t)T * (H / r) * dk * 4), rv = up((size_t)T * H * dv * 4);
         size_t at = 0;
         states = at, at += each;
         adj = at, at += each;
-        pq = at, at += Hq != H ? rk : 0;
-        pk = at, at += Hk != H ? rk : 0;
+        pq = at, at += Hq * r != H ? rk : 0;
+        pk = at, at += Hk * r != H ? rk : 0;
         pv = at, at += Hv != H ? rv : 0;
+        sums = at, at += r > 1 ? up((size_t)slots * (H / r) * C * dk * 8) : 0;
         dg = at, at += up((size_t)slots * H * 4);
         total = at;
     }
@@ -783,8 +862,10 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     g.states = (const unsigned char *)ws + L.states, g.adj = (const unsigned char *)ws + L.adj;
     g.init = a->initial_state != nullptr, g.fin = a->grad_final_state != nullptr;
     g.dq = (bf16 *)a->grad_q, g.dk = (bf16 *)a->grad_k, g.dv = (bf16 *)a->grad_v;
-    g.pq = rq > 1 ? (float *)(ws + L.pq) : nullptr;
-    g.pk = rk > 1 ? (float *)(ws + L.pk) : nullptr;
+    g.r = L.r;
+    g.pq = rq > L.r ? (float *)(ws + L.pq) : nullptr;
+    g.pk = rk > L.r ? (float *)(ws + L.pk) : nullptr;
+    g.sums = L.r > 1 ? (float4 *)(ws + L.sums) : nullptr;
     g.pv = rv > 1 ? (float *)(ws + L.pv) : nullptr;
     if (a->grad_g) {
         if (a->g_per_token) g.dg = a->grad_g;
@@ -794,10 +875,10 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     int dev = 0;
     g.sms = 152;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&g.sms, cudaDevAttrMultiProcessorCount, dev);
-    linear_grads_tc_kernel<DK, DV><<<(unsigned)(L.slots * a->H), THREADS, smem2, stream>>>(gm, g);
+    linear_grads_tc_kernel<DK, DV><<<(unsigned)(L.slots * (a->H / L.r)), THREADS, smem2, stream>>>(gm, g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return kda_cuda_status(e);
-    return kda_linear_sum_parts(a, g.pq, g.pk, g.pv, g.dg_slot, L.slots, stream);
+    return kda_linear_sum_parts(a, g.pq, g.pk, a->H / L.r, g.pv, g.dg_slot, L.slots, stream);
 }
 
 }  // namespace bw

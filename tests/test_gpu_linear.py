@@ -113,6 +113,22 @@ def test_many_short_sequences(dtype):
     _check_bwd(d, _run_bwd(d))
 
 
+@pytest.mark.parametrize("N,Hq,Hk,Hv,dk,dv,decay,state", [(770, 2, 2, 8, 64, 64, "token", True),
+                                                         (770, 2, 1, 8, 64, 64, "head", False),
+                                                         (390, 4, 1, 8, 64, 128, "none", True),
+                                                         (390, 2, 4, 8, 128, 64, "token", False)])
+def test_backward_many_chunks_of_shared_heads(N, Hq, Hk, Hv, dk, dv, decay, state):
+    """Chunks enough that a block runs over several of the 8 heads that share a row of q and of k: all of them, or
+    some; ragged and whole chunks, sequences of one chunk and of several, with and without states at the ends."""
+    lens = [300, 256, 0, 128, 130] + [(5 * i) % 11 for i in range(N - 5)]
+    d = LU.batch(lens, 8, dk, dv, "bf16", N + Hq, Hq=Hq, Hk=Hk, Hv=Hv, decay=decay, state=state)
+    r = _run_bwd(d)
+    _check_bwd(d, r)
+    again = _run_bwd(d)
+    for n in r:
+        assert r[n] is None or torch.equal(r[n], again[n]), n
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_erasing_decays(dtype):
     """Log-decays of -inf, far below exp's range, and zero, alone and in runs."""
