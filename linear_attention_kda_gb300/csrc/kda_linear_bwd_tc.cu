@@ -339,7 +339,7 @@ enum { T_X = 0, T_Y = 128, T_Q = 256, T_K = 384 };  // tensor memory: X, then dV
 // A block takes a chunk and r heads, one after the other.  Bound by latency: of a head's 12 to 14 us the ten products hold
 // the tensor pipe a fifth, tiles and images come (256 KB) and results leave (96 KB) while little is computed, since no
 // second block fits an SM; 4096 tokens of 32 heads, d = 128: 99 us, 0.44 of HBM.
-template <int DK, int DV>
+template <int DK, int DV, bool ONE>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_constant__ grads_args a) {
     using L = grads_smem<DK, DV>;
@@ -355,13 +355,13 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = a.H / a.r, h0 = (int)(blockIdx.x % groups) * a.r;
-    const int64_t slot = blockIdx.x / groups;
+    const int per = ONE ? 1 : a.r, groups = a.H / per, h0 = (int)(blockIdx.x % groups) * per;
+    const int slot = (int)(blockIdx.x / groups);
     const bool decay = a.dg || a.dg_slot;
     chunk c;
     if (!find_chunk<C>(a.cu, a.T, a.N, slot, &c)) {
         if (a.dg_slot)
-            for (int i = tid; i < a.r; i += THREADS) a.dg_slot[slot * a.H + h0 + i] = 0.f;
+            for (int i = tid; i < per; i += THREADS) a.dg_slot[(int64_t)slot * a.H + h0 + i] = 0.f;
         return;
     }
     if (tid == 0) {
@@ -374,8 +374,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     __syncthreads();
     fence_after_sync();
     const uint32_t tb = *tmem_slot;
-    const int len = c.len;
-    const unsigned char *S0 = a.states + (slot * a.H + h0) * (int64_t)(2 * L::SI), *G0 = a.adj + (slot * a.H + h0) * (int64_t)(2 * L::SI);
+    const int len = c.len, tok0 = (int)c.tok0;
     const bool has_s = !c.first || a.init, has_l = !c.last || a.fin;  // zeros otherwise
     bool ok = true;
     // Head i of the block is the i-th phase of every barrier (f_qk has one, the others' tiles come with each head).
@@ -383,11 +382,12 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 
     if (warp == 0) {
         if (lane == 0) {
-            const int t = (int)c.tok0, hq = h0 / a.rq, hk = h0 / a.rk;
+            const int t = tok0, hq = h0 / a.rq, hk = h0 / a.rk;
             int n_qk = 0, n_ov = 0, n_s = 0, n_l = 0, n_ll = 0;  // copies asked for
-            for (int i = 0; i < a.r; ++i) {
+            for (int i = 0; i < per; ++i) {
                 const int h = h0 + i, ph = i & 1;
-                const unsigned char *S = S0 + (int64_t)i * (2 * L::SI), *G = G0 + (int64_t)i * (2 * L::SI);
+                const int64_t image = ((int64_t)slot * a.H + h) * (2 * L::SI);
+                const unsigned char *S = a.states + image, *G = a.adj + image;
                 // (the states first: their product with one another is taken while the tiles are on their way)
                 if (has_s) {
                     if (i && !(ok = bar_wait(k_done, ph ^ 1))) break;
@@ -439,7 +439,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             const uint32_t id_c = idesc_bf16(128, 128), id_k = idesc_bf16(128, DK), id_v = idesc_bf16(128, DV, false, true),
                            id_dq = idesc_bf16(128, DK, false, true), id_dk = idesc_bf16(128, DK, true, true),
                            id_dv = idesc_bf16(128, DV, true, true);
-            for (int i = 0; i < a.r; ++i) {
+            for (int i = 0; i < per; ++i) {
                 const int ph = i & 1;
                 // the first head's q and k are to be cleared, all heads' rows of dO and V
                 if (!(ok = i ? bar_wait(t_free, ph ^ 1) : bar_wait(f_qk, 0) && (len == C || bar_wait(clean, 0)))) break;
@@ -476,8 +476,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             }
         }
     } else if (warp == 2) {
-        for (int i = 0; i < a.r; ++i) {
-            const float4 g = load_log_decays(a.g ? a.g + c.tok0 * a.g_stride + h0 + i : nullptr, a.g_stride, len);
+        for (int i = 0; i < per; ++i) {
+            const float4 g = load_log_decays(a.g ? a.g + (int64_t)tok0 * a.g_stride + h0 + i : nullptr, a.g_stride, len);
             if (i) wait(end, (i - 1) & 1);
             if (!ok) break;
             make_decays(g, d, rel_lo);
@@ -486,10 +486,10 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     } else if (warp == 3) {
         // What the next head, or the block that runs here next, will load (blocks start in order, one on each SM): its
         // way from memory is half of a block's time otherwise, since all blocks load at once and then compute at once.
-        for (int i = 0; i < a.r; ++i) {
-            const bool more = i + 1 < a.r;
+        for (int i = 0; i < per; ++i) {
+            const bool more = i + 1 < per;
             const int64_t next = more ? blockIdx.x : (int64_t)blockIdx.x + a.sms, at = next / groups;
-            const int g = more ? h0 + i + 1 : (int)(next % groups) * a.r;
+            const int g = more ? h0 + i + 1 : (int)(next % groups) * per;
             chunk x;
             if (next >= gridDim.x || !find_chunk<C>(a.cu, a.T, a.N, at, &x)) break;
             if (lane || !bar_wait(f_ov, i & 1)) continue;
@@ -515,7 +515,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (int it = 0; it < a.r; ++it) {
+#pragma unroll 1
+        for (int it = 0; it < per; ++it) {
         const int h = h0 + it, ph = it & 1;
         float dot = 0.f, qdq = 0.f, kdk = 0.f, w_row = 0.f, w_col = 0.f;
         if (decay && !(has_s && has_l)) {
@@ -523,8 +524,9 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         } else if (decay) {  // <S, Lambda>, both parts of each; Lambda's second one straight from memory
             constexpr int PER = L::SI / 16 / 512;  // 16-byte pieces of a thread
             uint4 l[PER];
+            const unsigned char *G = a.adj + ((int64_t)slot * a.H + h) * (2 * L::SI);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) l[i] = __ldg(reinterpret_cast<const uint4 *>(G0 + it * (int64_t)(2 * L::SI) + L::SI) + (tid - 128) + 512 * i);
+            for (int i = 0; i < PER; ++i) l[i] = __ldg(reinterpret_cast<const uint4 *>(G + L::SI) + (tid - 128) + 512 * i);
             wait(f_s, ph);
             wait(f_l, ph);
             if (ok) {
@@ -712,14 +714,14 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                     before += kk[i];
                     const int r = 4 * lane + i;
                     if (r < len) {
-                        if (a.dg) a.dg[(c.tok0 + r) * a.H + h] = out[i];
+                        if (a.dg) a.dg[(int64_t)(tok0 + r) * a.H + h] = out[i];
                         total += out[i];
                     }
                 }
                 if (a.dg_slot) {
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-                    if (lane == 0) a.dg_slot[slot * a.H + h] = total;
+                    if (lane == 0) a.dg_slot[(int64_t)slot * a.H + h] = total;
                 }
             }
         }
@@ -742,13 +744,13 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                             x[i] += y.x, x[i + 1] += y.y, x[i + 2] += y.z, x[i + 3] += y.w;
                         }
                     }
-                    if (it + 1 < a.r) {
+                    if (it + 1 < per) {
 #pragma unroll
                         for (int i = 0; i < N; i += 4) own[512 * (i / 4)] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                         return;
                     }
                 }
-                const int64_t at = ((c.tok0 + row) * heads + head) * D + N * part;
+                const int64_t at = ((int64_t)(tok0 + row) * heads + head) * D + N * part;
                 if (shared) {
                     if (row < len) {
 #pragma unroll
@@ -766,9 +768,9 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 }
             };
             using kw = std::integral_constant<int, KW>;
-            float4 *sum = a.sums ? a.sums + blockIdx.x * (int64_t)(C * DK / 2) : nullptr;
-            put(kw{}, T_Q, sm + L::Q, a.dq, a.pq, DK, groups, h0 / a.r, sum);
-            put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / a.r, sum ? sum + C * DK / 4 : nullptr);
+            float4 *sum = !ONE ? a.sums + blockIdx.x * (int64_t)(C * DK / 2) : nullptr;
+            put(kw{}, T_Q, sm + L::Q, a.dq, a.pq, DK, groups, h0 / per, sum);
+            put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / per, sum ? sum + C * DK / 4 : nullptr);
             put(std::integral_constant<int, VW>{}, T_X, sm + L::O, a.dv, a.pv, DV, a.H, h, nullptr);
             fence_before_sync();
             fence_proxy_async();
@@ -777,8 +779,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         bar_sync(1, 512);
         if (warp == 4 && lane == 0) {
             if (ok && len == C) {
-                const int t = (int)c.tok0;
-                const bool last = it + 1 == a.r;
+                const int t = tok0;
+                const bool last = it + 1 == per;
                 if (!a.pq && last)
                     for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dq, sm + L::Q + b * C * 128, 64 * b, h0 / a.rq, t);
                 if (!a.pk && last)
@@ -848,10 +850,8 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     sm.d[1] = {gm.q, gm.o, rq, 1, a->grad_final_state, a->grad_initial_state, (unsigned char *)ws + L.adj, a->scale};
     const states_args s{a->g, gs, a->cu_seqlens, a->T, a->N, a->H, a->grad_g != nullptr, err};
     constexpr int smem1 = states_smem<DK>::BYTES, smem2 = grads_smem<DK, DV>::BYTES;
-    static std::atomic<uint64_t> states_allowed{0}, grads_allowed{0};
+    static std::atomic<uint64_t> states_allowed{0}, one_allowed{0}, some_allowed{0};
     cudaError_t e = allow_smem(linear_bwd_states_tc_kernel<DK, DV>, smem1, states_allowed);
-    if (e == cudaSuccess)
-        e = allow_smem(linear_grads_tc_kernel<DK, DV>, smem2, grads_allowed);
     if (e != cudaSuccess) return kda_cuda_status(e);
     linear_bwd_states_tc_kernel<DK, DV><<<dim3((unsigned)(a->N * a->H * (DV / W)), 2), THREADS, smem1, stream>>>(sm, s);
     e = cudaGetLastError();
@@ -875,7 +875,10 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     int dev = 0;
     g.sms = 152;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&g.sms, cudaDevAttrMultiProcessorCount, dev);
-    linear_grads_tc_kernel<DK, DV><<<(unsigned)(L.slots * (a->H / L.r)), THREADS, smem2, stream>>>(gm, g);
+    const auto grads = L.r == 1 ? linear_grads_tc_kernel<DK, DV, true> : linear_grads_tc_kernel<DK, DV, false>;
+    e = allow_smem(grads, smem2, L.r == 1 ? one_allowed : some_allowed);
+    if (e != cudaSuccess) return kda_cuda_status(e);
+    grads<<<(unsigned)(L.slots * (a->H / L.r)), THREADS, smem2, stream>>>(gm, g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return kda_cuda_status(e);
     return kda_linear_sum_parts(a, g.pq, g.pk, a->H / L.r, g.pv, g.dg_slot, L.slots, stream);
