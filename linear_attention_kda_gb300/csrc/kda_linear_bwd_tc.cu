@@ -49,21 +49,23 @@ constexpr int W = 64;      // value columns of a CTA
 
 template <int DK> struct states_smem {
     static constexpr int AT = C * DK * 2, BT = C * W * 2, STAGE = AT + BT, IMG = DK * W * 2;
-    static constexpr int MID = 3 * STAGE, LO = MID + AT;  // second and third parts of the scaled rows
-    static constexpr int DEC = LO + AT;
+    static constexpr int PARTS = 3 * STAGE;  // three parts of the scaled rows of the second tile
+    static constexpr int DEC = PARTS + 3 * BT;
     static constexpr int BAR = DEC + 3 * (int)sizeof(decays);
     static constexpr int BYTES = BAR + 256;
     static_assert(2 * IMG <= AT, "a chunk's images leave through the rows' tile of the chunk before");
 };
 
-// The chain of 64 value columns of one (sequence, head), S [dk rows][64 columns] in the threads' registers; a chunk's
-// products, three parts of the scaled rows (with two, 2^-16 of a term, the decay's gradient was off by 1e-5), are made
-// anew in tensor memory and added there in fp32: an accumulator that the chain itself ran through would lose a little at
-// every K-step, always in one direction (2.6e-6 of a slowly decaying state).  Under a chunk's products the state before
-// it goes to memory as images and the next chunk's rows are scaled and split; a step takes 2.2 us at d = 128, 5 TB/s of
-// tiles and images between L2 and the SMs (the three products in accumulators of their own: the same).  Three stages of tiles: with two, a
-// chunk's tiles were asked for when the last product but one had ended, and their way (2000 cycles) and the scaling
-// (1200) made the step.
+// The chain of 64 value columns of one (sequence, head), S [dk rows][64 columns] in the threads' registers.  A chunk's
+// factors go to the tile of 64 columns (half the values of the other), as three parts side by side (with two, 2^-16 of a
+// term, the decay's gradient was off by 1e-5), which take one product of 192 columns, made anew in tensor memory and
+// added in fp32 registers, smallest part first: an accumulator that the chain itself ran through would lose a little at
+// every K-step, always in one direction (2.6e-6 of a slowly decaying state).  Under a chunk's product the state before
+// it goes to memory as images and the next chunk's rows are scaled and split.  Three stages of tiles: with two, a
+// chunk's tiles were asked for when the last product but one had ended.
+// 4096 tokens of 32 heads, d = 128: 62 us, 1.9 us a step, 0.64 of HBM for the tiles and images (the factors on the other
+// tile and three products of 64 columns, in one accumulator or in three: 71 us).  Bound by what lies between two
+// products: sum, images, split, two fences.
 template <int DK, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __grid_constant__ states_args a) {
@@ -99,7 +101,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         for (int i = 0; i < 10; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 7 || i == 9 ? 1 : 16);
         *fail = 0;
     }
-    if (warp == 1) tmem_alloc(tmem_slot, 2 * W);
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
     fence_proxy_async();
     fence_before_sync();
     __syncthreads();
@@ -126,17 +128,13 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint32_t id = idesc_bf16(128, W, true, true);
+            const uint32_t id = idesc_bf16(128, 3 * W, true, true), parts = smem_u32(sm + L::PARTS);
             constexpr uint32_t ALBO = DK == 128 ? 16384 : 0;  // dk = 64: lanes 64 .. 127 repeat lanes 0 .. 63, unread
             for (int i = 0; i < np; ++i) {
-                const uint32_t st = smem_u32(sm + i % 3 * L::STAGE);
                 ok = bar_wait(s_ready, i & 1) && bar_wait(in + i % 3, (i / 3) & 1);
                 if (!ok) break;
                 fence_after_sync();
-                const uint32_t t = tb + (i & 1) * W;  // smallest terms first
-                mma_bf16_mnmn(t, smem_u32(sm + L::LO), ALBO, st + L::AT, 16384, C / 16, id, false);
-                mma_bf16_mnmn(t, smem_u32(sm + L::MID), ALBO, st + L::AT, 16384, C / 16, id, true);
-                mma_bf16_mnmn(t, st, ALBO, st + L::AT, 16384, C / 16, id, true);
+                mma_bf16_mnmn(tb + (i & 1) * 256, smem_u32(sm + i % 3 * L::STAGE), ALBO, parts, L::BT, C / 16, id, false);
                 mma_commit(u_done);
             }
         }
@@ -169,7 +167,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             }
         }
     } else {
-        constexpr int KC = DK / 32, CW = W / 4;
+        constexpr int KC = DK / 32, VC = W / 32, CW = W / 4;
         const int quarter = warp & 3, part = (warp - 4) >> 2, row = 32 * quarter + lane;
         const bool mine = row < DK;
         const uint32_t ts = tmem_addr(tb, 32 * quarter, CW * part);
@@ -178,7 +176,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        uint4 mid[KC], low[KC];  // of the next chunk's rows
+        uint4 hi[VC], mid[VC], low[VC];  // of the next chunk's rows
         auto split_rows = [&](int i) {
             const int len = len_of(i);
             unsigned char *st = sm + i % 3 * L::STAGE;
@@ -186,8 +184,9 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             if (!ok) return;
             const decays &d = dec[i % 3];
             const float f = back ? D.scale * expf(ends(d, quarter - 1, -1) + d.rel[row]) : expf(ends(d, 3, quarter)) * d.w[row];
-            split_chunks<KC>(st, row, KC * part, row < len ? f : 0.f, mid, low);
-            if (row >= len) clear_chunks<W / 32>(st + L::AT, row, W / 32 * part);
+            const float own = row < len ? f : 0.f;
+            split_chunks<VC>(st + L::AT, row, VC * part, own, hi, mid, low);
+            if (own == 0.f) clear_chunks<KC>(st, row, KC * part);  // (zeros times no number would be none)
         };
         float x[CW];
 #pragma unroll
@@ -198,10 +197,14 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         if (np > 0) split_rows(0);
         float all = 1.f;
         auto add_products = [&](int i) {  // of chunk i, behind the whole decay of it
-            float y[CW];
-            tmem_load<CW>(ts + (i & 1) * W, y);
+            float y[CW], z[CW];
+            tmem_load<CW>(ts + (i & 1) * 256 + 2 * W, y);
+            tmem_load<CW>(ts + (i & 1) * 256 + W, z);
 #pragma unroll
-            for (int c = 0; c < CW; ++c) x[c] = fmaf(x[c], all, y[c]);
+            for (int c = 0; c < CW; ++c) y[c] += z[c];
+            tmem_load<CW>(ts + (i & 1) * 256, z);
+#pragma unroll
+            for (int c = 0; c < CW; ++c) x[c] = fmaf(x[c], all, y[c] + z[c]);
         };
         for (int i = 0; i < nc; ++i) {
             if (i > 0) {
@@ -211,9 +214,11 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             }
             if (i < np) {
 #pragma unroll
-                for (int j = 0; j < KC; ++j) {
-                    *reinterpret_cast<uint4 *>(sm + L::MID + img_chunk_off(C, row, KC * part + j)) = mid[j];
-                    *reinterpret_cast<uint4 *>(sm + L::LO + img_chunk_off(C, row, KC * part + j)) = low[j];
+                for (int j = 0; j < VC; ++j) {
+                    unsigned char *p = sm + L::PARTS + img_chunk_off(C, row, VC * part + j);
+                    *reinterpret_cast<uint4 *>(p) = hi[j];
+                    *reinterpret_cast<uint4 *>(p + L::BT) = mid[j];
+                    *reinterpret_cast<uint4 *>(p + 2 * L::BT) = low[j];
                 }
                 fence_proxy_async();
                 arrive(s_ready);
@@ -228,7 +233,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 if (mine) {
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
-                        uint4 hi, lo;
+                        uint4 hi, lo;  // of the state
                         split2(x[c], x[c + 1], hi.x, lo.x);
                         split2(x[c + 2], x[c + 3], hi.y, lo.y);
                         split2(x[c + 4], x[c + 5], hi.z, lo.z);
@@ -260,7 +265,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     if (!ok) atomicExch(fail, 1);
     fence_before_sync();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tb, 2 * W);
+    if (warp == 1) tmem_dealloc(tb, 512);
     if (tid == 0 && *fail) set_error(a.err, KDA_ERR_DEVICE_TIMEOUT);
 }
 

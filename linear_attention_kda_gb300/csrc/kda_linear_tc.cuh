@@ -126,25 +126,24 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-// The same in three parts, which together are the fp32 product: hi in place, mid and lo left in registers.
+// A row's values multiplied by f, in three parts which together are the fp32 product.
 template <int N>
-__device__ __forceinline__ void split_chunks(unsigned char *tile, int row, int j0, float f, uint4 *mid, uint4 *lo) {
+__device__ __forceinline__ void split_chunks(const unsigned char *tile, int row, int j0, float f, uint4 *hi, uint4 *mid, uint4 *lo) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        unsigned char *at = tile + img_chunk_off(C, row, j0 + j);
-        uint4 u = *reinterpret_cast<const uint4 *>(at);
+        uint4 u = *reinterpret_cast<const uint4 *>(tile + img_chunk_off(C, row, j0 + j));
         if (f == 0.f) u = make_uint4(0, 0, 0, 0);  // erased, whatever the row holds
-        uint32_t *x = reinterpret_cast<uint32_t *>(&u), *m = reinterpret_cast<uint32_t *>(mid + j),
+        const uint32_t *x = reinterpret_cast<const uint32_t *>(&u);
+        uint32_t *h = reinterpret_cast<uint32_t *>(hi + j), *m = reinterpret_cast<uint32_t *>(mid + j),
                  *l = reinterpret_cast<uint32_t *>(lo + j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float a = bf_lo(x[i]) * f, b = bf_hi(x[i]) * f;
-            x[i] = pack_bf16(a, b);
-            a -= bf_lo(x[i]), b -= bf_hi(x[i]);
+            h[i] = pack_bf16(a, b);
+            a -= bf_lo(h[i]), b -= bf_hi(h[i]);
             m[i] = pack_bf16(a, b);
             l[i] = pack_bf16(a - bf_lo(m[i]), b - bf_hi(m[i]));
         }
-        *reinterpret_cast<uint4 *>(at) = u;
     }
 }
 template <int N>
