@@ -285,7 +285,6 @@ struct grads_args {
     bool init, fin;                     // the first chunks have an S, the last ones a Lambda
     bf16 *dq, *dk, *dv;
     float *pq, *pk, *pv;                // fp32 parts [T, H / r, dk] and [T, H, dv] instead, where others share the row
-    float4 *sums;                       // a block's sums over the heads so far of dQ and dK
     float *dg, *dg_slot;                // [T, H], or sums over a chunk [slots, H]; neither: no decay gradient
     int sms;
     int *err;
@@ -339,7 +338,8 @@ __device__ __forceinline__ float row_dot(const float *x, const unsigned char *ti
     return s;
 }
 
-enum { T_X = 0, T_Y = 128, T_Q = 256, T_K = 384 };  // tensor memory: X, then dV; Y; dQ; dK
+// tensor memory: X, then V Lambda^T; Y, then dO S^T, then dV; dQ and dK, summed over the block's heads
+enum { T_X = 0, T_Y = 128, T_Q = 256, T_K = 384 };
 
 // A block takes a chunk and r heads, one after the other.  Bound by latency: of a head's 12 to 14 us the ten products hold
 // the tensor pipe a fifth, tiles and images come (256 KB) and results leave (96 KB) while little is computed, since no
@@ -356,8 +356,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     uint64_t *f_qk = bars, *f_ov = bars + 1, *f_s = bars + 2, *f_l = bars + 3, *f_ll = bars + 4, *xy_done = bars + 5,
              *q_done = bars + 6, *k_done = bars + 7, *dot_done = bars + 8, *a_ready = bars + 9, *v_done = bars + 10,
              *d_ready = bars + 11, *out_done = bars + 12, *dec_ready = bars + 13, *clean = bars + 14, *t_free = bars + 15,
-             *end = bars + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
+             *end = bars + 16, *xy_read = bars + 17;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ONE ? 1 : a.r, groups = a.H / per, h0 = (int)(blockIdx.x % groups) * per;
@@ -370,7 +370,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 17; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 || i == 15 ? 16 : 1);
+        for (int i = 0; i < 18; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 || i == 15 || i == 17 ? 16 : 1);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -453,30 +453,32 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 if (!(ok = bar_wait(f_ov, ph) && (len == C || bar_wait(clean, ph)))) break;
                 mma_bf16_k(tb + T_Y, o, C, v, C, DV / 16, id_c, false);
                 mma_commit(xy_done);
+                if (!(ok = bar_wait(xy_read, ph))) break;
+                fence_after_sync();
                 if (has_s) {
                     if (!(ok = bar_wait(f_s, ph))) break;
-                    mma_bf16_k(tb + T_Q, o, C, b0, DK, DV / 16, id_k, false);
-                    if (decay) mma_bf16_k(tb + T_Q, o, C, b1, DK, DV / 16, id_k, true);
+                    mma_bf16_k(tb + T_Y, o, C, b0, DK, DV / 16, id_k, false);
+                    if (decay) mma_bf16_k(tb + T_Y, o, C, b1, DK, DV / 16, id_k, true);
                 }
                 mma_commit(q_done);
                 if (has_l) {
                     if (!(ok = bar_wait(f_l, ph))) break;
-                    mma_bf16_k(tb + T_K, v, C, b2, DK, DV / 16, id_k, false);
+                    mma_bf16_k(tb + T_X, v, C, b2, DK, DV / 16, id_k, false);
                     if (decay) {
                         if (!(ok = bar_wait(f_ll, ph))) break;
-                        mma_bf16_k(tb + T_K, v, C, b0, DK, DV / 16, id_k, true);
+                        mma_bf16_k(tb + T_X, v, C, b0, DK, DV / 16, id_k, true);
                     }
                 }
                 mma_commit(k_done);
                 if (!(ok = bar_wait(a_ready, ph))) break;
                 fence_after_sync();
-                if (has_l) mma_bf16_kmn(tb + T_X, k, C, b2, DK * 128, DK / 16, id_v, false);
+                if (has_l) mma_bf16_kmn(tb + T_Y, k, C, b2, DK * 128, DK / 16, id_v, false);
                 mma_commit(v_done);
                 if (!(ok = bar_wait(d_ready, ph))) break;
                 fence_after_sync();
                 mma_bf16_kmn(tb + T_Q, b1, C, k, 16384, C / 16, id_dq, true);
                 mma_bf16_mnmn(tb + T_K, b1, 16384, q, 16384, C / 16, id_dk, true);
-                mma_bf16_mnmn(tb + T_X, v, 16384, o, 16384, C / 16, id_dv, true);
+                mma_bf16_mnmn(tb + T_Y, v, 16384, o, 16384, C / 16, id_dv, true);
                 mma_commit(out_done);
             }
         }
@@ -523,6 +525,18 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 #pragma unroll 1
         for (int it = 0; it < per; ++it) {
         const int h = h0 + it, ph = it & 1;
+        auto add_store = [&](uint32_t t, float (&x)[KW]) {  // onto the sum over the heads before
+            if (it) {
+#pragma unroll
+                for (int i = 0; i < KW; i += 16) {
+                    float y[16];
+                    tmem_load<16>(t + i, y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[i + j] += y[j];
+                }
+            }
+            tmem_store<KW>(t, x);
+        };
         float dot = 0.f, qdq = 0.f, kdk = 0.f, w_row = 0.f, w_col = 0.f;
         if (decay && !(has_s && has_l)) {
             arrive(dot_done);
@@ -579,6 +593,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             float x[32], y[32];
             tmem_ld32(tl + T_X + 32 * part, x);
             tmem_ld32(tl + T_Y + 32 * part, y);
+            fence_before_sync();
+            arrive(xy_read);
             if (part < quarter) {  // all of it before the row's own block
                 const float u = a.scale * __expf(ends(d, quarter - 1, part) + rel);
 #pragma unroll
@@ -618,6 +634,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             }
             if (decay) w_col = transpose_sum(x);
         } else {
+            arrive(xy_read);
 #pragma unroll
             for (int e = 0; e < 16; ++e) pa[e] = pd[e] = 0;
         }
@@ -631,12 +648,12 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             // ---- dQ's first part
             fence_after_sync();
             float x[KW] = {};
-            if (has_s) tmem_load<KW>(tl + T_Q + KW * part, x);
+            if (has_s) tmem_load<KW>(tl + T_Y + KW * part, x);
             const float e = a.scale * expf(ends(d, quarter - 1, -1) + rel);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= e;
             if (decay) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
-            tmem_store<KW>(tl + T_Q + KW * part, x);
+            add_store(tl + T_Q + KW * part, x);
         }
         wait(k_done, ph);  // the values have been read: A may lie over them
         const float f = expf(ends(d, 3, quarter)) * d.w[row];
@@ -652,20 +669,20 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         if (ok) {  // ---- dK's first part
             fence_after_sync();
             float x[KW] = {};
-            if (has_l) tmem_load<KW>(tl + T_K + KW * part, x);
+            if (has_l) tmem_load<KW>(tl + T_X + KW * part, x);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= f;
             if (decay) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
-            tmem_store<KW>(tl + T_K + KW * part, x);
+            add_store(tl + T_K + KW * part, x);
         }
         wait(v_done, ph);  // ---- dV's first part; Lambda has been read
         if (ok) {
             fence_after_sync();
             float x[VW] = {};
-            if (has_l) tmem_load<VW>(tl + T_X + VW * part, x);
+            if (has_l) tmem_load<VW>(tl + T_Y + VW * part, x);
 #pragma unroll
             for (int i = 0; i < VW; ++i) x[i] *= f;
-            tmem_store<VW>(tl + T_X + VW * part, x);
+            tmem_store<VW>(tl + T_Y + VW * part, x);
             tmem_st_wait();
             fence_before_sync();
         }
@@ -733,28 +750,11 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         wait(out_done, ph);
         if (ok) {
             fence_after_sync();
-            // Whole chunks leave by TMA from where the tiles were; ragged ends, and fp32 parts of shared heads, row by
-            // row.  dQ and dK run over the block's heads by way of memory, a thread's own values.
-            auto put = [&](auto width, uint32_t t, unsigned char *stage, bf16 *out, float *shared, int D, int heads, int head,
-                           float4 *sum) {
+            // whole chunks leave by TMA from where the tiles were; ragged ends, and fp32 parts of shared heads, row by row
+            auto put = [&](auto width, uint32_t t, unsigned char *stage, bf16 *out, float *shared, int D, int heads, int head) {
                 constexpr int N = decltype(width)::value;
                 float x[N];
                 tmem_load<N>(tl + t + N * part, x);
-                if (sum) {
-                    float4 *own = sum + (tid - 128);
-                    if (it) {
-#pragma unroll
-                        for (int i = 0; i < N; i += 4) {
-                            const float4 y = own[512 * (i / 4)];
-                            x[i] += y.x, x[i + 1] += y.y, x[i + 2] += y.z, x[i + 3] += y.w;
-                        }
-                    }
-                    if (it + 1 < per) {
-#pragma unroll
-                        for (int i = 0; i < N; i += 4) own[512 * (i / 4)] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                        return;
-                    }
-                }
                 const int64_t at = ((int64_t)(tok0 + row) * heads + head) * D + N * part;
                 if (shared) {
                     if (row < len) {
@@ -772,11 +772,12 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                     else if (row < len) *reinterpret_cast<uint4 *>(out + at + i) = u;
                 }
             };
-            using kw = std::integral_constant<int, KW>;
-            float4 *sum = !ONE ? a.sums + blockIdx.x * (int64_t)(C * DK / 2) : nullptr;
-            put(kw{}, T_Q, sm + L::Q, a.dq, a.pq, DK, groups, h0 / per, sum);
-            put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / per, sum ? sum + C * DK / 4 : nullptr);
-            put(std::integral_constant<int, VW>{}, T_X, sm + L::O, a.dv, a.pv, DV, a.H, h, nullptr);
+            if (it + 1 == per) {
+                using kw = std::integral_constant<int, KW>;
+                put(kw{}, T_Q, sm + L::Q, a.dq, a.pq, DK, groups, h0 / per);
+                put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / per);
+            }
+            put(std::integral_constant<int, VW>{}, T_Y, sm + L::O, a.dv, a.pv, DV, a.H, h);
             fence_before_sync();
             fence_proxy_async();
         }
@@ -821,7 +822,7 @@ static int heads_of_block(int64_t slots, int H, int rq, int rk) {
 struct layout {
     int64_t slots;
     int r;
-    size_t states, adj, pq, pk, pv, sums, dg, total;
+    size_t states, adj, pq, pk, pv, dg, total;
     layout(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv) {
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
         slots = chunk_slots(T, N, C);
@@ -833,7 +834,6 @@ struct layout {
         pq = at, at += Hq * r != H ? rk : 0;
         pk = at, at += Hk * r != H ? rk : 0;
         pv = at, at += Hv != H ? rv : 0;
-        sums = at, at += r > 1 ? up((size_t)slots * (H / r) * C * dk * 8) : 0;
         dg = at, at += up((size_t)slots * H * 4);
         total = at;
     }
@@ -870,7 +870,6 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     g.r = L.r;
     g.pq = rq > L.r ? (float *)(ws + L.pq) : nullptr;
     g.pk = rk > L.r ? (float *)(ws + L.pk) : nullptr;
-    g.sums = L.r > 1 ? (float4 *)(ws + L.sums) : nullptr;
     g.pv = rv > 1 ? (float *)(ws + L.pv) : nullptr;
     if (a->grad_g) {
         if (a->g_per_token) g.dg = a->grad_g;
