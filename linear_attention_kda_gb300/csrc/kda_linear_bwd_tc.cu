@@ -42,6 +42,10 @@ struct states_args {
     const int32_t *cu;
     int64_t T, N;
     int H, lo;             // lo: the images' second parts are wanted
+    int64_t seg, slots;    // chunks of a segment and segment slots; 0: a chain is one piece
+    float *sums;           // [2 directions][slots, H][dk, dv] state behind a segment that begins with zeros (with the
+    float *decay;          // initial state, the chain's first one), and its whole decay [2][slots, H]
+    bool sum_pass;         // these are made, and nothing else
     int *err;
 };
 
@@ -66,7 +70,7 @@ template <int DK> struct states_smem {
 // 4096 tokens of 32 heads, d = 128: 62 us, 1.9 us a step, 0.64 of HBM for the tiles and images (the factors on the other
 // tile and three products of 64 columns, in one accumulator or in three: 71 us).  Bound by what lies between two
 // products: sum, images, split, two fences.
-template <int DK, int DV>
+template <int DK, int DV, bool CUT>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __grid_constant__ states_args a) {
     using L = states_smem<DK>;
@@ -82,19 +86,37 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     const bool back = blockIdx.y == 1;
     const states_dir &D = dirs.d[back];
     const int col = blockIdx.x % (DV / W);
-    const int64_t u = blockIdx.x / (DV / W), n = u / a.H;
-    const int h = (int)(u % a.H);
+    const int64_t piece = blockIdx.x / (DV / W), slot = piece / a.H;
+    const int h = (int)(piece % a.H);
+    int64_t n, index = 0;
     span sp;
-    if (!seq_span(a.cu, a.T, a.N, n, &sp)) {
-        if (tid == 0) set_error(a.err, KDA_ERR_BAD_SEQLENS);
-        return;
+    if (!CUT) {
+        n = longest_first(a.cu, a.N, slot, fail + 1);
+        if (!seq_span(a.cu, a.T, a.N, n, &sp)) {
+            if (tid == 0) set_error(a.err, KDA_ERR_BAD_SEQLENS);
+            return;
+        }
+    } else {
+        if (blockIdx.x == 0 && blockIdx.y == 0) check_seqlens(a.cu, a.T, a.N, a.err);
+        if (!find_slot(a.cu, a.T, a.N, a.seg * C, slot, &n, &index, &sp)) return;
     }
-    const int nc = (int)((sp.b - sp.a + C - 1) / C);
+    const int64_t u = n * a.H + h;
+    const int whole = (int)((sp.b - sp.a + C - 1) / C), c0 = CUT ? (int)(index * a.seg) : 0;  // the sequence's chunks, our first one
+    if (index > 0 && c0 >= whole) return;
+    const int nc = CUT && whole - c0 > a.seg ? (int)a.seg : whole - c0;
+    const bool left = c0 == 0, right = c0 + nc == whole, first = back ? right : left, last = back ? left : right;
+    float *fin = last ? D.fin : nullptr;
+    const bool sum_pass = CUT && a.sum_pass;
+    const int64_t sum_at = (back ? a.slots : 0) * a.H + piece;
+    if (sum_pass) {
+        if (last) return;
+        fin = a.sums + sum_at * (DK * DV);
+    }
     const int64_t slot0 = sp.a / C + n;
-    const int np = D.fin ? nc : nc - 1;  // chunks whose products are wanted
-    const int i0 = D.init ? 0 : 1;       // first chunk that has a state before it
-    if (np <= 0 && i0 >= nc && !D.fin) return;
-    auto chunk_of = [&](int i) { return back ? nc - 1 - i : i; };
+    const int np = fin ? nc : nc - 1;                                 // chunks whose products are wanted
+    const int i0 = sum_pass ? nc : first && !D.init ? 1 : 0;        // first chunk whose state before it is
+    if (np <= 0 && i0 >= nc && !fin) return;
+    auto chunk_of = [&](int i) { return c0 + (back ? nc - 1 - i : i); };
     auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
     auto len_of = [&](int i) { const int64_t r = sp.b - tok_of(i); return (int)(r < C ? r : C); };
     if (tid == 0) {
@@ -117,7 +139,9 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             for (; i < np; ++i) {
                 unsigned char *st = sm + i % 3 * L::STAGE;
                 const int t = (int)tok_of(i);
-                if (i >= 2 + i0) ok = bar_wait(stg_done, (i - i0) & 1);  // chunk i - 2's images have left by this stage
+                // chunk i - 2's images have left by this stage; where there are none, chunk i - 3 has been used
+                if (sum_pass ? i >= 3 : i >= 2 + i0)
+                    ok = sum_pass ? bar_wait(u_done, (i - 3) & 1) : bar_wait(stg_done, (i - i0) & 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(in + i % 3, L::STAGE);
                 for (int b = 0; b < DK / 64; ++b) tma_load_3d(st + b * C * 128, &D.a, 64 * b, ha, t, in + i % 3);
@@ -171,7 +195,8 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         const int quarter = warp & 3, part = (warp - 4) >> 2, row = 32 * quarter + lane;
         const bool mine = row < DK;
         const uint32_t ts = tmem_addr(tb, 32 * quarter, CW * part);
-        const int64_t at = u * (int64_t)(DK * DV) + (int64_t)row * DV + W * col + CW * part;
+        const int own = row * DV + W * col + CW * part;
+        const int64_t at = u * (int64_t)(DK * DV) + own;
         auto arrive = [&](uint64_t *bar) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
@@ -191,11 +216,26 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         float x[CW];
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
-            const float4 v = mine && D.init ? *reinterpret_cast<const float4 *>(D.init + at + c) : make_float4(0, 0, 0, 0);
+            const float4 v = mine && first && D.init ? *reinterpret_cast<const float4 *>(D.init + at + c) : make_float4(0, 0, 0, 0);
             x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
         }
+        if (!first && !sum_pass) {  // what the segments before this one leave, in the chain's order
+            const int before = back ? (whole + (int)a.seg - 1) / (int)a.seg - 1 - (int)index : (int)index;
+#pragma unroll 2
+            for (int j = before; j > 0; --j) {
+                const int64_t s = sum_at + (back ? j : -j) * (int64_t)a.H;
+                const float f = a.decay[s];
+                if (!mine) continue;
+#pragma unroll
+                for (int c = 0; c < CW; c += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(a.sums + s * (DK * DV) + own + c);
+                    x[c] = fmaf(x[c], f, v.x), x[c + 1] = fmaf(x[c + 1], f, v.y);
+                    x[c + 2] = fmaf(x[c + 2], f, v.z), x[c + 3] = fmaf(x[c + 3], f, v.w);
+                }
+            }
+        }
         if (np > 0) split_rows(0);
-        float all = 1.f;
+        float all = 1.f, decay = 1.f;
         auto add_products = [&](int i) {  // of chunk i, behind the whole decay of it
             float y[CW], z[CW];
             tmem_load<CW>(ts + (i & 1) * 256 + 2 * W, y);
@@ -227,6 +267,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             fence_before_sync();
             if (i < np) {
                 all = expf(dec[i % 3].hi[3]);
+                if (sum_pass) decay *= all;
                 arrive(dec_free + i % 3);
             }
             if (i >= i0) {  // the images, under the product, by way of the rows' tile of the chunk before
@@ -256,10 +297,12 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 add_products(nc - 1);
             }
         }
-        if (ok && D.fin && mine) {
+        if (ok && fin && mine) {
+            fin += sum_pass ? own : at;
 #pragma unroll
             for (int c = 0; c < CW; c += 4)
-                *reinterpret_cast<float4 *>(D.fin + at + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+                *reinterpret_cast<float4 *>(fin + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            if (sum_pass && col == 0 && row == 0 && part == 0) a.decay[sum_at] = decay;
         }
     }
     if (!ok) atomicExch(fail, 1);
@@ -819,10 +862,23 @@ static int heads_of_block(int64_t slots, int H, int rq, int rk) {
     return r;
 }
 
+// Chunks of a segment, 0 for chains in one piece.  A chain is one CTA's (two, dv = 128, and two directions), so few of them
+// leave the GPU idle.  Cut into `want` pieces each, they take a pass that sums the pieces and one that runs them, each
+// chunks / want steps long, and a launch more, which pays off where chunks - 2 chunks / want is above ten steps.
+// Measured, dv = 128 unless said, cut and whole: 8192 tokens of 2 heads, dv = 64, 71 / 117 us, 8 heads 121 / 168, 12 heads
+// 164 / 190; 65536 of 8 heads 773 / 1213; 2048 of 1 head 37 / 42; 1280 of 2 heads 33.5 / 32.3; four sequences of 2048
+// and 6 heads, dv = 64, 70.6 / 67.4.
+static int64_t chain_segment(int64_t T, int64_t N, int H, int dv) {
+    const int64_t want = 152 / (2 * N * H * (dv / W)), chunks = (T + C - 1) / C / N;  // of a sequence, on average
+    if (chunks * (want - 2) <= 10 * want) return 0;
+    const int64_t seg = (chunks + want - 1) / want;
+    return seg < 2 ? 2 : seg;
+}
+
 struct layout {
-    int64_t slots;
+    int64_t slots, seg, seg_slots;
     int r;
-    size_t states, adj, pq, pk, pv, dg, total;
+    size_t states, adj, pq, pk, pv, dg, sums, decay, total;
     layout(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv) {
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
         slots = chunk_slots(T, N, C);
@@ -835,6 +891,10 @@ struct layout {
         pk = at, at += Hk * r != H ? rk : 0;
         pv = at, at += Hv != H ? rv : 0;
         dg = at, at += up((size_t)slots * H * 4);
+        seg = chain_segment(T, N, H, dv);
+        seg_slots = seg ? T / (seg * C) + N : N;
+        sums = at, at += seg ? up((size_t)seg_slots * H * dk * dv * 8) : 0;
+        decay = at, at += seg ? up((size_t)seg_slots * H * 8) : 0;
         total = at;
     }
 };
@@ -853,14 +913,22 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     const int rq = a->H / a->Hq, rk = a->H / a->Hk, rv = a->H / a->Hv;
     sm.d[0] = {gm.k, gm.v, rk, rv, a->initial_state, nullptr, (unsigned char *)ws + L.states, 1.f};
     sm.d[1] = {gm.q, gm.o, rq, 1, a->grad_final_state, a->grad_initial_state, (unsigned char *)ws + L.adj, a->scale};
-    const states_args s{a->g, gs, a->cu_seqlens, a->T, a->N, a->H, a->grad_g != nullptr, err};
+    states_args s{};
+    s.g = a->g, s.g_stride = gs, s.cu = a->cu_seqlens, s.T = a->T, s.N = a->N, s.H = a->H, s.lo = a->grad_g != nullptr;
+    s.seg = L.seg, s.slots = L.seg_slots, s.err = err;
+    if (L.seg) s.sums = (float *)(ws + L.sums), s.decay = (float *)(ws + L.decay);
     constexpr int smem1 = states_smem<DK>::BYTES, smem2 = grads_smem<DK, DV>::BYTES;
-    static std::atomic<uint64_t> states_allowed{0}, one_allowed{0}, some_allowed{0};
-    cudaError_t e = allow_smem(linear_bwd_states_tc_kernel<DK, DV>, smem1, states_allowed);
+    static std::atomic<uint64_t> whole_allowed{0}, cut_allowed{0}, one_allowed{0}, some_allowed{0};
+    const auto chains = L.seg ? linear_bwd_states_tc_kernel<DK, DV, true> : linear_bwd_states_tc_kernel<DK, DV, false>;
+    cudaError_t e = allow_smem(chains, smem1, L.seg ? cut_allowed : whole_allowed);
     if (e != cudaSuccess) return kda_cuda_status(e);
-    linear_bwd_states_tc_kernel<DK, DV><<<dim3((unsigned)(a->N * a->H * (DV / W)), 2), THREADS, smem1, stream>>>(sm, s);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return kda_cuda_status(e);
+    const dim3 grid((unsigned)(L.seg_slots * a->H * (DV / W)), 2);
+    for (int pass = L.seg ? 0 : 1; pass < 2; ++pass) {
+        s.sum_pass = pass == 0;
+        chains<<<grid, THREADS, smem1, stream>>>(sm, s);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return kda_cuda_status(e);
+    }
     grads_args g{};
     g.g = a->g, g.g_stride = gs, g.scale = a->scale, g.cu = a->cu_seqlens, g.T = a->T, g.N = a->N, g.H = a->H;
     g.rq = rq, g.rk = rk, g.rv = rv;

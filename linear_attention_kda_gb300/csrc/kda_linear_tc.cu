@@ -67,28 +67,12 @@ struct work {
     bool last;                             // the sequence's last segment
     int h;
 };
-// Batches of up to this many sequences run longest first (32 sequences x 32 heads of 64 to 8192 tokens: 629 us, as they
-// come 665; 96 x 8: 569 and 672); ranks cost a scan of the lengths in every CTA, and longer batches even out by themselves.
-constexpr int SORTED = 128;
 __device__ __forceinline__ bool find_work(const chain_args &a, work *w, int *n_smem) {
     w->h = (int)(blockIdx.x % a.H);
     w->slot = blockIdx.x / a.H;
     span s;
     if (a.seg == 0) {
-        w->n = w->slot;
-        if (a.cu && a.N > 1 && a.N <= SORTED) {
-            if (threadIdx.x < a.N) {  // sequence t is the slot'th longest
-                const int t = threadIdx.x, len = a.cu[t + 1] - a.cu[t];
-                int rank = 0;
-                for (int m = 0; m < (int)a.N; ++m) {
-                    const int l = a.cu[m + 1] - a.cu[m];
-                    rank += l > len || (l == len && m < t);
-                }
-                if (rank == (int)w->slot) *n_smem = t;
-            }
-            __syncthreads();
-            w->n = *n_smem;
-        }
+        w->n = longest_first(a.cu, a.N, w->slot, n_smem);
         w->index = 0;
         if (!seq_span(a.cu, a.T, a.N, w->n, &s)) return false;
         w->tok0 = s.a;
@@ -106,14 +90,6 @@ __device__ __forceinline__ bool find_work(const chain_args &a, work *w, int *n_s
     w->end = s.b;
     return true;
 }
-// The first block looks all of cu_seqlens over.
-__device__ __forceinline__ void check_seqlens(const int32_t *cu, int64_t T, int64_t N, int *err) {
-    for (int64_t n = threadIdx.x; n < N; n += blockDim.x) {
-        span s;
-        if (!seq_span(cu, T, N, n, &s)) set_error(err, KDA_ERR_BAD_SEQLENS);
-    }
-}
-
 // ---------------------------------------------------------------------------------------------------- forward
 template <int DK, int DV> struct fwd_smem {
     static constexpr int TILE = C * (DK > DV ? DK : DV) * 2;

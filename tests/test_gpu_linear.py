@@ -240,6 +240,21 @@ def test_few_long_sequences(dk, dv, lens):
     _check_bwd(d, _run_bwd(d))
 
 
+@pytest.mark.parametrize("lens,Hq,dk,dv,decay,state", [([1, 9000, 130, 0], 2, 64, 64, "token", True),
+                                                     ([0, 129, 8000, 1], 1, 128, 64, "head", False),
+                                                     ([9100], 2, 64, 128, "none", True)])
+def test_gradients_of_few_chains_cut_into_segments(lens, Hq, dk, dv, decay, state):
+    """Segments of a sequence that others stand beside, with and without states at its ends."""
+    d = LU.batch(lens, 2, dk, dv, "bf16", len(lens), Hq=Hq, decay=decay, state=state)
+    r = _run_bwd(d)
+    _check_bwd(d, r)
+    again = _run_bwd(d, workspace=torch.full((kda.linear_chunk_bwd_workspace_size(
+        sum(lens), len(lens), 2, dk, dv, torch.bfloat16, Hq=Hq),), 255, dtype=torch.uint8, device="cuda"))
+    _no_error()
+    for n in r:
+        assert torch.equal(r[n], again[n]), n
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_split_prompt_equals_whole(dtype):
     """Two calls, the second from the first one's state, against the oracle of the whole."""
