@@ -117,10 +117,14 @@ size_t kda_linear_fwd_tc_bytes(int64_t T, int64_t N, int H, int dk, int dv);
 kda_status_t kda_launch_linear_fwd_tc(const kda_linear_args *a, void *ws, cudaStream_t stream, int *err);
 size_t kda_linear_bwd_tc_bytes(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv);
 kda_status_t kda_launch_linear_bwd_tc(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream, int *err);
-// fp32 parts, pq and pk [T, parts, dk], pv [T, H, dv], summed over those that share a row into grad_q, grad_k, grad_v (NULL:
-// nothing to sum), and a decay gradient's sums per chunk [slots, H] into grad_g
-kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const float *pq, const float *pk, int parts, const float *pv,
-                                  const float *dg_slot, int64_t slots, cudaStream_t stream);
+// fp32 parts of a gradient's rows, [T, parts, d] (NULL: none), summed over those that share a row into grad_q, grad_k and
+// grad_v, and a decay gradient's sums per chunk [slots, H] into grad_g
+struct kda_row_parts {
+    const float *part;
+    int parts;
+};
+kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const kda_row_parts &pq, const kda_row_parts &pk,
+                                  const kda_row_parts &pv, const float *dg_slot, int64_t slots, cudaStream_t stream);
 kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_linear_step(const kda_linear_step_args *a, cudaStream_t stream);

@@ -323,11 +323,11 @@ struct grads_args {
     const int32_t *cu;
     int64_t T, N;
     int H, rq, rk, rv;
-    int r;                              // heads of a block, all of one head of q and of one of k
+    int r;                              // heads of a block, all of one head of q and of k, or of k and of v
     const unsigned char *states, *adj;  // images of S before and Lambda behind every chunk
     bool init, fin;                     // the first chunks have an S, the last ones a Lambda
     bf16 *dq, *dk, *dv;
-    float *pq, *pk, *pv;                // fp32 parts [T, H / r, dk] and [T, H, dv] instead, where others share the row
+    float *pq, *pk, *pv;                // fp32 parts [T, H or H / r, d] instead, where other blocks share the row
     float *dg, *dg_slot;                // [T, H], or sums over a chunk [slots, H]; neither: no decay gradient
     int sms;
     int *err;
@@ -381,13 +381,16 @@ __device__ __forceinline__ float row_dot(const float *x, const unsigned char *ti
     return s;
 }
 
-// tensor memory: X, then V Lambda^T; Y, then dO S^T, then dV; dQ and dK, summed over the block's heads
-enum { T_X = 0, T_Y = 128, T_Q = 256, T_K = 384 };
+// What a block's heads share: there is one, q and k, or k and v (the heads' own gradients leave with each of them).
+enum { ONE = 0, QK = 1, KV = 2 };
+// tensor memory: X, then V Lambda^T, then (KV) K Lambda; Y, then dO S^T, then dV or (KV) dQ; dQ or (KV) dV, and dK, summed
+// over the block's heads
+enum { T_X = 0, T_Y = 128, T_S = 256, T_K = 384 };
 
 // A block takes a chunk and r heads, one after the other.  Bound by latency: of a head's 8 to 14 us the ten products hold
 // the tensor pipe a fifth, tiles and images come (256 KB) and results leave (96 KB) while little is computed, since no
 // second block fits an SM; 4096 tokens of 32 heads, d = 128: 90 us; 32768 of 32 heads that share 8, dv = 64: 471 us.
-template <int DK, int DV, bool ONE>
+template <int DK, int DV, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_constant__ grads_args a) {
     using L = grads_smem<DK, DV>;
@@ -403,7 +406,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int per = ONE ? 1 : a.r, groups = a.H / per, h0 = (int)(blockIdx.x % groups) * per;
+    const int per = MODE == ONE ? 1 : a.r, groups = a.H / per, h0 = (int)(blockIdx.x % groups) * per;
     const int slot = (int)(blockIdx.x / groups);
     const bool decay = a.dg || a.dg_slot;
     chunk c;
@@ -425,12 +428,12 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
     const int len = c.len, tok0 = (int)c.tok0;
     const bool has_s = !c.first || a.init, has_l = !c.last || a.fin;  // zeros otherwise
     bool ok = true;
-    // Head i of the block is the i-th phase of every barrier (f_qk has one, the others' tiles come with each head).
+    // Head i of the block is the i-th phase of every barrier, but that shared q and k come once.
     auto wait = [&](uint64_t *bar, uint32_t ph) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, ph)); };
 
     if (warp == 0) {
         if (lane == 0) {
-            const int t = tok0, hq = h0 / a.rq, hk = h0 / a.rk;
+            const int t = tok0;
             int n_qk = 0, n_ov = 0, n_s = 0, n_l = 0, n_ll = 0;  // copies asked for
             for (int i = 0; i < per; ++i) {
                 const int h = h0 + i, ph = i & 1;
@@ -450,20 +453,29 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                     ++n_l;
                     bulk_g2s(sm + L::B2, G, L::SI, f_l);
                 };
-                if (!i) {
-                    if (has_l) lambda();
-                    mbar_arrive_expect_tx(f_qk, 2 * L::QT);
+                if (!i && has_l) lambda();
+                if (!i || MODE == KV) {
+                    mbar_arrive_expect_tx(f_qk, i ? L::QT : 2 * L::QT);
                     ++n_qk;
                     for (int b = 0; b < DK / 64; ++b) {
-                        tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, hq, t, f_qk);
-                        tma_load_3d(sm + L::K + b * C * 128, &tm.k, 64 * b, hk, t, f_qk);
+                        tma_load_3d(sm + L::Q + b * C * 128, &tm.q, 64 * b, h / a.rq, t, f_qk);
+                        if (!i) tma_load_3d(sm + L::K + b * C * 128, &tm.k, 64 * b, h / a.rk, t, f_qk);
                     }
                 }
+                auto load_o = [&] {
+                    for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
+                };
+                auto load_v = [&] {
+                    for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, h / a.rv, t, f_ov);
+                };
                 mbar_arrive_expect_tx(f_ov, 2 * L::VT);
                 ++n_ov;
-                for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm + L::V + b * C * 128, &tm.v, 64 * b, h / a.rv, t, f_ov);
+                // (a head's own gradient leaves by way of dO's or V's place)
+                if (MODE == KV) load_o();
+                else load_v();
                 if (i && !(ok = bar_wait(end, ph ^ 1))) break;
-                for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm + L::O + b * C * 128, &tm.o, 64 * b, h, t, f_ov);
+                if (MODE == KV) load_v();
+                else load_o();
                 if (i && has_l) lambda();
                 if (decay && has_l) {
                     if (!(ok = bar_wait(q_done, ph) && bar_wait(dot_done, ph))) break;
@@ -489,8 +501,9 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                            id_dv = idesc_bf16(128, DV, true, true);
             for (int i = 0; i < per; ++i) {
                 const int ph = i & 1;
-                // the first head's q and k are to be cleared, all heads' rows of dO and V
-                if (!(ok = i ? bar_wait(t_free, ph ^ 1) : bar_wait(f_qk, 0) && (len == C || bar_wait(clean, 0)))) break;
+                // a ragged chunk's tiles are to be cleared first, those that come with this head
+                if (i && !(ok = bar_wait(t_free, ph ^ 1))) break;
+                if ((!i || MODE == KV) && !(ok = bar_wait(f_qk, ph) && (len == C || bar_wait(clean, ph)))) break;
                 fence_after_sync();
                 mma_bf16_k(tb + T_X, q, C, k, C, DK / 16, id_c, false);
                 if (!(ok = bar_wait(f_ov, ph) && (len == C || bar_wait(clean, ph)))) break;
@@ -515,13 +528,13 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 mma_commit(k_done);
                 if (!(ok = bar_wait(a_ready, ph))) break;
                 fence_after_sync();
-                if (has_l) mma_bf16_kmn(tb + T_Y, k, C, b2, DK * 128, DK / 16, id_v, false);
+                if (has_l) mma_bf16_kmn(tb + (MODE == KV ? T_X : T_Y), k, C, b2, DK * 128, DK / 16, id_v, false);
                 mma_commit(v_done);
                 if (!(ok = bar_wait(d_ready, ph))) break;
                 fence_after_sync();
-                mma_bf16_kmn(tb + T_Q, b1, C, k, 16384, C / 16, id_dq, true);
+                mma_bf16_kmn(tb + (MODE == KV ? T_Y : T_S), b1, C, k, 16384, C / 16, id_dq, true);
                 mma_bf16_mnmn(tb + T_K, b1, 16384, q, 16384, C / 16, id_dk, true);
-                mma_bf16_mnmn(tb + T_Y, v, 16384, o, 16384, C / 16, id_dv, true);
+                mma_bf16_mnmn(tb + (MODE == KV ? T_S : T_Y), v, 16384, o, 16384, C / 16, id_dv, true);
                 mma_commit(out_done);
             }
         }
@@ -545,10 +558,10 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             if (lane || !bar_wait(f_ov, i & 1)) continue;
             const int t = (int)x.tok0;
             const int64_t image = (at * a.H + g) * (int64_t)(2 * L::SI);
-            if (!more)
+            if (!more || MODE == KV)
                 for (int b = 0; b < DK / 64; ++b) {
                     tma_prefetch_3d(&tm.q, 64 * b, g / a.rq, t);
-                    tma_prefetch_3d(&tm.k, 64 * b, g / a.rk, t);
+                    if (!more) tma_prefetch_3d(&tm.k, 64 * b, g / a.rk, t);
                 }
             for (int b = 0; b < DV / 64; ++b) {
                 tma_prefetch_3d(&tm.o, 64 * b, g, t);
@@ -568,18 +581,21 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 #pragma unroll 1
         for (int it = 0; it < per; ++it) {
         const int h = h0 + it, ph = it & 1;
-        auto add_store = [&](uint32_t t, float (&x)[KW]) {  // onto the sum over the heads before
+        auto add_store = [&](auto width, uint32_t t, float *x) {  // onto the sum over the heads before
+            constexpr int N = decltype(width)::value;
             if (it) {
 #pragma unroll
-                for (int i = 0; i < KW; i += 16) {
+                for (int i = 0; i < N; i += 16) {
                     float y[16];
                     tmem_load<16>(t + i, y);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) x[i + j] += y[j];
                 }
             }
-            tmem_store<KW>(t, x);
+            tmem_store<N>(t, x);
         };
+        using kw = std::integral_constant<int, KW>;
+        using vw = std::integral_constant<int, VW>;
         float dot = 0.f, qdq = 0.f, kdk = 0.f, w_row = 0.f, w_col = 0.f;
         if (decay && !(has_s && has_l)) {
             arrive(dot_done);
@@ -613,13 +629,11 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             arrive(dot_done);
         }
         if (len < C) {  // rows behind the sequence are another's: zeros from here on
-            wait(f_qk, 0);
+            wait(f_qk, MODE == KV ? ph : 0);
             wait(f_ov, ph);
             if (ok && row >= len) {
-                if (!it) {
-                    clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
-                    clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
-                }
+                if (!it || MODE == KV) clear_chunks<DK / 32>(sm + L::Q, row, DK / 32 * part);
+                if (!it) clear_chunks<DK / 32>(sm + L::K, row, DK / 32 * part);
                 clear_chunks<DV / 32>(sm + L::O, row, DV / 32 * part);
                 clear_chunks<DV / 32>(sm + L::V, row, DV / 32 * part);
             }
@@ -696,7 +710,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= e;
             if (decay) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
-            add_store(tl + T_Q + KW * part, x);
+            if (MODE == KV) tmem_store<KW>(tl + T_Y + KW * part, x);
+            else add_store(kw{}, tl + T_S + KW * part, x);
         }
         wait(k_done, ph);  // the values have been read: A may lie over them
         const float f = expf(ends(d, 3, quarter)) * d.w[row];
@@ -708,24 +723,31 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             fence_proxy_async();
             fence_before_sync();
         }
-        arrive(a_ready);
+        if (MODE != KV) arrive(a_ready);
         if (ok) {  // ---- dK's first part
             fence_after_sync();
             float x[KW] = {};
             if (has_l) tmem_load<KW>(tl + T_X + KW * part, x);
+            if (MODE == KV) {  // K Lambda comes where this was
+                fence_before_sync();
+                arrive(a_ready);
+            }
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= f;
             if (decay) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
-            add_store(tl + T_K + KW * part, x);
+            add_store(kw{}, tl + T_K + KW * part, x);
+        } else if (MODE == KV) {
+            arrive(a_ready);
         }
         wait(v_done, ph);  // ---- dV's first part; Lambda has been read
         if (ok) {
             fence_after_sync();
             float x[VW] = {};
-            if (has_l) tmem_load<VW>(tl + T_Y + VW * part, x);
+            if (has_l) tmem_load<VW>(tl + (MODE == KV ? T_X : T_Y) + VW * part, x);
 #pragma unroll
             for (int i = 0; i < VW; ++i) x[i] *= f;
-            tmem_store<VW>(tl + T_Y + VW * part, x);
+            if (MODE == KV) add_store(vw{}, tl + T_S + VW * part, x);
+            else tmem_store<VW>(tl + T_Y + VW * part, x);
             tmem_st_wait();
             fence_before_sync();
         }
@@ -815,12 +837,15 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                     else if (row < len) *reinterpret_cast<uint4 *>(out + at + i) = u;
                 }
             };
-            if (it + 1 == per) {
-                using kw = std::integral_constant<int, KW>;
-                put(kw{}, T_Q, sm + L::Q, a.dq, a.pq, DK, groups, h0 / per);
-                put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / per);
+            const bool done = it + 1 == per;
+            if (MODE == KV) {
+                put(kw{}, T_Y, sm + L::V, a.dq, a.pq, DK, a.H, h);
+                if (done) put(vw{}, T_S, sm + L::O, a.dv, a.pv, DV, groups, h0 / per);
+            } else {
+                if (done) put(kw{}, T_S, sm + L::Q, a.dq, a.pq, DK, groups, h0 / per);
+                put(vw{}, T_Y, sm + L::O, a.dv, a.pv, DV, a.H, h);
             }
-            put(std::integral_constant<int, VW>{}, T_Y, sm + L::O, a.dv, a.pv, DV, a.H, h);
+            if (done) put(kw{}, T_K, sm + L::K, a.dk, a.pk, DK, groups, h0 / per);
             fence_before_sync();
             fence_proxy_async();
         }
@@ -830,12 +855,13 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             if (ok && len == C) {
                 const int t = tok0;
                 const bool last = it + 1 == per;
-                if (!a.pq && last)
-                    for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dq, sm + L::Q + b * C * 128, 64 * b, h0 / a.rq, t);
+                if (!a.pq && (MODE == KV || last))
+                    for (int b = 0; b < DK / 64; ++b)
+                        tma_store_3d(&tm.dq, sm + (MODE == KV ? L::V : L::Q) + b * C * 128, 64 * b, h / a.rq, t);
                 if (!a.pk && last)
-                    for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dk, sm + L::K + b * C * 128, 64 * b, h0 / a.rk, t);
-                if (!a.pv)
-                    for (int b = 0; b < DV / 64; ++b) tma_store_3d(&tm.dv, sm + L::O + b * C * 128, 64 * b, h, t);
+                    for (int b = 0; b < DK / 64; ++b) tma_store_3d(&tm.dk, sm + L::K + b * C * 128, 64 * b, h / a.rk, t);
+                if (!a.pv && (MODE != KV || last))
+                    for (int b = 0; b < DV / 64; ++b) tma_store_3d(&tm.dv, sm + L::O + b * C * 128, 64 * b, h / a.rv, t);
                 bulk_commit();
                 bulk_wait_read0();
             }
@@ -851,8 +877,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 }
 
 // ---------------------------------------------------------------------------------------------------- launches
-// Heads that a block takes in turn, a divisor of those that share a head of q and one of k: the sum over them then stays
-// with the block, which also loads q and k once.  As many as leave a block for every second SM: d = 128, 32 heads that
+// Heads that a block takes in turn, a divisor of those that share a head of q and one of k (or of k and v): the sum over
+// them then stays with the block, which also loads what they share once.  As many as leave a block for every second SM: d = 128, 32 heads that
 // share 8, 16384 tokens: 4 heads to a block 600 us, one 860; 4096 tokens 173 and 237; 2048 tokens: 4 heads 90, two 125;
 // 1024 tokens of 32 heads that share one: 4 heads 65, two 78, 32 heads 365.
 static int heads_of_block(int64_t slots, int H, int rq, int rk) {
@@ -877,19 +903,22 @@ static int64_t chain_segment(int64_t T, int64_t N, int H, int dv) {
 
 struct layout {
     int64_t slots, seg, seg_slots;
-    int r;
+    int r, mode, nq, nk, nv;  // heads of a block, what they share, parts of a row of dQ, dK and dV
     size_t states, adj, pq, pk, pv, dg, sums, decay, total;
     layout(int64_t T, int64_t N, int H, int Hq, int Hk, int Hv, int dk, int dv) {
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
         slots = chunk_slots(T, N, C);
-        r = heads_of_block(slots, H, H / Hq, H / Hk);
-        const size_t each = up((size_t)slots * H * dk * dv * 4), rk = up((size_t)T * (H / r) * dk * 4), rv = up((size_t)T * H * dv * 4);
+        mode = QK, r = heads_of_block(slots, H, H / Hq, H / Hk);
+        if (r == 1) mode = KV, r = heads_of_block(slots, H, H / Hk, H / Hv);
+        if (r == 1) mode = ONE;
+        nq = mode == KV ? H : H / r, nk = H / r, nv = mode == KV ? H / r : H;
+        const size_t each = up((size_t)slots * H * dk * dv * 4);
         size_t at = 0;
         states = at, at += each;
         adj = at, at += each;
-        pq = at, at += Hq * r != H ? rk : 0;
-        pk = at, at += Hk * r != H ? rk : 0;
-        pv = at, at += Hv != H ? rv : 0;
+        pq = at, at += nq != Hq ? up((size_t)T * nq * dk * 4) : 0;
+        pk = at, at += nk != Hk ? up((size_t)T * nk * dk * 4) : 0;
+        pv = at, at += nv != Hv ? up((size_t)T * nv * dv * 4) : 0;
         dg = at, at += up((size_t)slots * H * 4);
         seg = chain_segment(T, N, H, dv);
         seg_slots = seg ? T / (seg * C) + N : N;
@@ -918,7 +947,7 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     s.seg = L.seg, s.slots = L.seg_slots, s.err = err;
     if (L.seg) s.sums = (float *)(ws + L.sums), s.decay = (float *)(ws + L.decay);
     constexpr int smem1 = states_smem<DK>::BYTES, smem2 = grads_smem<DK, DV>::BYTES;
-    static std::atomic<uint64_t> whole_allowed{0}, cut_allowed{0}, one_allowed{0}, some_allowed{0};
+    static std::atomic<uint64_t> whole_allowed{0}, cut_allowed{0}, grads_allowed[3];
     const auto chains = L.seg ? linear_bwd_states_tc_kernel<DK, DV, true> : linear_bwd_states_tc_kernel<DK, DV, false>;
     cudaError_t e = allow_smem(chains, smem1, L.seg ? cut_allowed : whole_allowed);
     if (e != cudaSuccess) return kda_cuda_status(e);
@@ -936,9 +965,9 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     g.init = a->initial_state != nullptr, g.fin = a->grad_final_state != nullptr;
     g.dq = (bf16 *)a->grad_q, g.dk = (bf16 *)a->grad_k, g.dv = (bf16 *)a->grad_v;
     g.r = L.r;
-    g.pq = rq > L.r ? (float *)(ws + L.pq) : nullptr;
-    g.pk = rk > L.r ? (float *)(ws + L.pk) : nullptr;
-    g.pv = rv > 1 ? (float *)(ws + L.pv) : nullptr;
+    g.pq = L.nq != a->Hq ? (float *)(ws + L.pq) : nullptr;
+    g.pk = L.nk != a->Hk ? (float *)(ws + L.pk) : nullptr;
+    g.pv = L.nv != a->Hv ? (float *)(ws + L.pv) : nullptr;
     if (a->grad_g) {
         if (a->g_per_token) g.dg = a->grad_g;
         else g.dg_slot = (float *)(ws + L.dg);
@@ -947,13 +976,15 @@ static kda_status_t run(const kda_linear_bwd_args *a, char *ws, cudaStream_t str
     int dev = 0;
     g.sms = 152;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&g.sms, cudaDevAttrMultiProcessorCount, dev);
-    const auto grads = L.r == 1 ? linear_grads_tc_kernel<DK, DV, true> : linear_grads_tc_kernel<DK, DV, false>;
-    e = allow_smem(grads, smem2, L.r == 1 ? one_allowed : some_allowed);
+    const auto grads = L.mode == ONE  ? linear_grads_tc_kernel<DK, DV, ONE>
+                       : L.mode == QK ? linear_grads_tc_kernel<DK, DV, QK>
+                                      : linear_grads_tc_kernel<DK, DV, KV>;
+    e = allow_smem(grads, smem2, grads_allowed[L.mode]);
     if (e != cudaSuccess) return kda_cuda_status(e);
     grads<<<(unsigned)(L.slots * (a->H / L.r)), THREADS, smem2, stream>>>(gm, g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return kda_cuda_status(e);
-    return kda_linear_sum_parts(a, g.pq, g.pk, a->H / L.r, g.pv, g.dg_slot, L.slots, stream);
+    return kda_linear_sum_parts(a, {g.pq, L.nq}, {g.pk, L.nk}, {g.pv, L.nv}, g.dg_slot, L.slots, stream);
 }
 
 }  // namespace bw

@@ -557,20 +557,19 @@ struct bwd_layout {
 };
 
 template <typename T>
-static cudaError_t sum_heads(const float *part, int parts, void *out, const kda_linear_bwd_args *a, int Hx, int D,
-                             cudaStream_t stream) {
-    if (!part) return cudaSuccess;
+static cudaError_t sum_heads(const kda_row_parts &p, void *out, const kda_linear_bwd_args *a, int Hx, int D, cudaStream_t stream) {
+    if (!p.part) return cudaSuccess;
     const int64_t want = (a->T * Hx * D + NT - 1) / NT;
     linear_sum_heads_kernel<T><<<(unsigned)(want < 4096 ? want : 4096), NT, 0, stream>>>(
-        part, (T *)out, a->T, a->N, a->cu_seqlens, Hx, parts / Hx, D);
+        p.part, (T *)out, a->T, a->N, a->cu_seqlens, Hx, p.parts / Hx, D);
     return cudaGetLastError();
 }
 template <typename T>
-static cudaError_t sum_parts(const kda_linear_bwd_args *a, const float *pq, const float *pk, int parts, const float *pv,
+static cudaError_t sum_parts(const kda_linear_bwd_args *a, const kda_row_parts &pq, const kda_row_parts &pk, const kda_row_parts &pv,
                              const float *dg_slot, int64_t slots, cudaStream_t stream) {
-    cudaError_t e = sum_heads<T>(pq, parts, a->grad_q, a, a->Hq, a->dk, stream);
-    if (e == cudaSuccess) e = sum_heads<T>(pk, parts, a->grad_k, a, a->Hk, a->dk, stream);
-    if (e == cudaSuccess) e = sum_heads<T>(pv, a->H, a->grad_v, a, a->Hv, a->dv, stream);
+    cudaError_t e = sum_heads<T>(pq, a->grad_q, a, a->Hq, a->dk, stream);
+    if (e == cudaSuccess) e = sum_heads<T>(pk, a->grad_k, a, a->Hk, a->dk, stream);
+    if (e == cudaSuccess) e = sum_heads<T>(pv, a->grad_v, a, a->Hv, a->dv, stream);
     if (e == cudaSuccess && dg_slot) {
         linear_sum_decay_kernel<<<(unsigned)a->H, NT, 0, stream>>>(dg_slot, a->grad_g, slots, a->H);
         e = cudaGetLastError();
@@ -616,7 +615,7 @@ static cudaError_t bwd(const kda_linear_bwd_args *a, char *ws, cudaStream_t stre
     linear_grads_kernel<DK, DV><<<(unsigned)(slots * a->H), NT, smem, stream>>>(G);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return sum_parts<float>(a, G.pq, G.pk, a->H, G.pv, G.dg_slot, slots, stream);
+    return sum_parts<float>(a, {G.pq, a->H}, {G.pk, a->H}, {G.pv, a->H}, G.dg_slot, slots, stream);
 }
 
 static cudaError_t fwd_d(const kda_linear_args *a, char *ws, cudaStream_t s, int *err) {
@@ -656,8 +655,8 @@ kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaS
     return kda_cuda_status(kda::lin::bwd_d(a, (char *)ws, stream, err));
 }
 
-kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const float *pq, const float *pk, int parts, const float *pv,
-                                  const float *dg_slot, int64_t slots, cudaStream_t stream) {
-    return kda_cuda_status(a->dtype == KDA_BF16 ? kda::lin::sum_parts<kda::bf16>(a, pq, pk, parts, pv, dg_slot, slots, stream)
-                                                : kda::lin::sum_parts<float>(a, pq, pk, parts, pv, dg_slot, slots, stream));
+kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const kda_row_parts &pq, const kda_row_parts &pk,
+                                  const kda_row_parts &pv, const float *dg_slot, int64_t slots, cudaStream_t stream) {
+    return kda_cuda_status(a->dtype == KDA_BF16 ? kda::lin::sum_parts<kda::bf16>(a, pq, pk, pv, dg_slot, slots, stream)
+                                                : kda::lin::sum_parts<float>(a, pq, pk, pv, dg_slot, slots, stream));
 }

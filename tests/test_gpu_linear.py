@@ -116,10 +116,15 @@ def test_many_short_sequences(dtype):
 @pytest.mark.parametrize("N,Hq,Hk,Hv,dk,dv,decay,state", [(770, 2, 2, 8, 64, 64, "token", True),
                                                          (770, 2, 1, 8, 64, 64, "head", False),
                                                          (390, 4, 1, 8, 64, 128, "none", True),
-                                                         (390, 2, 4, 8, 128, 64, "token", False)])
+                                                         (390, 2, 4, 8, 128, 64, "token", False),
+                                                         (770, 8, 2, 2, 64, 64, "token", True),
+                                                         (770, 8, 1, 2, 64, 64, "head", False),
+                                                         (390, 8, 2, 1, 64, 128, "token", True),
+                                                         (390, 8, 4, 2, 128, 64, "none", False),
+                                                         (200, 8, 2, 2, 128, 128, "token", True)])
 def test_backward_many_chunks_of_shared_heads(N, Hq, Hk, Hv, dk, dv, decay, state):
-    """Chunks enough that a block runs over several of the 8 heads that share a row of q and of k: all of them, or
-    some; ragged and whole chunks, sequences of one chunk and of several, with and without states at the ends."""
+    """Chunks enough that a block runs over several of the 8 heads that share a row of q and k, or of k and v: all of
+    them, or some; ragged and whole chunks, sequences of one chunk and of several, with and without states at the ends."""
     lens = [300, 256, 0, 128, 130] + [(5 * i) % 11 for i in range(N - 5)]
     d = LU.batch(lens, 8, dk, dv, "bf16", N + Hq, Hq=Hq, Hk=Hk, Hv=Hv, decay=decay, state=state)
     r = _run_bwd(d)
