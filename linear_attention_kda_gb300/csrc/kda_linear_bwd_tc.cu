@@ -878,9 +878,10 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 
 // ---------------------------------------------------------------------------------------------------- launches
 // Heads that a block takes in turn, a divisor of those that share a head of q and one of k (or of k and v): the sum over
-// them then stays with the block, which also loads what they share once.  As many as leave a block for every second SM: d = 128, 32 heads that
-// share 8, 16384 tokens: 4 heads to a block 600 us, one 860; 4096 tokens 173 and 237; 2048 tokens: 4 heads 90, two 125;
-// 1024 tokens of 32 heads that share one: 4 heads 65, two 78, 32 heads 365.
+// them then stays with the block, which also loads what they share once.  As many as leave a block for every second SM.
+// Whole calls, 32 heads, d = 128, 4 heads to a block and one: 8 heads of q and k, 16384 tokens 525 / 827 us, 4096 tokens
+// 152 / 227, 2048 tokens 79 / 127 (a block for every SM, two heads: 116); 8 of k and v 542 / 844, 158 / 234, 83 / 131; one
+// head of q and k, 1024 tokens: 4 heads to a block 60, one or two 74, all 32 298.
 static int heads_of_block(int64_t slots, int H, int rq, int rk) {
     int r = 1;
     for (int d = 2; d <= rq && d <= rk; ++d)
