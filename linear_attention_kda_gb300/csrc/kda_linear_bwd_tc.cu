@@ -101,7 +101,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         if (!find_slot(a.cu, a.T, a.N, a.seg * C, slot, &n, &index, &sp)) return;
     }
     const int64_t u = n * a.H + h;
-    const int whole = (int)((sp.b - sp.a + C - 1) / C), c0 = CUT ? (int)(index * a.seg) : 0;  // the sequence's chunks, our first one
+    const int whole = (int)((sp.b - sp.a + C - 1) / C), c0 = CUT ? (int)(index * a.seg) : 0;  // chunks, first one here
     if (index > 0 && c0 >= whole) return;
     const int nc = CUT && whole - c0 > a.seg ? (int)a.seg : whole - c0;
     const bool left = c0 == 0, right = c0 + nc == whole, first = back ? right : left, last = back ? left : right;
@@ -113,8 +113,8 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
         fin = a.sums + sum_at * (DK * DV);
     }
     const int64_t slot0 = sp.a / C + n;
-    const int np = fin ? nc : nc - 1;                                 // chunks whose products are wanted
-    const int i0 = sum_pass ? nc : first && !D.init ? 1 : 0;        // first chunk whose state before it is
+    const int np = fin ? nc : nc - 1;                         // chunks whose products are wanted
+    const int i0 = sum_pass ? nc : first && !D.init ? 1 : 0;  // first chunk whose state before it is
     if (np <= 0 && i0 >= nc && !fin) return;
     auto chunk_of = [&](int i) { return c0 + (back ? nc - 1 - i : i); };
     auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
@@ -209,14 +209,15 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             if (!ok) return;
             const decays &d = dec[i % 3];
             const float f = back ? D.scale * expf(ends(d, quarter - 1, -1) + d.rel[row]) : expf(ends(d, 3, quarter)) * d.w[row];
-            const float own = row < len ? f : 0.f;
-            split_chunks<VC>(st + L::AT, row, VC * part, own, hi, mid, low);
-            if (own == 0.f) clear_chunks<KC>(st, row, KC * part);  // (zeros times no number would be none)
+            const float m = row < len ? f : 0.f;
+            split_chunks<VC>(st + L::AT, row, VC * part, m, hi, mid, low);
+            if (m == 0.f) clear_chunks<KC>(st, row, KC * part);  // (zeros times no number would be none)
         };
         float x[CW];
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
-            const float4 v = mine && first && D.init ? *reinterpret_cast<const float4 *>(D.init + at + c) : make_float4(0, 0, 0, 0);
+            float4 v = make_float4(0, 0, 0, 0);
+            if (mine && first && D.init) v = *reinterpret_cast<const float4 *>(D.init + at + c);
             x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
         }
         if (!first && !sum_pass) {  // what the segments before this one leave, in the chain's order
@@ -271,6 +272,9 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 arrive(dec_free + i % 3);
             }
             if (i >= i0) {  // the images, under the product, by way of the rows' tile of the chunk before
+                // (those before them have left, so that stg_full is never two phases ahead of who waits for it)
+                if (i > i0) wait(stg_done, (i - 1 - i0) & 1);
+                if (!ok) break;
                 if (mine) {
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
@@ -416,7 +420,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 18; ++i) mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 || i == 15 || i == 17 ? 16 : 1);
+        for (int i = 0; i < 18; ++i)
+            mbar_init(bars + i, i == 8 || i == 9 || i == 11 || i == 14 || i == 15 || i == 17 ? 16 : i == 16 ? 2 : 1);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -553,9 +558,11 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             const bool more = i + 1 < per;
             const int64_t next = more ? blockIdx.x : (int64_t)blockIdx.x + a.sms, at = next / groups;
             const int g = more ? h0 + i + 1 : (int)(next % groups) * per;
-            chunk x;
-            if (next >= gridDim.x || !find_chunk<C>(a.cu, a.T, a.N, at, &x)) break;
-            if (lane || !bar_wait(f_ov, i & 1)) continue;
+            chunk x = c;
+            if (!more && (next >= gridDim.x || !find_chunk<C>(a.cu, a.T, a.N, at, &x))) break;
+            if (lane) continue;
+            ok = bar_wait(f_ov, i & 1) && ok;
+            if (more) mbar_arrive(end);  // (f_ov is never two phases ahead of this wait)
             const int t = (int)x.tok0;
             const int64_t image = (at * a.H + g) * (int64_t)(2 * L::SI);
             if (!more || MODE == KV)
