@@ -125,8 +125,8 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *free_ = full + L::SLOTS, *dec_ready = free_ + L::SLOTS,
              *dec_free = dec_ready + 2, *x_done = dec_free + 2, *p_ready = x_done + 1, *s_ready = p_ready + 1,
              *k_ready = s_ready + 1, *u_done = k_ready + 1, *o_done = u_done + 1, *o_read = o_done + 1, *o_staged = o_read + 1, *o_stored = o_staged + 1,
-             *d_done = o_stored + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_done + 1);
+             *d_done = o_stored + 1, *x_read = d_done + 1;  // x_read: one for each lane quarter
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_read + 4);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -153,6 +153,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
         mbar_init(o_staged, 16);
         mbar_init(o_stored, 1);
         mbar_init(d_done, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(x_read + i, 4);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -395,7 +396,11 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                     for (int c = 0; c < 16; ++c) p[c] = 0;
                 }
                 fence_before_sync();
-                bar_sync(1 + quarter, 128);  // the quarter's X is read: P may lie over it
+                // The quarter's X is read: P may lie over it.  (A wait with a limit, as all others here: at a hardware
+                // barrier a warp would stay for good where another one's wait has run out before it.)
+                arrive(x_read + quarter);
+                wait(x_read + quarter, i & 1);
+                if (!ok) break;
                 fence_after_sync();
                 tmem_st16u(tx + 16 * part, p);
                 wait(d_done, i & 1);

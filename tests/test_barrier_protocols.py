@@ -1,0 +1,100 @@
+"""Every order of events of the linear-attention kernels' warps, small models on the CPU: no wait on a barrier's parity
+can miss the phase that it is for, and a wait that runs out leaves nobody at a barrier without a limit.
+
+A role is a list of steps: ("wait", barrier, phase), ("arrive", barrier), ("sync", barrier) for a hardware barrier
+that all of its members reach.  A parity wait passes where the barrier has completed an odd number of phases more than
+`phase` before it, which is what the hardware tells: two phases ahead looks like none.  The kind of the prefill's meeting
+is read from its source."""
+import os
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "linear_attention_kda_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def explore(roles, counts, can_time_out):
+    """First state, as positions in the roles, from which nothing moves though a role has not ended; None if there is none."""
+    arrivals = [{} for _ in roles]
+    for r, prog in enumerate(roles):
+        done = {}
+        for i, step in enumerate(prog):
+            arrivals[r][i] = dict(done)
+            if step[0] == "arrive":
+                done[step[1]] = done.get(step[1], 0) + 1
+        arrivals[r][len(prog)] = dict(done)
+    members = {s[1]: [r for r, p in enumerate(roles) if any(x[0] == "sync" and x[1] == s[1] for x in p)] for p in roles for s in p if s[0] == "sync"}
+    # what a role has arrived at depends on where it is, and, once it has given up, on where it did so
+    start = tuple((0, None) for _ in roles)
+    seen, todo = {start}, [start]
+    while todo:
+        state = todo.pop()
+
+        def completed(bar):
+            n = 0
+            for r, (at, gave_up) in enumerate(state):
+                n += arrivals[r][gave_up if gave_up is not None else at].get(bar, 0)
+            return n // counts[bar]
+
+        def step_of(r):
+            at = state[r][0]
+            return roles[r][at] if at < len(roles[r]) else None
+
+        after = []
+        for r, (at, gave_up) in enumerate(state):
+            step = step_of(r)
+            if step is None:
+                continue
+            nxt = lambda at, g: after.append(state[:r] + ((at, g),) + state[r + 1:])  # noqa: B023, E731
+            if step[0] == "arrive":
+                nxt(at + 1, gave_up)
+            elif step[0] == "wait":
+                if (completed(step[1]) - step[2]) % 2 == 1:
+                    nxt(at + 1, gave_up)
+                elif can_time_out:  # leaves for the steps behind ("end",)
+                    nxt(roles[r].index(("end",)), at)
+            elif step[0] == "end":
+                nxt(at + 1, gave_up)
+        for bar, who in members.items():
+            if all(step_of(r) == ("sync", bar) for r in who):
+                after.append(tuple((at + 1, g) if r in who else (at, g) for r, (at, g) in enumerate(state)))
+        if not after and any(at < len(roles[r]) for r, (at, _) in enumerate(state)):
+            return state
+        for s in after:
+            if s not in seen:
+                seen.add(s)
+                todo.append(s)
+    return None
+
+
+# ------------------------------------------------------------------ prefill: the meeting of a quarter's warps
+def meeting(nc, hardware):
+    """Two of the warps that read a quarter of X before one of them writes P over it, and the warp that issues products."""
+    work = []
+    for i in range(nc):
+        work += [("wait", "x_done", i), ("arrive", "k_ready")]
+        work += [("sync", "quarter")] if hardware else [("arrive", "x_read"), ("wait", "x_read", i)]
+        work += [("wait", "d_done", i), ("arrive", "p_ready")]
+    mma = [("arrive", "x_done")]
+    for i in range(nc):
+        mma += [("arrive", "d_done"), ("wait", "k_ready", i), ("wait", "p_ready", i)]
+        if i + 1 < nc:
+            mma.append(("arrive", "x_done"))
+    end = [("end",), ("sync", "block")]
+    return [work + end, work + end, mma + end], {"x_done": 1, "d_done": 1, "k_ready": 2, "p_ready": 2, "x_read": 2}
+
+
+@pytest.mark.parametrize("can_time_out", [False, True])
+@pytest.mark.parametrize("nc", [1, 3])
+def test_prefill_ends_whatever_gives_up(nc, can_time_out):
+    hardware = "bar_sync(" in source("kda_linear_tc.cu")
+    assert explore(*meeting(nc, hardware), can_time_out) is None
+
+
+def test_a_hardware_barrier_behind_a_wait_would_not_end():
+    assert explore(*meeting(1, True), False) is None
+    assert explore(*meeting(1, True), True) is not None
