@@ -50,6 +50,10 @@ struct states_args {
 };
 
 constexpr int W = 64;      // value columns of a CTA
+// Barriers that the chunks' images take in turn when they have left.  The loader waits for image i - 2 of the tiles i that
+// it is to fetch, and image i - 1 may have left by then: on one barrier for all images that looks as if neither had, and
+// image i needs the very tile.
+constexpr int IMAGE_BARS = 3;
 
 template <int DK> struct states_smem {
     static constexpr int AT = C * DK * 2, BT = C * W * 2, STAGE = AT + BT, IMG = DK * W * 2;
@@ -80,7 +84,8 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     // in: a chunk's tiles and its decays
     uint64_t *in = bars, *dec_free = bars + 3, *s_ready = bars + 6, *u_done = bars + 7, *stg_full = bars + 8,
              *stg_done = bars + 9;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 10);
+    constexpr int BARS = 9 + IMAGE_BARS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + BARS);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool back = blockIdx.y == 1;
@@ -120,7 +125,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     auto tok_of = [&](int i) { return sp.a + (int64_t)chunk_of(i) * C; };
     auto len_of = [&](int i) { const int64_t r = sp.b - tok_of(i); return (int)(r < C ? r : C); };
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 7 || i == 9 ? 1 : 16);
+        for (int i = 0; i < BARS; ++i) mbar_init(bars + i, i < 3 ? 2 : i == 7 || i >= 9 ? 1 : 16);
         *fail = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -131,6 +136,8 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
     const uint32_t tb = *tmem_slot;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, bar_wait(bar, parity)); };
+    auto image_bar = [&](int j) { return stg_done + j % IMAGE_BARS; };  // j: images before it
+    auto image_phase = [&](int j) { return (uint32_t)(j / IMAGE_BARS) & 1; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -141,7 +148,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 const int t = (int)tok_of(i);
                 // chunk i - 2's images have left by this stage; where there are none, chunk i - 3 has been used
                 if (sum_pass ? i >= 3 : i >= 2 + i0)
-                    ok = sum_pass ? bar_wait(u_done, (i - 3) & 1) : bar_wait(stg_done, (i - i0) & 1);
+                    ok = sum_pass ? bar_wait(u_done, (i - 3) & 1) : bar_wait(image_bar(i - 2 - i0), image_phase(i - 2 - i0));
                 if (!ok) break;
                 mbar_arrive_expect_tx(in + i % 3, L::STAGE);
                 for (int b = 0; b < DK / 64; ++b) tma_load_3d(st + b * C * 128, &D.a, 64 * b, ha, t, in + i % 3);
@@ -187,7 +194,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 if (a.lo) bulk_s2g(dst + DK * DV * 2, src + L::IMG, L::IMG);
                 bulk_commit();
                 bulk_wait_read0();
-                mbar_arrive(stg_done);
+                mbar_arrive(image_bar(i - i0));
             }
         }
     } else {
@@ -273,7 +280,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
             }
             if (i >= i0) {  // the images, under the product, by way of the rows' tile of the chunk before
                 // (those before them have left, so that stg_full is never two phases ahead of who waits for it)
-                if (i > i0) wait(stg_done, (i - 1 - i0) & 1);
+                if (i > i0) wait(image_bar(i - 1 - i0), image_phase(i - 1 - i0));
                 if (!ok) break;
                 if (mine) {
 #pragma unroll

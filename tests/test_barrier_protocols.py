@@ -3,9 +3,10 @@ can miss the phase that it is for, and a wait that runs out leaves nobody at a b
 
 A role is a list of steps: ("wait", barrier, phase), ("arrive", barrier), ("sync", barrier) for a hardware barrier
 that all of its members reach.  A parity wait passes where the barrier has completed an odd number of phases more than
-`phase` before it, which is what the hardware tells: two phases ahead looks like none.  The kind of the prefill's meeting
-is read from its source."""
+`phase` before it, which is what the hardware tells: two phases ahead looks like none.  How many
+barriers the images take in turn and the kind of the prefill's meeting are read from the sources."""
 import os
+import re
 
 import pytest
 
@@ -69,6 +70,60 @@ def explore(roles, counts, can_time_out):
                 seen.add(s)
                 todo.append(s)
     return None
+
+
+# ------------------------------------------------------------------ chains of the gradients: tiles and images
+def chain(nc, i0, bars):
+    """Loader, products, images and one worker of linear_bwd_states_tc_kernel on nc chunks, whose images begin with chunk
+    i0; `bars`: barriers that the images' phases go round."""
+    image = lambda j: (("stg_done", j % bars), j // bars)  # noqa: E731
+    load, mma, img, work = [], [], [], []
+    for i in range(nc):
+        if i >= 2 + i0:
+            load.append(("wait", *image(i - 2 - i0)))
+        load.append(("arrive", ("in", i % 3)))
+        mma += [("wait", "s_ready", i), ("wait", ("in", i % 3), i // 3), ("arrive", "u_done")]
+    for i in range(i0, nc):
+        img += [("wait", "stg_full", i - i0), ("arrive", image(i - i0)[0])]
+    work.append(("wait", ("in", 0), 0))
+    for i in range(nc):
+        if i:
+            work.append(("wait", "u_done", i - 1))
+        work.append(("arrive", "s_ready"))
+        if i >= i0:
+            if i > i0:
+                work.append(("wait", *image(i - 1 - i0)))
+            work.append(("arrive", "stg_full"))
+        if i + 1 < nc:
+            work.append(("wait", ("in", (i + 1) % 3), (i + 1) // 3))
+    work.append(("wait", "u_done", nc - 1))
+    roles = [load, mma, img, work]
+    counts = {s[1]: 1 for p in roles for s in p}
+    return roles, counts
+
+
+@pytest.mark.parametrize("i0", [0, 1])
+@pytest.mark.parametrize("nc", [1, 2, 3, 5, 9])
+def test_chains_never_miss_a_phase(nc, i0):
+    bars = re.search(r"constexpr int IMAGE_BARS = (\d+);", source("kda_linear_bwd_tc.cu"))
+    assert explore(*chain(nc, i0, int(bars.group(1)) if bars else 1), False) is None
+
+
+@pytest.mark.parametrize("nc", [1, 4, 9])
+def test_sums_of_segments_never_miss_a_phase(nc):
+    """Their loader waits for the products of three chunks before."""
+    load, mma, work = [], [], [("wait", ("in", 0), 0)]
+    for i in range(nc):
+        load += ([("wait", "u_done", i - 3)] if i >= 3 else []) + [("arrive", ("in", i % 3))]
+        mma += [("wait", "s_ready", i), ("wait", ("in", i % 3), i // 3), ("arrive", "u_done")]
+        work += ([("wait", "u_done", i - 1)] if i else []) + [("arrive", "s_ready")]
+        if i + 1 < nc:
+            work.append(("wait", ("in", (i + 1) % 3), (i + 1) // 3))
+    assert explore([load, mma, work], {s[1]: 1 for p in (load, mma, work) for s in p}, False) is None
+
+
+def test_one_barrier_for_all_images_would_miss_one():
+    assert explore(*chain(5, 0, 1), False) is not None
 
 
 # ------------------------------------------------------------------ prefill: the meeting of a quarter's warps
