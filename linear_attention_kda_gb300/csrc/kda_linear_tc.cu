@@ -3,13 +3,16 @@
 //   linear_fwd_tc_kernel      one CTA runs the chain of a (sequence, head), or of one segment of it: per chunk
 //                                 X = Q K^T,  P = Tril[X * e^{G_r - G_j}],  O = scale (P V + e^G (Q S)),
 //                                 S <- e^{G_C} S + (K e^{G_C - G})^T V
-//                             with S in tensor memory (fp32), so that q, k and v are read once and o is written once.
+//                             with S in fp32 on the chip, so that q, k and v are read once and o is written once.
 //   linear_segments_tc_kernel where there are few chains: what each segment adds to the state, (K f)^T V over its
 //                             chunks; the first kernel then begins every segment from those before it.
 //
 // Numerics: products take bf16 operands and add in fp32.  P and the state that multiplies Q are rounded to bf16 once
 // (they go into bf16 outputs); the keys that go into the fp32 state are kept as two bf16 parts, K f = hi + lo, and
-// take two products, so that a state is good to 2^-16 of its terms instead of 2^-8.
+// take two products, so that a state is good to 2^-16 of its terms instead of 2^-8.  The tensor cores make each chunk's
+// (K f)^T V by itself, and the threads add it to the state: an accumulator that a whole chain runs through is cut at every
+// K-step, always towards zero (without decay -7.4e-5 of the state after 16,384 tokens and growing with their number; now
+// below 1e-6 at any length).  It costs 2 % of a chain's step and up to 6 % where loads are late.
 #include "kda_linear_tc.cuh"
 
 namespace kda {
@@ -105,7 +108,9 @@ static_assert(sizeof(decays) % 16 == 0, "alignment");
 static_assert(fwd_smem<128, 128>::BYTES <= 227 * 1024, "shared memory");
 
 constexpr int FWD_THREADS = 640;
-enum { T_X = 0, T_D = 256, T_S = 384 };  // tensor memory columns: X of two chunks in turn (P, bf16, lies over it), outputs, state
+// Tensor memory columns: two that take turns (a chunk's X, over which P lies as bf16, in one; what it adds to the state in
+// the other, from after P V of the chunk before to before X of the next), outputs, state.
+enum { T_X = 0, T_D = 256, T_S = 384 };
 
 // Warps: 0 loads tiles, 1 issues the products, 2 makes the decays; 4-19 work on what the products leave, all of them on
 // one thing after the other: warp w has lane quarter w % 4 and column quarter (w - 4) / 4 of every 128 x 128 piece.
@@ -113,9 +118,9 @@ enum { T_X = 0, T_D = 256, T_S = 384 };  // tensor memory columns: X of two chun
 // one warp's own latency, and a step of the chain 8400 cycles.)
 //
 // Tiles of 128 tokens go through a ring of four slots in the order Q K V Q K V ..., each freed by the product that
-// reads it last.  Products are issued in the order Q S, the next chunk's X, (K f)^T V twice, P V: X is there before
-// its keys are scaled (in place), the state's loop (products, read, scale, image) has the outputs and P made beside
-// it.  Q S lands where P V adds to it, its rows multiplied by e^G in between.
+// reads it last.  Products are issued in the order X, Q S, (K f)^T V twice, P V; X of the next chunk stands behind P V, in
+// other columns, and is made while the state is added up and the outputs leave; the state's part of a chunk (products, sum,
+// image) has the outputs and P made beside it.  Q S lands where P V adds to it, its rows multiplied by e^G in between.
 template <int DK, int DV>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
 linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ chain_args a) {
@@ -125,7 +130,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BAR), *free_ = full + L::SLOTS, *dec_ready = free_ + L::SLOTS,
              *dec_free = dec_ready + 2, *x_done = dec_free + 2, *p_ready = x_done + 1, *s_ready = p_ready + 1,
              *k_ready = s_ready + 1, *u_done = k_ready + 1, *o_done = u_done + 1, *o_read = o_done + 1, *o_staged = o_read + 1, *o_stored = o_staged + 1,
-             *d_done = o_stored + 1, *x_read = d_done + 1;  // x_read: one for each lane quarter
+             *d_done = o_stored + 1, *u_read = d_done + 1, *x_read = u_read + 1;  // x_read: one for each lane quarter
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_read + 4);
     int *fail = reinterpret_cast<int *>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -153,6 +158,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
         mbar_init(o_staged, 16);
         mbar_init(o_stored, 1);
         mbar_init(d_done, 1);
+        mbar_init(u_read, 16);
         for (int i = 0; i < 4; ++i) mbar_init(x_read + i, 4);
         *fail = 0;
     }
@@ -203,31 +209,30 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                 mma_commit(x_done);
             };
 #pragma unroll 1
-            for (int i = -1; i < nc && nc > 0; ++i) {
-                if (i >= 0) {
-                    const uint32_t k = smem_u32(tile(3 * i + 1)), v = smem_u32(tile(3 * i + 2));
-                    ok = bar_wait(s_ready, i & 1) && (i == 0 || bar_wait(o_read, (i - 1) & 1));
-                    if (!ok) break;
-                    fence_after_sync();
-                    mma_bf16_kmn(tb + T_D, smem_u32(tile(3 * i)), C, simg, DK * 128, DK / 16, id_d1, false);
-                    mma_commit(d_done);
-                    mma_commit(free_ + (3 * i) % L::SLOTS);
-                    ok = bar_wait(k_ready, i & 1) && bar_wait(full + (3 * i + 2) % L::SLOTS, tile_phase(3 * i + 2));
-                    if (!ok) break;
-                    fence_after_sync();
-                    mma_bf16_mnmn(tb + T_S, k, KLBO, v, 16384, C / 16, id_u, true);
-                    mma_bf16_mnmn(tb + T_S, klo, KLBO, v, 16384, C / 16, id_u, true);
-                    mma_commit(u_done);
-                    mma_commit(free_ + (3 * i + 1) % L::SLOTS);
-                    ok = bar_wait(p_ready, i & 1);
-                    if (!ok) break;
-                    fence_after_sync();
-                    mma_ts_mn(tb + T_D, tb + T_X + 128 * (i & 1), v, 16384, C / 16, id_d1, true);
-                    mma_commit(o_done);
-                    mma_commit(free_ + (3 * i + 2) % L::SLOTS);
-                }
-                if (i + 1 < nc) x_of(i + 1);
+            for (int i = 0; i < nc; ++i) {
+                const uint32_t k = smem_u32(tile(3 * i + 1)), v = smem_u32(tile(3 * i + 2));
+                const uint32_t x = tb + T_X + 128 * (i & 1), u = tb + T_X + 128 * (~i & 1);
+                if (i > 0) ok = bar_wait(u_read, (i - 1) & 1);  // X may lie where the state's last part was
+                x_of(i);
+                ok = ok && bar_wait(s_ready, i & 1) && (i == 0 || bar_wait(o_read, (i - 1) & 1));
                 if (!ok) break;
+                fence_after_sync();
+                mma_bf16_kmn(tb + T_D, smem_u32(tile(3 * i)), C, simg, DK * 128, DK / 16, id_d1, false);
+                mma_commit(d_done);
+                mma_commit(free_ + (3 * i) % L::SLOTS);
+                ok = bar_wait(k_ready, i & 1) && bar_wait(full + (3 * i + 2) % L::SLOTS, tile_phase(3 * i + 2));
+                if (!ok) break;
+                fence_after_sync();
+                mma_bf16_mnmn(u, k, KLBO, v, 16384, C / 16, id_u, false);
+                mma_bf16_mnmn(u, klo, KLBO, v, 16384, C / 16, id_u, true);
+                mma_commit(u_done);
+                mma_commit(free_ + (3 * i + 1) % L::SLOTS);
+                ok = bar_wait(p_ready, i & 1);
+                if (!ok) break;
+                fence_after_sync();
+                mma_ts_mn(tb + T_D, x, v, 16384, C / 16, id_d1, true);
+                mma_commit(o_done);
+                mma_commit(free_ + (3 * i + 2) % L::SLOTS);
             }
         }
     } else if (warp == 2) {
@@ -294,6 +299,21 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
             tmem_store<CW>(ts, x);
             tmem_st_wait();
         }
+        auto load_state = [&](int i, float *x) {  // before chunk i, with what chunk i - 1 adds to it
+            if (i == 0) {
+                tmem_load<CW>(ts, x);
+                return;
+            }
+#pragma unroll
+            for (int c = 0; c < CW; c += 16) {
+                float y[16];
+                tmem_load_pair(ts + c, tl + T_X + 128 * (i & 1) + CW * part + c, x + c, y);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[c + j] += y[j];
+            }
+            fence_before_sync();
+            arrive(u_read);
+        };
         for (int i = 0; i <= nc; ++i) {
             // ---- the state after chunk i - 1: its bf16 image, and itself times the chunk's whole decay
             if (i > 0) wait(u_done, (i - 1) & 1);
@@ -303,7 +323,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
             const decays &d = dec[i & 1];
             if (i < nc) {
                 float x[CW];
-                tmem_load<CW>(ts, x);
+                load_state(i, x);
                 if (mine) {
                     unsigned char *img = sm + L::SIMG + (CW * part >> 6) * (DK * 128) + row * 128;
 #pragma unroll
@@ -423,7 +443,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
         }
         if (ok && w.last && a.final) {  // the loop's last round has waited for the last state products
             float x[CW];
-            tmem_load<CW>(ts, x);
+            load_state(nc, x);
             if (mine) {
 #pragma unroll
                 for (int c = 0; c < CW; c += 4)
@@ -450,7 +470,8 @@ template <int DK, int DV> struct seg_smem {
 constexpr int SEG_THREADS = 640;
 
 // Every segment but a sequence's last: the state that its tokens leave behind (the first one's begins from the
-// initial state).  Warps as in the forward kernel; each chunk's keys are scaled before the state is read.
+// initial state), in the threads' registers; a chunk's products are added to it as in the forward kernel.  Warps as there;
+// each chunk's keys are scaled before the last one's products are waited for.
 template <int DK, int DV>
 __global__ void __launch_bounds__(SEG_THREADS, 1)
 linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ chain_args a) {
@@ -510,7 +531,7 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
                 ok = bar_wait(ready, i & 1) && bar_wait(full + (i & 1), (i >> 1) & 1);
                 if (!ok) break;
                 fence_after_sync();
-                mma_bf16_mnmn(tb, st, KLBO, st + L::KT, 16384, C / 16, id_u, true);
+                mma_bf16_mnmn(tb, st, KLBO, st + L::KT, 16384, C / 16, id_u, false);
                 mma_bf16_mnmn(tb, smem_u32(sm + L::LO + (i & 1) * L::KT), KLBO, st + L::KT, 16384, C / 16, id_u, true);
                 mma_commit(u_done);
                 mma_commit(free_ + (i & 1));
@@ -543,6 +564,18 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
                               ? a.initial + (w.n * a.H + w.h) * (int64_t)(DK * DV) + (int64_t)row * DV + CW * part : nullptr;
 #pragma unroll
         for (int c = 0; c < CW; ++c) x[c] = s0 ? s0[c] : 0.f;
+        auto add_products = [&](int i) {  // of chunk i
+            wait(u_done, i & 1);
+            if (!ok) return;
+            fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < CW; c += 16) {
+                float y[16];
+                tmem_load<16>(ts + c, y);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[c + j] += y[j];
+            }
+        };
         for (int i = 0; i < nc; ++i) {
             wait(dec_ready + (i & 1), (i >> 1) & 1);
             wait(full + (i & 1), (i >> 1) & 1);
@@ -551,16 +584,10 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
             scale_chunks<KC>(sm + (i & 1) * L::STAGE, sm + L::LO + (i & 1) * L::KT, row, KC * part,
                              expf(ends(d, 3, quarter)) * d.w[row]);
             const float all = expf(d.hi[3]);
-            if (i > 0) {
-                wait(u_done, (i - 1) & 1);
-                if (!ok) break;
-                fence_after_sync();
-                tmem_load<CW>(ts, x);
-            }
+            if (i > 0) add_products(i - 1);
+            if (!ok) break;
 #pragma unroll
             for (int c = 0; c < CW; ++c) x[c] *= all;
-            tmem_store<CW>(ts, x);
-            tmem_st_wait();
             fence_proxy_async();
             fence_before_sync();
             __syncwarp();
@@ -569,10 +596,8 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
                 mbar_arrive(dec_free + (i & 1));
             }
         }
-        wait(u_done, (nc - 1) & 1);
+        if (ok) add_products(nc - 1);
         if (ok) {
-            fence_after_sync();
-            tmem_load<CW>(ts, x);
             float *p = a.sums + (w.slot * a.H + w.h) * (int64_t)(DK * DV) + (CW * part * DK + row * 4);
             if (mine) {
 #pragma unroll
