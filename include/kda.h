@@ -542,7 +542,8 @@ int kda_abi_version(void);
  * kda_recurrent_step, kda_recurrent_replay, kda_output_gate, kda_chunk_bwd, the three kda_linear_* calls
  * and kda_rope where its outputs are dense) launches one more pass
  * over what it wrote (outputs, final or updated states, gradients) that sets KDA_ERR_NUMERIC in the
- * device error word (kda_get_device_error) when any value is NaN or infinite.  The pass reads those
+ * device error word (kda_get_device_error) when any value is NaN or infinite; of a
+ * kda_linear_recurrent_step, the rows and slots of its state_indices alone.  The pass reads those
  * results once more from HBM.  Index checks need no switch: cu_seqlens contents, state indices and
  * replay counts are always checked on the device.  Process-wide; 0 (the default) turns the checks
  * off.  KDA_ERR_INVALID_ARG for an unknown flag. */

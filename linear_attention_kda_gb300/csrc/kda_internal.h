@@ -127,6 +127,10 @@ kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const kda_row_pa
                                   const kda_row_parts &pv, const float *dg_slot, int64_t slots, cudaStream_t stream);
 kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream);
+// kda_check_finite for N rows of `len` elements, `len` a multiple of 8 and p 16-byte aligned: of those whose used[n] (NULL:
+// all) lies in [0, slots), row at[n] of p (NULL: row n)
+kda_status_t kda_check_finite_rows(const void *p, int64_t len, int64_t N, const int32_t *used, const int32_t *at, int64_t slots,
+                                   kda_dtype_t dtype, cudaStream_t stream);
 kda_status_t kda_launch_linear_step(const kda_linear_step_args *a, cudaStream_t stream);
 kda_status_t kda_launch_state_copy(const kda_state_copy_args *a, cudaStream_t stream);
 kda_status_t kda_launch_rope(const kda_rope_args *a, cudaStream_t stream);

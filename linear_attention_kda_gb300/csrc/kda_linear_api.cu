@@ -158,8 +158,12 @@ kda_status_t kda_linear_recurrent_step(const kda_linear_step_args *a, struct CUs
     if (st != KDA_OK) return st;
     st = kda_launch_linear_step(a, (cudaStream_t)stream);
     if (st == KDA_OK && (kda_debug_flags() & KDA_CHECK_FINITE)) {
-        st = kda_check_finite(a->o, a->N * a->H * (int64_t)a->dv, a->dtype, (cudaStream_t)stream);
-        if (st == KDA_OK) st = kda_check_finite(a->state, slots * per_slot, KDA_F32, (cudaStream_t)stream);
+        // (the rows and slots of this call: an unused row's output and other slots may hold anything)
+        const int64_t row = (int64_t)a->H * a->dv;
+        st = kda_check_finite_rows(a->o, row, a->N, a->state_indices, nullptr, slots, a->dtype, (cudaStream_t)stream);
+        if (st == KDA_OK)
+            st = kda_check_finite_rows(a->state, per_slot, a->N, a->state_indices, a->state_indices, slots, KDA_F32,
+                                       (cudaStream_t)stream);
     }
     return st;
 }
