@@ -380,7 +380,10 @@ kda_status_t kda_recurrent_step(const kda_step_args *args, struct CUstream_st *s
  *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t
  * with one log-decay g per head and token (g_per_token = 1, [T, H]), one per head ([H]), or none
  * (g NULL: exp(g) = 1).  g is fp32 and at most 0; a log-decay below -104 (-inf included) counts as
- * -104, whose factor is 0 in fp32: it erases the state.  Values above 0 are computed as given and may
+ * -104, whose factor is 0 in fp32: it erases the state, infinities and NaN that it holds included, so that a slot
+ * which was never cleared may begin a sequence whose first token has such a decay.  (In the chunked calls so does a
+ * chunk's whole decay, or several chunks', where it is 0 in fp32; and an infinity or a NaN that a token's own k or v brings
+ * may outlast an erasing decay of the same chunk.)  Values above 0 are computed as given and may
  * overflow; a NaN spreads over its sequence and head from its token on (in a gradient, over the sequence).
  * A NaN or an infinity in q, k, v or grad_o stays in its sequence and head too, but may reach the tokens before it in
  * its chunk (64 tokens in fp32, 128 in bf16): products with masked zeros are formed there.

@@ -93,6 +93,14 @@ __device__ __forceinline__ ff ff_shfl(const ff &a, int lane) {
 // A log-decay below -104 counts as -104 (exp of it is 0 in fp32); a NaN stays one.
 __device__ __forceinline__ float clamp_decay(float g) { return g < -104.f ? -104.f : g; }
 
+// To be called on values that decay by the factor f: where f is 0 nothing of them is left, infinities and NaN included.
+template <int N> __device__ __forceinline__ void erase(float (&x)[N], float f) {
+    if (f == 0.f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = 0.f;
+    }
+}
+
 // Cumulative log-decays G of one chunk, by one warp, kept as fp32 pairs hi + lo: the difference of two of them, (hi_r -
 // hi_j) + (lo_r - lo_j), is then good to an fp32 rounding of itself even where many erasing decays have made both
 // large.  x: this lane's log-decays, tokens lane * C / 32 on.

@@ -234,6 +234,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
                 const int64_t s = sum_at + (back ? j : -j) * (int64_t)a.H;
                 const float f = a.decay[s];
                 if (!mine) continue;
+                erase(x, f);
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(a.sums + s * (DK * DV) + own + c);
@@ -251,6 +252,7 @@ linear_bwd_states_tc_kernel(const __grid_constant__ states_maps dirs, const __gr
 #pragma unroll
             for (int c = 0; c < CW; ++c) y[c] += z[c];
             tmem_load<CW>(ts + (i & 1) * 256, z);
+            erase(x, all);
 #pragma unroll
             for (int c = 0; c < CW; ++c) x[c] = fmaf(x[c], all, y[c] + z[c]);
         };
@@ -720,9 +722,10 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             fence_after_sync();
             float x[KW] = {};
             if (has_s) tmem_load<KW>(tl + T_Y + KW * part, x);
-            const float e = a.scale * expf(ends(d, quarter - 1, -1) + rel);
+            const float e = expf(ends(d, quarter - 1, -1) + rel), se = a.scale * e;
+            erase(x, e);
 #pragma unroll
-            for (int i = 0; i < KW; ++i) x[i] *= e;
+            for (int i = 0; i < KW; ++i) x[i] *= se;
             if (decay) qdq = row_dot<KW>(x, sm + L::Q, row, KW * part);
             if (MODE == KV) tmem_store<KW>(tl + T_Y + KW * part, x);
             else add_store(kw{}, tl + T_S + KW * part, x);
@@ -746,6 +749,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 fence_before_sync();
                 arrive(a_ready);
             }
+            erase(x, f);
 #pragma unroll
             for (int i = 0; i < KW; ++i) x[i] *= f;
             if (decay) kdk = row_dot<KW>(x, sm + L::K, row, KW * part);
@@ -758,6 +762,7 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
             fence_after_sync();
             float x[VW] = {};
             if (has_l) tmem_load<VW>(tl + (MODE == KV ? T_X : T_Y) + VW * part, x);
+            erase(x, f);
 #pragma unroll
             for (int i = 0; i < VW; ++i) x[i] *= f;
             if (MODE == KV) add_store(vw{}, tl + T_S + VW * part, x);
@@ -781,7 +786,9 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
                 float p[4], kk[4], after = 0.f, before = 0.f, whole = lane < 16 ? sums.dot[lane] : 0.f;
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
-                whole = __shfl_sync(0xffffffffu, whole, 0) * expf(d.hi[3]);
+                const float left = expf(d.hi[3]);
+                whole = __shfl_sync(0xffffffffu, whole, 0);
+                whole = left == 0.f ? 0.f : whole * left;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 4 * lane + i;

@@ -131,9 +131,11 @@ __global__ void __launch_bounds__(NT) linear_states_kernel(states_args fwd, stat
         __syncthreads();
         fetch(i + 1);
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < 4; ++a) {
+            erase(S[a], all);
 #pragma unroll
             for (int j = 0; j < TN; ++j) S[a][j] *= all;
+        }
 #pragma unroll 8
         for (int t = 0; t < C; ++t) {
             const float4 x = *reinterpret_cast<const float4 *>(&s_k[t][r0]);
@@ -281,6 +283,7 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(const float *q, const fl
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float e = expf(s_hi[ty + 16 * i]);
+        erase(acc[i], e);
 #pragma unroll
         for (int j = 0; j < DV / 16; ++j) acc[i][j] *= e;
     }
@@ -425,8 +428,11 @@ __global__ void __launch_bounds__(NT) linear_grads_kernel(grads_args A) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
-        const float e = scale * expf(s_hi[r]), f = expf((Gh - s_hi[r]) + (Gl - s_lo[r]));
+        const float w = expf(s_hi[r]), e = scale * w, f = expf((Gh - s_hi[r]) + (Gl - s_lo[r]));
         float a = 0.f, b = 0.f;
+        erase(dq[i], w);
+        erase(dk[i], f);
+        erase(dv[i], f);
 #pragma unroll
         for (int j = 0; j < DK / 16; ++j) {
             dq[i][j] *= e;
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(NT) linear_grads_kernel(grads_args A) {
     if (tid < 32) {
         ff whole{0.f, 0.f};
         for (int w = 0; w < NT / 32; ++w) whole = ff_add(whole, {s_dot[w], 0.f});
-        const float all = (whole.h + whole.l) * expf(Gh);
+        const float left = expf(Gh), all = left == 0.f ? 0.f : (whole.h + whole.l) * left;
         const ff x0 = ff_add({s_row[2 * tid], 0.f}, {s_qdq[2 * tid], 0.f});
         const ff own = ff_add(x0, ff_add({s_row[2 * tid + 1], 0.f}, {s_qdq[2 * tid + 1], 0.f}));
         const float k0 = s_kdk[2 * tid];

@@ -288,6 +288,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                 for (int64_t s = w.slot - w.index; s < w.slot; ++s) {
                     const float f = expf((float)a.sum_g[s * a.H + w.h]);
                     const float *p = a.sums + (s * a.H + w.h) * (int64_t)(DK * DV) + (CW * part * DK + row * 4);
+                    erase(x, f);
 #pragma unroll
                     for (int c = 0; c < CW; c += 4) {
                         const float4 u = __ldcg(reinterpret_cast<const float4 *>(p + c * DK));
@@ -333,6 +334,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                                        pack_bf16(x[c + 4], x[c + 5]), pack_bf16(x[c + 6], x[c + 7]));
                 }
                 const float all = expf(d.hi[3]);
+                erase(x, all);
 #pragma unroll
                 for (int c = 0; c < CW; ++c) x[c] *= all;
                 tmem_store<CW>(ts, x);
@@ -429,6 +431,7 @@ linear_fwd_tc_kernel(const __grid_constant__ maps tm, const __grid_constant__ ch
                 const float e = expf(ends(d, quarter - 1, -1) + rel);
                 float y[CW];
                 tmem_load<CW>(tl + T_D + CW * part, y);
+                erase(y, e);
 #pragma unroll
                 for (int c = 0; c < CW; ++c) y[c] *= e;
                 tmem_store<CW>(tl + T_D + CW * part, y);
@@ -586,6 +589,7 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
             const float all = expf(d.hi[3]);
             if (i > 0) add_products(i - 1);
             if (!ok) break;
+            erase(x, all);
 #pragma unroll
             for (int c = 0; c < CW; ++c) x[c] *= all;
             fence_proxy_async();
