@@ -485,7 +485,7 @@ typedef struct {
     const void *src_pool;          /* [src_slots] slots, 16-byte aligned; NULL if every src is -1 and src_slots is 0 */
     void *dst_pool;                /* [dst_slots] slots, 16-byte aligned */
     int64_t slot_bytes;
-    int64_t src_slots, dst_slots;  /* at most 2^31 - 1 each */
+    int64_t src_slots, dst_slots;  /* at most 2^31 - 1 each, and 2^48 bytes of slots */
     int64_t P;                     /* pairs */
     const int32_t *src, *dst;      /* [P] device */
 } kda_state_copy_args;

@@ -22,6 +22,9 @@ bool overlap(const range &a, const range &b) {
     return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
 
+// Pools are below 2^48 bytes, so that no product of their sizes leaves 64 bits.
+bool pool_ok(int64_t slots, int64_t slot_bytes) { return slot_bytes == 0 || slots <= ((int64_t)1 << 48) / slot_bytes; }
+
 bool dim_ok(int32_t d) { return d == 64 || d == 128; }
 
 // sizes that every linear call checks; rows is T, or N for the step
@@ -142,8 +145,8 @@ kda_status_t kda_linear_recurrent_step(const kda_linear_step_args *a, struct CUs
     if (!a->q || !a->k || !a->v || !a->o || !a->state) return KDA_ERR_INVALID_ARG;
     if (!a->state_indices && a->num_slots != 0 && a->num_slots < a->N) return KDA_ERR_INVALID_ARG;
     const int64_t slots = a->num_slots ? a->num_slots : a->N, es = dtype_size(a->dtype);
-    if (slots > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
     const int64_t per_slot = (int64_t)a->H * a->dk * a->dv;
+    if (slots > INT32_MAX || !pool_ok(slots, per_slot * 4)) return KDA_ERR_UNSUPPORTED_SHAPE;
     const range in[] = {{a->q, a->N * a->Hq * a->dk * es}, {a->k, a->N * a->Hk * a->dk * es},
                         {a->v, a->N * a->Hv * a->dv * es}, {a->g, (a->g_per_token ? a->N : 1) * a->H * 4},
                         {a->state_indices, a->N * 4}};
@@ -172,7 +175,7 @@ kda_status_t kda_state_copy(const kda_state_copy_args *a, struct CUstream_st *st
     if (!a) return KDA_ERR_INVALID_ARG;
     if (a->P < 0 || a->src_slots < 0 || a->dst_slots < 0 || a->slot_bytes < 0) return KDA_ERR_INVALID_ARG;
     if (a->P > INT32_MAX || a->src_slots > INT32_MAX || a->dst_slots > INT32_MAX || a->slot_bytes % 16 != 0 ||
-        a->slot_bytes > ((int64_t)1 << 40))
+        !pool_ok(a->src_slots, a->slot_bytes) || !pool_ok(a->dst_slots, a->slot_bytes))
         return KDA_ERR_UNSUPPORTED_SHAPE;
     if (a->P == 0 || a->slot_bytes == 0) return KDA_OK;
     if (!a->src || !a->dst || !a->dst_pool || (!a->src_pool && a->src_slots > 0)) return KDA_ERR_INVALID_ARG;

@@ -204,3 +204,13 @@ def test_rope_frequencies():
     for bad in (lambda: kda.rope_frequencies(7), lambda: kda.rope_frequencies(8, scaling="odd"), lambda: kda.rope_frequencies(8, scaling="yarn", factor=2.0)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("a", [
+    # a pool of 2^64 bytes begins a slot before the other one and would end where it began
+    _copy(slot_bytes=1 << 40, src_slots=1 << 24, dst_slots=1 << 24, dst_pool=FAKE + 4096),
+    _copy(slot_bytes=1 << 40, src_slots=1, dst_slots=1 << 23, dst_pool=FAKE - 4096),
+    _step(H=65535, Hq=65535, Hk=65535, Hv=65535, N=1, num_slots=(1 << 31) - 1, state=FAKE - 4096, g_per_token=0),
+])
+def test_pools_that_no_address_reaches_are_refused(lib, a):
+    assert _call(lib, a) == 2
