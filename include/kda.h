@@ -396,7 +396,9 @@ kda_status_t kda_recurrent_step(const kda_step_args *args, struct CUstream_st *s
  * [N, H, dk, dv] fp32.  Memory, packing, streams and errors are as for kda_chunk_fwd; cu_seqlens
  * contents are checked on the device (KDA_ERR_BAD_SEQLENS; sequences with a bad range are skipped, their
  * gradients' rows unspecified, and rows that belong to no sequence are left as they were).  An empty sequence's final state is its
- * initial state, exactly.  Outputs may not overlap inputs, except that final_state may be
+ * initial state, exactly.  fp32 calls are in fp32 throughout (2e-7 of an element's terms, as a norm).  bf16 calls round
+ * the products that make bf16 results to bf16 once, and hold the terms of the fp32 ones in two bf16 parts: final states
+ * and grad_g are good to 2^-16 of their terms (3e-6 as a norm), at any length.  Outputs may not overlap inputs, except that final_state may be
  * initial_state.  Every call is free of atomics on its results: the same inputs give the same bits. */
 typedef struct {
     int64_t T, N;                  /* tokens (all sequences packed), sequences (>= 1) */

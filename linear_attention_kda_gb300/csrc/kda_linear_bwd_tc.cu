@@ -900,8 +900,8 @@ linear_grads_tc_kernel(const __grid_constant__ grads_maps tm, const __grid_const
 // ---------------------------------------------------------------------------------------------------- launches
 // Heads that a block takes in turn, a divisor of those that share a head of q and one of k (or of k and v): the sum over
 // them then stays with the block, which also loads what they share once.  As many as leave a block for every second SM.
-// Whole calls, 32 heads, d = 128, 4 heads to a block and one: 8 heads of q and k, 16384 tokens 525 / 827 us, 4096 tokens
-// 152 / 227, 2048 tokens 79 / 127 (a block for every SM, two heads: 116); 8 of k and v 542 / 844, 158 / 234, 83 / 131; one
+// Whole calls, 32 heads, d = 128, 4 heads to a block and one: 8 heads of q and k, 16384 tokens 539 / 845 us, 4096 tokens
+// 159 / 235, 2048 tokens 84 / 132 (a block for every SM, two heads: 116); 8 of k and v 542 / 841, 158 / 232, 84 / 131; one
 // head of q and k, 1024 tokens: 4 heads to a block 60, one or two 74, all 32 298.
 static int heads_of_block(int64_t slots, int H, int rq, int rk) {
     int r = 1;
@@ -913,9 +913,9 @@ static int heads_of_block(int64_t slots, int H, int rq, int rk) {
 // Chunks of a segment, 0 for chains in one piece.  A chain is one CTA's (two, dv = 128, and two directions), so few of them
 // leave the GPU idle.  Cut into `want` pieces each, they take a pass that sums the pieces and one that runs them, each
 // chunks / want steps long, and a launch more, which pays off where chunks - 2 chunks / want is above ten steps.
-// Measured, dv = 128 unless said, cut and whole: 8192 tokens of 2 heads, dv = 64, 71 / 117 us, 8 heads 121 / 168, 12 heads
-// 164 / 190; 65536 of 8 heads 773 / 1213; 2048 of 1 head 37 / 42; 1280 of 2 heads 33.5 / 32.3; four sequences of 2048
-// and 6 heads, dv = 64, 70.6 / 67.4.
+// Measured, dv = 128 unless said, cut and whole: 8192 tokens of 2 heads, dv = 64, 69 / 119 us, 8 heads 131 / 172, 12 heads
+// 175 / 193; 65536 of 8 heads 815 / 1224; 2048 of 1 head 37 / 42; 1280 of 2 heads 35 / 33; four sequences of 2048
+// and 6 heads, dv = 64, 74 / 68.
 static int64_t chain_segment(int64_t T, int64_t N, int H, int dv) {
     const int64_t want = 152 / (2 * N * H * (dv / W)), chunks = (T + C - 1) / C / N;  // of a sequence, on average
     if (chunks * (want - 2) <= 10 * want) return 0;

@@ -1,7 +1,7 @@
 // Linear attention with a decay per head in fp32 on the CUDA cores: every product of the chunked form (chunks of
 // C = 64 tokens), forward and backward, for fp32 tensors.  Bound by shared memory and FMA issue; 4096 tokens of 32
-// heads, d = 128: 0.52 ms forward and 1.2 ms backward on bf16 tensors, against 0.049 and 0.155 on the tensor cores, and
-// 64 tokens 27 / 68 us against 7 / 19, so that bf16 goes there at every length.
+// heads, d = 128, replayed from a graph: 0.57 ms forward and 1.27 ms backward, where bf16 tensors take 0.056 and 0.162 on
+// the tensor cores, and 64 tokens 29 / 70 us against 10 / 18, so that bf16 goes there at every length.
 //
 //   linear_states_kernel  the recurrence over chunks, S <- e^{G_C} S + (K e^{G_C - G})^T V, and backwards
 //                         Lambda <- e^{G_C} Lambda + scale (Q e^G)^T dO; leaves each chunk's entering S and
@@ -20,16 +20,14 @@ namespace lin {
 constexpr int C = 64;
 constexpr int NT = 256;
 
-// C x D tile (rows of `stride` elements in memory, zeros behind `len`) to shared memory rows of `pitch` floats,
-// row r multiplied by f[r] where given.
+// C x D tile (rows of `stride` elements in memory, zeros behind `len`) to shared memory rows of `pitch` floats.
 template <int D>
-__device__ __forceinline__ void load_tile(float *s, int pitch, const float *p, int64_t stride, int len, const float *f) {
+__device__ __forceinline__ void load_tile(float *s, int pitch, const float *p, int64_t stride, int len) {
     constexpr int V = 4, PER = D / V;
 #pragma unroll 4
     for (int e = threadIdx.x; e < C * PER; e += NT) {
         const int r = e / PER, c = (e % PER) * V;
         float4 x = r < len ? *reinterpret_cast<const float4 *>(p + r * stride + c) : make_float4(0, 0, 0, 0);
-        if (f && r < len) x.x *= f[r], x.y *= f[r], x.z *= f[r], x.w *= f[r];
         *reinterpret_cast<float4 *>(s + r * pitch + c) = x;
     }
 }
@@ -254,9 +252,9 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(const float *q, const fl
         load_decays<C>(g ? g + c.tok0 * g_tok + h : nullptr, g_stride, c.len, x);
         chunk_decays<C>(x, s_hi, s_lo);
     }
-    load_tile<DK>(s_q, PK, q + (c.tok0 * Hq + h / (H / Hq)) * DK, (int64_t)Hq * DK, c.len, nullptr);
-    load_tile<DK>(s_b, PK, k + (c.tok0 * Hk + h / (H / Hk)) * DK, (int64_t)Hk * DK, c.len, nullptr);
-    load_tile<DV>(s_v, PV, v + (c.tok0 * Hv + h / (H / Hv)) * DV, (int64_t)Hv * DV, c.len, nullptr);
+    load_tile<DK>(s_q, PK, q + (c.tok0 * Hq + h / (H / Hq)) * DK, (int64_t)Hq * DK, c.len);
+    load_tile<DK>(s_b, PK, k + (c.tok0 * Hk + h / (H / Hk)) * DK, (int64_t)Hk * DK, c.len);
+    load_tile<DV>(s_v, PV, v + (c.tok0 * Hv + h / (H / Hv)) * DV, (int64_t)Hv * DV, c.len);
     __syncthreads();
     {
         float x[4][4];
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(const float *q, const fl
     zero(acc);
     const float *S = states + (slot * H + h) * (int64_t)(DK * DV);
     for (int p = 0; p < DK; p += C) {  // the state, C rows at a time
-        load_tile<DV>(s_b, PV, S + (int64_t)p * DV, DV, C, nullptr);
+        load_tile<DV>(s_b, PV, S + (int64_t)p * DV, DV, C);
         __syncthreads();
         mm_nn<4, DV / 16, C>(acc, s_q + p, PK, s_b, PV);
         __syncthreads();
@@ -360,10 +358,10 @@ __global__ void __launch_bounds__(NT) linear_grads_kernel(grads_args A) {
         load_decays<C>(A.g ? A.g + c.tok0 * A.g_tok + h : nullptr, A.g_stride, c.len, x);
         chunk_decays<C>(x, s_hi, s_lo);
     }
-    load_tile<DK>(s_q, PK, (const float *)A.q + (c.tok0 * A.Hq + h / (H / A.Hq)) * DK, (int64_t)A.Hq * DK, c.len, nullptr);
-    load_tile<DK>(s_k, PK, (const float *)A.k + (c.tok0 * A.Hk + h / (H / A.Hk)) * DK, (int64_t)A.Hk * DK, c.len, nullptr);
-    load_tile<DV>(s_v, PV, (const float *)A.v + (c.tok0 * A.Hv + h / (H / A.Hv)) * DV, (int64_t)A.Hv * DV, c.len, nullptr);
-    load_tile<DV>(s_o, PV, (const float *)A.go + (c.tok0 * H + h) * DV, (int64_t)H * DV, c.len, nullptr);
+    load_tile<DK>(s_q, PK, (const float *)A.q + (c.tok0 * A.Hq + h / (H / A.Hq)) * DK, (int64_t)A.Hq * DK, c.len);
+    load_tile<DK>(s_k, PK, (const float *)A.k + (c.tok0 * A.Hk + h / (H / A.Hk)) * DK, (int64_t)A.Hk * DK, c.len);
+    load_tile<DV>(s_v, PV, (const float *)A.v + (c.tok0 * A.Hv + h / (H / A.Hv)) * DV, (int64_t)A.Hv * DV, c.len);
+    load_tile<DV>(s_o, PV, (const float *)A.go + (c.tok0 * H + h) * DV, (int64_t)H * DV, c.len);
     __syncthreads();
     const float scale = A.scale;
     {

@@ -620,8 +620,8 @@ linear_segments_tc_kernel(const __grid_constant__ maps tm, const __grid_constant
 // ---------------------------------------------------------------------------------------------------- launches
 // Chunks of a segment, 0 for one chain per sequence and head.  A chain has one SM to itself, so fewer chains than
 // half of the SMs leave the GPU idle; segments of at least two chunks are then cut until there is a CTA for every SM.
-// Measured, d = 128, cut and whole: 4096 tokens of 1 head 25 / 99 us, 32 heads 49 / 103, 76 heads 89 / 103, 96 heads
-// 107 / 104; 32 heads of 2048 tokens 30 / 54, 1024 21 / 29, 640 20.2 / 20.1, 512 19.9 / 17.2.
+// Measured, d = 128, cut and whole: 4096 tokens of 1 head 28 / 106 us, 32 heads 55 / 110, 76 heads 96 / 111, 96 heads
+// 154 / 112; 32 heads of 2048 tokens 33 / 59, 1024 24 / 33, 640 20 / 23, 512 22 / 20.
 static int64_t segment_chunks(int64_t T, int64_t N, int H) {
     const int64_t chains = N * H, chunks = (T + C - 1) / C;  // of all sequences together
     if (chains > 76 || chunks <= 4 * N) return 0;

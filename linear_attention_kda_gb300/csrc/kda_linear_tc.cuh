@@ -127,7 +127,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 // The i-th longest sequence of a batch; every thread of the block calls it.  Batches of up to SORTED sequences run
-// longest first (32 sequences x 32 heads of 64 to 8192 tokens: 629 us, as they come 665; 96 x 8: 569 and 672); ranks cost
+// longest first (32 sequences x 32 heads of 64 to 8192 tokens: 680 us, as they come 716; 96 x 8: 610 and 722); ranks cost
 // a scan of the lengths in every CTA, and longer batches even out by themselves.
 constexpr int SORTED = 128;
 __device__ __forceinline__ int64_t longest_first(const int32_t *cu, int64_t N, int64_t i, int *n_smem) {

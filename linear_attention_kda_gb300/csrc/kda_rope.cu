@@ -3,14 +3,15 @@
 // Angles.  An angle matters modulo one turn, and positions are integers, so a frequency is kept as turns per
 // position in 64-bit fixed point, F = round(freq / 2 pi * 2^64) mod 2^64, and the angle of position p is p * F mod
 // 2^64: one integer product, wrong by at most |p| / 2 units of 2^-64 turns (2^-34 turns at the largest int32), where
-// an fp32 product p * freq would be wrong by half a radian at a position of 2^23.  The high 32 bits, as a signed
-// fraction of a turn, go to sincospif.
+// an fp32 product p * freq would be wrong by half a radian at a position of 2^23.  The high 32 bits, a signed fraction of
+// a turn, are rounded to an fp32 (2^-26 turns at most, next to half a turn: 1e-7 radians, about what an fp32 sine is good
+// to) and go to sincospif.
 //
 // A CTA takes TB tokens: it first writes their sines and cosines (shared by all heads) to shared memory, then
 // streams the heads' rows in 16-byte pieces, four in flight per thread.  Bound by HBM: q and k read once and written
 // once; channels behind `rot` are copied, or left alone when the output is the input.  131071 tokens, 32 + 8 heads of
-// 128 bf16 channels, 64 of them turned: 405 us, 6.6 TB/s (one token and piece at a time: 601 us; with conversions and
-// index divisions element by element: 1065 us, bound by instructions).
+// 128 bf16 channels, 64 of them turned, into other tensors: 395 us, 6.8 TB/s (one token and piece at a time: 601 us; with
+// conversions and index divisions element by element: 1065 us, bound by instructions); in place 225 us.
 #include <math.h>
 
 #include <type_traits>
@@ -168,8 +169,8 @@ static void launch(const kda_rope_args *a, const turns &F, cudaStream_t stream) 
                    make_divisor((uint32_t)(turn + (copied ? (a->d - a->rot) / V : 0)))};
     };
     // Enough tokens to a CTA for a few rounds of its pieces, as long as every SM still has three CTAs.  bf16, 32 + 8
-    // heads of 128, into other tensors, by 1, 2, 4, 8 and 16 tokens: 131071 tokens 718, 502, 460, 424 and 424 us, 4096
-    // tokens 20.0, 17.3, 18.1, 17.8 and 18.2, 256 tokens 3.5, 3.5, -, 6.6 and 11.1.  (At most 2048 rows, or one token:
+    // heads of 128, 64 channels turned, into other tensors, by 1, 2, 4, 8 and 16 tokens: 131071 tokens 573, 432, 403, 394
+    // and 405 us, 4096 tokens 16.8, 14.0, 13.3, 14.4 and 18.1, 256 tokens 3.1, 3.3, 4.5, 7.0 and 12.1.  (At most 2048 rows, or one token:
     // quotient()'s range.)
     int64_t TB = 2048 / (a->Hq + a->Hk);
     if (TB > a->T / (3 * 152)) TB = a->T / (3 * 152);
@@ -184,8 +185,8 @@ static void launch(const kda_rope_args *a, const turns &F, cudaStream_t stream) 
 template <typename T>
 static void launch_t(const kda_rope_args *a, const turns &F, cudaStream_t stream) {
     // The widest vector (up to 16 bytes) that divides what a lane moves and that every row's address is a multiple
-    // of; single elements (pairs of them, interleaved) otherwise.  131071 tokens of 32 + 8 heads by 8, 4 and 1 elements: 460,
-    // 501 and 1091 us.
+    // of; single elements (pairs of them, interleaved) otherwise.  The same 131071 tokens by 8, 4 and 1 elements: 395, 498
+    // and 1111 us.
     auto fits = [&](int w) {
         const int64_t part = a->layout == KDA_ROPE_HALF ? a->rot / 2 : a->rot;
         if (part % w || (a->d - a->rot) % w || a->d % w) return false;
