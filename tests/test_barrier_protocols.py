@@ -153,3 +153,41 @@ def test_prefill_ends_whatever_gives_up(nc, can_time_out):
 def test_a_hardware_barrier_behind_a_wait_would_not_end():
     assert explore(*meeting(1, True), False) is None
     assert explore(*meeting(1, True), True) is not None
+
+
+# ------------------------------------------------------------------ prefill: all of a chain's barriers
+def prefill(nc, ragged):
+    """Loader, products, decays, stores and one worker of linear_fwd_tc_kernel on nc chunks, the last one short or whole."""
+    slot = lambda t: t % 4  # noqa: E731
+    load, mma, dec, store, work = [], [], [], [], []
+    for t in range(3 * nc):
+        if t >= 4:
+            load.append(("wait", ("free", slot(t)), t // 4 - 1))
+        load.append(("arrive", ("full", slot(t))))
+    full = lambda t: ("wait", ("full", slot(t)), t // 4)  # noqa: E731
+    for i in range(nc):
+        mma += ([("wait", "u_read", i - 1)] if i else []) + [full(3 * i), full(3 * i + 1), ("arrive", "x_done"), ("wait", "s_ready", i)]
+        mma += ([("wait", "o_read", i - 1)] if i else []) + [("arrive", "d_done"), ("arrive", ("free", slot(3 * i)))]
+        mma += [("wait", "k_ready", i), full(3 * i + 2), ("arrive", "u_done"), ("arrive", ("free", slot(3 * i + 1)))]
+        mma += [("wait", "p_ready", i), ("arrive", "o_done"), ("arrive", ("free", slot(3 * i + 2)))]
+        dec += ([("wait", ("dec_free", i % 2), i // 2 - 1)] if i >= 2 else []) + [("arrive", ("dec_ready", i % 2))]
+        if not (ragged and i == nc - 1):
+            store += [("wait", "o_staged", i), ("arrive", "o_stored")]
+    for i in range(nc + 1):
+        work += ([("wait", "u_done", i - 1)] if i else []) + ([("wait", ("dec_ready", i % 2), i // 2)] if i < nc else [])
+        if i < nc:
+            work += ([("arrive", "u_read")] if i else []) + [("arrive", "s_ready")]
+        if i:
+            work += ([("wait", "o_stored", i - 2)] if i > 1 else []) + [("wait", "o_done", i - 1), ("arrive", "o_read")]
+            work += [] if ragged and i == nc else [("arrive", "o_staged")]
+        if i < nc:
+            work += [("wait", "x_done", i)] + ([full(3 * i + 2)] if ragged and i == nc - 1 else []) + [("arrive", "k_ready")]
+            work += [("arrive", "x_read"), ("wait", "x_read", i), ("wait", "d_done", i), ("arrive", "p_ready"), ("arrive", ("dec_free", i % 2))]
+    roles = [load, mma, dec, store, work]
+    return roles, {s[1]: 1 for p in roles for s in p}
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("nc", [1, 2, 5])
+def test_prefill_never_misses_a_phase(nc, ragged):
+    assert explore(*prefill(nc, ragged), False) is None
