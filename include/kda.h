@@ -527,6 +527,253 @@ typedef struct {
 
 kda_status_t kda_rope(const kda_rope_args *args, struct CUstream_st *stream);
 
+/* ------------------------------------------------------------------ kda_scan
+ * The gated linear recurrence over channels, for the recurrent layers with a vector state that models place beside
+ * KDA layers: for every channel of a sequence
+ *     h_t = a_t h_{t-1} + c(a_t) Sigmoid(i_t) x_t,      a_t = exp(g_t),
+ * with the log-decay g from a logit z as in kda_gate (A_log and dt_bias per channel here),
+ *     KDA_SCAN_LOWER_BOUND   g = g_min Sigmoid(exp(A_log) (z + dt_bias))     (Eq. 5)
+ *     KDA_SCAN_SOFTPLUS      g = -exp(A_log) Softplus(z + dt_bias)
+ *     KDA_SCAN_SIGMOID       g = -exp(A_log) Sigmoid(z + dt_bias)
+ *     KDA_SCAN_LOG           g = z (A_log and dt_bias NULL)
+ * and what enters scaled by c = 1 (KDA_SCAN_INPUT_PLAIN), 1 - a (_COMPLEMENT: h is a mean of what entered) or
+ * sqrt(1 - a^2) (_NORM: of independent inputs, h keeps their variance; 0 where a >= 1).  The input gate i may be
+ * absent (factor 1).
+ *
+ * Values: g is at most 0 in use; greater ones (KDA_SCAN_LOG) are computed as given and may overflow.  A decay of 0
+ * (g = -inf, or so low that exp(g) is 0 in fp32) erases what the state held, infinities and NaN included; so does,
+ * for the states after them, a run of tokens whose whole decay is 0 in fp32.  A NaN or an infinity stays in its sequence and
+ * channel.  Arithmetic and states are fp32; a decay near 1 is kept as a - 1, so that what a long memory holds does not drift with the
+ * rounding of a; h is rounded once to dtype.
+ *
+ * Shapes: x, z, input_gate and h [T, D], any D; tokens of x, z and input_gate are *_stride elements apart (0: D,
+ * dense), so that slices of one projection can be read where they lie.  Tensors of dtype are aligned to their
+ * element at least (rows whose addresses and strides allow it move as wide vectors), states and parameters fp32 and 4-byte
+ * aligned.  Packing, cu_seqlens (checked on the device; sequences with a bad range are skipped and rows that belong
+ * to no sequence are left as they were), streams and errors are as for kda_linear_chunk_fwd.  Outputs may not overlap inputs,
+ * except that final_state may be initial_state.  An empty sequence's final state is its initial state.  The calls use no atomics on
+ * results: the same inputs give the same bits. */
+#define KDA_SCAN_LOWER_BOUND 0
+#define KDA_SCAN_SOFTPLUS 1
+#define KDA_SCAN_SIGMOID 2
+#define KDA_SCAN_LOG 3
+#define KDA_SCAN_INPUT_PLAIN 0
+#define KDA_SCAN_INPUT_COMPLEMENT 1
+#define KDA_SCAN_INPUT_NORM 2
+#define KDA_SCAN_CHECKPOINT 64     /* tokens from one checkpoint to the next */
+typedef struct {
+    int64_t T, N;                  /* tokens (all sequences packed), sequences (>= 1) */
+    int32_t D;                     /* channels, 1 .. 2^20 */
+    kda_dtype_t dtype;             /* dtype of x, z, input_gate and h */
+    int32_t gate_kind, input_scale;
+    float g_min;                   /* < 0; KDA_SCAN_LOWER_BOUND only */
+    const void *x, *z, *input_gate;
+    int64_t x_stride, z_stride, i_stride;
+    const float *A_log, *dt_bias;  /* [D] each, or NULL (zero) */
+    const int32_t *cu_seqlens;     /* [N + 1] device, or NULL for N sequences of T / N tokens */
+    const float *initial_state;    /* [N, D] or NULL (zero) */
+    float *final_state;            /* [N, D] or NULL */
+    float *checkpoints;            /* [T / 64 + N, D] or NULL: for kda_scan_bwd, the states that enter tokens 0, 64,
+                                      128, ... of every sequence; sequence n's begin in row cu_seqlens[n] / 64 + n, rows
+                                      between one sequence's and the next's are left as they were */
+    void *h;
+} kda_scan_args;
+
+/* Bytes of device scratch the two calls need for these sizes (0 on invalid sizes, or where none is needed). */
+size_t kda_scan_fwd_workspace_size(int64_t T, int64_t N, int32_t D, kda_dtype_t dtype);
+size_t kda_scan_bwd_workspace_size(int64_t T, int64_t N, int32_t D, kda_dtype_t dtype);
+
+/* The recurrence over whole sequences.  workspace: at least kda_scan_fwd_workspace_size() bytes, 256-byte aligned;
+ * its contents need no initialisation; calls that share one (captured graphs among them) must not overlap in time. */
+kda_status_t kda_scan_fwd(const kda_scan_args *args, void *workspace, size_t workspace_bytes,
+                          struct CUstream_st *stream);
+
+/* Gradients of kda_scan_fwd given dL/dh and optionally dL/dh_T, from its inputs and checkpoints.  With the adjoint
+ * lambda_t = dh_t + a_{t+1} lambda_{t+1}:
+ *     dx = c s lambda,  di = c x s (1 - s) lambda,  dg = (a h_{t-1} + dc/dg s x) lambda,  dh_0 = a_1 lambda_1,
+ * s = Sigmoid(i); dz, dA_log and ddt_bias follow from dg (dc/dg counts as 0 where c = sqrt(1 - a^2) is 0).  grad_x,
+ * grad_z and grad_input_gate are dense [T, D] and rounded once to dtype; parameters' gradients are sums over all
+ * tokens in fp32, in a fixed order. */
+typedef struct {
+    int64_t T, N;
+    int32_t D;
+    kda_dtype_t dtype;             /* dtype of x, z, input_gate, grad_h and their gradients */
+    int32_t gate_kind, input_scale;
+    float g_min;
+    const void *x, *z, *input_gate;
+    int64_t x_stride, z_stride, i_stride;
+    const float *A_log, *dt_bias;
+    const int32_t *cu_seqlens;
+    const float *checkpoints;      /* as kda_scan_fwd wrote them */
+    const void *grad_h;            /* [T, D] */
+    const float *grad_final_state; /* [N, D] or NULL (zero) */
+    void *grad_x, *grad_z;         /* [T, D] */
+    void *grad_input_gate;         /* [T, D]; NULL when input_gate is */
+    float *grad_A_log;             /* [D], or NULL to skip (not with KDA_SCAN_LOG) */
+    float *grad_dt_bias;           /* [D], or NULL to skip (not with KDA_SCAN_LOG) */
+    float *grad_initial_state;     /* [N, D], or NULL to skip */
+} kda_scan_bwd_args;
+
+kda_status_t kda_scan_bwd(const kda_scan_bwd_args *args, void *workspace, size_t workspace_bytes,
+                          struct CUstream_st *stream);
+
+/* One decode token per sequence: the recurrence once per (sequence, channel), the state updated in place.
+ * state_indices as for kda_linear_recurrent_step: -1 marks an unused row (nothing is read or written for it), and a
+ * row whose slot an earlier row has is skipped and sets KDA_ERR_BAD_STATE_INDEX. */
+typedef struct {
+    int64_t N;
+    int32_t D;
+    kda_dtype_t dtype;
+    int32_t gate_kind, input_scale;
+    float g_min;
+    const void *x, *z, *input_gate;    /* [N, D] */
+    int64_t x_stride, z_stride, i_stride;
+    const float *A_log, *dt_bias;
+    float *state;                      /* [num_slots, D] fp32 */
+    const int32_t *state_indices;      /* [N], or NULL (slot n) */
+    int64_t num_slots;                 /* 0 = N */
+    void *h;                           /* [N, D] */
+} kda_scan_step_args;
+
+kda_status_t kda_scan_step(const kda_scan_step_args *args, struct CUstream_st *stream);
+
+/* ------------------------------------------------------------ kda_short_conv
+ * The short causal convolution over each channel's last K tokens that Eq. 2 (section 2.1.1) puts in front of q, k and
+ * v (and recurrent blocks in front of kda_scan), with what follows it there:
+ *     p_t = bias + sum_j weight[:, j] x_{t-K+1+j},   s_t = Swish(p_t) or p_t,   y_t = s_t or L2Norm(s_t),
+ * L2Norm over each head of norm_dim channels, s / sqrt(sum s^2 + norm_eps).  Tokens before a sequence's first come
+ * from its history, the last K - 1 inputs (zero where there is none); the new history is what the next call or step
+ * continues from.  Arithmetic is fp32, y is rounded once to dtype, histories are exact copies of inputs.
+ *
+ * Shapes: x and y [T, D], any D (a multiple of norm_dim); x may have a token stride as in kda_scan; weight [D, K];
+ * histories [N, K - 1, D] in dtype, oldest token first.  Outputs may not overlap inputs, except that final_state may be
+ * initial_state.  Packing, alignment, errors and reproducibility as for kda_scan. */
+#define KDA_CONV_NONE 0
+#define KDA_CONV_SILU 1
+typedef struct {
+    int64_t T, N;
+    int32_t D;                     /* 1 .. 2^20 */
+    int32_t K;                     /* taps, 2 .. 4 */
+    kda_dtype_t dtype;             /* dtype of x, y and the histories */
+    int32_t activation;            /* KDA_CONV_NONE, KDA_CONV_SILU */
+    int32_t norm_dim;              /* 0 (no norm), 32, 64, 128 or 256 */
+    float norm_eps;                /* > 0 where there is a norm */
+    const void *x;
+    int64_t x_stride;
+    const float *weight;           /* [D, K], the last tap is the token's own */
+    const float *bias;             /* [D] or NULL */
+    const int32_t *cu_seqlens;
+    const void *initial_state;     /* [N, K - 1, D] or NULL (zero) */
+    void *final_state;             /* [N, K - 1, D] or NULL */
+    void *y;
+} kda_short_conv_args;
+
+kda_status_t kda_short_conv_fwd(const kda_short_conv_args *args, struct CUstream_st *stream);
+
+/* Gradients of kda_short_conv_fwd given dL/dy and optionally dL/d(final history); everything else is computed
+ * again.  grad_x is dense; the gradients of weight and bias are sums over all tokens in fp32, in a fixed order. */
+typedef struct {
+    int64_t T, N;
+    int32_t D, K;
+    kda_dtype_t dtype;
+    int32_t activation, norm_dim;
+    float norm_eps;
+    const void *x;
+    int64_t x_stride;
+    const float *weight, *bias;
+    const int32_t *cu_seqlens;
+    const void *initial_state;
+    const void *grad_y;            /* [T, D] */
+    const void *grad_final_state;  /* [N, K - 1, D] or NULL (zero) */
+    void *grad_x;                  /* [T, D] */
+    float *grad_weight;            /* [D, K], or NULL to skip */
+    float *grad_bias;              /* [D], or NULL to skip */
+    void *grad_initial_state;      /* [N, K - 1, D], or NULL to skip */
+} kda_short_conv_bwd_args;
+
+size_t kda_short_conv_bwd_workspace_size(int64_t T, int64_t N, int32_t D, int32_t K, kda_dtype_t dtype);
+kda_status_t kda_short_conv_bwd(const kda_short_conv_bwd_args *args, void *workspace, size_t workspace_bytes,
+                                struct CUstream_st *stream);
+
+/* One decode token per sequence: y from the slot's history and x, the history moved on by one token in place.
+ * state_indices as for kda_scan_step. */
+typedef struct {
+    int64_t N;
+    int32_t D, K;
+    kda_dtype_t dtype;
+    int32_t activation, norm_dim;
+    float norm_eps;
+    const void *x;                 /* [N, D] */
+    int64_t x_stride;
+    const float *weight, *bias;
+    void *state;                   /* [num_slots, K - 1, D] in dtype */
+    const int32_t *state_indices;
+    int64_t num_slots;
+    void *y;                       /* [N, D] */
+} kda_short_conv_step_args;
+
+kda_status_t kda_short_conv_step(const kda_short_conv_step_args *args, struct CUstream_st *stream);
+
+/* ------------------------------------------------------------ kda_block_norm
+ * What stands between one block of a layer and the next: the norm behind a block, its gate and its scale into the
+ * residual stream, and the norm in front of the next block, in one pass over the token's D channels:
+ *     r' = r + scale * Sigmoid(gate) * P(y),    P(y) = post_weight * y / sqrt(mean y^2 + eps), or y,
+ *     n  = pre_weight * r' / sqrt(mean r'^2 + eps).
+ * Each part may be absent: P (post_norm = 0), the gate, n (pre_norm = 0, behind the last block), or the block itself
+ * (y NULL: n of r alone, in front of the first block).  The gate's logits are per channel [T, D] or per token [T]; scale is one
+ * number or one per channel.  The residual stream may be fp32 beside bf16 blocks.  fp32 arithmetic; n is made from the unrounded r'.
+ * Dense tensors, D 1 .. 8192, aligned to their elements (wide vectors where addresses and D allow).  residual_out
+ * may be residual, normed may be y; no other output may overlap an input. */
+#define KDA_NORM_GATE_NONE 0
+#define KDA_NORM_GATE_CHANNEL 1
+#define KDA_NORM_GATE_TOKEN 2
+typedef struct {
+    int64_t T;
+    int32_t D;
+    kda_dtype_t dtype;             /* dtype of y, gate and normed */
+    kda_dtype_t residual_dtype;    /* dtype of the residual stream: dtype or KDA_F32 */
+    int32_t gate_kind, post_norm, pre_norm;
+    float eps;                     /* > 0 */
+    float scale;                   /* where scale_vec is NULL */
+    const float *scale_vec;        /* [D] or NULL */
+    const void *y;                 /* [T, D], or NULL: no block */
+    const void *gate;              /* [T, D], [T] or NULL */
+    const void *residual;          /* [T, D] */
+    const float *post_weight;      /* [D], or NULL (ones) */
+    const float *pre_weight;       /* [D], or NULL (ones) */
+    void *residual_out;            /* [T, D] (NULL without y) */
+    void *normed;                  /* [T, D] (NULL without pre_norm) */
+} kda_block_norm_args;
+
+kda_status_t kda_block_norm_fwd(const kda_block_norm_args *args, struct CUstream_st *stream);
+
+/* Gradients of kda_block_norm_fwd given those of r' and n (either may be NULL: zero); r' is computed again from the call's
+ * inputs.  grad_y, grad_gate and grad_residual are rounded once; the gradients of the weights and of scale_vec are
+ * sums over all tokens in fp32, in a fixed order.  grad_residual may be grad_residual_out and grad_y may be y or
+ * grad_normed; no other output may overlap an input. */
+typedef struct {
+    int64_t T;
+    int32_t D;
+    kda_dtype_t dtype, residual_dtype;
+    int32_t gate_kind, post_norm, pre_norm;
+    float eps, scale;
+    const float *scale_vec;
+    const void *y, *gate, *residual;
+    const float *post_weight, *pre_weight;
+    const void *grad_residual_out; /* [T, D] in residual_dtype, or NULL */
+    const void *grad_normed;       /* [T, D] in dtype, or NULL */
+    void *grad_y;                  /* [T, D] (NULL without y) */
+    void *grad_gate;               /* shape of gate (NULL without) */
+    void *grad_residual;           /* [T, D] */
+    float *grad_post_weight;       /* [D], or NULL to skip (NULL without post_norm) */
+    float *grad_pre_weight;        /* [D], or NULL to skip (NULL without pre_norm) */
+    float *grad_scale;             /* [D], or NULL to skip (NULL without y) */
+} kda_block_norm_bwd_args;
+
+size_t kda_block_norm_bwd_workspace_size(int64_t T, int32_t D, kda_dtype_t dtype);
+kda_status_t kda_block_norm_bwd(const kda_block_norm_bwd_args *args, void *workspace, size_t workspace_bytes,
+                                struct CUstream_st *stream);
+
 /* ------------------------------------------------------------------ errors */
 const char *kda_status_string(kda_status_t status);
 
@@ -544,8 +791,8 @@ int kda_abi_version(void);
 /* ------------------------------------------------------------- debug checks
  * Not an operation of the paper: optional checks for debugging a model.  With KDA_CHECK_FINITE set,
  * every entry point that writes results (kda_gate, kda_chunk_fwd and kda_chunk_fwd_static_ws,
- * kda_recurrent_step, kda_recurrent_replay, kda_output_gate, kda_chunk_bwd, the three kda_linear_* calls
- * and kda_rope where its outputs are dense) launches one more pass
+ * kda_recurrent_step, kda_recurrent_replay, kda_output_gate, kda_chunk_bwd, the three kda_linear_* calls,
+ * kda_rope where its outputs are dense, the kda_scan_*, kda_short_conv_* and kda_block_norm_* calls) launches one more pass
  * over what it wrote (outputs, final or updated states, gradients) that sets KDA_ERR_NUMERIC in the
  * device error word (kda_get_device_error) when any value is NaN or infinite; of a
  * kda_linear_recurrent_step, the rows and slots of its state_indices alone.  The pass reads those

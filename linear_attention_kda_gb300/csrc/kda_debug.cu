@@ -20,22 +20,24 @@ template <typename T> __device__ __forceinline__ bool not_finite(const uint4 &u)
     return bad;
 }
 
+template <typename T> __device__ __forceinline__ bool not_finite(const T *p) {
+    if (sizeof(T) == 4) return (*reinterpret_cast<const uint32_t *>(p) & 0x7F800000u) == 0x7F800000u;
+    return (*reinterpret_cast<const uint16_t *>(p) & 0x7F80u) == 0x7F80u;
+}
+
 // Grid-stride scan for a non-finite value: 16-byte loads over the 16-byte-aligned body, scalars for
-// the tail.  bf16 is checked on its bit pattern (exponent all ones).
+// the head and the tail.  bf16 is checked on its bit pattern (exponent all ones).
 template <typename T>
 __global__ void __launch_bounds__(256) check_finite_kernel(const T *__restrict__ p, int64_t n, int *err) {
     constexpr int PER = 16 / sizeof(T);
-    const int64_t nv = n / PER;
+    int64_t head = (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T);
+    if (head > n) head = n;
+    const int64_t nv = (n - head) / PER, first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     bool bad = false;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nv; i += stride) {
-        bad |= not_finite<T>(reinterpret_cast<const uint4 *>(p)[i]);
-    }
-    for (int64_t i = nv * PER + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
-        uint32_t x;
-        if (sizeof(T) == 4) x = reinterpret_cast<const uint32_t *>(p)[i] & 0x7F800000u, bad |= x == 0x7F800000u;
-        else x = reinterpret_cast<const uint16_t *>(p)[i] & 0x7F80u, bad |= x == 0x7F80u;
-    }
+    for (int64_t i = first; i < nv; i += stride) bad |= not_finite<T>(reinterpret_cast<const uint4 *>(p + head)[i]);
+    for (int64_t i = first; i < head; i += stride) bad |= not_finite<T>(p + i);
+    for (int64_t i = head + nv * PER + first; i < n; i += stride) bad |= not_finite<T>(p + i);
     if (__syncthreads_or(bad) && threadIdx.x == 0) set_error(err, KDA_ERR_NUMERIC);
 }
 
@@ -43,12 +45,17 @@ __global__ void __launch_bounds__(256) check_finite_kernel(const T *__restrict__
 template <typename T>
 __global__ void __launch_bounds__(256) check_finite_rows_kernel(const T *__restrict__ p, int64_t len, int64_t N, const int32_t *used,
                                                                 const int32_t *at, int64_t slots, int *err) {
+    const bool wide = len % (16 / (int)sizeof(T)) == 0 && ((uintptr_t)p & 15) == 0;
     const int64_t per_row = len / (16 / (int)sizeof(T)), stride = (int64_t)gridDim.x * blockDim.x;
     bool bad = false;
     for (int64_t n = blockIdx.y; n < N; n += gridDim.y) {
         if (used && (used[n] < 0 || used[n] >= slots)) continue;
-        const uint4 *row = reinterpret_cast<const uint4 *>(p + (at ? at[n] : n) * len);
-        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < per_row; i += stride) bad |= not_finite<T>(row[i]);
+        const T *row = p + (at ? at[n] : n) * len;
+        const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+        if (wide)
+            for (int64_t i = first; i < per_row; i += stride) bad |= not_finite<T>(reinterpret_cast<const uint4 *>(row)[i]);
+        else
+            for (int64_t i = first; i < len; i += stride) bad |= not_finite<T>(row + i);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) set_error(err, KDA_ERR_NUMERIC);
 }

@@ -11,7 +11,7 @@ void kda_profile_mark(int i, cudaStream_t stream);
 kda_status_t kda_cuda_status(cudaError_t e);
 
 // Debug checks (kda_set_debug_checks): the flags in force, and the scan that sets KDA_ERR_NUMERIC in
-// the device error word when [p, p + n) holds a NaN or an infinity (p 16-byte aligned).
+// the device error word when [p, p + n) holds a NaN or an infinity.
 int32_t kda_debug_flags();
 kda_status_t kda_check_finite(const void *p, int64_t n, kda_dtype_t dtype, cudaStream_t stream);
 
@@ -127,10 +127,25 @@ kda_status_t kda_linear_sum_parts(const kda_linear_bwd_args *a, const kda_row_pa
                                   const kda_row_parts &pv, const float *dg_slot, int64_t slots, cudaStream_t stream);
 kda_status_t kda_launch_linear_fwd(const kda_linear_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_linear_bwd(const kda_linear_bwd_args *a, void *ws, cudaStream_t stream);
-// kda_check_finite for N rows of `len` elements, `len` a multiple of 8 and p 16-byte aligned: of those whose used[n] (NULL:
-// all) lies in [0, slots), row at[n] of p (NULL: row n)
+// kda_check_finite for N rows of `len` elements: of those whose used[n] (NULL: all) lies in [0, slots), row at[n] of p
+// (NULL: row n)
 kda_status_t kda_check_finite_rows(const void *p, int64_t len, int64_t N, const int32_t *used, const int32_t *at, int64_t slots,
                                    kda_dtype_t dtype, cudaStream_t stream);
 kda_status_t kda_launch_linear_step(const kda_linear_step_args *a, cudaStream_t stream);
 kda_status_t kda_launch_state_copy(const kda_state_copy_args *a, cudaStream_t stream);
 kda_status_t kda_launch_rope(const kda_rope_args *a, cudaStream_t stream);
+
+// What stands around a recurrence in a layer: the gated recurrence over channels, the short convolution and the norms
+// around a block (kda_layer_api.cu checks the arguments; these launch).
+size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D);
+kda_status_t kda_launch_scan_fwd(const kda_scan_args *a, void *ws, cudaStream_t stream);
+size_t kda_scan_bwd_bytes(int64_t T, int64_t N, int D);
+kda_status_t kda_launch_scan_bwd(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream);
+kda_status_t kda_launch_scan_step(const kda_scan_step_args *a, cudaStream_t stream);
+kda_status_t kda_launch_short_conv_fwd(const kda_short_conv_args *a, cudaStream_t stream);
+size_t kda_short_conv_bwd_bytes(int64_t T, int64_t N, int D, int K);
+kda_status_t kda_launch_short_conv_bwd(const kda_short_conv_bwd_args *a, void *ws, cudaStream_t stream);
+kda_status_t kda_launch_short_conv_step(const kda_short_conv_step_args *a, cudaStream_t stream);
+kda_status_t kda_launch_block_norm_fwd(const kda_block_norm_args *a, cudaStream_t stream);
+size_t kda_block_norm_bwd_bytes(int64_t T, int D);
+kda_status_t kda_launch_block_norm_bwd(const kda_block_norm_bwd_args *a, void *ws, cudaStream_t stream);

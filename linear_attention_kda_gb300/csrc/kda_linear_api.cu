@@ -3,27 +3,13 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "kda_checks.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
+using namespace kda;
+
 namespace {
-
-bool dtype_ok(kda_dtype_t t) { return t == KDA_F32 || t == KDA_BF16; }
-int64_t dtype_size(kda_dtype_t t) { return t == KDA_BF16 ? 2 : 4; }
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-struct range {  // a tensor's bytes; absent ones overlap nothing
-    const void *p;
-    int64_t bytes;
-};
-bool overlap(const range &a, const range &b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
-}
-
-// Pools are below 2^48 bytes, so that no product of their sizes leaves 64 bits.
-bool pool_ok(int64_t slots, int64_t slot_bytes) { return slot_bytes == 0 || slots <= ((int64_t)1 << 48) / slot_bytes; }
 
 bool dim_ok(int32_t d) { return d == 64 || d == 128; }
 

@@ -37,7 +37,10 @@ EXPORTED = ["kda_gate", "kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_re
             "kda_selftest_bounded_wait", "kda_set_debug_checks", "kda_set_chunk_schedule",
             "kda_chunk_bwd_workspace_size_min", "kda_linear_chunk_fwd", "kda_linear_chunk_fwd_workspace_size",
             "kda_linear_chunk_bwd", "kda_linear_chunk_bwd_workspace_size", "kda_linear_recurrent_step",
-            "kda_state_copy", "kda_rope"]
+            "kda_state_copy", "kda_rope", "kda_scan_fwd", "kda_scan_fwd_workspace_size", "kda_scan_bwd",
+            "kda_scan_bwd_workspace_size", "kda_scan_step", "kda_short_conv_fwd", "kda_short_conv_bwd",
+            "kda_short_conv_bwd_workspace_size", "kda_short_conv_step", "kda_block_norm_fwd", "kda_block_norm_bwd",
+            "kda_block_norm_bwd_workspace_size"]
 STATIC_WORKSPACE_BYTES = 64 << 20
 
 _vp = ctypes.c_void_p
@@ -121,6 +124,59 @@ class RopeArgs(ctypes.Structure):
                 ("q_out_stride", _i64), ("k_out_stride", _i64)]
 
 
+_SCAN_INPUTS = [("x", _vp), ("z", _vp), ("input_gate", _vp), ("x_stride", _i64), ("z_stride", _i64), ("i_stride", _i64),
+                ("A_log", _vp), ("dt_bias", _vp)]
+_SCAN_SPEC = [("D", _i32), ("dtype", ctypes.c_int), ("gate_kind", _i32), ("input_scale", _i32), ("g_min", _f32)]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64)] + _SCAN_SPEC + _SCAN_INPUTS + [
+        ("cu_seqlens", _vp), ("initial_state", _vp), ("final_state", _vp), ("checkpoints", _vp), ("h", _vp)]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64)] + _SCAN_SPEC + _SCAN_INPUTS + [
+        ("cu_seqlens", _vp), ("checkpoints", _vp), ("grad_h", _vp), ("grad_final_state", _vp), ("grad_x", _vp), ("grad_z", _vp),
+        ("grad_input_gate", _vp), ("grad_A_log", _vp), ("grad_dt_bias", _vp), ("grad_initial_state", _vp)]
+
+
+class ScanStepArgs(ctypes.Structure):
+    _fields_ = [("N", _i64)] + _SCAN_SPEC + _SCAN_INPUTS + [("state", _vp), ("state_indices", _vp), ("num_slots", _i64), ("h", _vp)]
+
+
+_CONV_SPEC = [("D", _i32), ("K", _i32), ("dtype", ctypes.c_int), ("activation", _i32), ("norm_dim", _i32), ("norm_eps", _f32),
+              ("x", _vp), ("x_stride", _i64), ("weight", _vp), ("bias", _vp)]
+
+
+class ShortConvArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64)] + _CONV_SPEC + [("cu_seqlens", _vp), ("initial_state", _vp), ("final_state", _vp), ("y", _vp)]
+
+
+class ShortConvBwdArgs(ctypes.Structure):
+    _fields_ = [("T", _i64), ("N", _i64)] + _CONV_SPEC + [
+        ("cu_seqlens", _vp), ("initial_state", _vp), ("grad_y", _vp), ("grad_final_state", _vp), ("grad_x", _vp), ("grad_weight", _vp),
+        ("grad_bias", _vp), ("grad_initial_state", _vp)]
+
+
+class ShortConvStepArgs(ctypes.Structure):
+    _fields_ = [("N", _i64)] + _CONV_SPEC + [("state", _vp), ("state_indices", _vp), ("num_slots", _i64), ("y", _vp)]
+
+
+_NORM_SPEC = [("T", _i64), ("D", _i32), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int), ("gate_kind", _i32), ("post_norm", _i32),
+              ("pre_norm", _i32), ("eps", _f32), ("scale", _f32), ("scale_vec", _vp), ("y", _vp), ("gate", _vp), ("residual", _vp),
+              ("post_weight", _vp), ("pre_weight", _vp)]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = _NORM_SPEC + [("residual_out", _vp), ("normed", _vp)]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    _fields_ = _NORM_SPEC + [
+        ("grad_residual_out", _vp), ("grad_normed", _vp), ("grad_y", _vp), ("grad_gate", _vp), ("grad_residual", _vp),
+        ("grad_post_weight", _vp), ("grad_pre_weight", _vp), ("grad_scale", _vp)]
+
+
 class KDAError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = int(code)
@@ -182,16 +238,21 @@ def load_library(path: Optional[str] = None):
         L.kda_output_gate.argtypes = [ctypes.POINTER(OutputGateArgs), _vp]
         L.kda_output_gate.restype = ctypes.c_int
         # (arguments as packed bytes or by reference to their ctypes structures)
-        for name in ("kda_linear_chunk_fwd", "kda_linear_chunk_bwd"):
+        for name in ("kda_linear_chunk_fwd", "kda_linear_chunk_bwd", "kda_scan_fwd", "kda_scan_bwd", "kda_short_conv_bwd", "kda_block_norm_bwd"):
             getattr(L, name).argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
             getattr(L, name).restype = ctypes.c_int
-        for name in ("kda_linear_recurrent_step", "kda_state_copy", "kda_rope"):
+        for name in ("kda_linear_recurrent_step", "kda_state_copy", "kda_rope", "kda_scan_step", "kda_short_conv_fwd", "kda_short_conv_step",
+                     "kda_block_norm_fwd"):
             getattr(L, name).argtypes = [_vp, _vp]
             getattr(L, name).restype = ctypes.c_int
         L.kda_linear_chunk_fwd_workspace_size.argtypes = [_i64, _i64, _i32, _i32, _i32, ctypes.c_int]
         L.kda_linear_chunk_fwd_workspace_size.restype = ctypes.c_size_t
         L.kda_linear_chunk_bwd_workspace_size.argtypes = [_i64, _i64] + [_i32] * 6 + [ctypes.c_int]
         L.kda_linear_chunk_bwd_workspace_size.restype = ctypes.c_size_t
+        for name, sizes in (("kda_scan_fwd", [_i64, _i64, _i32]), ("kda_scan_bwd", [_i64, _i64, _i32]),
+                            ("kda_short_conv_bwd", [_i64, _i64, _i32, _i32]), ("kda_block_norm_bwd", [_i64, _i32])):
+            getattr(L, name + "_workspace_size").argtypes = sizes + [ctypes.c_int]
+            getattr(L, name + "_workspace_size").restype = ctypes.c_size_t
         L.kda_last_cuda_error.argtypes = []
         L.kda_last_cuda_error.restype = _i32
         _lib = L
@@ -733,6 +794,350 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
          _ROPE.pack(T, Hq, Hk, d, 2 * freqs.numel(), code, ROPE_LAYOUTS[layout], int(inverse), scale, positions.data_ptr(),
                     freqs.data_ptr(), _p(q), _p(k), _p(yq), _p(yk), sq, sk, oq, ok))
     return yq, yk
+
+
+# ---------------------------------------------------------------- gated recurrence over channels
+SCAN_GATES = {"lower_bound": 0, "softplus": 1, "sigmoid": 2, "log": 3}
+SCAN_INPUT_SCALES = {"none": 0, "complement": 1, "norm": 2}
+SCAN_CHECKPOINT = 64
+_SCAN = struct.Struct("@qqiiiifPPPqqqPPPPPPP")
+_SCAN_BWD = struct.Struct("@qqiiiifPPPqqq" + "P" * 12)
+_SCAN_STEP = struct.Struct("@qiiiifPPPqqqPPPPqP")
+_CONV = struct.Struct("@qqiiiiifPqPPPPPP")
+_CONV_BWD = struct.Struct("@qqiiiiifPq" + "P" * 10)
+_CONV_STEP = struct.Struct("@qiiiiifPqPPPPqP")
+_NORM = struct.Struct("@qiiiiiiff" + "P" * 8)
+_NORM_BWD = struct.Struct("@qiiiiiiff" + "P" * 14)
+assert [x.size for x in (_SCAN, _SCAN_BWD, _SCAN_STEP, _CONV, _CONV_BWD, _CONV_STEP, _NORM, _NORM_BWD)] == [ctypes.sizeof(x) for x in (
+    ScanArgs, ScanBwdArgs, ScanStepArgs, ShortConvArgs, ShortConvBwdArgs, ShortConvStepArgs, BlockNormArgs, BlockNormBwdArgs)]
+
+
+def _tokens(where, name, t, rows, D, dtype, device) -> int:
+    """Checks [rows, D] tokens that may lie a stride apart; returns the stride (0: dense)."""
+    if t.shape == (rows, D) and t.dtype is dtype and t.get_device() == device:
+        if t.is_contiguous():
+            return 0
+        if rows == 0 or (t.stride(1) == 1 or D == 1) and (rows == 1 or t.stride(0) >= D):
+            return t.stride(0) if rows > 1 else 0
+        raise ValueError(f"{where}: {name}'s channels must be dense, its tokens at most strided")
+    if t.shape != (rows, D):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {(rows, D)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, not {dtype}")
+    raise ValueError(f"{where}: {name} is not on the device of the others")
+
+
+def _scan_inputs(where, x, z, input_gate, A_log, dt_bias, gate, input_scale):
+    """(rows, D, dtype, device, dtype code, gate, input scale, strides) of a scan's inputs, checked."""
+    if gate not in SCAN_GATES:
+        raise ValueError(f"{where}: gate must be one of {sorted(SCAN_GATES)}")
+    if input_scale not in SCAN_INPUT_SCALES:
+        raise ValueError(f"{where}: input_scale must be one of {sorted(SCAN_INPUT_SCALES)}")
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x has shape [tokens, channels]")
+    (T, D), dt, dev = x.shape, x.dtype, x.get_device()
+    code = _dtype_code(x)
+    strides = (_tokens(where, "x", x, T, D, dt, dev), _tokens(where, "z", z, T, D, dt, dev),
+               0 if input_gate is None else _tokens(where, "input_gate", input_gate, T, D, dt, dev))
+    f32 = torch.float32
+    if (A_log is not None and _off(A_log, (D,), f32, dev)) or (dt_bias is not None and _off(dt_bias, (D,), f32, dev)):
+        _require(where, dev, (("A_log", A_log, (D,), f32), ("dt_bias", dt_bias, (D,), f32)))
+    return T, D, dt, dev, code, SCAN_GATES[gate], SCAN_INPUT_SCALES[input_scale], strides
+
+
+def scan_checkpoints(T: int, N: int, D: int, device=None) -> torch.Tensor:
+    """A buffer for the checkpoints that scan_fwd leaves for scan_bwd: fp32 [T // 64 + N, D]."""
+    return torch.empty((T // SCAN_CHECKPOINT + N, D), dtype=torch.float32, device=device or "cuda")
+
+
+def scan_fwd_workspace_size(T, N, D, dtype: torch.dtype) -> int:
+    """kda_scan_fwd_workspace_size (bytes; 0 on invalid sizes, and where none is needed)."""
+    return int(load_library().kda_scan_fwd_workspace_size(T, N, D, KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+
+
+def scan_bwd_workspace_size(T, N, D, dtype: torch.dtype) -> int:
+    """kda_scan_bwd_workspace_size (bytes; 0 on invalid sizes)."""
+    return int(load_library().kda_scan_bwd_workspace_size(T, N, D, KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+
+
+def scan_fwd(x, z, input_gate=None, *, A_log=None, dt_bias=None, gate: str = "softplus", g_min: float = -5.0, input_scale: str = "none",
+             cu_seqlens: Optional[torch.Tensor] = None, n_seq: int = 1, initial_state: Optional[torch.Tensor] = None,
+             output_final_state: bool = False, final_state: Optional[torch.Tensor] = None, checkpoints: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """kda_scan_fwd: the gated recurrence over channels, h_t = a_t h_{t-1} + c(a_t) sigmoid(input_gate_t) x_t, over whole
+    sequences.  Returns (h, final_state).
+
+    x, z, input_gate (may be None): [T, D], fp32 or bf16, views with a token stride allowed; a = exp(g) with g from z by
+    gate: "lower_bound" (g_min sigmoid(e^A_log (z + dt_bias))), "softplus" (-e^A_log softplus(z + dt_bias)), "sigmoid"
+    (-e^A_log sigmoid(z + dt_bias)) or "log" (z itself); c by input_scale: "none" (1), "complement" (1 - a) or "norm"
+    (sqrt(1 - a^2)).  A_log, dt_bias: fp32 [D]; states: fp32 [N, D]; checkpoints: a buffer of scan_checkpoints, filled
+    for scan_bwd."""
+    where, L, f32 = "scan_fwd", _lib or load_library(), torch.float32
+    T, D, dt, dev, code, gk, ik, strides = _scan_inputs(where, x, z, input_gate, A_log, dt_bias, gate, input_scale)
+    N = _n_sequences(where, cu_seqlens, n_seq)
+    kept = (T // SCAN_CHECKPOINT + N, D)
+    if (dev < 0 or (cu_seqlens is not None and _off(cu_seqlens, (N + 1,), torch.int32, dev))
+            or (initial_state is not None and _off(initial_state, (N, D), f32, dev))
+            or (final_state is not None and _off(final_state, (N, D), f32, dev))
+            or (checkpoints is not None and _off(checkpoints, kept, f32, dev)) or (out is not None and _off(out, (T, D), dt, dev))):
+        _require(where, dev, (("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, (N, D), f32),
+                              ("final_state", final_state, (N, D), f32), ("checkpoints", checkpoints, kept, f32), ("out", out, (T, D), dt)))
+    if out is None:
+        out = torch.empty((T, D), dtype=dt, device=x.device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, D), dtype=f32, device=x.device)
+    ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_scan_fwd_workspace_size(T, N, D, code), x.device)
+    _run("kda_scan_fwd", dev, L.kda_scan_fwd,
+         _SCAN.pack(T, N, D, code, gk, ik, g_min, _p(x), _p(z), _p(input_gate), *strides, _p(A_log), _p(dt_bias), _p(cu_seqlens),
+                    _p(initial_state), _p(final_state), _p(checkpoints), _p(out)), ws, ws_bytes)
+    return out, final_state
+
+
+def scan_bwd(x, z, input_gate, grad_h, checkpoints, *, A_log=None, dt_bias=None, gate: str = "softplus", g_min: float = -5.0,
+             input_scale: str = "none", cu_seqlens: Optional[torch.Tensor] = None, n_seq: int = 1,
+             grad_final_state: Optional[torch.Tensor] = None, param_grads: bool = True, state_grad: bool = True,
+             workspace: Optional[torch.Tensor] = None) -> dict:
+    """kda_scan_bwd: gradients of scan_fwd given grad_h [T, D] (and grad_final_state), with the checkpoints that scan_fwd
+    filled for the same inputs.  Returns a dict with x, z, input_gate (where there is one; dtype of x) and, when asked,
+    A_log, dt_bias (fp32 [D], not for gate "log") and initial_state (fp32 [N, D])."""
+    where, L, f32 = "scan_bwd", _lib or load_library(), torch.float32
+    T, D, dt, dev, code, gk, ik, strides = _scan_inputs(where, x, z, input_gate, A_log, dt_bias, gate, input_scale)
+    N = _n_sequences(where, cu_seqlens, n_seq)
+    kept = (T // SCAN_CHECKPOINT + N, D)
+    if (dev < 0 or _off(grad_h, (T, D), dt, dev) or _off(checkpoints, kept, f32, dev)
+            or (cu_seqlens is not None and _off(cu_seqlens, (N + 1,), torch.int32, dev))
+            or (grad_final_state is not None and _off(grad_final_state, (N, D), f32, dev))):
+        _require(where, dev, (("grad_h", grad_h, (T, D), dt), ("checkpoints", checkpoints, kept, f32),
+                              ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("grad_final_state", grad_final_state, (N, D), f32)))
+    empty = lambda *s, dtype=f32: torch.empty(s, dtype=dtype, device=x.device)  # noqa: E731
+    grads = {"x": empty(T, D, dtype=dt), "z": empty(T, D, dtype=dt)}
+    if input_gate is not None:
+        grads["input_gate"] = empty(T, D, dtype=dt)
+    if param_grads and gate != "log":
+        grads["A_log"], grads["dt_bias"] = empty(D), empty(D)
+    if state_grad:
+        grads["initial_state"] = empty(N, D)
+    ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_scan_bwd_workspace_size(T, N, D, code), x.device)
+    _run("kda_scan_bwd", dev, L.kda_scan_bwd,
+         _SCAN_BWD.pack(T, N, D, code, gk, ik, g_min, _p(x), _p(z), _p(input_gate), *strides, _p(A_log), _p(dt_bias), _p(cu_seqlens),
+                        _p(checkpoints), _p(grad_h), _p(grad_final_state), _p(grads["x"]), _p(grads["z"]), _p(grads.get("input_gate")),
+                        _p(grads.get("A_log")), _p(grads.get("dt_bias")), _p(grads.get("initial_state"))), ws, ws_bytes)
+    return grads
+
+
+def scan_step(x, z, input_gate, state, *, A_log=None, dt_bias=None, gate: str = "softplus", g_min: float = -5.0, input_scale: str = "none",
+              state_indices: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """kda_scan_step: one decode token per sequence of the gated recurrence over channels; `state` fp32 [slots, D] is
+    updated in place.  Options as scan_fwd with N rows; state_indices int32 [N] (-1: an unused row, left alone with its
+    row of the output).  Returns h [N, D]."""
+    where, L = "scan_step", _lib or load_library()
+    N, D, dt, dev, code, gk, ik, strides = _scan_inputs(where, x, z, input_gate, A_log, dt_bias, gate, input_scale)
+    slots = _slots(where, state, 2, (D,), torch.float32, dev, N, state_indices, out, dt)
+    if out is None:
+        out = torch.empty((N, D), dtype=dt, device=x.device)
+    _run("kda_scan_step", dev, L.kda_scan_step,
+         _SCAN_STEP.pack(N, D, code, gk, ik, g_min, _p(x), _p(z), _p(input_gate), *strides, _p(A_log), _p(dt_bias), _p(state),
+                         _p(state_indices), slots, _p(out)))
+    return out
+
+
+def _slots(where, state, dims, shape, dtype, dev, N, state_indices, out, out_dtype):
+    """Checks a step's pool [slots, *shape], indices and output [N, channels]; returns the number of slots."""
+    if state.dim() != dims:
+        raise ValueError(f"{where}: state has shape [slots, {', '.join(map(str, shape))}]")
+    slots, rows = state.shape[0], (N, shape[-1])
+    if (dev < 0 or _off(state, (slots,) + shape, dtype, dev) or (state_indices is not None and _off(state_indices, (N,), torch.int32, dev))
+            or (out is not None and _off(out, rows, out_dtype, dev))):
+        _require(where, dev, (("state", state, (slots,) + shape, dtype), ("state_indices", state_indices, (N,), torch.int32),
+                              ("out", out, rows, out_dtype)))
+    if N > 0 and slots < (1 if state_indices is not None else N):
+        raise ValueError(f"{where}: {slots} state slots for {N} sequences")
+    return slots
+
+
+# ---------------------------------------------------------------- short causal convolution
+CONV_ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def _conv_inputs(where, x, weight, bias, activation):
+    """(rows, D, taps, dtype, device, dtype code, activation, x's stride) of a convolution's inputs, checked."""
+    if activation not in CONV_ACTIVATIONS:
+        raise ValueError(f"{where}: activation must be one of {sorted(CONV_ACTIVATIONS)}")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError(f"{where}: x has shape [tokens, channels], weight [channels, taps]")
+    (T, D), K, dt, dev, f32 = x.shape, weight.shape[1], x.dtype, x.get_device(), torch.float32
+    code, stride = _dtype_code(x), _tokens(where, "x", x, T, D, x.dtype, dev)
+    if _off(weight, (D, K), f32, dev) or (bias is not None and _off(bias, (D,), f32, dev)):
+        _require(where, dev, (("weight", weight, (D, K), f32), ("bias", bias, (D,), f32)))
+    if not 2 <= K <= 4:
+        raise ValueError(f"{where}: {K} taps (2, 3 or 4 are supported)")
+    return T, D, K, dt, dev, code, CONV_ACTIVATIONS[activation], stride
+
+
+def short_conv_fwd(x, weight, bias=None, *, activation: str = "silu", norm_dim: int = 0, norm_eps: float = 1e-6,
+                   cu_seqlens: Optional[torch.Tensor] = None, n_seq: int = 1, initial_state: Optional[torch.Tensor] = None,
+                   output_final_state: bool = False, final_state: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """kda_short_conv_fwd: the causal convolution of each channel with its last K inputs, SiLU (activation "silu" or
+    "none") and, with norm_dim, the L2 norm of every head of norm_dim channels (Eq. 2 without projections).
+    Returns (y, final_state).
+
+    x: [T, D], fp32 or bf16, a view with a token stride allowed; weight: fp32 [D, K], the last tap is the token's own; bias: fp32 [D]
+    or None; histories, the K - 1 inputs before a sequence's first and up to its last token: [N, K - 1, D] in x's dtype."""
+    where, L = "short_conv_fwd", _lib or load_library()
+    T, D, K, dt, dev, code, act, stride = _conv_inputs(where, x, weight, bias, activation)
+    N = _n_sequences(where, cu_seqlens, n_seq)
+    hist = (N, K - 1, D)
+    if (dev < 0 or (cu_seqlens is not None and _off(cu_seqlens, (N + 1,), torch.int32, dev)) or (initial_state is not None and _off(initial_state, hist, dt, dev))
+            or (final_state is not None and _off(final_state, hist, dt, dev)) or (out is not None and _off(out, (T, D), dt, dev))):
+        _require(where, dev, (("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, hist, dt),
+                              ("final_state", final_state, hist, dt), ("out", out, (T, D), dt)))
+    if out is None:
+        out = torch.empty((T, D), dtype=dt, device=x.device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(hist, dtype=dt, device=x.device)
+    _run("kda_short_conv_fwd", dev, L.kda_short_conv_fwd,
+         _CONV.pack(T, N, D, K, code, act, norm_dim, norm_eps, _p(x), stride, _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
+                    _p(final_state), _p(out)))
+    return out, final_state
+
+
+def short_conv_bwd_workspace_size(T, N, D, K, dtype: torch.dtype) -> int:
+    """kda_short_conv_bwd_workspace_size (bytes; 0 on invalid sizes)."""
+    return int(load_library().kda_short_conv_bwd_workspace_size(T, N, D, K, KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+
+
+def short_conv_bwd(x, weight, bias, grad_y, *, activation: str = "silu", norm_dim: int = 0, norm_eps: float = 1e-6,
+                   cu_seqlens: Optional[torch.Tensor] = None, n_seq: int = 1, initial_state: Optional[torch.Tensor] = None,
+                   grad_final_state: Optional[torch.Tensor] = None, param_grads: bool = True, state_grad: bool = True,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """kda_short_conv_bwd: gradients of short_conv_fwd given grad_y [T, D] (and grad_final_state).  Returns a dict with x
+    and, when asked, weight and bias (fp32; bias where there is one) and initial_state (dtype of x)."""
+    where, L = "short_conv_bwd", _lib or load_library()
+    T, D, K, dt, dev, code, act, stride = _conv_inputs(where, x, weight, bias, activation)
+    N = _n_sequences(where, cu_seqlens, n_seq)
+    hist = (N, K - 1, D)
+    if (dev < 0 or _off(grad_y, (T, D), dt, dev) or (cu_seqlens is not None and _off(cu_seqlens, (N + 1,), torch.int32, dev))
+            or (initial_state is not None and _off(initial_state, hist, dt, dev))
+            or (grad_final_state is not None and _off(grad_final_state, hist, dt, dev))):
+        _require(where, dev, (("grad_y", grad_y, (T, D), dt), ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32),
+                              ("initial_state", initial_state, hist, dt), ("grad_final_state", grad_final_state, hist, dt)))
+    empty = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device=x.device)  # noqa: E731
+    grads = {"x": empty(T, D, dtype=dt)}
+    if param_grads:
+        grads["weight"] = empty(D, K)
+        if bias is not None:
+            grads["bias"] = empty(D)
+    if state_grad:
+        grads["initial_state"] = empty(*hist, dtype=dt)
+    ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_short_conv_bwd_workspace_size(T, N, D, K, code), x.device)
+    _run("kda_short_conv_bwd", dev, L.kda_short_conv_bwd,
+         _CONV_BWD.pack(T, N, D, K, code, act, norm_dim, norm_eps, _p(x), stride, _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
+                        _p(grad_y), _p(grad_final_state), _p(grads["x"]), _p(grads.get("weight")), _p(grads.get("bias")),
+                        _p(grads.get("initial_state"))), ws, ws_bytes)
+    return grads
+
+
+def short_conv_step(x, weight, bias, state, *, activation: str = "silu", norm_dim: int = 0, norm_eps: float = 1e-6,
+                    state_indices: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """kda_short_conv_step: one decode token per sequence; `state` [slots, K - 1, D] (x's dtype), the histories, moves on by
+    one token in place.  Options as short_conv_fwd with N rows; state_indices int32 [N] (-1: an unused row, left alone with
+    its row of the output).  Returns y [N, D]."""
+    where, L = "short_conv_step", _lib or load_library()
+    N, D, K, dt, dev, code, act, stride = _conv_inputs(where, x, weight, bias, activation)
+    slots = _slots(where, state, 3, (K - 1, D), dt, dev, N, state_indices, out, dt)
+    if out is None:
+        out = torch.empty((N, D), dtype=dt, device=x.device)
+    _run("kda_short_conv_step", dev, L.kda_short_conv_step,
+         _CONV_STEP.pack(N, D, K, code, act, norm_dim, norm_eps, _p(x), stride, _p(weight), _p(bias), _p(state), _p(state_indices), slots,
+                         _p(out)))
+    return out
+
+
+# ---------------------------------------------------------------- norms around a block
+def _norm_inputs(where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm, more):
+    """(T, D, dtype, device, code, residual code, gate kind, post_norm, scale, scale vector) of a block norm's inputs, checked with
+    `more`: (name, tensor or None, which shape and dtype: "res", "tok" or "gate")."""
+    if residual.dim() != 2:
+        raise ValueError(f"{where}: residual has shape [tokens, channels]")
+    if y is None and (gate is not None or post_weight is not None or not pre_norm or isinstance(scale, torch.Tensor)):
+        raise ValueError(f"{where}: without y there is a norm in front of the next block alone")
+    (T, D), rt, dev, f32 = residual.shape, residual.dtype, residual.get_device(), torch.float32
+    dt = next((t.dtype for t in (y,) + tuple(t for n, t, k in more if k == "tok") if t is not None), rt)
+    code = KDA_BF16 if dt is torch.bfloat16 else KDA_F32 if dt is f32 else _dtype_code(y)
+    vec = scale if isinstance(scale, torch.Tensor) else None
+    kind = 0 if gate is None else 2 if gate.dim() == 1 else 1
+    gs = (T,) if kind == 2 else (T, D)
+    shapes = {"res": ((T, D), rt), "tok": ((T, D), dt), "gate": (gs, dt)}
+    for name, t, shape, dtype in (("residual", residual, (T, D), rt), ("y", y, (T, D), dt), ("gate", gate, gs, dt),
+                                  ("post_weight", post_weight, (D,), f32), ("pre_weight", pre_weight, (D,), f32), ("scale", vec, (D,), f32)):
+        if t is not None and _off(t, shape, dtype, dev) or dev < 0:
+            _require(where, dev, ((name, t, shape, dtype),))
+    for name, t, k in more:
+        if t is not None and _off(t, *shapes[k], dev):
+            _require(where, dev, ((name, t) + shapes[k],))
+    return (T, D, dt, dev, code, _dtype_code(residual), kind, int(post_norm and y is not None), 1.0 if vec is not None else float(scale), vec)
+
+
+def block_norm_fwd(y, residual, gate=None, *, post_weight=None, pre_weight=None, scale=1.0, post_norm: bool = True, pre_norm: bool = True,
+                   eps: float = 1e-6, residual_out: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None):
+    """kda_block_norm_fwd: what stands between two blocks, r' = residual + scale * sigmoid(gate) * RMSNorm(y) and n =
+    RMSNorm(r').  Returns (r', n).
+
+    y: [T, D], the block's output (fp32 or bf16), or None in front of the first block (then r' is residual itself);
+    residual: [T, D], y's dtype or fp32; gate: logits [T, D] or [T] in y's dtype, or None; post_weight, pre_weight: fp32 [D]
+    or None (ones); scale: a number or fp32 [D].  post_norm=False adds y without its norm, pre_norm=False leaves n out
+    (None).  residual_out=residual and normed=y work in place."""
+    where, L = "block_norm_fwd", _lib or load_library()
+    T, D, dt, dev, code, rcode, kind, post, scale, vec = _norm_inputs(
+        where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm,
+        (("normed", normed, "tok"), ("residual_out", residual_out, "res")))
+    if y is None:
+        if residual_out is not None:
+            raise ValueError(f"{where}: without y the residual stream stays as it is")
+        out = None
+    else:
+        out = torch.empty_like(residual) if residual_out is None else residual_out
+    if not pre_norm:
+        normed = None
+    elif normed is None:
+        normed = torch.empty((T, D), dtype=dt, device=residual.device)
+    _run("kda_block_norm_fwd", dev, L.kda_block_norm_fwd,
+         _NORM.pack(T, D, code, rcode, kind, post, int(pre_norm), eps, scale, _p(vec), _p(y), _p(gate), _p(residual), _p(post_weight),
+                    _p(pre_weight), _p(out), _p(normed)))
+    return (residual if y is None else out), normed
+
+
+def block_norm_bwd_workspace_size(T, D, dtype: torch.dtype) -> int:
+    """kda_block_norm_bwd_workspace_size (bytes; 0 on invalid sizes)."""
+    return int(load_library().kda_block_norm_bwd_workspace_size(T, D, KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+
+
+def block_norm_bwd(y, residual, gate, grad_residual, grad_normed, *, post_weight=None, pre_weight=None, scale=1.0, post_norm: bool = True,
+                   pre_norm: bool = True, eps: float = 1e-6, param_grads: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """kda_block_norm_bwd: gradients of block_norm_fwd given those of r' (grad_residual) and n (grad_normed); either may be
+    None (zero).  Returns a dict with residual and, where the call has them, y, gate and (param_grads) post_weight,
+    pre_weight and scale (fp32 [D]; scale where it is a vector)."""
+    where, L = "block_norm_bwd", _lib or load_library()
+    if grad_normed is not None and not pre_norm:
+        raise ValueError(f"{where}: grad_normed without pre_norm")
+    T, D, dt, dev, code, rcode, kind, post, scale, vec = _norm_inputs(
+        where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm,
+        (("grad_normed", grad_normed, "tok"), ("grad_residual", grad_residual, "res")))
+    grads = {"residual": torch.empty_like(residual)}
+    if y is not None:
+        grads["y"] = torch.empty_like(y)
+    if gate is not None:
+        grads["gate"] = torch.empty_like(gate)
+    if param_grads:
+        for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight), ("scale", vec)):
+            if w is not None:
+                grads[name] = torch.empty_like(w)
+    ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_block_norm_bwd_workspace_size(T, D, code), residual.device)
+    _run("kda_block_norm_bwd", dev, L.kda_block_norm_bwd,
+         _NORM_BWD.pack(T, D, code, rcode, kind, post, int(pre_norm), eps, scale, _p(vec), _p(y), _p(gate), _p(residual), _p(post_weight),
+                        _p(pre_weight), _p(grad_residual), _p(grad_normed), _p(grads.get("y")), _p(grads.get("gate")), _p(grads["residual"]),
+                        _p(grads.get("post_weight")), _p(grads.get("pre_weight")), _p(grads.get("scale"))), ws, ws_bytes)
+    return grads
 
 
 def selftest_bounded_wait(device=None) -> tuple:

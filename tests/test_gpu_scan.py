@@ -1,0 +1,393 @@
+"""GPU tests of the gated recurrence over channels (sequences, gradients, single tokens) against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_kda_gb300 import kda
+from tests import layer_util as U
+
+pytestmark = pytest.mark.gpu
+DTYPES = ("f32", "bf16")
+
+
+def _no_error():
+    torch.cuda.synchronize()
+    assert kda.get_device_error() == 0
+
+
+def _how(x):
+    return dict(A_log=x["A_log"], dt_bias=x["dt_bias"], gate=x["gate"], input_scale=x["input_scale"], cu_seqlens=x["cu_seqlens"])
+
+
+def _fwd(d, **kw):
+    x = U.to(d)
+    keep = torch.full((d["x"].shape[0] // 64 + len(d["lens"]), d["D"]), float("nan"), device="cuda")
+    h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, checkpoints=keep, **_how(x), **kw)
+    return h, last, keep
+
+
+def _bwd(d, keep, **kw):
+    x = U.to(d)
+    return kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, grad_final_state=x["grad_final_state"], **_how(x), **kw)
+
+
+def _check_fwd(d, got):
+    _no_error()
+    want, size, n = U.scan_ref(d), U.scan_ref(d, True), U.scan_roundings(d)
+    U.close("h", got[0], want[0], size[0], n, U.HALF[d["dtype"]])
+    U.close("final_state", got[1], want[1], size[1], n, U.U32)
+    held = ~np.isnan(want[2])
+    assert (np.isnan(U.f64(got[2])) == ~held).all()  # rows without a checkpoint are left as they were
+    U.close("checkpoints", got[2].cpu()[torch.from_numpy(held)], want[2][held], size[2][held], n, U.U32)
+
+
+def _check_bwd(d, got):
+    _no_error()
+    # states and adjoints both carry a scan's roundings, parameters' gradients those of a sum over all tokens as well
+    want, size, n = U.scan_grads_ref(d), U.scan_grads_ref(d, True), 2 * U.scan_roundings(d)
+    assert set(got) == {"x", "z", "initial_state"} | ({"input_gate"} if d["input_gate"] is not None else set()) | (
+        set() if d["gate"] == "log" else {"A_log", "dt_bias"})
+    for k in got:
+        par = k in ("A_log", "dt_bias")
+        U.close(k, got[k], want[k], size[k], n + (d["x"].shape[0] if par else 0), U.U32 if par or k == "initial_state" else U.HALF[d["dtype"]])
+
+
+CASES = [(t, g, i, {}) for t in DTYPES for g in U.GATES for i in U.INPUTS] + \
+        [(t, "softplus", "norm", kw) for t in DTYPES for kw in (dict(gated=False), dict(params=False), dict(state=False))]
+
+
+@pytest.mark.parametrize("dtype,gate,input_scale,kw", CASES)
+def test_varlen(dtype, gate, input_scale, kw):
+    d = U.scan_batch(U.LENS, 136, dtype, 1, gate=gate, input_scale=input_scale, **kw)
+    r = _fwd(d)
+    _check_fwd(d, r)
+    _check_bwd(d, _bwd(d, r[2]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [1, 2, 3, 7, 8, 31, 33, 64, 100, 127, 130, 260, 1032])
+def test_widths(dtype, D):
+    d = U.scan_batch([70, 5, 129], D, dtype, D, gate="sigmoid", input_scale="norm")
+    r = _fwd(d)
+    _check_fwd(d, r)
+    _check_bwd(d, _bwd(d, r[2]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens", [[1], [20000], [1023, 1025], [1, 4097, 1024], [2] * 300, [64] * 40])
+def test_lengths(dtype, lens):
+    d = U.scan_batch(lens, 8, dtype, len(lens), gate="lower_bound", input_scale="complement")
+    r = _fwd(d)
+    _check_fwd(d, r)
+    _check_bwd(d, _bwd(d, r[2]))
+
+
+def test_equal_lengths_without_cu_seqlens():
+    d = U.scan_batch([50] * 6, 24, "f32", 2)
+    r = _fwd(d)
+    x = U.to(d)
+    how = {**_how(x), "cu_seqlens": None, "n_seq": 6}
+    h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, **how)
+    _no_error()
+    assert torch.equal(h, r[0]) and torch.equal(last, r[1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_empty_batch(dtype):
+    d = U.scan_batch([0, 0, 0], 40, dtype, 3)
+    h, last, keep = _fwd(d)
+    g = _bwd(d, keep)
+    _no_error()
+    assert h.shape == (0, 40) and torch.equal(last.cpu(), d["initial_state"]) and torch.equal(g["initial_state"].cpu(), d["grad_final_state"])
+    assert (g["A_log"] == 0).all() and (g["dt_bias"] == 0).all()
+
+
+def test_slow_decays_do_not_drift():
+    """A state that remembers 10,000 tokens, fed a constant: 1 / (1 - a) in the end.  Every 8 tokens or more share one
+    decay of the state before them, so it goes through 2 * 60000 / 8 roundings with weights that sum to 2 * 10000 / 8."""
+    T, g = 60000, -1e-4
+    z = torch.full((T, 16), g, device="cuda")
+    _, last = kda.scan_fwd(torch.ones_like(z), z, gate="log", output_final_state=True)
+    _no_error()
+    a = np.exp(np.float64(np.float32(g)))
+    want = (1 - a ** T) / (1 - a)
+    assert abs(float(last[0, 0]) / want - 1) <= 2 * 10000 / 8 * U.U32, float(last[0, 0]) / want - 1
+    assert (last == last[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_erasing_decays(dtype):
+    """exp(g) = 0 leaves nothing of the state, infinities and NaN included; -inf and -200 are such decays."""
+    d = U.scan_batch([100, 80], 24, dtype, 4, gate="log")
+    d["z"][0, :] = -float("inf")
+    d["z"][100, :] = -200.0
+    d["z"][57, ::2] = -float("inf")
+    clean = {**d, "initial_state": d["initial_state"].clone()}
+    d["initial_state"][0, :8], d["initial_state"][1, 8:16] = float("nan"), float("inf")
+    r = _fwd(d)
+    _no_error()
+    want, size, n = U.scan_ref(clean), U.scan_ref(clean, True), U.scan_roundings(d)
+    U.close("h", r[0], want[0], size[0], n, U.HALF[dtype])
+    U.close("final_state", r[1], want[1], size[1], n, U.U32)
+    g = _bwd(clean, _fwd(clean)[2])
+    _check_bwd(clean, g)
+    assert (g["initial_state"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_nan_stays_in_its_channel(dtype):
+    d = U.scan_batch([200, 150], 40, dtype, 5, gate="softplus", input_scale="norm")
+    h0, last0, keep0 = _fwd(d)
+    g0 = _bwd(d, keep0)
+    d["x"][77, 13], d["z"][250, 20] = float("nan"), float("nan")
+    h, last, keep = _fwd(d)
+    g = _bwd(d, keep)
+    _no_error()
+    bad = torch.zeros((350, 40), dtype=torch.bool)
+    bad[77:200, 13], bad[250:, 20] = True, True
+    assert torch.equal(h.isnan().cpu(), bad) and torch.equal(h.cpu()[~bad], h0.cpu()[~bad])
+    assert torch.equal(last.isnan().cpu(), torch.stack((bad[199], bad[349])))
+    other = torch.ones(40, dtype=torch.bool)
+    other[13] = other[20] = False
+    for k in g:
+        assert torch.equal(g[k].cpu()[..., other], g0[k].cpu()[..., other]), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_views(dtype):
+    """Slices of one projection, rows that begin at odd elements, the final state over the initial one."""
+    d = U.scan_batch([90, 200], 64, dtype, 6)
+    r = _fwd(d)
+    g = _bwd(d, r[2])
+    x = U.to(d)
+    for pad in (0, 3):
+        wide = torch.zeros((290, 3 * 64 + pad), dtype=U.DT[dtype], device="cuda")
+        v = [wide[:, pad + 64 * k:pad + 64 * (k + 1)] for k in range(3)]
+        for a, b in zip(v, ("x", "z", "input_gate")):
+            a.copy_(x[b])
+        state, keep = x["initial_state"].clone(), torch.full_like(r[2], float("nan"))
+        h, last = kda.scan_fwd(*v, initial_state=state, final_state=state, checkpoints=keep, **_how(x))
+        g2 = kda.scan_bwd(*v, x["grad_h"], keep, grad_final_state=x["grad_final_state"], **_how(x))
+        _no_error()
+        assert torch.equal(h, r[0]) and torch.equal(last, r[1]) and last is state
+        assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_outputs_at_odd_elements():
+    d = U.scan_batch([90, 200], 64, "bf16", 6)
+    r = _fwd(d)
+    buf = torch.zeros(290 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    for k in (1, 4):
+        out = buf[k:k + 290 * 64].view(290, 64)
+        buf.zero_()
+        h = _fwd(d, out=out)[0]
+        _no_error()
+        assert h.data_ptr() == out.data_ptr() and torch.equal(h, r[0])
+        assert (buf[:k] == 0).all() and (buf[k + 290 * 64:] == 0).all()
+
+
+def test_same_bits_again():
+    d = U.scan_batch([3000, 1, 700], 200, "bf16", 7, input_scale="norm")
+    a = _fwd(d)
+    g = _bwd(d, a[2])
+    for _ in range(3):
+        b = _fwd(d)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(a[2].nan_to_num(), b[2].nan_to_num())
+        g2 = _bwd(d, a[2])
+        assert all(torch.equal(g[k], g2[k]) for k in g)
+    _no_error()
+
+
+def test_a_sequence_does_not_depend_on_its_neighbours():
+    """The same bits alone and in a batch whose tokens before it pass 2^32 elements."""
+    D, T0, T1 = 8192, 530000, 200
+    d = U.scan_batch([T1], D, "bf16", 8, gated=False)
+    x = U.to(d)
+    h1, last1 = kda.scan_fwd(x["x"], x["z"], initial_state=x["initial_state"], output_final_state=True, **_how(x))
+    big = [torch.zeros((T0 + T1, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    big[0][T0:], big[1][T0:] = x["x"], x["z"]
+    state = torch.cat((torch.zeros_like(x["initial_state"]), x["initial_state"]))
+    how = {**_how(x), "cu_seqlens": U.cu([T0, T1]).cuda()}
+    h2, last2 = kda.scan_fwd(*big, initial_state=state, output_final_state=True, **how)
+    _no_error()
+    assert torch.equal(h2[T0:], h1) and torch.equal(last2[1:], last1) and (h2[:T0:1000] == 0).all() and (last2[0] == 0).all()
+
+
+def test_bad_cu_seqlens():
+    d = U.scan_batch([64, 100, 36], 40, "bf16", 9)
+    x = U.to(d)
+    good = _fwd(d)
+    for bad in ([0, 64, 50, 200], [0, 64, 300, 200], [0, 64, 164, 190], [5, 64, 164, 200], [0, -7, 164, 200]):
+        how = {**_how(x), "cu_seqlens": torch.tensor(bad, dtype=torch.int32).cuda()}
+        out = torch.full_like(x["x"], 7.0)
+        keep = torch.zeros((200 // 64 + 3, 40), device="cuda")
+        kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, checkpoints=keep, out=out, **how)
+        torch.cuda.synchronize()
+        assert kda.get_device_error() == 7, bad
+        if bad[1] == 64 and bad[0] == 0 and bad[2] >= 64:
+            assert torch.equal(out[:64], good[0][:64])
+        kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, **how)
+        torch.cuda.synchronize()
+        assert kda.get_device_error() == 7, bad
+
+
+def test_streams_and_graphs():
+    """Another stream; two captured graphs that share a workspace, replayed in turn with other contents."""
+    d1, d2 = U.scan_batch([2000, 300], 72, "bf16", 10), U.scan_batch([700] * 3, 72, "bf16", 11, gate="sigmoid", input_scale="norm")
+    want = [(_fwd(d), None) for d in (d1, d2)]
+    want = [(f, _bwd(d, f[2])) for d, (f, _) in zip((d1, d2), want)]
+    need = max(max(kda.scan_fwd_workspace_size(2300, 3, 72, torch.bfloat16), kda.scan_bwd_workspace_size(2300, 3, 72, torch.bfloat16)), 256)
+    ws, stream, runs = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    for d in (d1, d2):
+        x = U.to(d)
+        src = {k: x[k].clone() for k in ("x", "z", "input_gate")}
+        keep = torch.zeros((d["x"].shape[0] // 64 + len(d["lens"]), 72), device="cuda")
+
+        def call(x=x, keep=keep):
+            h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, checkpoints=keep,
+                                   workspace=ws, **_how(x))
+            return h, last, kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, grad_final_state=x["grad_final_state"], workspace=ws, **_how(x))
+
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = call()
+        runs.append((graph, x, src, out))
+    for turn in range(3):
+        for (graph, x, src, out), (f, g) in zip(runs, want):
+            for k in src:
+                x[k].copy_(src[k] if turn != 1 else torch.zeros_like(src[k]))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], f[0]) == (turn != 1)
+            if turn != 1:
+                assert torch.equal(out[1], f[1]) and all(torch.equal(out[2][k], g[k]) for k in g)
+    _no_error()
+
+
+def test_finite_checks():
+    d = U.scan_batch([100, 30], 33, "bf16", 12)
+    kda.set_debug_checks(kda.CHECK_FINITE)
+    try:
+        r = _fwd(d)
+        assert kda.get_device_error() == 0
+        _bwd(d, r[2])
+        assert kda.get_device_error() == 0
+        d["x"][120, 32] = float("inf")
+        r = _fwd(d)
+        assert kda.get_device_error() == 12
+        _bwd(d, r[2])
+        assert kda.get_device_error() == 12
+    finally:
+        kda.set_debug_checks(0)
+
+
+# ---------------------------------------------------------------- single tokens
+def _step_batch(N, D, dtype, seed, slots, **kw):
+    d = U.scan_batch([1] * N, D, dtype, seed, **kw)
+    g = torch.Generator().manual_seed(seed)
+    pool = torch.randn((slots, D), generator=g)
+    idx = torch.randperm(slots, generator=g)[:N].to(torch.int32)
+    pool[idx.long()] = d["initial_state"]
+    return d, pool, idx
+
+
+def _step(d, pool, idx, **kw):
+    x = U.to(d)
+    how = _how(x)
+    how.pop("cu_seqlens")
+    return kda.scan_step(x["x"], x["z"], x["input_gate"], pool, state_indices=None if idx is None else idx.cuda(), **how, **kw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("gate", U.GATES)
+@pytest.mark.parametrize("N,D", [(1, 8), (5, 100), (3, 4096), (200, 33), (1, 1)])
+def test_step(dtype, gate, N, D):
+    d, pool, idx = _step_batch(N, D, dtype, N + D, N + 3, gate=gate, input_scale=U.INPUTS[N % 3], gated=N != 5)
+    p = pool.cuda()
+    h = _step(d, p, idx)
+    _no_error()
+    want, size, n = U.scan_ref(d), U.scan_ref(d, True), U.scan_roundings(d)
+    U.close("h", h, want[0], size[0], n, U.HALF[dtype])
+    U.close("state", p[idx.long().cuda()], want[1], size[1], n, U.U32)
+    rest = torch.ones(N + 3, dtype=torch.bool)
+    rest[idx.long()] = False
+    assert torch.equal(p.cpu()[rest], pool[rest])
+    q = pool[idx.long()].contiguous().cuda()
+    assert torch.equal(_step(d, q, None), h) and torch.equal(q, p[idx.long().cuda()])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_step_padded_and_bad_rows(dtype):
+    d, pool, idx = _step_batch(40, 50, dtype, 1, 60)
+    want = _step(d, pool.cuda(), idx)
+    bad = idx.clone()
+    bad[[3, 17]] = -1
+    bad[20], bad[30], bad[31] = 60, -5, bad[7]
+    skipped = torch.tensor([3, 17, 20, 30, 31])
+    p, out = pool.cuda(), torch.full((40, 50), 9.0, dtype=U.DT[dtype], device="cuda")
+    h = _step(d, p, bad, out=out)
+    torch.cuda.synchronize()
+    assert kda.get_device_error() == 8 and h is out
+    used = torch.ones(40, dtype=torch.bool)
+    used[skipped] = False
+    assert torch.equal(h.cpu()[used], want.cpu()[used]) and (h.cpu()[~used] == 9).all()
+    untouched = torch.ones(60, dtype=torch.bool)
+    untouched[idx.long()[used]] = False
+    assert torch.equal(p.cpu()[untouched], pool[untouched])
+    p = pool.cuda()
+    _step(d, p, torch.full((40,), -1, dtype=torch.int32))
+    _no_error()
+    assert torch.equal(p.cpu(), pool)
+
+
+def test_step_slots_behind_32_bits():
+    D, slots = 8192, 530000  # 4.3e9 elements
+    d, pool, _ = _step_batch(2, D, "bf16", 3, 4)
+    p = torch.empty((slots, D), device="cuda")
+    idx = torch.tensor([slots - 1, 3], dtype=torch.int32)
+    p[idx.long().cuda()] = d["initial_state"].cuda()
+    h = _step(d, p, idx)
+    _no_error()
+    q = d["initial_state"].cuda()
+    assert torch.equal(h, _step(d, q, None)) and torch.equal(p[idx.long().cuda()], q)
+
+
+def test_step_finite_checks():
+    d, pool, idx = _step_batch(6, 20, "bf16", 2, 9)
+    idx[2] = -1
+    rest = torch.ones(9, dtype=torch.bool)
+    rest[idx[idx >= 0].long()] = False
+    pool[rest] = float("nan")
+    kda.set_debug_checks(kda.CHECK_FINITE)
+    try:
+        out = torch.full((6, 20), float("nan"), dtype=torch.bfloat16, device="cuda")
+        p = pool.cuda()
+        _step(d, p, idx, out=out)
+        assert kda.get_device_error() == 0
+        p[idx[5].long(), 19] = float("inf")
+        _step(d, p, idx, out=out)
+        assert kda.get_device_error() == 12
+    finally:
+        kda.set_debug_checks(0)
+
+
+@pytest.mark.parametrize("gate,input_scale", [("softplus", "norm"), ("lower_bound", "complement")])
+def test_steps_continue_a_prefill(gate, input_scale):
+    """A prompt in two parts and then token by token, against one pass: fp32, each bound by the oracle."""
+    d = U.scan_batch([150], 48, "f32", 13, gate=gate, input_scale=input_scale)
+    x = U.to(d)
+    how = _how(x)
+    how.pop("cu_seqlens")
+    at = lambda a, b: (x["x"][a:b], x["z"][a:b], x["input_gate"][a:b])  # noqa: E731
+    h1, s = kda.scan_fwd(*at(0, 70), initial_state=x["initial_state"], output_final_state=True, **how)
+    h2, s = kda.scan_fwd(*at(70, 140), initial_state=s, final_state=s, **how)
+    rest = [kda.scan_step(*at(t, t + 1), s, **how) for t in range(140, 150)]
+    _no_error()
+    want, size, n = U.scan_ref(d), U.scan_ref(d, True), U.scan_roundings(d)
+    U.close("h", torch.cat([h1, h2] + rest), want[0], size[0], n, U.U32)
+    U.close("state", s, want[1], size[1], n, U.U32)
