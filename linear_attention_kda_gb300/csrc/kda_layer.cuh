@@ -10,6 +10,19 @@ template <typename T, int V> struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V :
     T x[V];
 };
 template <typename T, int V> __device__ __forceinline__ vec<T, V> load(const T *p) { return *reinterpret_cast<const vec<T, V> *>(p); }
+// read once, written once: evicted first
+template <typename T, int V> __device__ __forceinline__ vec<T, V> load_once(const T *p) {
+    vec<T, V> v;
+    if constexpr (sizeof(v) == 16) *reinterpret_cast<uint4 *>(&v) = __ldcs(reinterpret_cast<const uint4 *>(p));
+    else if constexpr (sizeof(v) == 8) *reinterpret_cast<uint2 *>(&v) = __ldcs(reinterpret_cast<const uint2 *>(p));
+    else v = load<T, V>(p);
+    return v;
+}
+template <typename T, int V> __device__ __forceinline__ void store_once(T *p, const vec<T, V> &v) {
+    if constexpr (sizeof(v) == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(&v));
+    else if constexpr (sizeof(v) == 8) __stcs(reinterpret_cast<uint2 *>(p), *reinterpret_cast<const uint2 *>(&v));
+    else *reinterpret_cast<vec<T, V> *>(p) = v;
+}
 template <typename T, int V> __device__ __forceinline__ void store(T *p, const vec<T, V> &v) { *reinterpret_cast<vec<T, V> *>(p) = v; }
 
 // V values as fp32 and back, two bf16 at a time

@@ -1,4 +1,4 @@
-// kda_scan_fwd, kda_scan_bwd: a thread per (sequence, channel) goes through the tokens.
+// kda_scan_bwd: a thread per (sequence, channel) goes through the tokens.
 #include "kda_internal.h"
 #include "kda_linear.cuh"
 #include "kda_scan.cuh"
@@ -7,29 +7,6 @@ namespace kda {
 namespace scan {
 
 constexpr int CK = KDA_SCAN_CHECKPOINT;
-
-template <typename T>
-__global__ void __launch_bounds__(128) scan_fwd_kernel(kda_scan_args A, spec S, int *err) {
-    const int c = blockIdx.x * 128 + threadIdx.x;
-    const int64_t n = blockIdx.y;
-    lin::span s;
-    if (!lin::seq_span(A.cu_seqlens, A.T, A.N, n, &s)) {
-        if (threadIdx.x == 0) set_error(err, KDA_ERR_BAD_SEQLENS);
-        return;
-    }
-    if (c >= A.D) return;
-    const channel C = load_channel(A.A_log, A.dt_bias, c);
-    float h = A.initial_state ? A.initial_state[n * A.D + c] : 0.f;
-    for (int64_t t = s.a; t < s.b; ++t) {
-        if (A.checkpoints && (t - s.a) % CK == 0) A.checkpoints[(s.a / CK + n + (t - s.a) / CK) * A.D + c] = h;
-        const decay d = decay_of(log_decay(S, C, ld((const T *)A.z + t * A.z_stride + c)));
-        const float u = entering(S, d.m, ld((const T *)A.x + t * A.x_stride + c), A.input_gate != nullptr,
-                                 A.input_gate ? ld((const T *)A.input_gate + t * A.i_stride + c) : 0.f);
-        h = decayed(d.d, h) + u;
-        st((T *)A.h + t * A.D + c, h);
-    }
-    if (A.final_state) A.final_state[n * A.D + c] = h;
-}
 
 template <typename T>
 __global__ void __launch_bounds__(128) scan_bwd_kernel(kda_scan_bwd_args A, spec S, float *part, int *err) {
@@ -92,19 +69,7 @@ __global__ void __launch_bounds__(128) scan_params_kernel(const float *part, int
 }  // namespace scan
 }  // namespace kda
 
-size_t kda_scan_fwd_bytes(int64_t, int64_t, int) { return 0; }
 size_t kda_scan_bwd_bytes(int64_t, int64_t N, int D) { return (size_t)N * D * 8; }
-
-kda_status_t kda_launch_scan_fwd(const kda_scan_args *a, void *, cudaStream_t stream) {
-    int *err = kda_device_error_ptr();
-    if (!err) return KDA_ERR_CUDA;
-    using namespace kda::scan;
-    const spec S{a->gate_kind, a->input_scale, a->g_min};
-    const dim3 grid((a->D + 127) / 128, (unsigned)a->N);
-    if (a->dtype == KDA_BF16) scan_fwd_kernel<kda::bf16><<<grid, 128, 0, stream>>>(*a, S, err);
-    else scan_fwd_kernel<float><<<grid, 128, 0, stream>>>(*a, S, err);
-    return kda_cuda_status(cudaGetLastError());
-}
 
 kda_status_t kda_launch_scan_bwd(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
