@@ -1,5 +1,7 @@
 // Shared by the kernels of what stands around a recurrence: vectors of elements, and the slots of decode steps.
 #pragma once
+#include <type_traits>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -51,6 +53,59 @@ template <typename T, int V> __device__ __forceinline__ vec<T, V> pack(const flo
     }
     return v;
 }
+
+// Arithmetic on one fp32 or on two at a time (one instruction for both)
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+template <typename F> __device__ __forceinline__ F splat(float x);
+template <> __device__ __forceinline__ float splat<float>(float x) { return x; }
+template <> __device__ __forceinline__ float2 splat<float2>(float x) { return make_float2(x, x); }
+// f of each
+template <typename Fn> __device__ __forceinline__ float each(Fn f, float a) { return f(a); }
+template <typename Fn> __device__ __forceinline__ float2 each(Fn f, float2 a) { return make_float2(f(a.x), f(a.y)); }
+template <typename Fn> __device__ __forceinline__ float each(Fn f, float a, float b) { return f(a, b); }
+template <typename Fn> __device__ __forceinline__ float2 each(Fn f, float2 a, float2 b) { return make_float2(f(a.x, b.x), f(a.y, b.y)); }
+template <typename Fn> __device__ __forceinline__ float each(Fn f, float a, float b, float c) { return f(a, b, c); }
+template <typename Fn> __device__ __forceinline__ float2 each(Fn f, float2 a, float2 b, float2 c) {
+    return make_float2(f(a.x, b.x, c.x), f(a.y, b.y, c.y));
+}
+// 2^x, 1 / x and 1 / sqrt(x) by the special function unit, each to about 2^-22 of itself; results (and arguments) below the
+// normal range count as 0
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsq(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
+__device__ __forceinline__ float2 rsq(float2 x) { return make_float2(rsq(x.x), rsq(x.y)); }
+
+// V values as V / K pairs or single ones
+template <int V> struct lanes {
+    static constexpr int K = V % 2 == 0 ? 2 : 1, N = V / K;
+    using F = typename std::conditional<K == 2, float2, float>::type;
+};
+template <typename T, int V, typename F> __device__ __forceinline__ void unpack(const vec<T, V> &v, F *f) {
+    unpack<T, V>(v, reinterpret_cast<float *>(f));
+}
+template <typename T, int V, typename F> __device__ __forceinline__ vec<T, V> pack(const F *f) {
+    return pack<T, V>(reinterpret_cast<const float *>(f));
+}
+template <typename F> __device__ __forceinline__ F unpack_one(const float *p) { return *reinterpret_cast<const F *>(p); }
 
 // The slot of row n of a step.  False for a row of a padded batch (-1), for a slot outside the pool, and for one
 // that an earlier row has (both set the device error); every thread of the block of NT gets the same answer.

@@ -1,127 +1,159 @@
 // Arithmetic of the gated recurrence over channels, h <- a h + c(a) Sigmoid(i) x with a = exp(g), shared by its
-// kernels: the gates, the step and its derivative.
+// kernels: the gates, the step and their derivatives.  F is one fp32 or a pair of them.
 //
-// The decay a is kept as one fp32 `d`: d < 0 stands for a = 1 + d (a in [3/4, 1)), d >= 0 for a = d.  Near 1 an fp32 a
-// is good to 2^-25, which a state that remembers 1 / (1 - a) tokens takes in as many times; a - 1 is good to 2^-24 of
-// itself, which it takes in once (4096 tokens at g = -1e-4: final states off by 9e-6 with a, 1e-7 with a - 1).  A run of
-// tokens is described by the sum of its log-decays and the state that it leaves from zero.
+// The decay a is kept as one fp32 `d`: d < 0 stands for a = 1 + d (a in [0.778, 1)), d >= 0 for a = d.  Near 1 an fp32 a
+// is good to 2^-25, which a state that remembers 1 / (1 - a) tokens takes in as many times; a - 1 is good to 2^-23 of
+// itself, which it takes in once.  A run of tokens is described by the sum of its log-decays and the state that it
+// leaves from zero.
+//
+// Bound by instructions before it is bound by HBM (8 bytes an element in bf16 leave about 42 of them an element at the copy
+// rate): everything that can be is done on two channels at a time, exponentials and quotients by the special function
+// unit (2^-22, so far below what the recurrence itself rounds).
 #pragma once
-#include "kda_common.cuh"
+#include "kda_layer.cuh"
 
 namespace kda {
 namespace scan {
+
+using layer::add;
+using layer::each;
+using layer::ex2;
+using layer::fma;
+using layer::mul;
+using layer::rcp;
+using layer::rsq;
+using layer::splat;
 
 struct spec {  // how a call forms a and c(a)
     int gate, input;
     float g_min;
 };
-struct channel {  // a channel's parameters
-    float b, rate;  // dt_bias and exp(A_log)
+template <typename F> struct channel {  // a channel's parameters: dt_bias and exp(A_log)
+    F b, rate;
 };
 
-// Sigmoid(y) and 1 - Sigmoid(y), each to a few units of 2^-24 of itself
-struct sig {
-    float s, n;
+constexpr float LOG2E = 1.4426950408889634f;
+
+// Sigmoid(y); 2^-y overflows to infinity and the quotient is 0
+template <typename F> __device__ __forceinline__ F sigmoid(F y) { return rcp(add(ex2(mul(y, splat<F>(-LOG2E))), splat<F>(1.f))); }
+// Sigmoid(y) and 1 - Sigmoid(y), each to a few units of 2^-23 of itself
+template <typename F> struct sig {
+    F s, n;
 };
-__device__ __forceinline__ sig sigmoid(float y) {
-    const float e = __expf(-fabsf(y)), r = __fdividef(1.f, 1.f + e), q = e * r;
-    return {y >= 0.f ? r : q, y >= 0.f ? q : r};
+template <typename F> __device__ __forceinline__ sig<F> sigmoids(F y) {
+    const F e = each([](float v) { return fminf(v, 1e30f); }, ex2(mul(y, splat<F>(-LOG2E))));
+    // (the clamp loses a NaN, y's own is kept)
+    const F s = each([](float v, float w) { return w != w ? w : v; }, rcp(add(e, splat<F>(1.f))), y);
+    return {s, mul(e, s)};
 }
 // Softplus(y) = max(y, 0) + ln(1 + e), e = exp(-|y|): ln(1 + e) / e by the polynomial of degree 8 that meets it in the
 // Chebyshev points of [0, 1] (2e-7 with its roundings)
-__device__ __forceinline__ float softplus(float y) {
-    const float e = __expf(-fabsf(y));
-    float p = 0.005126102361828089f;
-    p = fmaf(p, e, -0.029074065387248993f);
-    p = fmaf(p, e, 0.0775160863995552f);
-    p = fmaf(p, e, -0.13602247834205627f);
-    p = fmaf(p, e, 0.19076880812644958f);
-    p = fmaf(p, e, -0.2483539879322052f);
-    p = fmaf(p, e, 0.3331812024116516f);
-    p = fmaf(p, e, -0.4999944567680359f);
-    p = fmaf(p, e, 0.9999999403953552f);
-    return fmaf(p, e, fmaxf(y, 0.f));
-}
-// exp(g) - 1 to a few units of 2^-24 of itself: its series to g^7 / 7! where |g| < 1/4 (the rest is below 2e-9 of it), else by exp(g),
-// which is at least 2/9 away from 1 there
-__device__ __forceinline__ float small_expm1(float g) {
-    float p = 1.f / 5040.f;
-    p = fmaf(p, g, 1.f / 720.f);
-    p = fmaf(p, g, 1.f / 120.f);
-    p = fmaf(p, g, 1.f / 24.f);
-    p = fmaf(p, g, 1.f / 6.f);
-    p = fmaf(p, g, 0.5f);
-    return fmaf(p * g, g, g);
+template <typename F> __device__ __forceinline__ F softplus(F y) {
+    const F e = ex2(each([](float v) { return fabsf(v) * -LOG2E; }, y));
+    F p = fma(splat<F>(0.005126102361828089f), e, splat<F>(-0.029074065387248993f));
+    p = fma(p, e, splat<F>(0.0775160863995552f));
+    p = fma(p, e, splat<F>(-0.13602247834205627f));
+    p = fma(p, e, splat<F>(0.19076880812644958f));
+    p = fma(p, e, splat<F>(-0.2483539879322052f));
+    p = fma(p, e, splat<F>(0.3331812024116516f));
+    p = fma(p, e, splat<F>(-0.4999944567680359f));
+    p = fma(p, e, splat<F>(0.9999999403953552f));
+    return fma(p, e, each([](float v) { return fmaxf(v, 0.f); }, y));
 }
 
-// d of a log-decay, and exp(g) - 1
-struct decay {
-    float d, m;
+// d of a log-decay, and m = exp(g) - 1: by its series to g^6 / 6! where -1/4 < g < 0 (the rest is below 5e-8 of it), else from exp(g),
+// which is at least 2/9 away from 1 there (what g > 0 KDA_SCAN_LOG may bring is computed as given, a = exp(g))
+template <typename F> struct decay {
+    F d, m;
 };
-__device__ __forceinline__ decay decay_of(float g) {
-    const float e = __expf(g), m = small_expm1(g);
-    const bool near = fabsf(g) < 0.25f;
-    // (g = 0 and the small g > 0 that KDA_SCAN_LOG may bring: a = 1 + m)
-    return {near ? (m < 0.f ? m : 1.f + m) : e, near ? m : e - 1.f};
+template <typename F> __device__ __forceinline__ decay<F> decay_of(F g) {
+    const F e = ex2(mul(g, splat<F>(LOG2E)));
+    F p = fma(splat<F>(1.f / 720.f), g, splat<F>(1.f / 120.f));
+    p = fma(p, g, splat<F>(1.f / 24.f));
+    p = fma(p, g, splat<F>(1.f / 6.f));
+    p = fma(p, g, splat<F>(0.5f));
+    p = fma(mul(p, g), g, g);
+    // as integers, -0 and the negative floats above -1/4 lie below the bits of -1/4
+    const auto near = [](float v) { return __float_as_int(v) < (int)0xBE800000; };
+    return {each([&](float v, float s, float f) { return near(v) ? fminf(s, -1e-38f) : f; }, g, p, e),
+            each([&](float v, float s, float f) { return near(v) ? s : f; }, g, p, add(e, splat<F>(-1.f)))};
 }
-__device__ __forceinline__ float factor(float d) { return d < 0.f ? 1.f + d : d; }
-// a h, where nothing is left of h if a is 0, an infinity or a NaN in h included
-__device__ __forceinline__ float decayed(float d, float h) {
-    const float k = d == 0.f ? 0.f : h;
-    return fmaf(d, k, d < 0.f ? k : 0.f);
+template <typename F> __device__ __forceinline__ F factor(F d) {
+    return each([](float v) { return v < 0.f ? 1.f + v : v; }, d);
 }
+// a h + u for finite h
+template <typename F> __device__ __forceinline__ F step(F d, F h, F u) {
+    return fma(d, h, fma(each([](float v) { return v < 0.f ? 1.f : 0.f; }, d), h, u));
+}
+// the same where nothing is left of h if a is 0, an infinity or a NaN in h included
+template <typename F> __device__ __forceinline__ F step_or_erase(F d, F h, F u) {
+    return step(d, each([](float v, float w) { return v == 0.f ? 0.f : w; }, d, h), u);
+}
+__device__ __forceinline__ bool finite(float h) { return fabsf(h) <= 3.402823466e38f; }
+__device__ __forceinline__ bool finite(float2 h) { return finite(h.x) && finite(h.y); }
 
 // g, and for the gradients dg/dz and dg/dA_log
-__device__ __forceinline__ float log_decay(const spec &S, const channel &C, float z) {
+template <typename F> __device__ __forceinline__ F log_decay(const spec &S, const channel<F> &C, F z) {
     if (S.gate == KDA_SCAN_LOG) return z;
-    const float y = z + C.b;
-    if (S.gate == KDA_SCAN_SOFTPLUS) return -C.rate * softplus(y);
-    if (S.gate == KDA_SCAN_SIGMOID) return -C.rate * sigmoid(y).s;
-    return S.g_min * sigmoid(C.rate * y).s;
+    const F y = add(z, C.b), k = mul(C.rate, splat<F>(-1.f));
+    if (S.gate == KDA_SCAN_SOFTPLUS) return mul(k, softplus(y));
+    if (S.gate == KDA_SCAN_SIGMOID) return mul(k, sigmoid(y));
+    return mul(splat<F>(S.g_min), sigmoid(mul(C.rate, y)));
 }
-__device__ __forceinline__ float log_decay(const spec &S, const channel &C, float z, float *dz, float *dA) {
+template <typename F> __device__ __forceinline__ F log_decay(const spec &S, const channel<F> &C, F z, F *dz, F *dA) {
     if (S.gate == KDA_SCAN_LOG) {
-        *dz = 1.f;
-        *dA = 0.f;
+        *dz = splat<F>(1.f);
+        *dA = splat<F>(0.f);
         return z;
     }
-    const float y = z + C.b;
+    const F y = add(z, C.b), k = mul(C.rate, splat<F>(-1.f));
     if (S.gate == KDA_SCAN_LOWER_BOUND) {
-        const sig w = sigmoid(C.rate * y);
-        const float g = S.g_min * w.s;
-        *dz = g * w.n * C.rate;
-        *dA = *dz * y;
+        const sig<F> w = sigmoids(mul(C.rate, y));
+        const F g = mul(splat<F>(S.g_min), w.s);
+        *dz = mul(mul(g, w.n), C.rate);
+        *dA = mul(*dz, y);
         return g;
     }
-    const sig w = sigmoid(y);
-    const float g = -C.rate * (S.gate == KDA_SCAN_SOFTPLUS ? softplus(y) : w.s);
-    *dz = S.gate == KDA_SCAN_SOFTPLUS ? -C.rate * w.s : g * w.n;
+    const sig<F> w = sigmoids(y);
+    const F g = mul(k, S.gate == KDA_SCAN_SOFTPLUS ? softplus(y) : w.s);
+    *dz = S.gate == KDA_SCAN_SOFTPLUS ? mul(k, w.s) : mul(g, w.n);
     *dA = g;
     return g;
 }
 
-// c(a) from m = a - 1: 1 - a^2 = -m (2 + m) has no cancellation.  Where it is not above 0, c = sqrt(1 - a^2) and its derivative count as 0.
-__device__ __forceinline__ float input_factor(const spec &S, float m) {
-    if (S.input == KDA_SCAN_INPUT_PLAIN) return 1.f;
-    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return -m;
-    const float q = -m * (2.f + m);
-    return q > 0.f ? q * rsqrtf(q) : (q <= 0.f ? 0.f : q);
+// c(a) from m = a - 1: 1 - a^2 = -m (2 + m) has no cancellation.  Where it is not above 0, c = sqrt(1 - a^2) and its
+// derivative count as 0.
+template <typename F> __device__ __forceinline__ F input_factor(const spec &S, F m) {
+    const F k = mul(m, splat<F>(-1.f));
+    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return k;
+    const F q = each([](float v) { return v < 0.f ? 0.f : v; }, mul(k, add(m, splat<F>(2.f))));
+    return mul(q, rsq(add(q, splat<F>(1e-37f))));
 }
 // dc/dg: -a of 1 - a, -a^2 / c of sqrt(1 - a^2)
-__device__ __forceinline__ float input_slope(const spec &S, float a, float c) {
-    if (S.input == KDA_SCAN_INPUT_PLAIN) return 0.f;
-    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return -a;
-    return c > 0.f ? -a * __fdividef(a, c) : (c <= 0.f ? 0.f : c);
+template <typename F> __device__ __forceinline__ F input_slope(const spec &S, F a, F c) {
+    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return mul(a, splat<F>(-1.f));
+    return each([](float v, float w) { return w > 0.f ? -v * v * rcp(w) : (w <= 0.f ? 0.f : w); }, a, c);
 }
 
 // What enters at a token, c(a) Sigmoid(i) x
-__device__ __forceinline__ float entering(const spec &S, float m, float x, bool gated, float i) {
-    const float u = gated ? x * sigmoid(i).s : x;
-    return S.input == KDA_SCAN_INPUT_PLAIN ? u : u * input_factor(S, m);
+template <typename F> __device__ __forceinline__ F entering(const spec &S, F m, F x, bool gated, F i) {
+    if (gated) x = mul(x, sigmoid(i));
+    return S.input == KDA_SCAN_INPUT_PLAIN ? x : mul(x, input_factor(S, m));
 }
 
-__device__ __forceinline__ channel load_channel(const float *A_log, const float *dt_bias, int c) {
-    return {dt_bias ? dt_bias[c] : 0.f, A_log ? expf(A_log[c]) : 1.f};
+template <int V, typename F>
+__device__ __forceinline__ void load_channels(const float *A_log, const float *dt_bias, int c, bool some, channel<F> *C) {
+    float b[V], r[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        b[v] = some && dt_bias ? dt_bias[c + v] : 0.f;
+        r[v] = some && A_log ? expf(A_log[c + v]) : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < layer::lanes<V>::N; ++i) {
+        if constexpr (std::is_same<F, float2>::value) C[i] = {make_float2(b[2 * i], b[2 * i + 1]), make_float2(r[2 * i], r[2 * i + 1])};
+        else C[i] = {b[i], r[i]};
+    }
 }
 
 }  // namespace scan

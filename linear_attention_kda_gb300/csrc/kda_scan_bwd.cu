@@ -18,7 +18,8 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(kda_scan_bwd_args A, spec
     if (c >= A.D) return;
     float sA = 0.f, sb = 0.f;
     if (good) {
-        const channel C = load_channel(A.A_log, A.dt_bias, c);
+        channel<float> C[1];
+        load_channels<1>(A.A_log, A.dt_bias, c, true, C);
         float lam = A.grad_final_state ? A.grad_final_state[n * A.D + c] : 0.f, before[CK];
         for (int64_t k = (s.b - s.a + CK - 1) / CK - 1; k >= 0; --k) {
             const int64_t t0 = s.a + k * CK;
@@ -27,25 +28,25 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(kda_scan_bwd_args A, spec
             for (int r = 0; r < len; ++r) {
                 const int64_t t = t0 + r;
                 before[r] = h;
-                const decay d = decay_of(log_decay(S, C, ld((const T *)A.z + t * A.z_stride + c)));
-                h = decayed(d.d, h) + entering(S, d.m, ld((const T *)A.x + t * A.x_stride + c), A.input_gate != nullptr,
-                                               A.input_gate ? ld((const T *)A.input_gate + t * A.i_stride + c) : 0.f);
+                const decay<float> d = decay_of(log_decay(S, C[0], ld((const T *)A.z + t * A.z_stride + c)));
+                h = step_or_erase(d.d, h, entering(S, d.m, ld((const T *)A.x + t * A.x_stride + c), A.input_gate != nullptr,
+                                                   A.input_gate ? ld((const T *)A.input_gate + t * A.i_stride + c) : 0.f));
             }
             for (int r = len - 1; r >= 0; --r) {
                 const int64_t t = t0 + r;
                 float dz, dA;
-                const decay d = decay_of(log_decay(S, C, ld((const T *)A.z + t * A.z_stride + c), &dz, &dA));
-                const float x = ld((const T *)A.x + t * A.x_stride + c), cf = input_factor(S, d.m);
-                sig w{1.f, 0.f};
-                if (A.input_gate) w = sigmoid(ld((const T *)A.input_gate + t * A.i_stride + c));
+                const decay<float> d = decay_of(log_decay(S, C[0], ld((const T *)A.z + t * A.z_stride + c), &dz, &dA));
+                const float x = ld((const T *)A.x + t * A.x_stride + c), cf = S.input == KDA_SCAN_INPUT_PLAIN ? 1.f : input_factor(S, d.m);
+                sig<float> w{1.f, 0.f};
+                if (A.input_gate) w = sigmoids(ld((const T *)A.input_gate + t * A.i_stride + c));
                 lam += ld((const T *)A.grad_h + t * A.D + c);
                 st((T *)A.grad_x + t * A.D + c, cf * w.s * lam);
                 if (A.input_gate) st((T *)A.grad_input_gate + t * A.D + c, cf * x * w.s * w.n * lam);
-                const float dg = (decayed(d.d, before[r]) + input_slope(S, factor(d.d), cf) * w.s * x) * lam;
+                const float dg = step_or_erase(d.d, before[r], S.input == KDA_SCAN_INPUT_PLAIN ? 0.f : input_slope(S, factor(d.d), cf) * w.s * x) * lam;
                 st((T *)A.grad_z + t * A.D + c, dg * dz);
                 sA += dg * dA;
                 sb += dg * dz;
-                lam = decayed(d.d, lam);
+                lam = step_or_erase(d.d, lam, 0.f);
             }
         }
         if (A.grad_initial_state) A.grad_initial_state[n * A.D + c] = lam;

@@ -16,22 +16,23 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
     int64_t slot;
     if (!layer::find_slot<128>(A.state_indices, A.num_slots, n, &slot, err) || c >= A.D) return;
     const spec S{A.gate_kind, A.input_scale, A.g_min};
-    layer::vec<T, V> x, z, i, h;
-    layer::vec<float, V> s;
+    constexpr int P = layer::lanes<V>::N;
+    using F = typename layer::lanes<V>::F;
     float *state = A.state + slot * A.D + c;
-    x = layer::load<T, V>((const T *)A.x + n * A.x_stride + c);
-    z = layer::load<T, V>((const T *)A.z + n * A.z_stride + c);
-    if (A.input_gate) i = layer::load<T, V>((const T *)A.input_gate + n * A.i_stride + c);
-    s = layer::load<float, V>(state);
+    F x[P], z[P], i[P], h[P];
+    layer::unpack<T, V>(layer::load<T, V>((const T *)A.x + n * A.x_stride + c), x);
+    layer::unpack<T, V>(layer::load<T, V>((const T *)A.z + n * A.z_stride + c), z);
+    if (A.input_gate) layer::unpack<T, V>(layer::load<T, V>((const T *)A.input_gate + n * A.i_stride + c), i);
+    layer::unpack<float, V>(layer::load<float, V>(state), h);
+    channel<F> C[P];
+    load_channels<V>(A.A_log, A.dt_bias, c, true, C);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const channel C = load_channel(A.A_log, A.dt_bias, c + e);
-        const decay d = decay_of(log_decay(S, C, ld(&z.x[e])));
-        s.x[e] = decayed(d.d, s.x[e]) + entering(S, d.m, ld(&x.x[e]), A.input_gate != nullptr, A.input_gate ? ld(&i.x[e]) : 0.f);
-        st(&h.x[e], s.x[e]);
+    for (int k = 0; k < P; ++k) {
+        const decay<F> d = decay_of(log_decay(S, C[k], z[k]));
+        h[k] = step_or_erase(d.d, h[k], entering(S, d.m, x[k], A.input_gate != nullptr, i[k]));
     }
-    layer::store(state, s);
-    layer::store((T *)A.h + n * A.D + c, h);
+    layer::store(state, layer::pack<float, V>(h));
+    layer::store((T *)A.h + n * A.D + c, layer::pack<T, V>(h));
 }
 
 template <typename T, int V>
