@@ -1,193 +1,144 @@
-// kda_scan_fwd: a block takes tiles of 64 tokens by 32 V channels (kda_scan_tiles.cuh), each of its eight warps 8
-// tokens, each lane V channels.  A thread forms the decay and the input of its elements once, keeps both in registers,
-// runs them from zero for the tile's sums, asks for its elements of the next tile, and, when it knows what enters, runs
-// them again for h.
+// kda_scan_fwd: a block takes tiles of 64 tokens by 64 channels (kda_scan_tiles.cuh), each of its eight warps 8 tokens,
+// each lane two channels.  Tiles come by TMA two ahead.  A thread forms the decay and the input of its elements once,
+// keeps both in registers, runs them from zero for the tile's sums, and, when it knows what enters, runs them again for h.
 #include "kda_scan_tiles.cuh"
 
 namespace kda {
 namespace scan {
 
-template <typename T, int V>
-__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__ board B, int joined,
-                                                         int blocks, int *err) {
-    constexpr int W = 32 * V, P = layer::lanes<V>::N;
-    using F = typename layer::lanes<V>::F;
-    extern __shared__ __align__(16) char memory[];
-    tile_memory<W> &M = *reinterpret_cast<tile_memory<W> *>(memory);
-    ahead<T, V, 3> &next = *reinterpret_cast<ahead<T, V, 3> *>(memory + sizeof(tile_memory<W>));
+template <typename T> struct fwd_memory {
+    ring<T, 3> next;
+    tile_memory M;
+};
+
+// TMA: rows are 16-byte aligned.  Else a thread reads its elements when it needs them.
+template <typename T, bool TMA>
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 3 : 2)
+scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<3> maps, int joined,
+                int blocks, int *err) {
+    extern __shared__ __align__(128) char memory[];
+    fwd_memory<T> &S = *reinterpret_cast<fwd_memory<T> *>(memory);
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const spec S{A.gate_kind, A.input_scale, A.g_min};
+    const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
-    const bool serial = joined && __ldcg(B.bad) != 0;
-    const int64_t items = serial ? A.N * blocks : lin::chunk_slots(A.T, A.N, L) * blocks;
-
-    // the tile of an item; p = -1: none
-    auto take = [&](int64_t item) {
-        tile t{0, -1, 0, 0, 0, 0};
-        if (item >= items) return t;
-        t.block = (int)(item % blocks);
-        const int64_t i = item / blocks;
-        if (joined && !serial) {
-            const int4 q = __ldg(B.plan + i);
-            t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
-        } else {
-            int64_t n = i, p = 0;
-            lin::span s;
-            if (serial ? lin::seq_span(A.cu_seqlens, A.T, A.N, n, &s) : lin::find_slot(A.cu_seqlens, A.T, A.N, L, i, &n, &p, &s)) {
-                if (p == 0 || p < (s.b - s.a + L - 1) / L) t.p = (int)p;
-                t.n = (int)n, t.a = (int)s.a, t.b = (int)s.b;
-            }
-        }
-        t.count = (t.b - t.a + L - 1) / L;
-        return t;
+    const course way(B, A.cu_seqlens, A.T, A.N, blocks, joined);
+    const bool loader = w == NW - 1;
+    // asks for a tile's boxes
+    auto ask = [&](const course::place &x, int stage) {
+        if (!TMA || x.t.p < 0 || lane != 0) return;
+        const int tok = x.t.a + x.t.p * L, n = gated ? 3 : 2;
+        tc::mbar_arrive_expect_tx(&S.next.full[stage], (uint32_t)(n * L * W * sizeof(T)));
+        for (int i = 0; i < n; ++i) tc::tma_load_3d(&S.next.x[stage][i][0][0], &maps.m[i], x.t.block * W, 0, tok, &S.next.full[stage]);
     };
-    auto ask = [&](const tile &t) {
-        const int64_t tok = t.a + (int64_t)t.p * L + w * R;
-        const int c = t.block * W + lane * V;
-        if (t.p < 0 || c >= A.D) return;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (tok + r < t.b) {
-                next.ask(r, 0, (const T *)A.z + (tok + r) * A.z_stride + c);
-                next.ask(r, 1, (const T *)A.x + (tok + r) * A.x_stride + c);
-                if (gated) next.ask(r, 2, (const T *)A.input_gate + (tok + r) * A.i_stride + c);
-            }
-    };
-
-    int64_t item = blockIdx.x;
-    tile t = take(item);
-    ask(t);
-    channel<F> C[P];
-    int of = -1;  // the block of channels whose parameters C holds
-    while (item < items) {
-        if (t.p < 0) {
-            t = take(item += gridDim.x);
-            ask(t);
-            continue;
-        }
-        const int64_t tok = t.a + (int64_t)t.p * L + w * R;
-        const int len = (int)(t.b - tok < R ? t.b - tok : R), c = t.block * W + lane * V;  // tokens of this warp, below 1 where it has none
-        const bool mine = c < A.D;
-        if (of != t.block) load_channels<V>(A.A_log, A.dt_bias, c, mine, C);
-        of = t.block;
-        tile then = t;  // the tile after this one
-        int64_t after = item;
-        if (serial && t.p + 1 < t.count) ++then.p;
-        else then = take(after += gridDim.x);
-        cp_async_wait_all();
-        F d[R][P], u[R][P], sum[P], h[P], whole[P];
-#pragma unroll
-        for (int i = 0; i < P; ++i) sum[i] = h[i] = splat<F>(0.f);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (mine && r < len) {
-                F z[P], x[P], g[P];
-                layer::unpack<T, V>(next.x[r][0][threadIdx.x], z);
-                layer::unpack<T, V>(next.x[r][1][threadIdx.x], x);
-                if (gated) layer::unpack<T, V>(next.x[r][2][threadIdx.x], g);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const F k = log_decay(S, C[i], z[i]);
-                    const decay<F> e = decay_of(k);
-                    sum[i] = add(sum[i], k);
-                    d[r][i] = e.d;
-                    u[r][i] = entering(S, e.m, x[i], gated, g[i]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    d[r][i] = splat<F>(1.f);
-                    u[r][i] = splat<F>(0.f);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) h[i] = step(d[r][i], h[i], u[r][i]);
-        }
-        ask(then);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int at = lane * V + i * layer::lanes<V>::K;
-            *reinterpret_cast<F *>(&M.g[w][at]) = sum[i];
-            *reinterpret_cast<F *>(&M.d[w][at]) = decay_of(sum[i]).d;
-            *reinterpret_cast<F *>(&M.b[w][at]) = h[i];
-        }
-        join<W>(B, joined && !serial, serial && t.p > 0, t, A.D, A.initial_state, M, err);
-        enter<W, V>(M, w, lane, h, whole);
-        if (A.checkpoints && w == 0 && mine && t.count > 0)
-#pragma unroll
-            for (int v = 0; v < V; ++v) A.checkpoints[((int64_t)t.first() + t.p) * A.D + c + v] = reinterpret_cast<const float *>(whole)[v];
-        // what enters may be an infinity or a NaN, which a decay of 0 erases
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < P; ++i) odd |= !finite(h[i]);
-        odd = __any_sync(0xffffffffu, odd);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (odd) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) h[i] = each([](float v, float s) { return v == 0.f ? 0.f : s; }, d[r][i], h[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) h[i] = step(d[r][i], h[i], u[r][i]);
-            if (mine && r < len) layer::store_once((T *)A.h + (tok + r) * A.D + c, layer::pack<T, V>(h));
-        }
-        if (serial) __syncthreads();  // M.from has been read
-        if (w == NW - 1) {
-            const float *last = reinterpret_cast<const float *>(h);
-            if (A.final_state && mine && t.p + 1 >= t.count)
-#pragma unroll
-                for (int v = 0; v < V; ++v) A.final_state[(int64_t)t.n * A.D + c + v] = last[v];
-            if (serial)
-#pragma unroll
-                for (int v = 0; v < V; ++v) M.from[lane * V + v] = last[v];
-            else if (joined)
-                leave<W, V>(B, t, lane, A.D, h);
-        }
-        t = then;
-        item = after;
+    if (TMA && threadIdx.x == 0) {
+        tc::mbar_init(&S.next.full[0], 1);
+        tc::mbar_init(&S.next.full[1], 1);
+        tc::fence_proxy_async();
     }
-    if (!joined && blockIdx.x == 0)
-        for (int64_t n = threadIdx.x; n < A.N; n += NT) {
-            lin::span s;
-            if (!lin::seq_span(A.cu_seqlens, A.T, A.N, n, &s)) set_error(err, KDA_ERR_BAD_SEQLENS);
+    __syncthreads();
+    course::place now = way.begin(false), far = now;
+    if (loader) {
+        ask(far, 0);
+        far = way.next(far, false);
+        ask(far, 1);
+    }
+    channel<float2> C{};
+    int of = -1;  // the block of channels whose parameters C holds
+    for (int turn = 0; now.t.p >= 0; ++turn) {
+        const tile t = now.t;
+        const int tok = t.a + t.p * L + w * R, len = t.b - tok < R ? t.b - tok : R;  // tokens of this warp, below 1 where it has none
+        const int c = t.block * W + lane * 2, have = A.D - c;
+        if (of != t.block) C = load_channel(A.A_log, A.dt_bias, c, have);
+        of = t.block;
+        now = way.next(now, false);
+        const int stage = turn & 1;
+        if (TMA && !tc::mbar_wait(&S.next.full[stage], (turn >> 1) & 1)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+        float2 d[R], u[R], sum = make_float2(0.f, 0.f), h = sum;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            d[r] = make_float2(1.f, 1.f);
+            u[r] = make_float2(0.f, 0.f);
+            if (r < len) {
+                float2 z, x, i = sum;
+                if constexpr (TMA) {
+                    z = load_pair<T, true>(&S.next.x[stage][0][w * R + r][lane * 2], 2);
+                    x = load_pair<T, true>(&S.next.x[stage][1][w * R + r][lane * 2], 2);
+                    if (gated) i = load_pair<T, true>(&S.next.x[stage][2][w * R + r][lane * 2], 2);
+                } else {
+                    z = load_pair<T, false>((const T *)A.z + (tok + r) * A.z_stride + c, have);
+                    x = load_pair<T, false>((const T *)A.x + (tok + r) * A.x_stride + c, have);
+                    if (gated) i = load_pair<T, false>((const T *)A.input_gate + (tok + r) * A.i_stride + c, have);
+                }
+                const float2 g = log_decay(K, C, z);
+                const decay<float2> e = decay_of(g);
+                sum = add(sum, g);
+                d[r] = e.d;
+                u[r] = entering(K, e.m, x, gated, i);
+            }
+            h = step(d[r], h, u[r]);
         }
+        *reinterpret_cast<float2 *>(&S.M.g[w][lane * 2]) = sum;
+        *reinterpret_cast<float2 *>(&S.M.d[w][lane * 2]) = decay_of(sum).d;
+        *reinterpret_cast<float2 *>(&S.M.b[w][lane * 2]) = h;
+        join(B, joined && !way.serial, way.serial, t, A.D, A.initial_state, A.final_state, A.checkpoints, S.M, err);
+        if (loader) {  // every warp is done with this stage
+            far = way.next(far, false);
+            ask(far, stage);
+        }
+        h = *reinterpret_cast<const float2 *>(&S.M.g[w][lane * 2]);
+        // what enters may be an infinity or a NaN, which a decay of 0 erases
+        const bool odd = __any_sync(0xffffffffu, !finite(h));
+        T *out = (T *)A.h + (int64_t)tok * A.D + c;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (odd) h = each([](float v, float s) { return v == 0.f ? 0.f : s; }, d[r], h);
+            h = step(d[r], h, u[r]);
+            if (r < len && have > 0) store_pair<T, TMA>(out, h, have);
+            out += A.D;
+        }
+    }
+    if (!joined) check_all(A.cu_seqlens, A.T, A.N, err);
 }
 
-template <typename T, int V>
-static cudaError_t launch(const kda_scan_args *a, void *ws, cudaStream_t stream, int *err) {
+template <typename T, bool TMA>
+static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void *ws, cudaStream_t stream, int *err) {
     static std::atomic<int> running[64];
-    constexpr size_t smem = sizeof(tile_memory<32 * V>) + sizeof(ahead<T, V, 3>);
-    int blocks = (a->D + 32 * V - 1) / (32 * V), grid = 0;
+    constexpr size_t smem = sizeof(fwd_memory<T>);
+    int blocks = (a->D + W - 1) / W, grid = 0;
     const int64_t tiles = lin::chunk_slots(a->T, a->N, L) * blocks;
     board B{};
-    int joined = board_layout(a->T, a->N, a->D, 32 * V, ws, &B) > 0;
-    const cudaError_t e = running_blocks(scan_fwd_kernel<T, V>, smem, running, tiles, &grid);
+    int joined = board_layout(a->T, a->N, a->D, ws, &B) > 0;
+    const cudaError_t e = running_blocks(scan_fwd_kernel<T, TMA>, smem, running, tiles, &grid);
     if (e != cudaSuccess) return e;
     if (!joined) {
-        scan_fwd_kernel<T, V><<<grid, NT, smem, stream>>>(*a, B, 0, blocks, err);
+        scan_fwd_kernel<T, TMA><<<grid, NT, smem, stream>>>(*a, B, maps, 0, blocks, err);
         return cudaGetLastError();
     }
     launch_plan(B, a->cu_seqlens, a->T, a->N, stream, err);
     kda_scan_args args = *a;
-    void *p[] = {&args, &B, &joined, &blocks, &err};
-    return cudaLaunchCooperativeKernel((const void *)scan_fwd_kernel<T, V>, dim3(grid), dim3(NT), p, smem, stream);
+    row_maps<3> m = maps;
+    void *p[] = {&args, &B, &m, &joined, &blocks, &err};
+    return cudaLaunchCooperativeKernel((const void *)scan_fwd_kernel<T, TMA>, dim3(grid), dim3(NT), p, smem, stream);
 }
 
 }  // namespace scan
 }  // namespace kda
 
-size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D) { return kda::scan::board_layout(T, N, D, 32, nullptr, nullptr); }
+size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D) { return kda::scan::board_layout(T, N, D, nullptr, nullptr); }
 
 kda_status_t kda_launch_scan_fwd(const kda_scan_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::scan;
-    // 8 bytes a lane where every row's address allows it
-    auto wide = [&](int V) {
-        const uintptr_t bytes = V * (a->dtype == KDA_BF16 ? 2 : 4);
-        return a->D % V == 0 && a->x_stride % V == 0 && a->z_stride % V == 0 && a->i_stride % V == 0 &&
-               (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate | (uintptr_t)a->h) % bytes) == 0;
-    };
-    if (a->dtype == KDA_BF16) return kda_cuda_status(wide(4) ? launch<kda::bf16, 4>(a, ws, stream, err) : launch<kda::bf16, 1>(a, ws, stream, err));
-    return kda_cuda_status(wide(2) ? launch<float, 2>(a, ws, stream, err) : launch<float, 1>(a, ws, stream, err));
+    row_maps<3> maps{};
+    const int64_t es = a->dtype == KDA_BF16 ? 2 : 4, per = 16 / es;
+    const bool tma = a->T > 0 && a->D % 2 == 0 && (uintptr_t)a->h % (2 * es) == 0 &&
+                     (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate) & 15) == 0 && a->x_stride % per == 0 &&
+                     a->z_stride % per == 0 && (!a->input_gate || a->i_stride % per == 0);
+    if (tma && (!make_row_map(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype) || !make_row_map(&maps.m[1], a->x, a->T, a->D, a->x_stride, a->dtype) ||
+                (a->input_gate && !make_row_map(&maps.m[2], a->input_gate, a->T, a->D, a->i_stride, a->dtype))))
+        return KDA_ERR_CUDA;
+    if (a->dtype == KDA_BF16)
+        return kda_cuda_status(tma ? launch<kda::bf16, true>(a, maps, ws, stream, err) : launch<kda::bf16, false>(a, maps, ws, stream, err));
+    return kda_cuda_status(tma ? launch<float, true>(a, maps, ws, stream, err) : launch<float, false>(a, maps, ws, stream, err));
 }
