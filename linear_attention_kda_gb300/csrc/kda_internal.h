@@ -137,9 +137,9 @@ kda_status_t kda_launch_rope(const kda_rope_args *a, cudaStream_t stream);
 
 // What stands around a recurrence in a layer: the gated recurrence over channels, the short convolution and the norms
 // around a block (kda_layer_api.cu checks the arguments; these launch).
-size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D);
+size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D, kda_dtype_t dtype);
 kda_status_t kda_launch_scan_fwd(const kda_scan_args *a, void *ws, cudaStream_t stream);
-size_t kda_scan_bwd_bytes(int64_t T, int64_t N, int D);
+size_t kda_scan_bwd_bytes(int64_t T, int64_t N, int D, kda_dtype_t dtype);
 kda_status_t kda_launch_scan_bwd(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream);
 kda_status_t kda_launch_scan_step(const kda_scan_step_args *a, cudaStream_t stream);
 kda_status_t kda_launch_short_conv_fwd(const kda_short_conv_args *a, cudaStream_t stream);

@@ -65,11 +65,11 @@ kda_status_t finite(const void *p, int64_t n, kda_dtype_t t, struct CUstream_st 
 extern "C" {
 
 size_t kda_scan_fwd_workspace_size(int64_t T, int64_t N, int32_t D, kda_dtype_t dtype) {
-    return N < 1 || check_sizes(T, N, D, dtype) != KDA_OK ? 0 : kda_scan_fwd_bytes(T, N, D);
+    return N < 1 || check_sizes(T, N, D, dtype) != KDA_OK ? 0 : kda_scan_fwd_bytes(T, N, D, dtype);
 }
 
 size_t kda_scan_bwd_workspace_size(int64_t T, int64_t N, int32_t D, kda_dtype_t dtype) {
-    return N < 1 || check_sizes(T, N, D, dtype) != KDA_OK ? 0 : kda_scan_bwd_bytes(T, N, D);
+    return N < 1 || check_sizes(T, N, D, dtype) != KDA_OK ? 0 : kda_scan_bwd_bytes(T, N, D, dtype);
 }
 
 kda_status_t kda_scan_fwd(const kda_scan_args *args, void *workspace, size_t workspace_bytes, struct CUstream_st *stream) {
@@ -93,7 +93,7 @@ kda_status_t kda_scan_fwd(const kda_scan_args *args, void *workspace, size_t wor
     if (!aligned(a->x, es) || !aligned(a->z, es) || !aligned(a->input_gate, es) || !aligned(a->h, es) ||
         !aligned(a->cu_seqlens, 4) || !aligned(a->initial_state, 4) || !aligned(a->final_state, 4) || !aligned(a->checkpoints, 4))
         return KDA_ERR_MISALIGNED;
-    const size_t need = kda_scan_fwd_bytes(a->T, a->N, a->D);
+    const size_t need = kda_scan_fwd_bytes(a->T, a->N, a->D, a->dtype);
     if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
     st = kda_check_device();
@@ -132,7 +132,7 @@ kda_status_t kda_scan_bwd(const kda_scan_bwd_args *args, void *workspace, size_t
         if (!aligned(in[k].p, k == 6 ? es : 4)) return KDA_ERR_MISALIGNED;
     for (int k = 0; k < 6; ++k)
         if (!aligned(out[k].p, k < 3 ? es : 4)) return KDA_ERR_MISALIGNED;
-    const size_t need = kda_scan_bwd_bytes(a->T, a->N, a->D);
+    const size_t need = kda_scan_bwd_bytes(a->T, a->N, a->D, a->dtype);
     if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
     st = kda_check_device();

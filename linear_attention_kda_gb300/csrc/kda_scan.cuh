@@ -61,8 +61,11 @@ template <typename F> __device__ __forceinline__ F softplus(F y) {
     return fma(p, e, each([](float v) { return fmaxf(v, 0.f); }, y));
 }
 
-// d of a log-decay, and m = exp(g) - 1: by its series to g^6 / 6! where -1/4 < g < 0 (the rest is below 5e-8 of it), else from exp(g),
-// which is at least 2/9 away from 1 there (what g > 0 KDA_SCAN_LOG may bring is computed as given, a = exp(g))
+// Log-decays are moved by this much, which changes nothing but 0 and -0 to a decay below 1 (d < 0)
+constexpr float NUDGE = -1e-37f;
+
+// d of a log-decay (nudged), and m = exp(g) - 1: by its series to g^6 / 6! where -1/4 < g < 0 (the rest is below 5e-8 of it), else from
+// exp(g), which is at least 2/9 away from 1 there (what g > 0 KDA_SCAN_LOG may bring is computed as given, a = exp(g))
 template <typename F> struct decay {
     F d, m;
 };
@@ -73,9 +76,9 @@ template <typename F> __device__ __forceinline__ decay<F> decay_of(F g) {
     p = fma(p, g, splat<F>(1.f / 6.f));
     p = fma(p, g, splat<F>(0.5f));
     p = fma(mul(p, g), g, g);
-    // as integers, -0 and the negative floats above -1/4 lie below the bits of -1/4
+    // as integers, the negative floats above -1/4 lie below the bits of -1/4
     const auto near = [](float v) { return __float_as_int(v) < (int)0xBE800000; };
-    return {each([&](float v, float s, float f) { return near(v) ? fminf(s, -1e-38f) : f; }, g, p, e),
+    return {each([&](float v, float s, float f) { return near(v) ? s : f; }, g, p, e),
             each([&](float v, float s, float f) { return near(v) ? s : f; }, g, p, add(e, splat<F>(-1.f)))};
 }
 template <typename F> __device__ __forceinline__ F factor(F d) {
@@ -92,30 +95,23 @@ template <typename F> __device__ __forceinline__ F step_or_erase(F d, F h, F u) 
 __device__ __forceinline__ bool finite(float h) { return fabsf(h) <= 3.402823466e38f; }
 __device__ __forceinline__ bool finite(float2 h) { return finite(h.x) && finite(h.y); }
 
-// g, and for the gradients dg/dz and dg/dA_log
-template <typename F> __device__ __forceinline__ F log_decay(const spec &S, const channel<F> &C, F z) {
-    if (S.gate == KDA_SCAN_LOG) return z;
-    const F y = add(z, C.b), k = mul(C.rate, splat<F>(-1.f));
-    if (S.gate == KDA_SCAN_SOFTPLUS) return mul(k, softplus(y));
-    if (S.gate == KDA_SCAN_SIGMOID) return mul(k, sigmoid(y));
-    return mul(splat<F>(S.g_min), sigmoid(mul(C.rate, y)));
-}
+// g, dg/dz and dg/dA_log
 template <typename F> __device__ __forceinline__ F log_decay(const spec &S, const channel<F> &C, F z, F *dz, F *dA) {
     if (S.gate == KDA_SCAN_LOG) {
         *dz = splat<F>(1.f);
         *dA = splat<F>(0.f);
-        return z;
+        return add(z, splat<F>(NUDGE));
     }
     const F y = add(z, C.b), k = mul(C.rate, splat<F>(-1.f));
     if (S.gate == KDA_SCAN_LOWER_BOUND) {
         const sig<F> w = sigmoids(mul(C.rate, y));
-        const F g = mul(splat<F>(S.g_min), w.s);
+        const F g = fma(splat<F>(S.g_min), w.s, splat<F>(NUDGE));
         *dz = mul(mul(g, w.n), C.rate);
         *dA = mul(*dz, y);
         return g;
     }
     const sig<F> w = sigmoids(y);
-    const F g = mul(k, S.gate == KDA_SCAN_SOFTPLUS ? softplus(y) : w.s);
+    const F g = fma(k, S.gate == KDA_SCAN_SOFTPLUS ? softplus(y) : w.s, splat<F>(NUDGE));
     *dz = S.gate == KDA_SCAN_SOFTPLUS ? mul(k, w.s) : mul(g, w.n);
     *dA = g;
     return g;
@@ -126,7 +122,8 @@ template <typename F> __device__ __forceinline__ F log_decay(const spec &S, cons
 template <typename F> __device__ __forceinline__ F input_factor(const spec &S, F m) {
     const F k = mul(m, splat<F>(-1.f));
     if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return k;
-    const F q = each([](float v) { return v < 0.f ? 0.f : v; }, mul(k, add(m, splat<F>(2.f))));
+    // (a NaN's c is 0, but its decay is a NaN, too)
+    const F q = each([](float v) { return fmaxf(v, 0.f); }, mul(k, add(m, splat<F>(2.f))));
     return mul(q, rsq(add(q, splat<F>(1e-37f))));
 }
 // dc/dg: -a of 1 - a, -a^2 / c of sqrt(1 - a^2)
@@ -135,10 +132,37 @@ template <typename F> __device__ __forceinline__ F input_slope(const spec &S, F 
     return each([](float v, float w) { return w > 0.f ? -v * v * rcp(w) : (w <= 0.f ? 0.f : w); }, a, c);
 }
 
-// What enters at a token, c(a) Sigmoid(i) x
-template <typename F> __device__ __forceinline__ F entering(const spec &S, F m, F x, bool gated, F i) {
-    if (gated) x = mul(x, sigmoid(i));
-    return S.input == KDA_SCAN_INPUT_PLAIN ? x : mul(x, input_factor(S, m));
+// N tokens' log-decays from their logits, in place, and what enters at them, x -> c(a) Sigmoid(i) x with m = a - 1.  The
+// kinds are told apart outside the loops, so that a polynomial's constants are set up once for all tokens.
+template <int N, typename F> __device__ __forceinline__ void log_decays(const spec &S, const channel<F> &C, F (&z)[N]) {
+    const F k = mul(C.rate, splat<F>(-1.f)), nudge = splat<F>(NUDGE);
+    if (S.gate == KDA_SCAN_LOG) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = add(z[i], nudge);
+    } else if (S.gate == KDA_SCAN_SOFTPLUS) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fma(k, softplus(add(z[i], C.b)), nudge);
+    } else if (S.gate == KDA_SCAN_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fma(k, sigmoid(add(z[i], C.b)), nudge);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fma(splat<F>(S.g_min), sigmoid(mul(C.rate, add(z[i], C.b))), nudge);
+    }
+}
+template <int N, typename F> __device__ __forceinline__ void scale_inputs(const spec &S, const F (&m)[N], F (&x)[N]) {
+    if (S.input == KDA_SCAN_INPUT_PLAIN) return;
+    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = mul(x[i], mul(m[i], splat<F>(-1.f)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = mul(x[i], input_factor(S, m[i]));
+    }
+}
+template <int N, typename F> __device__ __forceinline__ void gate_inputs(const F (&i)[N], F (&x)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = mul(x[k], sigmoid(i[k]));
 }
 
 template <int V, typename F>

@@ -28,9 +28,16 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(kda_scan_bwd_args A, spec
             for (int r = 0; r < len; ++r) {
                 const int64_t t = t0 + r;
                 before[r] = h;
-                const decay<float> d = decay_of(log_decay(S, C[0], ld((const T *)A.z + t * A.z_stride + c)));
-                h = step_or_erase(d.d, h, entering(S, d.m, ld((const T *)A.x + t * A.x_stride + c), A.input_gate != nullptr,
-                                                   A.input_gate ? ld((const T *)A.input_gate + t * A.i_stride + c) : 0.f));
+                float dz, dA;
+                const decay<float> d = decay_of(log_decay(S, C[0], ld((const T *)A.z + t * A.z_stride + c), &dz, &dA));
+                const float m[1] = {d.m};
+                float x[1] = {ld((const T *)A.x + t * A.x_stride + c)}, i[1];
+                scale_inputs(S, m, x);
+                if (A.input_gate) {
+                    i[0] = ld((const T *)A.input_gate + t * A.i_stride + c);
+                    gate_inputs(i, x);
+                }
+                h = step_or_erase(d.d, h, x[0]);
             }
             for (int r = len - 1; r >= 0; --r) {
                 const int64_t t = t0 + r;
@@ -70,7 +77,7 @@ __global__ void __launch_bounds__(128) scan_params_kernel(const float *part, int
 }  // namespace scan
 }  // namespace kda
 
-size_t kda_scan_bwd_bytes(int64_t, int64_t N, int D) { return (size_t)N * D * 8; }
+size_t kda_scan_bwd_bytes(int64_t, int64_t N, int D, kda_dtype_t) { return (size_t)N * D * 8; }
 
 kda_status_t kda_launch_scan_bwd(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();

@@ -28,8 +28,13 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
     load_channels<V>(A.A_log, A.dt_bias, c, true, C);
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-        const decay<F> d = decay_of(log_decay(S, C[k], z[k]));
-        h[k] = step_or_erase(d.d, h[k], entering(S, d.m, x[k], A.input_gate != nullptr, i[k]));
+        F zk[1] = {z[k]}, xk[1] = {x[k]}, ik[1] = {i[k]};
+        log_decays(S, C[k], zk);
+        const decay<F> d = decay_of(zk[0]);
+        const F m[1] = {d.m};
+        scale_inputs(S, m, xk);
+        if (A.input_gate) gate_inputs(ik, xk);
+        h[k] = step_or_erase(d.d, h[k], xk[0]);
     }
     layer::store(state, layer::pack<float, V>(h));
     layer::store((T *)A.h + n * A.D + c, layer::pack<T, V>(h));
