@@ -25,14 +25,18 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
-    const course<L> way(B, A.cu_seqlens, A.T, A.N, blocks, joined);
-    const bool loader = w == NW - 1;
-    // asks for a tile's boxes
-    auto ask = [&](const typename course<L>::place &x, int stage) {
-        if (!TMA || x.t.p < 0 || lane != 0) return;
-        const int tok = x.t.a + x.t.p * L, n = gated ? 3 : 2;
+    const bool chains = joined && __ldcg(B.mode) != 0, loader = w == NW - 1;
+    course<L> way(B, A.cu_seqlens, A.T, A.N, blocks, joined, false);
+    // the next tile of the course, its boxes asked for
+    auto ask = [&](int stage) {
+        way.next();
+        if (lane != 0) return;
+        S.next.t[stage] = way.t;
+        if (!TMA || way.t.p < 0) return;
+        const int tok = way.t.a + way.t.p * L, n = gated ? 3 : 2;
+        tc::fence_proxy_async();  // (join() has written to the stage)
         tc::mbar_arrive_expect_tx(&S.next.full[stage], (uint32_t)(n * L * W * sizeof(T)));
-        for (int i = 0; i < n; ++i) tc::tma_load_3d(&S.next.x[stage][i][0][0], &maps.m[i], x.t.block * W, 0, tok, &S.next.full[stage]);
+        for (int i = 0; i < n; ++i) tc::tma_load_3d(&S.next.x[stage][i][0][0], &maps.m[i], way.t.block * W, 0, tok, &S.next.full[stage]);
     };
     if (TMA && threadIdx.x == 0) {
         tc::mbar_init(&S.next.full[0], 1);
@@ -40,21 +44,20 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         tc::fence_proxy_async();
     }
     __syncthreads();
-    typename course<L>::place now = way.begin(false), far = now;
     if (loader) {
-        ask(far, 0);
-        far = way.next(far, false);
-        ask(far, 1);
+        ask(0);
+        ask(1);
     }
+    __syncthreads();
     channel<float2> C{};
     int of = -1;  // the block of channels whose parameters C holds
-    for (int turn = 0; now.t.p >= 0; ++turn) {
-        const tile t = now.t;
+    for (int turn = 0;; ++turn) {
+        const tile t = S.next.t[turn & 1];
+        if (t.p < 0) break;
         const int tok = t.a + t.p * L + w * R, len = t.b - tok < R ? t.b - tok : R;  // tokens of this warp, below 1 where it has none
         const int c = t.block * W + lane * 2, have = A.D - c;
         if (of != t.block) C = load_channel(A.A_log, A.dt_bias, c, have);
         of = t.block;
-        now = way.next(now, false);
         const int stage = turn & 1;
         if (TMA && !tc::mbar_wait(&S.next.full[stage], (turn >> 1) & 1)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
         float2 u[R], d[R], sum = make_float2(0.f, 0.f), h = sum;
@@ -102,12 +105,10 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         *reinterpret_cast<float2 *>(&S.M.g[w][lane * 2]) = sum;
         *reinterpret_cast<float2 *>(&S.M.d[w][lane * 2]) = decay_of(sum).d;
         *reinterpret_cast<float2 *>(&S.M.b[w][lane * 2]) = h;
-        join<R>(B, joined && !way.serial, way.serial, t, A.D, A.initial_state, A.final_state,
-                A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr, (t.b - t.a - t.p * L + CK - 1) / CK, S.M, err);
-        if (loader) {  // every warp is done with this stage
-            far = way.next(far, false);
-            ask(far, stage);
-        }
+        join<R>(B, joined && !chains, t, A.D, A.initial_state, A.final_state,
+                A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr, (t.b - t.a - t.p * L + CK - 1) / CK, S.M,
+                *reinterpret_cast<entries *>(&S.next.x[stage]), err);
+        if (loader) ask(stage);  // every warp is done with this stage
         h = *reinterpret_cast<const float2 *>(&S.M.g[w][lane * 2]);
         // what enters may be an infinity or a NaN, which a decay of 0 erases
         const bool odd = __any_sync(0xffffffffu, !finite(h));
@@ -137,7 +138,7 @@ static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void 
         scan_fwd_kernel<T, TMA><<<grid, NT, smem, stream>>>(*a, B, maps, 0, blocks, err);
         return cudaGetLastError();
     }
-    launch_plan(B, a->cu_seqlens, a->T, a->N, stream, err);
+    launch_plan(B, a->cu_seqlens, a->T, a->N, blocks, grid, stream, err);
     kda_scan_args args = *a;
     row_maps<3> m = maps;
     void *p[] = {&args, &B, &m, &joined, &blocks, &err};

@@ -1,17 +1,18 @@
 // How the two sequence-long directions of kda_scan split a batch and join it again.
 //
-// A tile is L tokens of one sequence by W = 64 channels, taken by one block of threads; it reads its inputs once and
-// keeps what it made of them.  What a tile does to the state that enters it is two numbers per channel, its decay and the state that it
-// leaves from zero, and tiles join at three levels, each in a fixed order, so that the result does not depend on which
-// block ran first:
+// A tile is L tokens of one sequence by W = 64 channels, taken by one block of threads; it reads its inputs once and keeps
+// what it made of them.  The tiles of a sequence and its 64 channels are a chain.  Where the chains are many and none much longer than
+// the rest, a block goes through whole chains, longest first, and hands the state on by shared memory.  Else the blocks take every
+// gridDim-th tile, and tiles join through L2: what a tile does to the state that enters it is two numbers per channel, its decay
+// and the state that it leaves from zero, and there are three levels of them, each folded in a fixed order, so that the
+// result does not depend on which block ran first:
 //   - a tile leaves its (decay, value) as soon as it has them, waiting for nothing;
 //   - the last of 16 tiles folds them into the group's, waiting for the tiles alone;
 //   - the last of 16 groups leaves the state behind it, from the last such state and the groups and tiles since.
-// The state that enters a tile is the fold of what lies between, at most 1 + 15 + 15 entries, and the chain of waits
-// grows by one per 256 tiles.  An entry is one 64-bit word, cleared to all ones before, so that reading it and seeing that it is
-// there are one access: a flag beside the data took a fence, a barrier and a second trip to L2.  The blocks of a
-// cooperative launch, all of them running, take every gridDim-th tile in the direction of the scan: the first tile that is not
-// done waits for none that is not, so that every wait ends; they are limited all the same.
+// The state that enters a tile is the fold of what lies between, at most 1 + 15 + 15 entries, and the chain of waits grows
+// by one per 256 tiles.  An entry is one 64-bit word, cleared to all ones before, so that reading it and seeing that it is there are
+// one access: a flag beside the data took a fence, a barrier and a second trip to L2.  All blocks of a cooperative launch
+// run, and the first tile that is not done waits for none that is not, so that every wait ends; they are limited all the same.
 #pragma once
 #include <cuda.h>
 
@@ -34,7 +35,8 @@ constexpr int G = 16;                   // tiles of a group, groups of a supergr
 // The workspace.  A sequence whose first tile has slot f (lin::chunk_slots) has its groups from f / 16 + n on and its
 // supergroups from f / 256 + n on, for the reason that keeps the slots apart.
 struct board {
-    int32_t *bad;              // whether any of cu_seqlens is
+    int32_t *mode;             // [2]: whether blocks take whole chains; how many chains are taken
+    int4 *order;               // [N] sequences as chains are taken: sequence, 0 (-1: none), first token and that behind the last
     int4 *plan;                // [slots] tiles: sequence, index in it (-1: none), first token and that behind the last
     unsigned long long *entry[3];  // per level [slots, D]: decay and value; of the third level a state
     int64_t slots, words;      // words: of all entries
@@ -55,7 +57,8 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    x.bad = (int32_t *)take(4);
+    x.mode = (int32_t *)take(8);
+    x.order = (int4 *)take(N * sizeof(int4));
     x.plan = (int4 *)take(x.slots * sizeof(int4));
     int64_t before[3];
     for (int i = 0; i < 3; ++i) {
@@ -68,22 +71,24 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
     return at;
 }
 
-// Clears the entries, looks at all of cu_seqlens and says which tiles there are.  Where any part of cu_seqlens is
-// bad no tile waits for another (the slots may not be those that the sequences think), and a block goes through each
-// good sequence by itself.
-__global__ void __launch_bounds__(256) scan_plan_kernel(const __grid_constant__ board B, const int32_t *cu, int64_t T, int64_t N, int *err) {
+// Clears the entries, looks at all of cu_seqlens, lists the tiles and the chains and chooses between the two ways: whole chains where
+// the longest one is no more than a block's share of all tiles (XXX), and where any part of cu_seqlens is bad (the slots may not be
+// those that the sequences think, so that no tile may wait for another).
+__global__ void __launch_bounds__(256) scan_plan_kernel(const __grid_constant__ board B, const int32_t *cu, int64_t T, int64_t N, int blocks,
+                                                        int grid, int *err) {
     const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, each = (int64_t)gridDim.x * 256;
     const int L = B.L;
     // (the entries begin on a 256-byte boundary and end before a multiple of it)
     for (int64_t i = first; i < (B.words + 1) / 2; i += each) reinterpret_cast<uint4 *>(B.entry[0])[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-    // Where in the plan a tile stands: first tiles of all sequences first, then their second ones and so on, so that what a tile
-    // waits for was begun long before it wherever there are several sequences (32 sequences of 4096 channels: XXX).  A tile's place is a sum over
-    // all sequences, so this is for up to 1024 of them; more are short enough in the order of their slots.
-    const bool rounds = N > 1 && N <= 1024;
+    // the tiles of a sequence (an empty one has one, too: its final state; 0: a bad range)
     auto tiles = [&](int64_t n) {
         lin::span s;
         return lin::seq_span(cu, T, N, n, &s) ? s.b > s.a ? (s.b - s.a + L - 1) / L : 1 : 0;
     };
+    // Sums over all sequences are for up to 1024 of them; more are short enough in the order in which they come.
+    const bool sorted = N <= 1024;
+    // Where in the plan a tile stands: first tiles of all sequences first, then their second ones and so on, so that what a tile
+    // waits for was begun long before it wherever there are several sequences.
     for (int64_t i = first; i < B.slots; i += each) {
         int64_t lo = 0, hi = N;
         while (hi - lo > 1) {
@@ -96,10 +101,9 @@ __global__ void __launch_bounds__(256) scan_plan_kernel(const __grid_constant__ 
         int64_t p = -1;
         if (lin::seq_span(cu, T, N, lo, &s)) {
             p = i - (s.a / L + lo);
-            // (an empty sequence has a slot, too: its final state)
             if (p >= 0 && p < tiles(lo)) q = make_int4((int)lo, (int)p, (int)s.a, (int)s.b);
         }
-        if (!rounds) {
+        if (!sorted || N == 1) {
             B.plan[i] = q;
         } else if (q.y >= 0) {
             int64_t at = 0;
@@ -112,37 +116,49 @@ __global__ void __launch_bounds__(256) scan_plan_kernel(const __grid_constant__ 
             if (at < B.slots) B.plan[at] = q;
         }
     }
-    // places behind the last tile
-    if (rounds && blockIdx.x == gridDim.x - 1) {
-        int64_t all = 0;
-        for (int64_t n = threadIdx.x; n < N; n += 256) all += tiles(n);
-        __shared__ unsigned long long total;
-        if (threadIdx.x == 0) total = 0;
-        __syncthreads();
-        atomicAdd(&total, (unsigned long long)all);
-        __syncthreads();
-        for (int64_t i = (int64_t)total + threadIdx.x; i < B.slots; i += 256) B.plan[i] = make_int4(0, -1, 0, 0);
+    for (int64_t n = first; n < N; n += each) {
+        lin::span s;
+        const bool good = lin::seq_span(cu, T, N, n, &s);
+        int64_t at = n;
+        if (sorted) {
+            const int64_t mine = tiles(n);
+            at = 0;
+            for (int64_t m = 0; m < N; ++m) {
+                const int64_t k = tiles(m);
+                at += k > mine || (k == mine && m < n);
+            }
+        }
+        B.order[at] = good ? make_int4((int)n, 0, (int)s.a, (int)s.b) : make_int4((int)n, -1, 0, 0);
     }
     if (blockIdx.x > 0) return;
+    __shared__ unsigned long long total, longest;
+    if (threadIdx.x == 0) total = longest = 0;
+    __syncthreads();
+    unsigned long long all = 0, most = 0;
     bool bad = false;
     for (int64_t n = threadIdx.x; n < N; n += 256) {
-        lin::span s;
-        bad |= !lin::seq_span(cu, T, N, n, &s);
+        const unsigned long long k = tiles(n);
+        all += k;
+        most = most > k ? most : k;
+        bad |= k == 0;
     }
+    atomicAdd(&total, all);
+    atomicMax(&longest, most);
     bad = __syncthreads_or(bad);
+    if (sorted && N > 1)  // places behind the last tile
+        for (int64_t i = (int64_t)total + threadIdx.x; i < B.slots; i += 256) B.plan[i] = make_int4(0, -1, 0, 0);
     if (threadIdx.x == 0) {
-        *B.bad = bad;
+        B.mode[0] = bad || longest * grid <= total * blocks;
+        B.mode[1] = 0;
         if (bad) set_error(err, KDA_ERR_BAD_SEQLENS);
     }
 }
-inline void launch_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, cudaStream_t stream, int *err) {
-    const int64_t words = B.words / 2 > B.slots ? B.words / 2 : B.slots;
+inline void launch_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int grid, cudaStream_t stream, int *err) {
+    int64_t words = B.words / 2 > B.slots ? B.words / 2 : B.slots;
+    if (N > words) words = N;
     const int64_t want = (words + 1023) / 1024;
-    scan_plan_kernel<<<(unsigned)(want < 1216 ? want : 1216), 256, 0, stream>>>(B, cu, T, N, err);
+    scan_plan_kernel<<<(unsigned)(want < 1216 ? want : 1216), 256, 0, stream>>>(B, cu, T, N, blocks, grid, err);
 }
-
-__device__ __forceinline__ void sync_some(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
-__device__ __forceinline__ void arrive_some(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // An entry; its upper half is never all ones
 __device__ __forceinline__ void put(unsigned long long *p, float d, float b) {
@@ -193,151 +209,141 @@ struct tile {
 
 struct tile_memory {
     float g[NW][W], d[NW][W], b[NW][W];  // the warps' sums of log-decays, decays and values; after join() g is the state that enters each warp's tokens
-    float from[W];                       // the state that enters the run of tiles before this one in its group
+    float from[W];                       // the state behind the last tile, where a block takes whole chains
 };
+// entries on their way through a block: those of the supergroup, of the groups and of the tiles before a tile
+typedef unsigned long long entries[1 + 2 * (G - 1)][W];
 
 // With every warp's (g, d, b) of its R tokens in place: leaves the tile's sum for others and finds what enters each warp's tokens.  start, end:
-// the state (or adjoint) before and behind the sequence, [N, D] or NULL; kept: where the checkpoints of this tile go (NULL: nowhere), `room` rows.  links: tiles of this sequence wait for one another; else `serial` may say that M.from is in place for all tiles but the
-// first, and is left so for the next.
+// the state (or adjoint) before and behind the sequence, [N, D] or NULL; kept: where the checkpoints of this tile go (NULL: nowhere), `room` rows.
+// links: tiles of this sequence wait for one another; E: memory that every warp is done with at the first barrier.
 template <int R>
-__device__ __forceinline__ void join(const board &B, bool links, bool serial, const tile &t, int D, const float *start, float *end, float *kept, int room,
-                                     tile_memory &M, int *err) {
-    static_assert(2 * W <= NT, "two halves");
-    const int tid = threadIdx.x, half = tid / W, ch = tid % W, c = t.block * W + ch;
+__device__ __forceinline__ void join(const board &B, bool links, const tile &t, int D, const float *start, float *end, float *kept, int room,
+                                     tile_memory &M, entries &E, int *err) {
+    static_assert(4 * W <= NT, "four quarters");
+    const int tid = threadIdx.x, quarter = tid / W, ch = tid % W, c = t.block * W + ch;
+    const bool more = t.p + 1 < t.count;
     __syncthreads();
-    const int q = links ? t.p % G : 0, gq = links ? t.p / G % G : 0, super = t.p / (G * G);
+    const int q = links ? t.p % G : 0, gq = links ? t.p / G % G : 0, super = links ? t.p / (G * G) : 0;
     const int64_t slot = t.first + t.p;
-    const bool more = links && t.p + 1 < t.count;
-    unsigned long long e[BATCH];
-    if (half == 0) {
-        if (more) {
-            float sum = 0.f, v = 0.f;
+    float sum = 0.f, v = 0.f, h = 0.f;
+    if (quarter == 0) {
+        if (t.p == 0) h = start && c < D ? start[(int64_t)t.n * D + c] : 0.f;
+        else if (!links) h = M.from[ch];
+    }
+    if (links) {
+        unsigned long long e[BATCH];
+        auto fetch = [&](const unsigned long long *p, int from, int n, int to) {  // entries [from, n), up to BATCH
+            n = n - from < BATCH ? n - from : BATCH;
+            if (n <= 0 || c >= D) return;
+            get_batch(p + (int64_t)from * D + c, D, n, e, err);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                sum += M.g[w][ch];
-                v = step_or_erase(M.d[w][ch], v, M.b[w][ch]);
-            }
-            float d = decay_of(sum).d;
-            if (t.p == 0) {  // nothing enters the first tile: its value is the state behind it
-                v = step_or_erase(d, start && c < D ? start[(int64_t)t.n * D + c] : 0.f, v);
-                d = 0.f;
-            }
-            if (c < D) put(B.entry[0] + slot * D + c, d, v);
-            if (q == G - 1 && c < D) {
-                float gd = 1.f, gb = 0.f;
-                for (int i0 = 0; i0 < G - 1; i0 += BATCH) {
-                    const int n = G - 1 - i0 < BATCH ? G - 1 - i0 : BATCH;
-                    get_batch(B.entry[0] + (slot - q + i0) * D + c, D, n, e, err);
+            for (int i = 0; i < BATCH; ++i)
+                if (i < n) E[to + from + i][ch] = e[i];
+        };
+        const unsigned long long *tiles = B.entry[0] + (slot - q) * D,
+                                 *groups = B.entry[1] + ((int64_t)t.first / G + t.n + super * G) * D;
+        if (quarter == 0) {
+            if (more) {
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i)
-                        if (i < n) {
-                            gb = step_or_erase(entry_d(e[i]), gb, entry_b(e[i]));
-                            gd = compose(gd, entry_d(e[i]));
-                        }
+                for (int w = 0; w < NW; ++w) {
+                    sum += M.g[w][ch];
+                    v = step_or_erase(M.d[w][ch], v, M.b[w][ch]);
                 }
-                put(B.entry[1] + ((int64_t)t.first / G + t.n + t.p / G) * D + c, compose(gd, d), step_or_erase(d, gb, v));
+                sum = decay_of(sum).d;
+                if (t.p == 0) {  // nothing enters the first tile: its value is the state behind it
+                    v = step_or_erase(sum, h, v);
+                    sum = 0.f;
+                }
+                if (c < D) put(B.entry[0] + slot * D + c, sum, v);
             }
+        } else if (quarter == 1) {
+            if (super > 0) fetch(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super - 1) * D, 0, 1, 0);
+            fetch(groups, 0, gq, 1);
+        } else if (quarter == 2) {
+            fetch(tiles, 0, q, G);
+        } else {
+            fetch(tiles, BATCH, q, G);
+            fetch(groups, BATCH, gq, 1);
         }
-        if (q > 0 && c < D) get_batch(B.entry[0] + (slot - q) * D + c, D, q < BATCH ? q : BATCH, e, err);
-        sync_some(1, 2 * W);
-        float h = M.from[ch];
-        if (c < D)
-            for (int i0 = 0; i0 < q; i0 += BATCH) {
-                if (i0 > 0) get_batch(B.entry[0] + (slot - q + i0) * D + c, D, q - i0 < BATCH ? q - i0 : BATCH, e, err);
+        __syncthreads();
+    }
+    if (quarter == 0) {
+        if (links && c < D) {
+            if (q == G - 1 && more) {
+                float gd = 1.f, gb = 0.f;
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-                    if (i0 + i < q) h = step_or_erase(entry_d(e[i]), h, entry_b(e[i]));
+                for (int i = 0; i < G - 1; ++i) {
+                    const unsigned long long x = E[G + i][ch];
+                    gb = step_or_erase(entry_d(x), gb, entry_b(x));
+                    gd = compose(gd, entry_d(x));
+                }
+                put(B.entry[1] + ((int64_t)t.first / G + t.n + t.p / G) * D + c, compose(gd, sum), step_or_erase(sum, gb, v));
             }
+            if (super > 0) h = entry_d(E[0][ch]);
+            for (int i = 0; i < gq; ++i) h = step_or_erase(entry_d(E[1 + i][ch]), h, entry_b(E[1 + i][ch]));
+            for (int i = 0; i < q; ++i) h = step_or_erase(entry_d(E[G + i][ch]), h, entry_b(E[G + i][ch]));
+        }
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             if (w * R % CK == 0 && kept && w * R / CK < room && c < D) kept[(int64_t)(w * R / CK) * D + c] = h;
             M.g[w][ch] = h;
             h = step_or_erase(M.d[w][ch], h, M.b[w][ch]);
         }
-        if (more && t.p % (G * G) == G * G - 1 && c < D)
+        if (links && more && t.p % (G * G) == G * G - 1 && c < D)
             put(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super) * D + c, h, 0.f);
-        if (end && c < D && t.p + 1 >= t.count) end[(int64_t)t.n * D + c] = h;
-        if (serial) M.from[ch] = h;
-    } else if (half == 1) {
-        if (!(serial && t.p > 0)) {
-            float v = 0.f;
-            if (t.p == 0) {
-                if (start && c < D) v = start[(int64_t)t.n * D + c];
-            } else if (c < D) {
-                if (super > 0) {
-                    get_batch(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super - 1) * D + c, D, 1, e, err);
-                    v = entry_d(e[0]);
-                }
-                const unsigned long long *groups = B.entry[1] + ((int64_t)t.first / G + t.n + super * G) * D + c;
-                for (int i0 = 0; i0 < gq; i0 += BATCH) {
-                    get_batch(groups + (int64_t)i0 * D, D, gq - i0 < BATCH ? gq - i0 : BATCH, e, err);
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i)
-                        if (i0 + i < gq) v = step_or_erase(entry_d(e[i]), v, entry_b(e[i]));
-                }
-            }
-            M.from[ch] = v;
-        }
-        arrive_some(1, 2 * W);
+        if (end && c < D && !more) end[(int64_t)t.n * D + c] = h;
+        M.from[ch] = h;
     }
     __syncthreads();
 }
 
-// Which tiles a block goes through: every gridDim.x-th, channels innermost; in a batch whose cu_seqlens is bad, all tiles of
-// every gridDim.x-th sequence and block of channels.
+// The tiles that a block goes through, as one warp of it finds them.
 template <int L> struct course {
     const board &B;
     const int32_t *cu;
-    int64_t T, N, items;
-    int blocks, joined, serial;
-    struct place {
-        int64_t item;
-        tile t;
-    };
-    __device__ __forceinline__ course(const board &b, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, int joined_)
-        : B(b), cu(cu_), T(T_), N(N_), blocks(blocks_), joined(joined_) {
-        serial = joined && __ldcg(B.bad) != 0;
-        items = (serial ? N : lin::chunk_slots(T, N, L)) * blocks;
+    int64_t T, N, item;
+    int blocks, back;
+    bool joined, chains;
+    tile t;  // p = -1 behind the last
+    __device__ __forceinline__ course(const board &b, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, bool joined_, bool back_)
+        : B(b), cu(cu_), T(T_), N(N_), item(-1), blocks(blocks_), back(back_), joined(joined_) {
+        chains = joined && __ldcg(B.mode) != 0;
+        t = tile{0, -1, 0, 0, 0, 0, 0};
     }
-    __device__ __forceinline__ tile at(int64_t item, bool back) const {
-        tile t{0, -1, 0, 0, 0, 0, 0};
-        if (item >= items) return t;
-        const int64_t r = back ? items - 1 - item : item, i = r / blocks;
-        t.block = (int)(r - i * blocks);
-        if (joined && !serial) {
-            const int4 q = __ldg(B.plan + i);
-            t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
-        } else {
-            int64_t n = i, p = 0;
-            lin::span s;
-            if (serial ? lin::seq_span(cu, T, N, n, &s) : lin::find_slot(cu, T, N, L, i, &n, &p, &s)) {
-                if (p == 0 || p < (s.b - s.a + L - 1) / L) t.p = (int)p;
-                t.n = (int)n, t.a = (int)s.a, t.b = (int)s.b;
-            }
+    __device__ __forceinline__ void next() {
+        if (chains && t.p + 1 < t.count) {
+            ++t.p;
+            return;
         }
+        const int64_t items = (chains ? N : lin::chunk_slots(T, N, L)) * blocks;
+        do {
+            if (chains) {
+                int ticket = 0;
+                if ((threadIdx.x & 31) == 0) ticket = atomicAdd(B.mode + 1, 1);
+                item = __shfl_sync(0xffffffffu, ticket, 0);
+            } else {
+                item = item < 0 ? blockIdx.x : item + gridDim.x;
+            }
+            t.p = -1;
+            if (item >= items) return;
+            const int64_t r = back && !chains ? items - 1 - item : item, i = r / blocks;
+            t.block = (int)(r - i * blocks);
+            if (joined) {
+                const int4 q = __ldg((chains ? B.order : B.plan) + i);
+                t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
+            } else {
+                int64_t n = 0, p = 0;
+                lin::span s;
+                if (lin::find_slot(cu, T, N, L, i, &n, &p, &s)) {
+                    if (p == 0 || p < (s.b - s.a + L - 1) / L) t.p = (int)p;
+                    t.n = (int)n, t.a = (int)s.a, t.b = (int)s.b;
+                }
+            }
+        } while (t.p < 0);
         t.count = (t.b - t.a + L - 1) / L;
         t.first = t.a / L + t.n;
-        if (back && !serial && t.p >= 0 && t.count > 0) t.p = t.count - 1 - t.p;  // positions count from the end
-        return t;
-    }
-    // Every lane of a warp calls these.
-    __device__ __forceinline__ void skip(place &x, bool back) const {
-        while (x.t.p < 0 && x.item < items) x.t = at(x.item += gridDim.x, back);
-    }
-    __device__ __forceinline__ place begin(bool back) const {
-        place x{(int64_t)blockIdx.x, at(blockIdx.x, back)};
-        skip(x, back);
-        return x;
-    }
-    __device__ __forceinline__ place next(place x, bool back) const {
-        if (x.item >= items) return x;
-        if (serial && x.t.p + 1 < x.t.count) {
-            ++x.t.p;
-            return x;
-        }
-        x.t = at(x.item += gridDim.x, back);
-        skip(x, back);
-        return x;
+        if (back && !chains && t.count > 0) t.p = t.count - 1 - t.p;  // positions count from the end
     }
 };
 
@@ -350,10 +356,11 @@ __device__ __forceinline__ void check_all(const int32_t *cu, int64_t T, int64_t 
     }
 }
 
-// A tile's boxes of NI tensors, two tiles ahead of their use
+// Two tiles and their boxes of NI tensors: each is asked for when the one before the last is done with
 template <typename T, int NI, int L> struct ring {
     T x[2][NI][L][W];
     uint64_t full[2];
+    tile t[2];
 };
 template <int NI> struct row_maps {
     CUtensorMap m[NI];
