@@ -25,6 +25,7 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
+    if (joined) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
     const bool chains = joined && __ldcg(B.mode) != 0, loader = w == NW - 1;
     course<L> way(B, A.cu_seqlens, A.T, A.N, blocks, joined, false);
     // the next tile of the course, its boxes asked for
@@ -61,8 +62,8 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         const int stage = turn & 1;
         if (TMA && !tc::mbar_wait(&S.next.full[stage], (turn >> 1) & 1)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
         float2 u[R], d[R], sum = make_float2(0.f, 0.f), h = sum;
-        // PART tokens at a time: with all eight the logits do not fit beside d and u
-        constexpr int PART = 4;
+        // PART tokens at a time, so that their logits fit beside d and u
+        constexpr int PART = 8;
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += PART) {
             auto get = [&](int k, const void *p, int64_t stride, float2 (&f)[PART]) {
@@ -138,7 +139,6 @@ static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void 
         scan_fwd_kernel<T, TMA><<<grid, NT, smem, stream>>>(*a, B, maps, 0, blocks, err);
         return cudaGetLastError();
     }
-    launch_plan(B, a->cu_seqlens, a->T, a->N, blocks, grid, stream, err);
     kda_scan_args args = *a;
     row_maps<3> m = maps;
     void *p[] = {&args, &B, &m, &joined, &blocks, &err};

@@ -14,6 +14,7 @@
 // one access: a flag beside the data took a fence, a barrier and a second trip to L2.  All blocks of a cooperative launch
 // run, and the first tile that is not done waits for none that is not, so that every wait ends; they are limited all the same.
 #pragma once
+#include <cooperative_groups.h>
 #include <cuda.h>
 
 #include <atomic>
@@ -74,9 +75,9 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
 // Clears the entries, looks at all of cu_seqlens, lists the tiles and the chains and chooses between the two ways: whole chains where
 // the longest one is no more than a block's share of all tiles (XXX), and where any part of cu_seqlens is bad (the slots may not be
 // those that the sequences think, so that no tile may wait for another).
-__global__ void __launch_bounds__(256) scan_plan_kernel(const __grid_constant__ board B, const int32_t *cu, int64_t T, int64_t N, int blocks,
-                                                        int grid, int *err) {
-    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, each = (int64_t)gridDim.x * 256;
+// Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 12 us more.)
+static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int *err) {
+    const int64_t first = (int64_t)blockIdx.x * NT + threadIdx.x, each = (int64_t)gridDim.x * NT;
     const int L = B.L;
     // (the entries begin on a 256-byte boundary and end before a multiple of it)
     for (int64_t i = first; i < (B.words + 1) / 2; i += each) reinterpret_cast<uint4 *>(B.entry[0])[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -130,34 +131,30 @@ __global__ void __launch_bounds__(256) scan_plan_kernel(const __grid_constant__ 
         }
         B.order[at] = good ? make_int4((int)n, 0, (int)s.a, (int)s.b) : make_int4((int)n, -1, 0, 0);
     }
-    if (blockIdx.x > 0) return;
-    __shared__ unsigned long long total, longest;
-    if (threadIdx.x == 0) total = longest = 0;
-    __syncthreads();
-    unsigned long long all = 0, most = 0;
-    bool bad = false;
-    for (int64_t n = threadIdx.x; n < N; n += 256) {
-        const unsigned long long k = tiles(n);
-        all += k;
-        most = most > k ? most : k;
-        bad |= k == 0;
+    if (blockIdx.x == 0) {
+        __shared__ unsigned long long total, longest;
+        if (threadIdx.x == 0) total = longest = 0;
+        __syncthreads();
+        unsigned long long all = 0, most = 0;
+        bool bad = false;
+        for (int64_t n = threadIdx.x; n < N; n += NT) {
+            const unsigned long long k = tiles(n);
+            all += k;
+            most = most > k ? most : k;
+            bad |= k == 0;
+        }
+        atomicAdd(&total, all);
+        atomicMax(&longest, most);
+        bad = __syncthreads_or(bad);
+        if (sorted && N > 1)  // places behind the last tile
+            for (int64_t i = (int64_t)total + threadIdx.x; i < B.slots; i += NT) B.plan[i] = make_int4(0, -1, 0, 0);
+        if (threadIdx.x == 0) {
+            B.mode[0] = bad || longest * gridDim.x <= total * blocks;
+            B.mode[1] = 0;
+            if (bad) set_error(err, KDA_ERR_BAD_SEQLENS);
+        }
     }
-    atomicAdd(&total, all);
-    atomicMax(&longest, most);
-    bad = __syncthreads_or(bad);
-    if (sorted && N > 1)  // places behind the last tile
-        for (int64_t i = (int64_t)total + threadIdx.x; i < B.slots; i += 256) B.plan[i] = make_int4(0, -1, 0, 0);
-    if (threadIdx.x == 0) {
-        B.mode[0] = bad || longest * grid <= total * blocks;
-        B.mode[1] = 0;
-        if (bad) set_error(err, KDA_ERR_BAD_SEQLENS);
-    }
-}
-inline void launch_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int grid, cudaStream_t stream, int *err) {
-    int64_t words = B.words / 2 > B.slots ? B.words / 2 : B.slots;
-    if (N > words) words = N;
-    const int64_t want = (words + 1023) / 1024;
-    scan_plan_kernel<<<(unsigned)(want < 1216 ? want : 1216), 256, 0, stream>>>(B, cu, T, N, blocks, grid, err);
+    cooperative_groups::this_grid().sync();
 }
 
 // An entry; its upper half is never all ones
@@ -330,7 +327,7 @@ template <int L> struct course {
             const int64_t r = back && !chains ? items - 1 - item : item, i = r / blocks;
             t.block = (int)(r - i * blocks);
             if (joined) {
-                const int4 q = __ldg((chains ? B.order : B.plan) + i);
+                const int4 q = __ldcg((chains ? B.order : B.plan) + i);
                 t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
             } else {
                 int64_t n = 0, p = 0;
