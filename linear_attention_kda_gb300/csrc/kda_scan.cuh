@@ -84,6 +84,10 @@ template <typename F> __device__ __forceinline__ decay<F> decay_of(F g) {
 template <typename F> __device__ __forceinline__ F factor(F d) {
     return each([](float v) { return v < 0.f ? 1.f + v : v; }, d);
 }
+// a - 1
+template <typename F> __device__ __forceinline__ F below_one(F d) {
+    return each([](float v) { return v < 0.f ? v : v - 1.f; }, d);
+}
 // a h + u for finite h
 template <typename F> __device__ __forceinline__ F step(F d, F h, F u) {
     return fma(d, h, fma(each([](float v) { return v < 0.f ? 1.f : 0.f; }, d), h, u));
@@ -95,26 +99,39 @@ template <typename F> __device__ __forceinline__ F step_or_erase(F d, F h, F u) 
 __device__ __forceinline__ bool finite(float h) { return fabsf(h) <= 3.402823466e38f; }
 __device__ __forceinline__ bool finite(float2 h) { return finite(h.x) && finite(h.y); }
 
-// g, dg/dz and dg/dA_log
-template <typename F> __device__ __forceinline__ F log_decay(const spec &S, const channel<F> &C, F z, F *dz, F *dA) {
+// For the gradients: N tokens' dg/dz, in the place of z, and dg/dA_log
+template <int N, typename F>
+__device__ __forceinline__ void decay_slopes(const spec &S, const channel<F> &C, F (&z)[N], F (&dA)[N]) {
+    const F k = mul(C.rate, splat<F>(-1.f));
     if (S.gate == KDA_SCAN_LOG) {
-        *dz = splat<F>(1.f);
-        *dA = splat<F>(0.f);
-        return add(z, splat<F>(NUDGE));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            z[i] = splat<F>(1.f);
+            dA[i] = splat<F>(0.f);
+        }
+    } else if (S.gate == KDA_SCAN_LOWER_BOUND) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const F y = add(z[i], C.b);
+            const sig<F> w = sigmoids(mul(C.rate, y));
+            z[i] = mul(mul(mul(splat<F>(S.g_min), C.rate), w.s), w.n);
+            dA[i] = mul(z[i], y);
+        }
+    } else if (S.gate == KDA_SCAN_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const sig<F> w = sigmoids(add(z[i], C.b));
+            dA[i] = mul(k, w.s);
+            z[i] = mul(dA[i], w.n);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const F y = add(z[i], C.b);
+            dA[i] = mul(k, softplus(y));
+            z[i] = mul(k, sigmoid(y));
+        }
     }
-    const F y = add(z, C.b), k = mul(C.rate, splat<F>(-1.f));
-    if (S.gate == KDA_SCAN_LOWER_BOUND) {
-        const sig<F> w = sigmoids(mul(C.rate, y));
-        const F g = fma(splat<F>(S.g_min), w.s, splat<F>(NUDGE));
-        *dz = mul(mul(g, w.n), C.rate);
-        *dA = mul(*dz, y);
-        return g;
-    }
-    const sig<F> w = sigmoids(y);
-    const F g = fma(k, S.gate == KDA_SCAN_SOFTPLUS ? softplus(y) : w.s, splat<F>(NUDGE));
-    *dz = S.gate == KDA_SCAN_SOFTPLUS ? mul(k, w.s) : mul(g, w.n);
-    *dA = g;
-    return g;
 }
 
 // c(a) from m = a - 1: 1 - a^2 = -m (2 + m) has no cancellation.  Where it is not above 0, c = sqrt(1 - a^2) and its

@@ -1,93 +1,309 @@
-// kda_scan_bwd: a thread per (sequence, channel) goes through the tokens.
-#include "kda_internal.h"
-#include "kda_linear.cuh"
-#include "kda_scan.cuh"
+// kda_scan_bwd: tiles of 64 tokens by 64 channels as in kda_scan_fwd, taken from a sequence's last to its first.  With the
+// adjoint lambda_t = dh_t + m_{t+1}, m_t = a_t lambda_t is what goes on to the token before.
+//
+// A thread forms decays and inputs of its eight tokens, runs the state forwards and the adjoint backwards from zero for the
+// tile's sums, and, when it knows what enters from both sides (the state from the tile's checkpoint, the adjoint from the
+// tiles behind it), runs them again: the states are kept in the place of the inputs, and the gates are formed once
+// more, with their slopes, as the adjoint passes.  Sums over tokens for A_log and dt_bias leave a row for each tile, which
+// a second kernel adds up.  About 85 instructions an element for 14 bytes in bf16: bound by instructions as much as by HBM.
+#include "kda_scan_tiles.cuh"
 
 namespace kda {
 namespace scan {
 
-constexpr int CK = KDA_SCAN_CHECKPOINT;
+constexpr int BWD_L = CK;  // a tile begins at a checkpoint
+constexpr int BWD_R = BWD_L / NW;
 
-template <typename T>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(kda_scan_bwd_args A, spec S, float *part, int *err) {
-    const int c = blockIdx.x * 128 + threadIdx.x;
-    const int64_t n = blockIdx.y;
-    lin::span s;
-    const bool good = lin::seq_span(A.cu_seqlens, A.T, A.N, n, &s);
-    if (!good && threadIdx.x == 0) set_error(err, KDA_ERR_BAD_SEQLENS);
-    if (c >= A.D) return;
-    float sA = 0.f, sb = 0.f;
-    if (good) {
-        channel<float> C[1];
-        load_channels<1>(A.A_log, A.dt_bias, c, true, C);
-        float lam = A.grad_final_state ? A.grad_final_state[n * A.D + c] : 0.f, before[CK];
-        for (int64_t k = (s.b - s.a + CK - 1) / CK - 1; k >= 0; --k) {
-            const int64_t t0 = s.a + k * CK;
-            const int len = (int)(s.b - t0 < CK ? s.b - t0 : CK);
-            float h = A.checkpoints[(s.a / CK + n + k) * A.D + c];
-            for (int r = 0; r < len; ++r) {
-                const int64_t t = t0 + r;
-                before[r] = h;
-                float dz, dA;
-                const decay<float> d = decay_of(log_decay(S, C[0], ld((const T *)A.z + t * A.z_stride + c), &dz, &dA));
-                const float m[1] = {d.m};
-                float x[1] = {ld((const T *)A.x + t * A.x_stride + c)}, i[1];
-                scale_inputs(S, m, x);
-                if (A.input_gate) {
-                    i[0] = ld((const T *)A.input_gate + t * A.i_stride + c);
-                    gate_inputs(i, x);
-                }
-                h = step_or_erase(d.d, h, x[0]);
+template <typename T> struct bwd_memory {
+    ring<T, 4, BWD_L> next;
+    tile_memory M;
+    entries E;
+    float f[NW][W];               // the warps' values of the state, then the states that enter their tokens
+    float sA[NW][W], sb[NW][W];   // the warps' sums for A_log and dt_bias
+};
+
+struct sums_of {
+    float *rows;  // [slots][2][D], or NULL
+};
+
+template <typename T, bool TMA>
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1)
+scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<4> maps,
+                const __grid_constant__ sums_of out, int blocks, int *err) {
+    constexpr int L = BWD_L, R = BWD_R;
+    extern __shared__ __align__(128) char memory[];
+    bwd_memory<T> &S = *reinterpret_cast<bwd_memory<T> *>(memory);
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const spec K{A.gate_kind, A.input_scale, A.g_min};
+    const bool gated = A.input_gate != nullptr;
+    if (out.rows)
+        for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < B.slots * 2 * A.D; i += (int64_t)gridDim.x * NT) out.rows[i] = 0.f;
+    make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
+    const bool chains = __ldcg(B.mode) != 0, loader = w == NW - 1;
+    course<L> way(B, A.cu_seqlens, A.T, A.N, blocks, true, true);
+    // the first token of a tile
+    auto begin = [](const tile &t) { return t.a + (t.count > 0 ? t.count - 1 - t.p : 0) * L; };
+    auto ask = [&](int turn) {
+        if (!TMA || lane != 0) return;
+        const tile &t = S.next.t[turn & 3];
+        if (t.p < 0) return;
+        const int stage = turn & 1, tok = begin(t), n = gated ? 4 : 3;
+        tc::mbar_arrive_expect_tx(&S.next.full[stage], (uint32_t)(n * L * W * sizeof(T)));
+        for (int i = 0; i < n; ++i) tc::tma_load_3d(&S.next.x[stage][i][0][0], &maps.m[i], t.block * W, 0, tok, &S.next.full[stage]);
+    };
+    auto advance = [&](int turn) {
+        way.next();
+        if (lane == 0) S.next.t[turn & 3] = way.t;
+        __syncwarp();
+    };
+    if (TMA && threadIdx.x == 0) {
+        tc::mbar_init(&S.next.full[0], 1);
+        tc::mbar_init(&S.next.full[1], 1);
+        tc::fence_proxy_async();
+    }
+    __syncthreads();
+    if (loader) {
+        advance(0);
+        advance(1);
+        ask(0);
+    }
+    __syncthreads();
+    channel<float2> C{};
+    int of = -1;      // the block of channels whose parameters C holds
+    tile last{0, -1, 0, 0, 0, 0, 0};  // the tile before, whose sums are in place
+    auto add_up = [&](int ch) {
+        if (!out.rows || last.p < 0 || last.count == 0 || last.block * W + ch >= A.D) return;
+        float sA = 0.f, sb = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            sA += S.sA[i][ch];
+            sb += S.sb[i][ch];
+        }
+        float *row = out.rows + (int64_t)(last.first + last.p) * 2 * A.D + last.block * W + ch;
+        row[0] = sA;
+        row[A.D] = sb;
+    };
+    for (int turn = 0;; ++turn) {
+        const tile t = S.next.t[turn & 3];
+        if (t.p < 0) break;
+        const int stage = turn & 1, first = begin(t), tok = first + w * R, len = t.b - tok < R ? t.b - tok : R;
+        const int c = t.block * W + lane * 2, have = A.D - c;
+        if (of != t.block) C = load_channel(A.A_log, A.dt_bias, c, have);
+        of = t.block;
+        // the state that enters the tile, asked for early by those who will run it over the warps
+        float checkpoint = 0.f;
+        if (threadIdx.x / W == 2 && t.count > 0 && t.block * W + (int)threadIdx.x % W < A.D)
+            checkpoint = A.checkpoints[((int64_t)t.a / CK + t.n + (first - t.a) / CK) * A.D + t.block * W + threadIdx.x % W];
+        if (TMA && !tc::mbar_wait(&S.next.full[stage], (turn >> 1) & 1)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+        // PART tokens from r0 on of input k (z, x, grad_h, input_gate)
+        constexpr int PART = 4;
+        auto get = [&](int k, int r0, const void *p, int64_t stride, float2 (&f)[PART]) {
+#pragma unroll
+            for (int r = 0; r < PART; ++r)  // (by TMA there are rows of other sequences behind the last token)
+                f[r] = TMA ? load_pair<T, true>(&S.next.x[stage][k][w * R + r0 + r][lane * 2], 2)
+                           : load_pair<T, false>((const T *)p + (int64_t)(tok + r0 + r) * stride + c, r0 + r < len ? have : 0);
+        };
+        float2 u[R], d[R], sum = make_float2(0.f, 0.f), h = sum, m = sum;
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += PART) {
+            float2 z[PART], x[PART];
+            get(0, r0, A.z, A.z_stride, z);
+            log_decays(K, C, z);
+            if (len < r0 + PART) {
+#pragma unroll
+                for (int r = 0; r < PART; ++r)
+                    if (r0 + r >= len) z[r] = make_float2(0.f, 0.f);
             }
-            for (int r = len - 1; r >= 0; --r) {
-                const int64_t t = t0 + r;
-                float dz, dA;
-                const decay<float> d = decay_of(log_decay(S, C[0], ld((const T *)A.z + t * A.z_stride + c), &dz, &dA));
-                const float x = ld((const T *)A.x + t * A.x_stride + c), cf = S.input == KDA_SCAN_INPUT_PLAIN ? 1.f : input_factor(S, d.m);
-                sig<float> w{1.f, 0.f};
-                if (A.input_gate) w = sigmoids(ld((const T *)A.input_gate + t * A.i_stride + c));
-                lam += ld((const T *)A.grad_h + t * A.D + c);
-                st((T *)A.grad_x + t * A.D + c, cf * w.s * lam);
-                if (A.input_gate) st((T *)A.grad_input_gate + t * A.D + c, cf * x * w.s * w.n * lam);
-                const float dg = step_or_erase(d.d, before[r], S.input == KDA_SCAN_INPUT_PLAIN ? 0.f : input_slope(S, factor(d.d), cf) * w.s * x) * lam;
-                st((T *)A.grad_z + t * A.D + c, dg * dz);
-                sA += dg * dA;
-                sb += dg * dz;
-                lam = step_or_erase(d.d, lam, 0.f);
+#pragma unroll
+            for (int r = 0; r < PART; ++r) {
+                const decay<float2> e = decay_of(z[r]);
+                sum = add(sum, z[r]);
+                d[r0 + r] = e.d;
+                z[r] = e.m;
+            }
+            get(1, r0, A.x, A.x_stride, x);
+            scale_inputs(K, z, x);
+            if (gated) {
+                get(3, r0, A.input_gate, A.i_stride, z);
+                gate_inputs(z, x);
+            }
+#pragma unroll
+            for (int r = 0; r < PART; ++r) u[r0 + r] = x[r];
+        }
+        if (len < R) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r >= len) u[r] = make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) h = step(d[r], h, u[r]);
+#pragma unroll
+        for (int r0 = R - PART; r0 >= 0; r0 -= PART) {
+            float2 g[PART];
+            get(2, r0, A.grad_h, A.D, g);
+#pragma unroll
+            for (int r = PART - 1; r >= 0; --r) {
+                if (r0 + r >= len) g[r] = make_float2(0.f, 0.f);
+                m = step(d[r0 + r], add(m, g[r]), make_float2(0.f, 0.f));
             }
         }
-        if (A.grad_initial_state) A.grad_initial_state[n * A.D + c] = lam;
+        *reinterpret_cast<float2 *>(&S.M.g[w][lane * 2]) = sum;
+        *reinterpret_cast<float2 *>(&S.M.d[w][lane * 2]) = decay_of(sum).d;
+        *reinterpret_cast<float2 *>(&S.M.b[w][lane * 2]) = m;
+        *reinterpret_cast<float2 *>(&S.f[w][lane * 2]) = h;
+        join<R, true>(B, !chains, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, err, [&](int quarter, int ch) {
+            if (quarter == 2) {
+                float v = checkpoint;
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    const float b = S.f[i][ch];
+                    S.f[i][ch] = v;
+                    v = step_or_erase(S.M.d[i][ch], v, b);
+                }
+            } else {
+                add_up(ch);
+            }
+        });
+        if (loader) {
+            // every warp is done with the tile before, whose stage the next one takes
+            ask(turn + 1);
+            advance(turn + 2);
+        }
+        h = *reinterpret_cast<const float2 *>(&S.f[w][lane * 2]);
+        m = *reinterpret_cast<const float2 *>(&S.M.g[w][lane * 2]);
+        // what enters may be an infinity or a NaN, which a decay of 0 erases
+        const bool odd = __any_sync(0xffffffffu, !finite(h) || !finite(m));
+        auto erase = [&](float2 &v, float2 by) {
+            if (odd) v = each([](float k, float s) { return k == 0.f ? 0.f : s; }, by, v);
+        };
+#pragma unroll
+        for (int r = 0; r < R; ++r) {  // u: a h before each token
+            const float2 v = u[r];
+            erase(h, d[r]);
+            u[r] = step(d[r], h, make_float2(0.f, 0.f));
+            h = add(u[r], v);
+        }
+        float2 sA = make_float2(0.f, 0.f), sb = sA;
+        const int64_t at = (int64_t)tok * A.D + c;
+#pragma unroll
+        for (int r0 = R - PART; r0 >= 0; r0 -= PART) {
+            if (len <= r0) continue;
+            float2 z[PART], kA[PART], x[PART], g[PART], s[PART], n[PART];
+            get(0, r0, A.z, A.z_stride, z);
+            decay_slopes(K, C, z, kA);
+            get(1, r0, A.x, A.x_stride, x);
+            get(2, r0, A.grad_h, A.D, g);
+            if (gated) {
+                float2 i[PART];
+                get(3, r0, A.input_gate, A.i_stride, i);
+#pragma unroll
+                for (int r = 0; r < PART; ++r) {
+                    const sig<float2> v = sigmoids(i[r]);
+                    s[r] = v.s;
+                    n[r] = v.n;
+                }
+            }
+#pragma unroll
+            for (int r = PART - 1; r >= 0; --r) {
+                const int k = r0 + r;
+                if (k >= len) continue;
+                const float2 lam = add(m, g[r]);
+                m = lam;
+                erase(m, d[k]);
+                m = step(d[k], m, make_float2(0.f, 0.f));
+                float2 xs = gated ? mul(x[r], s[r]) : x[r], q = gated ? mul(s[r], lam) : lam, e = u[k];  // s x, s lambda, dh/dg
+                if (K.input != KDA_SCAN_INPUT_PLAIN) {
+                    const float2 cf = input_factor(K, below_one(d[k]));
+                    e = fma(input_slope(K, factor(d[k]), cf), xs, e);
+                    q = mul(q, cf);
+                }
+                const float2 dg = mul(e, lam), dz = mul(dg, z[r]);
+                sA = fma(dg, kA[r], sA);
+                sb = add(sb, dz);
+                if (have > 0) {
+                    const int64_t o = at + (int64_t)k * A.D;
+                    store_pair<T, TMA>((T *)A.grad_x + o, q, have);
+                    store_pair<T, TMA>((T *)A.grad_z + o, dz, have);
+                    if (gated) store_pair<T, TMA>((T *)A.grad_input_gate + o, mul(mul(q, x[r]), n[r]), have);
+                }
+            }
+        }
+        *reinterpret_cast<float2 *>(&S.sA[w][lane * 2]) = sA;
+        *reinterpret_cast<float2 *>(&S.sb[w][lane * 2]) = sb;
+        last = t;
     }
-    part[(2 * n) * A.D + c] = sA;
-    part[(2 * n + 1) * A.D + c] = sb;
+    __syncthreads();
+    if (threadIdx.x / W == 3) add_up(threadIdx.x % W);
 }
 
-__global__ void __launch_bounds__(128) scan_params_kernel(const float *part, int64_t N, int D, float *dA, float *db) {
-    const int c = blockIdx.x * 128 + threadIdx.x;
-    if (c >= D) return;
-    float sA = 0.f, sb = 0.f;
-    for (int64_t n = 0; n < N; ++n) {
-        sA += part[2 * n * D + c];
-        sb += part[(2 * n + 1) * D + c];
+// Column sums of the tiles' rows: 32 columns to a block, its eight warps every eighth row.
+__global__ void __launch_bounds__(256) scan_sums_kernel(const float *rows, int64_t slots, int D, float *dA, float *db) {
+    __shared__ float part[8][32];
+    float *to = blockIdx.y == 0 ? dA : db;
+    if (!to) return;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float v[4] = {};
+    if (c < D) {
+        const float *p = rows + (int64_t)blockIdx.y * D + c;
+        int64_t r = w;
+        for (; r + 24 < slots; r += 32)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += p[(r + 8 * i) * 2 * D];
+        for (; r < slots; r += 8) v[0] += p[r * 2 * D];
     }
-    if (dA) dA[c] = sA;
-    if (db) db[c] = sb;
+    part[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+    __syncthreads();
+    if (w == 0 && c < D) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += part[i][lane];
+        to[c] = s;
+    }
+}
+
+template <typename T, bool TMA>
+static cudaError_t launch(const kda_scan_bwd_args *a, const row_maps<4> &maps, void *ws, cudaStream_t stream, int *err) {
+    static std::atomic<int> running[64];
+    constexpr size_t smem = sizeof(bwd_memory<T>);
+    int blocks = (a->D + W - 1) / W, grid = 0;
+    board B{};
+    const size_t rows = board_layout(a->T, a->N, a->D, BWD_L, ws, &B);
+    sums_of out{a->grad_A_log || a->grad_dt_bias ? (float *)((char *)ws + rows) : nullptr};
+    cudaError_t e = running_blocks(scan_bwd_kernel<T, TMA>, smem, running, B.slots * blocks, &grid);
+    if (e != cudaSuccess) return e;
+    kda_scan_bwd_args args = *a;
+    row_maps<4> m = maps;
+    void *p[] = {&args, &B, &m, &out, &blocks, &err};
+    e = cudaLaunchCooperativeKernel((const void *)scan_bwd_kernel<T, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+    if (e != cudaSuccess || !out.rows) return e;
+    scan_sums_kernel<<<dim3((a->D + 31) / 32, 2), 256, 0, stream>>>(out.rows, B.slots, a->D, a->grad_A_log, a->grad_dt_bias);
+    return cudaGetLastError();
 }
 
 }  // namespace scan
 }  // namespace kda
 
-size_t kda_scan_bwd_bytes(int64_t, int64_t N, int D, kda_dtype_t) { return (size_t)N * D * 8; }
+size_t kda_scan_bwd_bytes(int64_t T, int64_t N, int D, kda_dtype_t) {
+    using namespace kda::scan;
+    return board_layout(T, N, D, BWD_L, nullptr, nullptr) + (size_t)kda::lin::chunk_slots(T, N, BWD_L) * 2 * D * 4;
+}
 
 kda_status_t kda_launch_scan_bwd(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::scan;
-    const spec S{a->gate_kind, a->input_scale, a->g_min};
-    const dim3 grid((a->D + 127) / 128, (unsigned)a->N);
-    if (a->dtype == KDA_BF16) scan_bwd_kernel<kda::bf16><<<grid, 128, 0, stream>>>(*a, S, (float *)ws, err);
-    else scan_bwd_kernel<float><<<grid, 128, 0, stream>>>(*a, S, (float *)ws, err);
-    if (a->grad_A_log || a->grad_dt_bias)
-        scan_params_kernel<<<grid.x, 128, 0, stream>>>((const float *)ws, a->N, a->D, a->grad_A_log, a->grad_dt_bias);
-    return kda_cuda_status(cudaGetLastError());
+    row_maps<4> maps{};
+    const int64_t es = a->dtype == KDA_BF16 ? 2 : 4, per = 16 / es;
+    const bool tma = a->T > 0 && a->D % per == 0 &&
+                     (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate | (uintptr_t)a->grad_h) & 15) == 0 &&
+                     (((uintptr_t)a->grad_x | (uintptr_t)a->grad_z | (uintptr_t)a->grad_input_gate) % (2 * es)) == 0 && a->x_stride % per == 0 &&
+                     a->z_stride % per == 0 && (!a->input_gate || a->i_stride % per == 0);
+    if (tma && (!make_row_map(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype, BWD_L) ||
+                !make_row_map(&maps.m[1], a->x, a->T, a->D, a->x_stride, a->dtype, BWD_L) ||
+                !make_row_map(&maps.m[2], a->grad_h, a->T, a->D, a->D, a->dtype, BWD_L) ||
+                (a->input_gate && !make_row_map(&maps.m[3], a->input_gate, a->T, a->D, a->i_stride, a->dtype, BWD_L))))
+        return KDA_ERR_CUDA;
+    if (a->dtype == KDA_BF16)
+        return kda_cuda_status(tma ? launch<kda::bf16, true>(a, maps, ws, stream, err) : launch<kda::bf16, false>(a, maps, ws, stream, err));
+    return kda_cuda_status(tma ? launch<float, true>(a, maps, ws, stream, err) : launch<float, false>(a, maps, ws, stream, err));
 }

@@ -106,9 +106,9 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         *reinterpret_cast<float2 *>(&S.M.g[w][lane * 2]) = sum;
         *reinterpret_cast<float2 *>(&S.M.d[w][lane * 2]) = decay_of(sum).d;
         *reinterpret_cast<float2 *>(&S.M.b[w][lane * 2]) = h;
-        join<R>(B, joined && !chains, t, A.D, A.initial_state, A.final_state,
+        join<R, false>(B, joined && !chains, t, A.D, A.initial_state, A.final_state,
                 A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr, (t.b - t.a - t.p * L + CK - 1) / CK, S.M,
-                *reinterpret_cast<entries *>(&S.next.x[stage]), err);
+                *reinterpret_cast<entries *>(&S.next.x[stage]), err, [](int, int) {});
         if (loader) ask(stage);  // every warp is done with this stage
         h = *reinterpret_cast<const float2 *>(&S.M.g[w][lane * 2]);
         // what enters may be an infinity or a NaN, which a decay of 0 erases
@@ -132,7 +132,8 @@ static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void 
     int blocks = (a->D + W - 1) / W, grid = 0;
     const int64_t tiles = lin::chunk_slots(a->T, a->N, fwd_tile<T>) * blocks;
     board B{};
-    int joined = board_layout(a->T, a->N, a->D, fwd_tile<T>, ws, &B) > 0;
+    int joined = a->T > fwd_tile<T>;  // else no sequence has a second tile
+    if (joined) board_layout(a->T, a->N, a->D, fwd_tile<T>, ws, &B);
     const cudaError_t e = running_blocks(scan_fwd_kernel<T, TMA>, smem, running, tiles, &grid);
     if (e != cudaSuccess) return e;
     if (!joined) {
@@ -150,7 +151,8 @@ static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void 
 
 size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D, kda_dtype_t dtype) {
     using namespace kda::scan;
-    return board_layout(T, N, D, dtype == KDA_BF16 ? fwd_tile<kda::bf16> : fwd_tile<float>, nullptr, nullptr);
+    const int L = dtype == KDA_BF16 ? fwd_tile<kda::bf16> : fwd_tile<float>;
+    return T > L ? board_layout(T, N, D, L, nullptr, nullptr) : 0;
 }
 
 kda_status_t kda_launch_scan_fwd(const kda_scan_args *a, void *ws, cudaStream_t stream) {

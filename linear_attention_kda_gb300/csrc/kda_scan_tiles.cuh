@@ -46,9 +46,8 @@ struct board {
 inline int64_t level_slots(int64_t slots, int64_t N, int level) {
     return level == 0 ? slots : level == 1 ? slots / G + N : slots / (G * G) + N;
 }
-// Bytes of the workspace (0 where no sequence can have a second tile); sets *b where it is given.
+// Bytes of the workspace; sets *b where it is given.
 inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *b) {
-    if (T <= L) return 0;
     board x{};
     x.L = L;
     x.slots = lin::chunk_slots(T, N, L);
@@ -75,7 +74,7 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
 // Clears the entries, looks at all of cu_seqlens, lists the tiles and the chains and chooses between the two ways: whole chains where
 // the longest one is no more than a block's share of all tiles (XXX), and where any part of cu_seqlens is bad (the slots may not be
 // those that the sequences think, so that no tile may wait for another).
-// Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 12 us more.)
+// Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 2 us more.)
 static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int *err) {
     const int64_t first = (int64_t)blockIdx.x * NT + threadIdx.x, each = (int64_t)gridDim.x * NT;
     const int L = B.L;
@@ -214,9 +213,11 @@ typedef unsigned long long entries[1 + 2 * (G - 1)][W];
 // With every warp's (g, d, b) of its R tokens in place: leaves the tile's sum for others and finds what enters each warp's tokens.  start, end:
 // the state (or adjoint) before and behind the sequence, [N, D] or NULL; kept: where the checkpoints of this tile go (NULL: nowhere), `room` rows.
 // links: tiles of this sequence wait for one another; E: memory that every warp is done with at the first barrier.
-template <int R>
+// BACK: the direction is from the last token to the first, so from the last warp to the first.  more_work(quarter, channel): what
+// two otherwise idle quarters of the block (2 and 3) do meanwhile.
+template <int R, bool BACK, typename F>
 __device__ __forceinline__ void join(const board &B, bool links, const tile &t, int D, const float *start, float *end, float *kept, int room,
-                                     tile_memory &M, entries &E, int *err) {
+                                     tile_memory &M, entries &E, int *err, F &&more_work) {
     static_assert(4 * W <= NT, "four quarters");
     const int tid = threadIdx.x, quarter = tid / W, ch = tid % W, c = t.block * W + ch;
     const bool more = t.p + 1 < t.count;
@@ -243,7 +244,8 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
         if (quarter == 0) {
             if (more) {
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
+                for (int i = 0; i < NW; ++i) {
+                    const int w = BACK ? NW - 1 - i : i;
                     sum += M.g[w][ch];
                     v = step_or_erase(M.d[w][ch], v, M.b[w][ch]);
                 }
@@ -282,8 +284,9 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
             for (int i = 0; i < q; ++i) h = step_or_erase(entry_d(E[G + i][ch]), h, entry_b(E[G + i][ch]));
         }
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w * R % CK == 0 && kept && w * R / CK < room && c < D) kept[(int64_t)(w * R / CK) * D + c] = h;
+        for (int i = 0; i < NW; ++i) {
+            const int w = BACK ? NW - 1 - i : i;
+            if (!BACK && w * R % CK == 0 && kept && w * R / CK < room && c < D) kept[(int64_t)(w * R / CK) * D + c] = h;
             M.g[w][ch] = h;
             h = step_or_erase(M.d[w][ch], h, M.b[w][ch]);
         }
@@ -291,6 +294,8 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
             put(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super) * D + c, h, 0.f);
         if (end && c < D && !more) end[(int64_t)t.n * D + c] = h;
         M.from[ch] = h;
+    } else if (quarter > 1) {
+        more_work(quarter, ch);
     }
     __syncthreads();
 }
@@ -340,7 +345,7 @@ template <int L> struct course {
         } while (t.p < 0);
         t.count = (t.b - t.a + L - 1) / L;
         t.first = t.a / L + t.n;
-        if (back && !chains && t.count > 0) t.p = t.count - 1 - t.p;  // positions count from the end
+        if (back && !chains && t.count > 0) t.p = t.count - 1 - t.p;  // positions count in the direction of the scan
     }
 };
 
@@ -353,11 +358,11 @@ __device__ __forceinline__ void check_all(const int32_t *cu, int64_t T, int64_t 
     }
 }
 
-// Two tiles and their boxes of NI tensors: each is asked for when the one before the last is done with
+// Boxes of NI tensors of two tiles, and which tiles come next
 template <typename T, int NI, int L> struct ring {
     T x[2][NI][L][W];
     uint64_t full[2];
-    tile t[2];
+    tile t[4];
 };
 template <int NI> struct row_maps {
     CUtensorMap m[NI];
