@@ -41,9 +41,13 @@ template <typename F> struct sig {
     F s, n;
 };
 template <typename F> __device__ __forceinline__ sig<F> sigmoids(F y) {
-    const F e = each([](float v) { return fminf(v, 1e30f); }, ex2(mul(y, splat<F>(-LOG2E))));
-    // (the clamp loses a NaN, y's own is kept)
-    const F s = each([](float v, float w) { return w != w ? w : v; }, rcp(add(e, splat<F>(1.f))), y);
+    // (2^125 and its quotient are in range, so that their product is 1; min.NaN keeps a NaN)
+    const F e = ex2(each([](float v) {
+        float t;
+        asm("min.NaN.f32 %0, %1, 0f42FA0000;" : "=f"(t) : "f"(v));
+        return t;
+    }, mul(y, splat<F>(-LOG2E))));
+    const F s = rcp(add(e, splat<F>(1.f)));
     return {s, mul(e, s)};
 }
 // Softplus(y) = max(y, 0) + ln(1 + e), e = exp(-|y|): ln(1 + e) / e by the polynomial of degree 8 that meets it in the
@@ -134,19 +138,12 @@ __device__ __forceinline__ void decay_slopes(const spec &S, const channel<F> &C,
     }
 }
 
-// c(a) from m = a - 1: 1 - a^2 = -m (2 + m) has no cancellation.  Where it is not above 0, c = sqrt(1 - a^2) and its
-// derivative count as 0.
-template <typename F> __device__ __forceinline__ F input_factor(const spec &S, F m) {
-    const F k = mul(m, splat<F>(-1.f));
-    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return k;
-    // (a NaN's c is 0, but its decay is a NaN, too)
-    const F q = each([](float v) { return fmaxf(v, 0.f); }, mul(k, add(m, splat<F>(2.f))));
-    return mul(q, rsq(add(q, splat<F>(1e-37f))));
-}
-// dc/dg: -a of 1 - a, -a^2 / c of sqrt(1 - a^2)
-template <typename F> __device__ __forceinline__ F input_slope(const spec &S, F a, F c) {
-    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) return mul(a, splat<F>(-1.f));
-    return each([](float v, float w) { return w > 0.f ? -v * v * rcp(w) : (w <= 0.f ? 0.f : w); }, a, c);
+// c(a) = sqrt(1 - a^2) from m = a - 1: 1 - a^2 = -m (2 + m) has no cancellation.  Where it is not above 1e-30, c and its derivative
+// count as 0.  (A NaN's c is 0, but its decay is a NaN, too.)  inverse: 1 / c
+template <typename F> __device__ __forceinline__ F norm_factor(F m, F *inverse) {
+    const F q = each([](float v) { return fmaxf(v, 0.f); }, fma(mul(m, splat<F>(-1.f)), add(m, splat<F>(2.f)), splat<F>(-1e-30f)));
+    *inverse = rsq(add(q, splat<F>(1e-37f)));
+    return mul(q, *inverse);
 }
 
 // N tokens' log-decays from their logits, in place, and what enters at them, x -> c(a) Sigmoid(i) x with m = a - 1.  The
@@ -174,12 +171,38 @@ template <int N, typename F> __device__ __forceinline__ void scale_inputs(const 
         for (int i = 0; i < N; ++i) x[i] = mul(x[i], mul(m[i], splat<F>(-1.f)));
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = mul(x[i], input_factor(S, m[i]));
+        for (int i = 0; i < N; ++i) {
+            F inverse;
+            x[i] = mul(x[i], norm_factor(m[i], &inverse));
+        }
     }
 }
 template <int N, typename F> __device__ __forceinline__ void gate_inputs(const F (&i)[N], F (&x)[N]) {
 #pragma unroll
     for (int k = 0; k < N; ++k) x[k] = mul(x[k], sigmoid(i[k]));
+}
+
+// For the gradients: with d the decays, x what enters but for c(a), and e = a h: e += dc/dg x, and x's factor s *= c.  dc/dg is -a of
+// c = 1 - a and -a^2 / c of sqrt(1 - a^2).
+template <int N, typename F>
+__device__ __forceinline__ void input_slopes(const spec &S, const F *d, const F (&x)[N], F (&e)[N], F (&s)[N]) {
+    const F minus = splat<F>(-1.f);
+    if (S.input == KDA_SCAN_INPUT_COMPLEMENT) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            e[i] = fma(mul(factor(d[i]), minus), x[i], e[i]);
+            s[i] = mul(s[i], mul(below_one(d[i]), minus));
+        }
+    } else if (S.input == KDA_SCAN_INPUT_NORM) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            F inverse;
+            const F c = norm_factor(below_one(d[i]), &inverse), a = factor(d[i]);
+            // (c / c is 0 where c is)
+            e[i] = fma(mul(mul(mul(a, a), inverse), mul(mul(c, inverse), minus)), x[i], e[i]);
+            s[i] = mul(s[i], c);
+        }
+    }
 }
 
 template <int V, typename F>

@@ -95,27 +95,28 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
         if (threadIdx.x / W == 2 && t.count > 0 && t.block * W + (int)threadIdx.x % W < A.D)
             checkpoint = A.checkpoints[((int64_t)t.a / CK + t.n + (first - t.a) / CK) * A.D + t.block * W + threadIdx.x % W];
         if (TMA && !tc::mbar_wait(&S.next.full[stage], (turn >> 1) & 1)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
-        // PART tokens from r0 on of input k (z, x, grad_h, input_gate)
-        constexpr int PART = 4;
-        auto get = [&](int k, int r0, const void *p, int64_t stride, float2 (&f)[PART]) {
+        // some tokens from r0 on of input k (z, x, grad_h, input_gate)
+        auto get = [&](int k, int r0, const void *p, int64_t stride, auto &f) {
+            constexpr int N = sizeof(f) / sizeof(f[0]);
 #pragma unroll
-            for (int r = 0; r < PART; ++r)  // (by TMA there are rows of other sequences behind the last token)
+            for (int r = 0; r < N; ++r)  // (by TMA there are rows of other sequences behind the last token)
                 f[r] = TMA ? load_pair<T, true>(&S.next.x[stage][k][w * R + r0 + r][lane * 2], 2)
                            : load_pair<T, false>((const T *)p + (int64_t)(tok + r0 + r) * stride + c, r0 + r < len ? have : 0);
         };
         float2 u[R], d[R], sum = make_float2(0.f, 0.f), h = sum, m = sum;
+        constexpr int P1 = 4, P2 = 2;  // tokens whose gates are formed at a time, before the join and after it
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += PART) {
-            float2 z[PART], x[PART];
+        for (int r0 = 0; r0 < R; r0 += P1) {
+            float2 z[P1], x[P1];
             get(0, r0, A.z, A.z_stride, z);
             log_decays(K, C, z);
-            if (len < r0 + PART) {
+            if (len < r0 + P1) {
 #pragma unroll
-                for (int r = 0; r < PART; ++r)
+                for (int r = 0; r < P1; ++r)
                     if (r0 + r >= len) z[r] = make_float2(0.f, 0.f);
             }
 #pragma unroll
-            for (int r = 0; r < PART; ++r) {
+            for (int r = 0; r < P1; ++r) {
                 const decay<float2> e = decay_of(z[r]);
                 sum = add(sum, z[r]);
                 d[r0 + r] = e.d;
@@ -128,7 +129,7 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
                 gate_inputs(z, x);
             }
 #pragma unroll
-            for (int r = 0; r < PART; ++r) u[r0 + r] = x[r];
+            for (int r = 0; r < P1; ++r) u[r0 + r] = x[r];
         }
         if (len < R) {
 #pragma unroll
@@ -138,11 +139,11 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
 #pragma unroll
         for (int r = 0; r < R; ++r) h = step(d[r], h, u[r]);
 #pragma unroll
-        for (int r0 = R - PART; r0 >= 0; r0 -= PART) {
-            float2 g[PART];
+        for (int r0 = R - P1; r0 >= 0; r0 -= P1) {
+            float2 g[P1];
             get(2, r0, A.grad_h, A.D, g);
 #pragma unroll
-            for (int r = PART - 1; r >= 0; --r) {
+            for (int r = P1 - 1; r >= 0; --r) {
                 if (r0 + r >= len) g[r] = make_float2(0.f, 0.f);
                 m = step(d[r0 + r], add(m, g[r]), make_float2(0.f, 0.f));
             }
@@ -186,45 +187,52 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
         float2 sA = make_float2(0.f, 0.f), sb = sA;
         const int64_t at = (int64_t)tok * A.D + c;
 #pragma unroll
-        for (int r0 = R - PART; r0 >= 0; r0 -= PART) {
-            if (len <= r0) continue;
-            float2 z[PART], kA[PART], x[PART], g[PART], s[PART], n[PART];
+        for (int r0 = R - P2; r0 >= 0; r0 -= P2) {
+            float2 z[P2], kA[P2], x[P2], s[P2], e[P2], g[P2], lam[P2];
             get(0, r0, A.z, A.z_stride, z);
             decay_slopes(K, C, z, kA);
             get(1, r0, A.x, A.x_stride, x);
             get(2, r0, A.grad_h, A.D, g);
-            if (gated) {
-                float2 i[PART];
-                get(3, r0, A.input_gate, A.i_stride, i);
+            if (len < r0 + P2) {
 #pragma unroll
-                for (int r = 0; r < PART; ++r) {
-                    const sig<float2> v = sigmoids(i[r]);
-                    s[r] = v.s;
-                    n[r] = v.n;
-                }
+                for (int r = 0; r < P2; ++r)
+                    if (r0 + r >= len) z[r] = kA[r] = g[r] = make_float2(0.f, 0.f);
             }
 #pragma unroll
-            for (int r = PART - 1; r >= 0; --r) {
-                const int k = r0 + r;
-                if (k >= len) continue;
-                const float2 lam = add(m, g[r]);
-                m = lam;
-                erase(m, d[k]);
-                m = step(d[k], m, make_float2(0.f, 0.f));
-                float2 xs = gated ? mul(x[r], s[r]) : x[r], q = gated ? mul(s[r], lam) : lam, e = u[k];  // s x, s lambda, dh/dg
-                if (K.input != KDA_SCAN_INPUT_PLAIN) {
-                    const float2 cf = input_factor(K, below_one(d[k]));
-                    e = fma(input_slope(K, factor(d[k]), cf), xs, e);
-                    q = mul(q, cf);
+            for (int r = P2 - 1; r >= 0; --r) {
+                lam[r] = m = add(m, g[r]);
+                erase(m, d[r0 + r]);
+                m = step(d[r0 + r], m, make_float2(0.f, 0.f));
+            }
+            // g: what x is multiplied by but for c(a) and the gate's slope, s (1 - s)
+            if (gated) {
+                get(3, r0, A.input_gate, A.i_stride, g);
+#pragma unroll
+                for (int r = 0; r < P2; ++r) {
+                    const sig<float2> v = sigmoids(g[r]);
+                    s[r] = v.s;
+                    g[r] = mul(v.n, x[r]);
+                    x[r] = mul(x[r], v.s);
                 }
-                const float2 dg = mul(e, lam), dz = mul(dg, z[r]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < P2; ++r) s[r] = make_float2(1.f, 1.f);
+            }
+#pragma unroll
+            for (int r = 0; r < P2; ++r) e[r] = u[r0 + r];
+            input_slopes(K, &d[r0], x, e, s);
+#pragma unroll
+            for (int r = 0; r < P2; ++r) {
+                const float2 dg = mul(e[r], lam[r]);
                 sA = fma(dg, kA[r], sA);
-                sb = add(sb, dz);
-                if (have > 0) {
-                    const int64_t o = at + (int64_t)k * A.D;
-                    store_pair<T, TMA>((T *)A.grad_x + o, q, have);
-                    store_pair<T, TMA>((T *)A.grad_z + o, dz, have);
-                    if (gated) store_pair<T, TMA>((T *)A.grad_input_gate + o, mul(mul(q, x[r]), n[r]), have);
+                z[r] = mul(dg, z[r]);
+                sb = add(sb, z[r]);
+                s[r] = mul(s[r], lam[r]);
+                if (r0 + r < len && have > 0) {
+                    const int64_t o = at + (int64_t)(r0 + r) * A.D;
+                    store_pair<T, TMA>((T *)A.grad_x + o, s[r], have);
+                    store_pair<T, TMA>((T *)A.grad_z + o, z[r], have);
+                    if (gated) store_pair<T, TMA>((T *)A.grad_input_gate + o, mul(s[r], g[r]), have);
                 }
             }
         }
