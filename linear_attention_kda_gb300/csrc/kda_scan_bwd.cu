@@ -104,7 +104,7 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
                            : load_pair<T, false>((const T *)p + (int64_t)(tok + r0 + r) * stride + c, r0 + r < len ? have : 0);
         };
         float2 u[R], d[R], sum = make_float2(0.f, 0.f), h = sum, m = sum;
-        constexpr int P1 = 4, P2 = 2;  // tokens whose gates are formed at a time, before the join and after it
+        constexpr int P1 = 8, P2 = 2;  // tokens whose gates are formed at a time, before the join and after it
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += P1) {
             float2 z[P1], x[P1];
