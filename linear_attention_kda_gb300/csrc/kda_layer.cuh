@@ -94,6 +94,25 @@ __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), e
 __device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
 __device__ __forceinline__ float2 rsq(float2 x) { return make_float2(rsq(x.x), rsq(x.y)); }
 
+constexpr float LOG2E = 1.4426950408889634f;
+
+// Sigmoid(y); 2^-y overflows to infinity and the quotient is 0
+template <typename F> __device__ __forceinline__ F sigmoid(F y) { return rcp(add(ex2(mul(y, splat<F>(-LOG2E))), splat<F>(1.f))); }
+// Sigmoid(y) and 1 - Sigmoid(y), each to a few units of 2^-23 of itself; both 0 where Sigmoid(y) is below 2^-126
+template <typename F> struct sig {
+    F s, n;
+};
+template <typename F> __device__ __forceinline__ sig<F> sigmoids(F y) {
+    // (at most 2^127, whose quotient counts as 0, so that no infinity meets it; min.NaN keeps a NaN)
+    const F e = ex2(each([](float v) {
+        float t;
+        asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(t) : "f"(v));
+        return t;
+    }, mul(y, splat<F>(-LOG2E))));
+    const F s = rcp(add(e, splat<F>(1.f)));
+    return {s, mul(e, s)};
+}
+
 // V values as V / K pairs or single ones
 template <int V> struct lanes {
     static constexpr int K = V % 2 == 0 ? 2 : 1, N = V / K;

@@ -22,6 +22,10 @@ using layer::fma;
 using layer::mul;
 using layer::rcp;
 using layer::rsq;
+using layer::LOG2E;
+using layer::sig;
+using layer::sigmoid;
+using layer::sigmoids;
 using layer::splat;
 
 struct spec {  // how a call forms a and c(a)
@@ -32,24 +36,6 @@ template <typename F> struct channel {  // a channel's parameters: dt_bias and e
     F b, rate;
 };
 
-constexpr float LOG2E = 1.4426950408889634f;
-
-// Sigmoid(y); 2^-y overflows to infinity and the quotient is 0
-template <typename F> __device__ __forceinline__ F sigmoid(F y) { return rcp(add(ex2(mul(y, splat<F>(-LOG2E))), splat<F>(1.f))); }
-// Sigmoid(y) and 1 - Sigmoid(y), each to a few units of 2^-23 of itself
-template <typename F> struct sig {
-    F s, n;
-};
-template <typename F> __device__ __forceinline__ sig<F> sigmoids(F y) {
-    // (2^125 and its quotient are in range, so that their product is 1; min.NaN keeps a NaN)
-    const F e = ex2(each([](float v) {
-        float t;
-        asm("min.NaN.f32 %0, %1, 0f42FA0000;" : "=f"(t) : "f"(v));
-        return t;
-    }, mul(y, splat<F>(-LOG2E))));
-    const F s = rcp(add(e, splat<F>(1.f)));
-    return {s, mul(e, s)};
-}
 // Softplus(y) = max(y, 0) + ln(1 + e), e = exp(-|y|): ln(1 + e) / e by the polynomial of degree 8 that meets it in the
 // Chebyshev points of [0, 1] (2e-7 with its roundings)
 template <typename F> __device__ __forceinline__ F softplus(F y) {

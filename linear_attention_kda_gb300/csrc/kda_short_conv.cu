@@ -1,229 +1,175 @@
-// kda_short_conv_fwd, _bwd, _step: a thread per (token, channel).
-#include "kda_internal.h"
-#include "kda_layer.cuh"
-#include "kda_linear.cuh"
+// kda_short_conv_fwd: a warp takes a run of L tokens of one sequence by 256 channels, eight to a lane, and goes through the
+// tokens with the last K - 1 of them in registers; the sums of a head's squares meet by shuffles between the lanes that
+// hold it.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each run) and y written once: about ten
+// instructions an element for 4 bytes in bf16.
+//
+// kda_short_conv_step: the same for one token, whose history is a slot of a pool.
+#include "kda_short_conv.cuh"
 
 namespace kda {
 namespace conv {
 
-struct spec {
-    int64_t T, N;
-    int D, K, act, norm;
-    float eps;
-    const float *w, *b;
-    const int32_t *cu;
-};
+constexpr int V = 8;
 
-// element e of a sequence's history and tokens, one after the other
-template <typename T>
-__device__ __forceinline__ float row(const spec &S, const T *x, int64_t stride, const T *hist, int64_t n, int64_t a, int64_t e, int c) {
-    if (e < S.K - 1) return hist ? ld(hist + (n * (S.K - 1) + e) * S.D + c) : 0.f;
-    return ld(x + (a + e - (S.K - 1)) * stride + c);
-}
-
-__device__ __forceinline__ float head_sum(float v, int norm) {
-    __shared__ float part[8];
+// One token from its K rows: y's V values
+template <int K>
+__device__ __forceinline__ void one(const spec &S, const taps<V, K> &P, const float2 (&row)[K][V / 2], float2 (&y)[V / 2]) {
+    float ss = 0.f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int w = norm / 32, first = (threadIdx.x >> 5) / w * w;
-    v = 0.f;
-    for (int i = 0; i < w; ++i) v += part[first + i];
-    return v;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) conv_fwd_kernel(spec S, const T *x, int64_t stride, const T *hist, T *y) {
-    const int64_t t = blockIdx.x;
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int64_t n = S.cu ? find_seq(S.cu, (int)S.N, t) : t / (S.T / S.N);
-    lin::span s;
-    if (!lin::seq_span(S.cu, S.T, S.N, n, &s) || t < s.a || t >= s.b) return;
-    float p = 0.f;
-    if (c < S.D) {
-        p = S.b ? S.b[c] : 0.f;
-        for (int j = 0; j < S.K; ++j) p = fmaf(S.w[(int64_t)c * S.K + j], row(S, x, stride, hist, n, s.a, t - s.a + j, c), p);
-        if (S.act) p = p / (1.f + expf(-p));
+    for (int i = 0; i < V / 2; ++i) {
+        y[i] = P.b[i];
+#pragma unroll
+        for (int k = 0; k < K; ++k) y[i] = fma(P.w[k][i], row[k][i], y[i]);
     }
-    if (S.norm) p *= rsqrtf(head_sum(p * p, S.norm) + S.eps);
-    if (c < S.D) st(y + t * S.D + c, p);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) conv_tail_kernel(spec S, const T *x, int64_t stride, const T *hist, T *out, int *err) {
-    const int64_t n = blockIdx.x;
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    lin::span s;
-    if (!lin::seq_span(S.cu, S.T, S.N, n, &s)) {
-        if (threadIdx.x == 0) set_error(err, KDA_ERR_BAD_SEQLENS);
-        return;
-    }
-    if (c >= S.D || !out) return;
-    float v[3];
-    for (int r = 0; r < S.K - 1; ++r) v[r] = row(S, x, stride, hist, n, s.a, s.b - s.a + r, c);
-    for (int r = 0; r < S.K - 1; ++r) st(out + (n * (S.K - 1) + r) * S.D + c, v[r]);
-}
-
-// dL/dp of every token
-template <typename T>
-__global__ void __launch_bounds__(256) conv_dp_kernel(spec S, const T *x, int64_t stride, const T *hist, const T *dy, float *dp) {
-    const int64_t t = blockIdx.x;
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int64_t n = S.cu ? find_seq(S.cu, (int)S.N, t) : t / (S.T / S.N);
-    lin::span s;
-    if (!lin::seq_span(S.cu, S.T, S.N, n, &s) || t < s.a || t >= s.b) return;
-    float p = 0.f, d = 0.f, v = 0.f, sg = 1.f;
-    if (c < S.D) {
-        p = S.b ? S.b[c] : 0.f;
-        for (int j = 0; j < S.K; ++j) p = fmaf(S.w[(int64_t)c * S.K + j], row(S, x, stride, hist, n, s.a, t - s.a + j, c), p);
-        if (S.act) sg = 1.f / (1.f + expf(-p));
-        v = p * sg;
-        d = ld(dy + t * S.D + c);
+    if (S.act) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) y[i] = mul(y[i], layer::sigmoid(y[i]));
     }
     if (S.norm) {
-        const float r = rsqrtf(head_sum(v * v, S.norm) + S.eps);
-        d = r * (d - v * r * (head_sum(d * v, S.norm) * r));
+        float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) q = fma(y[i], y[i], q);
+        ss = head_sum<V>(q.x + q.y, S.norm);
+        const float r = rsqrtf(ss + S.eps);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) y[i] = mul(y[i], make_float2(r, r));
     }
-    if (S.act) d *= sg * (1.f + p * (1.f - sg));
-    if (c < S.D) dp[t * S.D + c] = d;
 }
 
-// dL/d(element e of history and tokens)
-template <typename T>
-__device__ __forceinline__ float row_grad(const spec &S, const float *dp, const T *dtail, int64_t n, const lin::span &s, int64_t e, int c) {
-    const int64_t len = s.b - s.a;
-    float d = 0.f;
-    for (int j = 0; j < S.K; ++j) {
-        const int64_t t = e - j;
-        if (t >= 0 && t < len) d = fmaf(S.w[(int64_t)c * S.K + j], dp[(s.a + t) * S.D + c], d);
-    }
-    if (dtail && e >= len) d += ld(dtail + (n * (S.K - 1) + e - len) * S.D + c);
-    return d;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) conv_dx_kernel(spec S, const float *dp, const T *dtail, T *dx) {
-    const int64_t t = blockIdx.x;
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    const int64_t n = S.cu ? find_seq(S.cu, (int)S.N, t) : t / (S.T / S.N);
+template <typename T, int K, bool WIDE>
+__global__ void __launch_bounds__(128, 4) conv_fwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, T *tail, T *y, int L, int blocks,
+                                                       int64_t items, int *err) {
+    check_all(S, err);
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (item >= items) return;
+    int64_t n, first;
     lin::span s;
-    if (!lin::seq_span(S.cu, S.T, S.N, n, &s) || t < s.a || t >= s.b || c >= S.D) return;
-    st(dx + t * S.D + c, row_grad(S, dp, dtail, n, s, t - s.a + S.K - 1, c));
-}
-
-// per sequence: the history's gradient and the sums for weight and bias
-template <typename T>
-__global__ void __launch_bounds__(256) conv_sums_kernel(spec S, const T *x, int64_t stride, const T *hist, const float *dp, const T *dtail,
-                                                        T *dhist, float *part, int *err) {
-    const int64_t n = blockIdx.x;
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    lin::span s;
-    const bool good = lin::seq_span(S.cu, S.T, S.N, n, &s);
-    if (!good && threadIdx.x == 0) set_error(err, KDA_ERR_BAD_SEQLENS);
-    if (c >= S.D) return;
-    float sum[5] = {};
-    if (good) {
-        for (int r = 0; dhist && r < S.K - 1; ++r) st(dhist + (n * (S.K - 1) + r) * S.D + c, row_grad(S, dp, dtail, n, s, r, c));
-        for (int64_t t = s.a; t < s.b; ++t) {
-            const float d = dp[t * S.D + c];
-            for (int j = 0; j < S.K; ++j) sum[j] = fmaf(d, row(S, x, stride, hist, n, s.a, t - s.a + j, c), sum[j]);
-            sum[4] += d;
+    if (!find_run(S, item / blocks, L, &n, &s, &first)) return;
+    const int c = (int)(item % blocks) * 32 * V + lane * V, have = S.D - c;
+    const int64_t len = s.b - s.a, last = first + L < len ? first + L : len;
+    const rows<T, V, WIDE> X{x + s.a * S.stride + c, hist ? hist + n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
+    if (first < len) {
+        const taps<V, K> P(S, c, have);
+        constexpr int U = 4;  // tokens on their way while as many are computed
+        float2 row[K - 1 + U][V / 2];
+        vec<T, V> next[U];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) layer::unpack<T, V>(X.at(first - (K - 1) + k), row[k]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (first + u < last) next[u] = X.at(first + u);
+        T *out = y + (s.a + first) * S.D + c;
+        for (int64_t t = first; t < last; t += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) layer::unpack<T, V>(next[u], row[K - 1 + u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t + U + u < last) next[u] = X.at(t + U + u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float2 v[V / 2];
+                one<K>(S, P, *reinterpret_cast<const float2(*)[K][V / 2]>(&row[u]), v);
+                if (t + u < last) store<T, V, WIDE>(out, layer::pack<T, V>(v), have);
+                out += S.D;
+            }
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) row[k][i] = row[U + k][i];
         }
     }
-    for (int j = 0; j < 5; ++j) part[(n * 5 + j) * S.D + c] = sum[j];
-}
-
-__global__ void __launch_bounds__(256) conv_params_kernel(const float *part, int64_t N, int D, int K, float *dw, float *db) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= D) return;
-    for (int j = 0; j < 5; ++j) {
-        float v = 0.f;
-        for (int64_t n = 0; n < N; ++n) v += part[(n * 5 + j) * D + c];
-        if (j < K && dw) dw[(int64_t)c * K + j] = v;
-        if (j == 4 && db) db[c] = v;
+    // The history behind the sequence, by the lanes that alone read the one before it: the two may be the same
+    if (tail && first == 0) {
+        vec<T, V> v[K - 1];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) v[k] = X.at(len - (K - 1) + k);
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) store<T, V, WIDE>(tail + (n * (K - 1) + k) * S.D + c, v[k], have);
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) conv_step_kernel(spec S, const T *x, int64_t stride, T *state, const int32_t *idx, int64_t slots,
-                                                        T *y, int *err) {
+template <typename T, int K, bool WIDE>
+__global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ spec S, const T *x, T *state, const int32_t *idx, int64_t slots, T *y,
+                                                        int *err) {
     const int64_t n = blockIdx.x;
-    const int c = blockIdx.y * 256 + threadIdx.x;
     int64_t slot;
-    if (!layer::find_slot<256>(idx, slots, n, &slot, err)) return;
-    float p = 0.f, v[4];
-    if (c < S.D) {
-        p = S.b ? S.b[c] : 0.f;
-        for (int j = 0; j < S.K; ++j) {
-            v[j] = row(S, x + n * stride, stride, (const T *)state, slot, 0, j, c);
-            p = fmaf(S.w[(int64_t)c * S.K + j], v[j], p);
-        }
-        for (int j = 1; j < S.K; ++j) st(state + (slot * (S.K - 1) + j - 1) * S.D + c, v[j]);
-        if (S.act) p = p / (1.f + expf(-p));
-    }
-    if (S.norm) p *= rsqrtf(head_sum(p * p, S.norm) + S.eps);
-    if (c < S.D) st(y + n * S.D + c, p);
+    if (!layer::find_slot<128>(idx, slots, n, &slot, err)) return;
+    const int c = (blockIdx.y * 128 + threadIdx.x) * V, have = S.D - c;
+    T *hist = state + slot * (K - 1) * S.D + c;
+    const rows<T, V, WIDE> X{x + n * S.stride + c, hist, S.stride, S.D, K, have};
+    vec<T, V> v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = X.at(k - (K - 1));
+    const taps<V, K> P(S, c, have);
+    float2 row[K][V / 2], out[V / 2];
+#pragma unroll
+    for (int k = 0; k < K; ++k) layer::unpack<T, V>(v[k], row[k]);
+    one<K>(S, P, row, out);
+#pragma unroll
+    for (int k = 0; k + 1 < K; ++k) store<T, V, WIDE>(hist + k * S.D, v[k + 1], have);
+    store<T, V, WIDE>(y + n * S.D + c, layer::pack<T, V>(out), have);
 }
 
-template <typename A>
-static spec spec_of(const A *a) {
-    return {a->T, a->N, a->D, a->K, a->activation, a->norm_dim, a->norm_eps, a->weight, a->bias, a->cu_seqlens};
-}
-
-template <typename T>
+template <typename T, int K, bool WIDE>
 static void fwd(const kda_short_conv_args *a, cudaStream_t stream, int *err) {
-    const spec S = spec_of(a);
-    const unsigned by = (a->D + 255) / 256;
-    if (a->T > 0) conv_fwd_kernel<T><<<dim3((unsigned)a->T, by), 256, 0, stream>>>(S, (const T *)a->x, a->x_stride, (const T *)a->initial_state, (T *)a->y);
-    conv_tail_kernel<T><<<dim3((unsigned)a->N, by), 256, 0, stream>>>(S, (const T *)a->x, a->x_stride, (const T *)a->initial_state, (T *)a->final_state, err);
+    const int blocks = (a->D + 32 * V - 1) / (32 * V);
+    // Runs of 64 tokens read 5 % of them twice (from L2), of 16 a fifth: short ones where long ones leave SMs without
+    // eight warps.
+    int L = 64;
+    while (L > 16 && (a->T / L) * blocks < 8 * 152) L /= 2;
+    const int64_t items = lin::chunk_slots(a->T, a->N, L) * blocks;
+    conv_fwd_kernel<T, K, WIDE><<<(unsigned)((items + 3) / 4), 128, 0, stream>>>(spec_of(a, a->T, a->cu_seqlens), (const T *)a->x,
+                                                                                (const T *)a->initial_state, (T *)a->final_state, (T *)a->y, L,
+                                                                                blocks, items, err);
 }
 
-template <typename T>
-static void bwd(const kda_short_conv_bwd_args *a, void *ws, cudaStream_t stream, int *err) {
-    const spec S = spec_of(a);
-    const unsigned by = (a->D + 255) / 256;
-    float *dp = (float *)ws, *part = dp + a->T * a->D;
-    const T *x = (const T *)a->x, *hist = (const T *)a->initial_state, *dtail = (const T *)a->grad_final_state;
-    if (a->T > 0) {
-        conv_dp_kernel<T><<<dim3((unsigned)a->T, by), 256, 0, stream>>>(S, x, a->x_stride, hist, (const T *)a->grad_y, dp);
-        conv_dx_kernel<T><<<dim3((unsigned)a->T, by), 256, 0, stream>>>(S, dp, dtail, (T *)a->grad_x);
-    }
-    conv_sums_kernel<T><<<dim3((unsigned)a->N, by), 256, 0, stream>>>(S, x, a->x_stride, hist, dp, dtail, (T *)a->grad_initial_state, part, err);
-    if (a->grad_weight || a->grad_bias) conv_params_kernel<<<by, 256, 0, stream>>>(part, a->N, a->D, a->K, a->grad_weight, a->grad_bias);
+template <typename T, int K, bool WIDE>
+static void step(const kda_short_conv_step_args *a, cudaStream_t stream, int *err) {
+    const int per = 128 * V;
+    conv_step_kernel<T, K, WIDE><<<dim3((unsigned)a->N, (a->D + per - 1) / per), 128, 0, stream>>>(
+        spec_of(a, a->N, nullptr), (const T *)a->x, (T *)a->state, a->state_indices, a->num_slots, (T *)a->y, err);
+}
+
+template <typename T, typename A, typename F>
+static void choose(const A *a, bool wide, F &&go) {
+    auto taps_of = [&](auto k) {
+        if (wide) go(k, std::true_type{});
+        else go(k, std::false_type{});
+    };
+    if (a->K == 2) taps_of(std::integral_constant<int, 2>{});
+    else if (a->K == 3) taps_of(std::integral_constant<int, 3>{});
+    else taps_of(std::integral_constant<int, 4>{});
 }
 
 }  // namespace conv
 }  // namespace kda
 
-size_t kda_short_conv_bwd_bytes(int64_t T, int64_t N, int D, int) { return (size_t)(T + 5 * N) * D * 4; }
-
 kda_status_t kda_launch_short_conv_fwd(const kda_short_conv_args *a, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
-    if (a->dtype == KDA_BF16) kda::conv::fwd<kda::bf16>(a, stream, err);
-    else kda::conv::fwd<float>(a, stream, err);
-    return kda_cuda_status(cudaGetLastError());
-}
-
-kda_status_t kda_launch_short_conv_bwd(const kda_short_conv_bwd_args *a, void *ws, cudaStream_t stream) {
-    int *err = kda_device_error_ptr();
-    if (!err) return KDA_ERR_CUDA;
-    if (a->dtype == KDA_BF16) kda::conv::bwd<kda::bf16>(a, ws, stream, err);
-    else kda::conv::bwd<float>(a, ws, stream, err);
+    using namespace kda::conv;
+    const bool wide = a->D % V == 0 && a->x_stride % V == 0 &&
+                      (((uintptr_t)a->x | (uintptr_t)a->y | (uintptr_t)a->initial_state | (uintptr_t)a->final_state) & 15) == 0;
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        choose<T>(a, wide, [&](auto k, auto w) { fwd<T, decltype(k)::value, decltype(w)::value>(a, stream, err); });
+    };
+    if (a->dtype == KDA_BF16) go(kda::bf16{});
+    else go(float{});
     return kda_cuda_status(cudaGetLastError());
 }
 
 kda_status_t kda_launch_short_conv_step(const kda_short_conv_step_args *a, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
-    const kda::conv::spec S{a->N, a->N, a->D, a->K, a->activation, a->norm_dim, a->norm_eps, a->weight, a->bias, nullptr};
-    const dim3 grid((unsigned)a->N, (a->D + 255) / 256);
-    using kda::bf16;
-    if (a->dtype == KDA_BF16)
-        kda::conv::conv_step_kernel<bf16><<<grid, 256, 0, stream>>>(S, (const bf16 *)a->x, a->x_stride, (bf16 *)a->state, a->state_indices, a->num_slots, (bf16 *)a->y, err);
-    else
-        kda::conv::conv_step_kernel<float><<<grid, 256, 0, stream>>>(S, (const float *)a->x, a->x_stride, (float *)a->state, a->state_indices, a->num_slots, (float *)a->y, err);
+    using namespace kda::conv;
+    const bool wide = a->D % V == 0 && a->x_stride % V == 0 && (((uintptr_t)a->x | (uintptr_t)a->y | (uintptr_t)a->state) & 15) == 0;
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        choose<T>(a, wide, [&](auto k, auto w) { step<T, decltype(k)::value, decltype(w)::value>(a, stream, err); });
+    };
+    if (a->dtype == KDA_BF16) go(kda::bf16{});
+    else go(float{});
     return kda_cuda_status(cudaGetLastError());
 }

@@ -1,0 +1,112 @@
+// Shared by the kernels of the short convolution.
+#pragma once
+#include "kda_internal.h"
+#include "kda_layer.cuh"
+#include "kda_linear.cuh"
+
+namespace kda {
+namespace conv {
+
+using layer::add;
+using layer::fma;
+using layer::mul;
+using layer::splat;
+using layer::vec;
+
+struct spec {
+    int64_t T, N;
+    int D, K, act, norm;
+    float eps;
+    const float *w, *b;
+    const int32_t *cu;
+    int64_t stride;  // of x
+};
+template <typename A> inline spec spec_of(const A *a, int64_t T, const int32_t *cu) {
+    return {T, a->N, a->D, a->K, a->activation, a->norm_dim, a->norm_eps, a->weight, a->bias, cu, a->x_stride};
+}
+
+// V channels from p on, of which `have` exist: as 16-byte (8-byte) vectors where every row allows them (WIDE), else one by one
+template <typename T, int V, bool WIDE> __device__ __forceinline__ vec<T, V> load(const T *p, int have) {
+    vec<T, V> v;
+    if constexpr (WIDE) {
+        if (have > 0) v = layer::load<T, V>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < have) v.x[i] = p[i];
+    }
+    return v;
+}
+template <typename T, int V, bool WIDE> __device__ __forceinline__ void store(T *p, const vec<T, V> &v, int have) {
+    if constexpr (WIDE) {
+        if (have > 0) layer::store_once(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < have) p[i] = v.x[i];
+    }
+}
+template <typename T, int V> __device__ __forceinline__ vec<T, V> zeros() {
+    vec<T, V> v;
+#pragma unroll
+    for (int i = 0; i < V; ++i) st(&v.x[i], 0.f);
+    return v;
+}
+
+// Taps and bias of V channels
+template <int V, int K> struct taps {
+    float2 w[K][V / 2], b[V / 2];
+    __device__ __forceinline__ taps(const spec &S, int c, int have) {
+        float t[K][V], u[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            u[v] = S.b && v < have ? S.b[c + v] : 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) t[k][v] = v < have ? S.w[(int64_t)(c + v) * K + k] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            b[i] = make_float2(u[2 * i], u[2 * i + 1]);
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][i] = make_float2(t[k][2 * i], t[k][2 * i + 1]);
+        }
+    }
+};
+
+// Sums over the lanes that hold a head (norm / V of them, V channels each)
+template <int V> __device__ __forceinline__ float head_sum(float v, int norm) {
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2)
+        if (off * V < norm) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// Where rows of a sequence come from: its history and then its tokens
+template <typename T, int V, bool WIDE> struct rows {
+    const T *x, *hist;  // the sequence's first token and history (NULL: zeros), at this lane's channels
+    int64_t stride, D;
+    int K, have;
+    __device__ __forceinline__ vec<T, V> at(int64_t i) const {  // token i, from -(K - 1) on
+        if (i >= 0) return load<T, V, WIDE>(x + i * stride, have);
+        return hist ? load<T, V, WIDE>(hist + (i + K - 1) * D, have) : zeros<T, V>();
+    }
+};
+
+// The sequence and the run of L tokens of a slot.  False: none; an empty sequence has a run of no tokens.
+__device__ __forceinline__ bool find_run(const spec &S, int64_t slot, int L, int64_t *n, lin::span *s, int64_t *first) {
+    int64_t i;
+    if (!lin::find_slot(S.cu, S.T, S.N, L, slot, n, &i, s)) return false;
+    *first = i * L;
+    return i == 0 || s->a + *first < s->b;
+}
+
+__device__ __forceinline__ void check_all(const spec &S, int *err) {
+    if (blockIdx.x > 0 || blockIdx.y > 0) return;
+    for (int64_t n = threadIdx.x; n < S.N; n += blockDim.x) {
+        lin::span s;
+        if (!lin::seq_span(S.cu, S.T, S.N, n, &s)) set_error(err, KDA_ERR_BAD_SEQLENS);
+    }
+}
+
+}  // namespace conv
+}  // namespace kda

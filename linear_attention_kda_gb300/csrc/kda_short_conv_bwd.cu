@@ -1,0 +1,222 @@
+// kda_short_conv_bwd: a warp takes a run of L tokens of one sequence by 32 V channels.  At token t it forms p, s and y once
+// more, from the last K rows in registers, and with them
+//     ds = (dy - y sum(dy y)) / |s|  (or dy),      dp_t = ds dSwish(p)  (or ds),
+// whose last K - 1 are in registers too: dx_{t-K+1} = sum_j weight_j dp_{t-j} is then complete, for K - 1 tokens behind
+// the run as well, whose dp is formed a second time by the next one.  weight and bias gather their sums over tokens in
+// registers; the eight warps of a block, which have eight runs of the same channels, add theirs up in shared memory, and
+// a second kernel adds up the blocks' rows, all in a fixed order.  About twenty instructions an element for 6 bytes in bf16.
+#include "kda_short_conv.cuh"
+
+namespace kda {
+namespace conv {
+
+constexpr int NW = 8;
+
+template <typename T, int K, int V, bool WIDE>
+__global__ void __launch_bounds__(32 * NW)
+conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const T *dy, const T *dtail, T *dx, T *dhist, float *sums, int L,
+                int64_t slots, int *err) {
+    __shared__ float part[NW][32 * V];
+    check_all(S, err);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t slot = (int64_t)blockIdx.x * NW + w;
+    const int c = (int)blockIdx.y * 32 * V + lane * V, have = S.D - c;
+    float2 dw[K][V / 2], db[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        db[i] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) dw[k][i] = db[i];
+    }
+    int64_t n, first;
+    lin::span s;
+    if (slot < slots && find_run(S, slot, L, &n, &s, &first)) {
+        const int64_t len = s.b - s.a, last = first + L < len ? first + L : len;  // this run's tokens
+        const rows<T, V, WIDE> X{x + s.a * S.stride + c, hist ? hist + n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
+        const T *g = dy + s.a * S.D + c;
+        const taps<V, K> P(S, c, have);
+        constexpr int U = 2;
+        float2 row[K - 1 + U][V / 2], dp[K - 1 + U][V / 2];
+        vec<T, V> nx[U], ng[U];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) {
+            layer::unpack<T, V>(X.at(first - (K - 1) + k), row[k]);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) dp[k][i] = make_float2(0.f, 0.f);
+        }
+        // tokens behind the run's end that its gradients need; those behind the sequence have dp = 0
+        const int64_t stop = last + K - 1;
+        auto fetch = [&](int64_t t, int u) {
+            if (t < stop && t < len) {
+                nx[u] = X.at(t);
+                ng[u] = load<T, V, WIDE>(g + t * S.D, have);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(first + u, u);
+        for (int64_t t0 = first; t0 < stop; t0 += U) {
+            float2 d[U][V / 2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                layer::unpack<T, V>(nx[u], row[K - 1 + u]);
+                layer::unpack<T, V>(ng[u], d[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) fetch(t0 + U + u, u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t0 + u;
+                float2 p[V / 2], ds[V / 2];
+                float2 q = make_float2(0.f, 0.f), e = q;
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    p[i] = P.b[i];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) p[i] = fma(P.w[k][i], row[u + k][i], p[i]);
+                    ds[i] = make_float2(1.f, 1.f);
+                    if (S.act) {
+                        const layer::sig<float2> v = layer::sigmoids(p[i]);
+                        ds[i] = fma(mul(p[i], v.n), v.s, v.s);
+                        p[i] = mul(p[i], v.s);
+                    }
+                    q = fma(p[i], p[i], q);
+                    e = fma(d[u][i], p[i], e);
+                }
+                if (S.norm) {
+                    const float r = rsqrtf(head_sum<V>(q.x + q.y, S.norm) + S.eps), dot = head_sum<V>(e.x + e.y, S.norm) * r * r;
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i)
+                        d[u][i] = mul(fma(p[i], make_float2(-dot, -dot), d[u][i]), make_float2(r, r));
+                }
+                const bool there = t < len, own = t < last;
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    d[u][i] = there ? mul(d[u][i], ds[i]) : make_float2(0.f, 0.f);
+                    dp[K - 1 + u][i] = d[u][i];
+                }
+                if (own) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        db[i] = add(db[i], d[u][i]);
+#pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k][i] = fma(d[u][i], row[u + k][i], dw[k][i]);
+                    }
+                }
+                // row t - K + 1 of the sequence, its history's where that is below 0
+                const int64_t at = t - (K - 1);
+                if (at < last && (at >= first || first == 0) && (at >= 0 || dhist)) {
+                    float2 v[V / 2];
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        v[i] = mul(P.w[0][i], dp[K - 1 + u][i]);
+#pragma unroll
+                        for (int k = 1; k < K; ++k) v[i] = fma(P.w[k][i], dp[K - 1 + u - k][i], v[i]);
+                    }
+                    if (dtail && at >= len - (K - 1)) {
+                        float2 f[V / 2];
+                        layer::unpack<T, V>(load<T, V, WIDE>(dtail + (n * (K - 1) + at - len + K - 1) * S.D + c, have), f);
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) v[i] = add(v[i], f[i]);
+                    }
+                    store<T, V, WIDE>(at >= 0 ? dx + (s.a + at) * S.D + c : dhist + (n * (K - 1) + at + K - 1) * S.D + c, layer::pack<T, V>(v), have);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    row[k][i] = row[U + k][i];
+                    dp[k][i] = dp[U + k][i];
+                }
+        }
+    }
+    if (!sums) return;
+    // [block of runs][K + 1][D]
+#pragma unroll
+    for (int k = 0; k <= K; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) *reinterpret_cast<float2 *>(&part[w][lane * V + 2 * i]) = k < K ? dw[k < K ? k : 0][i] : db[i];
+        __syncthreads();
+        for (int ch = threadIdx.x; ch < 32 * V; ch += 32 * NW) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) v += part[i][ch];
+            const int at = (int)blockIdx.y * 32 * V + ch;
+            if (at < S.D) sums[((int64_t)blockIdx.x * (K + 1) + k) * S.D + at] = v;
+        }
+    }
+}
+
+// Column sums of the blocks' rows: 32 columns of one tap (or the bias) to a block, its eight warps every eighth row.
+__global__ void __launch_bounds__(256) conv_sums_kernel(const float *sums, int64_t rows, int D, int K, float *dw, float *db) {
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, k = blockIdx.y;
+    if (!(k < K ? dw : db)) return;
+    float v = 0.f;
+    if (c < D)
+        for (int64_t r = w; r < rows; r += 8) v += sums[(r * (K + 1) + k) * D + c];
+    part[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && c < D) {
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += part[i][lane];
+        if (k < K) dw[(int64_t)c * K + k] = v;
+        else db[c] = v;
+    }
+}
+
+// Tokens of a run: long ones form less dp twice (K - 1 tokens of each), short ones make more blocks.
+static int run_length(int64_t T, int D) {
+    int L = 128;
+    while (L > 16 && (T / (L * NW)) * ((D + 127) / 128) < 2 * 152) L /= 2;
+    return L;
+}
+
+template <typename T, int K, int V, bool WIDE>
+static void launch(const kda_short_conv_bwd_args *a, float *sums, cudaStream_t stream, int *err) {
+    const int L = run_length(a->T, a->D);
+    const int64_t slots = lin::chunk_slots(a->T, a->N, L), rows = (slots + NW - 1) / NW;
+    const dim3 grid((unsigned)rows, (a->D + 32 * V - 1) / (32 * V));
+    conv_bwd_kernel<T, K, V, WIDE><<<grid, 32 * NW, 0, stream>>>(spec_of(a, a->T, a->cu_seqlens), (const T *)a->x, (const T *)a->initial_state,
+                                                              (const T *)a->grad_y, (const T *)a->grad_final_state, (T *)a->grad_x,
+                                                              (T *)a->grad_initial_state, sums, L, slots, err);
+    if (sums) conv_sums_kernel<<<dim3((a->D + 31) / 32, K + 1), 256, 0, stream>>>(sums, rows, a->D, K, a->grad_weight, a->grad_bias);
+}
+
+template <typename T, int K>
+static void choose(const kda_short_conv_bwd_args *a, float *sums, bool wide, cudaStream_t stream, int *err) {
+    // four channels a lane, eight where a head is 256 wide and has to lie in a warp
+    if (a->norm_dim == 256) wide ? launch<T, K, 8, true>(a, sums, stream, err) : launch<T, K, 8, false>(a, sums, stream, err);
+    else wide ? launch<T, K, 4, true>(a, sums, stream, err) : launch<T, K, 4, false>(a, sums, stream, err);
+}
+
+}  // namespace conv
+}  // namespace kda
+
+size_t kda_short_conv_bwd_bytes(int64_t T, int64_t N, int D, int K) {
+    using namespace kda::conv;
+    return (size_t)((kda::lin::chunk_slots(T, N, run_length(T, D)) + NW - 1) / NW) * (K + 1) * D * 4;
+}
+
+kda_status_t kda_launch_short_conv_bwd(const kda_short_conv_bwd_args *a, void *ws, cudaStream_t stream) {
+    int *err = kda_device_error_ptr();
+    if (!err) return KDA_ERR_CUDA;
+    using namespace kda::conv;
+    const int V = a->norm_dim == 256 ? 8 : 4;
+    const uintptr_t bytes = V * (a->dtype == KDA_BF16 ? 2 : 4) < 16 ? 8 : 16;
+    const bool wide = a->D % V == 0 && a->x_stride % V == 0 &&
+                      (((uintptr_t)a->x | (uintptr_t)a->grad_y | (uintptr_t)a->grad_x | (uintptr_t)a->initial_state |
+                        (uintptr_t)a->grad_final_state | (uintptr_t)a->grad_initial_state) % bytes) == 0;
+    float *sums = a->grad_weight || a->grad_bias ? (float *)ws : nullptr;
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        if (a->K == 2) choose<T, 2>(a, sums, wide, stream, err);
+        else if (a->K == 3) choose<T, 3>(a, sums, wide, stream, err);
+        else choose<T, 4>(a, sums, wide, stream, err);
+    };
+    if (a->dtype == KDA_BF16) go(kda::bf16{});
+    else go(float{});
+    return kda_cuda_status(cudaGetLastError());
+}
