@@ -1,7 +1,6 @@
-// kda_short_conv_fwd: a warp takes a run of L tokens of one sequence by 256 channels, eight to a lane, and goes through the
+// kda_short_conv_fwd: a warp takes a run of L tokens of one sequence by 32 V channels, V to a lane, and goes through the
 // tokens with the last K - 1 of them in registers; the sums of a head's squares meet by shuffles between the lanes that
-// hold it.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each run) and y written once: about ten
-// instructions an element for 4 bytes in bf16.
+// hold it.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each run) and y written once.
 //
 // kda_short_conv_step: the same for one token, whose history is a slot of a pool.
 #include "kda_short_conv.cuh"
@@ -9,10 +8,8 @@
 namespace kda {
 namespace conv {
 
-constexpr int V = 8;
-
 // One token from its K rows: y's V values
-template <int K>
+template <int K, int V>
 __device__ __forceinline__ void one(const spec &S, const taps<V, K> &P, const float2 (&row)[K][V / 2], float2 (&y)[V / 2]) {
     float ss = 0.f;
 #pragma unroll
@@ -36,41 +33,44 @@ __device__ __forceinline__ void one(const spec &S, const taps<V, K> &P, const fl
     }
 }
 
-template <typename T, int K, bool WIDE>
-__global__ void __launch_bounds__(128, 4) conv_fwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, T *tail, T *y, int L, int blocks,
+template <typename T, int K, int V, bool WIDE>
+__global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, T *tail, T *y, int L, int blocks,
                                                        int64_t items, int *err) {
     check_all(S, err);
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (item >= items) return;
-    int64_t n, first;
-    lin::span s;
-    if (!find_run(S, item / blocks, L, &n, &s, &first)) return;
+    run r;
+    if (!find_run(S, item / blocks, L, &r)) return;
     const int c = (int)(item % blocks) * 32 * V + lane * V, have = S.D - c;
-    const int64_t len = s.b - s.a, last = first + L < len ? first + L : len;
-    const rows<T, V, WIDE> X{x + s.a * S.stride + c, hist ? hist + n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
-    if (first < len) {
+    const rows<T, V, WIDE> X{x + r.a * S.stride + c, hist ? hist + r.n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
+    if (r.first < r.last) {
         const taps<V, K> P(S, c, have);
         constexpr int U = 4;  // tokens on their way while as many are computed
         float2 row[K - 1 + U][V / 2];
         vec<T, V> next[U];
+        const T *from = X.x + r.first * S.stride;
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) layer::unpack<T, V>(X.at(first - (K - 1) + k), row[k]);
+        for (int k = 0; k < K - 1; ++k) layer::unpack<T, V>(X.at(r.first - (K - 1) + k), row[k]);
+        auto fetch = [&](int left) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (first + u < last) next[u] = X.at(first + u);
-        T *out = y + (s.a + first) * S.D + c;
-        for (int64_t t = first; t < last; t += U) {
+            for (int u = 0; u < U; ++u) {
+                if (u < left) next[u] = load<T, V, WIDE>(from, have);
+                from += S.stride;
+            }
+        };
+        int left = r.last - r.first;
+        fetch(left);
+        T *out = y + (r.a + r.first) * S.D + c;
+        for (; left > 0; left -= U) {
 #pragma unroll
             for (int u = 0; u < U; ++u) layer::unpack<T, V>(next[u], row[K - 1 + u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + U + u < last) next[u] = X.at(t + U + u);
+            fetch(left - U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float2 v[V / 2];
-                one<K>(S, P, *reinterpret_cast<const float2(*)[K][V / 2]>(&row[u]), v);
-                if (t + u < last) store<T, V, WIDE>(out, layer::pack<T, V>(v), have);
+                one<K, V>(S, P, *reinterpret_cast<const float2(*)[K][V / 2]>(&row[u]), v);
+                if (u < left) store<T, V, WIDE>(out, layer::pack<T, V>(v), have);
                 out += S.D;
             }
 #pragma unroll
@@ -80,16 +80,16 @@ __global__ void __launch_bounds__(128, 4) conv_fwd_kernel(const __grid_constant_
         }
     }
     // The history behind the sequence, by the lanes that alone read the one before it: the two may be the same
-    if (tail && first == 0) {
+    if (tail && r.first == 0) {
         vec<T, V> v[K - 1];
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) v[k] = X.at(len - (K - 1) + k);
+        for (int k = 0; k < K - 1; ++k) v[k] = X.at(r.len - (K - 1) + k);
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) store<T, V, WIDE>(tail + (n * (K - 1) + k) * S.D + c, v[k], have);
+        for (int k = 0; k < K - 1; ++k) store<T, V, WIDE>(tail + (r.n * (K - 1) + k) * S.D + c, v[k], have);
     }
 }
 
-template <typename T, int K, bool WIDE>
+template <typename T, int K, int V, bool WIDE>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ spec S, const T *x, T *state, const int32_t *idx, int64_t slots, T *y,
                                                         int *err) {
     const int64_t n = blockIdx.x;
@@ -105,41 +105,54 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
     float2 row[K][V / 2], out[V / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k) layer::unpack<T, V>(v[k], row[k]);
-    one<K>(S, P, row, out);
+    one<K, V>(S, P, row, out);
 #pragma unroll
     for (int k = 0; k + 1 < K; ++k) store<T, V, WIDE>(hist + k * S.D, v[k + 1], have);
     store<T, V, WIDE>(y + n * S.D + c, layer::pack<T, V>(out), have);
 }
 
-template <typename T, int K, bool WIDE>
+template <typename T, int K, int V, bool WIDE>
 static void fwd(const kda_short_conv_args *a, cudaStream_t stream, int *err) {
     const int blocks = (a->D + 32 * V - 1) / (32 * V);
     // Runs of 64 tokens read 5 % of them twice (from L2), of 16 a fifth: short ones where long ones leave SMs without
-    // eight warps.
+    // sixteen warps.
     int L = 64;
-    while (L > 16 && (a->T / L) * blocks < 8 * 152) L /= 2;
+    while (L > 16 && (a->T / L) * blocks < 16 * 152) L /= 2;
     const int64_t items = lin::chunk_slots(a->T, a->N, L) * blocks;
-    conv_fwd_kernel<T, K, WIDE><<<(unsigned)((items + 3) / 4), 128, 0, stream>>>(spec_of(a, a->T, a->cu_seqlens), (const T *)a->x,
-                                                                                (const T *)a->initial_state, (T *)a->final_state, (T *)a->y, L,
-                                                                                blocks, items, err);
+    conv_fwd_kernel<T, K, V, WIDE><<<(unsigned)((items + 3) / 4), 128, 0, stream>>>(
+        spec_of(a, a->T, a->cu_seqlens), (const T *)a->x, (const T *)a->initial_state, (T *)a->final_state, (T *)a->y, L, blocks, items, err);
 }
 
-template <typename T, int K, bool WIDE>
+template <typename T, int K, int V, bool WIDE>
 static void step(const kda_short_conv_step_args *a, cudaStream_t stream, int *err) {
     const int per = 128 * V;
-    conv_step_kernel<T, K, WIDE><<<dim3((unsigned)a->N, (a->D + per - 1) / per), 128, 0, stream>>>(
+    conv_step_kernel<T, K, V, WIDE><<<dim3((unsigned)a->N, (a->D + per - 1) / per), 128, 0, stream>>>(
         spec_of(a, a->N, nullptr), (const T *)a->x, (T *)a->state, a->state_indices, a->num_slots, (T *)a->y, err);
 }
 
-template <typename T, typename A, typename F>
-static void choose(const A *a, bool wide, F &&go) {
-    auto taps_of = [&](auto k) {
-        if (wide) go(k, std::true_type{});
-        else go(k, std::false_type{});
+// Calls go(type, taps, channels to a lane, wide): four channels, eight where a head is 256 wide and has to lie in a warp.
+template <int I> using number = std::integral_constant<int, I>;
+template <typename A, typename F>
+static void choose(const A *a, const void *first, const void *second, F &&go) {
+    const int V = a->norm_dim == 256 ? 8 : 4;
+    const uintptr_t bytes = V == 4 && a->dtype == KDA_BF16 ? 8 : 16;
+    const bool wide = a->D % V == 0 && a->x_stride % V == 0 &&
+                      ((uintptr_t)a->x | (uintptr_t)a->y | (uintptr_t)first | (uintptr_t)second) % bytes == 0;
+    auto width = [&](auto t, auto k, auto v) {
+        if (wide) go(t, k, v, std::true_type{});
+        else go(t, k, v, std::false_type{});
     };
-    if (a->K == 2) taps_of(std::integral_constant<int, 2>{});
-    else if (a->K == 3) taps_of(std::integral_constant<int, 3>{});
-    else taps_of(std::integral_constant<int, 4>{});
+    auto channels = [&](auto t, auto k) {
+        if (V == 8) width(t, k, number<8>{});
+        else width(t, k, number<4>{});
+    };
+    auto taps_of = [&](auto t) {
+        if (a->K == 2) channels(t, number<2>{});
+        else if (a->K == 3) channels(t, number<3>{});
+        else channels(t, number<4>{});
+    };
+    if (a->dtype == KDA_BF16) taps_of(bf16{});
+    else taps_of(float{});
 }
 
 }  // namespace conv
@@ -149,14 +162,9 @@ kda_status_t kda_launch_short_conv_fwd(const kda_short_conv_args *a, cudaStream_
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::conv;
-    const bool wide = a->D % V == 0 && a->x_stride % V == 0 &&
-                      (((uintptr_t)a->x | (uintptr_t)a->y | (uintptr_t)a->initial_state | (uintptr_t)a->final_state) & 15) == 0;
-    auto go = [&](auto t) {
-        using T = decltype(t);
-        choose<T>(a, wide, [&](auto k, auto w) { fwd<T, decltype(k)::value, decltype(w)::value>(a, stream, err); });
-    };
-    if (a->dtype == KDA_BF16) go(kda::bf16{});
-    else go(float{});
+    choose(a, a->initial_state, a->final_state, [&](auto t, auto k, auto v, auto w) {
+        fwd<decltype(t), decltype(k)::value, decltype(v)::value, decltype(w)::value>(a, stream, err);
+    });
     return kda_cuda_status(cudaGetLastError());
 }
 
@@ -164,12 +172,8 @@ kda_status_t kda_launch_short_conv_step(const kda_short_conv_step_args *a, cudaS
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::conv;
-    const bool wide = a->D % V == 0 && a->x_stride % V == 0 && (((uintptr_t)a->x | (uintptr_t)a->y | (uintptr_t)a->state) & 15) == 0;
-    auto go = [&](auto t) {
-        using T = decltype(t);
-        choose<T>(a, wide, [&](auto k, auto w) { step<T, decltype(k)::value, decltype(w)::value>(a, stream, err); });
-    };
-    if (a->dtype == KDA_BF16) go(kda::bf16{});
-    else go(float{});
+    choose(a, a->state, nullptr, [&](auto t, auto k, auto v, auto w) {
+        step<decltype(t), decltype(k)::value, decltype(v)::value, decltype(w)::value>(a, stream, err);
+    });
     return kda_cuda_status(cudaGetLastError());
 }

@@ -84,20 +84,29 @@ template <int V> __device__ __forceinline__ float head_sum(float v, int norm) {
 // Where rows of a sequence come from: its history and then its tokens
 template <typename T, int V, bool WIDE> struct rows {
     const T *x, *hist;  // the sequence's first token and history (NULL: zeros), at this lane's channels
-    int64_t stride, D;
-    int K, have;
-    __device__ __forceinline__ vec<T, V> at(int64_t i) const {  // token i, from -(K - 1) on
+    int64_t stride;
+    int D, K, have;
+    __device__ __forceinline__ vec<T, V> at(int i) const {  // token i, from -(K - 1) on
         if (i >= 0) return load<T, V, WIDE>(x + i * stride, have);
-        return hist ? load<T, V, WIDE>(hist + (i + K - 1) * D, have) : zeros<T, V>();
+        return hist ? load<T, V, WIDE>(hist + (int64_t)(i + K - 1) * D, have) : zeros<T, V>();
     }
 };
 
-// The sequence and the run of L tokens of a slot.  False: none; an empty sequence has a run of no tokens.
-__device__ __forceinline__ bool find_run(const spec &S, int64_t slot, int L, int64_t *n, lin::span *s, int64_t *first) {
+// The sequence of a slot and the run of L of its tokens, [first, last).  False: none; an empty sequence has a run of no tokens.
+struct run {
+    int64_t n, a;          // sequence, its first token
+    int len, first, last;  // its tokens, the run's
+};
+__device__ __forceinline__ bool find_run(const spec &S, int64_t slot, int L, run *r) {
     int64_t i;
-    if (!lin::find_slot(S.cu, S.T, S.N, L, slot, n, &i, s)) return false;
-    *first = i * L;
-    return i == 0 || s->a + *first < s->b;
+    lin::span s;
+    if (!lin::find_slot(S.cu, S.T, S.N, L, slot, &r->n, &i, &s)) return false;
+    r->a = s.a;
+    r->len = (int)(s.b - s.a);
+    if (i > 0 && i * L >= r->len) return false;
+    r->first = (int)(i * L);
+    r->last = r->first + L < r->len ? r->first + L : r->len;
+    return true;
 }
 
 __device__ __forceinline__ void check_all(const spec &S, int *err) {

@@ -13,7 +13,7 @@ namespace conv {
 constexpr int NW = 8;
 
 template <typename T, int K, int V, bool WIDE>
-__global__ void __launch_bounds__(32 * NW)
+__global__ void __launch_bounds__(32 * NW, V == 4 ? 2 : 1)
 conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const T *dy, const T *dtail, T *dx, T *dhist, float *sums, int L,
                 int64_t slots, int *err) {
     __shared__ float part[NW][32 * V];
@@ -28,33 +28,34 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
 #pragma unroll
         for (int k = 0; k < K; ++k) dw[k][i] = db[i];
     }
-    int64_t n, first;
-    lin::span s;
-    if (slot < slots && find_run(S, slot, L, &n, &s, &first)) {
-        const int64_t len = s.b - s.a, last = first + L < len ? first + L : len;  // this run's tokens
-        const rows<T, V, WIDE> X{x + s.a * S.stride + c, hist ? hist + n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
-        const T *g = dy + s.a * S.D + c;
+    run r;
+    if (slot < slots && find_run(S, slot, L, &r)) {
+        const rows<T, V, WIDE> X{x + r.a * S.stride + c, hist ? hist + r.n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
         const taps<V, K> P(S, c, have);
         constexpr int U = 2;
         float2 row[K - 1 + U][V / 2], dp[K - 1 + U][V / 2];
         vec<T, V> nx[U], ng[U];
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) {
-            layer::unpack<T, V>(X.at(first - (K - 1) + k), row[k]);
+            layer::unpack<T, V>(X.at(r.first - (K - 1) + k), row[k]);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) dp[k][i] = make_float2(0.f, 0.f);
         }
         // tokens behind the run's end that its gradients need; those behind the sequence have dp = 0
-        const int64_t stop = last + K - 1;
-        auto fetch = [&](int64_t t, int u) {
-            if (t < stop && t < len) {
-                nx[u] = X.at(t);
-                ng[u] = load<T, V, WIDE>(g + t * S.D, have);
+        const int stop = r.last + K - 1, some = stop < r.len ? stop : r.len;
+        const T *px = X.x + r.first * S.stride, *pg = dy + (r.a + r.first) * S.D + c;
+        auto fetch = [&](int t, int u) {
+            if (t < some) {
+                nx[u] = load<T, V, WIDE>(px, have);
+                ng[u] = load<T, V, WIDE>(pg, have);
             }
+            px += S.stride;
+            pg += S.D;
         };
 #pragma unroll
-        for (int u = 0; u < U; ++u) fetch(first + u, u);
-        for (int64_t t0 = first; t0 < stop; t0 += U) {
+        for (int u = 0; u < U; ++u) fetch(r.first + u, u);
+        T *out = dx + (r.a + r.first - (K - 1)) * S.D + c;
+        for (int t0 = r.first; t0 < stop; t0 += U) {
             float2 d[U][V / 2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -65,7 +66,7 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
             for (int u = 0; u < U; ++u) fetch(t0 + U + u, u);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t t = t0 + u;
+                const int t = t0 + u;
                 float2 p[V / 2], ds[V / 2];
                 float2 q = make_float2(0.f, 0.f), e = q;
 #pragma unroll
@@ -83,12 +84,12 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
                     e = fma(d[u][i], p[i], e);
                 }
                 if (S.norm) {
-                    const float r = rsqrtf(head_sum<V>(q.x + q.y, S.norm) + S.eps), dot = head_sum<V>(e.x + e.y, S.norm) * r * r;
+                    const float k = rsqrtf(head_sum<V>(q.x + q.y, S.norm) + S.eps), dot = head_sum<V>(e.x + e.y, S.norm) * k * k;
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i)
-                        d[u][i] = mul(fma(p[i], make_float2(-dot, -dot), d[u][i]), make_float2(r, r));
+                        d[u][i] = mul(fma(p[i], make_float2(-dot, -dot), d[u][i]), make_float2(k, k));
                 }
-                const bool there = t < len, own = t < last;
+                const bool there = t < r.len, own = t < r.last;
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
                     d[u][i] = there ? mul(d[u][i], ds[i]) : make_float2(0.f, 0.f);
@@ -103,8 +104,8 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
                     }
                 }
                 // row t - K + 1 of the sequence, its history's where that is below 0
-                const int64_t at = t - (K - 1);
-                if (at < last && (at >= first || first == 0) && (at >= 0 || dhist)) {
+                const int at = t - (K - 1);
+                if (at < r.last && (at >= r.first || (r.first == 0 && dhist))) {
                     float2 v[V / 2];
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
@@ -112,14 +113,15 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
 #pragma unroll
                         for (int k = 1; k < K; ++k) v[i] = fma(P.w[k][i], dp[K - 1 + u - k][i], v[i]);
                     }
-                    if (dtail && at >= len - (K - 1)) {
+                    if (dtail && at >= r.len - (K - 1)) {
                         float2 f[V / 2];
-                        layer::unpack<T, V>(load<T, V, WIDE>(dtail + (n * (K - 1) + at - len + K - 1) * S.D + c, have), f);
+                        layer::unpack<T, V>(load<T, V, WIDE>(dtail + (r.n * (K - 1) + at - r.len + K - 1) * S.D + c, have), f);
 #pragma unroll
                         for (int i = 0; i < V / 2; ++i) v[i] = add(v[i], f[i]);
                     }
-                    store<T, V, WIDE>(at >= 0 ? dx + (s.a + at) * S.D + c : dhist + (n * (K - 1) + at + K - 1) * S.D + c, layer::pack<T, V>(v), have);
+                    store<T, V, WIDE>(at >= 0 ? out : dhist + (r.n * (K - 1) + at + K - 1) * S.D + c, layer::pack<T, V>(v), have);
                 }
+                out += S.D;
             }
 #pragma unroll
             for (int k = 0; k < K - 1; ++k)
