@@ -15,12 +15,12 @@
 // run, and the first tile that is not done waits for none that is not, so that every wait ends; they are limited all the same.
 #pragma once
 #include <cooperative_groups.h>
-#include <cuda.h>
 
 #include <atomic>
 
 #include "kda_internal.h"
 #include "kda_linear.cuh"
+#include "kda_row_map.h"
 #include "kda_scan.cuh"
 #include "tc_util.cuh"
 
@@ -367,27 +367,9 @@ template <typename T, int NI, int L> struct ring {
 template <int NI> struct row_maps {
     CUtensorMap m[NI];
 };
-// [T, D] rows a stride apart, boxes of L rows and W channels.  Needs 16-byte aligned rows.
+// boxes of L rows and W channels
 inline bool make_row_map(CUtensorMap *m, const void *base, int64_t T, int D, int64_t stride, kda_dtype_t dtype, int L) {
-    typedef CUresult (*encode_fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                  const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-    static const encode_fn encode = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return (encode_fn)p;
-    }();
-    if (!encode) return false;
-    const int64_t es = dtype == KDA_BF16 ? 2 : 4;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, 1, (cuuint64_t)T};
-    const cuuint64_t strides[2] = {(cuuint64_t)(stride * es), (cuuint64_t)(stride * es)};
-    const cuuint32_t box[3] = {W, 1, (cuuint32_t)L}, estr[3] = {1, 1, 1};
-    return encode(m, dtype == KDA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return layer::make_row_map(m, base, T, D, stride, dtype, W, L);
 }
 
 // Two neighbouring channels of a row: by one access where rows are aligned for it, else by their elements

@@ -1,8 +1,11 @@
 // kda_short_conv_fwd: a warp takes a run of L tokens of one sequence by 32 V channels, V to a lane, and goes through the
 // tokens with the last K - 1 of them in registers; the sums of a head's squares meet by shuffles between the lanes that
-// hold it.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each run) and y written once.
+// hold it.  Rows come by TMA, up to 24 tokens ahead.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each
+// run) and y written once.
 //
 // kda_short_conv_step: the same for one token, whose history is a slot of a pool.
+#include <atomic>
+
 #include "kda_short_conv.cuh"
 
 namespace kda {
@@ -34,45 +37,61 @@ __device__ __forceinline__ void one(const spec &S, const taps<V, K> &P, const fl
 }
 
 template <typename T, int K, int V, bool WIDE>
-__global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, T *tail, T *y, int L, int blocks,
-                                                       int64_t items, int *err) {
+__global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps maps, const T *x,
+                                                       const T *hist, T *tail, T *y, int L, int blocks, int64_t items, int *err) {
+    constexpr int U = some_rows<T, V>;
+    extern __shared__ __align__(128) char memory[];
     check_all(S, err);
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t item = (int64_t)blockIdx.x * 4 + w;
     if (item >= items) return;
     run r;
     if (!find_run(S, item / blocks, L, &r)) return;
-    const int c = (int)(item % blocks) * 32 * V + lane * V, have = S.D - c;
+    const int c0 = (int)(item % blocks) * 32 * V, c = c0 + lane * V, have = S.D - c;
     const rows<T, V, WIDE> X{x + r.a * S.stride + c, hist ? hist + r.n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
     if (r.first < r.last) {
+        ring<T, V, 1> &Q = reinterpret_cast<ring<T, V, 1> *>(memory)[w];
+        const int turns = (r.last - r.first + U - 1) / U;
+        auto ask = [&](int turn) {
+            if (!WIDE || lane != 0 || turn >= turns) return;
+            tc::mbar_arrive_expect_tx(&Q.full[turn % NS], sizeof(Q.x[0]));
+            tc::tma_load_3d(&Q.x[turn % NS], &maps.x, c0, 0, (int)r.a + r.first + turn * U, &Q.full[turn % NS]);
+        };
+        if (WIDE) {
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) tc::mbar_init(&Q.full[i], 1);
+                tc::fence_proxy_async();
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NS; ++i) ask(i);
+        }
         const taps<V, K> P(S, c, have);
-        constexpr int U = 4;  // tokens on their way while as many are computed
         float2 row[K - 1 + U][V / 2];
-        vec<T, V> next[U];
-        const T *from = X.x + r.first * S.stride;
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) layer::unpack<T, V>(X.at(r.first - (K - 1) + k), row[k]);
-        auto fetch = [&](int left) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u < left) next[u] = load<T, V, WIDE>(from, have);
-                from += S.stride;
-            }
-        };
-        int left = r.last - r.first;
-        fetch(left);
+        const T *from = X.x + r.first * S.stride;
         T *out = y + (r.a + r.first) * S.D + c;
-        for (; left > 0; left -= U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) layer::unpack<T, V>(next[u], row[K - 1 + u]);
-            fetch(left - U);
+        for (int turn = 0, stage = 0, phase = 0; turn < turns; ++turn) {
+            const int left = r.last - r.first - turn * U;
+            if (WIDE && !tc::mbar_wait(&Q.full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if constexpr (WIDE) {
+                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][u][lane * V]), row[K - 1 + u]);
+                } else {
+                    if (u < left) layer::unpack<T, V>(load<T, V, false>(from, have), row[K - 1 + u]);
+                    from += S.stride;
+                }
                 float2 v[V / 2];
                 one<K, V>(S, P, *reinterpret_cast<const float2(*)[K][V / 2]>(&row[u]), v);
                 if (u < left) store<T, V, WIDE>(out, layer::pack<T, V>(v), have);
                 out += S.D;
             }
+            __syncwarp();
+            ask(turn + NS);
+            if (++stage == NS) stage = 0, phase ^= 1;
 #pragma unroll
             for (int k = 0; k < K - 1; ++k)
 #pragma unroll
@@ -112,15 +131,25 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 }
 
 template <typename T, int K, int V, bool WIDE>
-static void fwd(const kda_short_conv_args *a, cudaStream_t stream, int *err) {
+static cudaError_t fwd(const kda_short_conv_args *a, cudaStream_t stream, int *err) {
     const int blocks = (a->D + 32 * V - 1) / (32 * V);
-    // Runs of 64 tokens read 5 % of them twice (from L2), of 16 a fifth: short ones where long ones leave SMs without
+    // Runs of 128 tokens read 2 % of them twice (from L2), of 16 a fifth: short ones where long ones leave SMs without
     // sixteen warps.
-    int L = 64;
+    int L = 128;
     while (L > 16 && (a->T / L) * blocks < 16 * 152) L /= 2;
     const int64_t items = lin::chunk_slots(a->T, a->N, L) * blocks;
-    conv_fwd_kernel<T, K, V, WIDE><<<(unsigned)((items + 3) / 4), 128, 0, stream>>>(
-        spec_of(a, a->T, a->cu_seqlens), (const T *)a->x, (const T *)a->initial_state, (T *)a->final_state, (T *)a->y, L, blocks, items, err);
+    row_maps maps{};
+    if (WIDE && !layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>)) return cudaErrorUnknown;
+    constexpr int smem = WIDE ? 4 * (int)sizeof(ring<T, V, 1>) : 0;
+    if (smem > 48 * 1024) {
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = lin::allow_smem(conv_fwd_kernel<T, K, V, WIDE>, smem, done);
+        if (e != cudaSuccess) return e;
+    }
+    conv_fwd_kernel<T, K, V, WIDE><<<(unsigned)((items + 3) / 4), 128, smem, stream>>>(spec_of(a, a->T, a->cu_seqlens), maps, (const T *)a->x,
+                                                                                      (const T *)a->initial_state, (T *)a->final_state,
+                                                                                      (T *)a->y, L, blocks, items, err);
+    return cudaGetLastError();
 }
 
 template <typename T, int K, int V, bool WIDE>
@@ -133,10 +162,10 @@ static void step(const kda_short_conv_step_args *a, cudaStream_t stream, int *er
 // Calls go(type, taps, channels to a lane, wide): four channels, eight where a head is 256 wide and has to lie in a warp.
 template <int I> using number = std::integral_constant<int, I>;
 template <typename A, typename F>
-static void choose(const A *a, const void *first, const void *second, F &&go) {
+static void choose(const A *a, const void *first, const void *second, bool wide, F &&go) {
     const int V = a->norm_dim == 256 ? 8 : 4;
     const uintptr_t bytes = V == 4 && a->dtype == KDA_BF16 ? 8 : 16;
-    const bool wide = a->D % V == 0 && a->x_stride % V == 0 &&
+    wide = wide && a->D % V == 0 && a->x_stride % V == 0 &&
                       ((uintptr_t)a->x | (uintptr_t)a->y | (uintptr_t)first | (uintptr_t)second) % bytes == 0;
     auto width = [&](auto t, auto k, auto v) {
         if (wide) go(t, k, v, std::true_type{});
@@ -162,17 +191,21 @@ kda_status_t kda_launch_short_conv_fwd(const kda_short_conv_args *a, cudaStream_
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::conv;
-    choose(a, a->initial_state, a->final_state, [&](auto t, auto k, auto v, auto w) {
-        fwd<decltype(t), decltype(k)::value, decltype(v)::value, decltype(w)::value>(a, stream, err);
+    cudaError_t e = cudaSuccess;
+    // (by TMA, where x's rows are multiples of 16 bytes)
+    const int64_t per = a->dtype == KDA_BF16 ? 8 : 4;
+    const bool rows = a->T > 0 && a->x_stride % per == 0 && ((uintptr_t)a->x & 15) == 0;
+    choose(a, a->initial_state, a->final_state, rows, [&](auto t, auto k, auto v, auto w) {
+        e = fwd<decltype(t), decltype(k)::value, decltype(v)::value, decltype(w)::value>(a, stream, err);
     });
-    return kda_cuda_status(cudaGetLastError());
+    return kda_cuda_status(e);
 }
 
 kda_status_t kda_launch_short_conv_step(const kda_short_conv_step_args *a, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::conv;
-    choose(a, a->state, nullptr, [&](auto t, auto k, auto v, auto w) {
+    choose(a, a->state, nullptr, true, [&](auto t, auto k, auto v, auto w) {
         step<decltype(t), decltype(k)::value, decltype(v)::value, decltype(w)::value>(a, stream, err);
     });
     return kda_cuda_status(cudaGetLastError());

@@ -3,6 +3,8 @@
 #include "kda_internal.h"
 #include "kda_layer.cuh"
 #include "kda_linear.cuh"
+#include "kda_row_map.h"
+#include "tc_util.cuh"
 
 namespace kda {
 namespace conv {
@@ -108,6 +110,18 @@ __device__ __forceinline__ bool find_run(const spec &S, int64_t slot, int L, run
     r->last = r->first + L < r->len ? r->first + L : r->len;
     return true;
 }
+
+// A warp's next rows, 2 KB of them at a time and up to NS times as many, on their way by TMA: the registers that as many loads
+// would take are those of four more warps.
+template <typename T, int V> constexpr int some_rows = 2048 / (32 * V * (int)sizeof(T));
+constexpr int NS = 3;
+template <typename T, int V, int NI> struct alignas(128) ring {
+    T x[NS][NI][some_rows<T, V>][32 * V];
+    uint64_t full[NS];
+};
+struct row_maps {
+    CUtensorMap x, dy;
+};
 
 __device__ __forceinline__ void check_all(const spec &S, int *err) {
     if (blockIdx.x > 0 || blockIdx.y > 0) return;

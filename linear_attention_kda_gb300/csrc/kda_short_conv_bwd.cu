@@ -5,6 +5,8 @@
 // the run as well, whose dp is formed a second time by the next one.  weight and bias gather their sums over tokens in
 // registers; the eight warps of a block, which have eight runs of the same channels, add theirs up in shared memory, and
 // a second kernel adds up the blocks' rows, all in a fixed order.  About twenty instructions an element for 6 bytes in bf16.
+#include <atomic>
+
 #include "kda_short_conv.cuh"
 
 namespace kda {
@@ -14,13 +16,15 @@ constexpr int NW = 8;
 
 template <typename T, int K, int V, bool WIDE>
 __global__ void __launch_bounds__(32 * NW, V == 4 ? 2 : 1)
-conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const T *dy, const T *dtail, T *dx, T *dhist, float *sums, int L,
+conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps maps, const T *x, const T *hist, const T *dy, const T *dtail, T *dx, T *dhist, float *sums, int L,
                 int64_t slots, int *err) {
-    __shared__ float part[NW][32 * V];
+    constexpr int U = some_rows<T, V>;
+    extern __shared__ __align__(128) char memory[];
+    float (*part)[32 * V] = reinterpret_cast<float(*)[32 * V]>(memory + (WIDE ? NW * sizeof(ring<T, V, 2>) : 0));
     check_all(S, err);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t slot = (int64_t)blockIdx.x * NW + w;
-    const int c = (int)blockIdx.y * 32 * V + lane * V, have = S.D - c;
+    const int c0 = (int)blockIdx.y * 32 * V, c = c0 + lane * V, have = S.D - c;
     float2 dw[K][V / 2], db[V / 2];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
@@ -32,40 +36,63 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
     if (slot < slots && find_run(S, slot, L, &r)) {
         const rows<T, V, WIDE> X{x + r.a * S.stride + c, hist ? hist + r.n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
         const taps<V, K> P(S, c, have);
-        constexpr int U = 2;
-        float2 row[K - 1 + U][V / 2], dp[K - 1 + U][V / 2];
-        vec<T, V> nx[U], ng[U];
+        // tokens behind the run's end that its gradients need; those behind the sequence have dp = 0
+        const int stop = r.last + K - 1, turns = (stop - r.first + U - 1) / U;
+        ring<T, V, 2> &Q = reinterpret_cast<ring<T, V, 2> *>(memory)[w];
+        auto ask = [&](int turn) {
+            if (!WIDE || lane != 0 || turn >= turns) return;
+            const int stage = turn % NS, tok = (int)r.a + r.first + turn * U;
+            tc::mbar_arrive_expect_tx(&Q.full[stage], sizeof(Q.x[0]));
+            tc::tma_load_3d(&Q.x[stage][0], &maps.x, c0, 0, tok, &Q.full[stage]);
+            tc::tma_load_3d(&Q.x[stage][1], &maps.dy, c0, 0, tok, &Q.full[stage]);
+        };
+        if (WIDE) {
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) tc::mbar_init(&Q.full[i], 1);
+                tc::fence_proxy_async();
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NS; ++i) ask(i);
+        }
+        constexpr int H = 2;  // tokens taken together
+        float2 row[K - 1 + H][V / 2], dp[K - 1 + H][V / 2];
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) {
             layer::unpack<T, V>(X.at(r.first - (K - 1) + k), row[k]);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) dp[k][i] = make_float2(0.f, 0.f);
         }
-        // tokens behind the run's end that its gradients need; those behind the sequence have dp = 0
-        const int stop = r.last + K - 1, some = stop < r.len ? stop : r.len;
         const T *px = X.x + r.first * S.stride, *pg = dy + (r.a + r.first) * S.D + c;
-        auto fetch = [&](int t, int u) {
-            if (t < some) {
-                nx[u] = load<T, V, WIDE>(px, have);
-                ng[u] = load<T, V, WIDE>(pg, have);
-            }
-            px += S.stride;
-            pg += S.D;
-        };
-#pragma unroll
-        for (int u = 0; u < U; ++u) fetch(r.first + u, u);
         T *out = dx + (r.a + r.first - (K - 1)) * S.D + c;
-        for (int t0 = r.first; t0 < stop; t0 += U) {
-            float2 d[U][V / 2];
+        int stage = 0, phase = 0, turn = 0;
+        for (int t0 = r.first; t0 < stop; t0 += H) {
+            const int in = (t0 - r.first) % U;
+            if (WIDE && in == 0 && !tc::mbar_wait(&Q.full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+            float2 d[H][V / 2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                layer::unpack<T, V>(nx[u], row[K - 1 + u]);
-                layer::unpack<T, V>(ng[u], d[u]);
+            for (int u = 0; u < H; ++u) {
+                if constexpr (WIDE) {  // (rows of the next sequence, or what a box beyond the last one is filled with, are left out below)
+                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][in + u][lane * V]), row[K - 1 + u]);
+                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][1][in + u][lane * V]), d[u]);
+                } else {
+                    if (t0 + u < r.len) {
+                        layer::unpack<T, V>(load<T, V, false>(px, have), row[K - 1 + u]);
+                        layer::unpack<T, V>(load<T, V, false>(pg, have), d[u]);
+                    }
+                    px += S.stride;
+                    pg += S.D;
+                }
+            }
+            if (in + H == U) {
+                __syncwarp();
+                ask(turn + NS);
+                ++turn;
+                if (++stage == NS) stage = 0, phase ^= 1;
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) fetch(t0 + U + u, u);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < H; ++u) {
                 const int t = t0 + u;
                 float2 p[V / 2], ds[V / 2];
                 float2 q = make_float2(0.f, 0.f), e = q;
@@ -127,8 +154,8 @@ conv_bwd_kernel(const __grid_constant__ spec S, const T *x, const T *hist, const
             for (int k = 0; k < K - 1; ++k)
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
-                    row[k][i] = row[U + k][i];
-                    dp[k][i] = dp[U + k][i];
+                    row[k][i] = row[H + k][i];
+                    dp[k][i] = dp[H + k][i];
                 }
         }
     }
@@ -177,21 +204,32 @@ static int run_length(int64_t T, int D) {
 }
 
 template <typename T, int K, int V, bool WIDE>
-static void launch(const kda_short_conv_bwd_args *a, float *sums, cudaStream_t stream, int *err) {
+static cudaError_t launch(const kda_short_conv_bwd_args *a, float *sums, cudaStream_t stream, int *err) {
     const int L = run_length(a->T, a->D);
     const int64_t slots = lin::chunk_slots(a->T, a->N, L), rows = (slots + NW - 1) / NW;
+    row_maps maps{};
+    if (WIDE && (!layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>) ||
+                 !layer::make_row_map(&maps.dy, a->grad_y, a->T, a->D, a->D, a->dtype, 32 * V, some_rows<T, V>)))
+        return cudaErrorUnknown;
+    constexpr int smem = (WIDE ? NW * (int)sizeof(ring<T, V, 2>) : 0) + NW * 32 * V * 4;
+    if (smem > 48 * 1024) {
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = lin::allow_smem(conv_bwd_kernel<T, K, V, WIDE>, smem, done);
+        if (e != cudaSuccess) return e;
+    }
     const dim3 grid((unsigned)rows, (a->D + 32 * V - 1) / (32 * V));
-    conv_bwd_kernel<T, K, V, WIDE><<<grid, 32 * NW, 0, stream>>>(spec_of(a, a->T, a->cu_seqlens), (const T *)a->x, (const T *)a->initial_state,
-                                                              (const T *)a->grad_y, (const T *)a->grad_final_state, (T *)a->grad_x,
-                                                              (T *)a->grad_initial_state, sums, L, slots, err);
+    conv_bwd_kernel<T, K, V, WIDE><<<grid, 32 * NW, smem, stream>>>(
+        spec_of(a, a->T, a->cu_seqlens), maps, (const T *)a->x, (const T *)a->initial_state, (const T *)a->grad_y, (const T *)a->grad_final_state,
+        (T *)a->grad_x, (T *)a->grad_initial_state, sums, L, slots, err);
     if (sums) conv_sums_kernel<<<dim3((a->D + 31) / 32, K + 1), 256, 0, stream>>>(sums, rows, a->D, K, a->grad_weight, a->grad_bias);
+    return cudaGetLastError();
 }
 
 template <typename T, int K>
-static void choose(const kda_short_conv_bwd_args *a, float *sums, bool wide, cudaStream_t stream, int *err) {
+static cudaError_t choose(const kda_short_conv_bwd_args *a, float *sums, bool wide, cudaStream_t stream, int *err) {
     // four channels a lane, eight where a head is 256 wide and has to lie in a warp
-    if (a->norm_dim == 256) wide ? launch<T, K, 8, true>(a, sums, stream, err) : launch<T, K, 8, false>(a, sums, stream, err);
-    else wide ? launch<T, K, 4, true>(a, sums, stream, err) : launch<T, K, 4, false>(a, sums, stream, err);
+    if (a->norm_dim == 256) return wide ? launch<T, K, 8, true>(a, sums, stream, err) : launch<T, K, 8, false>(a, sums, stream, err);
+    return wide ? launch<T, K, 4, true>(a, sums, stream, err) : launch<T, K, 4, false>(a, sums, stream, err);
 }
 
 }  // namespace conv
@@ -206,19 +244,16 @@ kda_status_t kda_launch_short_conv_bwd(const kda_short_conv_bwd_args *a, void *w
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::conv;
-    const int V = a->norm_dim == 256 ? 8 : 4;
-    const uintptr_t bytes = V * (a->dtype == KDA_BF16 ? 2 : 4) < 16 ? 8 : 16;
-    const bool wide = a->D % V == 0 && a->x_stride % V == 0 &&
-                      (((uintptr_t)a->x | (uintptr_t)a->grad_y | (uintptr_t)a->grad_x | (uintptr_t)a->initial_state |
-                        (uintptr_t)a->grad_final_state | (uintptr_t)a->grad_initial_state) % bytes) == 0;
+    // vectors of V channels, and x and grad_y by TMA, where rows allow both
+    const int V = a->norm_dim == 256 ? 8 : 4, per = a->dtype == KDA_BF16 ? 8 : 4;
+    const uintptr_t bytes = V == 4 && per == 8 ? 8 : 16;
+    const bool wide = a->T > 0 && a->D % (V > per ? V : per) == 0 && a->x_stride % per == 0 && (((uintptr_t)a->x | (uintptr_t)a->grad_y) & 15) == 0 &&
+                      (((uintptr_t)a->grad_x | (uintptr_t)a->initial_state | (uintptr_t)a->grad_final_state | (uintptr_t)a->grad_initial_state) % bytes) == 0;
     float *sums = a->grad_weight || a->grad_bias ? (float *)ws : nullptr;
     auto go = [&](auto t) {
         using T = decltype(t);
-        if (a->K == 2) choose<T, 2>(a, sums, wide, stream, err);
-        else if (a->K == 3) choose<T, 3>(a, sums, wide, stream, err);
-        else choose<T, 4>(a, sums, wide, stream, err);
+        return a->K == 2 ? choose<T, 2>(a, sums, wide, stream, err) : a->K == 3 ? choose<T, 3>(a, sums, wide, stream, err)
+                                                                              : choose<T, 4>(a, sums, wide, stream, err);
     };
-    if (a->dtype == KDA_BF16) go(kda::bf16{});
-    else go(float{});
-    return kda_cuda_status(cudaGetLastError());
+    return kda_cuda_status(a->dtype == KDA_BF16 ? go(kda::bf16{}) : go(float{}));
 }
