@@ -83,6 +83,20 @@ template <int V> __device__ __forceinline__ float head_sum(float v, int norm) {
     return v;
 }
 
+// Both sums at once: each half of the lanes takes one of them after the first step (six shuffles for ten)
+template <int V> __device__ __forceinline__ void head_sums(float &a, float &b, int norm) {
+    const int half = norm / V / 2;
+    const bool upper = (threadIdx.x & half) != 0;
+    float v = upper ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, upper ? a : b, half);
+#pragma unroll
+    for (int off = 1; off < 16; off *= 2)
+        if (off < half) v += __shfl_xor_sync(0xffffffffu, v, off);
+    const float w = __shfl_xor_sync(0xffffffffu, v, half);
+    a = upper ? w : v;
+    b = upper ? v : w;
+}
+
 // Where rows of a sequence come from: its history and then its tokens
 template <typename T, int V, bool WIDE> struct rows {
     const T *x, *hist;  // the sequence's first token and history (NULL: zeros), at this lane's channels

@@ -56,8 +56,7 @@ conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps
 #pragma unroll
             for (int i = 0; i < NS; ++i) ask(i);
         }
-        constexpr int H = 2;  // tokens taken together
-        float2 row[K - 1 + H][V / 2], dp[K - 1 + H][V / 2];
+        float2 row[K - 1 + U][V / 2], dp[K - 1 + U][V / 2];
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) {
             layer::unpack<T, V>(X.at(r.first - (K - 1) + k), row[k]);
@@ -66,68 +65,66 @@ conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps
         }
         const T *px = X.x + r.first * S.stride, *pg = dy + (r.a + r.first) * S.D + c;
         T *out = dx + (r.a + r.first - (K - 1)) * S.D + c;
-        int stage = 0, phase = 0, turn = 0;
-        for (int t0 = r.first; t0 < stop; t0 += H) {
-            const int in = (t0 - r.first) % U;
-            if (WIDE && in == 0 && !tc::mbar_wait(&Q.full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
-            float2 d[H][V / 2];
+        int t = r.first;
+        for (int turn = 0, stage = 0, phase = 0; turn < turns; ++turn) {
+            if (WIDE && !tc::mbar_wait(&Q.full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
 #pragma unroll
-            for (int u = 0; u < H; ++u) {
+            for (int u = 0; u < U; ++u, ++t, out += S.D) {
+                float2 d[V / 2], p[V / 2], ds[V / 2], q = make_float2(0.f, 0.f), e = q;
                 if constexpr (WIDE) {  // (rows of the next sequence, or what a box beyond the last one is filled with, are left out below)
-                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][in + u][lane * V]), row[K - 1 + u]);
-                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][1][in + u][lane * V]), d[u]);
+                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][u][lane * V]), row[K - 1 + u]);
+                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][1][u][lane * V]), d);
                 } else {
-                    if (t0 + u < r.len) {
+                    if (t < r.len) {
                         layer::unpack<T, V>(load<T, V, false>(px, have), row[K - 1 + u]);
-                        layer::unpack<T, V>(load<T, V, false>(pg, have), d[u]);
+                        layer::unpack<T, V>(load<T, V, false>(pg, have), d);
                     }
                     px += S.stride;
                     pg += S.D;
                 }
-            }
-            if (in + H == U) {
-                __syncwarp();
-                ask(turn + NS);
-                ++turn;
-                if (++stage == NS) stage = 0, phase ^= 1;
-            }
-#pragma unroll
-            for (int u = 0; u < H; ++u) {
-                const int t = t0 + u;
-                float2 p[V / 2], ds[V / 2];
-                float2 q = make_float2(0.f, 0.f), e = q;
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
                     p[i] = P.b[i];
 #pragma unroll
                     for (int k = 0; k < K; ++k) p[i] = fma(P.w[k][i], row[u + k][i], p[i]);
-                    ds[i] = make_float2(1.f, 1.f);
-                    if (S.act) {
+                }
+                if (S.act) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
                         const layer::sig<float2> v = layer::sigmoids(p[i]);
                         ds[i] = fma(mul(p[i], v.n), v.s, v.s);
                         p[i] = mul(p[i], v.s);
                     }
-                    q = fma(p[i], p[i], q);
-                    e = fma(d[u][i], p[i], e);
                 }
                 if (S.norm) {
-                    const float k = rsqrtf(head_sum<V>(q.x + q.y, S.norm) + S.eps), dot = head_sum<V>(e.x + e.y, S.norm) * k * k;
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i)
-                        d[u][i] = mul(fma(p[i], make_float2(-dot, -dot), d[u][i]), make_float2(k, k));
-                }
-                const bool there = t < r.len, own = t < r.last;
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i) {
-                    d[u][i] = there ? mul(d[u][i], ds[i]) : make_float2(0.f, 0.f);
-                    dp[K - 1 + u][i] = d[u][i];
-                }
-                if (own) {
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        db[i] = add(db[i], d[u][i]);
+                        q = fma(p[i], p[i], q);
+                        e = fma(d[i], p[i], e);
+                    }
+                    float k = q.x + q.y, dot = e.x + e.y;
+                    head_sums<V>(k, dot, S.norm);
+                    k = rsqrtf(k + S.eps);
+                    dot *= -k * k;
 #pragma unroll
-                        for (int k = 0; k < K; ++k) dw[k][i] = fma(d[u][i], row[u + k][i], dw[k][i]);
+                    for (int i = 0; i < V / 2; ++i) d[i] = mul(fma(p[i], make_float2(dot, dot), d[i]), make_float2(k, k));
+                }
+                if (S.act) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) d[i] = mul(d[i], ds[i]);
+                }
+                if (t >= r.len) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) d[i] = make_float2(0.f, 0.f);
+                }
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) dp[K - 1 + u][i] = d[i];
+                if (t < r.last) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        db[i] = add(db[i], d[i]);
+#pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k][i] = fma(d[i], row[u + k][i], dw[k][i]);
                     }
                 }
                 // row t - K + 1 of the sequence, its history's where that is below 0
@@ -136,7 +133,7 @@ conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps
                     float2 v[V / 2];
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        v[i] = mul(P.w[0][i], dp[K - 1 + u][i]);
+                        v[i] = mul(P.w[0][i], d[i]);
 #pragma unroll
                         for (int k = 1; k < K; ++k) v[i] = fma(P.w[k][i], dp[K - 1 + u - k][i], v[i]);
                     }
@@ -148,14 +145,16 @@ conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps
                     }
                     store<T, V, WIDE>(at >= 0 ? out : dhist + (r.n * (K - 1) + at + K - 1) * S.D + c, layer::pack<T, V>(v), have);
                 }
-                out += S.D;
             }
+            __syncwarp();
+            ask(turn + NS);
+            if (++stage == NS) stage = 0, phase ^= 1;
 #pragma unroll
             for (int k = 0; k < K - 1; ++k)
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
-                    row[k][i] = row[H + k][i];
-                    dp[k][i] = dp[H + k][i];
+                    row[k][i] = row[U + k][i];
+                    dp[k][i] = dp[U + k][i];
                 }
         }
     }
