@@ -11,10 +11,10 @@
 namespace kda {
 namespace conv {
 
-// One token from its K rows: y's V values
+// One token from its K rows: s's V values, and the sum of their squares
 template <int K, int V>
-__device__ __forceinline__ void one(const spec &S, const taps<V, K> &P, const float2 (&row)[K][V / 2], float2 (&y)[V / 2]) {
-    float ss = 0.f;
+__device__ __forceinline__ float one(const spec &S, const taps<V, K> &P, const float2 (*row)[V / 2], float2 (&y)[V / 2]) {
+    float2 q = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
         y[i] = P.b[i];
@@ -25,15 +25,14 @@ __device__ __forceinline__ void one(const spec &S, const taps<V, K> &P, const fl
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) y[i] = mul(y[i], layer::sigmoid(y[i]));
     }
-    if (S.norm) {
-        float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) q = fma(y[i], y[i], q);
-        ss = head_sum<V>(q.x + q.y, S.norm);
-        const float r = rsqrtf(ss + S.eps);
+    for (int i = 0; i < V / 2; ++i) q = fma(y[i], y[i], q);
+    return q.x + q.y;
+}
+template <int V> __device__ __forceinline__ void scale(float2 (&y)[V / 2], float squares, float eps) {
+    const float r = rsqrtf(squares + eps);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) y[i] = mul(y[i], make_float2(r, r));
-    }
+    for (int i = 0; i < V / 2; ++i) y[i] = mul(y[i], make_float2(r, r));
 }
 
 template <typename T, int K, int V, bool WIDE>
@@ -77,17 +76,30 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ s
             const int left = r.last - r.first - turn * U;
             if (WIDE && !tc::mbar_wait(&Q.full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if constexpr (WIDE) {
-                    layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][u][lane * V]), row[K - 1 + u]);
-                } else {
-                    if (u < left) layer::unpack<T, V>(load<T, V, false>(from, have), row[K - 1 + u]);
-                    from += S.stride;
+            for (int u0 = 0; u0 < U; u0 += 2) {  // two tokens, whose sums go over the lanes together
+                float2 v[2][V / 2];
+                float ss[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int u = u0 + j;
+                    if constexpr (WIDE) {
+                        layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][u][lane * V]), row[K - 1 + u]);
+                    } else {
+                        if (u < left) layer::unpack<T, V>(load<T, V, false>(from, have), row[K - 1 + u]);
+                        from += S.stride;
+                    }
+                    ss[j] = one<K, V>(S, P, &row[u], v[j]);
                 }
-                float2 v[V / 2];
-                one<K, V>(S, P, *reinterpret_cast<const float2(*)[K][V / 2]>(&row[u]), v);
-                if (u < left) store<T, V, WIDE>(out, layer::pack<T, V>(v), have);
-                out += S.D;
+                if (S.norm) {
+                    head_sums<V>(ss[0], ss[1], S.norm);
+                    scale<V>(v[0], ss[0], S.eps);
+                    scale<V>(v[1], ss[1], S.eps);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (u0 + j < left) store<T, V, WIDE>(out, layer::pack<T, V>(v[j]), have);
+                    out += S.D;
+                }
             }
             __syncwarp();
             ask(turn + NS);
@@ -124,7 +136,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
     float2 row[K][V / 2], out[V / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k) layer::unpack<T, V>(v[k], row[k]);
-    one<K, V>(S, P, row, out);
+    const float ss = one<K, V>(S, P, row, out);
+    if (S.norm) scale<V>(out, head_sum<V>(ss, S.norm), S.eps);
 #pragma unroll
     for (int k = 0; k + 1 < K; ++k) store<T, V, WIDE>(hist + k * S.D, v[k + 1], have);
     store<T, V, WIDE>(y + n * S.D + c, layer::pack<T, V>(out), have);
