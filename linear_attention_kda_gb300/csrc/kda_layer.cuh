@@ -126,22 +126,22 @@ template <typename T, int V, typename F> __device__ __forceinline__ vec<T, V> pa
 }
 template <typename F> __device__ __forceinline__ F unpack_one(const float *p) { return *reinterpret_cast<const F *>(p); }
 
-// The slot of row n of a step.  False for a row of a padded batch (-1), for a slot outside the pool, and for one
-// that an earlier row has (both set the device error); every thread of the block of NT gets the same answer.
-template <int NT>
-__device__ __forceinline__ bool find_slot(const int32_t *idx, int64_t slots, int64_t n, int64_t *slot, int *err) {
-    *slot = n;
-    if (!idx) return true;
+// The slot of row n of a step: -1 for a row of a padded batch and for a slot outside the pool (which sets the device error).  Whether an
+// earlier row has the slot, so that nothing of this one is written (an error as well), every thread of the block of NT asks
+// when it has its loads on their way: the answer takes a trip to memory for every NT rows.
+__device__ __forceinline__ int64_t slot_of(const int32_t *idx, int64_t slots, int64_t n, int *err) {
+    if (!idx) return n;
     const int32_t s = idx[n];
-    if (s == -1) return false;
-    bool bad = s < 0 || s >= slots;
-    if (!bad)
-        for (int64_t m = threadIdx.x; m < n; m += NT) bad |= idx[m] == s;
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) set_error(err, KDA_ERR_BAD_STATE_INDEX);
-        return false;
-    }
-    *slot = s;
+    if (s >= 0 && s < slots) return s;
+    if (s != -1 && threadIdx.x == 0) set_error(err, KDA_ERR_BAD_STATE_INDEX);
+    return -1;
+}
+template <int NT> __device__ __forceinline__ bool taken(const int32_t *idx, int64_t n, int64_t slot, int *err) {
+    if (!idx) return false;
+    bool bad = false;
+    for (int64_t m = threadIdx.x; m < n; m += NT) bad |= idx[m] == (int32_t)slot;
+    if (!__syncthreads_or(bad)) return false;
+    if (threadIdx.x == 0) set_error(err, KDA_ERR_BAD_STATE_INDEX);
     return true;
 }
 

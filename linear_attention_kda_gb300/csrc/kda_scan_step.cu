@@ -12,20 +12,29 @@ namespace scan {
 template <typename T, int V>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ kda_scan_step_args A, int *err) {
     const int c = (blockIdx.x * 128 + threadIdx.x) * V;
-    const int64_t n = blockIdx.y;
-    int64_t slot;
-    if (!layer::find_slot<128>(A.state_indices, A.num_slots, n, &slot, err) || c >= A.D) return;
+    const int64_t n = blockIdx.y, slot = layer::slot_of(A.state_indices, A.num_slots, n, err);
+    if (slot < 0) return;
     const spec S{A.gate_kind, A.input_scale, A.g_min};
     constexpr int P = layer::lanes<V>::N;
     using F = typename layer::lanes<V>::F;
     float *state = A.state + slot * A.D + c;
-    F x[P], z[P], i[P], h[P];
-    layer::unpack<T, V>(layer::load<T, V>((const T *)A.x + n * A.x_stride + c), x);
-    layer::unpack<T, V>(layer::load<T, V>((const T *)A.z + n * A.z_stride + c), z);
-    if (A.input_gate) layer::unpack<T, V>(layer::load<T, V>((const T *)A.input_gate + n * A.i_stride + c), i);
-    layer::unpack<float, V>(layer::load<float, V>(state), h);
+    const bool mine = c < A.D;
+    layer::vec<T, V> rx, rz, ri;
+    layer::vec<float, V> rs;
+    if (mine) {
+        rx = layer::load<T, V>((const T *)A.x + n * A.x_stride + c);
+        rz = layer::load<T, V>((const T *)A.z + n * A.z_stride + c);
+        if (A.input_gate) ri = layer::load<T, V>((const T *)A.input_gate + n * A.i_stride + c);
+        rs = layer::load<float, V>(state);
+    }
     channel<F> C[P];
-    load_channels<V>(A.A_log, A.dt_bias, c, true, C);
+    load_channels<V>(A.A_log, A.dt_bias, c, mine, C);
+    if (layer::taken<128>(A.state_indices, n, slot, err) || !mine) return;
+    F x[P], z[P], i[P], h[P];
+    layer::unpack<T, V>(rx, x);
+    layer::unpack<T, V>(rz, z);
+    if (A.input_gate) layer::unpack<T, V>(ri, i);
+    layer::unpack<float, V>(rs, h);
 #pragma unroll
     for (int k = 0; k < P; ++k) {
         F zk[1] = {z[k]}, xk[1] = {x[k]}, ik[1] = {i[k]};
@@ -48,7 +57,12 @@ static void launch(const kda_scan_step_args *a, cudaStream_t stream, int *err) {
 
 template <typename T>
 static void launch_t(const kda_scan_step_args *a, cudaStream_t stream, int *err) {
-    launch<T, 1>(a, stream, err);
+    // Four channels a thread where every row's address allows vectors of them (256 sequences of 4096 channels: XXX us one by one)
+    const uintptr_t tok = (uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate | (uintptr_t)a->h;
+    const bool wide = a->D % 4 == 0 && a->x_stride % 4 == 0 && a->z_stride % 4 == 0 && a->i_stride % 4 == 0 && tok % (4 * sizeof(T)) == 0 &&
+                      (uintptr_t)a->state % 16 == 0;
+    if (wide) launch<T, 4>(a, stream, err);
+    else launch<T, 1>(a, stream, err);
 }
 
 }  // namespace scan

@@ -124,8 +124,8 @@ template <typename T, int K, int V, bool WIDE>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ spec S, const T *x, T *state, const int32_t *idx, int64_t slots, T *y,
                                                         int *err) {
     const int64_t n = blockIdx.x;
-    int64_t slot;
-    if (!layer::find_slot<128>(idx, slots, n, &slot, err)) return;
+    const int64_t slot = layer::slot_of(idx, slots, n, err);
+    if (slot < 0) return;
     const int c = (blockIdx.y * 128 + threadIdx.x) * V, have = S.D - c;
     T *hist = state + slot * (K - 1) * S.D + c;
     const rows<T, V, WIDE> X{x + n * S.stride + c, hist, S.stride, S.D, K, have};
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = X.at(k - (K - 1));
     const taps<V, K> P(S, c, have);
+    if (layer::taken<128>(idx, n, slot, err)) return;
     float2 row[K][V / 2], out[V / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k) layer::unpack<T, V>(v[k], row[k]);
@@ -146,10 +147,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 template <typename T, int K, int V, bool WIDE>
 static cudaError_t fwd(const kda_short_conv_args *a, cudaStream_t stream, int *err) {
     const int blocks = (a->D + 32 * V - 1) / (32 * V);
-    // Runs of 128 tokens read 2 % of them twice (from L2), of 16 a fifth: short ones where long ones leave SMs without
-    // sixteen warps.
-    int L = 128;
-    while (L > 16 && (a->T / L) * blocks < 16 * 152) L /= 2;
+    const int L = run_length(a->T, a->N, (blocks + 3) / 4, 1, 6 * 152);
     const int64_t items = lin::chunk_slots(a->T, a->N, L) * blocks;
     row_maps maps{};
     if (WIDE && !layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>)) return cudaErrorUnknown;

@@ -137,6 +137,18 @@ struct row_maps {
     CUtensorMap x, dy;
 };
 
+// Tokens of a run: what a block takes is about L of them and 16 more (those that two runs share, and its beginning), and the
+// blocks come in rounds of as many as the GPU holds (`at_once`).  `runs` to a block, `blocks` of channels.
+inline int run_length(int64_t T, int64_t N, int blocks, int runs, int at_once) {
+    int best = 16;
+    int64_t least = INT64_MAX;
+    for (int L = 16; L <= 256; L *= 2) {
+        const int64_t grid = (lin::chunk_slots(T, N, L) + runs - 1) / runs * blocks, cost = (grid + at_once - 1) / at_once * (L + 16);
+        if (cost < least) least = cost, best = L;
+    }
+    return best;
+}
+
 __device__ __forceinline__ void check_all(const spec &S, int *err) {
     if (blockIdx.x > 0 || blockIdx.y > 0) return;
     for (int64_t n = threadIdx.x; n < S.N; n += blockDim.x) {

@@ -195,16 +195,12 @@ __global__ void __launch_bounds__(256) conv_sums_kernel(const float *sums, int64
     }
 }
 
-// Tokens of a run: long ones form less dp twice (K - 1 tokens of each), short ones make more blocks.
-static int run_length(int64_t T, int D) {
-    int L = 128;
-    while (L > 16 && (T / (L * NW)) * ((D + 127) / 128) < 2 * 152) L /= 2;
-    return L;
-}
+// (4096 tokens x 4096 channels by runs of 16, 32, 64 and 128: XXX)
+static int run_length(int64_t T, int64_t N, int D) { return run_length(T, N, (D + 127) / 128, NW, 2 * 152); }
 
 template <typename T, int K, int V, bool WIDE>
 static cudaError_t launch(const kda_short_conv_bwd_args *a, float *sums, cudaStream_t stream, int *err) {
-    const int L = run_length(a->T, a->D);
+    const int L = run_length(a->T, a->N, a->D);
     const int64_t slots = lin::chunk_slots(a->T, a->N, L), rows = (slots + NW - 1) / NW;
     row_maps maps{};
     if (WIDE && (!layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>) ||
@@ -236,7 +232,7 @@ static cudaError_t choose(const kda_short_conv_bwd_args *a, float *sums, bool wi
 
 size_t kda_short_conv_bwd_bytes(int64_t T, int64_t N, int D, int K) {
     using namespace kda::conv;
-    return (size_t)((kda::lin::chunk_slots(T, N, run_length(T, D)) + NW - 1) / NW) * (K + 1) * D * 4;
+    return (size_t)((kda::lin::chunk_slots(T, N, run_length(T, N, D)) + NW - 1) / NW) * (K + 1) * D * 4;
 }
 
 kda_status_t kda_launch_short_conv_bwd(const kda_short_conv_bwd_args *a, void *ws, cudaStream_t stream) {
