@@ -32,10 +32,19 @@ template <typename T, typename RT> __host__ __device__ __forceinline__ int row_b
 __device__ __forceinline__ float total(float v) { return v; }
 __device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
 
-// BULK: rows come by bulk copies into two places of shared memory in turn
+template <typename K, bool BULK> __device__ __forceinline__ const void *at_row(const void *p, int64_t base, const char *near) {
+    if constexpr (BULK) return near;
+    return (const K *)p + base;
+}
+template <typename K, int V, typename F, int P> __device__ __forceinline__ void row_part(const void *p, int c, F (&f)[P]) {
+    layer::unpack<K, V>(layer::load<K, V>((const K *)p + c), f);
+}
+
+// BULK: rows come by bulk copies into one or two places (`stages`) of shared memory in turn, and are read from there when they are needed.
+// Behind them, where there is room (`room`), lie scale * post_weight and pre_weight.
 template <typename T, typename RT, int V, int E, int NT, bool BULK>
 __global__ void __launch_bounds__(place<NT>::BLOCK, NT <= 256 ? 512 / place<NT>::BLOCK : 1)
-block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *sums, int *err) {
+block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *sums, int stages, int room, int *err) {
     using F = typename layer::lanes<V>::F;
     constexpr int P = layer::lanes<V>::N;  // values of a vector, one or two at a time
     __shared__ float parts[2 * 2 * (NT > 32 ? NT / 32 : 1)];
@@ -45,30 +54,36 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
     const int64_t first = (int64_t)blockIdx.x * place<NT>::ROWS + threadIdx.x / NT, each = (int64_t)gridDim.x * place<NT>::ROWS;
     const bool block = A.y != nullptr, channel = A.gate_kind == KDA_NORM_GATE_CHANNEL, pre = A.grad_normed != nullptr;
     const int stage_bytes = BULK ? row_bytes<T, RT>(A) : 0, rt = A.D * (int)sizeof(RT), tt = A.D * (int)sizeof(T);
+    // where the parts of a row begin in its place
+    const int at_d = rt, at_y = at_d + (A.grad_residual_out ? rt : 0), at_g = at_y + (block ? tt : 0), at_n = at_g + (channel ? tt : 0);
     auto ask = [&](int64_t row, int stage) {
         if (!BULK || threadIdx.x != 0 || row >= A.T) return;
         char *to = memory + stage * stage_bytes;
         tc::mbar_arrive_expect_tx(&full[stage], stage_bytes);
-        auto copy = [&](const void *p, int bytes) {
-            if (!p) return;
-            tc::bulk_g2s(to, (const char *)p + row * bytes, bytes, &full[stage]);
-            to += bytes;
+        auto copy = [&](const void *p, int at, int bytes) {
+            if (p) tc::bulk_g2s(to + at, (const char *)p + row * bytes, bytes, &full[stage]);
         };
-        copy(A.residual, rt);
-        copy(A.grad_residual_out, rt);
-        copy(A.y, tt);
-        copy(channel ? A.gate : nullptr, tt);
-        copy(A.grad_normed, tt);
+        copy(A.residual, 0, rt);
+        copy(A.grad_residual_out, at_d, rt);
+        copy(A.y, at_y, tt);
+        copy(channel ? A.gate : nullptr, at_g, tt);
+        copy(A.grad_normed, at_n, tt);
     };
+    float *const near = reinterpret_cast<float *>(memory + stages * stage_bytes);
     if (BULK) {
         if (threadIdx.x == 0) {
             tc::mbar_init(&full[0], 1);
             tc::mbar_init(&full[1], 1);
             tc::fence_proxy_async();
         }
+        if (room)
+            for (int c = threadIdx.x; c < A.D; c += NT) {
+                near[c] = (A.scale_vec ? A.scale_vec[c] : A.scale) * (A.post_weight ? A.post_weight[c] : 1.f);
+                near[A.D + c] = A.pre_weight ? A.pre_weight[c] : 1.f;
+            }
         __syncthreads();
         ask(first, 0);
-        ask(first + each, 1);
+        if (stages == 2) ask(first + each, 1);
     }
     int at = 0, stage = 0, phase = 0;
     F sq[E][P], sp[E][P];  // sums of d s yh and of dn rh
@@ -76,121 +91,137 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
     for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int i = 0; i < P; ++i) sq[e][i] = sp[e][i] = splat<F>(0.f);
+    auto column = [&](int e) { return (e * NT + tid) * V; };
+    // weights of a vector's channels
+    auto from = [&](const float *w, int c, F (&f)[P], float none) {
+        if (w) layer::unpack<float, V>(layer::load<float, V>(w + c), f);
+        else
+#pragma unroll
+            for (int i = 0; i < P; ++i) f[i] = splat<F>(none);
+    };
+    auto scaled = [&](int c, F (&f)[P]) {  // scale * post_weight
+        if (BULK && room) {
+            from(near, c, f, 0.f);
+        } else {
+            F w[P];
+            from(A.scale_vec, c, f, A.scale);
+            from(A.post_weight, c, w, 1.f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) f[i] = mul(f[i], w[i]);
+        }
+    };
+    auto normal = [&](int c, F (&f)[P]) { from(BULK && room ? near + A.D : A.pre_weight, c, f, 1.f); };
     const float inv = 1.f / A.D;
     for (int64_t row = first; row < A.T; row += each) {
         const int64_t base = row * A.D;
-        F r[E][P], d[E][P], y[E][P], s[E][P], dn[E][P];
-        if (BULK && !tc::mbar_wait(&full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
         const char *here = memory + stage * stage_bytes;
-        auto rows = [&](const void *p, auto kind, int bytes, F (&f)[E][P]) {
-            using K = decltype(kind);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = (e * NT + tid) * V;
-                if (p && c < A.D) layer::unpack<K, V>(layer::load<K, V>((BULK ? (const K *)here : (const K *)p + base) + c), f[e]);
-                else
-#pragma unroll
-                    for (int i = 0; i < P; ++i) f[e][i] = splat<F>(0.f);
-            }
-            if (p) here += bytes;
-        };
-        rows(A.residual, RT{}, rt, r);
-        rows(A.grad_residual_out, RT{}, rt, d);
-        rows(A.y, T{}, tt, y);
-        rows(channel ? A.gate : nullptr, T{}, tt, s);
-        rows(A.grad_normed, T{}, tt, dn);
+        if (BULK && !tc::mbar_wait(&full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+        F r[E][P], d[E][P], y[E][P], s[E][P];
         const float kt = A.gate_kind == KDA_NORM_GATE_TOKEN ? layer::sigmoid(ld((const T *)A.gate + row)) : 1.f;
-        if (BULK) {
-            __syncthreads();
-            ask(row + 2 * each, stage);
-            if (++stage == 2) stage = 0, phase ^= 1;
-        }
         float ky = 1.f;
-        if (A.post_norm) {
+        if (block) {
             F q = splat<F>(0.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
+            for (int e = 0; e < E; ++e) {
+                if (column(e) >= A.D) continue;
+                row_part<T, V>(at_row<T, BULK>(A.y, base, here + at_y), column(e), y[e]);
 #pragma unroll
                 for (int i = 0; i < P; ++i) q = fma(y[e][i], y[e][i], q);
-            float ss[1] = {total(q)};
-            row_sum<NT>(ss, parts, at);
-            ky = rsqrtf(ss[0] * inv + A.eps);
+            }
+            if (A.post_norm) {
+                float ss[1] = {total(q)};
+                row_sum<NT>(ss, parts, at);
+                ky = rsqrtf(ss[0] * inv + A.eps);
+            }
         }
-        // weights of a vector's channels: 1 where there are none, and behind the last channel
-        auto weights = [&](const float *w, int e, F (&f)[P], float none) {
-            const int c = (e * NT + tid) * V;
-            if (w && c < A.D) layer::unpack<float, V>(layer::load<float, V>(w + c), f);
-            else
+        F q = splat<F>(0.f), t = q;
 #pragma unroll
-                for (int i = 0; i < P; ++i) f[i] = splat<F>(none);
-        };
-        float sr[2] = {0.f, 0.f};
-        {
-            F q = splat<F>(0.f), t = q;
+        for (int e = 0; e < E; ++e) {
+            const int c = column(e);
+            if (c >= A.D) continue;
+            row_part<RT, V>(at_row<RT, BULK>(A.residual, base, here), c, r[e]);
+            if (block) {
+                F w[P];
+                scaled(c, w);
+                if (channel) {
+                    row_part<T, V>(at_row<T, BULK>(A.gate, base, here + at_g), c, s[e]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                F w[P], c[P], v[P];
-                weights(A.post_weight, e, w, 1.f);
-                weights(A.scale_vec, e, c, A.scale);
-                weights(A.pre_weight, e, v, 1.f);
+                    for (int i = 0; i < P; ++i) s[e][i] = layer::sigmoid(s[e][i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s[e][i] = splat<F>(kt);
+                }
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    if (block) {
-                        s[e][i] = channel ? layer::sigmoid(s[e][i]) : splat<F>(kt);
-                        y[e][i] = mul(y[e][i], splat<F>(ky));  // yh
-                        r[e][i] = fma(mul(y[e][i], w[i]), mul(c[i], s[e][i]), r[e][i]);
-                    }
+                    y[e][i] = mul(y[e][i], splat<F>(ky));  // yh
+                    r[e][i] = fma(mul(y[e][i], w[i]), s[e][i], r[e][i]);
+                }
+            }
+            if (pre) {
+                F n[P], v[P];
+                row_part<T, V>(at_row<T, BULK>(A.grad_normed, base, here + at_n), c, n);
+                normal(c, v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
                     q = fma(r[e][i], r[e][i], q);
-                    t = fma(mul(v[i], dn[e][i]), r[e][i], t);
+                    t = fma(mul(v[i], n[i]), r[e][i], t);
                 }
             }
-            sr[0] = total(q);
-            sr[1] = total(t);
         }
+        float k = 0.f, m = 0.f;
         if (pre) {
+            float sr[2] = {total(q), total(t)};
             row_sum<NT>(sr, parts, at);
-            const float k = rsqrtf(sr[0] * inv + A.eps), m = -sr[1] * k * k * inv;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                F v[P];
-                weights(A.pre_weight, e, v, 1.f);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    sp[e][i] = fma(mul(dn[e][i], splat<F>(k)), r[e][i], sp[e][i]);
-                    d[e][i] = fma(splat<F>(k), fma(r[e][i], splat<F>(m), mul(v[i], dn[e][i])), d[e][i]);
-                }
-            }
+            k = rsqrtf(sr[0] * inv + A.eps);
+            m = -sr[1] * k * k * inv;
         }
-        // d is complete
         F sy = splat<F>(0.f), sg = sy;  // sums of post_weight dp yh, and of d scale p for a token's gate
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = (e * NT + tid) * V;
-            if (c < A.D) layer::store_once((RT *)A.grad_residual + base + c, layer::pack<RT, V>(d[e]));
+            const int c = column(e);
+            if (c >= A.D) continue;
+            if (A.grad_residual_out) row_part<RT, V>(at_row<RT, BULK>(A.grad_residual_out, base, here + at_d), c, d[e]);
+            else
+#pragma unroll
+                for (int i = 0; i < P; ++i) d[e][i] = splat<F>(0.f);
+            if (pre) {
+                F n[P], v[P];
+                row_part<T, V>(at_row<T, BULK>(A.grad_normed, base, here + at_n), c, n);
+                normal(c, v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    sp[e][i] = fma(mul(n[i], splat<F>(k)), r[e][i], sp[e][i]);
+                    d[e][i] = fma(splat<F>(k), fma(r[e][i], splat<F>(m), mul(v[i], n[i])), d[e][i]);
+                }
+            }
+            layer::store_once((RT *)A.grad_residual + base + c, layer::pack<RT, V>(d[e]));
             if (!block) continue;
-            F w[P], cs[P], dg[P];
-            weights(A.post_weight, e, w, 1.f);
-            weights(A.scale_vec, e, cs, A.scale);
+            F w[P], dg[P];
+            scaled(c, w);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const F ds = mul(d[e][i], s[e][i]);
+                const F ds = mul(d[e][i], s[e][i]), g = mul(w[i], y[e][i]);  // d s, scale p
                 sq[e][i] = fma(ds, y[e][i], sq[e][i]);
-                const F g = mul(mul(cs[i], w[i]), y[e][i]);  // scale p
                 dg[i] = mul(mul(g, ds), fma(s[e][i], splat<F>(-1.f), splat<F>(1.f)));
                 sg = fma(d[e][i], g, sg);
                 sy = fma(ds, g, sy);
-                d[e][i] = mul(ds, mul(cs[i], w[i]));
+                d[e][i] = mul(ds, w[i]);
             }
-            if (channel && c < A.D) layer::store_once((T *)A.grad_gate + base + c, layer::pack<T, V>(dg));
+            if (channel) layer::store_once((T *)A.grad_gate + base + c, layer::pack<T, V>(dg));
+        }
+        if (BULK) {
+            __syncthreads();
+            ask(row + stages * each, stage);
+            if (++stage == stages) stage = 0, phase ^= 1;
         }
         if (!block) continue;
         float ss[2] = {total(sy), total(sg)};
         if (A.post_norm || A.gate_kind == KDA_NORM_GATE_TOKEN) row_sum<NT>(ss, parts, at);
         if (A.gate_kind == KDA_NORM_GATE_TOKEN && tid == 0) st((T *)A.grad_gate + row, ss[1] * kt * (1.f - kt));
-        const float m = A.post_norm ? -ss[0] * inv : 0.f;
+        m = A.post_norm ? -ss[0] * inv : 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = (e * NT + tid) * V;
+            const int c = column(e);
             if (c >= A.D) continue;
 #pragma unroll
             for (int i = 0; i < P; ++i) d[e][i] = mul(fma(y[e][i], splat<F>(m), d[e][i]), splat<F>(ky));
@@ -202,7 +233,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
     float *out = sums + first * 2 * A.D;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int c = (e * NT + tid) * V;
+        const int c = column(e);
         if (c >= A.D) continue;
         layer::store(out + c, layer::pack<float, V>(sq[e]));
         layer::store(out + A.D + c, layer::pack<float, V>(sp[e]));
@@ -232,22 +263,34 @@ __global__ void __launch_bounds__(256) block_norm_sums_kernel(const float *sums,
     }
 }
 
+struct share {
+    int smem, stages, room, per_sm;  // of a block
+};
 template <typename K, bool BULK>
-static cudaError_t launch(const kda_block_norm_bwd_args *a, float *sums, int smem, cudaStream_t stream, int *rows, int *err) {
+static cudaError_t launch(const kda_block_norm_bwd_args *a, float *sums, const share &S, cudaStream_t stream, int *rows, int *err) {
     using P = place<K::nt>;
     auto *kernel = block_norm_bwd_kernel<typename K::t, typename K::rt, K::v, K::e, K::nt, BULK>;
-    if (smem > 48 * 1024) {
+    if (S.smem > 46 * 1024) {  // (with what the kernel declares, above 48 KB)
         static std::atomic<uint64_t> done{0};
-        const cudaError_t e = lin::allow_smem(kernel, 227 * 1024 - 1024, done);
+        const cudaError_t e = lin::allow_smem(kernel, 226 * 1024 + 512, done);
         if (e != cudaSuccess) return e;
     }
-    // as many blocks as run at once: 512 threads to an SM
-    const int64_t most = 152 * (K::nt <= 256 ? 512 / P::BLOCK : 1);
     int64_t blocks = (a->T + P::ROWS - 1) / P::ROWS;
-    if (blocks > most) blocks = most;
+    if (blocks > 152 * S.per_sm) blocks = 152 * S.per_sm;
     *rows = (int)blocks * P::ROWS;
-    kernel<<<(unsigned)blocks, P::BLOCK, smem, stream>>>(*a, sums, err);
+    kernel<<<(unsigned)blocks, P::BLOCK, S.smem, stream>>>(*a, sums, S.stages, S.room, err);
     return cudaGetLastError();
+}
+
+// Two rows on their way where as many blocks as registers allow (512 threads) still fit into an SM, else where one does, else
+// one row.  An SM has 228 KB, of which a block takes 1 KB and some bytes beside its rows.
+static share share_of(int row, int weights, int per_sm) {
+    for (int n : {per_sm, 1}) {
+        const int most = 228 * 1024 / n - 1024 - 512;
+        if (2 * row + weights <= most) return {2 * row + weights, 2, 1, n};
+        if (2 * row <= most) return {2 * row, 2, 0, n};
+    }
+    return {row, 1, 0, 1};
 }
 
 }  // namespace norm
@@ -273,15 +316,11 @@ kda_status_t kda_launch_block_norm_bwd(const kda_block_norm_bwd_args *a, void *w
         choose(a->dtype, a->residual_dtype, a->D, wide, [&](auto t) {
             using K = decltype(t);
             float *sums = want ? (float *)ws : nullptr;
-            if constexpr (K::nt >= 128 && K::v > 1) {
-                // two rows ahead, where as many blocks still fit into an SM
-                const int smem = 2 * row_bytes<typename K::t, typename K::rt>(*a);
-                if (smem <= (K::nt <= 256 ? 112 * place<K::nt>::BLOCK / 256 : 224) * 1024) {
-                    e = launch<K, true>(a, sums, smem, stream, &rows, err);
-                    return;
-                }
-            }
-            e = launch<K, false>(a, sums, 0, stream, &rows, err);
+            const int per_sm = K::nt <= 256 ? 512 / place<K::nt>::BLOCK : 1;
+            if constexpr (K::nt >= 128 && K::v > 1)
+                e = launch<K, true>(a, sums, share_of(row_bytes<typename K::t, typename K::rt>(*a), 8 * a->D, per_sm), stream, &rows, err);
+            else
+                e = launch<K, false>(a, sums, {0, 0, 0, per_sm}, stream, &rows, err);
         });
     }
     if (e == cudaSuccess && want) {
