@@ -827,6 +827,11 @@ def _tokens(where, name, t, rows, D, dtype, device) -> int:
     raise ValueError(f"{where}: {name} is not on the device of the others")
 
 
+def _rows_like(x, stride):
+    """A dense tensor like x, whose rows may lie a stride apart (0: dense)."""
+    return torch.empty_like(x) if stride == 0 else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _scan_inputs(where, x, z, input_gate, A_log, dt_bias, gate, input_scale):
     """(rows, D, dtype, device, dtype code, gate, input scale, strides) of a scan's inputs, checked."""
     if gate not in SCAN_GATES:
@@ -883,7 +888,7 @@ def scan_fwd(x, z, input_gate=None, *, A_log=None, dt_bias=None, gate: str = "so
         _require(where, dev, (("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, (N, D), f32),
                               ("final_state", final_state, (N, D), f32), ("checkpoints", checkpoints, kept, f32), ("out", out, (T, D), dt)))
     if out is None:
-        out = torch.empty((T, D), dtype=dt, device=x.device)
+        out = _rows_like(x, strides[0])
     if final_state is None and output_final_state:
         final_state = torch.empty((N, D), dtype=f32, device=x.device)
     ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_scan_fwd_workspace_size(T, N, D, code), x.device)
@@ -909,10 +914,10 @@ def scan_bwd(x, z, input_gate, grad_h, checkpoints, *, A_log=None, dt_bias=None,
             or (grad_final_state is not None and _off(grad_final_state, (N, D), f32, dev))):
         _require(where, dev, (("grad_h", grad_h, (T, D), dt), ("checkpoints", checkpoints, kept, f32),
                               ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("grad_final_state", grad_final_state, (N, D), f32)))
-    empty = lambda *s, dtype=f32: torch.empty(s, dtype=dtype, device=x.device)  # noqa: E731
-    grads = {"x": empty(T, D, dtype=dt), "z": empty(T, D, dtype=dt)}
+    empty = lambda *s: torch.empty(s, dtype=f32, device=x.device)  # noqa: E731
+    grads = {"x": torch.empty_like(grad_h), "z": torch.empty_like(grad_h)}
     if input_gate is not None:
-        grads["input_gate"] = empty(T, D, dtype=dt)
+        grads["input_gate"] = torch.empty_like(grad_h)
     if param_grads and gate != "log":
         grads["A_log"], grads["dt_bias"] = empty(D), empty(D)
     if state_grad:
@@ -934,7 +939,7 @@ def scan_step(x, z, input_gate, state, *, A_log=None, dt_bias=None, gate: str = 
     N, D, dt, dev, code, gk, ik, strides = _scan_inputs(where, x, z, input_gate, A_log, dt_bias, gate, input_scale)
     slots = _slots(where, state, 2, (D,), torch.float32, dev, N, state_indices, out, dt)
     if out is None:
-        out = torch.empty((N, D), dtype=dt, device=x.device)
+        out = _rows_like(x, strides[0])
     _run("kda_scan_step", dev, L.kda_scan_step,
          _SCAN_STEP.pack(N, D, code, gk, ik, g_min, _p(x), _p(z), _p(input_gate), *strides, _p(A_log), _p(dt_bias), _p(state),
                          _p(state_indices), slots, _p(out)))
@@ -992,7 +997,7 @@ def short_conv_fwd(x, weight, bias=None, *, activation: str = "silu", norm_dim: 
         _require(where, dev, (("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, hist, dt),
                               ("final_state", final_state, hist, dt), ("out", out, (T, D), dt)))
     if out is None:
-        out = torch.empty((T, D), dtype=dt, device=x.device)
+        out = _rows_like(x, stride)
     if final_state is None and output_final_state:
         final_state = torch.empty(hist, dtype=dt, device=x.device)
     _run("kda_short_conv_fwd", dev, L.kda_short_conv_fwd,
@@ -1021,14 +1026,13 @@ def short_conv_bwd(x, weight, bias, grad_y, *, activation: str = "silu", norm_di
             or (grad_final_state is not None and _off(grad_final_state, hist, dt, dev))):
         _require(where, dev, (("grad_y", grad_y, (T, D), dt), ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32),
                               ("initial_state", initial_state, hist, dt), ("grad_final_state", grad_final_state, hist, dt)))
-    empty = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device=x.device)  # noqa: E731
-    grads = {"x": empty(T, D, dtype=dt)}
+    grads = {"x": torch.empty_like(grad_y)}
     if param_grads:
-        grads["weight"] = empty(D, K)
+        grads["weight"] = torch.empty_like(weight)
         if bias is not None:
-            grads["bias"] = empty(D)
+            grads["bias"] = torch.empty_like(bias)
     if state_grad:
-        grads["initial_state"] = empty(*hist, dtype=dt)
+        grads["initial_state"] = torch.empty(hist, dtype=dt, device=x.device)
     ws, ws_bytes, _keep = _workspace(where, workspace, L.kda_short_conv_bwd_workspace_size(T, N, D, K, code), x.device)
     _run("kda_short_conv_bwd", dev, L.kda_short_conv_bwd,
          _CONV_BWD.pack(T, N, D, K, code, act, norm_dim, norm_eps, _p(x), stride, _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
@@ -1046,7 +1050,7 @@ def short_conv_step(x, weight, bias, state, *, activation: str = "silu", norm_di
     N, D, K, dt, dev, code, act, stride = _conv_inputs(where, x, weight, bias, activation)
     slots = _slots(where, state, 3, (K - 1, D), dt, dev, N, state_indices, out, dt)
     if out is None:
-        out = torch.empty((N, D), dtype=dt, device=x.device)
+        out = _rows_like(x, stride)
     _run("kda_short_conv_step", dev, L.kda_short_conv_step,
          _CONV_STEP.pack(N, D, K, code, act, norm_dim, norm_eps, _p(x), stride, _p(weight), _p(bias), _p(state), _p(state_indices), slots,
                          _p(out)))
@@ -1054,28 +1058,26 @@ def short_conv_step(x, weight, bias, state, *, activation: str = "silu", norm_di
 
 
 # ---------------------------------------------------------------- norms around a block
-def _norm_inputs(where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm, more):
+def _norm_inputs(where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm, tokens, rows):
     """(T, D, dtype, device, code, residual code, gate kind, post_norm, scale, scale vector) of a block norm's inputs, checked with
-    `more`: (name, tensor or None, which shape and dtype: "res", "tok" or "gate")."""
+    `tokens` and `rows`: (name, tensor or None) of y's and of residual's dtype."""
     if residual.dim() != 2:
         raise ValueError(f"{where}: residual has shape [tokens, channels]")
-    if y is None and (gate is not None or post_weight is not None or not pre_norm or isinstance(scale, torch.Tensor)):
-        raise ValueError(f"{where}: without y there is a norm in front of the next block alone")
-    (T, D), rt, dev, f32 = residual.shape, residual.dtype, residual.get_device(), torch.float32
-    dt = next((t.dtype for t in (y,) + tuple(t for n, t, k in more if k == "tok") if t is not None), rt)
-    code = KDA_BF16 if dt is torch.bfloat16 else KDA_F32 if dt is f32 else _dtype_code(y)
     vec = scale if isinstance(scale, torch.Tensor) else None
+    if y is None and (gate is not None or post_weight is not None or not pre_norm or vec is not None):
+        raise ValueError(f"{where}: without y there is a norm in front of the next block alone")
+    shape, rt, dev, f32 = residual.shape, residual.dtype, residual.get_device(), torch.float32
+    dt = y.dtype if y is not None else rt if tokens[1] is None else tokens[1].dtype
     kind = 0 if gate is None else 2 if gate.dim() == 1 else 1
-    gs = (T,) if kind == 2 else (T, D)
-    shapes = {"res": ((T, D), rt), "tok": ((T, D), dt), "gate": (gs, dt)}
-    for name, t, shape, dtype in (("residual", residual, (T, D), rt), ("y", y, (T, D), dt), ("gate", gate, gs, dt),
-                                  ("post_weight", post_weight, (D,), f32), ("pre_weight", pre_weight, (D,), f32), ("scale", vec, (D,), f32)):
-        if t is not None and _off(t, shape, dtype, dev) or dev < 0:
-            _require(where, dev, ((name, t, shape, dtype),))
-    for name, t, k in more:
-        if t is not None and _off(t, *shapes[k], dev):
-            _require(where, dev, ((name, t) + shapes[k],))
-    return (T, D, dt, dev, code, _dtype_code(residual), kind, int(post_norm and y is not None), 1.0 if vec is not None else float(scale), vec)
+    gs, par = shape if kind < 2 else shape[:1], shape[1:]
+    if (dev < 0 or not residual.is_contiguous() or (y is not None and _off(y, shape, dt, dev)) or (gate is not None and _off(gate, gs, dt, dev))
+            or (post_weight is not None and _off(post_weight, par, f32, dev)) or (pre_weight is not None and _off(pre_weight, par, f32, dev))
+            or (vec is not None and _off(vec, par, f32, dev)) or (tokens[1] is not None and _off(tokens[1], shape, dt, dev))
+            or (rows[1] is not None and _off(rows[1], shape, rt, dev))):
+        _require(where, dev, (("residual", residual, shape, rt), ("y", y, shape, dt), ("gate", gate, gs, dt), ("post_weight", post_weight, par, f32),
+                              ("pre_weight", pre_weight, par, f32), ("scale", vec, par, f32), tokens + (shape, dt), rows + (shape, rt)))
+    return (shape[0], shape[1], dt, dev, KDA_BF16 if dt is torch.bfloat16 else _dtype_code(residual if y is None else y), _dtype_code(residual),
+            kind, int(post_norm and y is not None), 1.0 if vec is not None else float(scale), vec)
 
 
 def block_norm_fwd(y, residual, gate=None, *, post_weight=None, pre_weight=None, scale=1.0, post_norm: bool = True, pre_norm: bool = True,
@@ -1089,8 +1091,7 @@ def block_norm_fwd(y, residual, gate=None, *, post_weight=None, pre_weight=None,
     (None).  residual_out=residual and normed=y work in place."""
     where, L = "block_norm_fwd", _lib or load_library()
     T, D, dt, dev, code, rcode, kind, post, scale, vec = _norm_inputs(
-        where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm,
-        (("normed", normed, "tok"), ("residual_out", residual_out, "res")))
+        where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm, ("normed", normed), ("residual_out", residual_out))
     if y is None:
         if residual_out is not None:
             raise ValueError(f"{where}: without y the residual stream stays as it is")
@@ -1100,7 +1101,7 @@ def block_norm_fwd(y, residual, gate=None, *, post_weight=None, pre_weight=None,
     if not pre_norm:
         normed = None
     elif normed is None:
-        normed = torch.empty((T, D), dtype=dt, device=residual.device)
+        normed = torch.empty_like(residual, dtype=dt) if y is None else torch.empty_like(y)
     _run("kda_block_norm_fwd", dev, L.kda_block_norm_fwd,
          _NORM.pack(T, D, code, rcode, kind, post, int(pre_norm), eps, scale, _p(vec), _p(y), _p(gate), _p(residual), _p(post_weight),
                     _p(pre_weight), _p(out), _p(normed)))
@@ -1121,8 +1122,8 @@ def block_norm_bwd(y, residual, gate, grad_residual, grad_normed, *, post_weight
     if grad_normed is not None and not pre_norm:
         raise ValueError(f"{where}: grad_normed without pre_norm")
     T, D, dt, dev, code, rcode, kind, post, scale, vec = _norm_inputs(
-        where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm,
-        (("grad_normed", grad_normed, "tok"), ("grad_residual", grad_residual, "res")))
+        where, y, residual, gate, post_weight, pre_weight, scale, post_norm, pre_norm, ("grad_normed", grad_normed),
+        ("grad_residual", grad_residual))
     grads = {"residual": torch.empty_like(residual)}
     if y is not None:
         grads["y"] = torch.empty_like(y)
