@@ -1,4 +1,4 @@
-// kda_scan_bwd: tiles of 64 tokens by 64 channels as in kda_scan_fwd, taken from a sequence's last to its first.  With the
+// kda_scan_bwd: tiles of L tokens by W channels as in kda_scan_fwd, taken from a sequence's last to its first.  With the
 // adjoint lambda_t = dh_t + m_{t+1}, m_t = a_t lambda_t is what goes on to the token before.
 //
 // A thread forms decays and inputs of its eight tokens, runs the state forwards and the adjoint backwards from zero for the
@@ -11,13 +11,14 @@
 namespace kda {
 namespace scan {
 
-constexpr int BWD_L = CK;  // a tile begins at a checkpoint
-constexpr int BWD_R = BWD_L / NW;
+// a tile begins at a checkpoint: L = 64, 128 or 256 tokens
+template <int W> using bwd_shape = shape<W, 8>;
+static_assert(bwd_shape<64>::L % CK == 0, "checkpoints");
 
-template <typename T> struct bwd_memory {
-    ring<T, 4, BWD_L> next;
-    tile_memory M;
-    entries E;
+template <typename T, int W> struct bwd_memory {
+    ring<T, 4, bwd_shape<W>> next;
+    tile_memory<W> M;
+    entries<W> E;
     float f[NW][W];               // the warps' values of the state, then the states that enter their tokens
     float sA[NW][W], sb[NW][W];   // the warps' sums for A_log and dt_bias
 };
@@ -26,14 +27,15 @@ struct sums_of {
     float *rows;  // [slots][2][D], or NULL
 };
 
-template <typename T, bool TMA>
+template <typename T, int W, bool TMA>
 __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1)
 scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<4> maps,
                 const __grid_constant__ sums_of out, int blocks, int *err) {
-    constexpr int L = BWD_L, R = BWD_R;
+    using X = bwd_shape<W>;
+    constexpr int L = X::L, R = X::R;
     extern __shared__ __align__(128) char memory[];
-    bwd_memory<T> &S = *reinterpret_cast<bwd_memory<T> *>(memory);
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    bwd_memory<T, W> &S = *reinterpret_cast<bwd_memory<T, W> *>(memory);
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32, pair = lane % X::LPR * 2, row0 = w * X::RW + lane / X::LPR * R;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
     if (out.rows)
@@ -49,7 +51,7 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
         if (t.p < 0) return;
         const int stage = turn & 1, tok = begin(t), n = gated ? 4 : 3;
         tc::mbar_arrive_expect_tx(&S.next.full[stage], (uint32_t)(n * L * W * sizeof(T)));
-        for (int i = 0; i < n; ++i) tc::tma_load_3d(&S.next.x[stage][i][0][0], &maps.m[i], t.block * W, 0, tok, &S.next.full[stage]);
+        for (int i = 0; i < n; ++i) load_rows<X>(&S.next.x[stage][i][0][0], maps.m[i], t.block, tok, &S.next.full[stage]);
     };
     auto advance = [&](int turn) {
         way.next();
@@ -68,6 +70,8 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
         ask(0);
     }
     __syncthreads();
+    constexpr int WARPS = W > 32 ? W / 32 : 1;     // of a role in join(), and
+    const int mine = threadIdx.x % (32 * WARPS);  // this thread's channel in it
     channel<float2> C{};
     int of = -1;      // the block of channels whose parameters C holds
     tile last{0, -1, 0, 0, 0, 0, 0};  // the tile before, whose sums are in place
@@ -86,21 +90,21 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
     for (int turn = 0;; ++turn) {
         const tile t = S.next.t[turn & 3];
         if (t.p < 0) break;
-        const int stage = turn & 1, first = begin(t), tok = first + w * R, len = t.b - tok < R ? t.b - tok : R;
-        const int c = t.block * W + lane * 2, have = A.D - c;
+        const int stage = turn & 1, first = begin(t), tok = first + row0, len = t.b - tok < R ? t.b - tok : R;
+        const int c = t.block * W + pair, have = A.D - c;
         if (of != t.block) C = load_channel(A.A_log, A.dt_bias, c, have);
         of = t.block;
         // the state that enters the tile, asked for early by those who will run it over the warps
         float checkpoint = 0.f;
-        if (threadIdx.x / W == 2 && t.count > 0 && t.block * W + (int)threadIdx.x % W < A.D)
-            checkpoint = A.checkpoints[((int64_t)t.a / CK + t.n + (first - t.a) / CK) * A.D + t.block * W + threadIdx.x % W];
+        if (w / WARPS == 2 && mine < W && t.count > 0 && t.block * W + mine < A.D)
+            checkpoint = A.checkpoints[((int64_t)t.a / CK + t.n + (first - t.a) / CK) * A.D + t.block * W + mine];
         if (TMA && !tc::mbar_wait(&S.next.full[stage], (turn >> 1) & 1)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
         // some tokens from r0 on of input k (z, x, grad_h, input_gate)
         auto get = [&](int k, int r0, const void *p, int64_t stride, auto &f) {
             constexpr int N = sizeof(f) / sizeof(f[0]);
 #pragma unroll
             for (int r = 0; r < N; ++r)  // (by TMA there are rows of other sequences behind the last token)
-                f[r] = TMA ? load_pair<T, true>(&S.next.x[stage][k][w * R + r0 + r][lane * 2], 2)
+                f[r] = TMA ? load_pair<T, true>(&S.next.x[stage][k][row0 + r0 + r][pair], 2)
                            : load_pair<T, false>((const T *)p + (int64_t)(tok + r0 + r) * stride + c, r0 + r < len ? have : 0);
         };
         float2 u[R], d[R], sum = make_float2(0.f, 0.f), h = sum, m = sum;
@@ -148,12 +152,17 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
                 m = step(d[r0 + r], add(m, g[r]), make_float2(0.f, 0.f));
             }
         }
-        *reinterpret_cast<float2 *>(&S.M.g[w][lane * 2]) = sum;
-        *reinterpret_cast<float2 *>(&S.M.d[w][lane * 2]) = decay_of(sum).d;
-        *reinterpret_cast<float2 *>(&S.M.b[w][lane * 2]) = m;
-        *reinterpret_cast<float2 *>(&S.f[w][lane * 2]) = h;
-        join<R, true>(B, !chains, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, err, [&](int quarter, int ch) {
-            if (quarter == 2) {
+        float2 before_sum, before, behind_sum, behind, all = sum;
+        over_groups<X, false>(all, h, before_sum, before);
+        if (lane >= 32 - X::LPR) *reinterpret_cast<float2 *>(&S.f[w][pair]) = h;
+        over_groups<X, true>(sum, m, behind_sum, behind);
+        if (lane < X::LPR) {
+            *reinterpret_cast<float2 *>(&S.M.g[w][pair]) = sum;
+            *reinterpret_cast<float2 *>(&S.M.d[w][pair]) = decay_of(sum).d;
+            *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = m;
+        }
+        join<X, true>(B, !chains, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, err, [&](int role, int ch) {
+            if (role == 2) {
                 float v = checkpoint;
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
@@ -170,8 +179,8 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
             ask(turn + 1);
             advance(turn + 2);
         }
-        h = *reinterpret_cast<const float2 *>(&S.f[w][lane * 2]);
-        m = *reinterpret_cast<const float2 *>(&S.M.g[w][lane * 2]);
+        h = group_entry<X>(*reinterpret_cast<const float2 *>(&S.f[w][pair]), before_sum, before);
+        m = group_entry<X>(*reinterpret_cast<const float2 *>(&S.M.g[w][pair]), behind_sum, behind);
         // what enters may be an infinity or a NaN, which a decay of 0 erases
         const bool odd = __any_sync(0xffffffffu, !finite(h) || !finite(m));
         auto erase = [&](float2 &v, float2 by) {
@@ -236,12 +245,19 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
                 }
             }
         }
-        *reinterpret_cast<float2 *>(&S.sA[w][lane * 2]) = sA;
-        *reinterpret_cast<float2 *>(&S.sb[w][lane * 2]) = sb;
+#pragma unroll
+        for (int off = X::LPR; off < 32; off *= 2) {
+            sA = add(sA, make_float2(__shfl_xor_sync(0xffffffffu, sA.x, off), __shfl_xor_sync(0xffffffffu, sA.y, off)));
+            sb = add(sb, make_float2(__shfl_xor_sync(0xffffffffu, sb.x, off), __shfl_xor_sync(0xffffffffu, sb.y, off)));
+        }
+        if (lane < X::LPR) {
+            *reinterpret_cast<float2 *>(&S.sA[w][pair]) = sA;
+            *reinterpret_cast<float2 *>(&S.sb[w][pair]) = sb;
+        }
         last = t;
     }
     __syncthreads();
-    if (threadIdx.x / W == 3) add_up(threadIdx.x % W);
+    if (w / WARPS == 3 && mine < W) add_up(mine);
 }
 
 // Column sums of the tiles' rows: 32 columns to a block, its eight warps every eighth row.
@@ -269,23 +285,43 @@ __global__ void __launch_bounds__(256) scan_sums_kernel(const float *rows, int64
     }
 }
 
-template <typename T, bool TMA>
-static cudaError_t launch(const kda_scan_bwd_args *a, const row_maps<4> &maps, void *ws, cudaStream_t stream, int *err) {
+template <typename T, int W, bool TMA>
+static cudaError_t launch(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream, int *err) {
+    using X = bwd_shape<W>;
     static std::atomic<int> running[64];
-    constexpr size_t smem = sizeof(bwd_memory<T>);
+    constexpr size_t smem = sizeof(bwd_memory<T, W>);
+    row_maps<4> maps{};
+    if (TMA && (!make_row_map<X>(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype) ||
+                !make_row_map<X>(&maps.m[1], a->x, a->T, a->D, a->x_stride, a->dtype) ||
+                !make_row_map<X>(&maps.m[2], a->grad_h, a->T, a->D, a->D, a->dtype) ||
+                (a->input_gate && !make_row_map<X>(&maps.m[3], a->input_gate, a->T, a->D, a->i_stride, a->dtype))))
+        return cudaErrorUnknown;
     int blocks = (a->D + W - 1) / W, grid = 0;
     board B{};
-    const size_t rows = board_layout(a->T, a->N, a->D, BWD_L, ws, &B);
+    const size_t rows = board_layout(a->T, a->N, a->D, X::L, ws, &B);
     sums_of out{a->grad_A_log || a->grad_dt_bias ? (float *)((char *)ws + rows) : nullptr};
-    cudaError_t e = running_blocks(scan_bwd_kernel<T, TMA>, smem, running, B.slots * blocks, &grid);
+    cudaError_t e = running_blocks(scan_bwd_kernel<T, W, TMA>, smem, running, B.slots * blocks, &grid);
     if (e != cudaSuccess) return e;
     kda_scan_bwd_args args = *a;
-    row_maps<4> m = maps;
-    void *p[] = {&args, &B, &m, &out, &blocks, &err};
-    e = cudaLaunchCooperativeKernel((const void *)scan_bwd_kernel<T, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+    void *p[] = {&args, &B, &maps, &out, &blocks, &err};
+    e = cudaLaunchCooperativeKernel((const void *)scan_bwd_kernel<T, W, TMA>, dim3(grid), dim3(NT), p, smem, stream);
     if (e != cudaSuccess || !out.rows) return e;
     scan_sums_kernel<<<dim3((a->D + 31) / 32, 2), 256, 0, stream>>>(out.rows, B.slots, a->D, a->grad_A_log, a->grad_dt_bias);
     return cudaGetLastError();
+}
+
+template <typename T> static cudaError_t choose(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream, int *err) {
+    const int64_t es = sizeof(T), per = 16 / es;
+    const bool tma = a->T > 0 && a->D % per == 0 &&
+                     (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate | (uintptr_t)a->grad_h) & 15) == 0 &&
+                     (((uintptr_t)a->grad_x | (uintptr_t)a->grad_z | (uintptr_t)a->grad_input_gate) % (2 * es)) == 0 && a->x_stride % per == 0 &&
+                     a->z_stride % per == 0 && (!a->input_gate || a->i_stride % per == 0);
+    // (by element alignment alone the same tiles are taken, so that the results are the same)
+    switch (tile_width(a->N, a->D)) {
+        case 16: return tma ? launch<T, 16, true>(a, ws, stream, err) : launch<T, 16, false>(a, ws, stream, err);
+        case 32: return tma ? launch<T, 32, true>(a, ws, stream, err) : launch<T, 32, false>(a, ws, stream, err);
+        default: return tma ? launch<T, 64, true>(a, ws, stream, err) : launch<T, 64, false>(a, ws, stream, err);
+    }
 }
 
 }  // namespace scan
@@ -293,25 +329,14 @@ static cudaError_t launch(const kda_scan_bwd_args *a, const row_maps<4> &maps, v
 
 size_t kda_scan_bwd_bytes(int64_t T, int64_t N, int D, kda_dtype_t) {
     using namespace kda::scan;
-    return board_layout(T, N, D, BWD_L, nullptr, nullptr) + (size_t)kda::lin::chunk_slots(T, N, BWD_L) * 2 * D * 4;
+    // (the shortest tile's, which holds all)
+    constexpr int L = bwd_shape<64>::L;
+    return board_layout(T, N, D, L, nullptr, nullptr) + (size_t)kda::lin::chunk_slots(T, N, L) * 2 * D * 4;
 }
 
 kda_status_t kda_launch_scan_bwd(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream) {
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::scan;
-    row_maps<4> maps{};
-    const int64_t es = a->dtype == KDA_BF16 ? 2 : 4, per = 16 / es;
-    const bool tma = a->T > 0 && a->D % per == 0 &&
-                     (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate | (uintptr_t)a->grad_h) & 15) == 0 &&
-                     (((uintptr_t)a->grad_x | (uintptr_t)a->grad_z | (uintptr_t)a->grad_input_gate) % (2 * es)) == 0 && a->x_stride % per == 0 &&
-                     a->z_stride % per == 0 && (!a->input_gate || a->i_stride % per == 0);
-    if (tma && (!make_row_map(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype, BWD_L) ||
-                !make_row_map(&maps.m[1], a->x, a->T, a->D, a->x_stride, a->dtype, BWD_L) ||
-                !make_row_map(&maps.m[2], a->grad_h, a->T, a->D, a->D, a->dtype, BWD_L) ||
-                (a->input_gate && !make_row_map(&maps.m[3], a->input_gate, a->T, a->D, a->i_stride, a->dtype, BWD_L))))
-        return KDA_ERR_CUDA;
-    if (a->dtype == KDA_BF16)
-        return kda_cuda_status(tma ? launch<kda::bf16, true>(a, maps, ws, stream, err) : launch<kda::bf16, false>(a, maps, ws, stream, err));
-    return kda_cuda_status(tma ? launch<float, true>(a, maps, ws, stream, err) : launch<float, false>(a, maps, ws, stream, err));
+    return kda_cuda_status(a->dtype == KDA_BF16 ? choose<kda::bf16>(a, ws, stream, err) : choose<float>(a, ws, stream, err));
 }

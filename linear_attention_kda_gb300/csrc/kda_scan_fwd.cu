@@ -1,28 +1,29 @@
-// kda_scan_fwd: a block takes tiles of L tokens by 64 channels (kda_scan_tiles.cuh), each of its eight warps L / 8 tokens,
-// each lane two channels.  Tiles come by TMA two ahead.  A thread forms the decay and the input of its elements once,
+// kda_scan_fwd: a block takes tiles of L tokens by W channels (kda_scan_tiles.cuh), each of its eight warps L / 8 tokens,
+// each lane two channels and R of them.  Tiles come by TMA two ahead.  A thread forms the decay and the input of its elements once,
 // keeps both in registers, runs them from zero for the tile's sums, and, when it knows what enters, runs them again for h.
 #include "kda_scan_tiles.cuh"
 
 namespace kda {
 namespace scan {
 
-// Tokens of a tile: a long one shares the cost of joining, its inputs twice and d and u have to fit.
-template <typename T> constexpr int fwd_tile = sizeof(T) == 2 ? 128 : 64;
+// Many tokens a thread share the cost of joining; the tile's inputs twice (in shared memory) and d and u have to fit.
+template <typename T, int W> using fwd_shape = shape<W, sizeof(T) == 2 ? 16 : 8>;
 
-template <typename T> struct fwd_memory {
-    ring<T, 3, fwd_tile<T>> next;
-    tile_memory M;
+template <typename T, int W> struct fwd_memory {
+    ring<T, 3, fwd_shape<T, W>> next;
+    tile_memory<W> M;
 };
 
 // TMA: rows are 16-byte aligned.  Else a thread reads its elements when it needs them.
-template <typename T, bool TMA>
+template <typename T, int W, bool TMA>
 __global__ void __launch_bounds__(NT, 2)
 scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<3> maps, int joined,
                 int blocks, int *err) {
-    constexpr int L = fwd_tile<T>, R = L / NW;
+    using X = fwd_shape<T, W>;
+    constexpr int L = X::L, R = X::R;
     extern __shared__ __align__(128) char memory[];
-    fwd_memory<T> &S = *reinterpret_cast<fwd_memory<T> *>(memory);
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    fwd_memory<T, W> &S = *reinterpret_cast<fwd_memory<T, W> *>(memory);
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32, pair = lane % X::LPR * 2, row0 = w * X::RW + lane / X::LPR * R;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
     if (joined) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
@@ -37,7 +38,7 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         const int tok = way.t.a + way.t.p * L, n = gated ? 3 : 2;
         tc::fence_proxy_async();  // (join() has written to the stage)
         tc::mbar_arrive_expect_tx(&S.next.full[stage], (uint32_t)(n * L * W * sizeof(T)));
-        for (int i = 0; i < n; ++i) tc::tma_load_3d(&S.next.x[stage][i][0][0], &maps.m[i], way.t.block * W, 0, tok, &S.next.full[stage]);
+        for (int i = 0; i < n; ++i) load_rows<X>(&S.next.x[stage][i][0][0], maps.m[i], way.t.block, tok, &S.next.full[stage]);
     };
     if (TMA && threadIdx.x == 0) {
         tc::mbar_init(&S.next.full[0], 1);
@@ -55,8 +56,8 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     for (int turn = 0;; ++turn) {
         const tile t = S.next.t[turn & 1];
         if (t.p < 0) break;
-        const int tok = t.a + t.p * L + w * R, len = t.b - tok < R ? t.b - tok : R;  // tokens of this warp, below 1 where it has none
-        const int c = t.block * W + lane * 2, have = A.D - c;
+        const int tok = t.a + t.p * L + row0, len = t.b - tok < R ? t.b - tok : R;  // tokens of this thread, below 1 where it has none
+        const int c = t.block * W + pair, have = A.D - c;
         if (of != t.block) C = load_channel(A.A_log, A.dt_bias, c, have);
         of = t.block;
         const int stage = turn & 1;
@@ -69,7 +70,7 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
             auto get = [&](int k, const void *p, int64_t stride, float2 (&f)[PART]) {
 #pragma unroll
                 for (int r = 0; r < PART; ++r)  // (by TMA there are rows of other sequences behind the last token)
-                    f[r] = TMA ? load_pair<T, true>(&S.next.x[stage][k][w * R + r0 + r][lane * 2], 2)
+                    f[r] = TMA ? load_pair<T, true>(&S.next.x[stage][k][row0 + r0 + r][pair], 2)
                                : load_pair<T, false>((const T *)p + (int64_t)(tok + r0 + r) * stride + c, r0 + r < len ? have : 0);
             };
             float2 z[PART], x[PART];
@@ -103,14 +104,18 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) h = step(d[r], h, u[r]);
-        *reinterpret_cast<float2 *>(&S.M.g[w][lane * 2]) = sum;
-        *reinterpret_cast<float2 *>(&S.M.d[w][lane * 2]) = decay_of(sum).d;
-        *reinterpret_cast<float2 *>(&S.M.b[w][lane * 2]) = h;
-        join<R, false>(B, joined && !chains, t, A.D, A.initial_state, A.final_state,
-                A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr, (t.b - t.a - t.p * L + CK - 1) / CK, S.M,
-                *reinterpret_cast<entries *>(&S.next.x[stage]), err, [](int, int) {});
+        float2 before_sum, before;
+        over_groups<X, false>(sum, h, before_sum, before);
+        if (lane >= 32 - X::LPR) {
+            *reinterpret_cast<float2 *>(&S.M.g[w][pair]) = sum;
+            *reinterpret_cast<float2 *>(&S.M.d[w][pair]) = decay_of(sum).d;
+            *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = h;
+        }
+        join<X, false>(B, joined && !chains, t, A.D, A.initial_state, A.final_state,
+                       A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr,
+                       (t.b - t.a - t.p * L + CK - 1) / CK, S.M, *reinterpret_cast<entries<W> *>(&S.next.x[stage]), err, [](int, int) {});
         if (loader) ask(stage);  // every warp is done with this stage
-        h = *reinterpret_cast<const float2 *>(&S.M.g[w][lane * 2]);
+        h = group_entry<X>(*reinterpret_cast<const float2 *>(&S.M.g[w][pair]), before_sum, before);
         // what enters may be an infinity or a NaN, which a decay of 0 erases
         const bool odd = __any_sync(0xffffffffu, !finite(h));
         T *out = (T *)A.h + (int64_t)tok * A.D + c;
@@ -125,25 +130,39 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     if (!joined) check_all(A.cu_seqlens, A.T, A.N, err);
 }
 
-template <typename T, bool TMA>
-static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void *ws, cudaStream_t stream, int *err) {
+template <typename T, int W, bool TMA>
+static cudaError_t launch(const kda_scan_args *a, void *ws, cudaStream_t stream, int *err) {
+    using X = fwd_shape<T, W>;
     static std::atomic<int> running[64];
-    constexpr size_t smem = sizeof(fwd_memory<T>);
+    constexpr size_t smem = sizeof(fwd_memory<T, W>);
+    row_maps<3> maps{};
+    if (TMA && (!make_row_map<X>(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype) ||
+                !make_row_map<X>(&maps.m[1], a->x, a->T, a->D, a->x_stride, a->dtype) ||
+                (a->input_gate && !make_row_map<X>(&maps.m[2], a->input_gate, a->T, a->D, a->i_stride, a->dtype))))
+        return cudaErrorUnknown;
     int blocks = (a->D + W - 1) / W, grid = 0;
-    const int64_t tiles = lin::chunk_slots(a->T, a->N, fwd_tile<T>) * blocks;
     board B{};
-    int joined = a->T > fwd_tile<T>;  // else no sequence has a second tile
-    if (joined) board_layout(a->T, a->N, a->D, fwd_tile<T>, ws, &B);
-    const cudaError_t e = running_blocks(scan_fwd_kernel<T, TMA>, smem, running, tiles, &grid);
+    int joined = a->T > X::L;  // else no sequence has a second tile
+    if (joined) board_layout(a->T, a->N, a->D, X::L, ws, &B);
+    const cudaError_t e = running_blocks(scan_fwd_kernel<T, W, TMA>, smem, running, lin::chunk_slots(a->T, a->N, X::L) * blocks, &grid);
     if (e != cudaSuccess) return e;
-    if (!joined) {
-        scan_fwd_kernel<T, TMA><<<grid, NT, smem, stream>>>(*a, B, maps, 0, blocks, err);
-        return cudaGetLastError();
-    }
     kda_scan_args args = *a;
-    row_maps<3> m = maps;
-    void *p[] = {&args, &B, &m, &joined, &blocks, &err};
-    return cudaLaunchCooperativeKernel((const void *)scan_fwd_kernel<T, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+    void *p[] = {&args, &B, &maps, &joined, &blocks, &err};
+    if (!joined) return cudaLaunchKernel((const void *)scan_fwd_kernel<T, W, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+    return cudaLaunchCooperativeKernel((const void *)scan_fwd_kernel<T, W, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+}
+
+template <typename T> static cudaError_t choose(const kda_scan_args *a, void *ws, cudaStream_t stream, int *err) {
+    const int64_t es = sizeof(T), per = 16 / es;
+    const bool tma = a->T > 0 && a->D % 2 == 0 && (uintptr_t)a->h % (2 * es) == 0 &&
+                     (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate) & 15) == 0 && a->x_stride % per == 0 &&
+                     a->z_stride % per == 0 && (!a->input_gate || a->i_stride % per == 0);
+    // (by element alignment alone the same tiles are taken, so that the results are the same)
+    switch (tile_width(a->N, a->D)) {
+        case 16: return tma ? launch<T, 16, true>(a, ws, stream, err) : launch<T, 16, false>(a, ws, stream, err);
+        case 32: return tma ? launch<T, 32, true>(a, ws, stream, err) : launch<T, 32, false>(a, ws, stream, err);
+        default: return tma ? launch<T, 64, true>(a, ws, stream, err) : launch<T, 64, false>(a, ws, stream, err);
+    }
 }
 
 }  // namespace scan
@@ -151,7 +170,8 @@ static cudaError_t launch(const kda_scan_args *a, const row_maps<3> &maps, void 
 
 size_t kda_scan_fwd_bytes(int64_t T, int64_t N, int D, kda_dtype_t dtype) {
     using namespace kda::scan;
-    const int L = dtype == KDA_BF16 ? fwd_tile<kda::bf16> : fwd_tile<float>;
+    // (the shortest tile's, which holds all)
+    const int L = dtype == KDA_BF16 ? fwd_shape<kda::bf16, 64>::L : fwd_shape<float, 64>::L;
     return T > L ? board_layout(T, N, D, L, nullptr, nullptr) : 0;
 }
 
@@ -159,16 +179,5 @@ kda_status_t kda_launch_scan_fwd(const kda_scan_args *a, void *ws, cudaStream_t 
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     using namespace kda::scan;
-    row_maps<3> maps{};
-    const int64_t es = a->dtype == KDA_BF16 ? 2 : 4, per = 16 / es;
-    const int L = a->dtype == KDA_BF16 ? fwd_tile<kda::bf16> : fwd_tile<float>;
-    const bool tma = a->T > 0 && a->D % 2 == 0 && (uintptr_t)a->h % (2 * es) == 0 &&
-                     (((uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate) & 15) == 0 && a->x_stride % per == 0 &&
-                     a->z_stride % per == 0 && (!a->input_gate || a->i_stride % per == 0);
-    if (tma && (!make_row_map(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype, L) || !make_row_map(&maps.m[1], a->x, a->T, a->D, a->x_stride, a->dtype, L) ||
-                (a->input_gate && !make_row_map(&maps.m[2], a->input_gate, a->T, a->D, a->i_stride, a->dtype, L))))
-        return KDA_ERR_CUDA;
-    if (a->dtype == KDA_BF16)
-        return kda_cuda_status(tma ? launch<kda::bf16, true>(a, maps, ws, stream, err) : launch<kda::bf16, false>(a, maps, ws, stream, err));
-    return kda_cuda_status(tma ? launch<float, true>(a, maps, ws, stream, err) : launch<float, false>(a, maps, ws, stream, err));
+    return kda_cuda_status(a->dtype == KDA_BF16 ? choose<kda::bf16>(a, ws, stream, err) : choose<float>(a, ws, stream, err));
 }

@@ -1,7 +1,7 @@
 // How the two sequence-long directions of kda_scan split a batch and join it again.
 //
-// A tile is L tokens of one sequence by W = 64 channels, taken by one block of threads; it reads its inputs once and keeps
-// what it made of them.  The tiles of a sequence and its 64 channels are a chain.  Where the chains are many and none much longer than
+// A tile is L tokens of one sequence by W channels, taken by one block of threads; it reads its inputs once and keeps
+// what it made of them.  The tiles of a sequence and its W channels are a chain.  Where the chains are many and none much longer than
 // the rest, a block goes through whole chains, longest first, and hands the state on by shared memory.  Else the blocks take every
 // gridDim-th tile, and tiles join through L2: what a tile does to the state that enters it is two numbers per channel, its decay
 // and the state that it leaves from zero, and there are three levels of them, each folded in a fixed order, so that the
@@ -28,9 +28,15 @@ namespace kda {
 namespace scan {
 
 constexpr int CK = KDA_SCAN_CHECKPOINT;
-constexpr int W = 64;                   // channels of a tile, two a lane
 constexpr int NW = 8;                   // warps of a block
 constexpr int NT = 32 * NW;
+
+// A tile's shape: W channels, two a lane; a warp holds GW groups of R tokens one after the other.  64 channels are one group of 32
+// lanes; 32 or 16 make two or four times as many chains, each of a half or a quarter of the tiles (tile_width()).
+template <int W_, int R_> struct shape {
+    static constexpr int W = W_, R = R_, LPR = W / 2, GW = 32 / LPR, RW = R * GW, L = NW * RW;
+    static constexpr int BOX = L < 256 ? L : 256;  // rows of a TMA box
+};
 constexpr int G = 16;                   // tiles of a group, groups of a supergroup
 
 // The workspace.  A sequence whose first tile has slot f (lin::chunk_slots) has its groups from f / 16 + n on and its
@@ -72,7 +78,8 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
 }
 
 // Clears the entries, looks at all of cu_seqlens, lists the tiles and the chains and chooses between the two ways: whole chains where
-// the longest one is no more than a block's share of all tiles (XXX), and where any part of cu_seqlens is bad (the slots may not be
+// the longest one is no more than 1.4 times a block's share of all tiles (a tile of a chain takes 4.7 us, one that joins others 6.5: bf16,
+// forwards, two blocks to an SM), and where any part of cu_seqlens is bad (the slots may not be
 // those that the sequences think, so that no tile may wait for another).
 // Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 2 us more.)
 static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int *err) {
@@ -148,7 +155,7 @@ static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu,
         if (sorted && N > 1)  // places behind the last tile
             for (int64_t i = (int64_t)total + threadIdx.x; i < B.slots; i += NT) B.plan[i] = make_int4(0, -1, 0, 0);
         if (threadIdx.x == 0) {
-            B.mode[0] = bad || longest * gridDim.x <= total * blocks;
+            B.mode[0] = bad || longest * gridDim.x * 5 <= total * blocks * 7;
             B.mode[1] = 0;
             if (bad) set_error(err, KDA_ERR_BAD_SEQLENS);
         }
@@ -203,29 +210,59 @@ struct tile {
     int first;         // slot of the sequence's first tile
 };
 
-struct tile_memory {
+template <int W> struct tile_memory {
     float g[NW][W], d[NW][W], b[NW][W];  // the warps' sums of log-decays, decays and values; after join() g is the state that enters each warp's tokens
     float from[W];                       // the state behind the last tile, where a block takes whole chains
 };
 // entries on their way through a block: those of the supergroup, of the groups and of the tiles before a tile
-typedef unsigned long long entries[1 + 2 * (G - 1)][W];
+template <int W> using entries = unsigned long long[1 + 2 * (G - 1)][W];
 
-// With every warp's (g, d, b) of its R tokens in place: leaves the tile's sum for others and finds what enters each warp's tokens.  start, end:
+// Over the groups of a warp, in the direction of the scan: sum and value become those up to and with each group's, before_* those up to it.
+template <typename X, bool BACK>
+__device__ __forceinline__ void over_groups(float2 &sum, float2 &value, float2 &before_sum, float2 &before) {
+    before_sum = before = make_float2(0.f, 0.f);
+    if constexpr (X::GW > 1) {
+        const int lane = threadIdx.x & 31, grp = lane / X::LPR;
+        auto of = [&](float2 v, int groups) {
+            const int from = lane + (BACK ? groups : -groups) * X::LPR;
+            return make_float2(__shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from));
+        };
+#pragma unroll
+        for (int off = 1; off < X::GW; off *= 2) {
+            const float2 s = of(sum, off), v = of(value, off);
+            if (BACK ? grp + off < X::GW : grp >= off) {
+                value = step_or_erase(decay_of(sum).d, v, value);
+                sum = add(sum, s);
+            }
+        }
+        const float2 s = of(sum, 1), v = of(value, 1);
+        if (BACK ? grp < X::GW - 1 : grp > 0) before_sum = s, before = v;
+    }
+}
+// The state that enters a group's tokens from the one that enters the warp's
+template <typename X> __device__ __forceinline__ float2 group_entry(float2 warp, float2 before_sum, float2 before) {
+    if constexpr (X::GW > 1) return step_or_erase(decay_of(before_sum).d, warp, before);
+    return warp;
+}
+
+// With every warp's (g, d, b) in place: leaves the tile's sum for others and finds what enters each warp's tokens.  start, end:
 // the state (or adjoint) before and behind the sequence, [N, D] or NULL; kept: where the checkpoints of this tile go (NULL: nowhere), `room` rows.
 // links: tiles of this sequence wait for one another; E: memory that every warp is done with at the first barrier.
-// BACK: the direction is from the last token to the first, so from the last warp to the first.  more_work(quarter, channel): what
-// two otherwise idle quarters of the block (2 and 3) do meanwhile.
-template <int R, bool BACK, typename F>
+// BACK: the direction is from the last token to the first, so from the last warp to the first.  more_work(role, channel): what
+// two otherwise idle roles (2 and 3) do meanwhile.
+template <typename X, bool BACK, typename F>
 __device__ __forceinline__ void join(const board &B, bool links, const tile &t, int D, const float *start, float *end, float *kept, int room,
-                                     tile_memory &M, entries &E, int *err, F &&more_work) {
-    static_assert(4 * W <= NT, "four quarters");
-    const int tid = threadIdx.x, quarter = tid / W, ch = tid % W, c = t.block * W + ch;
+                                     tile_memory<X::W> &M, entries<X::W> &E, int *err, F &&more_work) {
+    // four roles, each of as many warps as its W threads need
+    constexpr int W = X::W, WARPS = W > 32 ? W / 32 : 1;
+    static_assert(4 * WARPS <= NW, "four roles");
+    const int ch = threadIdx.x % (32 * WARPS), role = ch < W ? (int)threadIdx.x / (32 * WARPS) : NW, c = t.block * W + ch;
     const bool more = t.p + 1 < t.count;
     __syncthreads();
     const int q = links ? t.p % G : 0, gq = links ? t.p / G % G : 0, super = links ? t.p / (G * G) : 0;
     const int64_t slot = t.first + t.p;
     float sum = 0.f, v = 0.f, h = 0.f;
-    if (quarter == 0) {
+    if (role == 0) {
         if (t.p == 0) h = start && c < D ? start[(int64_t)t.n * D + c] : 0.f;
         else if (!links) h = M.from[ch];
     }
@@ -241,7 +278,7 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
         };
         const unsigned long long *tiles = B.entry[0] + (slot - q) * D,
                                  *groups = B.entry[1] + ((int64_t)t.first / G + t.n + super * G) * D;
-        if (quarter == 0) {
+        if (role == 0) {
             if (more) {
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
@@ -256,18 +293,18 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
                 }
                 if (c < D) put(B.entry[0] + slot * D + c, sum, v);
             }
-        } else if (quarter == 1) {
+        } else if (role == 1) {
             if (super > 0) fetch(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super - 1) * D, 0, 1, 0);
             fetch(groups, 0, gq, 1);
-        } else if (quarter == 2) {
+        } else if (role == 2) {
             fetch(tiles, 0, q, G);
-        } else {
+        } else if (role == 3) {
             fetch(tiles, BATCH, q, G);
             fetch(groups, BATCH, gq, 1);
         }
         __syncthreads();
     }
-    if (quarter == 0) {
+    if (role == 0) {
         if (links && c < D) {
             if (q == G - 1 && more) {
                 float gd = 1.f, gb = 0.f;
@@ -286,7 +323,7 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
             const int w = BACK ? NW - 1 - i : i;
-            if (!BACK && w * R % CK == 0 && kept && w * R / CK < room && c < D) kept[(int64_t)(w * R / CK) * D + c] = h;
+            if (!BACK && w * X::RW % CK == 0 && kept && w * X::RW / CK < room && c < D) kept[(int64_t)(w * X::RW / CK) * D + c] = h;
             M.g[w][ch] = h;
             h = step_or_erase(M.d[w][ch], h, M.b[w][ch]);
         }
@@ -294,8 +331,8 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
             put(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super) * D + c, h, 0.f);
         if (end && c < D && !more) end[(int64_t)t.n * D + c] = h;
         M.from[ch] = h;
-    } else if (quarter > 1) {
-        more_work(quarter, ch);
+    } else if (role == 2 || role == 3) {
+        more_work(role, ch);
     }
     __syncthreads();
 }
@@ -359,17 +396,21 @@ __device__ __forceinline__ void check_all(const int32_t *cu, int64_t T, int64_t 
 }
 
 // Boxes of NI tensors of two tiles, and which tiles come next
-template <typename T, int NI, int L> struct ring {
-    T x[2][NI][L][W];
+template <typename T, int NI, typename X> struct ring {
+    T x[2][NI][X::L][X::W];
     uint64_t full[2];
     tile t[4];
 };
 template <int NI> struct row_maps {
     CUtensorMap m[NI];
 };
-// boxes of L rows and W channels
-inline bool make_row_map(CUtensorMap *m, const void *base, int64_t T, int D, int64_t stride, kda_dtype_t dtype, int L) {
-    return layer::make_row_map(m, base, T, D, stride, dtype, W, L);
+template <typename X> inline bool make_row_map(CUtensorMap *m, const void *base, int64_t T, int D, int64_t stride, kda_dtype_t dtype) {
+    return layer::make_row_map(m, base, T, D, stride, dtype, X::W, X::BOX);
+}
+// Asks for a tile's rows of one tensor
+template <typename X, typename T> __device__ __forceinline__ void load_rows(T *to, const CUtensorMap &m, int block, int tok, uint64_t *full) {
+#pragma unroll
+    for (int r = 0; r < X::L; r += X::BOX) tc::tma_load_3d(to + r * X::W, &m, block * X::W, 0, tok + r, full);
 }
 
 // Two neighbouring channels of a row: by one access where rows are aligned for it, else by their elements
@@ -392,6 +433,17 @@ __device__ __forceinline__ channel<float2> load_channel(const float *A_log, cons
     auto two = [&](const float *p, float none) { return make_float2(p && have > 0 ? p[c] : none, p && have > 1 ? p[c + 1] : none); };
     const float2 A = two(A_log, 0.f);
     return {two(dt_bias, 0.f), make_float2(expf(A.x), expf(A.y))};
+}
+
+// Channels of a tile.  64 cost least: each row of a tile is two sectors or more, a warp has no groups to join, and its reads of shared
+// memory no bank conflicts.  Fewer make more chains, so that more blocks have whole ones, of which the last ends sooner, and
+// tiles of more tokens, of which fewer join where they have to.  At 64 / 32 / 16 channels, bf16 (f32), D = 4096, us: forwards 16384 tokens of one
+// sequence (64 chains of 64 channels) 203 / 201 / 184, 131072 of D = 256 (4) 127 / 127 / 125 (180 / 152 / 137), 4 sequences (256) 250 / 191 / 197,
+// 6 (384) 334 / 246 / 260 (405 / 287 / 297), 8 (512) 360 / 345 / 375, 12 (768) 451 / 459 / 508 (555 / 558 / 575), 32 (2048) 1040 / 1092 / 1234;
+// gradients 8192 of one 242 / 236 / 223, 3 sequences (192) 276 / 263 / 236, 6 (384) 461 / 382 / 400, 12 (768) 690 / 718 / 765.
+inline int tile_width(int64_t N, int D) {
+    const int64_t chains = N * ((D + 63) / 64);
+    return chains < 2 * 152 ? 16 : chains < 4 * 152 ? 32 : 64;
 }
 
 // Blocks of a cooperative launch: as many as run at once, at most one for each tile.
