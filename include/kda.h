@@ -540,11 +540,12 @@ kda_status_t kda_rope(const kda_rope_args *args, struct CUstream_st *stream);
  * sqrt(1 - a^2) (_NORM: of independent inputs, h keeps their variance; 0 where a >= 1).  The input gate i may be
  * absent (factor 1).
  *
- * Values: g is at most 0 in use; greater ones (KDA_SCAN_LOG) are computed as given and may overflow.  A decay of 0
- * (g = -inf, or so low that exp(g) is 0 in fp32) erases what the state held, infinities and NaN included; so does,
- * for the states after them, a run of tokens whose whole decay is 0 in fp32.  A NaN or an infinity stays in its sequence and
- * channel.  Arithmetic and states are fp32; a decay near 1 is kept as a - 1, so that what a long memory holds does not drift with the
- * rounding of a; h is rounded once to dtype.
+ * Values: g is at most 0 in use; greater ones (KDA_SCAN_LOG) are computed as given and may overflow.  exp(g) counts as 0
+ * below the normal range of fp32 (g below about -87.3), c of _NORM where 1 - a^2 is at most 1e-30.  A decay of 0 erases what the state
+ * held before the call, infinities and NaN included; so does, for the states after them, a run of tokens whose whole decay is 0
+ * in fp32.  A NaN or an infinity stays in its sequence and channel; one that a token of the call itself brings in may last to
+ * the sequence's end whatever its decays.  Arithmetic and states are fp32; a decay near 1 is kept as a - 1, so that what a
+ * long memory holds does not drift with the rounding of a; h is rounded once to dtype.
  *
  * Shapes: x, z, input_gate and h [T, D], any D; tokens of x, z and input_gate are *_stride elements apart (0: D,
  * dense), so that slices of one projection can be read where they lie.  Tensors of dtype are aligned to their
@@ -562,8 +563,8 @@ kda_status_t kda_rope(const kda_rope_args *args, struct CUstream_st *stream);
 #define KDA_SCAN_INPUT_NORM 2
 #define KDA_SCAN_CHECKPOINT 64     /* tokens from one checkpoint to the next */
 typedef struct {
-    int64_t T, N;                  /* tokens (all sequences packed), sequences (>= 1) */
-    int32_t D;                     /* channels, 1 .. 2^20 */
+    int64_t T, N;                  /* tokens (all sequences packed), sequences (>= 1): each at most 2^31 - 4096 */
+    int32_t D;                     /* channels, 1 .. 2^20; (T / 16 + N) (D / 32 + 1) is below 2^31 */
     kda_dtype_t dtype;             /* dtype of x, z, input_gate and h */
     int32_t gate_kind, input_scale;
     float g_min;                   /* < 0; KDA_SCAN_LOWER_BOUND only */

@@ -13,11 +13,14 @@ namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 30;
 
-// Tokens and channels of a packed call.  Grids of (64 tokens x 32 channels) and the like stay below 2^31.
+// Tokens of a call: positions some tiles behind the last one still fit in 32 bits.
+constexpr int64_t kMaxTokens = INT32_MAX - 4095;
+
+// Tokens and channels of a packed call.  Grids of (16 tokens x 32 channels) and the like stay below 2^31.
 kda_status_t check_sizes(int64_t T, int64_t N, int32_t D, kda_dtype_t dtype) {
     if (T < 0 || N < 0 || D < 1) return KDA_ERR_INVALID_ARG;
     if (!dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED_DTYPE;
-    if (T > INT32_MAX || N > INT32_MAX || D > (1 << 20)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (T > kMaxTokens || N > kMaxTokens || D > (1 << 20)) return KDA_ERR_UNSUPPORTED_SHAPE;
     if ((T / 16 + N) * (int64_t)(D / 32 + 1) > INT32_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
     return KDA_OK;
 }

@@ -82,6 +82,53 @@ def test_lengths(dtype, lens):
     _check_bwd(d, _bwd(d, r[2]))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("long", (0, 3000))
+@pytest.mark.parametrize("N", (350, 700))
+def test_many_sequences(dtype, N, long):
+    """Tiles of 32 and of 64 channels, whole chains and (beside one long sequence) tiles that join others; the same bits from
+    rows at odd elements."""
+    lens = np.random.default_rng(N + long).integers(0, 520 if not long else 8, N).tolist()
+    lens[N // 3] = long or lens[N // 3]
+    d = U.scan_batch(lens, 36, dtype, N, gate="softplus" if long else "sigmoid", input_scale="norm")
+    r = _fwd(d)
+    g = _bwd(d, r[2])
+    _check_fwd(d, r)
+    _check_bwd(d, g)
+    x = U.to(d)
+    wide = torch.zeros((sum(lens), 3 * 36 + 1), dtype=U.DT[dtype], device="cuda")
+    v = [wide[:, 1 + 36 * k:37 + 36 * k] for k in range(3)]
+    for a, b in zip(v, ("x", "z", "input_gate")):
+        a.copy_(x[b])
+    keep = torch.full_like(r[2], float("nan"))
+    h, last = kda.scan_fwd(*v, initial_state=x["initial_state"], output_final_state=True, checkpoints=keep, **_how(x))
+    g2 = kda.scan_bwd(*v, x["grad_h"], keep, grad_final_state=x["grad_final_state"], **_how(x))
+    _no_error()
+    assert torch.equal(h, r[0]) and torch.equal(last, r[1]) and all(torch.equal(g2[k], g[k]) for k in g)
+
+
+def test_tokens_behind_32_bits():
+    """More than 2^31 elements: the last sequences against the oracle, the gradients of theirs too."""
+    D, T = 8192, 264000
+    d = U.scan_batch([130, 3, 70], D, "bf16", 17, gate="sigmoid", input_scale="norm")
+    x, m = U.to(d), sum(d["lens"])
+    big = {k: torch.zeros((T, D), dtype=torch.bfloat16, device="cuda") for k in ("x", "z", "input_gate", "grad_h")}
+    for k in big:
+        big[k][-m:] = x[k]
+    lens = [T - m] + d["lens"]
+    how = {**_how(x), "cu_seqlens": U.cu(lens).cuda()}
+    state, tail = (torch.cat((torch.zeros((1, D), device="cuda"), x[k])) for k in ("initial_state", "grad_final_state"))
+    keep = torch.empty((T // 64 + 4, D), device="cuda")
+    h, last = kda.scan_fwd(big["x"], big["z"], big["input_gate"], initial_state=state, output_final_state=True, checkpoints=keep, **how)
+    g = kda.scan_bwd(big["x"], big["z"], big["input_gate"], big["grad_h"], keep, grad_final_state=tail, **how)
+    _no_error()
+    want, size, n = U.scan_ref(d), U.scan_ref(d, True), U.scan_roundings(d)
+    U.close("h", h[-m:], want[0], size[0], n, U.HALF["bf16"])
+    U.close("final_state", last[1:], want[1], size[1], n, U.U32)
+    assert (h[:-m:1000] == 0).all() and (g["x"][:-m:1000] == 0).all()
+    _check_bwd(d, {k: v[-m:] if k in ("x", "z", "input_gate") else v[1:] if k == "initial_state" else v for k, v in g.items()})
+
+
 def test_equal_lengths_without_cu_seqlens():
     d = U.scan_batch([50] * 6, 24, "f32", 2)
     r = _fwd(d)
@@ -343,6 +390,17 @@ def test_step_padded_and_bad_rows(dtype):
     _step(d, p, torch.full((40,), -1, dtype=torch.int32))
     _no_error()
     assert torch.equal(p.cpu(), pool)
+
+
+def test_step_of_more_sequences_than_a_grid_is_high():
+    N = 70000
+    d, pool, idx = _step_batch(N, 5, "bf16", 12, N + 3)
+    p = pool.cuda()
+    h = _step(d, p, idx)
+    _no_error()
+    want, size, n = U.scan_ref(d), U.scan_ref(d, True), U.scan_roundings(d)
+    U.close("h", h, want[0], size[0], n, U.HALF["bf16"])
+    U.close("state", p[idx.long().cuda()], want[1], size[1], n, U.U32)
 
 
 def test_step_slots_behind_32_bits():

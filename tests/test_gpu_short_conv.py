@@ -243,6 +243,21 @@ def test_a_sequence_does_not_depend_on_its_neighbours():
     assert torch.equal(y2[T0:], y1) and torch.equal(t2[1:], t1)
 
 
+def test_gradients_behind_32_bits():
+    D, T0, lens = 8192, 264000, [100, 2, 70]
+    d = U.conv_batch(lens, D, 4, "bf16", 14, norm=128)
+    x, m = U.to(d), sum(lens)
+    big = {k: torch.zeros((T0 + m, D), dtype=torch.bfloat16, device="cuda") for k in ("x", "grad_y")}
+    for k in big:
+        big[k][T0:] = x[k]
+    hist, tail = (torch.cat((torch.zeros_like(x[k][:1]), x[k])) for k in ("initial_state", "grad_final_state"))
+    g = kda.short_conv_bwd(big["x"], x["weight"], x["bias"], big["grad_y"], activation="silu", norm_dim=128, cu_seqlens=U.cu([T0] + lens).cuda(),
+                           initial_state=hist, grad_final_state=tail)
+    _no_error()
+    assert (g["x"][:T0:1000] == 0).all()
+    _check_bwd(d, {"x": g["x"][T0:], "weight": g["weight"], "bias": g["bias"], "initial_state": g["initial_state"][1:]})
+
+
 # ---------------------------------------------------------------- single tokens
 def _step(d, pool, idx, **kw):
     x = U.to(d)

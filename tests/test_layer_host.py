@@ -184,6 +184,12 @@ def test_valid_calls_stop_at_the_device_check(lib, no_gpu, a):
     assert _call(lib, a) == 9
 
 
+@pytest.mark.parametrize("make", [_scan, _scan_bwd, _conv, _conv_bwd])
+def test_tokens_whose_tiles_end_behind_32_bits_are_refused(lib, make):
+    for kw in (dict(T=(1 << 31) - 4095, N=1), dict(T=1 << 33, N=1), dict(T=64, N=1 << 31), dict(T=(1 << 31) - 4096, N=1, D=1 << 14)):
+        assert _call(lib, make(**kw)) == 2, kw
+
+
 def test_empty_calls(lib):
     assert _call(lib, _scan_step(N=0)) == 0
     assert _call(lib, _conv_step(N=0)) == 0
