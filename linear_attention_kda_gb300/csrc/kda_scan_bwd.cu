@@ -41,8 +41,8 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
     if (out.rows)
         for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < B.slots * 2 * A.D; i += (int64_t)gridDim.x * NT) out.rows[i] = 0.f;
     make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
-    const bool chains = __ldcg(B.mode) != 0, loader = w == NW - 1;
-    course<L> way(B, A.cu_seqlens, A.T, A.N, blocks, true, true);
+    const bool chains = planned_chains(B), loader = w == NW - 1;
+    course<L, true> way(B, A.cu_seqlens, A.T, A.N, blocks, PLANNED, true);
     // the first token of a tile
     auto begin = [](const tile &t) { return t.a + (t.count > 0 ? t.count - 1 - t.p : 0) * L; };
     auto ask = [&](int turn) {

@@ -14,10 +14,11 @@ template <typename T, int W> struct fwd_memory {
     tile_memory<W> M;
 };
 
-// TMA: rows are 16-byte aligned.  Else a thread reads its elements when it needs them.
-template <typename T, int W, bool TMA>
+// TMA: rows are 16-byte aligned.  Else a thread reads its elements when it needs them.  PLAN: make_plan() says what the tiles are (a
+// kernel of its own for the others: one for all was 2 to 8 % slower where tiles join).
+template <typename T, int W, bool TMA, bool PLAN>
 __global__ void __launch_bounds__(NT, 2)
-scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<3> maps, int joined,
+scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<3> maps, layout how,
                 int blocks, int *err) {
     using X = fwd_shape<T, W>;
     constexpr int L = X::L, R = X::R;
@@ -26,9 +27,9 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, pair = lane % X::LPR * 2, row0 = w * X::RW + lane / X::LPR * R;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
-    if (joined) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
-    const bool chains = joined && __ldcg(B.mode) != 0, loader = w == NW - 1;
-    course<L> way(B, A.cu_seqlens, A.T, A.N, blocks, joined, false);
+    if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
+    const bool links = PLAN && !planned_chains(B), loader = w == NW - 1;
+    course<L, PLAN> way(B, A.cu_seqlens, A.T, A.N, blocks, how, false);
     // the next tile of the course, its boxes asked for
     auto ask = [&](int stage) {
         way.next();
@@ -111,7 +112,7 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
             *reinterpret_cast<float2 *>(&S.M.d[w][pair]) = decay_of(sum).d;
             *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = h;
         }
-        join<X, false>(B, joined && !chains, t, A.D, A.initial_state, A.final_state,
+        join<X, false>(B, links, t, A.D, A.initial_state, A.final_state,
                        A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr,
                        (t.b - t.a - t.p * L + CK - 1) / CK, S.M, *reinterpret_cast<entries<W> *>(&S.next.x[stage]), err, [](int, int) {});
         if (loader) ask(stage);  // every warp is done with this stage
@@ -127,13 +128,13 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
             out += A.D;
         }
     }
-    if (!joined) check_all(A.cu_seqlens, A.T, A.N, err);
+    if (!PLAN) check_all(A.cu_seqlens, A.T, A.N, err);
 }
 
 template <typename T, int W, bool TMA>
 static cudaError_t launch(const kda_scan_args *a, void *ws, cudaStream_t stream, int *err) {
     using X = fwd_shape<T, W>;
-    static std::atomic<int> running[64];
+    static std::atomic<int> running[2][64];
     constexpr size_t smem = sizeof(fwd_memory<T, W>);
     row_maps<3> maps{};
     if (TMA && (!make_row_map<X>(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype) ||
@@ -142,14 +143,18 @@ static cudaError_t launch(const kda_scan_args *a, void *ws, cudaStream_t stream,
         return cudaErrorUnknown;
     int blocks = (a->D + W - 1) / W, grid = 0;
     board B{};
-    int joined = a->T > X::L;  // else no sequence has a second tile
-    if (joined) board_layout(a->T, a->N, a->D, X::L, ws, &B);
-    const cudaError_t e = running_blocks(scan_fwd_kernel<T, W, TMA>, smem, running, lin::chunk_slots(a->T, a->N, X::L) * blocks, &grid);
-    if (e != cudaSuccess) return e;
+    layout how = SINGLE;
     kda_scan_args args = *a;
-    void *p[] = {&args, &B, &maps, &joined, &blocks, &err};
-    if (!joined) return cudaLaunchKernel((const void *)scan_fwd_kernel<T, W, TMA>, dim3(grid), dim3(NT), p, smem, stream);
-    return cudaLaunchCooperativeKernel((const void *)scan_fwd_kernel<T, W, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+    void *p[] = {&args, &B, &maps, &how, &blocks, &err};
+    cudaError_t e = running_blocks(scan_fwd_kernel<T, W, TMA, false>, smem, running[0], lin::chunk_slots(a->T, a->N, X::L) * blocks, &grid);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (a->T / a->N + X::L - 1) / X::L;  // of a sequence, where they are alike
+    if (a->T > X::L) how = (!a->cu_seqlens || a->N == 1) && rather_whole(tiles, tiles * a->N, blocks, grid) ? EQUAL : PLANNED;
+    if (how != PLANNED) return cudaLaunchKernel((const void *)scan_fwd_kernel<T, W, TMA, false>, dim3(grid), dim3(NT), p, smem, stream);
+    e = running_blocks(scan_fwd_kernel<T, W, TMA, true>, smem, running[1], lin::chunk_slots(a->T, a->N, X::L) * blocks, &grid);
+    if (e != cudaSuccess) return e;
+    board_layout(a->T, a->N, a->D, X::L, ws, &B);
+    return cudaLaunchCooperativeKernel((const void *)scan_fwd_kernel<T, W, TMA, true>, dim3(grid), dim3(NT), p, smem, stream);
 }
 
 template <typename T> static cudaError_t choose(const kda_scan_args *a, void *ws, cudaStream_t stream, int *err) {

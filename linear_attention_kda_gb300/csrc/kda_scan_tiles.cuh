@@ -77,9 +77,18 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
     return at;
 }
 
+// What a call's tiles are.  SINGLE: no sequence has a second one.  EQUAL: whole chains of sequences of one length, as the host can tell
+// where there are no cu_seqlens or there is one sequence (one of 4096 tokens and channels 51.5 us, 61.2 with a plan).  PLANNED: make_plan() says.
+enum layout : int { SINGLE, EQUAL, PLANNED };
+__device__ __forceinline__ bool planned_chains(const board &B) { return __ldcg(B.mode) != 0; }
+// whether chains, the longest of which has `longest` tiles of `total` in 1 / blocks of the channels, are taken whole by g blocks
+__host__ __device__ __forceinline__ bool rather_whole(int64_t longest, int64_t total, int64_t blocks, int64_t g) {
+    return longest * g * 5 <= total * blocks * 7;
+}
+
 // Clears the entries, looks at all of cu_seqlens, lists the tiles and the chains and chooses between the two ways: whole chains where
-// the longest one is no more than 1.4 times a block's share of all tiles (a tile of a chain takes 4.7 us, one that joins others 6.5: bf16,
-// forwards, two blocks to an SM), and where any part of cu_seqlens is bad (the slots may not be
+// the longest one is no more than 1.4 times a block's share of all tiles (a tile of a chain takes less than one that joins others; where both were tried,
+// 16384 tokens of one sequence 184 us by chains and 214, 4 sequences of 512 to 8192 197 and 254), and where any part of cu_seqlens is bad (the slots may not be
 // those that the sequences think, so that no tile may wait for another).
 // Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 2 us more.)
 static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int *err) {
@@ -155,7 +164,7 @@ static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu,
         if (sorted && N > 1)  // places behind the last tile
             for (int64_t i = (int64_t)total + threadIdx.x; i < B.slots; i += NT) B.plan[i] = make_int4(0, -1, 0, 0);
         if (threadIdx.x == 0) {
-            B.mode[0] = bad || longest * gridDim.x * 5 <= total * blocks * 7;
+            B.mode[0] = bad || rather_whole(longest, total, blocks, gridDim.x);
             B.mode[1] = 0;
             if (bad) set_error(err, KDA_ERR_BAD_SEQLENS);
         }
@@ -337,17 +346,27 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
     __syncthreads();
 }
 
+// An entry of the plan (of the chains) of a call that has none.
+static __device__ __noinline__ int4 unplanned(const int32_t *cu, int64_t T, int64_t N, int L, layout how, int64_t i) {
+    int64_t n = i, p = 0;
+    lin::span s;
+    const bool good = how == EQUAL ? lin::seq_span(cu, T, N, i, &s) : lin::find_slot(cu, T, N, L, i, &n, &p, &s);
+    if (!good || (p > 0 && p >= (s.b - s.a + L - 1) / L)) return make_int4(0, -1, 0, 0);
+    return make_int4((int)n, (int)p, (int)s.a, (int)s.b);
+}
+
 // The tiles that a block goes through, as one warp of it finds them.
-template <int L> struct course {
+template <int L, bool PLAN> struct course {
     const board &B;
     const int32_t *cu;
     int64_t T, N, item;
     int blocks, back;
-    bool joined, chains;
+    layout how;
+    bool chains;
     tile t;  // p = -1 behind the last
-    __device__ __forceinline__ course(const board &b, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, bool joined_, bool back_)
-        : B(b), cu(cu_), T(T_), N(N_), item(-1), blocks(blocks_), back(back_), joined(joined_) {
-        chains = joined && __ldcg(B.mode) != 0;
+    __device__ __forceinline__ course(const board &b, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, layout how_, bool back_)
+        : B(b), cu(cu_), T(T_), N(N_), item(-1), blocks(blocks_), back(back_), how(how_) {
+        chains = PLAN ? planned_chains(B) : how == EQUAL;
         t = tile{0, -1, 0, 0, 0, 0, 0};
     }
     __device__ __forceinline__ void next() {
@@ -357,7 +376,7 @@ template <int L> struct course {
         }
         const int64_t items = (chains ? N : lin::chunk_slots(T, N, L)) * blocks;
         do {
-            if (chains) {
+            if (PLAN && chains) {
                 int ticket = 0;
                 if ((threadIdx.x & 31) == 0) ticket = atomicAdd(B.mode + 1, 1);
                 item = __shfl_sync(0xffffffffu, ticket, 0);
@@ -368,17 +387,8 @@ template <int L> struct course {
             if (item >= items) return;
             const int64_t r = back && !chains ? items - 1 - item : item, i = r / blocks;
             t.block = (int)(r - i * blocks);
-            if (joined) {
-                const int4 q = __ldcg((chains ? B.order : B.plan) + i);
-                t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
-            } else {
-                int64_t n = 0, p = 0;
-                lin::span s;
-                if (lin::find_slot(cu, T, N, L, i, &n, &p, &s)) {
-                    if (p == 0 || p < (s.b - s.a + L - 1) / L) t.p = (int)p;
-                    t.n = (int)n, t.a = (int)s.a, t.b = (int)s.b;
-                }
-            }
+            const int4 q = PLAN ? __ldcg((chains ? B.order : B.plan) + i) : unplanned(cu, T, N, L, how, i);
+            t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
         } while (t.p < 0);
         t.count = (t.b - t.a + L - 1) / L;
         t.first = t.a / L + t.n;
@@ -386,7 +396,7 @@ template <int L> struct course {
     }
 };
 
-// Sets the error of a call whose tiles do not wait for one another (the plan kernel does it for the others).
+// Sets the error of a call that has no plan (make_plan() does it for the others).
 __device__ __forceinline__ void check_all(const int32_t *cu, int64_t T, int64_t N, int *err) {
     if (blockIdx.x > 0) return;
     for (int64_t n = threadIdx.x; n < N; n += NT) {
@@ -437,7 +447,7 @@ __device__ __forceinline__ channel<float2> load_channel(const float *A_log, cons
 
 // Channels of a tile.  64 cost least: each row of a tile is two sectors or more, a warp has no groups to join, and its reads of shared
 // memory no bank conflicts.  Fewer make more chains, so that more blocks have whole ones, of which the last ends sooner, and
-// tiles of more tokens, of which fewer join where they have to.  At 64 / 32 / 16 channels, bf16 (f32), D = 4096, us: forwards 16384 tokens of one
+// tiles of more tokens, of which fewer join where they have to.  At 64 / 32 / 16 channels, all by the kernel with a plan, bf16 (f32), D = 4096, us: forwards 16384 tokens of one
 // sequence (64 chains of 64 channels) 203 / 201 / 184, 131072 of D = 256 (4) 127 / 127 / 125 (180 / 152 / 137), 4 sequences (256) 250 / 191 / 197,
 // 6 (384) 334 / 246 / 260 (405 / 287 / 297), 8 (512) 360 / 345 / 375, 12 (768) 451 / 459 / 508 (555 / 558 / 575), 32 (2048) 1040 / 1092 / 1234;
 // gradients 8192 of one 242 / 236 / 223, 3 sequences (192) 276 / 263 / 236, 6 (384) 461 / 382 / 400, 12 (768) 690 / 718 / 765.
