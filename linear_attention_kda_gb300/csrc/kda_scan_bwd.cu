@@ -27,10 +27,11 @@ struct sums_of {
     float *rows;  // [slots][2][D], or NULL
 };
 
-template <typename T, int W, bool TMA>
+// PLAN: as for scan_fwd_kernel; the rows of slots without a tile are zeros then
+template <typename T, int W, bool TMA, bool PLAN>
 __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1)
 scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_constant__ board B, const __grid_constant__ row_maps<4> maps,
-                const __grid_constant__ sums_of out, int blocks, int *err) {
+                const __grid_constant__ sums_of out, layout how, int blocks, int *err) {
     using X = bwd_shape<W>;
     constexpr int L = X::L, R = X::R;
     extern __shared__ __align__(128) char memory[];
@@ -38,11 +39,11 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, pair = lane % X::LPR * 2, row0 = w * X::RW + lane / X::LPR * R;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
-    if (out.rows)
+    if (PLAN && out.rows)
         for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < B.slots * 2 * A.D; i += (int64_t)gridDim.x * NT) out.rows[i] = 0.f;
-    make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
-    const bool chains = planned_chains(B), loader = w == NW - 1;
-    course<L, true> way(B, A.cu_seqlens, A.T, A.N, blocks, PLANNED, true);
+    if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
+    const bool links = PLAN && !planned_chains(B), loader = w == NW - 1;
+    course<L, PLAN> way(B, A.cu_seqlens, A.T, A.N, blocks, how, true);
     // the first token of a tile
     auto begin = [](const tile &t) { return t.a + (t.count > 0 ? t.count - 1 - t.p : 0) * L; };
     auto ask = [&](int turn) {
@@ -161,7 +162,7 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
             *reinterpret_cast<float2 *>(&S.M.d[w][pair]) = decay_of(sum).d;
             *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = m;
         }
-        join<X, true>(B, !chains, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, err, [&](int role, int ch) {
+        join<X, true>(B, links, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, err, [&](int role, int ch) {
             if (role == 2) {
                 float v = checkpoint;
 #pragma unroll
@@ -258,10 +259,24 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
     }
     __syncthreads();
     if (w / WARPS == 3 && mine < W) add_up(mine);
+    if (!PLAN) check_all(A.cu_seqlens, A.T, A.N, err);
 }
 
+// The rows of a call without a plan: those of slots without a tile were not written, nor was any of one sequence that is bad.
+struct alike {
+    const int32_t *cu;
+    int64_t T, N;
+    int L;  // 0: a call with a plan
+    __device__ __forceinline__ bool has(int64_t slot) const {
+        if (L == 0) return true;
+        const int64_t each = T / N, n = ((slot + 1) * L - 1) / (each + L);  // the last sequence whose first slot, n each / L + n, is not behind
+        lin::span s;
+        return n < N && lin::seq_span(cu, T, N, n, &s) && slot - (s.a / L + n) < (each + L - 1) / L;
+    }
+};
+
 // Column sums of the tiles' rows: 32 columns to a block, its eight warps every eighth row.
-__global__ void __launch_bounds__(256) scan_sums_kernel(const float *rows, int64_t slots, int D, float *dA, float *db) {
+__global__ void __launch_bounds__(256) scan_sums_kernel(const float *rows, int64_t slots, const __grid_constant__ alike some, int D, float *dA, float *db) {
     __shared__ float part[8][32];
     float *to = blockIdx.y == 0 ? dA : db;
     if (!to) return;
@@ -272,8 +287,10 @@ __global__ void __launch_bounds__(256) scan_sums_kernel(const float *rows, int64
         int64_t r = w;
         for (; r + 24 < slots; r += 32)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += p[(r + 8 * i) * 2 * D];
-        for (; r < slots; r += 8) v[0] += p[r * 2 * D];
+            for (int i = 0; i < 4; ++i)
+                if (some.has(r + 8 * i)) v[i] += p[(r + 8 * i) * 2 * D];
+        for (; r < slots; r += 8)
+            if (some.has(r)) v[0] += p[r * 2 * D];
     }
     part[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
     __syncthreads();
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(256) scan_sums_kernel(const float *rows, int64
 template <typename T, int W, bool TMA>
 static cudaError_t launch(const kda_scan_bwd_args *a, void *ws, cudaStream_t stream, int *err) {
     using X = bwd_shape<W>;
-    static std::atomic<int> running[64];
+    static std::atomic<int> running[2][64];
     constexpr size_t smem = sizeof(bwd_memory<T, W>);
     row_maps<4> maps{};
     if (TMA && (!make_row_map<X>(&maps.m[0], a->z, a->T, a->D, a->z_stride, a->dtype) ||
@@ -300,13 +317,23 @@ static cudaError_t launch(const kda_scan_bwd_args *a, void *ws, cudaStream_t str
     board B{};
     const size_t rows = board_layout(a->T, a->N, a->D, X::L, ws, &B);
     sums_of out{a->grad_A_log || a->grad_dt_bias ? (float *)((char *)ws + rows) : nullptr};
-    cudaError_t e = running_blocks(scan_bwd_kernel<T, W, TMA>, smem, running, B.slots * blocks, &grid);
-    if (e != cudaSuccess) return e;
+    layout how = PLANNED;
     kda_scan_bwd_args args = *a;
-    void *p[] = {&args, &B, &maps, &out, &blocks, &err};
-    e = cudaLaunchCooperativeKernel((const void *)scan_bwd_kernel<T, W, TMA>, dim3(grid), dim3(NT), p, smem, stream);
+    void *p[] = {&args, &B, &maps, &out, &how, &blocks, &err};
+    cudaError_t e = running_blocks(scan_bwd_kernel<T, W, TMA, false>, smem, running[0], B.slots * blocks, &grid);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (a->T / a->N + X::L - 1) / X::L;  // of a sequence, where they are alike
+    if ((!a->cu_seqlens || a->N == 1) && rather_whole(tiles, tiles * a->N, blocks, grid)) {
+        how = EQUAL;
+        e = cudaLaunchKernel((const void *)scan_bwd_kernel<T, W, TMA, false>, dim3(grid), dim3(NT), p, smem, stream);
+    } else {
+        e = running_blocks(scan_bwd_kernel<T, W, TMA, true>, smem, running[1], B.slots * blocks, &grid);
+        if (e != cudaSuccess) return e;
+        e = cudaLaunchCooperativeKernel((const void *)scan_bwd_kernel<T, W, TMA, true>, dim3(grid), dim3(NT), p, smem, stream);
+    }
     if (e != cudaSuccess || !out.rows) return e;
-    scan_sums_kernel<<<dim3((a->D + 31) / 32, 2), 256, 0, stream>>>(out.rows, B.slots, a->D, a->grad_A_log, a->grad_dt_bias);
+    const alike some{a->cu_seqlens, a->T, a->N, how == EQUAL ? X::L : 0};
+    scan_sums_kernel<<<dim3((a->D + 31) / 32, 2), 256, 0, stream>>>(out.rows, B.slots, some, a->D, a->grad_A_log, a->grad_dt_bias);
     return cudaGetLastError();
 }
 

@@ -201,6 +201,18 @@ __device__ __forceinline__ void get_batch(const unsigned long long *p, int64_t p
         if (tries > 16) __nanosleep(50);
     }
 }
+// The state behind a supergroup
+__device__ __forceinline__ float get_state(const unsigned long long *p, int *err) {
+    unsigned long long e = get(p);
+    for (int tries = 0; (uint32_t)(e >> 32) == ~0u; ++tries, e = get(p)) {
+        if (tries > 1 << 20) {
+            set_error(err, KDA_ERR_DEVICE_TIMEOUT);
+            break;
+        }
+        __nanosleep(50);
+    }
+    return __uint_as_float((uint32_t)e);
+}
 __device__ __forceinline__ float entry_d(unsigned long long e) { return __uint_as_float((uint32_t)e); }
 __device__ __forceinline__ float entry_b(unsigned long long e) { return __uint_as_float((uint32_t)(e >> 32)); }
 // the decay of one run and then another
@@ -223,7 +235,7 @@ template <int W> struct tile_memory {
     float g[NW][W], d[NW][W], b[NW][W];  // the warps' sums of log-decays, decays and values; after join() g is the state that enters each warp's tokens
     float from[W];                       // the state behind the last tile, where a block takes whole chains
 };
-// entries on their way through a block: those of the supergroup, of the groups and of the tiles before a tile
+// entries on their way through a block: those of the groups (at 1) and of the tiles (at G) before a tile
 template <int W> using entries = unsigned long long[1 + 2 * (G - 1)][W];
 
 // Over the groups of a warp, in the direction of the scan: sum and value become those up to and with each group's, before_* those up to it.
@@ -276,15 +288,6 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
         else if (!links) h = M.from[ch];
     }
     if (links) {
-        unsigned long long e[BATCH];
-        auto fetch = [&](const unsigned long long *p, int from, int n, int to) {  // entries [from, n), up to BATCH
-            n = n - from < BATCH ? n - from : BATCH;
-            if (n <= 0 || c >= D) return;
-            get_batch(p + (int64_t)from * D + c, D, n, e, err);
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i)
-                if (i < n) E[to + from + i][ch] = e[i];
-        };
         const unsigned long long *tiles = B.entry[0] + (slot - q) * D,
                                  *groups = B.entry[1] + ((int64_t)t.first / G + t.n + super * G) * D;
         if (role == 0) {
@@ -302,15 +305,20 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
                 }
                 if (c < D) put(B.entry[0] + slot * D + c, sum, v);
             }
-        } else if (role == 1) {
-            if (super > 0) fetch(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super - 1) * D, 0, 1, 0);
-            fetch(groups, 0, gq, 1);
-        } else if (role == 2) {
-            fetch(tiles, 0, q, G);
-        } else if (role == 3) {
-            fetch(tiles, BATCH, q, G);
-            fetch(groups, BATCH, gq, 1);
         }
+        // A role's entries: the first groups (1), tiles (2) and more tiles (3), and, when its own is on its way, more groups (0).  One
+        // piece of code for all of them: instructions that do not fit beside the rest of a tile's are fetched anew for each tile.
+        {
+            const int from = role == 0 || role == 3 ? BATCH : 0, all = role > 1 ? q : gq, n = all - from < BATCH ? all - from : BATCH;
+            if (role < 4 && n > 0 && c < D) {
+                unsigned long long e[BATCH];
+                get_batch((role > 1 ? tiles : groups) + (int64_t)from * D + c, D, n, e, err);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    if (i < n) E[(role > 1 ? G : 1) + from + i][ch] = e[i];
+            }
+        }
+        if (role == 0 && super > 0 && c < D) h = get_state(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super - 1) * D + c, err);
         __syncthreads();
     }
     if (role == 0) {
@@ -325,7 +333,6 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
                 }
                 put(B.entry[1] + ((int64_t)t.first / G + t.n + t.p / G) * D + c, compose(gd, sum), step_or_erase(sum, gb, v));
             }
-            if (super > 0) h = entry_d(E[0][ch]);
             for (int i = 0; i < gq; ++i) h = step_or_erase(entry_d(E[1 + i][ch]), h, entry_b(E[1 + i][ch]));
             for (int i = 0; i < q; ++i) h = step_or_erase(entry_d(E[G + i][ch]), h, entry_b(E[G + i][ch]));
         }

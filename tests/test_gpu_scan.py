@@ -107,6 +107,15 @@ def test_many_sequences(dtype, N, long):
     assert torch.equal(h, r[0]) and torch.equal(last, r[1]) and all(torch.equal(g2[k], g[k]) for k in g)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_long_sequence(dtype):
+    """More tiles than share the first two levels of what joins them."""
+    d = U.scan_batch([140000, 5], 6, dtype, 18, gate="sigmoid")
+    r = _fwd(d)
+    _check_fwd(d, r)
+    _check_bwd(d, _bwd(d, r[2]))
+
+
 def test_tokens_behind_32_bits():
     """More than 2^31 elements: the last sequences against the oracle, the gradients of theirs too."""
     D, T = 8192, 264000
