@@ -269,6 +269,64 @@ def test_a_sequence_does_not_depend_on_its_neighbours():
     assert torch.equal(h2[T0:], h1) and torch.equal(last2[1:], last1) and (h2[:T0:1000] == 0).all() and (last2[0] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,length", [(5, 320), (7, 127), (2, 512), (3, 1), (1, 1024), (400, 70)])
+def test_the_same_bits_with_and_without_cu_seqlens(dtype, N, length):
+    """Sequences of one length: their tiles are known before the call."""
+    d = U.scan_batch([length] * N, 40, dtype, N, input_scale="norm")
+    r = _fwd(d)
+    g = _bwd(d, r[2])
+    _check_fwd(d, r)
+    _check_bwd(d, g)
+    x = U.to(d)
+    how = {**_how(x), "cu_seqlens": None, "n_seq": N}
+    keep = torch.full_like(r[2], float("nan"))
+    h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, checkpoints=keep, **how)
+    g2 = kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, grad_final_state=x["grad_final_state"], **how)
+    _no_error()
+    assert torch.equal(h, r[0]) and torch.equal(last, r[1]) and torch.equal(keep.nan_to_num(7.0), r[2].nan_to_num(7.0))
+    assert all(torch.equal(g2[k], g[k]) for k in g)
+
+
+@pytest.mark.parametrize("T", (30, 700))
+def test_bad_cu_seqlens_of_one_sequence(T):
+    d = U.scan_batch([T], 24, "f32", 19)
+    r = _fwd(d)
+    for bad in ([0, T - 1], [1, T], [0, T + 1], [T, 0]):
+        d["cu_seqlens"] = torch.tensor(bad, dtype=torch.int32)
+        out, state = torch.full_like(r[0], 3.0), torch.full_like(r[1], 4.0)
+        h, last, keep = _fwd(d, out=out, final_state=state)
+        torch.cuda.synchronize()
+        assert kda.get_device_error() == 7, bad
+        assert h is out and (h == 3).all() and (state == 4).all() and keep.isnan().all()
+        g = _bwd(d, r[2])
+        torch.cuda.synchronize()
+        assert kda.get_device_error() == 7, bad
+        assert (g["A_log"] == 0).all() and (g["dt_bias"] == 0).all()
+
+
+def test_two_calls_at_once():
+    """Two streams, each with tensors and a workspace of its own; tiles that wait for one another."""
+    ds = [U.scan_batch([4000, 100], 24, "bf16", 20), U.scan_batch([100, 6000, 3], 40, "bf16", 21, gate="sigmoid", input_scale="norm")]
+    want = [_fwd(d) for d in ds]
+    want = [(f, _bwd(d, f[2])) for d, f in zip(ds, want)]
+    _no_error()
+    streams, xs, got = [torch.cuda.Stream() for _ in ds], [U.to(d) for d in ds], [[] for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, x, d, f, o in zip(streams, xs, ds, [w[0] for w in want], got):
+            with torch.cuda.stream(s):
+                keep = torch.zeros_like(f[2])
+                h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True,
+                                       checkpoints=keep, **_how(x))
+                g = kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, grad_final_state=x["grad_final_state"], **_how(x))
+                o.append((h, last, g))
+    _no_error()
+    for o, (f, g) in zip(got, want):
+        for h, last, g2 in o:
+            assert torch.equal(h, f[0]) and torch.equal(last, f[1]) and all(torch.equal(g2[k], g[k]) for k in g)
+
+
 def test_bad_cu_seqlens():
     d = U.scan_batch([64, 100, 36], 40, "bf16", 9)
     x = U.to(d)
