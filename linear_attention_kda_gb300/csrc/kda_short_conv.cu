@@ -2,8 +2,8 @@
 // tokens with the last K - 1 of them in registers; the sums of a head's squares meet by shuffles between the lanes that
 // hold it.  Rows come by TMA, up to 24 tokens ahead.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each
 // run) and y written once, and close to that by instructions: 21 an element with the norm.  bf16, 32 sequences of 512 to 8192
-// tokens, 4096 channels, four taps: 330 us, 6.5 TB/s; with the norm over heads of 128 427 us, 5.1 TB/s (two tokens' sums at once; 479
-// one at a time).  V = 8 was no faster where 4 will do.
+// tokens, 4096 channels, four taps: 330 us, 6.5 TB/s; with the norm over heads of 128 410 us, 5.3 TB/s (four tokens' sums at once; 427 two
+// and 479 one at a time).  V = 8 was no faster where 4 will do.
 //
 // kda_short_conv_step: the same for one token, whose history is a slot of a pool.
 #include <atomic>
@@ -40,7 +40,7 @@ template <int V> __device__ __forceinline__ void scale(float2 (&y)[V / 2], float
 template <typename T, int K, int V, bool WIDE>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps maps, const T *x,
                                                        const T *hist, T *tail, T *y, int L, int blocks, int64_t items, int *err) {
-    constexpr int U = some_rows<T, V>;
+    constexpr int U = some_rows<T, V>, J = V == 4 ? 4 : 2;  // (four at V = 8 454 us for 440, registers)
     extern __shared__ __align__(128) char memory[];
     check_all(S, err);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -78,11 +78,11 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ s
             const int left = r.last - r.first - turn * U;
             if (WIDE && !tc::mbar_wait(&Q.full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
 #pragma unroll
-            for (int u0 = 0; u0 < U; u0 += 2) {  // two tokens, whose sums go over the lanes together
-                float2 v[2][V / 2];
-                float ss[2];
+            for (int u0 = 0; u0 < U; u0 += J) {  // J tokens, whose sums go over the lanes together
+                float2 v[J][V / 2];
+                float ss[J];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < J; ++j) {
                     const int u = u0 + j;
                     if constexpr (WIDE) {
                         layer::unpack<T, V>(layer::load<T, V>(&Q.x[stage][0][u][lane * V]), row[K - 1 + u]);
@@ -93,12 +93,12 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ s
                     ss[j] = one<K, V>(S, P, &row[u], v[j]);
                 }
                 if (S.norm) {
-                    head_sums<V>(ss[0], ss[1], S.norm);
-                    scale<V>(v[0], ss[0], S.eps);
-                    scale<V>(v[1], ss[1], S.eps);
+                    head_sums<V>(ss, S.norm);
+#pragma unroll
+                    for (int j = 0; j < J; ++j) scale<V>(v[j], ss[j], S.eps);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < J; ++j) {
                     if (u0 + j < left) store<T, V, WIDE>(out, layer::pack<T, V>(v[j]), have);
                     out += S.D;
                 }

@@ -97,6 +97,23 @@ template <int V> __device__ __forceinline__ void head_sums(float &a, float &b, i
     b = upper ? v : w;
 }
 
+// Four sums: a quarter of the lanes takes each of them after two steps (heads over eight lanes or more; ten shuffles for 24)
+template <int V> __device__ __forceinline__ void head_sums(float (&a)[4], int norm) {
+    const int lane = threadIdx.x & 31, half = norm / V / 2, quarter = half / 2;
+    const bool upper = (lane & half) != 0, second = (lane & quarter) != 0;
+    float v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[j] = (upper ? a[2 + j] : a[j]) + __shfl_xor_sync(0xffffffffu, upper ? a[j] : a[2 + j], half);
+    float s = (second ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, second ? v[0] : v[1], quarter);
+#pragma unroll
+    for (int off = 1; off < 8; off *= 2)
+        if (off < quarter) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const int base = lane & ~(2 * half - 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = __shfl_sync(0xffffffffu, s, base + j * quarter);
+}
+template <int V> __device__ __forceinline__ void head_sums(float (&a)[2], int norm) { head_sums<V>(a[0], a[1], norm); }
+
 // Where rows of a sequence come from: its history and then its tokens
 template <typename T, int V, bool WIDE> struct rows {
     const T *x, *hist;  // the sequence's first token and history (NULL: zeros), at this lane's channels

@@ -509,7 +509,7 @@ def _off(t, shape, dtype, device) -> bool:
 
 def _run(where: str, device: int, fn, packed: bytes, *more):
     """Calls fn(args, *more, stream) with `device` current, on its current stream."""
-    if torch.cuda.current_device() != device:
+    if torch._C._cuda_getDevice() != device:  # torch.cuda.current_device without its check that CUDA has begun (a tensor of it is there)
         with torch.cuda.device(device):
             code = fn(packed, *more, _raw_stream(device))
     else:
