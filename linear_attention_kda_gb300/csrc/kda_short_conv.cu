@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ s
     const int c0 = (int)(item % blocks) * 32 * V, c = c0 + lane * V, have = S.D - c;
     const rows<T, V, WIDE> X{x + r.a * S.stride + c, hist ? hist + r.n * (K - 1) * S.D + c : nullptr, S.stride, S.D, K, have};
     if (r.first < r.last) {
-        ring<T, V, 1> &Q = reinterpret_cast<ring<T, V, 1> *>(memory)[w];
+        ring<T, V, 1, some_rows<T, V>> &Q = reinterpret_cast<ring<T, V, 1, some_rows<T, V>> *>(memory)[w];
         const int turns = (r.last - r.first + U - 1) / U;
         auto ask = [&](int turn) {
             if (!WIDE || lane != 0 || turn >= turns) return;
@@ -153,7 +153,7 @@ static cudaError_t fwd(const kda_short_conv_args *a, cudaStream_t stream, int *e
     const int64_t items = lin::chunk_slots(a->T, a->N, L) * blocks;
     row_maps maps{};
     if (WIDE && !layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>)) return cudaErrorUnknown;
-    constexpr int smem = WIDE ? 4 * (int)sizeof(ring<T, V, 1>) : 0;
+    constexpr int smem = WIDE ? 4 * (int)sizeof(ring<T, V, 1, some_rows<T, V>>) : 0;
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = lin::allow_smem(conv_fwd_kernel<T, K, V, WIDE>, smem, done);

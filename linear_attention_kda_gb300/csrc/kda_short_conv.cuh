@@ -142,12 +142,12 @@ __device__ __forceinline__ bool find_run(const spec &S, int64_t slot, int L, run
     return true;
 }
 
-// A warp's next rows, 2 KB of them at a time and up to NS times as many, on their way by TMA: the registers that as many loads
+// A warp's next rows, 2 KB of them (or half as many) at a time and up to NS times as many, on their way by TMA: the registers that as many loads
 // would take are those of four more warps.
 template <typename T, int V> constexpr int some_rows = 2048 / (32 * V * (int)sizeof(T));
 constexpr int NS = 3;
-template <typename T, int V, int NI> struct alignas(128) ring {
-    T x[NS][NI][some_rows<T, V>][32 * V];
+template <typename T, int V, int NI, int ROWS> struct alignas(128) ring {
+    T x[NS][NI][ROWS][32 * V];
     uint64_t full[NS];
 };
 struct row_maps {

@@ -3,9 +3,9 @@
 //     ds = (dy - y sum(dy y)) / |s|  (or dy),      dp_t = ds dSwish(p)  (or ds),
 // whose last K - 1 are in registers too: dx_{t-K+1} = sum_j weight_j dp_{t-j} is then complete, for K - 1 tokens behind
 // the run as well, whose dp is formed a second time by the next one.  weight and bias gather their sums over tokens in
-// registers; the eight warps of a block, which have eight runs of the same channels, add theirs up in shared memory, and
+// registers; the four warps of a block, which have four runs of the same channels, add theirs up in shared memory, and
 // a second kernel adds up the blocks' rows, all in a fixed order.  Bound by instructions: 46 an element with the norm
-// over heads of 128, for 6 bytes in bf16.  65536 tokens of 4096 channels 584 us, 2.8 TB/s (without the norm 388 us), 4096 tokens 55 us.  Two tokens' sums at once
+// over heads of 128, for 6 bytes in bf16.  65536 tokens of 4096 channels 556 us, 2.9 TB/s (without the norm 370 us), 4096 tokens 55 us.  Two tokens' sums at once
 // and a second copy of the loop without questions about a run's ends cost more registers or instructions fetched than they saved.
 #include <atomic>
 
@@ -14,15 +14,19 @@
 namespace kda {
 namespace conv {
 
-constexpr int NW = 8;
+// Four warps, four blocks to an SM: 65536 tokens 560 us, 584 with eight and two
+constexpr int NW = 4;
+// Rows at a time, which is how far the loop over tokens is unrolled: bf16 by fours (8 sequences of 300 to 5000 tokens 215 us, 234 by eights; fp32 gained
+// nothing by twos, heads of 256 lost)
+template <typename T, int V> constexpr int bwd_rows = sizeof(T) == 2 && V == 4 ? some_rows<T, V> / 2 : some_rows<T, V>;
 
 template <typename T, int K, int V, bool WIDE>
-__global__ void __launch_bounds__(32 * NW, V == 4 ? 2 : 1)
+__global__ void __launch_bounds__(32 * NW, V == 4 ? 4 : 2)
 conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps maps, const T *x, const T *hist, const T *dy, const T *dtail, T *dx, T *dhist, float *sums, int L,
                 int64_t slots, int *err) {
-    constexpr int U = some_rows<T, V>;
+    constexpr int U = bwd_rows<T, V>;
     extern __shared__ __align__(128) char memory[];
-    float (*part)[32 * V] = reinterpret_cast<float(*)[32 * V]>(memory + (WIDE ? NW * sizeof(ring<T, V, 2>) : 0));
+    float (*part)[32 * V] = reinterpret_cast<float(*)[32 * V]>(memory + (WIDE ? NW * sizeof(ring<T, V, 2, bwd_rows<T, V>>) : 0));
     check_all(S, err);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t slot = (int64_t)blockIdx.x * NW + w;
@@ -40,7 +44,7 @@ conv_bwd_kernel(const __grid_constant__ spec S, const __grid_constant__ row_maps
         const taps<V, K> P(S, c, have);
         // tokens behind the run's end that its gradients need; those behind the sequence have dp = 0
         const int stop = r.last + K - 1, turns = (stop - r.first + U - 1) / U;
-        ring<T, V, 2> &Q = reinterpret_cast<ring<T, V, 2> *>(memory)[w];
+        ring<T, V, 2, bwd_rows<T, V>> &Q = reinterpret_cast<ring<T, V, 2, bwd_rows<T, V>> *>(memory)[w];
         auto ask = [&](int turn) {
             if (!WIDE || lane != 0 || turn >= turns) return;
             const int stage = turn % NS, tok = (int)r.a + r.first + turn * U;
@@ -198,17 +202,17 @@ __global__ void __launch_bounds__(256) conv_sums_kernel(const float *sums, int64
 }
 
 // (4096 tokens of 4096 channels by runs of 16, 32, 64 and 128: 73.7, 67.6, 57.3 and 92.2 us; kda_short_conv_fwd 30.7, 30.7, 28.7 and 36.9)
-static int run_length(int64_t T, int64_t N, int D) { return run_length(T, N, (D + 127) / 128, NW, 2 * 152); }
+static int run_length(int64_t T, int64_t N, int D) { return run_length(T, N, (D + 127) / 128, NW, 4 * 152); }
 
 template <typename T, int K, int V, bool WIDE>
 static cudaError_t launch(const kda_short_conv_bwd_args *a, float *sums, cudaStream_t stream, int *err) {
     const int L = run_length(a->T, a->N, a->D);
     const int64_t slots = lin::chunk_slots(a->T, a->N, L), rows = (slots + NW - 1) / NW;
     row_maps maps{};
-    if (WIDE && (!layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>) ||
-                 !layer::make_row_map(&maps.dy, a->grad_y, a->T, a->D, a->D, a->dtype, 32 * V, some_rows<T, V>)))
+    if (WIDE && (!layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, bwd_rows<T, V>) ||
+                 !layer::make_row_map(&maps.dy, a->grad_y, a->T, a->D, a->D, a->dtype, 32 * V, bwd_rows<T, V>)))
         return cudaErrorUnknown;
-    constexpr int smem = (WIDE ? NW * (int)sizeof(ring<T, V, 2>) : 0) + NW * 32 * V * 4;
+    constexpr int smem = (WIDE ? NW * (int)sizeof(ring<T, V, 2, bwd_rows<T, V>>) : 0) + NW * 32 * V * 4;
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = lin::allow_smem(conv_bwd_kernel<T, K, V, WIDE>, smem, done);
