@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 template <typename T, int K, int V, bool WIDE>
 static cudaError_t fwd(const kda_short_conv_args *a, cudaStream_t stream, int *err) {
     const int blocks = (a->D + 32 * V - 1) / (32 * V);
-    const int L = run_length(a->T, a->N, (blocks + 3) / 4, 1, 6 * 152);
+    // (five blocks an SM: 96 registers, in bf16 with the norm)
+    const int L = run_length(a->T, a->N, (blocks + 3) / 4, 1, 5 * 152);
     const int64_t items = lin::chunk_slots(a->T, a->N, L) * blocks;
     row_maps maps{};
     if (WIDE && !layer::make_row_map(&maps.x, a->x, a->T, a->D, a->x_stride, a->dtype, 32 * V, some_rows<T, V>)) return cudaErrorUnknown;

@@ -16,7 +16,7 @@ namespace conv {
 
 // Four warps, four blocks to an SM: 65536 tokens 560 us, 584 with eight and two
 constexpr int NW = 4;
-// Rows at a time, which is how far the loop over tokens is unrolled: bf16 by fours (8 sequences of 300 to 5000 tokens 215 us, 234 by eights; fp32 gained
+// Rows at a time, which is how far the loop over tokens is unrolled: bf16 by fours (8 sequences of 300 to 5000 tokens, runs of 64: 215 us, 234 by eights; fp32 gained
 // nothing by twos, heads of 256 lost)
 template <typename T, int V> constexpr int bwd_rows = sizeof(T) == 2 && V == 4 ? some_rows<T, V> / 2 : some_rows<T, V>;
 
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(256) conv_sums_kernel(const float *sums, int64
     }
 }
 
-// (4096 tokens of 4096 channels by runs of 16, 32, 64 and 128: 73.7, 67.6, 57.3 and 92.2 us; kda_short_conv_fwd 30.7, 30.7, 28.7 and 36.9)
+// (4096 channels by runs of 32, 48, 64, 96 and 128: 4096 tokens 58, 73, 55, 66 and 76 us, 65536 tokens 687,
+// 627, -, 568 and 557)
 static int run_length(int64_t T, int64_t N, int D) { return run_length(T, N, (D + 127) / 128, NW, 4 * 152); }
 
 template <typename T, int K, int V, bool WIDE>
