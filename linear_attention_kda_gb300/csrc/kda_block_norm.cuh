@@ -14,41 +14,40 @@ template <int NT> struct place {
     static constexpr int ROWS = BLOCK / NT;
 };
 
-// N sums over the NT threads of a row.  `at` alternates between two places of shared memory, so that one barrier
-// separates a sum's parts from the sum after the next.
+// N (one or two) sums over the NT threads of a row.  `at` alternates between two places of shared memory (16-byte aligned), so that one barrier
+// separates a sum's parts from the sum after the next.  Two sums go over the lanes as one, each half of a warp with its own.
 template <int NT, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float *shared, int &at) {
+    static_assert(N <= 2 && (NT == 32 || NT % 128 == 0), "shapes");
+    constexpr int H = 32 / N;  // lanes to a sum
+    const int lane = threadIdx.x & 31;
+    float x = v[0];
+    if constexpr (N == 2) x = (lane & 16 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, lane & 16 ? v[0] : v[1], 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int off = H / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if constexpr (NT == 32) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-    if constexpr (NT > 32) {
+        for (int i = 0; i < N; ++i) v[i] = N == 1 ? x : __shfl_sync(0xffffffffu, x, i * H);
+    } else {
         constexpr int W = NT / 32;
         float *s = shared + at * (2 * W);
         at ^= 1;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int i = 0; i < N; ++i) s[i * W + (threadIdx.x >> 5)] = v[i];
+        if (lane % H == 0) s[lane / H * W + (threadIdx.x >> 5)] = x;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             v[i] = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) v[i] += s[i * W + w];
+            for (int w = 0; w < W; w += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(s + i * W + w);
+                v[i] += (f.x + f.y) + (f.z + f.w);
+            }
         }
     }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-template <int V> __device__ __forceinline__ void load_weight(const float *w, int c, float *f) {
-    if (!w) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = 1.f;
-        return;
-    }
-    layer::unpack<float, V>(layer::load<float, V>(w + c), f);
-}
+__device__ __forceinline__ float total(float v) { return v; }
+__device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
 
 // Calls go(T, RT, V, E, NT as a tag) for a call's types and sizes: 16-byte vectors of dtype where every row's address allows
 // them, the fewest threads that hold a row at 8 (D up to 2048) or 16 elements each.

@@ -29,9 +29,6 @@ template <typename T, typename RT> __host__ __device__ __forceinline__ int row_b
     return rt + (A.grad_residual_out ? rt : 0) + (A.y ? t : 0) + (A.gate_kind == KDA_NORM_GATE_CHANNEL ? t : 0) + (A.grad_normed ? t : 0);
 }
 
-__device__ __forceinline__ float total(float v) { return v; }
-__device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
-
 template <typename K, bool BULK> __device__ __forceinline__ const void *at_row(const void *p, int64_t base, const char *near) {
     if constexpr (BULK) return near;
     return (const K *)p + base;
@@ -47,7 +44,7 @@ __global__ void __launch_bounds__(place<NT>::BLOCK, NT <= 256 ? 512 / place<NT>:
 block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *sums, int stages, int room, int *err) {
     using F = typename layer::lanes<V>::F;
     constexpr int P = layer::lanes<V>::N;  // values of a vector, one or two at a time
-    __shared__ float parts[2 * 2 * (NT > 32 ? NT / 32 : 1)];
+    __shared__ __align__(16) float parts[2 * 2 * (NT > 32 ? NT / 32 : 1)];
     __shared__ uint64_t full[2];
     extern __shared__ __align__(128) char memory[];
     const int tid = threadIdx.x % NT;
