@@ -38,10 +38,10 @@ template <typename K, int V, typename F, int P> __device__ __forceinline__ void 
 }
 
 // BULK: rows come by bulk copies into one or two places (`stages`) of shared memory in turn, and are read from there when they are needed.
-// Behind them, where there is room (`room`), lie scale * post_weight and pre_weight.
-template <typename T, typename RT, int V, int E, int NT, bool BULK>
+// Behind them, where there is room (ROOM), lie scale * post_weight and pre_weight.
+template <typename T, typename RT, int V, int E, int NT, bool BULK, bool ROOM>
 __global__ void __launch_bounds__(place<NT>::BLOCK, NT <= 256 ? 512 / place<NT>::BLOCK : 1)
-block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *sums, int stages, int room, int *err) {
+block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *sums, int stages, int *err) {
     using F = typename layer::lanes<V>::F;
     constexpr int P = layer::lanes<V>::N;  // values of a vector, one or two at a time
     __shared__ __align__(16) float parts[2 * 2 * (NT > 32 ? NT / 32 : 1)];
@@ -73,7 +73,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
             tc::mbar_init(&full[1], 1);
             tc::fence_proxy_async();
         }
-        if (room)
+        if (ROOM)
             for (int c = threadIdx.x; c < A.D; c += NT) {
                 near[c] = (A.scale_vec ? A.scale_vec[c] : A.scale) * (A.post_weight ? A.post_weight[c] : 1.f);
                 near[A.D + c] = A.pre_weight ? A.pre_weight[c] : 1.f;
@@ -97,8 +97,8 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
             for (int i = 0; i < P; ++i) f[i] = splat<F>(none);
     };
     auto scaled = [&](int c, F (&f)[P]) {  // scale * post_weight
-        if (BULK && room) {
-            from(near, c, f, 0.f);
+        if constexpr (ROOM) {
+            layer::unpack<float, V>(layer::load<float, V>(near + c), f);
         } else {
             F w[P];
             from(A.scale_vec, c, f, A.scale);
@@ -107,7 +107,10 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
             for (int i = 0; i < P; ++i) f[i] = mul(f[i], w[i]);
         }
     };
-    auto normal = [&](int c, F (&f)[P]) { from(BULK && room ? near + A.D : A.pre_weight, c, f, 1.f); };
+    auto normal = [&](int c, F (&f)[P]) {
+        if constexpr (ROOM) layer::unpack<float, V>(layer::load<float, V>(near + A.D + c), f);
+        else from(A.pre_weight, c, f, 1.f);
+    };
     const float inv = 1.f / A.D;
     for (int64_t row = first; row < A.T; row += each) {
         const int64_t base = row * A.D;
@@ -263,10 +266,10 @@ __global__ void __launch_bounds__(256) block_norm_sums_kernel(const float *sums,
 struct share {
     int smem, stages, room, per_sm;  // of a block
 };
-template <typename K, bool BULK>
+template <typename K, bool BULK, bool ROOM>
 static cudaError_t launch(const kda_block_norm_bwd_args *a, float *sums, const share &S, cudaStream_t stream, int *rows, int *err) {
     using P = place<K::nt>;
-    auto *kernel = block_norm_bwd_kernel<typename K::t, typename K::rt, K::v, K::e, K::nt, BULK>;
+    auto *kernel = block_norm_bwd_kernel<typename K::t, typename K::rt, K::v, K::e, K::nt, BULK, ROOM>;
     if (S.smem > 46 * 1024) {  // (with what the kernel declares, above 48 KB)
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = lin::allow_smem(kernel, 226 * 1024 + 512, done);
@@ -275,7 +278,7 @@ static cudaError_t launch(const kda_block_norm_bwd_args *a, float *sums, const s
     int64_t blocks = (a->T + P::ROWS - 1) / P::ROWS;
     if (blocks > 152 * S.per_sm) blocks = 152 * S.per_sm;
     *rows = (int)blocks * P::ROWS;
-    kernel<<<(unsigned)blocks, P::BLOCK, S.smem, stream>>>(*a, sums, S.stages, S.room, err);
+    kernel<<<(unsigned)blocks, P::BLOCK, S.smem, stream>>>(*a, sums, S.stages, err);
     return cudaGetLastError();
 }
 
@@ -314,10 +317,12 @@ kda_status_t kda_launch_block_norm_bwd(const kda_block_norm_bwd_args *a, void *w
             using K = decltype(t);
             float *sums = want ? (float *)ws : nullptr;
             const int per_sm = K::nt <= 256 ? 512 / place<K::nt>::BLOCK : 1;
-            if constexpr (K::nt >= 128 && K::v > 1)
-                e = launch<K, true>(a, sums, share_of(row_bytes<typename K::t, typename K::rt>(*a), 8 * a->D, per_sm), stream, &rows, err);
-            else
-                e = launch<K, false>(a, sums, {0, 0, 0, per_sm}, stream, &rows, err);
+            if constexpr (K::nt >= 128 && K::v > 1) {
+                const share S = share_of(row_bytes<typename K::t, typename K::rt>(*a), 8 * a->D, per_sm);
+                e = S.room ? launch<K, true, true>(a, sums, S, stream, &rows, err) : launch<K, true, false>(a, sums, S, stream, &rows, err);
+            } else {
+                e = launch<K, false, false>(a, sums, {0, 0, 0, per_sm}, stream, &rows, err);
+            }
         });
     }
     if (e == cudaSuccess && want) {
