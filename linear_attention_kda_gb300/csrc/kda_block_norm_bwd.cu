@@ -6,7 +6,7 @@
 //
 // Bound by HBM traffic: y, gate, r, dr' and dn read once, dr, dy and dgate written once (16 bytes per channel in bf16).  A
 // row stays in registers between its three sums, all arithmetic is on two channels at a time (64 instructions a channel, which take about
-// as long as the memory; one at a time and with gates formed twice 98).  16384 rows of 4096 in bf16: 215 us, 5.0 TB/s (588 at first).  A block takes every G-th row, the next one on its way to
+// as long as the memory; one at a time and with gates formed twice 98).  16384 rows of 4096 in bf16: 184 us, 5.8 TB/s (588 at first).  A block takes every G-th row, the next one on its way to
 // shared memory meanwhile, and keeps the tokens' sums of its columns in registers; the blocks' sums meet in a second kernel in a
 // fixed order.
 #include <atomic>
@@ -38,8 +38,8 @@ template <typename K, int V, typename F, int P> __device__ __forceinline__ void 
 }
 
 // BULK: rows come by bulk copies into one or two places (`stages`) of shared memory in turn, and are read from there when they are needed.
-// Behind them, where there is room (ROOM), lie scale * post_weight and pre_weight.
-template <typename T, typename RT, int V, int E, int NT, bool BULK, bool ROOM>
+// Behind them lie scale * post_weight and pre_weight.  FULL: the call has every part.
+template <typename T, typename RT, int V, int E, int NT, bool BULK, bool FULL>
 __global__ void __launch_bounds__(place<NT>::BLOCK, NT <= 256 ? 512 / place<NT>::BLOCK : 1)
 block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *sums, int stages, int *err) {
     using F = typename layer::lanes<V>::F;
@@ -49,10 +49,11 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
     extern __shared__ __align__(128) char memory[];
     const int tid = threadIdx.x % NT;
     const int64_t first = (int64_t)blockIdx.x * place<NT>::ROWS + threadIdx.x / NT, each = (int64_t)gridDim.x * place<NT>::ROWS;
-    const bool block = A.y != nullptr, channel = A.gate_kind == KDA_NORM_GATE_CHANNEL, pre = A.grad_normed != nullptr;
+    const bool block = FULL || A.y != nullptr, channel = FULL || A.gate_kind == KDA_NORM_GATE_CHANNEL, pre = FULL || A.grad_normed != nullptr,
+               post = FULL || A.post_norm, behind = FULL || A.grad_residual_out != nullptr, token = !FULL && A.gate_kind == KDA_NORM_GATE_TOKEN;
     const int stage_bytes = BULK ? row_bytes<T, RT>(A) : 0, rt = A.D * (int)sizeof(RT), tt = A.D * (int)sizeof(T);
     // where the parts of a row begin in its place
-    const int at_d = rt, at_y = at_d + (A.grad_residual_out ? rt : 0), at_g = at_y + (block ? tt : 0), at_n = at_g + (channel ? tt : 0);
+    const int at_d = rt, at_y = at_d + (behind ? rt : 0), at_g = at_y + (block ? tt : 0), at_n = at_g + (channel ? tt : 0);
     auto ask = [&](int64_t row, int stage) {
         if (!BULK || threadIdx.x != 0 || row >= A.T) return;
         char *to = memory + stage * stage_bytes;
@@ -73,11 +74,10 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
             tc::mbar_init(&full[1], 1);
             tc::fence_proxy_async();
         }
-        if (ROOM)
-            for (int c = threadIdx.x; c < A.D; c += NT) {
-                near[c] = (A.scale_vec ? A.scale_vec[c] : A.scale) * (A.post_weight ? A.post_weight[c] : 1.f);
-                near[A.D + c] = A.pre_weight ? A.pre_weight[c] : 1.f;
-            }
+        for (int c = threadIdx.x; c < A.D; c += NT) {
+            near[c] = (A.scale_vec ? A.scale_vec[c] : A.scale) * (A.post_weight ? A.post_weight[c] : 1.f);
+            near[A.D + c] = A.pre_weight ? A.pre_weight[c] : 1.f;
+        }
         __syncthreads();
         ask(first, 0);
         if (stages == 2) ask(first + each, 1);
@@ -97,7 +97,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
             for (int i = 0; i < P; ++i) f[i] = splat<F>(none);
     };
     auto scaled = [&](int c, F (&f)[P]) {  // scale * post_weight
-        if constexpr (ROOM) {
+        if constexpr (BULK) {
             layer::unpack<float, V>(layer::load<float, V>(near + c), f);
         } else {
             F w[P];
@@ -108,7 +108,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
         }
     };
     auto normal = [&](int c, F (&f)[P]) {
-        if constexpr (ROOM) layer::unpack<float, V>(layer::load<float, V>(near + A.D + c), f);
+        if constexpr (BULK) layer::unpack<float, V>(layer::load<float, V>(near + A.D + c), f);
         else from(A.pre_weight, c, f, 1.f);
     };
     const float inv = 1.f / A.D;
@@ -117,7 +117,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
         const char *here = memory + stage * stage_bytes;
         if (BULK && !tc::mbar_wait(&full[stage], phase)) set_error(err, KDA_ERR_DEVICE_TIMEOUT);
         F r[E][P], d[E][P], y[E][P], s[E][P];
-        const float kt = A.gate_kind == KDA_NORM_GATE_TOKEN ? layer::sigmoid(ld((const T *)A.gate + row)) : 1.f;
+        const float kt = token ? layer::sigmoid(ld((const T *)A.gate + row)) : 1.f;
         float ky = 1.f;
         if (block) {
             F q = splat<F>(0.f);
@@ -128,7 +128,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
 #pragma unroll
                 for (int i = 0; i < P; ++i) q = fma(y[e][i], y[e][i], q);
             }
-            if (A.post_norm) {
+            if (post) {
                 float ss[1] = {total(q)};
                 row_sum<NT>(ss, parts, at);
                 ky = rsqrtf(ss[0] * inv + A.eps);
@@ -180,7 +180,7 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
         for (int e = 0; e < E; ++e) {
             const int c = column(e);
             if (c >= A.D) continue;
-            if (A.grad_residual_out) row_part<RT, V>(at_row<RT, BULK>(A.grad_residual_out, base, here + at_d), c, d[e]);
+            if (behind) row_part<RT, V>(at_row<RT, BULK>(A.grad_residual_out, base, here + at_d), c, d[e]);
             else
 #pragma unroll
                 for (int i = 0; i < P; ++i) d[e][i] = splat<F>(0.f);
@@ -216,9 +216,9 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
         }
         if (!block) continue;
         float ss[2] = {total(sy), total(sg)};
-        if (A.post_norm || A.gate_kind == KDA_NORM_GATE_TOKEN) row_sum<NT>(ss, parts, at);
-        if (A.gate_kind == KDA_NORM_GATE_TOKEN && tid == 0) st((T *)A.grad_gate + row, ss[1] * kt * (1.f - kt));
-        m = A.post_norm ? -ss[0] * inv : 0.f;
+        if (post || token) row_sum<NT>(ss, parts, at);
+        if (token && tid == 0) st((T *)A.grad_gate + row, ss[1] * kt * (1.f - kt));
+        m = post ? -ss[0] * inv : 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int c = column(e);
@@ -264,12 +264,12 @@ __global__ void __launch_bounds__(256) block_norm_sums_kernel(const float *sums,
 }
 
 struct share {
-    int smem, stages, room, per_sm;  // of a block
+    int smem, stages, per_sm;  // of a block
 };
-template <typename K, bool BULK, bool ROOM>
+template <typename K, bool BULK, bool FULL>
 static cudaError_t launch(const kda_block_norm_bwd_args *a, float *sums, const share &S, cudaStream_t stream, int *rows, int *err) {
     using P = place<K::nt>;
-    auto *kernel = block_norm_bwd_kernel<typename K::t, typename K::rt, K::v, K::e, K::nt, BULK, ROOM>;
+    auto *kernel = block_norm_bwd_kernel<typename K::t, typename K::rt, K::v, K::e, K::nt, BULK, FULL>;
     if (S.smem > 46 * 1024) {  // (with what the kernel declares, above 48 KB)
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = lin::allow_smem(kernel, 226 * 1024 + 512, done);
@@ -282,15 +282,15 @@ static cudaError_t launch(const kda_block_norm_bwd_args *a, float *sums, const s
     return cudaGetLastError();
 }
 
-// Two rows on their way where as many blocks as registers allow (512 threads) still fit into an SM, else where one does, else
-// one row.  An SM has 228 KB, of which a block takes 1 KB and some bytes beside its rows.
+// The weights and two rows on their way where as many blocks as registers allow (512 threads) still fit into an SM, else the weights and one
+// row, else one block with two or one.  The largest row and its weights, fp32 of 8192, take 224 KB.  (bf16, 16384 rows of 4096 with an fp32
+// residual: one row 247 us, two without the weights 338, one block with two rows and weights 274.  fp32 of 5120: one row 462 us, two
+// without the weights 647.)  An SM has 228 KB, of which a block takes 1 KB and some bytes beside its rows.
 static share share_of(int row, int weights, int per_sm) {
-    for (int n : {per_sm, 1}) {
-        const int most = 228 * 1024 / n - 1024 - 512;
-        if (2 * row + weights <= most) return {2 * row + weights, 2, 1, n};
-        if (2 * row <= most) return {2 * row, 2, 0, n};
-    }
-    return {row, 1, 0, 1};
+    for (int n : {per_sm, 1})
+        for (int stages : {2, 1})
+            if (stages * row + weights <= 228 * 1024 / n - 1024 - 512) return {stages * row + weights, stages, n};
+    return {0, 0, 0};
 }
 
 }  // namespace norm
@@ -313,15 +313,20 @@ kda_status_t kda_launch_block_norm_bwd(const kda_block_norm_bwd_args *a, void *w
         const bool wide = all_wide(a->D, a->dtype, {a->residual, a->y, a->gate_kind == KDA_NORM_GATE_CHANNEL ? a->gate : nullptr, a->scale_vec,
                                                     a->post_weight, a->pre_weight, a->grad_residual_out, a->grad_normed, a->grad_y,
                                                     a->gate_kind == KDA_NORM_GATE_CHANNEL ? a->grad_gate : nullptr, a->grad_residual});
+        // a block, its norm and gate, and what comes behind them: the kernel that need not ask (16384 rows of 4096 185 us, 196;
+        // fp32 346 for 336, so bf16 alone)
+        const bool full = a->y && a->gate_kind == KDA_NORM_GATE_CHANNEL && a->post_norm && a->grad_normed && a->grad_residual_out;
         choose(a->dtype, a->residual_dtype, a->D, wide, [&](auto t) {
             using K = decltype(t);
             float *sums = want ? (float *)ws : nullptr;
             const int per_sm = K::nt <= 256 ? 512 / place<K::nt>::BLOCK : 1;
             if constexpr (K::nt >= 128 && K::v > 1) {
                 const share S = share_of(row_bytes<typename K::t, typename K::rt>(*a), 8 * a->D, per_sm);
-                e = S.room ? launch<K, true, true>(a, sums, S, stream, &rows, err) : launch<K, true, false>(a, sums, S, stream, &rows, err);
+                if (S.smem == 0) e = cudaErrorInvalidConfiguration;
+                else if (sizeof(typename K::t) == 2 && full) e = launch<K, true, sizeof(typename K::t) == 2>(a, sums, S, stream, &rows, err);
+                else e = launch<K, true, false>(a, sums, S, stream, &rows, err);
             } else {
-                e = launch<K, false, false>(a, sums, {0, 0, 0, per_sm}, stream, &rows, err);
+                e = launch<K, false, false>(a, sums, {0, 0, per_sm}, stream, &rows, err);
             }
         });
     }
