@@ -22,6 +22,7 @@
 #include "kda_linear.cuh"
 #include "kda_row_map.h"
 #include "kda_scan.cuh"
+#include "kda_scan_course.h"
 #include "tc_util.cuh"
 
 namespace kda {
@@ -224,13 +225,6 @@ __device__ __forceinline__ float compose(float d1, float d2) {
     return factor(d1) * factor(d2);
 }
 
-struct tile {
-    int n, p, count;   // sequence, position in the direction of the scan (-1: no tile), tiles of the sequence
-    int a, b;          // the sequence's tokens
-    int block;         // of channels
-    int first;         // slot of the sequence's first tile
-};
-
 template <int W> struct tile_memory {
     float g[NW][W], d[NW][W], b[NW][W];  // the warps' sums of log-decays, decays and values; after join() g is the state that enters each warp's tokens
     float from[W];                       // the state behind the last tile, where a block takes whole chains
@@ -367,22 +361,18 @@ template <int L, bool PLAN> struct course {
     const board &B;
     const int32_t *cu;
     int64_t T, N, item;
-    int blocks, back;
+    int blocks;
     layout how;
-    bool chains;
+    bool back, chains;
     tile t;  // p = -1 behind the last
     __device__ __forceinline__ course(const board &b, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, layout how_, bool back_)
-        : B(b), cu(cu_), T(T_), N(N_), item(-1), blocks(blocks_), back(back_), how(how_) {
+        : B(b), cu(cu_), T(T_), N(N_), item(-1), blocks(blocks_), how(how_), back(back_) {
         chains = PLAN ? planned_chains(B) : how == EQUAL;
         t = tile{0, -1, 0, 0, 0, 0, 0};
     }
     __device__ __forceinline__ void next() {
-        if (chains && t.p + 1 < t.count) {
-            ++t.p;
-            return;
-        }
         const int64_t items = (chains ? N : lin::chunk_slots(T, N, L)) * blocks;
-        do {
+        next_tile<L>(t, chains, back, [&](tile *to) {
             if (PLAN && chains) {
                 int ticket = 0;
                 if ((threadIdx.x & 31) == 0) ticket = atomicAdd(B.mode + 1, 1);
@@ -390,16 +380,13 @@ template <int L, bool PLAN> struct course {
             } else {
                 item = item < 0 ? blockIdx.x : item + gridDim.x;
             }
-            t.p = -1;
-            if (item >= items) return;
+            if (item >= items) return false;
             const int64_t r = back && !chains ? items - 1 - item : item, i = r / blocks;
-            t.block = (int)(r - i * blocks);
+            to->block = (int)(r - i * blocks);
             const int4 q = PLAN ? __ldcg((chains ? B.order : B.plan) + i) : unplanned(cu, T, N, L, how, i);
-            t.n = q.x, t.p = q.y, t.a = q.z, t.b = q.w;
-        } while (t.p < 0);
-        t.count = (t.b - t.a + L - 1) / L;
-        t.first = t.a / L + t.n;
-        if (back && !chains && t.count > 0) t.p = t.count - 1 - t.p;  // positions count in the direction of the scan
+            to->n = q.x, to->p = q.y, to->a = q.z, to->b = q.w;
+            return true;
+        });
     }
 };
 
