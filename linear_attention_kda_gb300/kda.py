@@ -1067,7 +1067,8 @@ def _norm_inputs(where, y, residual, gate, post_weight, pre_weight, scale, post_
     if y is None and (gate is not None or post_weight is not None or not pre_norm or vec is not None):
         raise ValueError(f"{where}: without y there is a norm in front of the next block alone")
     shape, rt, dev, f32 = residual.shape, residual.dtype, residual.get_device(), torch.float32
-    dt = y.dtype if y is not None else rt if tokens[1] is None else tokens[1].dtype
+    first = y if y is not None else residual if tokens[1] is None else tokens[1]  # whose dtype is that of y, gate and normed
+    dt, code, rcode = first.dtype, _dtype_code(first), _dtype_code(residual)
     kind = 0 if gate is None else 2 if gate.dim() == 1 else 1
     gs, par = shape if kind < 2 else shape[:1], shape[1:]
     if (dev < 0 or not residual.is_contiguous() or (y is not None and _off(y, shape, dt, dev)) or (gate is not None and _off(gate, gs, dt, dev))
@@ -1076,8 +1077,7 @@ def _norm_inputs(where, y, residual, gate, post_weight, pre_weight, scale, post_
             or (rows[1] is not None and _off(rows[1], shape, rt, dev))):
         _require(where, dev, (("residual", residual, shape, rt), ("y", y, shape, dt), ("gate", gate, gs, dt), ("post_weight", post_weight, par, f32),
                               ("pre_weight", pre_weight, par, f32), ("scale", vec, par, f32), tokens + (shape, dt), rows + (shape, rt)))
-    return (shape[0], shape[1], dt, dev, KDA_BF16 if dt is torch.bfloat16 else _dtype_code(residual if y is None else y), _dtype_code(residual),
-            kind, int(post_norm and y is not None), 1.0 if vec is not None else float(scale), vec)
+    return (shape[0], shape[1], dt, dev, code, rcode, kind, int(post_norm and y is not None), 1.0 if vec is not None else float(scale), vec)
 
 
 def block_norm_fwd(y, residual, gate=None, *, post_weight=None, pre_weight=None, scale=1.0, post_norm: bool = True, pre_norm: bool = True,

@@ -248,3 +248,23 @@ def test_binding_refuses_before_the_library():
     meta = lambda *s, **k: torch.empty(s, device="meta", **k)  # noqa: E731
     with pytest.raises(ValueError):
         kda.scan_fwd(meta(8, 64), meta(8, 64), cu_seqlens=meta(1, **i32))
+
+
+def test_norm_without_a_block_looks_at_the_type_of_what_it_writes(lib, no_gpu, monkeypatch):
+    """In front of the first block the type of normed (or of its gradient) says what the call computes in: types that there are, and
+    none that the residual stream may not stand beside."""
+    x, half = torch.zeros((8, 64)), torch.zeros((8, 64), dtype=torch.float16)
+    for call in (lambda: kda.block_norm_fwd(None, x, normed=half), lambda: kda.block_norm_bwd(None, x, None, None, half),
+                 lambda: kda.block_norm_fwd(None, half), lambda: kda.block_norm_fwd(None, x, normed=x.to(torch.int32))):
+        with pytest.raises(TypeError):
+            call()
+    monkeypatch.setattr(kda, "_require", lambda *a: None)  # (that the tensors are on the CPU; the library refuses or stops at its device check)
+    monkeypatch.setattr(kda, "_run", lambda where, device, fn, packed, *more: kda._check(fn(packed, *more, None), where))
+    for call in (lambda r, n: kda.block_norm_fwd(None, r, normed=n), lambda r, n: kda.block_norm_bwd(None, r, None, None, n)):
+        with pytest.raises(kda.KDAError) as e:
+            call(x.bfloat16(), x)
+        assert e.value.code == 3
+    for r, n in ((x, x), (x, x.bfloat16()), (x.bfloat16(), x.bfloat16())):
+        with pytest.raises(kda.KDAError) as e:
+            kda.block_norm_fwd(None, r, normed=n)
+        assert e.value.code == 9
