@@ -90,7 +90,8 @@ kda_status_t kda_check_finite_rows(const void *p, int64_t len, int64_t N, const 
     int *err = kda_device_error_ptr();
     if (!err) return KDA_ERR_CUDA;
     const int64_t per_row = len / (dtype == KDA_BF16 ? 8 : 4), want = (per_row + 255) / 256;
-    const dim3 grid((unsigned)(want < 32 ? want : 32), (unsigned)(N < 1024 ? N : 1024));
+    // (rows shorter than a vector have none of them, but a block)
+    const dim3 grid((unsigned)(want < 1 ? 1 : want < 32 ? want : 32), (unsigned)(N < 1024 ? N : 1024));
     if (dtype == KDA_BF16)
         kda::check_finite_rows_kernel<kda::bf16><<<grid, 256, 0, stream>>>((const kda::bf16 *)p, len, N, used, at, slots, err);
     else

@@ -501,6 +501,22 @@ def test_step_finite_checks():
         kda.set_debug_checks(0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [1, 3, 7])
+def test_step_finite_checks_of_short_rows(dtype, D):
+    d, pool, idx = _step_batch(3, D, dtype, 4, 5)
+    kda.set_debug_checks(kda.CHECK_FINITE)
+    try:
+        p = pool.cuda()
+        _step(d, p, idx)
+        assert kda.get_device_error() == 0
+        p[idx[2].long(), D - 1] = float("inf")
+        _step(d, p, idx)
+        assert kda.get_device_error() == 12
+    finally:
+        kda.set_debug_checks(0)
+
+
 @pytest.mark.parametrize("gate,input_scale", [("softplus", "norm"), ("lower_bound", "complement")])
 def test_steps_continue_a_prefill(gate, input_scale):
     """A prompt in two parts and then token by token, against one pass: fp32, each bound by the oracle."""

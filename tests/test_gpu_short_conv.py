@@ -323,3 +323,24 @@ def test_steps_continue_a_prefill(dtype):
     y, _ = U.conv_ref(d)
     U.close("y", torch.cat([y1, y2] + rest), y, U.conv_sizes(d), _roundings(d), U.HALF[dtype])
     U.close("y", whole, y, U.conv_sizes(d), _roundings(d), U.HALF[dtype])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D,K", [(1, 2), (2, 3), (7, 2), (33, 4)])
+def test_step_finite_checks(dtype, D, K):
+    """Of the rows and slots that the step wrote alone, rows shorter than a vector among them."""
+    d, pool, idx = _step_batch(6, D, K, dtype, 13, 9)
+    idx[2] = -1
+    rest = torch.ones(9, dtype=torch.bool)
+    rest[idx[idx >= 0].long()] = False
+    pool[rest] = float("nan")
+    kda.set_debug_checks(kda.CHECK_FINITE)
+    try:
+        p, out = pool.cuda(), torch.full((6, D), float("nan"), dtype=U.DT[dtype], device="cuda")
+        _step(d, p, idx, out=out)
+        assert kda.get_device_error() == 0
+        d["x"][5, D - 1] = float("inf")
+        _step(d, p, idx, out=out)
+        assert kda.get_device_error() == 12
+    finally:
+        kda.set_debug_checks(0)
