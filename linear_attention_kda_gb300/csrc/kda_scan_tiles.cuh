@@ -318,9 +318,10 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
     if (role == 0) {
         if (links && c < D) {
             if (q == G - 1 && more) {
-                float gd = 1.f, gb = 0.f;
+                // (from the first tile's, so that decays near 1 are joined as a - 1)
+                float gd = entry_d(E[G][ch]), gb = entry_b(E[G][ch]);
 #pragma unroll
-                for (int i = 0; i < G - 1; ++i) {
+                for (int i = 1; i < G - 1; ++i) {
                     const unsigned long long x = E[G + i][ch];
                     gb = step_or_erase(entry_d(x), gb, entry_b(x));
                     gd = compose(gd, entry_d(x));

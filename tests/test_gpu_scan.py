@@ -171,6 +171,21 @@ def test_slow_decays_do_not_drift():
     assert (last == last[0, 0]).all()
 
 
+def test_joined_tiles_keep_slow_decays():
+    """A state with nothing entering, over 4096 tiles of 256 tokens that join others, forwards and backwards: exp(T g) of it.  Behind every 256
+    tiles it goes through at most 16 groups', 15 tiles' and 8 warps' decays, a rounding each, and a decay's logarithm is a sum of roundings relative to
+    itself.  (Decays joined as 1 + d lose up to 1e-4 of the state here.)"""
+    T, rates = 1 << 20, [1e-10, 3e-10, 1e-9, 3e-9, 1e-8, 3e-8, 1e-7, 1e-6]
+    z = -torch.tensor(rates, device="cuda").expand(T, len(rates)).contiguous()
+    x, one, keep = torch.zeros_like(z), torch.ones((1, len(rates)), device="cuda"), kda.scan_checkpoints(T, 1, len(rates))
+    _, last = kda.scan_fwd(x, z, gate="log", initial_state=one, output_final_state=True, checkpoints=keep)
+    g = kda.scan_bwd(x, z, None, x, keep, gate="log", grad_final_state=one)
+    _no_error()
+    log = T * U.f64(z[0])
+    for got in (last[0], g["initial_state"][0]):
+        assert (abs(U.f64(got) / np.exp(log) - 1) <= (16 * 39 + 64 * abs(log)) * U.U32).all(), U.f64(got) / np.exp(log) - 1
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_erasing_decays(dtype):
     """exp(g) = 0 leaves nothing of the state, infinities and NaN included; -inf and -200 are such decays."""
