@@ -542,9 +542,9 @@ kda_status_t kda_rope(const kda_rope_args *args, struct CUstream_st *stream);
  *
  * Values: g is at most 0 in use; greater ones (KDA_SCAN_LOG) are computed as given and may overflow.  exp(g) counts as 0
  * below the normal range of fp32 (g below about -87.3), c of _NORM where 1 - a^2 is at most 1e-30.  A decay of 0 erases what the state
- * held before the call, infinities and NaN included; so does, for the states after them, a run of tokens whose whole decay is 0
- * in fp32.  A NaN or an infinity stays in its sequence and channel; one that a token of the call itself brings in may last to
- * the sequence's end whatever its decays.  Arithmetic and states are fp32; a decay near 1 is kept as a - 1, so that what a
+ * held, infinities and NaN included; so does, for the states after them, a run of tokens whose whole decay is 0
+ * in fp32.  Under other decays an infinity stays one.  A NaN or an infinity stays in its sequence and channel; a NaN that a token of the
+ * call itself brings in may last to the sequence's end whatever its decays. Arithmetic and states are fp32; a decay near 1 is kept as a - 1, so that what a
  * long memory holds does not drift with the rounding of a; h is rounded once to dtype.
  *
  * Shapes: x, z, input_gate and h [T, D], any D; tokens of x, z and input_gate are *_stride elements apart (0: D,

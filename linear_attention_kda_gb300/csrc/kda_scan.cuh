@@ -78,13 +78,19 @@ template <typename F> __device__ __forceinline__ F factor(F d) {
 template <typename F> __device__ __forceinline__ F below_one(F d) {
     return each([](float v) { return v < 0.f ? v : v - 1.f; }, d);
 }
-// a h + u for finite h
+// a h + u for finite h.  An infinity or a NaN leaves one of the two behind, whatever follows, so that a run of steps is looked at in its end
+// and, where it has to be, taken again by step_any().
 template <typename F> __device__ __forceinline__ F step(F d, F h, F u) {
     return fma(d, h, fma(each([](float v) { return v < 0.f ? 1.f : 0.f; }, d), h, u));
 }
-// the same where nothing is left of h if a is 0, an infinity or a NaN in h included
-template <typename F> __device__ __forceinline__ F step_or_erase(F d, F h, F u) {
-    return step(d, each([](float v, float w) { return v == 0.f ? 0.f : w; }, d, h), u);
+// a h + u for every h: nothing is left of it where a is 0, an infinity or a NaN included, and an infinity stays one under other decays (step()
+// would take it from itself)
+__device__ __forceinline__ float step_any(float d, float h, float u) {
+    const float finite = step(d, h, u), other = d == 0.f ? u : fma(fabsf(d), h, u);
+    return d == 0.f || fabsf(h) == __int_as_float(0x7F800000) ? other : finite;
+}
+__device__ __forceinline__ float2 step_any(float2 d, float2 h, float2 u) {
+    return make_float2(step_any(d.x, h.x, u.x), step_any(d.y, h.y, u.y));
 }
 __device__ __forceinline__ bool finite(float h) { return fabsf(h) <= 3.402823466e38f; }
 __device__ __forceinline__ bool finite(float2 h) { return finite(h.x) && finite(h.y); }

@@ -29,6 +29,65 @@ struct sums_of {
     float *rows;  // [slots][2][D], or NULL
 };
 
+// The tokens of a thread (up to 8) by step_any(), read again from memory, as in kda_scan_fwd: h and m, the state and the adjoint that enter them from
+// either side, become those that they leave; *sum: of the log-decays.  GRADS: leaves the tokens' gradients, and their sums for A_log and dt_bias,
+// in the order of the others.
+template <typename T, bool GRADS>
+static __device__ __noinline__ void run_any(const kda_scan_bwd_args &A, int tok, int len, int c, float2 *h, float2 *m, float2 *sum, float2 *sA, float2 *sb) {
+    constexpr int R = bwd_shape<64>::R;
+    const int have = A.D - c;
+    const spec K{A.gate_kind, A.input_scale, A.g_min};
+    const channel<float2> C = load_channel(A.A_log, A.dt_bias, c, have);
+    const float2 zero = make_float2(0.f, 0.f);
+    const bool gated = A.input_gate != nullptr;
+    auto get = [&](const void *p, int64_t stride, int r) { return load_pair<T, false>((const T *)p + (int64_t)(tok + r) * stride + c, have); };
+    float2 d[R], u[R];  // u: a h before each token
+    *sum = *sA = *sb = zero;
+    for (int r = 0; r < len; ++r) {
+        float2 z[1] = {get(A.z, A.z_stride, r)}, x[1] = {get(A.x, A.x_stride, r)};
+        log_decays(K, C, z);
+        const decay<float2> e = decay_of(z[0]);
+        *sum = add(*sum, z[0]);
+        d[r] = e.d;
+        z[0] = e.m;
+        scale_inputs(K, z, x);
+        if (gated) {
+            z[0] = get(A.input_gate, A.i_stride, r);
+            gate_inputs(z, x);
+        }
+        u[r] = step_any(d[r], *h, zero);
+        *h = GRADS ? add(u[r], x[0]) : step_any(d[r], *h, x[0]);
+    }
+    float2 lam[R];
+    for (int r = len - 1; r >= 0; --r) {
+        lam[r] = add(*m, get(A.grad_h, A.D, r));
+        *m = step_any(d[r], lam[r], zero);
+    }
+    if (!GRADS) return;
+    for (int i = 0; i < R; ++i) {  // two at a time from the last on
+        const int r = R - 2 - i / 2 * 2 + i % 2;
+        if (r >= len) continue;
+        float2 z[1] = {get(A.z, A.z_stride, r)}, kA[1], x[1] = {get(A.x, A.x_stride, r)}, s[1] = {make_float2(1.f, 1.f)}, e[1] = {u[r]}, g = zero;
+        decay_slopes(K, C, z, kA);
+        if (gated) {
+            const sig<float2> v = sigmoids(get(A.input_gate, A.i_stride, r));
+            s[0] = v.s;
+            g = mul(v.n, x[0]);
+            x[0] = mul(x[0], v.s);
+        }
+        input_slopes(K, &d[r], x, e, s);
+        const float2 dg = mul(e[0], lam[r]);
+        *sA = fma(dg, kA[0], *sA);
+        z[0] = mul(dg, z[0]);
+        *sb = add(*sb, z[0]);
+        s[0] = mul(s[0], lam[r]);
+        const int64_t o = (int64_t)(tok + r) * A.D + c;
+        store_pair<T, false>((T *)A.grad_x + o, s[0], have);
+        store_pair<T, false>((T *)A.grad_z + o, z[0], have);
+        if (gated) store_pair<T, false>((T *)A.grad_input_gate + o, mul(s[0], g), have);
+    }
+}
+
 // PLAN: as for scan_fwd_kernel; the rows of slots without a tile are zeros then
 template <typename T, int W, bool TMA, bool PLAN>
 __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1)
@@ -45,7 +104,7 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
         for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < B.slots * 2 * A.D; i += (int64_t)gridDim.x * NT) out.rows[i] = 0.f;
     if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
     const bool links = PLAN && !planned_chains(B), loader = w == NW - 1;
-    course<L, PLAN> way(B, A.cu_seqlens, A.T, A.N, blocks, how, true);
+    course<L, PLAN> way(B, S.next.way, A.cu_seqlens, A.T, A.N, blocks, how, true);
     // the first token of a tile
     auto begin = [](const tile &t) { return t.a + (t.count > 0 ? t.count - 1 - t.p : 0) * L; };
     auto ask = [&](int turn) {
@@ -57,10 +116,11 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
         for (int i = 0; i < n; ++i) load_rows<X>(&S.next.x[stage][i][0][0], maps.m[i], t.block, tok, &S.next.full[stage]);
     };
     auto advance = [&](int turn) {
-        way.next();
-        if (lane == 0) S.next.t[turn & 3] = way.t;
+        const tile t = way.next();
+        if (lane == 0) S.next.t[turn & 3] = t;
         __syncwarp();
     };
+    if (threadIdx.x == 0) S.M.odd = 0;
     if (TMA && threadIdx.x == 0) {
         tc::mbar_init(&S.next.full[0], 1);
         tc::mbar_init(&S.next.full[1], 1);
@@ -155,96 +215,113 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
                 m = step(d[r0 + r], add(m, g[r]), make_float2(0.f, 0.f));
             }
         }
+        if (!finite(h) || !finite(m)) S.M.odd = turn + 1;
         float2 before_sum, before, behind_sum, behind, all = sum;
-        over_groups<X, false>(all, h, before_sum, before);
+        over_groups<X, false, false>(all, h, before_sum, before);
         if (lane >= 32 - X::LPR) *reinterpret_cast<float2 *>(&S.f[w][pair]) = h;
-        over_groups<X, true>(sum, m, behind_sum, behind);
+        over_groups<X, true, false>(sum, m, behind_sum, behind);
         if (lane < X::LPR) {
             *reinterpret_cast<float2 *>(&S.M.g[w][pair]) = sum;
             *reinterpret_cast<float2 *>(&S.M.d[w][pair]) = decay_of(sum).d;
             *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = m;
         }
-        join<X, true>(B, links, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, err, [&](int role, int ch) {
+        const bool odd = join<X, true>(B, links, t, A.D, A.grad_final_state, A.grad_initial_state, nullptr, 0, S.M, S.E, turn + 1, err, [&](int role, int ch) {
             if (role == 2) {
-                float v = checkpoint;
+                float v = checkpoint, b[NW];
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
-                    const float b = S.f[i][ch];
+                    b[i] = S.f[i][ch];
                     S.f[i][ch] = v;
-                    v = step_or_erase(S.M.d[i][ch], v, b);
+                    v = step(S.M.d[i][ch], v, b[i]);
+                }
+                if (!finite(v)) {
+                    v = checkpoint;
+#pragma unroll
+                    for (int i = 0; i < NW; ++i) {
+                        S.f[i][ch] = v;
+                        v = step_any(S.M.d[i][ch], v, b[i]);
+                    }
                 }
             } else {
                 add_up(ch);
             }
+        }, [&] {
+            float2 s, f = make_float2(0.f, 0.f), b = f, none;
+            run_any<T, false>(A, tok, len, c, &f, &b, &s, &none, &none);
+            float2 up_to = s;
+            over_groups<X, false, true>(up_to, f, before_sum, before);
+            if (lane >= 32 - X::LPR) *reinterpret_cast<float2 *>(&S.f[w][pair]) = f;
+            over_groups<X, true, true>(s, b, behind_sum, behind);
+            if (lane < X::LPR) *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = b;
         });
         if (loader) {
             // every warp is done with the tile before, whose stage the next one takes
             ask(turn + 1);
             advance(turn + 2);
         }
-        h = group_entry<X>(*reinterpret_cast<const float2 *>(&S.f[w][pair]), before_sum, before);
-        m = group_entry<X>(*reinterpret_cast<const float2 *>(&S.M.g[w][pair]), behind_sum, behind);
-        // what enters may be an infinity or a NaN, which a decay of 0 erases
-        const bool odd = __any_sync(0xffffffffu, !finite(h) || !finite(m));
-        auto erase = [&](float2 &v, float2 by) {
-            if (odd) v = each([](float k, float s) { return k == 0.f ? 0.f : s; }, by, v);
-        };
-#pragma unroll
-        for (int r = 0; r < R; ++r) {  // u: a h before each token
-            const float2 v = u[r];
-            erase(h, d[r]);
-            u[r] = step(d[r], h, make_float2(0.f, 0.f));
-            h = add(u[r], v);
-        }
+        const float2 h_in = *reinterpret_cast<const float2 *>(&S.f[w][pair]), m_in = *reinterpret_cast<const float2 *>(&S.M.g[w][pair]);
+        h = group_entry<X, false>(h_in, before_sum, before);
+        m = group_entry<X, false>(m_in, behind_sum, behind);
         float2 sA = make_float2(0.f, 0.f), sb = sA;
-        const int64_t at = (int64_t)tok * A.D + c;
+        if (__any_sync(0xffffffffu, odd || !finite(h) || !finite(m))) {
+            float2 hs = group_entry<X, true>(h_in, before_sum, before), ms = group_entry<X, true>(m_in, behind_sum, behind), none, A2, b2;
+            run_any<T, true>(A, tok, len, c, &hs, &ms, &none, &A2, &b2);
+            sA = A2, sb = b2;
+        } else {
 #pragma unroll
-        for (int r0 = R - P2; r0 >= 0; r0 -= P2) {
-            float2 z[P2], kA[P2], x[P2], s[P2], e[P2], g[P2], lam[P2];
-            get(0, r0, A.z, A.z_stride, z);
-            decay_slopes(K, C, z, kA);
-            get(1, r0, A.x, A.x_stride, x);
-            get(2, r0, A.grad_h, A.D, g);
-            if (len < r0 + P2) {
-#pragma unroll
-                for (int r = 0; r < P2; ++r)
-                    if (r0 + r >= len) z[r] = kA[r] = g[r] = make_float2(0.f, 0.f);
+            for (int r = 0; r < R; ++r) {  // u: a h before each token
+                const float2 v = u[r];
+                u[r] = step(d[r], h, make_float2(0.f, 0.f));
+                h = add(u[r], v);
             }
+            const int64_t at = (int64_t)tok * A.D + c;
 #pragma unroll
-            for (int r = P2 - 1; r >= 0; --r) {
-                lam[r] = m = add(m, g[r]);
-                erase(m, d[r0 + r]);
-                m = step(d[r0 + r], m, make_float2(0.f, 0.f));
-            }
-            // g: what x is multiplied by but for c(a) and the gate's slope, s (1 - s)
-            if (gated) {
-                get(3, r0, A.input_gate, A.i_stride, g);
+            for (int r0 = R - P2; r0 >= 0; r0 -= P2) {
+                float2 z[P2], kA[P2], x[P2], s[P2], e[P2], g[P2], lam[P2];
+                get(0, r0, A.z, A.z_stride, z);
+                decay_slopes(K, C, z, kA);
+                get(1, r0, A.x, A.x_stride, x);
+                get(2, r0, A.grad_h, A.D, g);
+                if (len < r0 + P2) {
+#pragma unroll
+                    for (int r = 0; r < P2; ++r)
+                        if (r0 + r >= len) z[r] = kA[r] = g[r] = make_float2(0.f, 0.f);
+                }
+#pragma unroll
+                for (int r = P2 - 1; r >= 0; --r) {
+                    lam[r] = m = add(m, g[r]);
+                    m = step(d[r0 + r], m, make_float2(0.f, 0.f));
+                }
+                // g: what x is multiplied by but for c(a) and the gate's slope, s (1 - s)
+                if (gated) {
+                    get(3, r0, A.input_gate, A.i_stride, g);
+#pragma unroll
+                    for (int r = 0; r < P2; ++r) {
+                        const sig<float2> v = sigmoids(g[r]);
+                        s[r] = v.s;
+                        g[r] = mul(v.n, x[r]);
+                        x[r] = mul(x[r], v.s);
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < P2; ++r) s[r] = make_float2(1.f, 1.f);
+                }
+#pragma unroll
+                for (int r = 0; r < P2; ++r) e[r] = u[r0 + r];
+                input_slopes(K, &d[r0], x, e, s);
 #pragma unroll
                 for (int r = 0; r < P2; ++r) {
-                    const sig<float2> v = sigmoids(g[r]);
-                    s[r] = v.s;
-                    g[r] = mul(v.n, x[r]);
-                    x[r] = mul(x[r], v.s);
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < P2; ++r) s[r] = make_float2(1.f, 1.f);
-            }
-#pragma unroll
-            for (int r = 0; r < P2; ++r) e[r] = u[r0 + r];
-            input_slopes(K, &d[r0], x, e, s);
-#pragma unroll
-            for (int r = 0; r < P2; ++r) {
-                const float2 dg = mul(e[r], lam[r]);
-                sA = fma(dg, kA[r], sA);
-                z[r] = mul(dg, z[r]);
-                sb = add(sb, z[r]);
-                s[r] = mul(s[r], lam[r]);
-                if (r0 + r < len && have > 0) {
-                    const int64_t o = at + (int64_t)(r0 + r) * A.D;
-                    store_pair<T, TMA>((T *)A.grad_x + o, s[r], have);
-                    store_pair<T, TMA>((T *)A.grad_z + o, z[r], have);
-                    if (gated) store_pair<T, TMA>((T *)A.grad_input_gate + o, mul(s[r], g[r]), have);
+                    const float2 dg = mul(e[r], lam[r]);
+                    sA = fma(dg, kA[r], sA);
+                    z[r] = mul(dg, z[r]);
+                    sb = add(sb, z[r]);
+                    s[r] = mul(s[r], lam[r]);
+                    if (r0 + r < len && have > 0) {
+                        const int64_t o = at + (int64_t)(r0 + r) * A.D;
+                        store_pair<T, TMA>((T *)A.grad_x + o, s[r], have);
+                        store_pair<T, TMA>((T *)A.grad_z + o, z[r], have);
+                        if (gated) store_pair<T, TMA>((T *)A.grad_input_gate + o, mul(s[r], g[r]), have);
+                    }
                 }
             }
         }

@@ -19,6 +19,31 @@ template <typename T, int W> struct fwd_memory {
     tile_memory<W> M;
 };
 
+// The tokens of a thread by step_any() from h on, read again from memory: what a tile does in which infinities or NaN are found, out of the
+// way of the others, whose decays and inputs stay in registers.  *sum: of the log-decays; STORE: leaves the states.
+template <typename T, bool STORE>
+static __device__ __noinline__ float2 run_any(const kda_scan_args &A, int tok, int len, int c, float2 h, float2 *sum) {
+    const int have = A.D - c;
+    const spec K{A.gate_kind, A.input_scale, A.g_min};
+    const channel<float2> C = load_channel(A.A_log, A.dt_bias, c, have);
+    *sum = make_float2(0.f, 0.f);
+    for (int64_t t = tok; t < tok + len; ++t) {
+        float2 z[1] = {load_pair<T, false>((const T *)A.z + t * A.z_stride + c, have)}, x[1] = {load_pair<T, false>((const T *)A.x + t * A.x_stride + c, have)};
+        log_decays(K, C, z);
+        const decay<float2> e = decay_of(z[0]);
+        *sum = add(*sum, z[0]);
+        z[0] = e.m;
+        scale_inputs(K, z, x);
+        if (A.input_gate) {
+            z[0] = load_pair<T, false>((const T *)A.input_gate + t * A.i_stride + c, have);
+            gate_inputs(z, x);
+        }
+        h = step_any(e.d, h, x[0]);
+        if (STORE) store_pair<T, false>((T *)A.h + t * A.D + c, h, have);
+    }
+    return h;
+}
+
 // TMA: rows are 16-byte aligned.  Else a thread reads its elements when it needs them.  PLAN: make_plan() says what the tiles are (a
 // kernel of its own for the others: one for all was 2 to 8 % slower where tiles join).
 template <typename T, int W, bool TMA, bool PLAN>
@@ -34,18 +59,19 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     const bool gated = A.input_gate != nullptr;
     if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
     const bool links = PLAN && !planned_chains(B), loader = w == NW - 1;
-    course<L, PLAN> way(B, A.cu_seqlens, A.T, A.N, blocks, how, false);
+    course<L, PLAN> way(B, S.next.way, A.cu_seqlens, A.T, A.N, blocks, how, false);
     // the next tile of the course, its boxes asked for
     auto ask = [&](int stage) {
-        way.next();
+        const tile t = way.next();
         if (lane != 0) return;
-        S.next.t[stage] = way.t;
-        if (!TMA || way.t.p < 0) return;
-        const int tok = way.t.a + way.t.p * L, n = gated ? 3 : 2;
+        S.next.t[stage] = t;
+        if (!TMA || t.p < 0) return;
+        const int tok = t.a + t.p * L, n = gated ? 3 : 2;
         tc::fence_proxy_async();  // (join() has written to the stage)
         tc::mbar_arrive_expect_tx(&S.next.full[stage], (uint32_t)(n * L * W * sizeof(T)));
-        for (int i = 0; i < n; ++i) load_rows<X>(&S.next.x[stage][i][0][0], maps.m[i], way.t.block, tok, &S.next.full[stage]);
+        for (int i = 0; i < n; ++i) load_rows<X>(&S.next.x[stage][i][0][0], maps.m[i], t.block, tok, &S.next.full[stage]);
     };
+    if (threadIdx.x == 0) S.M.odd = 0;
     if (TMA && threadIdx.x == 0) {
         tc::mbar_init(&S.next.full[0], 1);
         tc::mbar_init(&S.next.full[1], 1);
@@ -110,24 +136,37 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) h = step(d[r], h, u[r]);
+        if (!finite(h)) S.M.odd = turn + 1;
         float2 before_sum, before;
-        over_groups<X, false>(sum, h, before_sum, before);
+        over_groups<X, false, false>(sum, h, before_sum, before);
         if (lane >= 32 - X::LPR) {
             *reinterpret_cast<float2 *>(&S.M.g[w][pair]) = sum;
             *reinterpret_cast<float2 *>(&S.M.d[w][pair]) = decay_of(sum).d;
             *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = h;
         }
-        join<X, false>(B, links, t, A.D, A.initial_state, A.final_state,
-                       A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr,
-                       (t.b - t.a - t.p * L + CK - 1) / CK, S.M, *reinterpret_cast<entries<W> *>(&S.next.x[stage]), err, [](int, int) {});
+        const bool odd = join<X, false>(
+            B, links, t, A.D, A.initial_state, A.final_state,
+            A.checkpoints ? A.checkpoints + ((int64_t)t.a / CK + t.n + t.p * (L / CK)) * A.D : nullptr,
+            (t.b - t.a - t.p * L + CK - 1) / CK, S.M, *reinterpret_cast<entries<W> *>(&S.next.x[stage]), turn + 1, err, [](int, int) {},
+            [&] {
+                float2 s, v = run_any<T, false>(A, tok, len, c, make_float2(0.f, 0.f), &s);
+                over_groups<X, false, true>(s, v, before_sum, before);
+                if (lane >= 32 - X::LPR) *reinterpret_cast<float2 *>(&S.M.b[w][pair]) = v;
+            });
         if (loader) ask(stage);  // every warp is done with this stage
-        h = group_entry<X>(*reinterpret_cast<const float2 *>(&S.M.g[w][pair]), before_sum, before);
-        // what enters may be an infinity or a NaN, which a decay of 0 erases
-        const bool odd = __any_sync(0xffffffffu, !finite(h));
+        const float2 enters = *reinterpret_cast<const float2 *>(&S.M.g[w][pair]);
+        h = group_entry<X, false>(enters, before_sum, before);
+        if (__any_sync(0xffffffffu, odd || !finite(h))) {
+            float2 s;
+            run_any<T, true>(A, tok, len, c, group_entry<X, true>(enters, before_sum, before), &s);
+            continue;
+        }
+        // (what the first pass made of the decays is not kept for the second: registers)
+#pragma unroll
+        for (int r = 0; r < R; ++r) asm("" : "+f"(d[r].x), "+f"(d[r].y));
         T *out = (T *)A.h + (int64_t)tok * A.D + c;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (odd) h = each([](float v, float s) { return v == 0.f ? 0.f : s; }, d[r], h);
             h = step(d[r], h, u[r]);
             if (r < len && have > 0) store_pair<T, TMA>(out, h, have);
             out += A.D;

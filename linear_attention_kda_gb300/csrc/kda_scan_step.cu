@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
         const F m[1] = {d.m};
         scale_inputs(S, m, xk);
         if (A.input_gate) gate_inputs(ik, xk);
-        h[k] = step_or_erase(d.d, h[k], xk[0]);
+        h[k] = step_any(d.d, h[k], xk[0]);
     }
     layer::store(state, layer::pack<float, V>(h));
     layer::store((T *)A.h + n * A.D + c, layer::pack<T, V>(h));

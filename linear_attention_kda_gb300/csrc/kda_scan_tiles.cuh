@@ -228,12 +228,14 @@ __device__ __forceinline__ float compose(float d1, float d2) {
 template <int W> struct tile_memory {
     float g[NW][W], d[NW][W], b[NW][W];  // the warps' sums of log-decays, decays and values; after join() g is the state that enters each warp's tokens
     float from[W];                       // the state behind the last tile, where a block takes whole chains
+    int odd;                             // the last turn in which a thread's tokens left an infinity or a NaN, counted from 1
 };
 // entries on their way through a block: those of the groups (at 1) and of the tiles (at G) before a tile
 template <int W> using entries = unsigned long long[1 + 2 * (G - 1)][W];
 
 // Over the groups of a warp, in the direction of the scan: sum and value become those up to and with each group's, before_* those up to it.
-template <typename X, bool BACK>
+// ANY: with infinities and NaN.
+template <typename X, bool BACK, bool ANY>
 __device__ __forceinline__ void over_groups(float2 &sum, float2 &value, float2 &before_sum, float2 &before) {
     before_sum = before = make_float2(0.f, 0.f);
     if constexpr (X::GW > 1) {
@@ -246,7 +248,8 @@ __device__ __forceinline__ void over_groups(float2 &sum, float2 &value, float2 &
         for (int off = 1; off < X::GW; off *= 2) {
             const float2 s = of(sum, off), v = of(value, off);
             if (BACK ? grp + off < X::GW : grp >= off) {
-                value = step_or_erase(decay_of(sum).d, v, value);
+                const float2 d = decay_of(sum).d;
+                value = ANY ? step_any(d, v, value) : step(d, v, value);
                 sum = add(sum, s);
             }
         }
@@ -255,28 +258,48 @@ __device__ __forceinline__ void over_groups(float2 &sum, float2 &value, float2 &
     }
 }
 // The state that enters a group's tokens from the one that enters the warp's
-template <typename X> __device__ __forceinline__ float2 group_entry(float2 warp, float2 before_sum, float2 before) {
-    if constexpr (X::GW > 1) return step_or_erase(decay_of(before_sum).d, warp, before);
+template <typename X, bool ANY> __device__ __forceinline__ float2 group_entry(float2 warp, float2 before_sum, float2 before) {
+    if constexpr (X::GW > 1) {
+        const float2 d = decay_of(before_sum).d;
+        return ANY ? step_any(d, warp, before) : step(d, warp, before);
+    }
     return warp;
+}
+// step_any() over n decays and values from h on, `pitch` apart; enters (or NULL): the state before each.  For what step() finds no longer
+// finite in the end, and out of the way of the rest.
+static __device__ __noinline__ float fold_any(float h, const float *d, const float *b, float *enters, int pitch, int n) {
+    for (int i = 0; i < n; ++i, d += pitch, b += pitch) {
+        if (enters) enters[i * pitch] = h;
+        h = step_any(*d, h, *b);
+    }
+    return h;
 }
 
 // With every warp's (g, d, b) in place: leaves the tile's sum for others and finds what enters each warp's tokens.  start, end:
 // the state (or adjoint) before and behind the sequence, [N, D] or NULL; kept: where the checkpoints of this tile go (NULL: nowhere), `room` rows.
 // links: tiles of this sequence wait for one another; E: memory that every warp is done with at the first barrier.
 // BACK: the direction is from the last token to the first, so from the last warp to the first.  more_work(role, channel): what
-// two otherwise idle roles (2 and 3) do meanwhile.
-template <typename X, bool BACK, typename F>
-__device__ __forceinline__ void join(const board &B, bool links, const tile &t, int D, const float *start, float *end, float *kept, int room,
-                                     tile_memory<X::W> &M, entries<X::W> &E, int *err, F &&more_work) {
+// two otherwise idle roles (2 and 3) do meanwhile.  again(): forms the warps' values again, with the infinities and NaN that one of them
+// is found to have in this turn (returned).
+template <typename X, bool BACK, typename F, typename Again>
+__device__ __forceinline__ bool join(const board &B, bool links, const tile &t, int D, const float *start, float *end, float *kept, int room,
+                                     tile_memory<X::W> &M, entries<X::W> &E, int turn, int *err, F &&more_work, Again &&again) {
     // four roles, each of as many warps as its W threads need
     constexpr int W = X::W, WARPS = W > 32 ? W / 32 : 1;
     static_assert(4 * WARPS <= NW, "four roles");
     const int ch = threadIdx.x % (32 * WARPS), role = ch < W ? (int)threadIdx.x / (32 * WARPS) : NW, c = t.block * W + ch;
     const bool more = t.p + 1 < t.count;
     __syncthreads();
+    const bool odd = M.odd == turn;
+    if (odd) {
+        again();
+        __syncthreads();
+    }
     const int q = links ? t.p % G : 0, gq = links ? t.p / G % G : 0, super = links ? t.p / (G * G) : 0;
     const int64_t slot = t.first + t.p;
     float sum = 0.f, v = 0.f, h = 0.f;
+    auto warp_at = [](int i) { return BACK ? NW - 1 - i : i; };  // the warps in the direction of the scan
+    constexpr int PITCH = BACK ? -W : W;
     if (role == 0) {
         if (t.p == 0) h = start && c < D ? start[(int64_t)t.n * D + c] : 0.f;
         else if (!links) h = M.from[ch];
@@ -288,13 +311,14 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
             if (more) {
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
-                    const int w = BACK ? NW - 1 - i : i;
+                    const int w = warp_at(i);
                     sum += M.g[w][ch];
-                    v = step_or_erase(M.d[w][ch], v, M.b[w][ch]);
+                    v = step(M.d[w][ch], v, M.b[w][ch]);
                 }
+                if (!finite(v)) v = fold_any(0.f, &M.d[warp_at(0)][ch], &M.b[warp_at(0)][ch], nullptr, PITCH, NW);
                 sum = decay_of(sum).d;
                 if (t.p == 0) {  // nothing enters the first tile: its value is the state behind it
-                    v = step_or_erase(sum, h, v);
+                    v = step_any(sum, h, v);
                     sum = 0.f;
                 }
                 if (c < D) put(B.entry[0] + slot * D + c, sum, v);
@@ -317,26 +341,45 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
     }
     if (role == 0) {
         if (links && c < D) {
+            // the state behind `all` entries from the i-th one on
+            auto over = [&](float h, int i, int all, float to) {
+                const float *e = reinterpret_cast<const float *>(&E[i][ch]);
+                return finite(to) ? to : fold_any(h, e, e + 1, nullptr, 2 * W, all);
+            };
             if (q == G - 1 && more) {
                 // (from the first tile's, so that decays near 1 are joined as a - 1)
                 float gd = entry_d(E[G][ch]), gb = entry_b(E[G][ch]);
 #pragma unroll
                 for (int i = 1; i < G - 1; ++i) {
                     const unsigned long long x = E[G + i][ch];
-                    gb = step_or_erase(entry_d(x), gb, entry_b(x));
+                    gb = step(entry_d(x), gb, entry_b(x));
                     gd = compose(gd, entry_d(x));
                 }
-                put(B.entry[1] + ((int64_t)t.first / G + t.n + t.p / G) * D + c, compose(gd, sum), step_or_erase(sum, gb, v));
+                gb = over(entry_b(E[G][ch]), G + 1, G - 2, gb);
+                put(B.entry[1] + ((int64_t)t.first / G + t.n + t.p / G) * D + c, compose(gd, sum), step_any(sum, gb, v));
             }
-            for (int i = 0; i < gq; ++i) h = step_or_erase(entry_d(E[1 + i][ch]), h, entry_b(E[1 + i][ch]));
-            for (int i = 0; i < q; ++i) h = step_or_erase(entry_d(E[G + i][ch]), h, entry_b(E[G + i][ch]));
+            const float before = h;
+            for (int i = 0; i < gq; ++i) h = step(entry_d(E[1 + i][ch]), h, entry_b(E[1 + i][ch]));
+            h = over(before, 1, gq, h);
+            const float behind = h;
+            for (int i = 0; i < q; ++i) h = step(entry_d(E[G + i][ch]), h, entry_b(E[G + i][ch]));
+            h = over(behind, G, q, h);
         }
+        const float from = h;
+        auto keep = [&](int w, float v) {
+            if (!BACK && w * X::RW % CK == 0 && kept && w * X::RW / CK < room && c < D) kept[(int64_t)(w * X::RW / CK) * D + c] = v;
+        };
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            const int w = BACK ? NW - 1 - i : i;
-            if (!BACK && w * X::RW % CK == 0 && kept && w * X::RW / CK < room && c < D) kept[(int64_t)(w * X::RW / CK) * D + c] = h;
+            const int w = warp_at(i);
+            keep(w, h);
             M.g[w][ch] = h;
-            h = step_or_erase(M.d[w][ch], h, M.b[w][ch]);
+            h = step(M.d[w][ch], h, M.b[w][ch]);
+        }
+        if (!finite(h)) {
+            h = fold_any(from, &M.d[warp_at(0)][ch], &M.b[warp_at(0)][ch], &M.g[warp_at(0)][ch], PITCH, NW);
+#pragma unroll 1
+            for (int w = 0; w < NW; ++w) keep(w, M.g[w][ch]);
         }
         if (links && more && t.p % (G * G) == G * G - 1 && c < D)
             put(B.entry[2] + ((int64_t)t.first / (G * G) + t.n + super) * D + c, h, 0.f);
@@ -346,6 +389,7 @@ __device__ __forceinline__ void join(const board &B, bool links, const tile &t, 
         more_work(role, ch);
     }
     __syncthreads();
+    return odd;
 }
 
 // An entry of the plan (of the chains) of a call that has none.
@@ -357,21 +401,29 @@ static __device__ __noinline__ int4 unplanned(const int32_t *cu, int64_t T, int6
     return make_int4((int)n, (int)p, (int)s.a, (int)s.b);
 }
 
-// The tiles that a block goes through, as one warp of it finds them.
+// Where a block is in its tiles, in shared memory: one warp asks for them, and in registers it would be in everybody's way.
+struct progress {
+    tile t;        // the last one
+    int64_t item;  // the chain's or the tile's place among the call's (-1: none yet)
+};
+// The tiles that a block goes through, as one warp of it finds them (p = -1 behind the last).
 template <int L, bool PLAN> struct course {
     const board &B;
+    progress &at;
     const int32_t *cu;
-    int64_t T, N, item;
+    int64_t T, N;
     int blocks;
     layout how;
     bool back, chains;
-    tile t;  // p = -1 behind the last
-    __device__ __forceinline__ course(const board &b, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, layout how_, bool back_)
-        : B(b), cu(cu_), T(T_), N(N_), item(-1), blocks(blocks_), how(how_), back(back_) {
+    __device__ __forceinline__ course(const board &b, progress &at_, const int32_t *cu_, int64_t T_, int64_t N_, int blocks_, layout how_, bool back_)
+        : B(b), at(at_), cu(cu_), T(T_), N(N_), blocks(blocks_), how(how_), back(back_) {
         chains = PLAN ? planned_chains(B) : how == EQUAL;
-        t = tile{0, -1, 0, 0, 0, 0, 0};
+        if (threadIdx.x == 0) at = progress{tile{0, -1, 0, 0, 0, 0, 0}, -1};  // (a barrier follows)
     }
-    __device__ __forceinline__ void next() {
+    __device__ __forceinline__ tile next() {
+        tile t = at.t;
+        int64_t item = at.item;
+        __syncwarp();
         const int64_t items = (chains ? N : lin::chunk_slots(T, N, L)) * blocks;
         next_tile<L>(t, chains, back, [&](tile *to) {
             if (PLAN && chains) {
@@ -388,6 +440,9 @@ template <int L, bool PLAN> struct course {
             to->n = q.x, to->p = q.y, to->a = q.z, to->b = q.w;
             return true;
         });
+        if ((threadIdx.x & 31) == 0) at = progress{t, item};
+        __syncwarp();
+        return t;
     }
 };
 
@@ -405,6 +460,7 @@ template <typename T, int NI, typename X> struct ring {
     T x[2][NI][X::L][X::W];
     uint64_t full[2];
     tile t[4];
+    progress way;
 };
 template <int NI> struct row_maps {
     CUtensorMap m[NI];

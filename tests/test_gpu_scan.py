@@ -205,6 +205,62 @@ def test_erasing_decays(dtype):
     assert (g["initial_state"] == 0).all()
 
 
+def _same(name, got, want, size, n, half):
+    """Infinities and NaN where the definition has them, the rest within its bound."""
+    got, bad = U.f64(got), ~np.isfinite(want)
+    assert np.array_equal(np.where(bad, got, 0), np.where(bad, want, 0), equal_nan=True), (name, np.argwhere(~((got == want) | np.isfinite(want) | np.isnan(got) & np.isnan(want)))[:9])
+    U.close(name, torch.from_numpy(np.where(bad, 0, got)), np.where(bad, 0, want), np.where(bad, 0, size), n, half)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("input_scale", U.INPUTS)
+@pytest.mark.parametrize("lens", [[150, 90], [60, 3000], [5000, 0, 17]])
+def test_infinities_stay_infinities(dtype, input_scale, lens):
+    """A state, an input or an adjoint of infinity is one from there on under decays above 0, and erased by one of 0."""
+    inf, last, T = float("inf"), len(lens) - 1, sum(lens)
+    d = U.scan_batch(lens, 40, dtype, 22, gate="log", input_scale=input_scale)
+    d["z"] = (d["z"].float() * 0.02).to(U.DT[dtype])  # (whose sum over a sequence is nowhere below -80)
+    d["z"][0, 5], d["z"][35, 14], d["z"][T - 1, 6] = -inf, -inf, -inf
+    clean = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+    n, size = U.scan_roundings(d), U.scan_ref(clean, True)
+    d["initial_state"][0, :8], d["initial_state"][last, 4:9] = inf, -inf
+    d["x"][40, 10], d["x"][lens[0] - 1, 11], d["x"][T - 9, 12], d["x"][20, 14] = inf, -inf, inf, inf
+    r, want = _fwd(d), U.scan_ref(d)
+    _no_error()
+    _same("h", r[0], want[0], size[0], n, U.HALF[dtype])
+    _same("final_state", r[1], want[1], size[1], n, U.U32)
+    held = ~np.isnan(size[2][:, 0])
+    _same("checkpoints", r[2].cpu()[torch.from_numpy(held)], want[2][held], size[2][held], n, U.U32)
+    assert np.isinf(want[0]).sum() > 100
+    # gradients: of infinite ones of the final state and of a token, and beside an infinite state
+    for k in ("grads", "state"):
+        e = {**clean, **{j: clean[j].clone() for j in ("grad_final_state", "grad_h", "initial_state")}}
+        if k == "grads":
+            e["grad_final_state"][last, :8], e["grad_h"][T - 9, 20] = inf, -inf
+        else:
+            e["initial_state"][0, :5] = inf  # (one that is erased leaves 0 here, 0 x infinity in the oracle)
+        got, want, sizes = _bwd(e, _fwd(e)[2]), U.scan_grads_ref(e), U.scan_grads_ref(clean, True)
+        _no_error()
+        assert sum(np.isinf(want[j]).sum() for j in ("x", "z")) > 50
+        for j in ("x", "z", "input_gate", "initial_state"):
+            _same(j, got[j], want[j], sizes[j], 2 * n, U.U32 if j == "initial_state" else U.HALF[dtype])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_step_keeps_infinities(dtype):
+    d, pool, idx = _step_batch(3, 20, dtype, 5, 4, gate="log")
+    pool[idx.long(), :4], d["z"][:, 2] = float("inf"), -float("inf")
+    pool[idx[1].long(), 3] = -float("inf")
+    d["initial_state"] = pool[idx.long()]
+    p = pool.cuda()
+    h = _step(d, p, idx)
+    _no_error()
+    want = U.scan_ref(d)[1]
+    assert np.isinf(want).sum() == 9
+    _same("h", h, want, abs(want), U.scan_roundings(d), U.HALF[dtype])
+    _same("state", p[idx.long().cuda()], want, abs(want), U.scan_roundings(d), U.U32)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_nan_stays_in_its_channel(dtype):
     d = U.scan_batch([200, 150], 40, dtype, 5, gate="softplus", input_scale="norm")
