@@ -218,13 +218,15 @@ block_norm_bwd_kernel(const __grid_constant__ kda_block_norm_bwd_args A, float *
         float ss[2] = {total(sy), total(sg)};
         if (post || token) row_sum<NT>(ss, parts, at);
         if (token && tid == 0) st((T *)A.grad_gate + row, ss[1] * kt * (1.f - kt));
-        m = post ? -ss[0] * inv : 0.f;
+        m = -ss[0] * inv;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int c = column(e);
             if (c >= A.D) continue;
+            if (post) {  // (without a norm nothing of y, which may be an infinity, is in its gradient)
 #pragma unroll
-            for (int i = 0; i < P; ++i) d[e][i] = mul(fma(y[e][i], splat<F>(m), d[e][i]), splat<F>(ky));
+                for (int i = 0; i < P; ++i) d[e][i] = mul(fma(y[e][i], splat<F>(m), d[e][i]), splat<F>(ky));
+            }
             layer::store_once((T *)A.grad_y + base + c, layer::pack<T, V>(d[e]));
         }
     }

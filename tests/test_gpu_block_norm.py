@@ -213,6 +213,19 @@ def test_nan_stays_in_its_row():
     assert g["gate"][20, 100] == 0 and g["gate"][21, 100] == 0  # a gate at its end has no slope
 
 
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("D", [101, 264, 1024])
+def test_gradients_of_infinities_without_a_norm(types, gate, D):
+    """Without its norm y's gradient is scale * sigmoid(gate) * dr', whatever y is."""
+    d = U.norm_batch(20, D, types[0], 12, res=types[1], gate=gate, post=False, pre=False)
+    want = _bwd(d)
+    d["y"][3, 5], d["y"][4, 6], d["y"][7, 0] = float("inf"), -float("inf"), float("nan")
+    g = _bwd(d)
+    _no_error()
+    assert torch.equal(g["y"], want["y"]) and torch.equal(g["residual"], want["residual"]) and want["y"].isfinite().all()
+
+
 def test_same_bits_again_and_graphs():
     d = U.norm_batch(3000, 1024, "bf16", 8, res="f32")
     r, g = _fwd(d), _bwd(d)
