@@ -226,6 +226,80 @@ def test_gradients_of_infinities_without_a_norm(types, gate, D):
     assert torch.equal(g["y"], want["y"]) and torch.equal(g["residual"], want["residual"]) and want["y"].isfinite().all()
 
 
+# ---------------------------------------------------------------- rows above 512 channels, several to a block: copies into places that are taken in turn
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("T,D", [(3100, 520), (3100, 1024), (1300, 2048), (1300, 4096), (700, 7168), (700, 8192)])
+def test_many_wide_rows(types, T, D):
+    d = U.norm_batch(T, D, types[0], D, res=types[1])
+    _check_fwd(d, _fwd(d))
+    _check_bwd(d, _bwd(d))
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("gate", ["channel", "token", "none"])
+@pytest.mark.parametrize("norms", [(True, True), (True, False), (False, True), (False, False)])
+def test_parts_of_many_wide_rows(types, gate, norms):
+    d = U.norm_batch(1900, 1024, types[0], 14, res=types[1], gate=gate, post=norms[0], pre=norms[1], vec=norms[0])
+    _check_fwd(d, _fwd(d))
+    _check_bwd(d, _bwd(d))
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_one_gradient_of_many_wide_rows(types):
+    d = U.norm_batch(1900, 1024, types[0], 15, res=types[1])
+    x = U.to(d)
+    for miss in ("grad_residual", "grad_normed"):
+        gr, gn = (None if k == miss else x[k] for k in ("grad_residual", "grad_normed"))
+        _check_bwd({**d, miss: torch.zeros_like(d[miss])}, kda.block_norm_bwd(x["y"], x["residual"], x["gate"], gr, gn, **U.norm_options(x)))
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_first_norm_of_many_wide_rows(types):
+    d = U.norm_batch(1900, 1024, types[0], 16, res=types[1])
+    x = U.to(d)
+    g = kda.block_norm_bwd(None, x["residual"], None, x["grad_residual"], x["grad_normed"], pre_weight=x["pre_weight"])
+    _no_error()
+    a = [R.block_norm_grads(None, U.f64(d["residual"]), None, 1.0, None, U.f64(d["pre_weight"]), U.f64(d["grad_residual"]), U.f64(d["grad_normed"]),
+                            magnitudes=m) for m in (False, True)]
+    U.close("residual", g["residual"], a[0]["r"], a[1]["r"], 3 * ROUNDINGS, U.HALF[types[1]])
+    U.close("pre_weight", g["pre_weight"], a[0]["pre"], a[1]["pre"], ROUNDINGS + 1900, U.U32)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("over", ["y", "grad_normed"])
+def test_many_wide_rows_in_place(types, over):
+    """By the C call: gradients over y or grad_normed, and over grad_residual_out."""
+    T, D, code = 1900, 1024, {"f32": 0, "bf16": 1}
+    d = U.norm_batch(T, D, types[0], 17, res=types[1])
+    want, x = _bwd(d), U.to(d)
+    ws = torch.empty(kda.block_norm_bwd_workspace_size(T, D, U.DT[types[0]]), dtype=torch.uint8, device="cuda")
+    w, gate = {k: torch.empty(D, device="cuda") for k in ("post_weight", "pre_weight", "scale")}, torch.empty_like(x["gate"])
+    p = {k: v.data_ptr() for k, v in x.items() if isinstance(v, torch.Tensor)}
+    a = kda.BlockNormBwdArgs(T=T, D=D, dtype=code[types[0]], residual_dtype=code[types[1]], gate_kind=1, post_norm=1, pre_norm=1, eps=1e-6, scale=1.0,
+                             scale_vec=p["scale"], y=p["y"], gate=p["gate"], residual=p["residual"], post_weight=p["post_weight"],
+                             pre_weight=p["pre_weight"], grad_residual_out=p["grad_residual"], grad_normed=p["grad_normed"], grad_y=p[over],
+                             grad_gate=gate.data_ptr(), grad_residual=p["grad_residual"], grad_post_weight=w["post_weight"].data_ptr(),
+                             grad_pre_weight=w["pre_weight"].data_ptr(), grad_scale=w["scale"].data_ptr())
+    stream = torch.cuda.current_stream().cuda_stream
+    assert kda.load_library().kda_block_norm_bwd(ctypes.byref(a), ws.data_ptr(), ws.numel(), stream) == 0
+    _no_error()
+    assert torch.equal(x[over], want["y"]) and torch.equal(x["grad_residual"], want["residual"]) and torch.equal(gate, want["gate"])
+    assert all(torch.equal(w[k], want[k]) for k in w)
+
+
+def test_gradients_behind_32_bits():
+    D, T = 8192, 264000
+    d = U.norm_batch(3, D, "bf16", 18, gate="token")
+    x = U.to(d)
+    big = {k: torch.zeros((T, D) if x[k].dim() == 2 else (T,), dtype=torch.bfloat16, device="cuda")
+           for k in ("y", "residual", "gate", "grad_residual", "grad_normed")}
+    for k in big:
+        big[k][-3:] = x[k]
+    g = kda.block_norm_bwd(big["y"], big["residual"], big["gate"], big["grad_residual"], big["grad_normed"], **U.norm_options(x))
+    _check_bwd(d, {k: v[-3:] if k in ("y", "residual", "gate") else v for k, v in g.items()})
+    assert (g["residual"][:-3:1000] == 0).all() and (g["y"][:-3:1000] == 0).all()
+
+
 def test_same_bits_again_and_graphs():
     d = U.norm_batch(3000, 1024, "bf16", 8, res="f32")
     r, g = _fwd(d), _bwd(d)

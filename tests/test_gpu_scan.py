@@ -108,6 +108,26 @@ def test_many_sequences(dtype, N, long):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("long", (0, 3000))
+@pytest.mark.parametrize("N", (350, 700))
+def test_many_sequences_by_copies(dtype, N, long):
+    """As above with rows of a multiple of 16 bytes, so that tiles of 32 and of 64 channels come by copies ahead of their use; infinite states too."""
+    lens = np.random.default_rng(N + long).integers(0, 520 if not long else 8, N).tolist()
+    lens[N // 3] = long or lens[N // 3]
+    d = U.scan_batch(lens, 40, dtype, N, gate="softplus" if long else "sigmoid", input_scale="norm")
+    r = _fwd(d)
+    _check_fwd(d, r)
+    _check_bwd(d, _bwd(d, r[2]))
+    size, n = U.scan_ref(d, True), U.scan_roundings(d)
+    for c, k in enumerate((5, N // 3, N - 1)):  # channels of slow decay, which never erases
+        d["initial_state"][k, c] = float("inf")
+    r, want = _fwd(d), U.scan_ref(d)
+    _no_error()
+    assert np.isinf(want[0]).sum() == sum(lens[k] for k in (5, N // 3, N - 1))
+    _same("h", r[0], want[0], size[0], n, U.HALF[dtype])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_a_long_sequence(dtype):
     """More tiles than share the first two levels of what joins them."""
     d = U.scan_batch([140000, 5], 6, dtype, 18, gate="sigmoid")
@@ -212,6 +232,7 @@ def _same(name, got, want, size, n, half):
     U.close(name, torch.from_numpy(np.where(bad, 0, got)), np.where(bad, 0, want), np.where(bad, 0, size), n, half)
 
 
+@pytest.mark.filterwarnings("ignore:invalid value")  # (the oracle's infinities times 0)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("input_scale", U.INPUTS)
 @pytest.mark.parametrize("lens", [[150, 90], [60, 3000], [5000, 0, 17]])
@@ -246,6 +267,7 @@ def test_infinities_stay_infinities(dtype, input_scale, lens):
             _same(j, got[j], want[j], sizes[j], 2 * n, U.U32 if j == "initial_state" else U.HALF[dtype])
 
 
+@pytest.mark.filterwarnings("ignore:invalid value")
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_step_keeps_infinities(dtype):
     d, pool, idx = _step_batch(3, 20, dtype, 5, 4, gate="log")
