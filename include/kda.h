@@ -550,8 +550,8 @@ kda_status_t kda_rope(const kda_rope_args *args, struct CUstream_st *stream);
  * Shapes: x, z, input_gate and h [T, D], any D; tokens of x, z and input_gate are *_stride elements apart (0: D,
  * dense), so that slices of one projection can be read where they lie.  Tensors of dtype are aligned to their
  * element at least (rows whose addresses and strides allow it move as wide vectors), states and parameters fp32 and 4-byte
- * aligned.  Packing, cu_seqlens (checked on the device; sequences with a bad range are skipped and rows that belong
- * to no sequence are left as they were), streams and errors are as for kda_linear_chunk_fwd.  Outputs may not overlap inputs,
+ * aligned.  Packing, cu_seqlens (checked on the device; sequences with a bad range are skipped, others of such a
+ * call may be, and rows that belong to no sequence are left as they were), streams and errors are as for kda_linear_chunk_fwd.  Outputs may not overlap inputs,
  * except that final_state may be initial_state.  An empty sequence's final state is its initial state.  The calls use no atomics on
  * results: the same inputs give the same bits. */
 #define KDA_SCAN_LOWER_BOUND 0

@@ -12,14 +12,7 @@ template <typename T, int V> struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V :
     T x[V];
 };
 template <typename T, int V> __device__ __forceinline__ vec<T, V> load(const T *p) { return *reinterpret_cast<const vec<T, V> *>(p); }
-// read once, written once: evicted first
-template <typename T, int V> __device__ __forceinline__ vec<T, V> load_once(const T *p) {
-    vec<T, V> v;
-    if constexpr (sizeof(v) == 16) *reinterpret_cast<uint4 *>(&v) = __ldcs(reinterpret_cast<const uint4 *>(p));
-    else if constexpr (sizeof(v) == 8) *reinterpret_cast<uint2 *>(&v) = __ldcs(reinterpret_cast<const uint2 *>(p));
-    else v = load<T, V>(p);
-    return v;
-}
+// written once: evicted first
 template <typename T, int V> __device__ __forceinline__ void store_once(T *p, const vec<T, V> &v) {
     if constexpr (sizeof(v) == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(&v));
     else if constexpr (sizeof(v) == 8) __stcs(reinterpret_cast<uint2 *>(p), *reinterpret_cast<const uint2 *>(&v));
@@ -124,7 +117,6 @@ template <typename T, int V, typename F> __device__ __forceinline__ void unpack(
 template <typename T, int V, typename F> __device__ __forceinline__ vec<T, V> pack(const F *f) {
     return pack<T, V>(reinterpret_cast<const float *>(f));
 }
-template <typename F> __device__ __forceinline__ F unpack_one(const float *p) { return *reinterpret_cast<const F *>(p); }
 
 // The slot of row n of a step: -1 for a row of a padded batch and for a slot outside the pool (which sets the device error).  Whether an
 // earlier row has the slot, so that nothing of this one is written (an error as well), every thread of the block of NT asks
