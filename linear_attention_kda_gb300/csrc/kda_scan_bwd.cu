@@ -102,7 +102,7 @@ scan_bwd_kernel(const __grid_constant__ kda_scan_bwd_args A, const __grid_consta
     const bool gated = A.input_gate != nullptr;
     if (PLAN && out.rows)
         for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < B.slots * 2 * A.D; i += (int64_t)gridDim.x * NT) out.rows[i] = 0.f;
-    if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
+    if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, A.D, blocks, err);
     const bool links = PLAN && !planned_chains(B), loader = w == NW - 1;
     course<L, PLAN> way(B, S.next.way, A.cu_seqlens, A.T, A.N, blocks, how, true);
     // the first token of a tile

@@ -57,7 +57,7 @@ scan_fwd_kernel(const __grid_constant__ kda_scan_args A, const __grid_constant__
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, pair = lane % X::LPR * 2, row0 = w * X::RW + lane / X::LPR * R;
     const spec K{A.gate_kind, A.input_scale, A.g_min};
     const bool gated = A.input_gate != nullptr;
-    if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, blocks, err);
+    if (PLAN) make_plan(B, A.cu_seqlens, A.T, A.N, A.D, blocks, err);
     const bool links = PLAN && !planned_chains(B), loader = w == NW - 1;
     course<L, PLAN> way(B, S.next.way, A.cu_seqlens, A.T, A.N, blocks, how, false);
     // the next tile of the course, its boxes asked for

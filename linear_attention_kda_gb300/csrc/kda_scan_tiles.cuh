@@ -92,7 +92,7 @@ __host__ __device__ __forceinline__ bool rather_whole(int64_t longest, int64_t t
 // 16384 tokens of one sequence 184 us by chains and 214, 4 sequences of 512 to 8192 197 and 254), and where any part of cu_seqlens is bad (the slots may not be
 // those that the sequences think, so that no tile may wait for another).
 // Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 2 us more.)
-static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int blocks, int *err) {
+static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int64_t D, int blocks, int *err) {
     const int64_t first = (int64_t)blockIdx.x * NT + threadIdx.x, each = (int64_t)gridDim.x * NT;
     const int L = B.L;
     // (the entries begin on a 256-byte boundary and end before a multiple of it)
@@ -102,8 +102,11 @@ static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu,
         lin::span s;
         return lin::seq_span(cu, T, N, n, &s) ? s.b > s.a ? (s.b - s.a + L - 1) / L : 1 : 0;
     };
-    // Sums over all sequences are for up to 1024 of them; more are short enough in the order in which they come.
-    const bool sorted = N <= 1024;
+    // Tiles and chains in order of length are worth a look at all sequences for each of them (0.7 us a sequence in all) where sequences are few for
+    // the call's size: the longest chain's end is about T D / N elements' work.  In order / as they come, bf16, us: 32 sequences of 512 to 8192 tokens
+    // of 4096 channels 1005 / 1073, gradients of 12 of 700 to 5000 684 / 777, 16 of 1 to 2000 168 / 173 and 64, near the border, 577 / 562; of 256 channels
+    // 8 of 1 to 2000 34 / 27, 512 of them 559 / 329, 1000 of 64 to 128 tokens 716 / 100.
+    const bool sorted = T * D / N >= N << 16;
     // Where in the plan a tile stands: first tiles of all sequences first, then their second ones and so on, so that what a tile
     // waits for was begun long before it wherever there are several sequences.
     for (int64_t i = first; i < B.slots; i += each) {

@@ -128,6 +128,16 @@ def test_many_sequences_by_copies(dtype, N, long):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens", [[9000, 30, 500, 0, 77], [700, 0, 1500, 2000, 64, 1, 900, 1200, 333, 1800], [5, 3000]])
+def test_few_sequences_of_many_channels(dtype, lens):
+    """Large enough a call for its sequences to be taken in order of length: whole chains, and tiles that join others."""
+    d = U.scan_batch(lens, 1040, dtype, 23, input_scale="complement")
+    r = _fwd(d)
+    _check_fwd(d, r)
+    _check_bwd(d, _bwd(d, r[2]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_a_long_sequence(dtype):
     """More tiles than share the first two levels of what joins them."""
     d = U.scan_batch([140000, 5], 6, dtype, 18, gate="sigmoid")
