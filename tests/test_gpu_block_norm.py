@@ -226,6 +226,24 @@ def test_gradients_of_infinities_without_a_norm(types, gate, D):
     assert torch.equal(g["y"], want["y"]) and torch.equal(g["residual"], want["residual"]) and want["y"].isfinite().all()
 
 
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("D", [101, 264, 1024])
+def test_another_eps(types, D):
+    d = U.norm_batch(40, D, types[0], 13, res=types[1])
+    r, g = _fwd(d, eps=0.3), _bwd(d, eps=0.3)
+    _no_error()
+    y, res, gate, s, post, pre = U.norm_args(d)
+    dr, dn = U.f64(d["grad_residual"]), U.f64(d["grad_normed"])
+    want = R.block_norm(y, res, gate, s, post, pre, 0.3)
+    U.close("residual", r[0], want[0], abs(want[0] - res) + abs(res), ROUNDINGS, U.HALF[types[1]])
+    U.close("normed", r[1], want[1], (abs(want[0] - res) + abs(res)) * abs(want[1]) / abs(want[0]).clip(1e-300) + abs(want[1]), ROUNDINGS, U.HALF[types[0]])
+    want, size = (R.block_norm_grads(y, res, gate, s, post, pre, dr, dn, 0.3, magnitudes=m) for m in (False, True))
+    for k, o in (("residual", "r"), ("y", "y"), ("gate", "gate"), ("post_weight", "post"), ("pre_weight", "pre"), ("scale", "scale")):
+        par = k in ("post_weight", "pre_weight", "scale")
+        half = U.U32 if par else U.HALF[types[1] if k == "residual" else types[0]]
+        U.close(k, g[k], want[o], 3 * size[o] + 0.05 * size[o].max(), 3 * ROUNDINGS + (40 if par else 0), half)
+
+
 # ---------------------------------------------------------------- rows above 512 channels, several to a block: copies into places that are taken in turn
 @pytest.mark.parametrize("types", TYPES)
 @pytest.mark.parametrize("T,D", [(3100, 520), (3100, 1024), (1300, 2048), (1300, 4096), (700, 7168), (700, 8192)])

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from linear_attention_kda_gb300 import kda
+from oracle import layer_ref as R
 from tests import layer_util as U
 
 pytestmark = pytest.mark.gpu
@@ -332,6 +333,62 @@ def test_views(dtype):
         assert all(torch.equal(g[k], g2[k]) for k in g)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_views_whose_rows_end_inside_a_copy(dtype):
+    """100 of 104 channels: rows come by copies, whose last channels are others' (and NaN)."""
+    d = U.scan_batch([90, 1, 200], 100, dtype, 24, input_scale="norm")
+    r = _fwd(d)
+    g = _bwd(d, r[2])
+    x = U.to(d)
+    for k in ("x", "z", "input_gate"):
+        wide = torch.full((291, 104), float("nan"), dtype=U.DT[dtype], device="cuda")
+        wide[:, :100] = x[k]
+        x[k] = wide[:, :100]
+    keep = torch.full_like(r[2], float("nan"))
+    h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, checkpoints=keep, **_how(x))
+    g2 = kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, grad_final_state=x["grad_final_state"], **_how(x))
+    _no_error()
+    assert torch.equal(h, r[0]) and torch.equal(last, r[1]) and all(torch.equal(g2[k], g[k]) for k in g)
+
+
+def test_rows_far_apart():
+    d = U.scan_batch([2, 1], 64, "bf16", 25)
+    r = _fwd(d)
+    g = _bwd(d, r[2])
+    x = U.to(d)
+    big = torch.empty((3, 1 << 29), dtype=torch.bfloat16, device="cuda")
+    for i, k in enumerate(("x", "z", "input_gate")):
+        big[:, 64 * i:64 * i + 64] = x[k]
+        x[k] = big[:, 64 * i:64 * i + 64]
+    h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], initial_state=x["initial_state"], output_final_state=True, **_how(x))
+    g2 = kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], r[2], grad_final_state=x["grad_final_state"], **_how(x))
+    _no_error()
+    assert torch.equal(h, r[0]) and torch.equal(last, r[1]) and all(torch.equal(g2[k], g[k]) for k in g)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_another_lower_bound(dtype):
+    """g_min: sequences, gradients and steps."""
+    d = U.scan_batch([80], 48, dtype, 26, gate="lower_bound", input_scale="norm", state=False)
+    x = U.to(d)
+    keep = kda.scan_checkpoints(80, 1, 48)
+    h, last = kda.scan_fwd(x["x"], x["z"], x["input_gate"], g_min=-0.5, checkpoints=keep, output_final_state=True, **_how(x))
+    g = kda.scan_bwd(x["x"], x["z"], x["input_gate"], x["grad_h"], keep, g_min=-0.5, **_how(x))
+    state, how = torch.zeros((1, 48), device="cuda"), {k: v for k, v in _how(x).items() if k != "cu_seqlens"}
+    steps = torch.cat([kda.scan_step(x["x"][t:t + 1], x["z"][t:t + 1], x["input_gate"][t:t + 1], state, g_min=-0.5, **how) for t in range(80)])
+    _no_error()
+    a = [U.f64(d[k]) for k in ("x", "z", "input_gate", "A_log", "dt_bias")]
+    want, size = (R.scan(f(a[0]), *a[1:], np.zeros(48), "lower_bound", -0.5, "norm") for f in (lambda v: v, np.abs))
+    n, half = U.scan_roundings(d), U.HALF[dtype]
+    U.close("h", h, want[0], size[0], n, half)
+    U.close("final_state", last[0], want[2], size[2], n, U.U32)
+    U.close("steps", steps, want[0], size[0], n, half)
+    U.close("state", state[0], want[2], size[2], n, U.U32)
+    want, size = (R.scan_grads(*a, np.zeros(48), U.f64(d["grad_h"]), np.zeros(48), "lower_bound", -0.5, "norm", magnitudes=m) for m in (False, True))
+    for k, o in (("x", "x"), ("z", "z"), ("input_gate", "i"), ("A_log", "A"), ("dt_bias", "b")):
+        U.close(k, g[k], want[o], size[o], 2 * n + 80, U.U32 if o in "Ab" else half)
+
+
 def test_outputs_at_odd_elements():
     d = U.scan_batch([90, 200], 64, "bf16", 6)
     r = _fwd(d)
@@ -560,6 +617,24 @@ def test_step_padded_and_bad_rows(dtype):
     _step(d, p, torch.full((40,), -1, dtype=torch.int32))
     _no_error()
     assert torch.equal(p.cpu(), pool)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", (0, 3))
+def test_step_views(dtype, pad):
+    """Slices of one projection."""
+    d, pool, idx = _step_batch(9, 64, dtype, 6, 12, input_scale="norm")
+    p, q = pool.cuda(), pool.cuda()
+    h = _step(d, p, idx)
+    x = U.to(d)
+    wide = torch.zeros((9, 3 * 64 + pad), dtype=U.DT[dtype], device="cuda")
+    for i, k in enumerate(("x", "z", "input_gate")):
+        v = wide[:, pad + 64 * i:pad + 64 * i + 64]
+        v.copy_(x[k])
+        x[k] = v
+    h2 = _step(x, q, idx)
+    _no_error()
+    assert torch.equal(h2, h) and torch.equal(p, q)
 
 
 def test_step_of_more_sequences_than_a_grid_is_high():

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from linear_attention_kda_gb300 import kda
+from oracle import layer_ref as R
 from tests import layer_util as U
 
 pytestmark = pytest.mark.gpu
@@ -165,6 +166,52 @@ def test_views(dtype, norm):
             U.close(k, g2[k], U.f64(g[k]), size[k], 2 * (4 * _roundings(d) + 200), 0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("norm", [0, 32])
+def test_views_whose_rows_end_inside_a_copy(dtype, norm):
+    """96 or 100 of 104 channels: rows come by copies, whose last channels are others' (and NaN)."""
+    D = 96 if norm else 100
+    d = U.conv_batch([90, 1, 109], D, 4, dtype, 15, norm=norm)
+    r, g = _fwd(d), _bwd(d)
+    wide = torch.full((200, 104), float("nan"), dtype=U.DT[dtype], device="cuda")
+    wide[:, :D] = d["x"].cuda()
+    v = {**d, "x": wide[:, :D]}
+    r2, g2 = _fwd(v), _bwd(v)
+    _no_error()
+    assert torch.equal(r2[0], r[0]) and torch.equal(r2[1], r[1]) and torch.equal(g2["x"], g["x"]) and torch.equal(g2["initial_state"], g["initial_state"])
+
+
+def test_rows_far_apart():
+    d = U.conv_batch([2, 1], 64, 4, "bf16", 16, norm=64)
+    r, g = _fwd(d), _bwd(d)
+    big = torch.empty((3, 1 << 29), dtype=torch.bfloat16, device="cuda")
+    big[:, 64:128] = d["x"].cuda()
+    v = {**d, "x": big[:, 64:128]}
+    r2, g2 = _fwd(v), _bwd(v)
+    _no_error()
+    assert torch.equal(r2[0], r[0]) and torch.equal(r2[1], r[1]) and all(torch.equal(g2[k], g[k]) for k in g)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_another_eps(dtype):
+    """norm_eps: sequences, gradients and steps."""
+    eps = 0.3
+    d = U.conv_batch([40], 64, 4, dtype, 17, norm=32)
+    y, tail = _fwd(d, norm_eps=eps)
+    g = _bwd(d, norm_eps=eps)
+    state, x = d["initial_state"].cuda(), U.to(d)
+    steps = torch.cat([kda.short_conv_step(x["x"][t:t + 1], x["weight"], x["bias"], state, norm_dim=32, norm_eps=eps) for t in range(40)])
+    _no_error()
+    a = [U.f64(d[k]) for k in ("x", "initial_state", "weight", "bias", "grad_y", "grad_final_state")]
+    want, _ = R.conv(a[0], a[1][0], a[2], a[3], "silu", 32, eps)
+    U.close("y", y, want, U.conv_sizes(d), _roundings(d), U.HALF[dtype])
+    U.close("steps", steps, want, U.conv_sizes(d), _roundings(d), U.HALF[dtype])
+    assert torch.equal(state, tail)
+    want, size = (R.conv_grads(a[0], a[1][0], a[2], a[3], a[4], a[5][0], "silu", 32, eps, magnitudes=m) for m in (False, True))
+    for k, o in (("x", "x"), ("weight", "w"), ("bias", "b")):
+        U.close(k, g[k], want[o], size[o] + 0.1 * abs(size[o]).max(), 4 * _roundings(d) + 40, U.HALF[dtype] if k == "x" else U.U32)
+
+
 def test_output_at_odd_elements():
     d = U.conv_batch([90, 110], 64, 4, "bf16", 7, norm=64)
     want = _fwd(d)[0]
@@ -306,6 +353,19 @@ def test_step_padded_and_bad_rows(dtype):
     untouched = torch.ones(60, dtype=torch.bool)
     untouched[idx.long()[used]] = False
     assert torch.equal(p.cpu()[untouched], pool[untouched])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", (0, 3))
+def test_step_views(dtype, pad):
+    d, pool, idx = _step_batch(9, 64, 4, dtype, 14, 12, norm=64)
+    p, q = pool.cuda(), pool.cuda()
+    y = _step(d, p, idx)
+    wide = torch.zeros((9, 128 + pad), dtype=U.DT[dtype], device="cuda")
+    wide[:, pad:pad + 64] = d["x"].cuda()
+    y2 = _step({**d, "x": wide[:, pad:pad + 64]}, q, idx)
+    _no_error()
+    assert torch.equal(y2, y) and torch.equal(p, q)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
