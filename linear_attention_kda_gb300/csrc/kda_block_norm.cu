@@ -2,8 +2,8 @@
 //
 // Bound by HBM traffic: y, the gate and r are read once, r' and n written once (10 bytes per channel in bf16, 14 with
 // an fp32 residual).  A row stays in the registers of its threads between the two sums that its norms need; the
-// weights come from L1 and L2.  65535 rows of 4096: with an fp32 residual 535 us, 7.0 TB/s,
-// in bf16 438 us, 6.1 TB/s (one channel at a time 481; 512 threads a row were no faster than 256).
+// weights come from L1 and L2.  65535 rows of 4096: with an fp32 residual 536 us, 7.0 TB/s,
+// in bf16 437 us, 6.1 TB/s (one channel at a time 481; 512 threads a row were no faster than 256).
 #include "kda_block_norm.cuh"
 
 namespace kda {

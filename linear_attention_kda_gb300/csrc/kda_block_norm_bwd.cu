@@ -5,10 +5,11 @@
 //     dpre_weight = sum dn rh,   dpost_weight = scale sum d s yh,   dscale = post_weight sum d s yh      over tokens
 //
 // Bound by HBM traffic: y, gate, r, dr' and dn read once, dr, dy and dgate written once (16 bytes per channel in bf16).  A
-// row stays in registers between its three sums, all arithmetic is on two channels at a time (64 instructions a channel, which take about
-// as long as the memory; one at a time and with gates formed twice 98).  16384 rows of 4096 in bf16: 184 us, 5.8 TB/s (588 at first).  A block takes every G-th row, the next one on its way to
+// row stays in registers between its three sums, all arithmetic is on two channels at a time (45 instructions a channel, half of
+// the issue slots).  16384 rows of 4096 in bf16: 185 us, 5.8 TB/s (588 at first); fp32 345 us, 6.2 TB/s.  A block takes every G-th row, the next one on its way to
 // shared memory meanwhile, and keeps the tokens' sums of its columns in registers; the blocks' sums meet in a second kernel in a
-// fixed order.
+// fixed order.  Rows of up to 512 channels, a warp to a row, have no next row on its way and wait for their loads: 262144 of 256 424 us, 2.5 TB/s,
+// 131072 of 512 445 us.
 #include <atomic>
 
 #include "kda_block_norm.cuh"

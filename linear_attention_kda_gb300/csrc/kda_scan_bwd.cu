@@ -5,9 +5,9 @@
 // tile's sums, and, when it knows what enters from both sides (the state from the tile's checkpoint, the adjoint from the
 // tiles behind it), runs them again: the states are kept in the place of the inputs, and the gates are formed once
 // more, with their slopes, as the adjoint passes.  Sums over tokens for A_log and dt_bias leave a row for each tile, which
-// a second kernel adds up.  Bound by instructions: 111 an element for 14 bytes in bf16 (gated, c of the norm), issued in
-// 63 % of the cycles.  12 sequences of 700 to 5000 tokens, 4096 channels, bf16: 692 us, 3.0 TB/s (a thread to a channel of a sequence 9055); one of
-// 8192 tokens 210 us.  Eight tokens a thread, as many as keep their states, decays and gradients in 128 registers, two blocks to an SM.
+// a second kernel adds up.  Bound by instructions: 106 an element for 14 bytes in bf16 (gated, c of the norm), issued in
+// 61 % of the cycles.  12 sequences of 700 to 5000 tokens, 4096 channels, bf16: 677 us, 3.0 TB/s (a thread to a channel of a sequence 9055); one of
+// 8192 tokens 209 us; the 12 in fp32, one block to an SM, 957 us, 4.3 TB/s.  Eight tokens a thread, as many as keep their states, decays and gradients in 128 registers, two blocks to an SM.
 #include "kda_scan_tiles.cuh"
 
 namespace kda {

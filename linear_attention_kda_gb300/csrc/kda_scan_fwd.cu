@@ -2,10 +2,11 @@
 // each lane two channels and R of them.  Tiles come by TMA two ahead.  A thread forms the decay and the input of its elements once,
 // keeps both in registers, runs them from zero for the tile's sums, and, when it knows what enters, runs them again for h.
 //
-// Bound by instructions: 47 an element (softplus, c of the norm, gated), issued in 60 % of the cycles, where all cycles at HBM's rate would hold
-// 42.  bf16, gated, D = 4096: 32 sequences of 512 to 8192 tokens 1030 us, 4.2 TB/s (a thread to a channel of a sequence, a token at a time,
-// 9110); 16 such sequences in fp32 6.5 TB/s; one sequence of 4096 tokens 49 us.  131072 tokens of 256 channels 102 us, bound by tiles that
-// wait for one another (issued in 35 % of the cycles).
+// Bound by instructions and by the two barriers of a tile: 45 instructions an element (softplus, c of the norm, gated; 5 of the special function
+// unit, 12 of the integer and selecting pipe, 21 multiply-adds), issued in 59 % of the cycles, where all cycles at HBM's rate would hold
+// 42.  bf16, gated, D = 4096: 32 sequences of 512 to 8192 tokens 1003 us, 4.3 TB/s (a thread to a channel of a sequence, a token at a time,
+// 9110); 16 such sequences in fp32 763 us, 6.4 TB/s; one sequence of 4096 tokens 47 us.  131072 tokens of 256 channels 104 us, bound by tiles that
+// wait for one another (issued in 33 % of the cycles).
 #include "kda_scan_tiles.cuh"
 
 namespace kda {

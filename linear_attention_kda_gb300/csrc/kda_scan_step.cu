@@ -1,8 +1,9 @@
 // kda_scan_step: one decode token per sequence of the gated recurrence over channels, states updated in place.
 //
 // Bound by HBM traffic (bf16 with an input gate: 8 bytes of tokens and 8 of state per channel), for few sequences by the
-// launch.  A thread takes V channels of one sequence; whether an earlier row has its slot is looked up while its own loads are on their
-// way.  256 sequences of 4096 channels, bf16, gated: 6.8 us, 2.5 TB/s (16.8 MB, whose copy takes 2.5 us).
+// launch.  A thread takes V channels of one sequence: its slot, then the state, then the block's vote on whether an earlier row has the slot, which is
+// looked up while the loads are on their way.  256 sequences of 4096 channels, bf16, gated: 4.4 us replayed one after the other, 8.1 us with
+// caches cold (16.8 MB, whose copy takes 2.5 us).
 #include "kda_internal.h"
 #include "kda_layer.cuh"
 #include "kda_scan.cuh"
@@ -58,8 +59,8 @@ static void launch(const kda_scan_step_args *a, cudaStream_t stream, int *err) {
 
 template <typename T>
 static void launch_t(const kda_scan_step_args *a, cudaStream_t stream, int *err) {
-    // Four channels a thread where every row's address allows vectors of them (256 sequences of 4096 channels, bf16: 6.8 us,
-    // 10.2 one by one)
+    // Four channels a thread where every row's address allows vectors of them (256 sequences of 4096 channels, bf16: two
+    // thirds of the time one by one)
     const uintptr_t tok = (uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->input_gate | (uintptr_t)a->h;
     const bool wide = a->D % 4 == 0 && a->x_stride % 4 == 0 && a->z_stride % 4 == 0 && a->i_stride % 4 == 0 && tok % (4 * sizeof(T)) == 0 &&
                       (uintptr_t)a->state % 16 == 0;

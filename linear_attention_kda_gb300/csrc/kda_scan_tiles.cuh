@@ -79,7 +79,7 @@ inline size_t board_layout(int64_t T, int64_t N, int D, int L, void *ws, board *
 }
 
 // What a call's tiles are.  SINGLE: no sequence has a second one.  EQUAL: whole chains of sequences of one length, as the host can tell
-// where there are no cu_seqlens or there is one sequence (one of 4096 tokens and channels 51.5 us, 61.2 with a plan).  PLANNED: make_plan() says.
+// where there are no cu_seqlens or there is one sequence (one of 4096 tokens and channels 50 us, 60 with a plan).  PLANNED: make_plan() says.
 enum layout : int { SINGLE, EQUAL, PLANNED };
 __device__ __forceinline__ bool planned_chains(const board &B) { return __ldcg(B.mode) != 0; }
 // whether chains, the longest of which has `longest` tiles of `total` in 1 / blocks of the channels, are taken whole by g blocks
@@ -89,7 +89,7 @@ __host__ __device__ __forceinline__ bool rather_whole(int64_t longest, int64_t t
 
 // Clears the entries, looks at all of cu_seqlens, lists the tiles and the chains and chooses between the two ways: whole chains where
 // the longest one is no more than 1.4 times a block's share of all tiles (a tile of a chain takes less than one that joins others; where both were tried,
-// 16384 tokens of one sequence 184 us by chains and 214, 4 sequences of 512 to 8192 197 and 254), and where any part of cu_seqlens is bad (the slots may not be
+// 16384 tokens of one sequence 193 us by chains and 213, 4 sequences of 512 to 8192 194 and 252), and where any part of cu_seqlens is bad (the slots may not be
 // those that the sequences think, so that no tile may wait for another).
 // Every thread of a cooperative launch calls it; behind it all blocks see all of it.  (As a kernel of its own it took 2 us more.)
 static __device__ __noinline__ void make_plan(const board &B, const int32_t *cu, int64_t T, int64_t N, int64_t D, int blocks, int *err) {
@@ -501,10 +501,10 @@ __device__ __forceinline__ channel<float2> load_channel(const float *A_log, cons
 
 // Channels of a tile.  64 cost least: each row of a tile is two sectors or more, a warp has no groups to join, and its reads of shared
 // memory no bank conflicts.  Fewer make more chains, so that more blocks have whole ones, of which the last ends sooner, and
-// tiles of more tokens, of which fewer join where they have to.  At 64 / 32 / 16 channels, all by the kernel with a plan, bf16 (f32), D = 4096, us: forwards 16384 tokens of one
-// sequence (64 chains of 64 channels) 203 / 201 / 184, 131072 of D = 256 (4) 127 / 127 / 125 (180 / 152 / 137), 4 sequences (256) 250 / 191 / 197,
-// 6 (384) 334 / 246 / 260 (405 / 287 / 297), 8 (512) 360 / 345 / 375, 12 (768) 451 / 459 / 508 (555 / 558 / 575), 32 (2048) 1040 / 1092 / 1234;
-// gradients 8192 of one 242 / 236 / 223, 3 sequences (192) 276 / 263 / 236, 6 (384) 461 / 382 / 400, 12 (768) 690 / 718 / 765.
+// tiles of more tokens, of which fewer join where they have to.  At 64 / 32 / 16 channels, bf16 (f32), D = 4096, us: forwards 16384 tokens of one
+// sequence (64 chains of 64 channels) 193 / 202 / 177, 131072 of D = 256 (4) 116 / 110 / 107 (191 / 147 / 134), 4 sequences (256) 224 / 195 / 193,
+// 6 (384) 301 / 245 / 257 (406 / 285 / 301), 8 (512) 349 / 345 / 370, 12 (768) 439 / 454 / 504 (558 / 567 / 583), 32 (2048) 1006 / 1082 / 1219;
+// gradients 8192 of one 227 / 237 / 209, 3 sequences (192) 268 / 271 / 247, 6 (384) 455 / 384 / 401, 12 (768) 682 / 731 / 770.
 inline int tile_width(int64_t N, int D) {
     const int64_t chains = N * ((D + 63) / 64);
     return chains < 2 * 152 ? 16 : chains < 4 * 152 ? 32 : 64;

@@ -1,8 +1,8 @@
 // kda_short_conv_fwd: a warp takes a run of L tokens of one sequence by 32 V channels, V to a lane, and goes through the
 // tokens with the last K - 1 of them in registers; the sums of a head's squares meet by shuffles between the lanes that
 // hold it.  Rows come by TMA, up to 24 tokens ahead.  Bound by HBM traffic, x read once (but for the K - 1 tokens before each
-// run) and y written once, and close to that by instructions: 21 an element with the norm.  bf16, 32 sequences of 512 to 8192
-// tokens, 4096 channels, four taps: 330 us, 6.5 TB/s; with the norm over heads of 128 410 us, 5.3 TB/s (four tokens' sums at once; 427 two
+// run) and y written once, and close to that by instructions: 20 an element with the norm.  bf16, 32 sequences of 512 to 8192
+// tokens, 4096 channels, four taps: 337 us, 6.4 TB/s; with the norm over heads of 128 409 us, 5.3 TB/s; 16 of them in fp32 371 us, 6.6 TB/s (four tokens' sums at once; 427 two
 // and 479 one at a time).  V = 8 was no faster where 4 will do.
 //
 // kda_short_conv_step: the same for one token, whose history is a slot of a pool.
