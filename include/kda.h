@@ -644,7 +644,7 @@ kda_status_t kda_scan_step(const kda_scan_step_args *args, struct CUstream_st *s
  *     p_t = bias + sum_j weight[:, j] x_{t-K+1+j},   s_t = Swish(p_t) or p_t,   y_t = s_t or L2Norm(s_t),
  * L2Norm over each head of norm_dim channels, s / sqrt(sum s^2 + norm_eps).  Tokens before a sequence's first come
  * from its history, the last K - 1 inputs (zero where there is none); the new history is what the next call or step
- * continues from.  Arithmetic is fp32, y is rounded once to dtype, histories are exact copies of inputs.
+ * continues from.  Arithmetic is fp32, squares included, y is rounded once to dtype, histories are exact copies of inputs.
  *
  * Shapes: x and y [T, D], any D (a multiple of norm_dim); x may have a token stride as in kda_scan; weight [D, K];
  * histories [N, K - 1, D] in dtype, oldest token first.  Outputs may not overlap inputs, except that final_state may be
@@ -722,7 +722,8 @@ kda_status_t kda_short_conv_step(const kda_short_conv_step_args *args, struct CU
  *     n  = pre_weight * r' / sqrt(mean r'^2 + eps).
  * Each part may be absent: P (post_norm = 0), the gate, n (pre_norm = 0, behind the last block), or the block itself
  * (y NULL: n of r alone, in front of the first block).  The gate's logits are per channel [T, D] or per token [T]; scale is one
- * number or one per channel.  The residual stream may be fp32 beside bf16 blocks.  fp32 arithmetic; n is made from the unrounded r'.
+ * number or one per channel.  The residual stream may be fp32 beside bf16 blocks.  fp32 arithmetic, squares
+ * included (of a row with values beyond about 1e18 they overflow: P and n are 0 there); n is made from the unrounded r'.
  * Dense tensors, D 1 .. 8192, aligned to their elements (wide vectors where addresses and D allow).  residual_out
  * may be residual, normed may be y; no other output may overlap an input. */
 #define KDA_NORM_GATE_NONE 0
